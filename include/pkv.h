@@ -14,6 +14,9 @@
  * pkv_seq_*) hands out block ids and reports the copy-on-write pairs that
  * pkv_copy_blocks copies on the GPU before the step's append.
  * Chunked prefill: pkv_kv_append_chunk and pkv_paged_prefill_attention.
+ * 8-bit cache: pkv_kv_append_q8, pkv_kv_read_blocks_q8,
+ * pkv_paged_decode_attention_q8; pkv_qk_norm_rope_append prepares queries and
+ * keys and appends in one pass, to either kind of cache.
  * Speculative decoding: pkv_spec_verify accepts or rejects draft tokens,
  * draws the correction or bonus token and returns the rolled-back lengths.
  *
@@ -71,7 +74,12 @@ typedef enum {
     PKV_ERR_CAPACITY = 7       /* host: the block pool has too few free blocks */
 } pkv_status;
 
-typedef enum { PKV_F32 = 0, PKV_BF16 = 1 } pkv_dtype;
+typedef enum {
+    PKV_F32 = 0,
+    PKV_BF16 = 1,
+    PKV_E4M3 = 2, /* 8-bit caches only: the calls that say so */
+    PKV_I8 = 3
+} pkv_dtype;
 
 /* Human-readable name of a status code (static string; never NULL). */
 const char* pkv_status_string(int status);
@@ -241,7 +249,7 @@ pkv_status pkv_sample_tokens(int32_t* tokens, const float* logits, int B, int V,
  * int32 [n_pairs].  The dst ids must be distinct and none may appear among the
  * src ids of the same call (the copies run in parallel); a block id outside
  * [0, num_blocks) skips its pair and records PKV_ERR_DEVICE_BOUNDS.
- * n_pairs == 0 is a no-op.  Bit copy, no arithmetic.
+ * n_pairs == 0 is a no-op.  Bit copy, no arithmetic.  dtype: any pkv_dtype.
  */
 pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const int32_t* src, const int32_t* dst, int n_pairs,
                            int Hkv, int D, int block_size, int num_blocks, pkv_dtype dtype, int32_t* dev_status,
@@ -390,6 +398,109 @@ pkv_status pkv_spec_verify(int32_t* tokens_out, int32_t* n_accepted, int32_t* se
                            const int32_t* seq_lens, int B, int gamma, int V, const float* temperature,
                            const uint64_t* seeds, const uint64_t* offsets, void* workspace, size_t workspace_bytes,
                            int32_t* dev_status, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The 8-bit KV cache.  A cache of type PKV_E4M3 or PKV_I8 is two pools of one
+ * byte per element in the layout above, k_cache and v_cache [num_blocks, Hkv,
+ * block_size, D], and one float32 scale per row (token and KV head) of each:
+ * k_scale and v_scale [num_blocks, Hkv, block_size].  A row x of D values is
+ * stored as
+ *   scale = max(max|x| * (1 / Q), 2^-64),   value_i = rne(x_i * (1 / scale)),
+ * Q = 448 (PKV_E4M3, 8-bit floating point with 3 mantissa bits) or 127 (PKV_I8,
+ * two's complement), every operation in float32, and stands for value_i *
+ * scale.  An element of a PKV_I8 row is off by at most scale / 2 (plus the
+ * float32 roundings), of a PKV_E4M3 row by at most |x_i| / 16 or scale * 2^-10,
+ * whichever is larger.  A row that holds a NaN or an infinity is stored as zeros
+ * with scale NaN and PKV_ERR_NONFINITE is recorded; attention over it gives
+ * NaN, as it does over such a row of an unquantised cache.
+ * Blocks are copied with pkv_copy_blocks, which takes the two 8-bit types for the
+ * pools; the scale pools are one more call of it with D = 1 and PKV_F32.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * pkv_kv_append and pkv_kv_append_chunk into an 8-bit cache: the rows are
+ * quantised as they are written.  q_start NULL: one token per sequence (T_new
+ * must be B), as pkv_kv_append; else the packed chunks of
+ * pkv_kv_append_chunk.  dtype: PKV_F32 or PKV_BF16, of k_new and v_new
+ * [T_new, Hkv, D]; cache_dtype: PKV_E4M3 or PKV_I8.  1 <= D <= 256.  Sequences
+ * with a bad length, chunk or block id are skipped and PKV_ERR_DEVICE_BOUNDS
+ * recorded.
+ */
+pkv_status pkv_kv_append_q8(const void* k_new, const void* v_new, void* k_cache, void* v_cache, float* k_scale,
+                            float* v_scale, const int32_t* block_tables, int max_blocks_per_seq,
+                            const int32_t* seq_lens, const int32_t* q_start, int B, int T_new, int Hkv, int D,
+                            int block_size, int num_blocks, pkv_dtype dtype, pkv_dtype cache_dtype,
+                            int32_t* dev_status, void* stream);
+
+/*
+ * Blocks of an 8-bit cache read back: for i in [0, n), block i of k_out and
+ * v_out [n, Hkv, block_size, D] (out_dtype PKV_F32 or PKV_BF16) becomes value *
+ * scale of block blocks[i], one float32 product per element rounded once.  The
+ * result is an unquantised pool of n blocks: with a table that names them,
+ * pkv_paged_prefill_attention runs on a cached prefix and its chunk.  blocks:
+ * device int32 [n]; a block may appear more than once; an id outside [0,
+ * num_blocks) gives a block of zeros and records PKV_ERR_DEVICE_BOUNDS.  Slots
+ * that no token was written to are read back as they are.  1 <= D <= 256.
+ */
+pkv_status pkv_kv_read_blocks_q8(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                                 const float* k_scale, const float* v_scale, const int32_t* blocks, int n, int Hkv,
+                                 int D, int block_size, int num_blocks, pkv_dtype out_dtype, pkv_dtype cache_dtype,
+                                 int32_t* dev_status, void* stream);
+
+/* Workspace bytes pkv_paged_decode_attention_q8 needs (num_sms <= 0: the current
+ * device).  Returns 0 on error.  Pure host arithmetic when num_sms > 0. */
+size_t pkv_decode_q8_workspace_bytes(int B, int Hq, int Hkv, int D, int num_sms);
+
+/*
+ * pkv_paged_decode_attention over an 8-bit cache: the same definition with
+ * K_j and V_j the numbers the cache's rows stand for.  q and out [B, Hq, D] in
+ * dtype (PKV_F32 or PKV_BF16).  Any Hq % Hkv == 0, any block_size, 1 <= D <=
+ * 256; L == 0 gives zeros.  workspace: device, 16-byte aligned, at least
+ * pkv_decode_q8_workspace_bytes(B, Hq, Hkv, D, 0) bytes, contents ignored on
+ * entry; calls that can overlap on the GPU need a workspace each.  Bad lengths
+ * and block ids give zero output and PKV_ERR_DEVICE_BOUNDS.  Slots past L are
+ * never used (their values and scales may be anything, NaN included).
+ */
+pkv_status pkv_paged_decode_attention_q8(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                         const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                         int max_blocks_per_seq, const int32_t* seq_lens, int B, int Hq, int Hkv,
+                                         int D, int block_size, int num_blocks, float scale, pkv_dtype dtype,
+                                         pkv_dtype cache_dtype, void* workspace, size_t workspace_bytes,
+                                         int32_t* dev_status, void* stream);
+
+/*
+ * Norm, rotation and append in one pass: what lies between the query / key /
+ * value projections and the attention of a step or a prefill chunk.  For every
+ * new token at position pos (as in pkv_kv_append, or with q_start as in
+ * pkv_kv_append_chunk), each query head's row and each KV head's key row x [D]:
+ *   y_i = x_i / sqrt(mean(x^2) + eps) * w_i    (weights [D] in dtype; a NULL
+ *                                               weight: no norm for that kind)
+ *   pairs (y_a, y_c) -> (y_a cos t - y_c sin t, y_c cos t + y_a sin t),
+ *     t = 2 pi pos freqs[j] 2^-64, j < rot_dim / 2, (a, c) = (j, j + rot_dim / 2)
+ *     or, with interleaved != 0, (2j, 2j + 1); elements from rot_dim on stay.
+ * The query rows go to q_out [T_new, Hq, D] (which may be q itself when q is
+ * dense), the key and value rows into the cache: as they are when cache_dtype
+ * == dtype (k_scale and v_scale ignored), quantised when it is PKV_E4M3 or
+ * PKV_I8.  Everything is float32 between one load and one rounding.
+ * freqs: device int64 [rot_dim / 2], turns per position as 64-bit fractions of a
+ * turn: round(f_j / (2 pi) * 2^64) for angle f_j per position; the integer
+ * product with pos wraps by whole turns, so far positions lose nothing.
+ * rot_dim 0: no rotation.  q, k_new, v_new: rows of a token dense ([H, D]),
+ * tokens q_stride / k_stride / v_stride elements apart (three views of one
+ * projection output, for instance).  1 <= D <= 256, rot_dim even and <= D.
+ * A sequence with a bad length or chunk gets zero q_out rows and no append, one
+ * with a bad block id no append; both record PKV_ERR_DEVICE_BOUNDS.  Rows of
+ * q_out behind the last sequence (t >= q_start[B]) are left as they were.
+ */
+pkv_status pkv_qk_norm_rope_append(void* q_out, const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+                                   const void* v_new, int64_t v_stride, const void* q_weight, const void* k_weight,
+                                   float eps, const int64_t* freqs, int rot_dim, int interleaved, void* k_cache,
+                                   void* v_cache, float* k_scale, float* v_scale, const int32_t* block_tables,
+                                   int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* q_start, int B,
+                                   int T_new, int Hq, int Hkv, int D, int block_size, int num_blocks, pkv_dtype dtype,
+                                   pkv_dtype cache_dtype, int32_t* dev_status, void* stream);
 
 /*
  * Reference-counted block pool (host only; "LLM inference serving tutorial"

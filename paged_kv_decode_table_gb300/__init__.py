@@ -16,13 +16,23 @@ Calls (names follow the C ABI):
   apply_logits_processors(logits, allow_mask=None, row_ptr=None, tokens=None, counts=None, ...)
   kv_append_chunk(k_new, v_new, k_cache, v_cache, block_tables, seq_lens, q_start)
   paged_prefill_attention(q, k_cache, v_cache, block_tables, seq_lens, q_start, out=None, scale=0.0)
+  kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens)
+  kv_append_chunk_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, q_start)
+  kv_read_blocks_q8(k_cache, v_cache, k_scale, v_scale, blocks, dtype=torch.bfloat16)
+  paged_decode_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, out=None, scale=0.0)
+  qk_norm_rope_append(q, k_new, v_new, q_weight, k_weight, eps, freqs, k_cache, v_cache, block_tables, seq_lens, ...)
+  rope_freqs(rot_dim, base=10000.0)                       the rotation's frequencies as 64-bit turns
   BlockPool(num_blocks, block_size, max_blocks_per_seq)   host-side refcounted block ids
   DecodeStep(q, k_new, v_new, k_cache, v_cache, block_tables, seq_lens, logits, ...).run()
       a whole decode step (append + attention + sampler) bound to fixed buffers
+
+An 8-bit cache is two torch.float8_e4m3fn or torch.int8 pools [num_blocks, Hkv,
+block_size, D] with float32 scales [num_blocks, Hkv, block_size], one per row.
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -33,11 +43,15 @@ __all__ = ["PkvError", "load_library", "library_path", "kv_append", "paged_decod
            "decode_workspace_bytes", "sample_tokens", "sample_workspace_bytes", "status_string",
            "new_status", "check_status", "STATUS", "copy_blocks", "BlockPool", "spec_verify",
            "spec_verify_workspace_bytes", "apply_logits_processors", "kv_append_chunk",
-           "paged_prefill_attention", "DecodeStep", "test_set_wait_limit"]
+           "paged_prefill_attention", "DecodeStep", "test_set_wait_limit", "kv_append_q8", "kv_append_chunk_q8",
+           "kv_read_blocks_q8", "paged_decode_attention_q8", "decode_q8_workspace_bytes", "qk_norm_rope_append",
+           "rope_freqs"]
 
 STATUS = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED", 3: "PKV_ERR_CUDA",
           4: "PKV_ERR_DEVICE_BOUNDS", 5: "PKV_ERR_TIMEOUT", 6: "PKV_ERR_NONFINITE", 7: "PKV_ERR_CAPACITY"}
-PKV_F32, PKV_BF16 = 0, 1
+PKV_F32, PKV_BF16, PKV_E4M3, PKV_I8 = 0, 1, 2, 3
+_CODES = {torch.float32: PKV_F32, torch.bfloat16: PKV_BF16}
+_CODES_Q8 = {torch.float8_e4m3fn: PKV_E4M3, torch.int8: PKV_I8}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libpkv.so")
@@ -122,6 +136,18 @@ def load_library():
         lib.pkv_seq_length.restype = i32
         lib.pkv_block_tables.argtypes = [P, P, i32, P, P]
         lib.pkv_block_tables.restype = i32
+        lib.pkv_kv_append_q8.argtypes = [P, P, P, P, P, P, P, i32, P, P, i32, i32, i32, i32, i32, i32, i32, i32, P, P]
+        lib.pkv_kv_append_q8.restype = i32
+        lib.pkv_kv_read_blocks_q8.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, P, P]
+        lib.pkv_kv_read_blocks_q8.restype = i32
+        lib.pkv_decode_q8_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+        lib.pkv_decode_q8_workspace_bytes.restype = sz
+        lib.pkv_paged_decode_attention_q8.argtypes = [P, P, P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32, f32,
+                                                      i32, i32, P, sz, P, P]
+        lib.pkv_paged_decode_attention_q8.restype = i32
+        lib.pkv_qk_norm_rope_append.argtypes = [P, P, i64, P, i64, P, i64, P, P, f32, P, i32, i32, P, P, P, P, P, i32,
+                                                P, P, i32, i32, i32, i32, i32, i32, i32, i32, i32, P, P]
+        lib.pkv_qk_norm_rope_append.restype = i32
         lib.pkv_test_set_wait_limit.argtypes = [ctypes.c_uint32, i32]
         lib.pkv_test_set_wait_limit.restype = i32
         _lib = lib
@@ -341,19 +367,25 @@ class DecodeStep:
     serving loop pays a few microseconds of host time per step instead of
     re-validating every tensor.  The tensors must stay alive, in place and of
     the same shapes while the object is used (refill them in place between
-    steps).  Returns the tokens tensor from run()."""
+    steps).  Returns the tokens tensor from run().  With k_scale and v_scale
+    the cache is an 8-bit one, and the append and the attention are
+    pkv_kv_append_q8 and pkv_paged_decode_attention_q8."""
 
     def __init__(self, q, k_new, v_new, k_cache, v_cache, block_tables, seq_lens, logits, temperature, top_k,
                  top_p, seeds, offsets, out=None, tokens=None, workspace=None, status=None, min_p=None,
-                 scale: float = 0.0, stream=None):
+                 scale: float = 0.0, stream=None, k_scale=None, v_scale=None):
         B, Hq, D = q.shape
         NB, Hkv, BS, D2 = k_cache.shape
         dev = q.device
         if D2 != D:
             raise ValueError("head_dim of q and the cache differ")
+        q8 = k_scale is not None or v_scale is not None
         _check_cuda("q", q)
-        _check_cuda("k_cache", k_cache, q.dtype, device=dev)
-        _check_cuda("v_cache", v_cache, q.dtype, k_cache.shape, dev)
+        if q8:
+            _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
+        else:
+            _check_cuda("k_cache", k_cache, q.dtype, device=dev)
+            _check_cuda("v_cache", v_cache, q.dtype, k_cache.shape, dev)
         _check_cuda("k_new", k_new, q.dtype, (B, Hkv, D), dev)
         _check_cuda("v_new", v_new, q.dtype, (B, Hkv, D), dev)
         _check_cuda("block_tables", block_tables, torch.int32, device=dev)
@@ -378,7 +410,8 @@ class DecodeStep:
         self.tokens = torch.empty(B, dtype=torch.int32, device=dev) if tokens is None else tokens
         _check_cuda("tokens", self.tokens, torch.int32, (B,), dev)
         lib = load_library()
-        need = int(lib.pkv_decode_workspace_bytes(B, Hq, D, 0))
+        need = int(lib.pkv_decode_q8_workspace_bytes(B, Hq, Hkv, D, 0) if q8
+                   else lib.pkv_decode_workspace_bytes(B, Hq, D, 0))
         self.workspace = (torch.empty(max(need, 16), dtype=torch.uint8, device=dev) if workspace is None
                           else workspace)
         _check_cuda("workspace", self.workspace, device=dev)
@@ -390,15 +423,27 @@ class DecodeStep:
         self.status = status
         # keep every bound tensor referenced for the object's lifetime
         self._keep = (q, k_new, v_new, k_cache, v_cache, block_tables, seq_lens, logits, temperature, top_k,
-                      top_p, seeds, offsets, min_p)
+                      top_p, seeds, offsets, min_p, k_scale, v_scale)
         self._dev = dev
         s = stream if stream is not None else torch.cuda.current_stream(dev)
         sp = ctypes.c_void_p(s.cuda_stream)
-        self._attn_fn = lib.pkv_paged_decode_attention_append
-        self._attn = [_ptr(self.out), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
-                      _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B, Hq, Hkv, D, BS, NB,
-                      ctypes.c_float(float(scale)), _dtype_code(q), _ptr(self.workspace), ws_bytes,
-                      _ptr(status), sp]
+        self._attn_name, self._append = "pkv_paged_decode_attention_append", None
+        if q8:
+            self._append = [_ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                            _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), None, B, B, Hkv, D, BS, NB,
+                            _dtype_code(q), _CODES_Q8[k_cache.dtype], _ptr(status), sp]
+            self._append_fn = lib.pkv_kv_append_q8
+            self._attn_fn, self._attn_name = lib.pkv_paged_decode_attention_q8, "pkv_paged_decode_attention_q8"
+            self._attn = [_ptr(self.out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                          _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B, Hq, Hkv, D, BS, NB,
+                          ctypes.c_float(float(scale)), _dtype_code(q), _CODES_Q8[k_cache.dtype],
+                          _ptr(self.workspace), ws_bytes, _ptr(status), sp]
+        else:
+            self._attn_fn = lib.pkv_paged_decode_attention_append
+            self._attn = [_ptr(self.out), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+                          _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens), B, Hq, Hkv, D, BS, NB,
+                          ctypes.c_float(float(scale)), _dtype_code(q), _ptr(self.workspace), ws_bytes,
+                          _ptr(status), sp]
         if min_p is None:
             self._samp_fn, self._samp_name = lib.pkv_sample_tokens, "pkv_sample_tokens"
             self._samp = [_ptr(self.tokens), _ptr(logits), B, V, _ptr(temperature), _ptr(top_k), _ptr(top_p),
@@ -412,13 +457,17 @@ class DecodeStep:
         """Enqueue later steps on `stream` (a torch.cuda.Stream)."""
         sp = ctypes.c_void_p(stream.cuda_stream)
         self._attn[-1] = sp
+        if self._append is not None:
+            self._append[-1] = sp
         self._samp[-1] = sp
 
     def run_attention(self) -> torch.Tensor:
         """The append and the attention only; returns out."""
+        if self._append is not None:
+            _raise("pkv_kv_append_q8", self._append_fn(*self._append))
         code = self._attn_fn(*self._attn)
         if code != 0:
-            raise PkvError("pkv_paged_decode_attention_append", code)
+            raise PkvError(self._attn_name, code)
         return self.out
 
     def run_sampler(self) -> torch.Tensor:
@@ -459,21 +508,33 @@ def sample_tokens_typical(logits, temperature, typical_p, seeds, offsets, tokens
     return tokens
 
 
-def copy_blocks(k_cache, v_cache, src, dst, status=None):
+def copy_blocks(k_cache, v_cache, src, dst, status=None, k_scale=None, v_scale=None):
     """Copy physical block src[i] onto dst[i] in both pools (copy-on-write);
-    src / dst are int32 device tensors of equal length."""
+    src / dst are int32 device tensors of equal length.  An 8-bit cache brings
+    its k_scale and v_scale, whose blocks are copied too."""
     NB, Hkv, BS, D = k_cache.shape
     dev = k_cache.device
     _check_cuda("k_cache", k_cache)
     _check_cuda("v_cache", v_cache, k_cache.dtype, k_cache.shape, dev)
+    if k_cache.dtype in _CODES_Q8:
+        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
+        dtype_code = _CODES_Q8[k_cache.dtype]
+    else:
+        if k_scale is not None or v_scale is not None:
+            raise TypeError("k_scale and v_scale belong to an 8-bit cache")
+        dtype_code = _dtype_code(k_cache)
     n = src.shape[0]
     _check_cuda("src", src, torch.int32, (n,), dev)
     _check_cuda("dst", dst, torch.int32, (n,), dev)
     if status is not None:
         _check_cuda("status", status, torch.int32, (1,), dev)
     code = load_library().pkv_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(src), _ptr(dst), n, Hkv, D, BS, NB,
-                                          _dtype_code(k_cache), _ptr(status), _stream(dev))
+                                          dtype_code, _ptr(status), _stream(dev))
     _raise("pkv_copy_blocks", code)
+    if k_scale is not None:
+        code = load_library().pkv_copy_blocks(_ptr(k_scale), _ptr(v_scale), _ptr(src), _ptr(dst), n, Hkv, 1, BS, NB,
+                                              PKV_F32, _ptr(status), _stream(dev))
+        _raise("pkv_copy_blocks", code)
 
 
 class BlockPool:
@@ -653,3 +714,236 @@ def paged_prefill_attention(q, k_cache, v_cache, block_tables, seq_lens, q_start
                                                       _dtype_code(q), _ptr(status), _stream(dev))
     _raise("pkv_paged_prefill_attention", code)
     return out
+
+
+# ---------------------------------------------------------------- 8-bit cache
+# These calls sit in decode loops whose kernels take a few microseconds, so a
+# good argument is recognised with a few attribute reads, and _check_cuda names
+# what is wrong with a bad one.
+def _expect(name, t, dtype, shape, dev):
+    if (type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or t.device != dev
+            or not t.is_contiguous()):
+        _check_cuda(name, t, dtype, shape, dev)
+
+
+def _expect_tables(block_tables, seq_lens, B, dev):
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [B, max_blocks_per_seq]")
+    _expect("block_tables", block_tables, torch.int32, block_tables.shape, dev)
+    _expect("seq_lens", seq_lens, torch.int32, (B,), dev)
+
+
+def _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev):
+    if k_cache.dtype not in _CODES_Q8:
+        raise TypeError(f"k_cache must be torch.float8_e4m3fn or torch.int8, got {k_cache.dtype}")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_blocks, Hkv, block_size, D]")
+    if dev.type != "cuda":
+        raise ValueError("k_cache must be a CUDA tensor")
+    shape = k_cache.shape
+    _expect("k_cache", k_cache, k_cache.dtype, shape, dev)
+    _expect("v_cache", v_cache, k_cache.dtype, shape, dev)
+    _expect("k_scale", k_scale, torch.float32, shape[:3], dev)
+    _expect("v_scale", v_scale, torch.float32, shape[:3], dev)
+
+
+def _status_ptr(status, dev):
+    if status is None:
+        return None
+    _expect("status", status, torch.int32, (1,), dev)
+    return status.data_ptr()
+
+
+def _code_of(t):
+    code = _CODES.get(t.dtype)
+    return _dtype_code(t) if code is None else code
+
+
+def _launch(name, dev, *args):
+    """Call the library's `name` on the current stream of `dev`, with `dev` current."""
+    fn = getattr(_lib or load_library(), name)
+    if torch.cuda.current_device() == dev.index:
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if code != 0:
+        raise PkvError(name, code)
+
+
+def _append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, q_start, status):
+    dev = k_cache.device
+    _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
+    NB, Hkv, BS, D = k_cache.shape
+    B = seq_lens.shape[0]
+    T = B if q_start is None else k_new.shape[0]
+    code = _code_of(k_new)
+    _expect("k_new", k_new, k_new.dtype, (T, Hkv, D), dev)
+    _expect("v_new", v_new, k_new.dtype, (T, Hkv, D), dev)
+    _expect_tables(block_tables, seq_lens, B, dev)
+    if q_start is not None:
+        _expect("q_start", q_start, torch.int32, (B + 1,), dev)
+    _launch("pkv_kv_append_q8", dev, k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+            seq_lens.data_ptr(), None if q_start is None else q_start.data_ptr(), B, T, Hkv, D, BS, NB, code,
+            _CODES_Q8[k_cache.dtype], _status_ptr(status, dev))
+
+
+def kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, status=None):
+    """kv_append into an 8-bit cache: k_new/v_new [B, Hkv, D] (float32 or
+    bfloat16) quantised row by row at position seq_lens[b]-1."""
+    _append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, None, status)
+
+
+def kv_append_chunk_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, q_start,
+                       status=None):
+    """kv_append_chunk into an 8-bit cache (packed rows as there)."""
+    if q_start is None:
+        raise TypeError("q_start must be a torch.Tensor")
+    _append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, q_start, status)
+
+
+def kv_read_blocks_q8(k_cache, v_cache, k_scale, v_scale, blocks, k_out=None, v_out=None, dtype=torch.bfloat16,
+                      status=None):
+    """Blocks `blocks` (int32 [n]) of an 8-bit cache as an unquantised pool:
+    returns (k, v) [n, Hkv, block_size, D] in `dtype` (that of k_out if given)."""
+    dev = k_cache.device
+    _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
+    NB, Hkv, BS, D = k_cache.shape
+    n = blocks.shape[0]
+    _expect("blocks", blocks, torch.int32, (n,), dev)
+    if k_out is None:
+        k_out = torch.empty((n, Hkv, BS, D), dtype=dtype if v_out is None else v_out.dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty_like(k_out)
+    code = _code_of(k_out)
+    _expect("k_out", k_out, k_out.dtype, (n, Hkv, BS, D), dev)
+    _expect("v_out", v_out, k_out.dtype, (n, Hkv, BS, D), dev)
+    _launch("pkv_kv_read_blocks_q8", dev, k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), blocks.data_ptr(), n, Hkv, D, BS, NB, code,
+            _CODES_Q8[k_cache.dtype], _status_ptr(status, dev))
+    return k_out, v_out
+
+
+def decode_q8_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, num_sms: int = 0) -> int:
+    return int(load_library().pkv_decode_q8_workspace_bytes(B, Hq, Hkv, D, num_sms))
+
+
+def paged_decode_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, out=None,
+                              scale: float = 0.0, workspace=None, status=None):
+    """paged_decode_attention over an 8-bit cache; q [B, Hq, D] float32 or
+    bfloat16; returns out [B, Hq, D].  Without `workspace` one is allocated for
+    the call, so calls on several streams, or captured in several graphs, do not
+    share it."""
+    dev = k_cache.device
+    _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
+    NB, Hkv, BS, D = k_cache.shape
+    B, Hq = q.shape[0], q.shape[1]
+    code = _code_of(q)
+    _expect("q", q, q.dtype, (B, Hq, D), dev)
+    _expect_tables(block_tables, seq_lens, B, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _expect("out", out, q.dtype, q.shape, dev)
+    if workspace is None:
+        lib = _lib or load_library()
+        sms = torch.cuda.get_device_properties(dev).multi_processor_count
+        need = lib.pkv_decode_q8_workspace_bytes(B, Hq, Hkv, D, sms)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        ws_bytes = need
+    else:
+        _check_cuda("workspace", workspace, device=dev)
+        ws_bytes = workspace.numel() * workspace.element_size()
+    _launch("pkv_paged_decode_attention_q8", dev, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], seq_lens.data_ptr(), B, Hq, Hkv, D, BS, NB, scale, code,
+            _CODES_Q8[k_cache.dtype], workspace.data_ptr(), ws_bytes, _status_ptr(status, dev))
+    return out
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, inv_freq=None, device="cuda") -> torch.Tensor:
+    """The rotation's frequencies for qk_norm_rope_append: int64 [rot_dim / 2],
+    turns per position in units of 2^-64.  Angles per position are
+    base ** (-2 j / rot_dim), or inv_freq (a float64 sequence, for scaled
+    frequencies), taken modulo a whole turn."""
+    if rot_dim < 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be even")
+    if inv_freq is None:
+        inv_freq = [base ** (-2.0 * j / rot_dim) for j in range(rot_dim // 2)]
+    if len(inv_freq) != rot_dim // 2:
+        raise ValueError(f"inv_freq must hold {rot_dim // 2} values")
+    turns = [int(math.ldexp(float(f) / (2.0 * math.pi) % 1.0, 64)) % (1 << 64) for f in inv_freq]
+    return torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def _expect_rows(name, t, dtype, shape, dev):
+    """A [T, H, D] view whose tokens may lie any distance apart; returns that distance."""
+    if (type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or t.device != dev):
+        if not isinstance(t, torch.Tensor) or t.dim() != 3 or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+            raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    T, H, D = shape
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+        raise ValueError(f"{name}: the heads of a token must be dense ([H, D] rows)")
+    if T <= 1:
+        return H * D
+    if st[0] < H * D:
+        raise ValueError(f"{name}: tokens overlap")
+    return st[0]
+
+
+def qk_norm_rope_append(q, k_new, v_new, q_weight, k_weight, eps, freqs, k_cache, v_cache, block_tables, seq_lens,
+                        q_start=None, k_scale=None, v_scale=None, interleaved: bool = False, q_out=None,
+                        status=None):
+    """Per-head RMS norm (weights [D] or None) and rotation (freqs from
+    rope_freqs, or None) of the queries and keys of the new tokens, and the
+    append of keys and values, in one pass; returns the prepared queries [T, Hq, D].
+
+    q [T, Hq, D], k_new / v_new [T, Hkv, D] (float32 or bfloat16; tokens may be
+    any distance apart, so views of one projection output will do).  T is B (one
+    token per sequence) or, with q_start, the packed chunks of kv_append_chunk.
+    The cache is of q's type, or an 8-bit one with its k_scale and v_scale."""
+    dev = k_cache.device
+    NB, Hkv, BS, D = k_cache.shape
+    code = _code_of(q)
+    if k_scale is None and v_scale is None:
+        if dev.type != "cuda":
+            raise ValueError("k_cache must be a CUDA tensor")
+        cache_code = code
+        _expect("k_cache", k_cache, q.dtype, k_cache.shape, dev)
+        _expect("v_cache", v_cache, q.dtype, k_cache.shape, dev)
+    else:
+        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
+        cache_code = _CODES_Q8[k_cache.dtype]
+    B, T, Hq = seq_lens.shape[0], q.shape[0], q.shape[1]
+    if q_start is not None:
+        _expect("q_start", q_start, torch.int32, (B + 1,), dev)
+    elif T != B:
+        raise ValueError(f"q has {T} tokens for {B} sequences: pass q_start")
+    qs = _expect_rows("q", q, q.dtype, (T, Hq, D), dev)
+    ks = _expect_rows("k_new", k_new, q.dtype, (T, Hkv, D), dev)
+    vs = _expect_rows("v_new", v_new, q.dtype, (T, Hkv, D), dev)
+    if q_weight is not None:
+        _expect("q_weight", q_weight, q.dtype, (D,), dev)
+    if k_weight is not None:
+        _expect("k_weight", k_weight, q.dtype, (D,), dev)
+    rot = 0
+    if freqs is not None:
+        rot = 2 * freqs.shape[0]
+        _expect("freqs", freqs, torch.int64, (rot // 2,), dev)
+    _expect_tables(block_tables, seq_lens, B, dev)
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+    else:
+        _expect("q_out", q_out, q.dtype, (T, Hq, D), dev)
+    _launch("pkv_qk_norm_rope_append", dev, q_out.data_ptr(), q.data_ptr(), qs, k_new.data_ptr(), ks,
+            v_new.data_ptr(), vs, None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), eps, None if freqs is None else freqs.data_ptr(), rot,
+            interleaved, k_cache.data_ptr(), v_cache.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+            None if v_scale is None else v_scale.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
+            seq_lens.data_ptr(), None if q_start is None else q_start.data_ptr(), B, T, Hq, Hkv, D, BS, NB, code,
+            cache_code, _status_ptr(status, dev))
+    return q_out

@@ -88,11 +88,12 @@ pkv_status pkv_kv_append(const void* k_new, const void* v_new, void* k_cache, vo
 pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const int32_t* src, const int32_t* dst, int n_pairs,
                            int Hkv, int D, int block_size, int num_blocks, pkv_dtype dtype, int32_t* dev_status,
                            void* stream) {
-    if (n_pairs < 0 || Hkv < 1 || D < 1 || block_size < 1 || num_blocks < 1 || !dtype_ok(dtype))
+    if (n_pairs < 0 || Hkv < 1 || D < 1 || block_size < 1 || num_blocks < 1 ||
+        (!dtype_ok(dtype) && dtype != PKV_E4M3 && dtype != PKV_I8))
         return PKV_ERR_INVALID_ARG;
     if (n_pairs == 0) return PKV_OK;
     if (!k_cache || !v_cache || !src || !dst) return PKV_ERR_INVALID_ARG;
-    const long long es = dtype == PKV_F32 ? 4 : 2;
+    const long long es = dtype == PKV_F32 ? 4 : dtype == PKV_BF16 ? 2 : 1;
     const long long block_bytes = static_cast<long long>(Hkv) * block_size * D * es;
     return cuda_status(pkv::launch_copy_blocks(k_cache, v_cache, src, dst, n_pairs, block_bytes, num_blocks,
                                                dev_status, static_cast<cudaStream_t>(stream)));

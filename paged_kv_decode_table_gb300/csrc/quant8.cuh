@@ -1,0 +1,67 @@
+// quant8.cuh -- the 8-bit row format of the quantised KV cache.
+//
+// A cached K or V row (one token, one KV head, D values) is stored as D 8-bit
+// values and one float32 scale:
+//   scale = max(amax * (1 / Q), 2^-64),  value_i = rne(x_i * (1 / scale)),
+//   x_i ~ value_i * scale,
+// with Q the type's largest number: 448 for e4m3 (floating, 3 mantissa bits),
+// 127 for int8.  Every operation above is a float32 operation rounded once, so
+// the bytes are the same on every path that stores a row.  The scale is taken per
+// row because a row is what a token writes and what attention reads as a whole:
+// appending needs no other token's data, and in attention the K scale multiplies
+// a score and the V scale a softmax weight, never a single element.  The floor
+// 2^-64 keeps 1 / scale finite for rows that are all zero.  x_i * (1 / scale) can
+// exceed Q by a rounding of the product; both conversions saturate.
+// A row that holds a NaN or an infinity is stored as zeros with scale NaN.
+#pragma once
+
+#include "pkv_common.cuh"
+
+namespace pkv {
+
+constexpr float kMinScale = 5.421010862427522e-20f;  // 2^-64
+
+struct FmtNone {  // rows kept in their own type
+    static constexpr bool kQuant = false;
+};
+
+struct FmtE4M3 {
+    static constexpr bool kQuant = true;
+    static constexpr float kInvQ = 1.0f / 448.0f;
+    // two floats -> two bytes (lo in bits 0-7)
+    static __device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+        uint16_t v;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
+        return v;
+    }
+    // bytes 0, 1 of v -> two halves (exact: every e4m3 number is a half)
+    static __device__ __forceinline__ uint32_t decode2(uint16_t v) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+        return r;
+    }
+    static __device__ __forceinline__ float decode(uint8_t v) {
+        const uint32_t h = decode2(v);
+        float f;
+        asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.f32.f16 %0, lo;}" : "=f"(f) : "r"(h));
+        return f;
+    }
+};
+
+struct FmtI8 {
+    static constexpr bool kQuant = true;
+    static constexpr float kInvQ = 1.0f / 127.0f;
+    static __device__ __forceinline__ uint32_t encode(float x) {
+        return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(x), -127.f), 127.f))) & 0xffu;
+    }
+    static __device__ __forceinline__ uint32_t encode2(float lo, float hi) { return encode(lo) | encode(hi) << 8; }
+    static __device__ __forceinline__ float decode(uint8_t v) {
+        return static_cast<float>(static_cast<int8_t>(v));
+    }
+};
+
+__device__ __forceinline__ float row_scale(float amax, float inv_q) {
+    return fmaxf(__fmul_rn(amax, inv_q), kMinScale);
+}
+
+}  // namespace pkv
