@@ -879,7 +879,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-static EncodeTiledFn get_encode_fn() {
+EncodeTiledFn get_encode_fn() {
     static EncodeTiledFn fn = nullptr;
     static bool tried = false;
     if (!tried) {
@@ -939,7 +939,7 @@ int device_sm_count() {
     return n;
 }
 
-static int max_optin_smem() {
+int max_optin_smem() {
     int dev = 0, n = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&n, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
@@ -982,6 +982,8 @@ cudaError_t launch_kv_append(const void* k_new, const void* v_new, void* k_cache
 // budget of the fast kernel's waits and the CTA whose loader stays silent.
 static std::atomic<uint32_t> g_wait_polls{kMaxWaitIters};
 static std::atomic<int> g_silent_cta{-1};
+uint32_t attention_wait_polls() { return g_wait_polls.load(); }
+int attention_silent_cta() { return g_silent_cta.load(); }
 
 // k_new / v_new non-null: append each sequence's new token first (same result
 // as launch_kv_append followed by attention).  The fast kernel does the append

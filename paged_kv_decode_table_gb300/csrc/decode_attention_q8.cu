@@ -6,15 +6,781 @@
 // float32 scales (quant8.cuh): a K scale multiplies a score, a V scale a
 // softmax weight.
 //
-// One CTA per (sequence, query head), CUDA-core fp32, chunked online softmax.
+// Fast path (D a multiple of 16 up to 128, block size a multiple of 16): a
+// persistent kernel, one CTA per SM, over balanced ranges, and a kernel that
+// joins the sequences that several ranges share.
+//  * A tile is 16 positions of one KV head.  A step is `slots` tiles of
+//    consecutive positions of `HG` KV heads (at most 8 tiles), fetched by TMA
+//    boxes (16 positions x HG heads of K, of V and of their scales) into one
+//    stage of an mbarrier ring.  The steps of all (sequence, head group) pairs, one
+//    after the other, are cut into one range per CTA; every CTA finds its range
+//    itself from seq_lens.
+//  * One consumer warp per (KV head, chunk of its query heads, slot) takes one
+//    tile of every step: with 8 KV heads the 8 warps are the heads, with one head
+//    they are 8 slots along the cache, so a model split over devices keeps every
+//    warp busy.  The slots' results are merged in shared memory when the range
+//    leaves the sequence.
+//  * The 8-bit numbers become float16 in registers (exact for both types) and
+//    both products run on mma.sync m16n8k16 with float32 accumulation.  K's order
+//    of dimensions inside a 16-byte chunk is permuted the same way in q, so a
+//    4-byte fragment of K is one register; V is read transposed in 16-bit units,
+//    which yields even and odd dimensions of two positions.
+//  * With at most 8 query heads per warp the upper 8 rows of the MMA are free:
+//    they carry what float16 rounding leaves of q and of the weights, so the
+//    result has float32 accuracy at no extra MMA (kSplit).  With 9 to 16 heads
+//    (bf16 only) the rows are heads, the weights plain float16 (2^-11).
+//  * Weights are normalised by the running maximum of s_j + log2(vs_j), the
+//    largest contribution rather than the largest score, so that p_j * vs_j is
+//    at most 1 and fits float16 whatever the V scales are.  Scales below 2^-64
+//    count as 2^-64 there, which bounds p_j by 2^64.
+//  * q is multiplied by a power of two per row that puts its largest element
+//    into [2^14, 2^15).
+// Other shapes: one CTA per (sequence, query head), CUDA-core fp32.
+#include <cuda.h>
 #include <math.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "quant8.cuh"
 
 namespace pkv {
 
 int device_sm_count();
+int max_optin_smem();
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn get_encode_fn();
+uint32_t attention_wait_polls();
+int attention_silent_cta();
 
+// ------------------------------------------------------------------ fast kernel
+constexpr int kQ8MaxStages = 12;
+constexpr int kQ8Tok = 16;  // positions per tile
+constexpr int kQ8Warps = 8;  // consumer warps at most
+
+// How a call is laid out; computed on the host, passed to both kernels.
+struct Q8Plan {
+    int HG, NG;      // KV heads per group, groups
+    int QC;          // chunks of query heads per KV head (8 or 16 heads each)
+    int slots;       // tiles along the cache per step
+    int R;           // query rows per group: HG * G
+    int nst;         // ring stages
+    int stage_bytes, scale_unit, q_bytes, scratch_bytes;
+    int B, Hq, Hkv, G, D, BS, NB, max_blocks;
+    float scale_log2;
+    uint32_t polls;
+    int silent_cta;
+};
+
+struct Q8Info {  // 16 bytes per (sequence, head group) with at least one step
+    int s;       // first step in the global order
+    int n;       // number of steps
+    int W;       // steps per range
+    int pad;
+};
+
+struct Q8Meta {
+    int vb;     // sequence * NG + group
+    int left;   // positions from the step's first one to the end
+    int flags;
+    int pad;
+};
+enum : int { kQFirst = 1, kQLast = 2, kQWhole = 4, kQHead = 8, kQBad = 16 };
+
+__device__ __forceinline__ float ex2f(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2f(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// two floats -> two halves, lo in bits 0-15
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) {
+    float2 f;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(v));
+    return f;
+}
+__device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void store_row4(__nv_bfloat16* p, float4 v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+__device__ __forceinline__ void store_row4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+
+// Steps of sequence b in one head group (0 for a length outside [0, max_blocks * BS]).
+__device__ __forceinline__ int q8_steps(const int32_t* seq_lens, int b, const Q8Plan& pl) {
+    const int L = seq_lens[b], T = pl.slots * kQ8Tok;
+    return (L >= 0 && static_cast<long long>(L) <= static_cast<long long>(pl.max_blocks) * pl.BS)
+               ? static_cast<int>((static_cast<long long>(L) + T - 1) / T)
+               : 0;
+}
+
+// Sum over the CTA and this thread's exclusive prefix; red holds 33 ints.
+__device__ __forceinline__ int q8_scan(int v, int* red, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) red[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < nw; ++w) {
+        const int r = red[w];
+        if (w < warp) before += r;
+        all += r;
+    }
+    __syncthreads();
+    total = all;
+    return before + x - v;
+}
+
+// Byte offset of 16-byte chunk c of row `row` in a TMA-swizzled tile of rows of DP
+// bytes (128-byte swizzle for rows of 128 bytes, 64-byte swizzle for 64).
+template <int DP>
+__device__ __forceinline__ uint32_t q8_at(int row, int c) {
+    if (DP == 128) return static_cast<uint32_t>(row * 128 + ((c ^ (row & 7)) << 4));
+    return static_cast<uint32_t>(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+}
+
+template <typename T, typename Fmt, int DP, bool kSplit>
+__global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
+    decode_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ CUtensorMap tmKs, const __grid_constant__ CUtensorMap tmVs,
+                     const __grid_constant__ Q8Plan pl, const T* __restrict__ q, T* __restrict__ out,
+                     const int32_t* __restrict__ block_tables, const int32_t* __restrict__ seq_lens,
+                     Q8Info* __restrict__ info, float* __restrict__ part_ml, float* __restrict__ part_o,
+                     int32_t* status) {
+    constexpr int kChunks = DP / 16;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int nst = pl.nst, HG = pl.HG, QC = pl.QC, slots = pl.slots;
+    const int HV = HG * QC, CW = HV * slots;
+    const int tile_bytes = kQ8Tok * DP, unit_bytes = HG * tile_bytes, half_stage = slots * unit_bytes;
+    const int scale_half = slots * pl.scale_unit;
+    uint8_t* scales = smem + static_cast<size_t>(nst) * pl.stage_bytes;
+    uint8_t* qring = scales + static_cast<size_t>(nst) * 2 * scale_half;
+    float* scratch = reinterpret_cast<float*>(qring + 2 * static_cast<size_t>(pl.q_bytes));
+    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(scratch) + pl.scratch_bytes);
+    uint64_t* empty = full + kQ8MaxStages;
+    uint64_t* qfull = empty + kQ8MaxStages;
+    uint64_t* qempty = qfull + 2;
+    uint64_t* mfull = qempty + 2;   // merge slots: one per consumer warp
+    uint64_t* mempty = mfull + kQ8Warps;
+    Q8Meta* meta = reinterpret_cast<Q8Meta*>(mempty + kQ8Warps);
+    int* sch = reinterpret_cast<int*>(meta + kQ8MaxStages);  // [0, 33) scan scratch, 33: b0, 34: s0
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < nst; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], CW);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&qfull[s], 1);
+            mbar_init(&qempty[s], CW);
+        }
+        for (int s = 0; s < kQ8Warps; ++s) {
+            mbar_init(&mfull[s], 1);
+            mbar_init(&mempty[s], 1);
+        }
+        fence_mbar_init();
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+        prefetch_tmap(&tmKs);
+        prefetch_tmap(&tmVs);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Only after the wait: the joining kernel reads seq_lens before its own wait.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- this CTA's range of steps
+    const int nthr = blockDim.x, B = pl.B, NG = pl.NG;
+    const int n_first = static_cast<int>(threadIdx.x) < B ? q8_steps(seq_lens, threadIdx.x, pl) : 0;
+    int tsum = n_first;
+    for (int b = threadIdx.x + nthr; b < B; b += nthr) tsum += q8_steps(seq_lens, b, pl);
+    int total;
+    q8_scan(tsum, sch, total);
+    total *= NG;
+    const int W = total > 0 ? (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x) : 1;
+    const int start = blockIdx.x * W, end = min(total, start + W);
+    if (start >= end) return;  // uniform over the CTA
+    {
+        int carry = 0;
+        for (int base = 0; base < B; base += nthr) {
+            const int b = base + threadIdx.x;
+            const int n = NG * (base == 0 ? n_first : (b < B ? q8_steps(seq_lens, b, pl) : 0));
+            int tot;
+            const int sb = carry + q8_scan(n, sch, tot);
+            if (n > 0 && sb <= start && start < sb + n) {  // exactly one thread of the CTA
+                sch[33] = b;
+                sch[34] = sb;
+            }
+            carry += tot;
+            if (carry > start) break;  // same decision in every thread
+        }
+        __syncthreads();
+    }
+
+    if (warp == CW) {
+        // ------------------------------------------------ producer warp
+        // Lane u fetches the tiles of slot u.  b, g, j: the step's sequence, head
+        // group and index; cn steps per group from cs on.
+        int b = sch[33], cs = sch[34];
+        int cn = q8_steps(seq_lens, b, pl), cL = seq_lens[b], g = 0;
+        while (cs + cn <= start) {
+            cs += cn;
+            ++g;
+        }
+        if (lane == 0) {  // what the join needs of every (sequence, group) that begins in this range
+            int bb = b, gg = g, bs = cs, bn = cn;
+            while (bs < end) {
+                if (bs >= start && bn > 0) {
+                    Q8Info si;
+                    si.s = bs;
+                    si.n = bn;
+                    si.W = W;
+                    si.pad = 0;
+                    info[bb * NG + gg] = si;
+                }
+                bs += bn;
+                if (++gg == NG || bn == 0) {
+                    gg = 0;
+                    if (++bb >= B) break;
+                    bn = q8_steps(seq_lens, bb, pl);
+                }
+            }
+        }
+        if (static_cast<int>(blockIdx.x) == pl.silent_cta) return;  // test hook: no copy is issued
+        const uint32_t unit_tx = 2u * unit_bytes + 2u * HG * (kQ8Tok * 4);
+        int piece = 0;
+        auto block_of = [&](int bb, int jj, int L) {  // lane u: the block of slot u, -2 behind the end
+            const long long pos = (static_cast<long long>(jj) * slots + lane) * kQ8Tok;
+            if (lane >= slots || pos >= L) return -2;
+            const int blk = block_tables[static_cast<size_t>(bb) * pl.max_blocks + pos / pl.BS];
+            return blk >= 0 && blk < pl.NB ? blk : -1;
+        };
+        // on a timeout: wait (bounded) for the copies in flight, so that none writes
+        // into shared memory after the CTA is gone
+        auto drain = [&](int it) {
+            if (lane != 0) return;
+            for (int k = max(0, it - nst); k < it; ++k)
+                mbar_wait(&full[k % nst], static_cast<uint32_t>(k / nst) & 1u, pl.polls);
+            for (int pk = max(0, piece - 2); pk < piece; ++pk)
+                mbar_wait(&qfull[pk & 1], static_cast<uint32_t>(pk >> 1) & 1u, pl.polls);
+        };
+        int blk = block_of(b, start - cs, cL);
+        int stage = 0;
+        uint32_t parity = 1;  // of the empty barriers: the first round finds them free
+        for (int i = start, it = 0; i < end; ++i, ++it) {
+            const int cb = b, cg = g, ccs = cs, ccn = cn, L = cL, j = i - cs, cblk = blk;
+            if (i + 1 < end) {  // the next step's block ids are on their way while this one waits
+                while (cs + cn <= i + 1) {
+                    cs += cn;
+                    if (++g == NG || cn == 0) {
+                        g = 0;
+                        ++b;
+                        cn = q8_steps(seq_lens, b, pl);
+                        cL = seq_lens[b];
+                    }
+                }
+                blk = block_of(b, i + 1 - cs, cL);
+            }
+            const bool first = j == 0 || i == start, last = j == ccn - 1 || i == end - 1;
+            const unsigned live = __ballot_sync(0xffffffffu, cblk >= 0);
+            const bool bad = __any_sync(0xffffffffu, cblk == -1);
+            bool ok = mbar_wait(&empty[stage], parity, pl.polls);
+            if (first && ok) ok = mbar_wait(&qempty[piece & 1], (static_cast<uint32_t>(piece >> 1) & 1u) ^ 1u, pl.polls);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+                drain(it);
+                return;
+            }
+            if (lane == 0) {
+                if (first) {
+                    const int qs = piece & 1;
+                    mbar_arrive_expect_tx(&qfull[qs], pl.q_bytes);
+                    tma_load_1d(qring + static_cast<size_t>(qs) * pl.q_bytes,
+                                q + (static_cast<size_t>(cb) * pl.Hq + static_cast<size_t>(cg) * pl.R) * pl.D,
+                                pl.q_bytes, &qfull[qs]);
+                }
+                Q8Meta mt;
+                mt.vb = cb * NG + cg;
+                mt.left = L - j * slots * kQ8Tok;
+                mt.flags = (first ? kQFirst : 0) | (last ? kQLast : 0) | (ccs >= start && ccs + ccn <= end ? kQWhole : 0) |
+                           (ccs < start ? kQHead : 0) | (bad ? kQBad : 0);
+                mt.pad = 0;
+                meta[stage] = mt;
+                if (bad) report(status, PKV_ERR_DEVICE_BOUNDS);
+                mbar_arrive_expect_tx(&full[stage], __popc(live) * unit_tx);
+            }
+            if (first) ++piece;
+            __syncwarp();
+            if (cblk >= 0) {
+                const int tok = static_cast<int>(((static_cast<long long>(j) * slots + lane) * kQ8Tok) % pl.BS);
+                const int row = cblk * pl.Hkv + cg * HG;
+                uint8_t* kd = smem + static_cast<size_t>(stage) * pl.stage_bytes + lane * unit_bytes;
+                uint8_t* sd = scales + static_cast<size_t>(stage) * 2 * scale_half + lane * pl.scale_unit;
+                tma_load_3d(kd, &tmK, 0, tok, row, &full[stage]);
+                tma_load_2d(sd, &tmKs, tok, row, &full[stage]);
+                tma_load_3d(kd + half_stage, &tmV, 0, tok, row, &full[stage]);
+                tma_load_2d(sd + scale_half, &tmVs, tok, row, &full[stage]);
+            }
+            if (++stage == nst) {
+                stage = 0;
+                parity ^= 1u;
+            }
+        }
+        return;
+    }
+
+    // ---------------------------------------------------- consumers
+    const int slot = warp / HV, vh = warp - slot * HV, hh = vh / QC, qc = vh - hh * QC;
+    const int g = lane >> 2, r = lane & 3, mi = lane >> 3, rr = lane & 7;
+    constexpr int kRows = kSplit ? 8 : 16;
+    const int row0 = qc * kRows + g, row1 = row0 + 8;     // query heads of this KV head
+    const bool live0 = row0 < pl.G, live1 = !kSplit && row1 < pl.G;
+    float O[kChunks][2][4];  // [16-dim chunk][even, odd dims][row g: 2 dims, row g + 8 (or the remainder): 2 dims]
+    uint32_t qa[kChunks][4];
+    float smul0 = 0.f, smul1 = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    bool poisoned = false;
+    int piece = 0, stage = 0;
+    uint32_t parity = 0;
+    const uint32_t smem_base = smem_u32(smem);
+    const int tile_off = (slot * HG + hh) * tile_bytes;
+    const int scale_off = slot * pl.scale_unit + hh * (kQ8Tok * 4);
+    // ldmatrix: lane group mi gives the rows of matrix mi: (positions 8 (mi & 1) ..,
+    // chunk + (mi >> 1))
+    const int lm_row = (mi & 1) * 8 + rr, lm_chunk = mi >> 1;
+
+    // one row of q, as float16 (and its float16 remainder), scaled by a power of two
+    auto load_q = [&](const T* row, bool live, float& smul, int lo_reg) {
+        float x[kChunks][4];
+        float amax = 0.f;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int d = c * 16 + 4 * r;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[c][e] = live && d < pl.D ? to_f32(row[d + e]) : 0.f;
+                amax = fmaxf(amax, fabsf(x[c][e]));
+            }
+        }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const int e = max(static_cast<int>(__float_as_uint(amax) >> 23), 27);  // biased exponent, at least 2^-100
+        // amax in [2^(e-127), 2^(e-126)) -> [2^14, 2^15); infinite amax: exponent 255
+        const float fac = __uint_as_float(static_cast<uint32_t>(max(268 - e, 1)) << 23);
+        smul = __uint_as_float(static_cast<uint32_t>(min(e - 14, 253)) << 23) * pl.scale_log2;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const float a = x[c][2 * p] * fac, b = x[c][2 * p + 1] * fac;
+                const uint32_t hi = pack_f16x2(a, b);
+                qa[c][2 * p + lo_reg] = hi;
+                if (kSplit) {
+                    const float2 f = unpack_f16x2(hi);
+                    qa[c][2 * p + 1] = pack_f16x2(a - f.x, b - f.y);
+                }
+            }
+    };
+
+    for (int i = start; i < end; ++i) {
+        if (!mbar_wait(&full[stage], parity, pl.polls)) {
+            if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+            return;
+        }
+        const Q8Meta mt = meta[stage];
+        if (mt.flags & kQFirst) {
+            const int qs = piece & 1;
+            if (!mbar_wait(&qfull[qs], static_cast<uint32_t>(piece >> 1) & 1u, pl.polls)) {
+                if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+                return;
+            }
+            const T* qsm = reinterpret_cast<const T*>(qring + static_cast<size_t>(qs) * pl.q_bytes) +
+                           static_cast<size_t>(hh * pl.G) * pl.D;
+            load_q(qsm + row0 * pl.D, live0, smul0, 0);
+            if (!kSplit) load_q(qsm + row1 * pl.D, live1, smul1, 1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&qempty[qs]);
+            m0 = m1 = -INFINITY;
+            l0 = l1 = 0.f;
+            poisoned = false;
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) O[c][p][0] = O[c][p][1] = O[c][p][2] = O[c][p][3] = 0.f;
+        }
+        const int ntok = mt.left - slot * kQ8Tok;  // positions in this warp's tile (may be more than 16, or none)
+        poisoned = poisoned || (mt.flags & kQBad);
+        if (ntok > 0 && !poisoned) {
+            const uint32_t kb = smem_base + static_cast<uint32_t>(stage) * pl.stage_bytes + tile_off;
+            const uint32_t vb = kb + half_stage;
+            const float* ks = reinterpret_cast<const float*>(scales + static_cast<size_t>(stage) * 2 * scale_half + scale_off);
+            const float* vs = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(ks) + scale_half);
+            // ---- S = Q K^T: two n-tiles of 8 positions
+            float s[2][4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+            for (int c = 0; c < kChunks; c += 2) {
+                uint32_t w[4], lo, hi;
+                ldmatrix_x4(w[0], w[1], w[2], w[3], kb + q8_at<DP>(lm_row, c + lm_chunk));
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    Fmt::decode4(w[u], lo, hi);
+                    mma_f16_16816(s[u & 1], qa[c + (u >> 1)], lo, hi);
+                }
+            }
+            // ---- online softmax in the log2 domain, normalised by the largest p_j vs_j
+            float x0[4], x1[4], vsc[4];  // position 8 (e >> 1) + 2 r + (e & 1)
+            float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float2 k2 = *reinterpret_cast<const float2*>(ks + 8 * t + 2 * r);
+                const float2 v2 = *reinterpret_cast<const float2*>(vs + 8 * t + 2 * r);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const bool in = 8 * t + 2 * r + e < ntok;
+                    const float kk = e ? k2.y : k2.x, vv = e ? v2.y : v2.x;
+                    const float lg = lg2f(fmaxf(fabsf(vv), kMinScale));
+                    vsc[2 * t + e] = in ? vv : 0.f;
+                    const float a0 = (kSplit ? s[t][e] + s[t][2 + e] : s[t][e]) * (smul0 * kk);
+                    x0[2 * t + e] = in ? a0 : -INFINITY;
+                    mx0 = fmaxf(mx0, in ? a0 + lg : -INFINITY);
+                    if (!kSplit) {
+                        const float a1 = s[t][2 + e] * (smul1 * kk);
+                        x1[2 * t + e] = in ? a1 : -INFINITY;
+                        mx1 = fmaxf(mx1, in ? a1 + lg : -INFINITY);
+                    }
+                }
+            }
+            auto renew = [](float& m, float mx, float& mu) {  // new maximum, and the factor of what was summed so far
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float mn = fmaxf(m, mx);
+                mu = mn == -INFINITY ? 0.f : mn;
+                const float a = ex2f(m - mu);
+                m = mn;
+                return a;
+            };
+            float mu0, mu1 = 0.f, al0 = renew(m0, mx0, mu0), al1 = 1.f;
+            if (!kSplit) al1 = renew(m1, mx1, mu1);
+            uint32_t pa[4];
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float p0 = ex2f(x0[2 * t] - mu0), p1 = ex2f(x0[2 * t + 1] - mu0);
+                sum0 += p0 + p1;
+                const float w0 = p0 * vsc[2 * t], w1 = p1 * vsc[2 * t + 1];
+                const uint32_t hi = pack_f16x2(w0, w1);
+                pa[2 * t] = hi;
+                if (kSplit) {
+                    const float2 f = unpack_f16x2(hi);
+                    pa[2 * t + 1] = pack_f16x2(w0 - f.x, w1 - f.y);
+                } else {
+                    const float y0 = ex2f(x1[2 * t] - mu1), y1 = ex2f(x1[2 * t + 1] - mu1);
+                    sum1 += y0 + y1;
+                    pa[2 * t + 1] = pack_f16x2(y0 * vsc[2 * t], y1 * vsc[2 * t + 1]);
+                }
+            }
+            l0 = fmaf(l0, al0, sum0);
+            l1 = fmaf(l1, al1, sum1);
+            if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
+                const float b1 = kSplit ? al0 : al1;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        O[c][p][0] *= al0;
+                        O[c][p][1] *= al0;
+                        O[c][p][2] *= b1;
+                        O[c][p][3] *= b1;
+                    }
+            }
+            // ---- O += P V.  Positions behind the end have weight 0; their bytes are
+            // cleared because an e4m3 NaN would survive the product.
+            uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+            if (ntok < kQ8Tok) {
+                keep0 = (2 * r < ntok ? 0xffffu : 0u) | (2 * r + 1 < ntok ? 0xffff0000u : 0u);
+                keep1 = (2 * r + 8 < ntok ? 0xffffu : 0u) | (2 * r + 9 < ntok ? 0xffff0000u : 0u);
+            }
+#pragma unroll
+            for (int c = 0; c < kChunks; c += 2) {
+                uint32_t w[4];
+                ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vb + q8_at<DP>(lm_row, c + lm_chunk));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t e0, o0, e1, o1;
+                    Fmt::decode4_pairs(w[2 * u] & keep0, e0, o0);
+                    Fmt::decode4_pairs(w[2 * u + 1] & keep1, e1, o1);
+                    mma_f16_16816(O[c + u][0], pa, e0, e1);
+                    mma_f16_16816(O[c + u][1], pa, o0, o1);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (++stage == nst) {
+            stage = 0;
+            parity ^= 1u;
+        }
+        if (!(mt.flags & kQLast)) continue;
+
+        // ---------------------------------------------- the range leaves (sequence, group) mt.vb
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        // row g, dims 16 c + 4 r .. + 3 (row 1: row g + 8)
+        auto value = [&](int c, int row) {
+            const int k = 2 * row;
+            float4 v = make_float4(O[c][0][k], O[c][1][k], O[c][0][k + 1], O[c][1][k + 1]);
+            if (kSplit) {
+                v.x += O[c][0][2];
+                v.y += O[c][1][2];
+                v.z += O[c][0][3];
+                v.w += O[c][1][3];
+            }
+            return v;
+        };
+        if (slots > 1) {
+            // merge the slots: at distance d = slots / 2, .., 1 warp slot in [d, 2d) hands its result
+            // to slot - d through its own scratch tile.  Each wait is bounded.
+            constexpr int kTile = kRows * DP + 2 * kRows;
+            const uint32_t ph = static_cast<uint32_t>(piece) & 1u;
+            bool sent = false;
+            for (int d = slots >> 1; d > 0; d >>= 1) {
+                if (slot >= 2 * d) continue;
+                if (slot >= d) {
+                    float* t = scratch + ((slot - 1) * HV + vh) * kTile;
+                    if (!mbar_wait(&mempty[warp], ph ^ 1u, pl.polls)) {
+                        if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+                        return;
+                    }
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        *reinterpret_cast<float4*>(t + g * DP + c * 16 + 4 * r) = value(c, 0);
+                        if (!kSplit) *reinterpret_cast<float4*>(t + (g + 8) * DP + c * 16 + 4 * r) = value(c, 1);
+                    }
+                    if (r == 0) {
+                        *reinterpret_cast<float2*>(t + kRows * DP + 2 * g) = make_float2(m0, l0);
+                        if (!kSplit) *reinterpret_cast<float2*>(t + kRows * DP + 2 * (g + 8)) = make_float2(m1, l1);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&mfull[warp]);
+                    sent = true;
+                    break;
+                }
+                const int from = warp + d * HV;
+                const float* t = scratch + ((slot + d - 1) * HV + vh) * kTile;
+                if (!mbar_wait(&mfull[from], ph, pl.polls)) {
+                    if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+                    return;
+                }
+                auto join = [](float& m, float& l, float2 ml, float& fb) {
+                    const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+                    const float fa = ex2f(m - mu);
+                    fb = ex2f(ml.x - mu);
+                    l = l * fa + ml.y * fb;
+                    m = mn;
+                    return fa;
+                };
+                float fb0, fb1 = 0.f;
+                const float fa0 = join(m0, l0, *reinterpret_cast<const float2*>(t + kRows * DP + 2 * g), fb0);
+                float fa1 = fa0;
+                if (!kSplit) fa1 = join(m1, l1, *reinterpret_cast<const float2*>(t + kRows * DP + 2 * (g + 8)), fb1);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const float4 a = *reinterpret_cast<const float4*>(t + g * DP + c * 16 + 4 * r);
+                    O[c][0][0] = fmaf(O[c][0][0], fa0, a.x * fb0);
+                    O[c][1][0] = fmaf(O[c][1][0], fa0, a.y * fb0);
+                    O[c][0][1] = fmaf(O[c][0][1], fa0, a.z * fb0);
+                    O[c][1][1] = fmaf(O[c][1][1], fa0, a.w * fb0);
+                    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (!kSplit) z = *reinterpret_cast<const float4*>(t + (g + 8) * DP + c * 16 + 4 * r);
+                    O[c][0][2] = fmaf(O[c][0][2], fa1, z.x * fb1);
+                    O[c][1][2] = fmaf(O[c][1][2], fa1, z.y * fb1);
+                    O[c][0][3] = fmaf(O[c][0][3], fa1, z.z * fb1);
+                    O[c][1][3] = fmaf(O[c][1][3], fa1, z.w * fb1);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&mempty[from]);
+            }
+            ++piece;
+            if (sent) continue;
+        } else {
+            ++piece;
+        }
+#pragma unroll
+        for (int row = 0; row < (kSplit ? 1 : 2); ++row) {
+            if (!(row ? live1 : live0)) continue;
+            const int qr = hh * pl.G + (row ? row1 : row0);  // row in the group
+            const float m = row ? m1 : m0, l = row ? l1 : l0;
+            if (mt.flags & kQWhole) {
+                const float inv = poisoned || l == 0.f ? 0.f : 1.f / l;
+                T* o = out + (static_cast<size_t>(mt.vb) * pl.R + qr) * pl.D;
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const int d = c * 16 + 4 * r;
+                    if (d >= pl.D) continue;
+                    const float4 v = value(c, row);
+                    if (poisoned)
+                        store_row4(o + d, make_float4(0.f, 0.f, 0.f, 0.f));
+                    else
+                        store_row4(o + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+                }
+            } else {
+                const size_t at = (2 * static_cast<size_t>(blockIdx.x) + ((mt.flags & kQHead) ? 0 : 1)) * pl.R + qr;
+                if (r == 0) *reinterpret_cast<float2*>(part_ml + 2 * at) = make_float2(m, poisoned ? -1.f : l);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const int d = c * 16 + 4 * r;
+                    if (d < pl.D) *reinterpret_cast<float4*>(part_o + at * pl.D + d) = value(c, row);
+                }
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ join
+// M = max m_c, out = sum o_c 2^(m_c - M) / sum l_c 2^(m_c - M) over the pieces of
+// a sequence that several ranges share: the piece of its first range f in slot
+// 2f + 1, of a later range c in slot 2c.  kUnitWarps warps per (sequence, query
+// head): one where there are many, four (over the pieces) where there are few.
+// Sequences within one range were written by the main kernel; empty and invalid
+// ones get zeros here.
+constexpr int kJoinWarps = 4;
+constexpr int kJoinGroup = 8;
+
+template <typename T, int kUnitWarps>
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    decode_q8_join_kernel(const __grid_constant__ Q8Plan pl, const Q8Info* __restrict__ info,
+                          const int32_t* __restrict__ seq_lens, const float* __restrict__ part_ml,
+                          const float* __restrict__ part_o, T* __restrict__ out, int P, int32_t* status) {
+    __shared__ float4 accsh[kJoinWarps][32];
+    __shared__ float mlsh[kJoinWarps][2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long units = static_cast<long long>(pl.B) * pl.Hq;
+    const long long u = static_cast<long long>(blockIdx.x) * (kJoinWarps / kUnitWarps) + warp / kUnitWarps;
+    const int w0 = warp % kUnitWarps;
+    const bool in = u < units;
+    const int b = in ? static_cast<int>(u / pl.Hq) : 0;
+    const long long vb = in ? u / pl.R : 0;
+    const int row = in ? static_cast<int>(u - vb * pl.R) : 0;
+    const int L = seq_lens[b];  // older than the main kernel, so read before the wait
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const bool valid = L >= 0 && static_cast<long long>(L) <= static_cast<long long>(pl.max_blocks) * pl.BS;
+    if (in && !valid && u % pl.Hq == 0 && w0 == 0 && lane == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
+    int pieces = 0, f = 0;
+    if (in && valid && L > 0) {
+        const Q8Info si = info[vb];
+        if (si.W > 0 && si.s >= 0 && si.n > 0) {
+            f = si.s / si.W;
+            pieces = (si.s + si.n - 1) / si.W - f + 1;
+        }
+        // a record that names slots outside the workspace (possible only when the
+        // main kernel gave up on a wait) joins nothing
+        if (f + pieces > P) pieces = 0;
+    }
+    const bool write = in && pieces != 1;
+    if (kUnitWarps == 1 && !write) return;
+    if (pieces == 1) pieces = 0;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, l = 0.f;
+    const bool col = 4 * lane < pl.D;
+    // pieces w0, w0 + kUnitWarps, ..: kJoinGroup of them in flight
+    for (int p0 = w0; p0 < pieces; p0 += kUnitWarps * kJoinGroup) {
+        float2 ml[kJoinGroup];
+        float4 o[kJoinGroup];
+#pragma unroll
+        for (int k = 0; k < kJoinGroup; ++k) {
+            const int p = p0 + k * kUnitWarps;
+            const size_t at = (static_cast<size_t>(2 * (f + p) + (p == 0 ? 1 : 0))) * pl.R + row;
+            ml[k] = p < pieces ? __ldg(reinterpret_cast<const float2*>(part_ml + 2 * at)) : make_float2(-INFINITY, 0.f);
+            o[k] = p < pieces && col ? __ldg(reinterpret_cast<const float4*>(part_o + at * pl.D + 4 * lane))
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float mn = M;
+#pragma unroll
+        for (int k = 0; k < kJoinGroup; ++k) mn = fmaxf(mn, ml[k].x);
+        const float mu = mn == -INFINITY ? 0.f : mn, fa = ex2f(M - mu);
+        bool bad = l < 0.f;
+        l *= fa;
+        acc = make_float4(acc.x * fa, acc.y * fa, acc.z * fa, acc.w * fa);
+        M = mn;
+#pragma unroll
+        for (int k = 0; k < kJoinGroup; ++k) {
+            const float w = ex2f(ml[k].x - mu);
+            bad = bad || ml[k].y < 0.f;
+            l = fmaf(ml[k].y, w, l);
+            acc.x = fmaf(o[k].x, w, acc.x);
+            acc.y = fmaf(o[k].y, w, acc.y);
+            acc.z = fmaf(o[k].z, w, acc.z);
+            acc.w = fmaf(o[k].w, w, acc.w);
+        }
+        if (bad) l = -INFINITY;  // stays: a poisoned piece makes the row zero
+    }
+    if (kUnitWarps > 1) {
+        accsh[warp][lane] = acc;
+        if (lane == 0) {
+            mlsh[warp][0] = M;
+            mlsh[warp][1] = l;
+        }
+        __syncthreads();
+        if (w0 != 0 || !write) return;
+        float mn = M;
+        for (int w = 1; w < kUnitWarps; ++w) mn = fmaxf(mn, mlsh[warp + w][0]);
+        const float mu = mn == -INFINITY ? 0.f : mn;
+        bool bad = l < 0.f;
+        const float fa = ex2f(M - mu);
+        l *= fa;
+        acc = make_float4(acc.x * fa, acc.y * fa, acc.z * fa, acc.w * fa);
+        for (int w = 1; w < kUnitWarps; ++w) {
+            const float f2 = ex2f(mlsh[warp + w][0] - mu);
+            const float4 o = accsh[warp + w][lane];
+            bad = bad || mlsh[warp + w][1] < 0.f;
+            l = fmaf(mlsh[warp + w][1], f2, l);
+            acc.x = fmaf(o.x, f2, acc.x);
+            acc.y = fmaf(o.y, f2, acc.y);
+            acc.z = fmaf(o.z, f2, acc.z);
+            acc.w = fmaf(o.w, f2, acc.w);
+        }
+        if (bad) l = -INFINITY;
+    }
+    if (!col) return;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (l != 0.f && l != -INFINITY) {
+        const float inv = 1.f / l;
+        v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    }
+    store_row4(out + u * pl.D + 4 * lane, v);
+}
+
+// ------------------------------------------------------------------ generic kernel
 constexpr int kGen8Threads = 128;
 
 template <typename T, typename Fmt>
@@ -96,12 +862,166 @@ __global__ void __launch_bounds__(kGen8Threads)
     }
 }
 
+// ------------------------------------------------------------------ host side
+struct Q8Layout {  // workspace
+    size_t ml, o, total;
+};
+
+// Group size and slots for a shape; false where the fast kernel does not apply.
+static bool q8_shape(int Hq, int Hkv, int D, int BS, pkv_dtype dt, Q8Plan& pl) {
+    if (D % 16 != 0 || D > 128 || BS % 16 != 0) return false;
+    const int G = Hq / Hkv, rows = dt == PKV_F32 || G <= 8 ? 8 : 16;
+    pl.QC = (G + rows - 1) / rows;
+    if (pl.QC > kQ8Warps) return false;
+    pl.HG = 1;
+    for (int h = 1; h <= kQ8Warps; ++h)
+        if (Hkv % h == 0 && h * pl.QC <= kQ8Warps) pl.HG = h;
+    pl.NG = Hkv / pl.HG;
+    pl.slots = 1;
+    while (pl.slots * 2 * pl.HG * pl.QC <= kQ8Warps) pl.slots *= 2;
+    pl.G = G;
+    pl.R = pl.HG * G;
+    return true;
+}
+
+static Q8Layout q8_layout(int B, int NG, int R, int D, int P) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    Q8Layout w;
+    w.ml = up(sizeof(Q8Info) * std::max<size_t>(static_cast<size_t>(B) * NG, 1));
+    w.o = up(w.ml + static_cast<size_t>(2) * P * R * 2 * sizeof(float));
+    w.total = up(w.o + static_cast<size_t>(2) * P * R * D * sizeof(float));
+    return w;
+}
+
+// A pool [NB * Hkv][BS][D] of bytes in boxes of 16 positions x HG heads x DP bytes
+// (bytes beyond D arrive as zeros), or its scales [NB * Hkv][BS] in boxes of 16 x HG.
+static bool q8_map(CUtensorMap* map, const void* pool, const Q8Plan& pl, int DP) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    const cuuint64_t heads = static_cast<cuuint64_t>(pl.NB) * pl.Hkv;
+    cuuint32_t one[3] = {1, 1, 1};
+    if (DP == 0) {
+        cuuint64_t dim[2] = {static_cast<cuuint64_t>(pl.BS), heads};
+        cuuint64_t stride[1] = {static_cast<cuuint64_t>(pl.BS) * 4};
+        cuuint32_t box[2] = {kQ8Tok, static_cast<cuuint32_t>(pl.HG)};
+        return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(pool), dim, stride, box, one,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
+    cuuint64_t dim[3] = {static_cast<cuuint64_t>(pl.D), static_cast<cuuint64_t>(pl.BS), heads};
+    cuuint64_t stride[2] = {static_cast<cuuint64_t>(pl.D), static_cast<cuuint64_t>(pl.D) * pl.BS};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(DP), kQ8Tok, static_cast<cuuint32_t>(pl.HG)};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dim, stride, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, DP == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, typename Fmt, int DP, bool kSplit>
+static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const void* k, const void* v, const float* ks,
+                                  const float* vs, const int32_t* block_tables, const int32_t* seq_lens,
+                                  void* workspace, int P, int32_t* status, cudaStream_t stream, bool* done) {
+    *done = false;
+    constexpr int kRows = kSplit ? 8 : 16;
+    const int tiles = pl.HG * pl.slots;
+    pl.stage_bytes = 2 * tiles * kQ8Tok * DP;
+    pl.scale_unit = (pl.HG * kQ8Tok * 4 + 127) / 128 * 128;
+    pl.q_bytes = pl.R * pl.D * static_cast<int>(sizeof(T));
+    pl.scratch_bytes = (pl.slots - 1) * pl.HG * pl.QC * (kRows * DP + 2 * kRows) * 4;
+    const size_t fixed = 1024 + 2 * static_cast<size_t>(pl.q_bytes) + pl.scratch_bytes +
+                         (2 * kQ8MaxStages + 4 + 2 * kQ8Warps) * sizeof(uint64_t) + kQ8MaxStages * sizeof(Q8Meta) +
+                         40 * sizeof(int) + 16;
+    const size_t per = pl.stage_bytes + 2 * static_cast<size_t>(pl.slots) * pl.scale_unit;
+    const size_t budget = static_cast<size_t>(max_optin_smem());
+    if (fixed + 2 * per > budget) return cudaSuccess;
+    pl.nst = static_cast<int>(std::min<size_t>(kQ8MaxStages, (budget - fixed) / per));
+    const size_t smem = fixed + pl.nst * per;
+    CUtensorMap tmK, tmV, tmKs, tmVs;
+    if (!q8_map(&tmK, k, pl, DP) || !q8_map(&tmV, v, pl, DP) || !q8_map(&tmKs, ks, pl, 0) || !q8_map(&tmVs, vs, pl, 0))
+        return cudaSuccess;
+    const Q8Layout wl = q8_layout(pl.B, pl.NG, pl.R, pl.D, P);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    Q8Info* info = reinterpret_cast<Q8Info*>(ws);
+    float* part_ml = reinterpret_cast<float*>(ws + wl.ml);
+    float* part_o = reinterpret_cast<float*>(ws + wl.o);
+    auto kern = decode_q8_kernel<T, Fmt, DP, kSplit>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(P), 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>((pl.HG * pl.QC * pl.slots + 1) * 32), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, tmKs, tmVs, pl, static_cast<const T*>(q), static_cast<T*>(out),
+                             block_tables, seq_lens, info, part_ml, part_o, status);
+    if (err != cudaSuccess) return err;
+    const long long units = static_cast<long long>(pl.B) * pl.Hq;
+    const bool many = units >= 8LL * P;
+    cfg.gridDim = dim3(static_cast<unsigned>(many ? (units + kJoinWarps - 1) / kJoinWarps : units), 1, 1);
+    cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    err = cudaLaunchKernelEx(&cfg, many ? decode_q8_join_kernel<T, 1> : decode_q8_join_kernel<T, kJoinWarps>, pl,
+                             static_cast<const Q8Info*>(info), seq_lens, static_cast<const float*>(part_ml),
+                             static_cast<const float*>(part_o), static_cast<T*>(out), P, status);
+    if (err != cudaSuccess) return err;
+    *done = true;
+    return cudaGetLastError();
+}
+
+template <typename T, typename Fmt>
+static cudaError_t launch_q8(Q8Plan pl, bool fast, void* out, const void* q, const void* k, const void* v,
+                             const float* ks, const float* vs, const int32_t* block_tables, const int32_t* seq_lens,
+                             float scale, void* workspace, int P, int32_t* status, cudaStream_t stream) {
+    if (fast) {
+        bool done = false;
+        cudaError_t err = cudaSuccess;
+        auto run = [&](auto dp, auto split) {
+            return launch_q8_fast<T, Fmt, decltype(dp)::value, decltype(split)::value>(
+                pl, out, q, k, v, ks, vs, block_tables, seq_lens, workspace, P, status, stream, &done);
+        };
+        using I64 = std::integral_constant<int, 64>;
+        using I128 = std::integral_constant<int, 128>;
+        if constexpr (sizeof(T) == 2) {
+            if (pl.G > 8) err = pl.D <= 64 ? run(I64(), std::false_type()) : run(I128(), std::false_type());
+        }
+        if (sizeof(T) == 4 || pl.G <= 8) err = pl.D <= 64 ? run(I64(), std::true_type()) : run(I128(), std::true_type());
+        if (err != cudaSuccess || done) return err;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(pl.B) * pl.Hq, 1, 1);
+    cfg.blockDim = dim3(kGen8Threads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t err = cudaLaunchKernelEx(
+        &cfg, decode_q8_generic_kernel<T, Fmt>, static_cast<T*>(out), static_cast<const T*>(q),
+        static_cast<const uint8_t*>(k), static_cast<const uint8_t*>(v), ks, vs, block_tables, pl.max_blocks, seq_lens,
+        pl.Hq, pl.Hkv, pl.D, pl.BS, pl.NB, scale, status);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
 }  // namespace pkv
 
 extern "C" size_t pkv_decode_q8_workspace_bytes(int B, int Hq, int Hkv, int D, int num_sms) {
+    using namespace pkv;
     if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1) return 0;
-    (void)num_sms;
-    return 256;
+    const int P = num_sms > 0 ? num_sms : device_sm_count();
+    if (P <= 0) return 0;
+    // the block size and the type do not change the layout's size, but for the chunk
+    // of query heads: take the larger
+    size_t need = 256;
+    for (pkv_dtype dt : {PKV_F32, PKV_BF16}) {
+        Q8Plan pl = {};
+        if (q8_shape(Hq, Hkv, D, 16, dt, pl)) need = std::max(need, q8_layout(B, pl.NG, pl.R, D, P).total);
+    }
+    return need;
 }
 
 extern "C" pkv_status pkv_paged_decode_attention_q8(
@@ -119,30 +1039,35 @@ extern "C" pkv_status pkv_paged_decode_attention_q8(
     if (!out || !q || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables || !seq_lens || !workspace)
         return PKV_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(workspace) & 15u) != 0) return PKV_ERR_INVALID_ARG;
-    if (workspace_bytes < pkv_decode_q8_workspace_bytes(B, Hq, Hkv, D, 0)) return PKV_ERR_INVALID_ARG;
+    const int P = device_sm_count();
+    if (workspace_bytes < pkv_decode_q8_workspace_bytes(B, Hq, Hkv, D, P > 0 ? P : 1)) return PKV_ERR_INVALID_ARG;
+    if (P <= 0) return PKV_ERR_CUDA;
     if (scale <= 0.f) scale = 1.0f / sqrtf(static_cast<float>(D));
-    auto go = [&](auto t, auto fmt) {
-        using T = decltype(t);
-        using Fmt = decltype(fmt);
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(B) * Hq, 1, 1);
-        cfg.blockDim = dim3(kGen8Threads, 1, 1);
-        cfg.stream = static_cast<cudaStream_t>(stream);
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        const cudaError_t err = cudaLaunchKernelEx(
-            &cfg, decode_q8_generic_kernel<T, Fmt>, static_cast<T*>(out), static_cast<const T*>(q),
-            static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache), k_scale, v_scale, block_tables,
-            max_blocks_per_seq, seq_lens, Hq, Hkv, D, block_size, num_blocks, scale, dev_status);
-        return err != cudaSuccess ? err : cudaGetLastError();
-    };
-    cudaError_t err;
-    if (dtype == PKV_F32)
-        err = cache_dtype == PKV_E4M3 ? go(float(), FmtE4M3()) : go(float(), FmtI8());
-    else
-        err = cache_dtype == PKV_E4M3 ? go(__nv_bfloat16(), FmtE4M3()) : go(__nv_bfloat16(), FmtI8());
+    Q8Plan pl = {};
+    bool fast = q8_shape(Hq, Hkv, D, block_size, dtype, pl);
+    pl.G = Hq / Hkv;
+    pl.B = B;
+    pl.Hq = Hq;
+    pl.Hkv = Hkv;
+    pl.D = D;
+    pl.BS = block_size;
+    pl.NB = num_blocks;
+    pl.max_blocks = max_blocks_per_seq;
+    pl.scale_log2 = scale * 1.4426950408889634f;
+    pl.polls = attention_wait_polls();
+    pl.silent_cta = attention_silent_cta();
+    auto aligned16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+    fast = fast && aligned16(q) && aligned16(out) && aligned16(k_cache) && aligned16(v_cache) && aligned16(k_scale) &&
+           aligned16(v_scale);
+    // step and row counts stay in 32 bits
+    if (fast) {
+        const long long steps = (static_cast<long long>(max_blocks_per_seq) * block_size) / (16 * pl.slots) + 1;
+        fast = steps * B * pl.NG < (1LL << 30) && static_cast<long long>(num_blocks) * Hkv < (1LL << 31);
+    }
+    auto go = dtype == PKV_F32 ? (cache_dtype == PKV_E4M3 ? launch_q8<float, FmtE4M3> : launch_q8<float, FmtI8>)
+                               : (cache_dtype == PKV_E4M3 ? launch_q8<__nv_bfloat16, FmtE4M3>
+                                                          : launch_q8<__nv_bfloat16, FmtI8>);
+    const cudaError_t err = go(pl, fast, out, q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, scale,
+                               workspace, P, dev_status, static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

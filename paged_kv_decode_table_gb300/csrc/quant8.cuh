@@ -40,6 +40,15 @@ struct FmtE4M3 {
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
         return r;
     }
+    // bytes (0, 1) and (2, 3) of v -> lo and hi
+    static __device__ __forceinline__ void decode4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+        lo = decode2(static_cast<uint16_t>(v));
+        hi = decode2(static_cast<uint16_t>(v >> 16));
+    }
+    // bytes (0, 2) and (1, 3) of v -> even and odd
+    static __device__ __forceinline__ void decode4_pairs(uint32_t v, uint32_t& even, uint32_t& odd) {
+        decode4(__byte_perm(v, 0u, 0x3120), even, odd);
+    }
     static __device__ __forceinline__ float decode(uint8_t v) {
         const uint32_t h = decode2(v);
         float f;
@@ -55,6 +64,22 @@ struct FmtI8 {
         return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(x), -127.f), 127.f))) & 0xffu;
     }
     static __device__ __forceinline__ uint32_t encode2(float lo, float hi) { return encode(lo) | encode(hi) << 8; }
+    // x + 128 in the low byte of a half whose ulp is 1: 1024 + (x + 128), minus 1152
+    static __device__ __forceinline__ uint32_t unbias(uint32_t h) {
+        uint32_t r;
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));
+        return r;
+    }
+    static __device__ __forceinline__ void decode4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+        v ^= 0x80808080u;
+        lo = unbias(__byte_perm(v, 0x64646464u, 0x4140));
+        hi = unbias(__byte_perm(v, 0x64646464u, 0x4342));
+    }
+    static __device__ __forceinline__ void decode4_pairs(uint32_t v, uint32_t& even, uint32_t& odd) {
+        v ^= 0x80808080u;
+        even = unbias(__byte_perm(v, 0x64646464u, 0x4240));
+        odd = unbias(__byte_perm(v, 0x64646464u, 0x4341));
+    }
     static __device__ __forceinline__ float decode(uint8_t v) {
         return static_cast<float>(static_cast<int8_t>(v));
     }
