@@ -15,26 +15,30 @@
 //    stage of an mbarrier ring.  The steps of all (sequence, head group) pairs, one
 //    after the other, are cut into one range per CTA; every CTA finds its range
 //    itself from seq_lens.
-//  * One consumer warp per (KV head, chunk of its query heads, slot) takes one
-//    tile of every step: with 8 KV heads the 8 warps are the heads, with one head
+//  * One consumer warp per (KV head, chunk of its query heads, slot) takes kSub
+//    tiles of every step: with 8 KV heads the 8 warps are the heads, with one head
 //    they are 8 slots along the cache, so a model split over devices keeps every
 //    warp busy.  The slots' results are merged in shared memory when the range
 //    leaves the sequence.
 //  * The 8-bit numbers become float16 in registers (exact for both types) and
-//    both products run on mma.sync m16n8k16 with float32 accumulation.  K's order
-//    of dimensions inside a 16-byte chunk is permuted the same way in q, so a
-//    4-byte fragment of K is one register; V is read transposed in 16-bit units,
-//    which yields even and odd dimensions of two positions.
-//  * With at most 8 query heads per warp the upper 8 rows of the MMA are free:
-//    they carry what float16 rounding leaves of q and of the weights, so the
-//    result has float32 accuracy at no extra MMA (kSplit).  With 9 to 16 heads
-//    (bf16 only) the rows are heads, the weights plain float16 (2^-11).
-//  * Weights are normalised by the running maximum of s_j + log2(vs_j), the
-//    largest contribution rather than the largest score, so that p_j * vs_j is
-//    at most 1 and fits float16 whatever the V scales are.  Scales below 2^-64
-//    count as 2^-64 there, which bounds p_j by 2^64.
-//  * q is multiplied by a power of two per row that puts its largest element
-//    into [2^14, 2^15).
+//    both products run transposed on mma.sync m16n8k16 with float32 accumulation:
+//    S^T = K Q^T (16 positions x 8 query heads) and O^T = V^T P^T (16 dimensions x 8
+//    query heads), so the cached tile is the 16-row operand and no MMA row is idle
+//    with 8 query heads.  K's order of dimensions inside a 16-byte chunk is permuted
+//    the same way in q, so a 4-byte fragment of K is one register; V is read
+//    transposed in 16-bit units, which yields even and odd dimensions of two
+//    positions, and rows g and g + 8 of the MMA are dimensions 2g and 2g + 1.
+//    movmatrix turns the weights from S^T's layout into P^T's.
+//  * bf16 queries are exact in float16 and the weights are rounded to it (2^-11);
+//    float32 queries carry what that rounding leaves of q and of the weights in a
+//    second float16 and a second MMA (kSplit), which gives float32 accuracy.
+//  * Weights are normalised by a running maximum of s_j + log2(vs_j), the largest
+//    contribution rather than the largest score, so that p_j * vs_j fits float16
+//    whatever the V scales are.  Scales below 2^-64 count as 2^-64 there, which
+//    bounds p_j by 2^72.  The maximum is renewed (shuffles, rescaled sums) only
+//    when a contribution exceeds it by 2^kLag: a vote decides.
+//  * q is multiplied by a power of two that puts the warp's largest element into
+//    [2^14, 2^15).
 // Other shapes: one CTA per (sequence, query head), CUDA-core fp32.
 #include <cuda.h>
 #include <math.h>
@@ -59,6 +63,8 @@ int attention_silent_cta();
 constexpr int kQ8MaxStages = 12;
 constexpr int kQ8Tok = 16;  // positions per tile
 constexpr int kQ8Warps = 8;  // consumer warps at most
+constexpr int kQ8Sub = 2;    // tiles a warp takes of one step
+constexpr float kLag = 8.f;  // contributions stay below 2^8 of the running maximum
 
 // How a call is laid out; computed on the host, passed to both kernels.
 struct Q8Plan {
@@ -120,6 +126,19 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// 8x8 halves: row g, columns 2r, 2r + 1 -> row 2r (and 2r + 1) as column g
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ void store_row2(__nv_bfloat16* p, float x, float y) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x, y);
+}
+__device__ __forceinline__ void store_row2(float* p, float x, float y) {
+    *reinterpret_cast<float2*>(p) = make_float2(x, y);
+}
 __device__ __forceinline__ void store_row4(__nv_bfloat16* p, float4 v) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
@@ -127,7 +146,7 @@ __device__ __forceinline__ void store_row4(float* p, float4 v) { *reinterpret_ca
 
 // Steps of sequence b in one head group (0 for a length outside [0, max_blocks * BS]).
 __device__ __forceinline__ int q8_steps(const int32_t* seq_lens, int b, const Q8Plan& pl) {
-    const int L = seq_lens[b], T = pl.slots * kQ8Tok;
+    const int L = seq_lens[b], T = pl.slots * kQ8Sub * kQ8Tok;
     return (L >= 0 && static_cast<long long>(L) <= static_cast<long long>(pl.max_blocks) * pl.BS)
                ? static_cast<int>((static_cast<long long>(L) + T - 1) / T)
                : 0;
@@ -163,7 +182,8 @@ __device__ __forceinline__ uint32_t q8_at(int row, int c) {
     return static_cast<uint32_t>(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
 }
 
-template <typename T, typename Fmt, int DP, bool kSplit>
+// kN: n-tiles of 8 query heads per warp; kSplit: float32 accuracy (see above).
+template <typename T, typename Fmt, int DP, int kN, bool kSplit>
 __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmKs, const __grid_constant__ CUtensorMap tmVs,
@@ -176,8 +196,9 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int nst = pl.nst, HG = pl.HG, QC = pl.QC, slots = pl.slots;
     const int HV = HG * QC, CW = HV * slots;
-    const int tile_bytes = kQ8Tok * DP, unit_bytes = HG * tile_bytes, half_stage = slots * unit_bytes;
-    const int scale_half = slots * pl.scale_unit;
+    const int units = slots * kQ8Sub;  // 16-position units per step
+    const int tile_bytes = kQ8Tok * DP, unit_bytes = HG * tile_bytes, half_stage = units * unit_bytes;
+    const int scale_half = units * pl.scale_unit;
     uint8_t* scales = smem + static_cast<size_t>(nst) * pl.stage_bytes;
     uint8_t* qring = scales + static_cast<size_t>(nst) * 2 * scale_half;
     float* scratch = reinterpret_cast<float*>(qring + 2 * static_cast<size_t>(pl.q_bytes));
@@ -244,7 +265,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
 
     if (warp == CW) {
         // ------------------------------------------------ producer warp
-        // Lane u fetches the tiles of slot u.  b, g, j: the step's sequence, head
+        // Lane u fetches unit u (slot u / kQ8Sub).  b, g, j: the step's sequence, head
         // group and index; cn steps per group from cs on.
         int b = sch[33], cs = sch[34];
         int cn = q8_steps(seq_lens, b, pl), cL = seq_lens[b], g = 0;
@@ -274,9 +295,9 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
         if (static_cast<int>(blockIdx.x) == pl.silent_cta) return;  // test hook: no copy is issued
         const uint32_t unit_tx = 2u * unit_bytes + 2u * HG * (kQ8Tok * 4);
         int piece = 0;
-        auto block_of = [&](int bb, int jj, int L) {  // lane u: the block of slot u, -2 behind the end
-            const long long pos = (static_cast<long long>(jj) * slots + lane) * kQ8Tok;
-            if (lane >= slots || pos >= L) return -2;
+        auto block_of = [&](int bb, int jj, int L) {  // lane u: the block of unit u, -2 behind the end
+            const long long pos = (static_cast<long long>(jj) * units + lane) * kQ8Tok;
+            if (lane >= units || pos >= L) return -2;
             const int blk = block_tables[static_cast<size_t>(bb) * pl.max_blocks + pos / pl.BS];
             return blk >= 0 && blk < pl.NB ? blk : -1;
         };
@@ -326,7 +347,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 }
                 Q8Meta mt;
                 mt.vb = cb * NG + cg;
-                mt.left = L - j * slots * kQ8Tok;
+                mt.left = L - j * units * kQ8Tok;
                 mt.flags = (first ? kQFirst : 0) | (last ? kQLast : 0) | (ccs >= start && ccs + ccn <= end ? kQWhole : 0) |
                            (ccs < start ? kQHead : 0) | (bad ? kQBad : 0);
                 mt.pad = 0;
@@ -337,7 +358,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             if (first) ++piece;
             __syncwarp();
             if (cblk >= 0) {
-                const int tok = static_cast<int>(((static_cast<long long>(j) * slots + lane) * kQ8Tok) % pl.BS);
+                const int tok = static_cast<int>(((static_cast<long long>(j) * units + lane) * kQ8Tok) % pl.BS);
                 const int row = cblk * pl.Hkv + cg * HG;
                 uint8_t* kd = smem + static_cast<size_t>(stage) * pl.stage_bytes + lane * unit_bytes;
                 uint8_t* sd = scales + static_cast<size_t>(stage) * 2 * scale_half + lane * pl.scale_unit;
@@ -357,54 +378,153 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     // ---------------------------------------------------- consumers
     const int slot = warp / HV, vh = warp - slot * HV, hh = vh / QC, qc = vh - hh * QC;
     const int g = lane >> 2, r = lane & 3, mi = lane >> 3, rr = lane & 7;
-    constexpr int kRows = kSplit ? 8 : 16;
-    const int row0 = qc * kRows + g, row1 = row0 + 8;     // query heads of this KV head
-    const bool live0 = row0 < pl.G, live1 = !kSplit && row1 < pl.G;
-    float O[kChunks][2][4];  // [16-dim chunk][even, odd dims][row g: 2 dims, row g + 8 (or the remainder): 2 dims]
-    uint32_t qa[kChunks][4];
-    float smul0 = 0.f, smul1 = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    constexpr int kHeads = 8 * kN;
+    // O^T: [16-dim chunk][n-tile][dims 2g, 2g + 1 of head 2r at 0, 2, of head 2r + 1 at 1, 3]
+    float O[kChunks][kN][4];
+    uint32_t qb[kN][kChunks][2];
+    [[maybe_unused]] uint32_t ql[kSplit ? kN : 1][kSplit ? kChunks : 1][2];
+    float smul = 0.f;
+    float m[kN][2], mu[kN][2], l[kN][2];  // of heads 8 n + 2 r + e; mu: m, or 0 where m is -inf
     bool poisoned = false;
     int piece = 0, stage = 0;
     uint32_t parity = 0;
     const uint32_t smem_base = smem_u32(smem);
-    const int tile_off = (slot * HG + hh) * tile_bytes;
-    const int scale_off = slot * pl.scale_unit + hh * (kQ8Tok * 4);
+    const int tile_off = (slot * kQ8Sub * HG + hh) * tile_bytes;
+    const int scale_off = slot * kQ8Sub * pl.scale_unit + hh * (kQ8Tok * 4);
     // ldmatrix: lane group mi gives the rows of matrix mi: (positions 8 (mi & 1) ..,
     // chunk + (mi >> 1))
     const int lm_row = (mi & 1) * 8 + rr, lm_chunk = mi >> 1;
 
-    // one row of q, as float16 (and its float16 remainder), scaled by a power of two
-    auto load_q = [&](const T* row, bool live, float& smul, int lo_reg) {
-        float x[kChunks][4];
-        float amax = 0.f;
+    // One step's kQ8Sub tiles; kPart: some of their positions lie behind the end.
+    auto tiles = [&](auto part, int ntok) {
+        constexpr bool kPart = decltype(part)::value;
+        const uint32_t kb0 = smem_base + static_cast<uint32_t>(stage) * pl.stage_bytes + tile_off;
+        const uint8_t* sc0 = scales + static_cast<size_t>(stage) * 2 * scale_half + scale_off;
+        float x[kQ8Sub][kN][4];  // scores of position g (+ 8 for 2, 3), heads 2r, 2r + 1
+        float vsc[kQ8Sub][2];
+        bool over = false;
+        float tmax[kN][2];
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) {
-            const int d = c * 16 + 4 * r;
+        for (int n = 0; n < kN; ++n) tmax[n][0] = tmax[n][1] = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[c][e] = live && d < pl.D ? to_f32(row[d + e]) : 0.f;
-                amax = fmaxf(amax, fabsf(x[c][e]));
-            }
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int e = max(static_cast<int>(__float_as_uint(amax) >> 23), 27);  // biased exponent, at least 2^-100
-        // amax in [2^(e-127), 2^(e-126)) -> [2^14, 2^15); infinite amax: exponent 255
-        const float fac = __uint_as_float(static_cast<uint32_t>(max(268 - e, 1)) << 23);
-        smul = __uint_as_float(static_cast<uint32_t>(min(e - 14, 253)) << 23) * pl.scale_log2;
+        for (int k = 0; k < kQ8Sub; ++k) {
+            // ---- S^T = K Q^T, in two independent chains
+            const uint32_t kb = kb0 + k * unit_bytes;
+            float s[kN][2][4];
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const float a = x[c][2 * p] * fac, b = x[c][2 * p + 1] * fac;
-                const uint32_t hi = pack_f16x2(a, b);
-                qa[c][2 * p + lo_reg] = hi;
-                if (kSplit) {
-                    const float2 f = unpack_f16x2(hi);
-                    qa[c][2 * p + 1] = pack_f16x2(a - f.x, b - f.y);
+                for (int e = 0; e < 4; ++e) s[n][0][e] = s[n][1][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < kChunks; c += 2) {
+                uint32_t w[4];
+                ldmatrix_x4(w[0], w[1], w[2], w[3], kb + q8_at<DP>(lm_row, c + lm_chunk));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t a[4];
+                    Fmt::decode4(w[2 * u], a[0], a[2]);
+                    Fmt::decode4(w[2 * u + 1], a[1], a[3]);
+#pragma unroll
+                    for (int n = 0; n < kN; ++n) {
+                        mma_f16_16816(s[n][u], a, qb[n][c + u][0], qb[n][c + u][1]);
+                        if constexpr (kSplit) mma_f16_16816(s[n][u], a, ql[n][c + u][0], ql[n][c + u][1]);
+                    }
                 }
             }
+            // ---- scaled scores, and the largest contribution s_j + log2(vs_j)
+            const float* ks = reinterpret_cast<const float*>(sc0 + k * pl.scale_unit);
+            const float* vs = reinterpret_cast<const float*>(sc0 + k * pl.scale_unit + scale_half);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const bool in = !kPart || k * kQ8Tok + 8 * t + g < ntok;
+                const float kk = ks[8 * t + g] * smul, vv = vs[8 * t + g];
+                const float lg = lg2f(fmaxf(fabsf(vv), kMinScale));
+                vsc[k][t] = in ? vv : 0.f;
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float a = (s[n][0][2 * t + e] + s[n][1][2 * t + e]) * kk;
+                        x[k][n][2 * t + e] = in ? a : -INFINITY;
+                        tmax[n][e] = fmaxf(tmax[n][e], in ? a + lg : -INFINITY);
+                    }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) over = over || tmax[n][e] > m[n][e] + kLag;
+        if (__any_sync(0xffffffffu, over)) {  // renew the maxima, rescale what was summed so far
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+                float al[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = tmax[n][e];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    const float mn = fmaxf(m[n][e], mx);
+                    mu[n][e] = mn == -INFINITY ? 0.f : mn;
+                    al[e] = ex2f(m[n][e] - mu[n][e]);
+                    m[n][e] = mn;
+                    l[n][e] *= al[e];
+                }
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    O[c][n][0] *= al[0];
+                    O[c][n][1] *= al[1];
+                    O[c][n][2] *= al[0];
+                    O[c][n][3] *= al[1];
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kQ8Sub; ++k) {
+            if (kPart && k * kQ8Tok >= ntok) break;
+            // ---- weights, float16, in P^T's layout
+            uint32_t pb[kN][2];
+            [[maybe_unused]] uint32_t pl2[kSplit ? kN : 1][2];
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const float p0 = ex2f(x[k][n][2 * t] - mu[n][0]), p1 = ex2f(x[k][n][2 * t + 1] - mu[n][1]);
+                    l[n][0] += p0;
+                    l[n][1] += p1;
+                    const float w0 = p0 * vsc[k][t], w1 = p1 * vsc[k][t];
+                    const uint32_t hi = pack_f16x2(w0, w1);
+                    pb[n][t] = transpose_8x8(hi);
+                    if constexpr (kSplit) {
+                        const float2 f = unpack_f16x2(hi);
+                        pl2[n][t] = transpose_8x8(pack_f16x2(w0 - f.x, w1 - f.y));
+                    }
+                }
+            // ---- O^T += V^T P^T.  Positions behind the end have weight 0; their bytes
+            // are cleared because an e4m3 NaN would survive the product.
+            const uint32_t vb = kb0 + half_stage + k * unit_bytes;
+            uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+            if (kPart) {
+                const int left = ntok - k * kQ8Tok - 2 * r;
+                keep0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+                keep1 = (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
+            }
+#pragma unroll
+            for (int c = 0; c < kChunks; c += 2) {
+                uint32_t w[4];
+                ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vb + q8_at<DP>(lm_row, c + lm_chunk));
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    uint32_t a[4];
+                    Fmt::decode4_pairs(kPart ? w[2 * u] & keep0 : w[2 * u], a[0], a[1]);
+                    Fmt::decode4_pairs(kPart ? w[2 * u + 1] & keep1 : w[2 * u + 1], a[2], a[3]);
+#pragma unroll
+                    for (int n = 0; n < kN; ++n) {
+                        mma_f16_16816(O[c + u][n], a, pb[n][0], pb[n][1]);
+                        if constexpr (kSplit) mma_f16_16816(O[c + u][n], a, pl2[n][0], pl2[n][1]);
+                    }
+                }
+            }
+        }
     };
 
     for (int i = start; i < end; ++i) {
@@ -419,127 +539,62 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 if (lane == 0) report(status, PKV_ERR_TIMEOUT);
                 return;
             }
+            // head g (of each n-tile): dims 16 c + 4 r .. + 3
             const T* qsm = reinterpret_cast<const T*>(qring + static_cast<size_t>(qs) * pl.q_bytes) +
                            static_cast<size_t>(hh * pl.G) * pl.D;
-            load_q(qsm + row0 * pl.D, live0, smul0, 0);
-            if (!kSplit) load_q(qsm + row1 * pl.D, live1, smul1, 1);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&qempty[qs]);
-            m0 = m1 = -INFINITY;
-            l0 = l1 = 0.f;
-            poisoned = false;
+            float v[kN][kChunks][4], amax = 0.f;
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
+            for (int n = 0; n < kN; ++n) {
+                const int row = qc * kHeads + 8 * n + g;
 #pragma unroll
-                for (int p = 0; p < 2; ++p) O[c][p][0] = O[c][p][1] = O[c][p][2] = O[c][p][3] = 0.f;
-        }
-        const int ntok = mt.left - slot * kQ8Tok;  // positions in this warp's tile (may be more than 16, or none)
-        poisoned = poisoned || (mt.flags & kQBad);
-        if (ntok > 0 && !poisoned) {
-            const uint32_t kb = smem_base + static_cast<uint32_t>(stage) * pl.stage_bytes + tile_off;
-            const uint32_t vb = kb + half_stage;
-            const float* ks = reinterpret_cast<const float*>(scales + static_cast<size_t>(stage) * 2 * scale_half + scale_off);
-            const float* vs = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(ks) + scale_half);
-            // ---- S = Q K^T: two n-tiles of 8 positions
-            float s[2][4];
+                for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-#pragma unroll
-            for (int c = 0; c < kChunks; c += 2) {
-                uint32_t w[4], lo, hi;
-                ldmatrix_x4(w[0], w[1], w[2], w[3], kb + q8_at<DP>(lm_row, c + lm_chunk));
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    Fmt::decode4(w[u], lo, hi);
-                    mma_f16_16816(s[u & 1], qa[c + (u >> 1)], lo, hi);
-                }
-            }
-            // ---- online softmax in the log2 domain, normalised by the largest p_j vs_j
-            float x0[4], x1[4], vsc[4];  // position 8 (e >> 1) + 2 r + (e & 1)
-            float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const float2 k2 = *reinterpret_cast<const float2*>(ks + 8 * t + 2 * r);
-                const float2 v2 = *reinterpret_cast<const float2*>(vs + 8 * t + 2 * r);
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const bool in = 8 * t + 2 * r + e < ntok;
-                    const float kk = e ? k2.y : k2.x, vv = e ? v2.y : v2.x;
-                    const float lg = lg2f(fmaxf(fabsf(vv), kMinScale));
-                    vsc[2 * t + e] = in ? vv : 0.f;
-                    const float a0 = (kSplit ? s[t][e] + s[t][2 + e] : s[t][e]) * (smul0 * kk);
-                    x0[2 * t + e] = in ? a0 : -INFINITY;
-                    mx0 = fmaxf(mx0, in ? a0 + lg : -INFINITY);
-                    if (!kSplit) {
-                        const float a1 = s[t][2 + e] * (smul1 * kk);
-                        x1[2 * t + e] = in ? a1 : -INFINITY;
-                        mx1 = fmaxf(mx1, in ? a1 + lg : -INFINITY);
+                    for (int e = 0; e < 4; ++e) {
+                        const int d = c * 16 + 4 * r;
+                        v[n][c][e] = row < pl.G && d < pl.D ? to_f32(qsm[row * pl.D + d + e]) : 0.f;
+                        amax = fmaxf(amax, fabsf(v[n][c][e]));
                     }
-                }
             }
-            auto renew = [](float& m, float mx, float& mu) {  // new maximum, and the factor of what was summed so far
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m, mx);
-                mu = mn == -INFINITY ? 0.f : mn;
-                const float a = ex2f(m - mu);
-                m = mn;
-                return a;
-            };
-            float mu0, mu1 = 0.f, al0 = renew(m0, mx0, mu0), al1 = 1.f;
-            if (!kSplit) al1 = renew(m1, mx1, mu1);
-            uint32_t pa[4];
-            float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const float p0 = ex2f(x0[2 * t] - mu0), p1 = ex2f(x0[2 * t + 1] - mu0);
-                sum0 += p0 + p1;
-                const float w0 = p0 * vsc[2 * t], w1 = p1 * vsc[2 * t + 1];
-                const uint32_t hi = pack_f16x2(w0, w1);
-                pa[2 * t] = hi;
-                if (kSplit) {
-                    const float2 f = unpack_f16x2(hi);
-                    pa[2 * t + 1] = pack_f16x2(w0 - f.x, w1 - f.y);
-                } else {
-                    const float y0 = ex2f(x1[2 * t] - mu1), y1 = ex2f(x1[2 * t + 1] - mu1);
-                    sum1 += y0 + y1;
-                    pa[2 * t + 1] = pack_f16x2(y0 * vsc[2 * t], y1 * vsc[2 * t + 1]);
-                }
-            }
-            l0 = fmaf(l0, al0, sum0);
-            l1 = fmaf(l1, al1, sum1);
-            if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
-                const float b1 = kSplit ? al0 : al1;
+            for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // amax in [2^(ex-127), 2^(ex-126)) -> [2^14, 2^15); not below 2^-100, infinite: 255
+            const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23), 27);
+            const float fac = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+            smul = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23) * pl.scale_log2;
+#pragma unroll
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c)
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        O[c][p][0] *= al0;
-                        O[c][p][1] *= al0;
-                        O[c][p][2] *= b1;
-                        O[c][p][3] *= b1;
+                        const float a = v[n][c][2 * p] * fac, b = v[n][c][2 * p + 1] * fac;
+                        qb[n][c][p] = pack_f16x2(a, b);
+                        if constexpr (kSplit) {
+                            const float2 f = unpack_f16x2(qb[n][c][p]);
+                            ql[n][c][p] = pack_f16x2(a - f.x, b - f.y);
+                        }
                     }
-            }
-            // ---- O += P V.  Positions behind the end have weight 0; their bytes are
-            // cleared because an e4m3 NaN would survive the product.
-            uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-            if (ntok < kQ8Tok) {
-                keep0 = (2 * r < ntok ? 0xffffu : 0u) | (2 * r + 1 < ntok ? 0xffff0000u : 0u);
-                keep1 = (2 * r + 8 < ntok ? 0xffffu : 0u) | (2 * r + 9 < ntok ? 0xffff0000u : 0u);
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&qempty[qs]);
+            poisoned = false;
 #pragma unroll
-            for (int c = 0; c < kChunks; c += 2) {
-                uint32_t w[4];
-                ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vb + q8_at<DP>(lm_row, c + lm_chunk));
+            for (int n = 0; n < kN; ++n) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint32_t e0, o0, e1, o1;
-                    Fmt::decode4_pairs(w[2 * u] & keep0, e0, o0);
-                    Fmt::decode4_pairs(w[2 * u + 1] & keep1, e1, o1);
-                    mma_f16_16816(O[c + u][0], pa, e0, e1);
-                    mma_f16_16816(O[c + u][1], pa, o0, o1);
+                for (int e = 0; e < 2; ++e) {
+                    m[n][e] = -INFINITY;
+                    mu[n][e] = l[n][e] = 0.f;
                 }
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) O[c][n][0] = O[c][n][1] = O[c][n][2] = O[c][n][3] = 0.f;
             }
+        }
+        const int ntok = mt.left - slot * (kQ8Sub * kQ8Tok);  // positions from this warp's first one to the end
+        poisoned = poisoned || (mt.flags & kQBad);
+        if (!poisoned) {
+            if (ntok >= kQ8Sub * kQ8Tok)
+                tiles(std::false_type(), ntok);
+            else if (ntok > 0)
+                tiles(std::true_type(), ntok);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
@@ -550,30 +605,21 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
         if (!(mt.flags & kQLast)) continue;
 
         // ---------------------------------------------- the range leaves (sequence, group) mt.vb
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-        // row g, dims 16 c + 4 r .. + 3 (row 1: row g + 8)
-        auto value = [&](int c, int row) {
-            const int k = 2 * row;
-            float4 v = make_float4(O[c][0][k], O[c][1][k], O[c][0][k + 1], O[c][1][k + 1]);
-            if (kSplit) {
-                v.x += O[c][0][2];
-                v.y += O[c][1][2];
-                v.z += O[c][0][3];
-                v.w += O[c][1][3];
-            }
-            return v;
-        };
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
         if (slots > 1) {
-            // merge the slots: at distance d = slots / 2, .., 1 warp slot in [d, 2d) hands its result
-            // to slot - d through its own scratch tile.  Each wait is bounded.
-            constexpr int kTile = kRows * DP + 2 * kRows;
+            // merge the slots: at distance d = slots / 2, .., 1 warp slot in [d, 2d) hands its
+            // result to slot - d through its own scratch tile (rows padded by 4 floats
+            // so that the 4 heads a quarter-warp touches fall on different banks).
+            // Each wait is bounded.
+            constexpr int kRow = DP + 4, kTile = kHeads * (kRow + 2);
             const uint32_t ph = static_cast<uint32_t>(piece) & 1u;
             bool sent = false;
             for (int d = slots >> 1; d > 0; d >>= 1) {
-                if (slot >= 2 * d) continue;
                 if (slot >= d) {
                     float* t = scratch + ((slot - 1) * HV + vh) * kTile;
                     if (!mbar_wait(&mempty[warp], ph ^ 1u, pl.polls)) {
@@ -581,14 +627,17 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                         return;
                     }
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        *reinterpret_cast<float4*>(t + g * DP + c * 16 + 4 * r) = value(c, 0);
-                        if (!kSplit) *reinterpret_cast<float4*>(t + (g + 8) * DP + c * 16 + 4 * r) = value(c, 1);
-                    }
-                    if (r == 0) {
-                        *reinterpret_cast<float2*>(t + kRows * DP + 2 * g) = make_float2(m0, l0);
-                        if (!kSplit) *reinterpret_cast<float2*>(t + kRows * DP + 2 * (g + 8)) = make_float2(m1, l1);
-                    }
+                    for (int n = 0; n < kN; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int head = 8 * n + 2 * r + e;
+#pragma unroll
+                            for (int c = 0; c < kChunks; ++c)
+                                *reinterpret_cast<float2*>(t + head * kRow + 16 * c + 2 * g) =
+                                    make_float2(O[c][n][e], O[c][n][2 + e]);
+                            if (g == 0)
+                                *reinterpret_cast<float2*>(t + kHeads * kRow + 2 * head) = make_float2(m[n][e], l[n][e]);
+                        }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&mfull[warp]);
                     sent = true;
@@ -600,32 +649,23 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                     if (lane == 0) report(status, PKV_ERR_TIMEOUT);
                     return;
                 }
-                auto join = [](float& m, float& l, float2 ml, float& fb) {
-                    const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
-                    const float fa = ex2f(m - mu);
-                    fb = ex2f(ml.x - mu);
-                    l = l * fa + ml.y * fb;
-                    m = mn;
-                    return fa;
-                };
-                float fb0, fb1 = 0.f;
-                const float fa0 = join(m0, l0, *reinterpret_cast<const float2*>(t + kRows * DP + 2 * g), fb0);
-                float fa1 = fa0;
-                if (!kSplit) fa1 = join(m1, l1, *reinterpret_cast<const float2*>(t + kRows * DP + 2 * (g + 8)), fb1);
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    const float4 a = *reinterpret_cast<const float4*>(t + g * DP + c * 16 + 4 * r);
-                    O[c][0][0] = fmaf(O[c][0][0], fa0, a.x * fb0);
-                    O[c][1][0] = fmaf(O[c][1][0], fa0, a.y * fb0);
-                    O[c][0][1] = fmaf(O[c][0][1], fa0, a.z * fb0);
-                    O[c][1][1] = fmaf(O[c][1][1], fa0, a.w * fb0);
-                    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (!kSplit) z = *reinterpret_cast<const float4*>(t + (g + 8) * DP + c * 16 + 4 * r);
-                    O[c][0][2] = fmaf(O[c][0][2], fa1, z.x * fb1);
-                    O[c][1][2] = fmaf(O[c][1][2], fa1, z.y * fb1);
-                    O[c][0][3] = fmaf(O[c][0][3], fa1, z.z * fb1);
-                    O[c][1][3] = fmaf(O[c][1][3], fa1, z.w * fb1);
-                }
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int head = 8 * n + 2 * r + e;
+                        const float2 ml = *reinterpret_cast<const float2*>(t + kHeads * kRow + 2 * head);
+                        const float mn = fmaxf(m[n][e], ml.x), base = mn == -INFINITY ? 0.f : mn;
+                        const float fa = ex2f(m[n][e] - base), fb = ex2f(ml.x - base);
+                        m[n][e] = mn;
+                        l[n][e] = fmaf(l[n][e], fa, ml.y * fb);
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c) {
+                            const float2 o = *reinterpret_cast<const float2*>(t + head * kRow + 16 * c + 2 * g);
+                            O[c][n][e] = fmaf(O[c][n][e], fa, o.x * fb);
+                            O[c][n][2 + e] = fmaf(O[c][n][2 + e], fa, o.y * fb);
+                        }
+                    }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&mempty[from]);
             }
@@ -635,33 +675,30 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             ++piece;
         }
 #pragma unroll
-        for (int row = 0; row < (kSplit ? 1 : 2); ++row) {
-            if (!(row ? live1 : live0)) continue;
-            const int qr = hh * pl.G + (row ? row1 : row0);  // row in the group
-            const float m = row ? m1 : m0, l = row ? l1 : l0;
-            if (mt.flags & kQWhole) {
-                const float inv = poisoned || l == 0.f ? 0.f : 1.f / l;
-                T* o = out + (static_cast<size_t>(mt.vb) * pl.R + qr) * pl.D;
+        for (int n = 0; n < kN; ++n)
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    const int d = c * 16 + 4 * r;
-                    if (d >= pl.D) continue;
-                    const float4 v = value(c, row);
-                    if (poisoned)
-                        store_row4(o + d, make_float4(0.f, 0.f, 0.f, 0.f));
-                    else
-                        store_row4(o + d, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
-                }
-            } else {
-                const size_t at = (2 * static_cast<size_t>(blockIdx.x) + ((mt.flags & kQHead) ? 0 : 1)) * pl.R + qr;
-                if (r == 0) *reinterpret_cast<float2*>(part_ml + 2 * at) = make_float2(m, poisoned ? -1.f : l);
+            for (int e = 0; e < 2; ++e) {
+                const int head = qc * kHeads + 8 * n + 2 * r + e;
+                if (head >= pl.G) continue;
+                const int qr = hh * pl.G + head;  // row in the group
+                if (mt.flags & kQWhole) {
+                    const float inv = poisoned || l[n][e] == 0.f ? 0.f : 1.f / l[n][e];
+                    T* o = out + (static_cast<size_t>(mt.vb) * pl.R + qr) * pl.D + 2 * g;
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    const int d = c * 16 + 4 * r;
-                    if (d < pl.D) *reinterpret_cast<float4*>(part_o + at * pl.D + d) = value(c, row);
+                    for (int c = 0; c < kChunks; ++c)
+                        if (16 * c < pl.D)
+                            store_row2(o + 16 * c, poisoned ? 0.f : O[c][n][e] * inv, poisoned ? 0.f : O[c][n][2 + e] * inv);
+                } else {
+                    const size_t at = (2 * static_cast<size_t>(blockIdx.x) + ((mt.flags & kQHead) ? 0 : 1)) * pl.R + qr;
+                    if (g == 0)
+                        *reinterpret_cast<float2*>(part_ml + 2 * at) = make_float2(m[n][e], poisoned ? -1.f : l[n][e]);
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c)
+                        if (16 * c < pl.D)
+                            *reinterpret_cast<float2*>(part_o + at * pl.D + 16 * c + 2 * g) =
+                                make_float2(O[c][n][e], O[c][n][2 + e]);
                 }
             }
-        }
     }
 }
 
@@ -870,7 +907,7 @@ struct Q8Layout {  // workspace
 // Group size and slots for a shape; false where the fast kernel does not apply.
 static bool q8_shape(int Hq, int Hkv, int D, int BS, pkv_dtype dt, Q8Plan& pl) {
     if (D % 16 != 0 || D > 128 || BS % 16 != 0) return false;
-    const int G = Hq / Hkv, rows = dt == PKV_F32 || G <= 8 ? 8 : 16;
+    const int G = Hq / Hkv, rows = dt == PKV_F32 || G <= 8 ? 8 : 16;  // query heads per warp
     pl.QC = (G + rows - 1) / rows;
     if (pl.QC > kQ8Warps) return false;
     pl.HG = 1;
@@ -916,21 +953,21 @@ static bool q8_map(CUtensorMap* map, const void* pool, const Q8Plan& pl, int DP)
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, typename Fmt, int DP, bool kSplit>
+template <typename T, typename Fmt, int DP, int kN>
 static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const void* k, const void* v, const float* ks,
                                   const float* vs, const int32_t* block_tables, const int32_t* seq_lens,
                                   void* workspace, int P, int32_t* status, cudaStream_t stream, bool* done) {
     *done = false;
-    constexpr int kRows = kSplit ? 8 : 16;
-    const int tiles = pl.HG * pl.slots;
+    constexpr bool kSplit = sizeof(T) == 4;
+    const int tiles = pl.HG * pl.slots * kQ8Sub;
     pl.stage_bytes = 2 * tiles * kQ8Tok * DP;
     pl.scale_unit = (pl.HG * kQ8Tok * 4 + 127) / 128 * 128;
     pl.q_bytes = pl.R * pl.D * static_cast<int>(sizeof(T));
-    pl.scratch_bytes = (pl.slots - 1) * pl.HG * pl.QC * (kRows * DP + 2 * kRows) * 4;
+    pl.scratch_bytes = (pl.slots - 1) * pl.HG * pl.QC * (8 * kN * (DP + 6)) * 4;
     const size_t fixed = 1024 + 2 * static_cast<size_t>(pl.q_bytes) + pl.scratch_bytes +
                          (2 * kQ8MaxStages + 4 + 2 * kQ8Warps) * sizeof(uint64_t) + kQ8MaxStages * sizeof(Q8Meta) +
                          40 * sizeof(int) + 16;
-    const size_t per = pl.stage_bytes + 2 * static_cast<size_t>(pl.slots) * pl.scale_unit;
+    const size_t per = pl.stage_bytes + 2 * static_cast<size_t>(pl.slots) * kQ8Sub * pl.scale_unit;
     const size_t budget = static_cast<size_t>(max_optin_smem());
     if (fixed + 2 * per > budget) return cudaSuccess;
     pl.nst = static_cast<int>(std::min<size_t>(kQ8MaxStages, (budget - fixed) / per));
@@ -943,7 +980,7 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     Q8Info* info = reinterpret_cast<Q8Info*>(ws);
     float* part_ml = reinterpret_cast<float*>(ws + wl.ml);
     float* part_o = reinterpret_cast<float*>(ws + wl.o);
-    auto kern = decode_q8_kernel<T, Fmt, DP, kSplit>;
+    auto kern = decode_q8_kernel<T, Fmt, DP, kN, kSplit>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -979,16 +1016,18 @@ static cudaError_t launch_q8(Q8Plan pl, bool fast, void* out, const void* q, con
     if (fast) {
         bool done = false;
         cudaError_t err = cudaSuccess;
-        auto run = [&](auto dp, auto split) {
-            return launch_q8_fast<T, Fmt, decltype(dp)::value, decltype(split)::value>(
+        auto run = [&](auto dp, auto n) {
+            return launch_q8_fast<T, Fmt, decltype(dp)::value, decltype(n)::value>(
                 pl, out, q, k, v, ks, vs, block_tables, seq_lens, workspace, P, status, stream, &done);
         };
+        using I1 = std::integral_constant<int, 1>;
+        using I2 = std::integral_constant<int, 2>;
         using I64 = std::integral_constant<int, 64>;
         using I128 = std::integral_constant<int, 128>;
         if constexpr (sizeof(T) == 2) {
-            if (pl.G > 8) err = pl.D <= 64 ? run(I64(), std::false_type()) : run(I128(), std::false_type());
+            if (pl.G > 8) err = pl.D <= 64 ? run(I64(), I2()) : run(I128(), I2());
         }
-        if (sizeof(T) == 4 || pl.G <= 8) err = pl.D <= 64 ? run(I64(), std::true_type()) : run(I128(), std::true_type());
+        if (sizeof(T) == 4 || pl.G <= 8) err = pl.D <= 64 ? run(I64(), I1()) : run(I128(), I1());
         if (err != cudaSuccess || done) return err;
     }
     cudaLaunchConfig_t cfg = {};
