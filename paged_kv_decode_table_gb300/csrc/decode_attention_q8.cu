@@ -64,6 +64,7 @@ constexpr int kQ8MaxStages = 12;
 constexpr int kQ8Tok = 16;  // positions per tile
 constexpr int kQ8Warps = 8;  // consumer warps at most
 constexpr int kQ8Sub = 2;    // tiles a warp takes of one step
+constexpr long long kDirectBytes = 256 << 10;  // a CTA's share up to which no split is worth a join
 constexpr float kLag = 8.f;  // contributions stay below 2^8 of the running maximum
 
 // How a call is laid out; computed on the host, passed to both kernels.
@@ -74,6 +75,8 @@ struct Q8Plan {
     int R;           // query rows per group: HG * G
     int nst;         // ring stages
     int stage_bytes, scale_unit, q_bytes, scratch_bytes;
+    int direct;      // one CTA per (sequence, group), no join
+    int pack;        // D = 64: two positions per 128-byte row of a tile
     int B, Hq, Hkv, G, D, BS, NB, max_blocks;
     float scale_log2;
     uint32_t polls;
@@ -174,12 +177,17 @@ __device__ __forceinline__ int q8_scan(int v, int* red, int& total) {
     return before + x - v;
 }
 
-// Byte offset of 16-byte chunk c of row `row` in a TMA-swizzled tile of rows of DP
-// bytes (128-byte swizzle for rows of 128 bytes, 64-byte swizzle for 64).
+// Byte offset of 16-byte chunk c of position `tok` in a TMA-swizzled tile: rows of 128
+// bytes (128-byte swizzle), rows of 64 (64-byte swizzle), or with pack rows of 128
+// bytes that hold two positions.
 template <int DP>
-__device__ __forceinline__ uint32_t q8_at(int row, int c) {
-    if (DP == 128) return static_cast<uint32_t>(row * 128 + ((c ^ (row & 7)) << 4));
-    return static_cast<uint32_t>(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+__device__ __forceinline__ uint32_t q8_at(int tok, int c, int pack) {
+    if (DP == 64 && pack) {
+        c += (tok & 1) * 4;
+        tok >>= 1;
+    }
+    if (DP == 128 || pack) return static_cast<uint32_t>(tok * 128 + ((c ^ (tok & 7)) << 4));
+    return static_cast<uint32_t>(tok * 64 + ((c ^ ((tok >> 1) & 3)) << 4));
 }
 
 // kN: n-tiles of 8 query heads per warp; kSplit: float32 accuracy (see above).
@@ -188,6 +196,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmKs, const __grid_constant__ CUtensorMap tmVs,
                      const __grid_constant__ Q8Plan pl, const T* __restrict__ q, T* __restrict__ out,
+                     const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                      const int32_t* __restrict__ block_tables, const int32_t* __restrict__ seq_lens,
                      Q8Info* __restrict__ info, float* __restrict__ part_ml, float* __restrict__ part_o,
                      int32_t* status) {
@@ -235,24 +244,42 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     // Only after the wait: the joining kernel reads seq_lens before its own wait.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- this CTA's range of steps
+    // ---- this CTA's range of steps: [start, end), which begins in sequence b0, whose
+    // first step is s0
     const int nthr = blockDim.x, B = pl.B, NG = pl.NG;
-    const int n_first = static_cast<int>(threadIdx.x) < B ? q8_steps(seq_lens, threadIdx.x, pl) : 0;
-    int tsum = n_first;
-    for (int b = threadIdx.x + nthr; b < B; b += nthr) tsum += q8_steps(seq_lens, b, pl);
-    int total;
-    q8_scan(tsum, sch, total);
-    total *= NG;
-    const int W = total > 0 ? (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x) : 1;
-    const int start = blockIdx.x * W, end = min(total, start + W);
-    if (start >= end) return;  // uniform over the CTA
-    {
+    int W = 1, start, end, b0, s0;
+    if (pl.direct) {
+        b0 = static_cast<int>(blockIdx.x) / NG;
+        start = (static_cast<int>(blockIdx.x) - b0 * NG);
+        const int n = q8_steps(seq_lens, b0, pl);
+        start *= n;
+        end = start + n;
+        s0 = 0;
+        if (n == 0) {  // empty or invalid: zeros
+            T* o = out + static_cast<size_t>(blockIdx.x) * pl.R * pl.D;
+            for (int e = threadIdx.x; e < pl.R * pl.D; e += nthr) o[e] = from_f32<T>(0.f);
+            if (threadIdx.x == 0 && seq_lens[b0] != 0) report(status, PKV_ERR_DEVICE_BOUNDS);
+            return;
+        }
+        __syncthreads();  // the barriers are initialised
+    } else {
+        const int n_first = static_cast<int>(threadIdx.x) < B ? NG * q8_steps(seq_lens, threadIdx.x, pl) : 0;
+        int tsum = n_first;
+        for (int b = threadIdx.x + nthr; b < B; b += nthr) tsum += NG * q8_steps(seq_lens, b, pl);
+        int total, before = q8_scan(tsum, sch, total);
+        if (total > 0) W = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+        start = blockIdx.x * W;
+        end = min(total, start + W);
+        if (start >= end) return;  // uniform over the CTA
         int carry = 0;
         for (int base = 0; base < B; base += nthr) {
             const int b = base + threadIdx.x;
-            const int n = NG * (base == 0 ? n_first : (b < B ? q8_steps(seq_lens, b, pl) : 0));
-            int tot;
-            const int sb = carry + q8_scan(n, sch, tot);
+            int n = n_first, tot = total;
+            if (B > nthr) {  // else the scan above was this one
+                if (base > 0) n = b < B ? NG * q8_steps(seq_lens, b, pl) : 0;
+                before = q8_scan(n, sch, tot);
+            }
+            const int sb = carry + before;
             if (n > 0 && sb <= start && start < sb + n) {  // exactly one thread of the CTA
                 sch[33] = b;
                 sch[34] = sb;
@@ -261,19 +288,21 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             if (carry > start) break;  // same decision in every thread
         }
         __syncthreads();
+        b0 = sch[33];
+        s0 = sch[34];
     }
 
     if (warp == CW) {
         // ------------------------------------------------ producer warp
         // Lane u fetches unit u (slot u / kQ8Sub).  b, g, j: the step's sequence, head
         // group and index; cn steps per group from cs on.
-        int b = sch[33], cs = sch[34];
+        int b = b0, cs = s0;
         int cn = q8_steps(seq_lens, b, pl), cL = seq_lens[b], g = 0;
         while (cs + cn <= start) {
             cs += cn;
             ++g;
         }
-        if (lane == 0) {  // what the join needs of every (sequence, group) that begins in this range
+        if (lane == 0 && !pl.direct) {  // what the join needs of every (sequence, group) that begins in this range
             int bb = b, gg = g, bs = cs, bn = cn;
             while (bs < end) {
                 if (bs >= start && bn > 0) {
@@ -362,10 +391,16 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 const int row = cblk * pl.Hkv + cg * HG;
                 uint8_t* kd = smem + static_cast<size_t>(stage) * pl.stage_bytes + lane * unit_bytes;
                 uint8_t* sd = scales + static_cast<size_t>(stage) * 2 * scale_half + lane * pl.scale_unit;
-                tma_load_3d(kd, &tmK, 0, tok, row, &full[stage]);
-                tma_load_2d(sd, &tmKs, tok, row, &full[stage]);
-                tma_load_3d(kd + half_stage, &tmV, 0, tok, row, &full[stage]);
-                tma_load_2d(sd + scale_half, &tmVs, tok, row, &full[stage]);
+                tma_load_3d(kd, &tmK, 0, tok >> pl.pack, row, &full[stage]);
+                tma_load_3d(kd + half_stage, &tmV, 0, tok >> pl.pack, row, &full[stage]);
+                if (pl.BS == kQ8Tok) {  // the unit's scales are one run
+                    const size_t at = static_cast<size_t>(row) * kQ8Tok;
+                    tma_load_1d(sd, k_scale + at, HG * (kQ8Tok * 4), &full[stage]);
+                    tma_load_1d(sd + scale_half, v_scale + at, HG * (kQ8Tok * 4), &full[stage]);
+                } else {
+                    tma_load_2d(sd, &tmKs, tok, row, &full[stage]);
+                    tma_load_2d(sd + scale_half, &tmVs, tok, row, &full[stage]);
+                }
             }
             if (++stage == nst) {
                 stage = 0;
@@ -393,7 +428,9 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     const int scale_off = slot * kQ8Sub * pl.scale_unit + hh * (kQ8Tok * 4);
     // ldmatrix: lane group mi gives the rows of matrix mi: (positions 8 (mi & 1) ..,
     // chunk + (mi >> 1))
-    const int lm_row = (mi & 1) * 8 + rr, lm_chunk = mi >> 1;
+    uint32_t lm[kChunks / 2];
+#pragma unroll
+    for (int c = 0; c < kChunks / 2; ++c) lm[c] = q8_at<DP>((mi & 1) * 8 + rr, 2 * c + (mi >> 1), pl.pack);
 
     // One step's kQ8Sub tiles; kPart: some of their positions lie behind the end.
     auto tiles = [&](auto part, int ntok) {
@@ -418,7 +455,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
 #pragma unroll
             for (int c = 0; c < kChunks; c += 2) {
                 uint32_t w[4];
-                ldmatrix_x4(w[0], w[1], w[2], w[3], kb + q8_at<DP>(lm_row, c + lm_chunk));
+                ldmatrix_x4(w[0], w[1], w[2], w[3], kb + lm[c / 2]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     uint32_t a[4];
@@ -511,7 +548,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
 #pragma unroll
             for (int c = 0; c < kChunks; c += 2) {
                 uint32_t w[4];
-                ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vb + q8_at<DP>(lm_row, c + lm_chunk));
+                ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vb + lm[c / 2]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     uint32_t a[4];
@@ -725,16 +762,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     const int w0 = warp % kUnitWarps;
     const bool in = u < units;
     const int b = in ? static_cast<int>(u / pl.Hq) : 0;
-    const long long vb = in ? u / pl.R : 0;
-    const int row = in ? static_cast<int>(u - vb * pl.R) : 0;
+    const size_t vb = in ? static_cast<size_t>(u / pl.R) : 0;
+    const int row = in ? static_cast<int>(u - static_cast<long long>(vb) * pl.R) : 0;
     const int L = seq_lens[b];  // older than the main kernel, so read before the wait
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int4 si4 = __ldg(reinterpret_cast<const int4*>(info + vb));  // unused where there are no steps
+    const Q8Info si{si4.x, si4.y, si4.z, 0};
     const bool valid = L >= 0 && static_cast<long long>(L) <= static_cast<long long>(pl.max_blocks) * pl.BS;
     if (in && !valid && u % pl.Hq == 0 && w0 == 0 && lane == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
     int pieces = 0, f = 0;
     if (in && valid && L > 0) {
-        const Q8Info si = info[vb];
         if (si.W > 0 && si.s >= 0 && si.n > 0) {
             f = si.s / si.W;
             pieces = (si.s + si.n - 1) / si.W - f + 1;
@@ -914,6 +952,7 @@ static bool q8_shape(int Hq, int Hkv, int D, int BS, pkv_dtype dt, Q8Plan& pl) {
     for (int h = 1; h <= kQ8Warps; ++h)
         if (Hkv % h == 0 && h * pl.QC <= kQ8Warps) pl.HG = h;
     pl.NG = Hkv / pl.HG;
+    pl.pack = D == 64;
     pl.slots = 1;
     while (pl.slots * 2 * pl.HG * pl.QC <= kQ8Warps) pl.slots *= 2;
     pl.G = G;
@@ -945,11 +984,13 @@ static bool q8_map(CUtensorMap* map, const void* pool, const Q8Plan& pl, int DP)
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     }
-    cuuint64_t dim[3] = {static_cast<cuuint64_t>(pl.D), static_cast<cuuint64_t>(pl.BS), heads};
-    cuuint64_t stride[2] = {static_cast<cuuint64_t>(pl.D), static_cast<cuuint64_t>(pl.D) * pl.BS};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(DP), kQ8Tok, static_cast<cuuint32_t>(pl.HG)};
+    const int pack = pl.pack;  // 128-byte rows of two positions
+    cuuint64_t dim[3] = {static_cast<cuuint64_t>(pl.D) << pack, static_cast<cuuint64_t>(pl.BS) >> pack, heads};
+    cuuint64_t stride[2] = {static_cast<cuuint64_t>(pl.D) << pack, static_cast<cuuint64_t>(pl.D) * pl.BS};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(DP) << pack, static_cast<cuuint32_t>(kQ8Tok) >> pack,
+                         static_cast<cuuint32_t>(pl.HG)};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dim, stride, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, DP == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, DP == 128 || pack ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -984,7 +1025,12 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(P), 1, 1);
+    // Short sequences (by the table's width) and few of them: one CTA each, so that no
+    // join is launched.
+    const int step_tok = pl.slots * kQ8Sub * kQ8Tok;
+    const long long most = (static_cast<long long>(pl.max_blocks) * pl.BS + step_tok - 1) / step_tok;
+    pl.direct = static_cast<long long>(pl.B) * pl.NG <= P && most * static_cast<long long>(per) <= kDirectBytes;
+    cfg.gridDim = dim3(static_cast<unsigned>(pl.direct ? pl.B * pl.NG : P), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>((pl.HG * pl.QC * pl.slots + 1) * 32), 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -994,8 +1040,12 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, tmKs, tmVs, pl, static_cast<const T*>(q), static_cast<T*>(out),
-                             block_tables, seq_lens, info, part_ml, part_o, status);
+                             ks, vs, block_tables, seq_lens, info, part_ml, part_o, status);
     if (err != cudaSuccess) return err;
+    if (pl.direct) {
+        *done = true;
+        return cudaGetLastError();
+    }
     const long long units = static_cast<long long>(pl.B) * pl.Hq;
     const bool many = units >= 8LL * P;
     cfg.gridDim = dim3(static_cast<unsigned>(many ? (units + kJoinWarps - 1) / kJoinWarps : units), 1, 1);
