@@ -9,10 +9,9 @@
 // Fast path (D a multiple of 16 up to 128, block size a multiple of 16): a
 // persistent kernel, one CTA per SM, over balanced ranges, and a kernel that
 // joins the sequences that several ranges share.
-//  * A tile is 16 positions of one KV head.  A step is `slots` tiles of
-//    consecutive positions of `HG` KV heads (at most 8 tiles), fetched by TMA
-//    boxes (16 positions x HG heads of K, of V and of their scales) into one
-//    stage of an mbarrier ring.  The steps of all (sequence, head group) pairs, one
+//  * A tile is 16 positions of one KV head.  A step is slots x kSub tiles of
+//    consecutive positions of `HG` KV heads (at most 8 x kSub tiles), fetched by TMA
+//    boxes of 16 positions x HG heads into one stage of an mbarrier ring.  The steps of all (sequence, head group) pairs, one
 //    after the other, are cut into one range per CTA; every CTA finds its range
 //    itself from seq_lens.
 //  * One consumer warp per (KV head, chunk of its query heads, slot) takes kSub
@@ -69,10 +68,11 @@ constexpr float kLag = 8.f;  // contributions stay below 2^8 of the running maxi
 
 // How a call is laid out; computed on the host, passed to both kernels.
 struct Q8Plan {
-    int HG, NG;      // KV heads per group, groups
+    int HG, NG;      // KV heads per group, groups (the last one may have fewer heads)
     int QC;          // chunks of query heads per KV head (8 or 16 heads each)
     int slots;       // tiles along the cache per step
     int R;           // query rows per group: HG * G
+    int UB;          // units of 16 positions per block
     int nst;         // ring stages
     int stage_bytes, scale_unit, q_bytes, scratch_bytes;
     int direct;      // one CTA per (sequence, group), no join
@@ -81,13 +81,6 @@ struct Q8Plan {
     float scale_log2;
     uint32_t polls;
     int silent_cta;
-};
-
-struct Q8Info {  // 16 bytes per (sequence, head group) with at least one step
-    int s;       // first step in the global order
-    int n;       // number of steps
-    int W;       // steps per range
-    int pad;
 };
 
 struct Q8Meta {
@@ -147,6 +140,14 @@ __device__ __forceinline__ void store_row4(__nv_bfloat16* p, float4 v) {
 }
 __device__ __forceinline__ void store_row4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// One arrival on the barrier once this thread's earlier cp.async copies have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // Steps of sequence b in one head group (0 for a length outside [0, max_blocks * BS]).
 __device__ __forceinline__ int q8_steps(const int32_t* seq_lens, int b, const Q8Plan& pl) {
     const int L = seq_lens[b], T = pl.slots * kQ8Sub * kQ8Tok;
@@ -194,11 +195,10 @@ __device__ __forceinline__ uint32_t q8_at(int tok, int c, int pack) {
 template <typename T, typename Fmt, int DP, int kN, bool kSplit>
 __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ CUtensorMap tmKs, const __grid_constant__ CUtensorMap tmVs,
                      const __grid_constant__ Q8Plan pl, const T* __restrict__ q, T* __restrict__ out,
                      const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                      const int32_t* __restrict__ block_tables, const int32_t* __restrict__ seq_lens,
-                     Q8Info* __restrict__ info, float* __restrict__ part_ml, float* __restrict__ part_o,
+                     float* __restrict__ part_ml, float* __restrict__ part_o,
                      int32_t* status) {
     constexpr int kChunks = DP / 16;
     extern __shared__ uint8_t smem_raw[];
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < nst; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 1 + 32);  // the TMA bytes, and each producer lane's scale copies
             mbar_init(&empty[s], CW);
         }
         for (int s = 0; s < 2; ++s) {
@@ -237,8 +237,6 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
         fence_mbar_init();
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
-        prefetch_tmap(&tmKs);
-        prefetch_tmap(&tmVs);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // Only after the wait: the joining kernel reads seq_lens before its own wait.
@@ -256,8 +254,9 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
         end = start + n;
         s0 = 0;
         if (n == 0) {  // empty or invalid: zeros
-            T* o = out + static_cast<size_t>(blockIdx.x) * pl.R * pl.D;
-            for (int e = threadIdx.x; e < pl.R * pl.D; e += nthr) o[e] = from_f32<T>(0.f);
+            const int g = static_cast<int>(blockIdx.x) - b0 * NG, rows = min(pl.R, pl.Hq - g * pl.R);
+            T* o = out + (static_cast<size_t>(b0) * pl.Hq + g * pl.R) * pl.D;
+            for (int e = threadIdx.x; e < rows * pl.D; e += nthr) o[e] = from_f32<T>(0.f);
             if (threadIdx.x == 0 && seq_lens[b0] != 0) report(status, PKV_ERR_DEVICE_BOUNDS);
             return;
         }
@@ -294,71 +293,73 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
 
     if (warp == CW) {
         // ------------------------------------------------ producer warp
-        // Lane u fetches unit u (slot u / kQ8Sub).  b, g, j: the step's sequence, head
-        // group and index; cn steps per group from cs on.
+        // Lane u fetches the K and V tiles of unit u (slot u / kQ8Sub) by TMA; the
+        // scales, 64 bytes per unit and head, come by 16-byte cp.async of the whole warp
+        // (a TMA copy of 64 bytes costs as much issue time as one of 16 KB).  The
+        // block ids are read two steps ahead.
+        // b, g: the walk's sequence and head group; cn steps per group from cs on.
         int b = b0, cs = s0;
         int cn = q8_steps(seq_lens, b, pl), cL = seq_lens[b], g = 0;
-        while (cs + cn <= start) {
-            cs += cn;
-            ++g;
-        }
-        if (lane == 0 && !pl.direct) {  // what the join needs of every (sequence, group) that begins in this range
-            int bb = b, gg = g, bs = cs, bn = cn;
-            while (bs < end) {
-                if (bs >= start && bn > 0) {
-                    Q8Info si;
-                    si.s = bs;
-                    si.n = bn;
-                    si.W = W;
-                    si.pad = 0;
-                    info[bb * NG + gg] = si;
-                }
-                bs += bn;
-                if (++gg == NG || bn == 0) {
-                    gg = 0;
-                    if (++bb >= B) break;
-                    bn = q8_steps(seq_lens, bb, pl);
+        struct Step {
+            int b, g, j, n, cs, L;
+            int blk;  // lane u: the block of unit u, -1: invalid, -2: behind the end
+            int tok;  // lane u: the unit's first slot in its block
+        };
+        auto fetch = [&](int i) {  // walk on to step i
+            while (cs + cn <= i) {
+                cs += cn;
+                if (++g == NG || cn == 0) {
+                    g = 0;
+                    ++b;
+                    cn = q8_steps(seq_lens, b, pl);
+                    cL = seq_lens[b];
                 }
             }
-        }
-        if (static_cast<int>(blockIdx.x) == pl.silent_cta) return;  // test hook: no copy is issued
-        const uint32_t unit_tx = 2u * unit_bytes + 2u * HG * (kQ8Tok * 4);
-        int piece = 0;
-        auto block_of = [&](int bb, int jj, int L) {  // lane u: the block of unit u, -2 behind the end
-            const long long pos = (static_cast<long long>(jj) * units + lane) * kQ8Tok;
-            if (lane >= units || pos >= L) return -2;
-            const int blk = block_tables[static_cast<size_t>(bb) * pl.max_blocks + pos / pl.BS];
-            return blk >= 0 && blk < pl.NB ? blk : -1;
+            Step s{b, g, i - cs, cn, cs, cL, -2, 0};
+            const unsigned u = static_cast<unsigned>(s.j) * units + lane;
+            if (lane < units && u * kQ8Tok < static_cast<unsigned>(cL)) {
+                const unsigned lb = pl.UB == 1 ? u : u / static_cast<unsigned>(pl.UB);
+                s.tok = static_cast<int>(u - lb * pl.UB) * kQ8Tok;
+                s.blk = block_tables[static_cast<size_t>(b) * pl.max_blocks + lb];
+            }
+            return s;
         };
+        if (static_cast<int>(blockIdx.x) == pl.silent_cta) return;  // test hook: no copy is issued
+        Step cur = fetch(start), nxt = cur;
+        if (start + 1 < end) nxt = fetch(start + 1);
+        // this lane's chunks of the scales: (unit, head, quarter) of chunk lane + 32 x
+        const int chunks = units * HG * 4;
+        constexpr int kScaleChunks = kQ8Warps * kQ8Sub * 4 / 32;
+        int su[kScaleChunks], srow[kScaleChunks], sq[kScaleChunks];
+#pragma unroll
+        for (int x = 0; x < kScaleChunks; ++x) {
+            const int c = lane + 32 * x;
+            su[x] = c < chunks ? c / (HG * 4) : -1;
+            srow[x] = (c >> 2) - max(su[x], 0) * HG;
+            sq[x] = c & 3;
+        }
+        const uint32_t unit_tx = 2u * unit_bytes;
+        int piece = 0;
         // on a timeout: wait (bounded) for the copies in flight, so that none writes
         // into shared memory after the CTA is gone
         auto drain = [&](int it) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
             if (lane != 0) return;
             for (int k = max(0, it - nst); k < it; ++k)
                 mbar_wait(&full[k % nst], static_cast<uint32_t>(k / nst) & 1u, pl.polls);
             for (int pk = max(0, piece - 2); pk < piece; ++pk)
                 mbar_wait(&qfull[pk & 1], static_cast<uint32_t>(pk >> 1) & 1u, pl.polls);
         };
-        int blk = block_of(b, start - cs, cL);
         int stage = 0;
         uint32_t parity = 1;  // of the empty barriers: the first round finds them free
         for (int i = start, it = 0; i < end; ++i, ++it) {
-            const int cb = b, cg = g, ccs = cs, ccn = cn, L = cL, j = i - cs, cblk = blk;
-            if (i + 1 < end) {  // the next step's block ids are on their way while this one waits
-                while (cs + cn <= i + 1) {
-                    cs += cn;
-                    if (++g == NG || cn == 0) {
-                        g = 0;
-                        ++b;
-                        cn = q8_steps(seq_lens, b, pl);
-                        cL = seq_lens[b];
-                    }
-                }
-                blk = block_of(b, i + 1 - cs, cL);
-            }
-            const bool first = j == 0 || i == start, last = j == ccn - 1 || i == end - 1;
-            const unsigned live = __ballot_sync(0xffffffffu, cblk >= 0);
-            const bool bad = __any_sync(0xffffffffu, cblk == -1);
+            const Step s = cur;
+            cur = nxt;
+            if (i + 2 < end) nxt = fetch(i + 2);
+            const bool first = s.j == 0 || i == start, last = s.j == s.n - 1 || i == end - 1;
+            const bool good = s.blk >= 0 && s.blk < pl.NB;
+            const unsigned live = __ballot_sync(0xffffffffu, good);
+            const bool bad = __any_sync(0xffffffffu, s.blk != -2 && !good);
             bool ok = mbar_wait(&empty[stage], parity, pl.polls);
             if (first && ok) ok = mbar_wait(&qempty[piece & 1], (static_cast<uint32_t>(piece >> 1) & 1u) ^ 1u, pl.polls);
             if (!__all_sync(0xffffffffu, ok)) {
@@ -367,41 +368,49 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 return;
             }
             if (lane == 0) {
-                if (first) {
-                    const int qs = piece & 1;
-                    mbar_arrive_expect_tx(&qfull[qs], pl.q_bytes);
-                    tma_load_1d(qring + static_cast<size_t>(qs) * pl.q_bytes,
-                                q + (static_cast<size_t>(cb) * pl.Hq + static_cast<size_t>(cg) * pl.R) * pl.D,
-                                pl.q_bytes, &qfull[qs]);
-                }
                 Q8Meta mt;
-                mt.vb = cb * NG + cg;
-                mt.left = L - j * units * kQ8Tok;
-                mt.flags = (first ? kQFirst : 0) | (last ? kQLast : 0) | (ccs >= start && ccs + ccn <= end ? kQWhole : 0) |
-                           (ccs < start ? kQHead : 0) | (bad ? kQBad : 0);
+                mt.vb = s.b * NG + s.g;
+                mt.left = s.L - s.j * units * kQ8Tok;
+                mt.flags = (first ? kQFirst : 0) | (last ? kQLast : 0) | (s.cs >= start && s.cs + s.n <= end ? kQWhole : 0) |
+                           (s.cs < start ? kQHead : 0) | (bad ? kQBad : 0);
                 mt.pad = 0;
                 meta[stage] = mt;
-                if (bad) report(status, PKV_ERR_DEVICE_BOUNDS);
-                mbar_arrive_expect_tx(&full[stage], __popc(live) * unit_tx);
+                mbar_arrive_expect_tx(&full[stage], __popc(live) * unit_tx);  // releases the metadata
             }
-            if (first) ++piece;
             __syncwarp();
-            if (cblk >= 0) {
-                const int tok = static_cast<int>(((static_cast<long long>(j) * units + lane) * kQ8Tok) % pl.BS);
-                const int row = cblk * pl.Hkv + cg * HG;
+            const int row = s.blk * pl.Hkv + s.g * HG;
+            if (good) {
                 uint8_t* kd = smem + static_cast<size_t>(stage) * pl.stage_bytes + lane * unit_bytes;
-                uint8_t* sd = scales + static_cast<size_t>(stage) * 2 * scale_half + lane * pl.scale_unit;
-                tma_load_3d(kd, &tmK, 0, tok >> pl.pack, row, &full[stage]);
-                tma_load_3d(kd + half_stage, &tmV, 0, tok >> pl.pack, row, &full[stage]);
-                if (pl.BS == kQ8Tok) {  // the unit's scales are one run
-                    const size_t at = static_cast<size_t>(row) * kQ8Tok;
-                    tma_load_1d(sd, k_scale + at, HG * (kQ8Tok * 4), &full[stage]);
-                    tma_load_1d(sd + scale_half, v_scale + at, HG * (kQ8Tok * 4), &full[stage]);
-                } else {
-                    tma_load_2d(sd, &tmKs, tok, row, &full[stage]);
-                    tma_load_2d(sd + scale_half, &tmVs, tok, row, &full[stage]);
+                tma_load_3d(kd, &tmK, 0, s.tok >> pl.pack, row, &full[stage]);
+                tma_load_3d(kd + half_stage, &tmV, 0, s.tok >> pl.pack, row, &full[stage]);
+            }
+            if (first) {
+                if (lane == 0) {
+                    const int qs = piece & 1;
+                    const int rows = min(pl.R, pl.Hq - s.g * pl.R);  // the last group may have fewer heads
+                    const uint32_t bytes = static_cast<uint32_t>(rows) * pl.D * sizeof(T);
+                    mbar_arrive_expect_tx(&qfull[qs], bytes);
+                    tma_load_1d(qring + static_cast<size_t>(qs) * pl.q_bytes,
+                                q + (static_cast<size_t>(s.b) * pl.Hq + static_cast<size_t>(s.g) * pl.R) * pl.D, bytes,
+                                &qfull[qs]);
+                }
+                ++piece;
+            }
+            if (bad && lane == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
+            uint8_t* sd = scales + static_cast<size_t>(stage) * 2 * scale_half;
+#pragma unroll
+            for (int x = 0; x < kScaleChunks; ++x) {
+                const int u = max(su[x], 0);
+                const int r0 = __shfl_sync(0xffffffffu, row, u), t0 = __shfl_sync(0xffffffffu, s.tok, u);
+                // heads behind the last one (a group with fewer) have no scales to read
+                if (su[x] >= 0 && ((live >> u) & 1u) && s.g * HG + srow[x] < pl.Hkv) {
+                    const size_t at = static_cast<size_t>(r0 + srow[x]) * pl.BS + t0 + 4 * sq[x];
+                    uint8_t* d = sd + u * pl.scale_unit + (4 * srow[x] + sq[x]) * 16;
+                    cp_async16(d, k_scale + at);
+                    cp_async16(d + scale_half, v_scale + at);
                 }
             }
+            cp_async_arrive(&full[stage]);
             if (++stage == nst) {
                 stage = 0;
                 parity ^= 1u;
@@ -579,6 +588,8 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             // head g (of each n-tile): dims 16 c + 4 r .. + 3
             const T* qsm = reinterpret_cast<const T*>(qring + static_cast<size_t>(qs) * pl.q_bytes) +
                            static_cast<size_t>(hh * pl.G) * pl.D;
+            // (none for the heads that a last, smaller group lacks)
+            const int qrows = (mt.vb % NG) * HG + hh < pl.Hkv ? pl.G : 0;
             float v[kN][kChunks][4], amax = 0.f;
 #pragma unroll
             for (int n = 0; n < kN; ++n) {
@@ -588,7 +599,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int d = c * 16 + 4 * r;
-                        v[n][c][e] = row < pl.G && d < pl.D ? to_f32(qsm[row * pl.D + d + e]) : 0.f;
+                        v[n][c][e] = row < qrows && d < pl.D ? to_f32(qsm[row * pl.D + d + e]) : 0.f;
                         amax = fmaxf(amax, fabsf(v[n][c][e]));
                     }
             }
@@ -716,11 +727,12 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int head = qc * kHeads + 8 * n + 2 * r + e;
-                if (head >= pl.G) continue;
                 const int qr = hh * pl.G + head;  // row in the group
+                const int vb_g = mt.vb % NG, row = (mt.vb / NG) * pl.Hq + vb_g * pl.R + qr;  // row of out
+                if (head >= pl.G || vb_g * pl.R + qr >= pl.Hq) continue;
                 if (mt.flags & kQWhole) {
                     const float inv = poisoned || l[n][e] == 0.f ? 0.f : 1.f / l[n][e];
-                    T* o = out + (static_cast<size_t>(mt.vb) * pl.R + qr) * pl.D + 2 * g;
+                    T* o = out + static_cast<size_t>(row) * pl.D + 2 * g;
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c)
                         if (16 * c < pl.D)
@@ -751,36 +763,55 @@ constexpr int kJoinGroup = 8;
 
 template <typename T, int kUnitWarps>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    decode_q8_join_kernel(const __grid_constant__ Q8Plan pl, const Q8Info* __restrict__ info,
-                          const int32_t* __restrict__ seq_lens, const float* __restrict__ part_ml,
-                          const float* __restrict__ part_o, T* __restrict__ out, int P, int32_t* status) {
+    decode_q8_join_kernel(const __grid_constant__ Q8Plan pl, const int32_t* __restrict__ seq_lens,
+                          const float* __restrict__ part_ml, const float* __restrict__ part_o, T* __restrict__ out,
+                          int P, int32_t* status) {
     __shared__ float4 accsh[kJoinWarps][32];
     __shared__ float mlsh[kJoinWarps][2];
+    __shared__ int sums[kJoinWarps][2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long units = static_cast<long long>(pl.B) * pl.Hq;
-    const long long u = static_cast<long long>(blockIdx.x) * (kJoinWarps / kUnitWarps) + warp / kUnitWarps;
+    const unsigned units = static_cast<unsigned>(pl.B) * pl.Hq;
+    const unsigned u0 = blockIdx.x * (kJoinWarps / kUnitWarps), u = u0 + warp / kUnitWarps;
     const int w0 = warp % kUnitWarps;
     const bool in = u < units;
-    const int b = in ? static_cast<int>(u / pl.Hq) : 0;
-    const size_t vb = in ? static_cast<size_t>(u / pl.R) : 0;
-    const int row = in ? static_cast<int>(u - static_cast<long long>(vb) * pl.R) : 0;
-    const int L = seq_lens[b];  // older than the main kernel, so read before the wait
+    const int b = static_cast<int>((in ? u : u0) / pl.Hq), bfirst = static_cast<int>(u0 / pl.Hq);
+    const int qh = in ? static_cast<int>(u - static_cast<unsigned>(b) * pl.Hq) : 0, grp = qh / pl.R;
+    // Where the sequence's steps lie in the order, from the lengths: they are older than the
+    // main kernel, which launched this one after its own wait, so everything up to the
+    // partials' addresses is done before the wait.
+    const int L = seq_lens[b];
+    int all = 0, before = 0;
+    for (int x = threadIdx.x; x < pl.B; x += kJoinWarps * 32) {
+        const int n = q8_steps(seq_lens, x, pl);
+        all += n;
+        before += x < bfirst ? n : 0;
+    }
+    all = __reduce_add_sync(0xffffffffu, all);
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) {
+        sums[warp][0] = all;
+        sums[warp][1] = before;
+    }
+    __syncthreads();
+    all = before = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        all += sums[w][0];
+        before += sums[w][1];
+    }
+    for (int x = bfirst; x < b; ++x) before += q8_steps(seq_lens, x, pl);
+    const bool valid = L >= 0 && static_cast<long long>(L) <= static_cast<long long>(pl.max_blocks) * pl.BS;
+    const int n = valid ? q8_steps(seq_lens, b, pl) : 0;
+    int pieces = 0, f = 0;
+    if (in && n > 0) {
+        const int W = (all * pl.NG + P - 1) / P, first = before * pl.NG + grp * n;
+        f = first / W;
+        pieces = (first + n - 1) / W - f + 1;
+    }
+    const int row = qh - grp * pl.R;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int4 si4 = __ldg(reinterpret_cast<const int4*>(info + vb));  // unused where there are no steps
-    const Q8Info si{si4.x, si4.y, si4.z, 0};
-    const bool valid = L >= 0 && static_cast<long long>(L) <= static_cast<long long>(pl.max_blocks) * pl.BS;
-    if (in && !valid && u % pl.Hq == 0 && w0 == 0 && lane == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
-    int pieces = 0, f = 0;
-    if (in && valid && L > 0) {
-        if (si.W > 0 && si.s >= 0 && si.n > 0) {
-            f = si.s / si.W;
-            pieces = (si.s + si.n - 1) / si.W - f + 1;
-        }
-        // a record that names slots outside the workspace (possible only when the
-        // main kernel gave up on a wait) joins nothing
-        if (f + pieces > P) pieces = 0;
-    }
+    if (in && !valid && qh == 0 && w0 == 0 && lane == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
     const bool write = in && pieces != 1;
     if (kUnitWarps == 1 && !write) return;
     if (pieces == 1) pieces = 0;
@@ -852,7 +883,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         const float inv = 1.f / l;
         v = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     }
-    store_row4(out + u * pl.D + 4 * lane, v);
+    store_row4(out + static_cast<size_t>(u) * pl.D + 4 * lane, v);
 }
 
 // ------------------------------------------------------------------ generic kernel
@@ -939,7 +970,7 @@ __global__ void __launch_bounds__(kGen8Threads)
 
 // ------------------------------------------------------------------ host side
 struct Q8Layout {  // workspace
-    size_t ml, o, total;
+    size_t o, total;
 };
 
 // Group size and slots for a shape; false where the fast kernel does not apply.
@@ -948,10 +979,13 @@ static bool q8_shape(int Hq, int Hkv, int D, int BS, pkv_dtype dt, Q8Plan& pl) {
     const int G = Hq / Hkv, rows = dt == PKV_F32 || G <= 8 ? 8 : 16;  // query heads per warp
     pl.QC = (G + rows - 1) / rows;
     if (pl.QC > kQ8Warps) return false;
-    pl.HG = 1;
-    for (int h = 1; h <= kQ8Warps; ++h)
-        if (Hkv % h == 0 && h * pl.QC <= kQ8Warps) pl.HG = h;
-    pl.NG = Hkv / pl.HG;
+    // as few groups as the warps allow, of equal size (the last one up to NG - 1 heads
+    // smaller: 11 heads are 6 + 5; the tile of the missing head is read and not used)
+    const int most = kQ8Warps / pl.QC;
+    pl.NG = (Hkv + most - 1) / most;
+    pl.HG = (Hkv + pl.NG - 1) / pl.NG;
+    pl.NG = (Hkv + pl.HG - 1) / pl.HG;
+    pl.UB = BS / kQ8Tok;
     pl.pack = D == 64;
     pl.slots = 1;
     while (pl.slots * 2 * pl.HG * pl.QC <= kQ8Warps) pl.slots *= 2;
@@ -960,30 +994,22 @@ static bool q8_shape(int Hq, int Hkv, int D, int BS, pkv_dtype dt, Q8Plan& pl) {
     return true;
 }
 
-static Q8Layout q8_layout(int B, int NG, int R, int D, int P) {
+// Two partial results per CTA of (max, sum) and D floats for every row of a group.
+static Q8Layout q8_layout(int R, int D, int P) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     Q8Layout w;
-    w.ml = up(sizeof(Q8Info) * std::max<size_t>(static_cast<size_t>(B) * NG, 1));
-    w.o = up(w.ml + static_cast<size_t>(2) * P * R * 2 * sizeof(float));
+    w.o = up(static_cast<size_t>(2) * P * R * 2 * sizeof(float));
     w.total = up(w.o + static_cast<size_t>(2) * P * R * D * sizeof(float));
     return w;
 }
 
 // A pool [NB * Hkv][BS][D] of bytes in boxes of 16 positions x HG heads x DP bytes
-// (bytes beyond D arrive as zeros), or its scales [NB * Hkv][BS] in boxes of 16 x HG.
+// (bytes beyond D arrive as zeros).
 static bool q8_map(CUtensorMap* map, const void* pool, const Q8Plan& pl, int DP) {
     EncodeTiledFn enc = get_encode_fn();
     if (!enc) return false;
     const cuuint64_t heads = static_cast<cuuint64_t>(pl.NB) * pl.Hkv;
     cuuint32_t one[3] = {1, 1, 1};
-    if (DP == 0) {
-        cuuint64_t dim[2] = {static_cast<cuuint64_t>(pl.BS), heads};
-        cuuint64_t stride[1] = {static_cast<cuuint64_t>(pl.BS) * 4};
-        cuuint32_t box[2] = {kQ8Tok, static_cast<cuuint32_t>(pl.HG)};
-        return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(pool), dim, stride, box, one,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    }
     const int pack = pl.pack;  // 128-byte rows of two positions
     cuuint64_t dim[3] = {static_cast<cuuint64_t>(pl.D) << pack, static_cast<cuuint64_t>(pl.BS) >> pack, heads};
     cuuint64_t stride[2] = {static_cast<cuuint64_t>(pl.D) << pack, static_cast<cuuint64_t>(pl.D) * pl.BS};
@@ -1002,7 +1028,7 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     constexpr bool kSplit = sizeof(T) == 4;
     const int tiles = pl.HG * pl.slots * kQ8Sub;
     pl.stage_bytes = 2 * tiles * kQ8Tok * DP;
-    pl.scale_unit = (pl.HG * kQ8Tok * 4 + 127) / 128 * 128;
+    pl.scale_unit = pl.HG * kQ8Tok * 4;
     pl.q_bytes = pl.R * pl.D * static_cast<int>(sizeof(T));
     pl.scratch_bytes = (pl.slots - 1) * pl.HG * pl.QC * (8 * kN * (DP + 6)) * 4;
     const size_t fixed = 1024 + 2 * static_cast<size_t>(pl.q_bytes) + pl.scratch_bytes +
@@ -1013,13 +1039,11 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     if (fixed + 2 * per > budget) return cudaSuccess;
     pl.nst = static_cast<int>(std::min<size_t>(kQ8MaxStages, (budget - fixed) / per));
     const size_t smem = fixed + pl.nst * per;
-    CUtensorMap tmK, tmV, tmKs, tmVs;
-    if (!q8_map(&tmK, k, pl, DP) || !q8_map(&tmV, v, pl, DP) || !q8_map(&tmKs, ks, pl, 0) || !q8_map(&tmVs, vs, pl, 0))
-        return cudaSuccess;
-    const Q8Layout wl = q8_layout(pl.B, pl.NG, pl.R, pl.D, P);
+    CUtensorMap tmK, tmV;
+    if (!q8_map(&tmK, k, pl, DP) || !q8_map(&tmV, v, pl, DP)) return cudaSuccess;
+    const Q8Layout wl = q8_layout(pl.R, pl.D, P);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    Q8Info* info = reinterpret_cast<Q8Info*>(ws);
-    float* part_ml = reinterpret_cast<float*>(ws + wl.ml);
+    float* part_ml = reinterpret_cast<float*>(ws);
     float* part_o = reinterpret_cast<float*>(ws + wl.o);
     auto kern = decode_q8_kernel<T, Fmt, DP, kN, kSplit>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -1039,8 +1063,8 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, tmKs, tmVs, pl, static_cast<const T*>(q), static_cast<T*>(out),
-                             ks, vs, block_tables, seq_lens, info, part_ml, part_o, status);
+    err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, pl, static_cast<const T*>(q), static_cast<T*>(out),
+                             ks, vs, block_tables, seq_lens, part_ml, part_o, status);
     if (err != cudaSuccess) return err;
     if (pl.direct) {
         *done = true;
@@ -1052,8 +1076,8 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
     cfg.dynamicSmemBytes = 0;
     err = cudaLaunchKernelEx(&cfg, many ? decode_q8_join_kernel<T, 1> : decode_q8_join_kernel<T, kJoinWarps>, pl,
-                             static_cast<const Q8Info*>(info), seq_lens, static_cast<const float*>(part_ml),
-                             static_cast<const float*>(part_o), static_cast<T*>(out), P, status);
+                             seq_lens, static_cast<const float*>(part_ml), static_cast<const float*>(part_o),
+                             static_cast<T*>(out), P, status);
     if (err != cudaSuccess) return err;
     *done = true;
     return cudaGetLastError();
@@ -1108,7 +1132,7 @@ extern "C" size_t pkv_decode_q8_workspace_bytes(int B, int Hq, int Hkv, int D, i
     size_t need = 256;
     for (pkv_dtype dt : {PKV_F32, PKV_BF16}) {
         Q8Plan pl = {};
-        if (q8_shape(Hq, Hkv, D, 16, dt, pl)) need = std::max(need, q8_layout(B, pl.NG, pl.R, D, P).total);
+        if (q8_shape(Hq, Hkv, D, 16, dt, pl)) need = std::max(need, q8_layout(pl.R, D, P).total);
     }
     return need;
 }
