@@ -6,60 +6,146 @@
 // anything else that reads such a pool) runs on it with a table that counts 0, 1,
 // 2, ...
 //
-// One warp per row of D values.
+// A thread holds kVec elements of a row: 8 for bf16 (8 bytes in, 16 out), 4 for
+// float32 (4 in, 16 out), so that stores are 16 bytes and neighbouring threads
+// write neighbouring 16 bytes; 1 where D or an address does not allow it.  A CTA takes
+// kReadPasses passes of as many whole rows as its threads cover, all loads of the
+// passes first.
 #include "quant8.cuh"
 
 namespace pkv {
 
-constexpr int kReadWarps = 8;
+constexpr int kReadThreads = 256;
+constexpr int kReadPasses = 8;
 
-template <typename T, typename Fmt>
-__global__ void __launch_bounds__(kReadWarps * 32)
+// kVec bytes as loaded.
+template <int kVec>
+struct Bytes {
+    uint32_t w[kVec == 8 ? 2 : 1];
+};
+template <int kVec>
+__device__ __forceinline__ Bytes<kVec> load_bytes(const uint8_t* src) {
+    Bytes<kVec> r;
+    if constexpr (kVec == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+        r.w[0] = v.x;
+        r.w[1] = v.y;
+    } else if constexpr (kVec == 4) {
+        r.w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+    } else {
+        r.w[0] = __ldg(src);
+    }
+    return r;
+}
+
+template <typename Fmt, int kVec>
+__device__ __forceinline__ void decode_row(const Bytes<kVec>& r, float (&x)[kVec]) {
+    if constexpr (kVec == 1) {
+        x[0] = Fmt::decode(static_cast<uint8_t>(r.w[0]));
+    } else {
+#pragma unroll
+        for (int k = 0; k < kVec / 4; ++k) {
+            uint32_t lo, hi;
+            Fmt::decode4(r.w[k], lo, hi);
+            const float2 a = unpack_f16x2(lo), b = unpack_f16x2(hi);
+            x[4 * k] = a.x;
+            x[4 * k + 1] = a.y;
+            x[4 * k + 2] = b.x;
+            x[4 * k + 3] = b.y;
+        }
+    }
+}
+
+template <typename T, int kVec>
+__device__ __forceinline__ void store_row(T* dst, const float (&x)[kVec]) {
+    if constexpr (kVec == 1) {
+        *dst = from_f32<T>(x[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+    } else if constexpr (kVec == 8) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                    pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    } else {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    }
+}
+
+template <typename T, typename Fmt, int kVec>
+__global__ void __launch_bounds__(kReadThreads)
     kv_read_kernel(T* __restrict__ k_out, T* __restrict__ v_out, const uint8_t* __restrict__ k_cache,
                    const uint8_t* __restrict__ v_cache, const float* __restrict__ k_scale,
-                   const float* __restrict__ v_scale, const int32_t* __restrict__ blocks, long long rows, int R, int D,
+                   const float* __restrict__ v_scale, const int32_t* __restrict__ blocks, int chunks, int R, int D,
                    int NB, int32_t* status) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long u = static_cast<long long>(blockIdx.x) * kReadWarps + warp;  // (K or V, block, row)
-    if (u >= 2 * rows) return;
-    const bool is_v = u >= rows;
-    const long long orow = is_v ? u - rows : u;
-    const int blk = blocks[orow / R];
-    T* dst = (is_v ? v_out : k_out) + orow * D;
-    if (blk < 0 || blk >= NB) {
-        if (lane == 0 && !is_v && orow % R == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
-        for (int i = lane; i < D; i += 32) dst[i] = from_f32<T>(0.f);
-        return;
+    // CTA: (block, K or V, chunk of rows)
+    const unsigned chunk = blockIdx.x % chunks, bp = blockIdx.x / chunks;
+    const bool is_v = bp & 1u;
+    const int i = static_cast<int>(bp >> 1);
+    const int blk = blocks[i];
+    const bool good = blk >= 0 && blk < NB;
+    if (!good && threadIdx.x == 0 && !is_v && chunk == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
+    const int per_row = D / kVec, rows = kReadThreads / per_row;  // threads per row, rows per pass
+    const int sub = threadIdx.x / per_row, col = (threadIdx.x - sub * per_row) * kVec;
+    if (sub >= rows) return;
+    const int r0 = chunk * rows * kReadPasses + sub, last = R - 1;
+    const uint8_t* src = (is_v ? v_cache : k_cache) + static_cast<size_t>(good ? blk : 0) * R * D + col;
+    const float* sc = (is_v ? v_scale : k_scale) + static_cast<size_t>(good ? blk : 0) * R;
+    T* dst = (is_v ? v_out : k_out) + static_cast<size_t>(i) * R * D + col;
+    // every load before the first use; rows behind the block's end read its last row again
+    Bytes<kVec> raw[kReadPasses];
+    float scale[kReadPasses];
+#pragma unroll
+    for (int p = 0; p < kReadPasses; ++p) {
+        const int r = min(r0 + p * rows, last);
+        raw[p] = load_bytes<kVec>(src + r * D);
+        scale[p] = __ldg(sc + r);
     }
-    const long long irow = static_cast<long long>(blk) * R + orow % R;
-    const float scale = (is_v ? v_scale : k_scale)[irow];
-    const uint8_t* src = (is_v ? v_cache : k_cache) + irow * D;
-    for (int i = lane; i < D; i += 32) dst[i] = from_f32<T>(Fmt::decode(src[i]) * scale);
+#pragma unroll
+    for (int p = 0; p < kReadPasses; ++p) {
+        const int r = r0 + p * rows;
+        if (r > last) break;
+        float x[kVec];
+        decode_row<Fmt, kVec>(raw[p], x);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) x[e] = good ? x[e] * scale[p] : 0.f;
+        store_row<T, kVec>(dst + r * D, x);
+    }
 }
 
 template <typename T, typename Fmt>
 static cudaError_t launch_read(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
                                const float* k_scale, const float* v_scale, const int32_t* blocks, int n, int R, int D,
                                int NB, int32_t* status, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(n) * R;
-    const long long grid = (2 * rows + kReadWarps - 1) / kReadWarps;
-    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(kReadWarps * 32, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(
-        &cfg, kv_read_kernel<T, Fmt>, static_cast<T*>(k_out), static_cast<T*>(v_out),
-        static_cast<const uint8_t*>(k_cache), static_cast<const uint8_t*>(v_cache), k_scale, v_scale, blocks, rows, R,
-        D, NB, status);
-    return err != cudaSuccess ? err : cudaGetLastError();
+    auto fits = [&](int vec) {
+        const uintptr_t out = reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out);
+        const uintptr_t in = reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache);
+        return D % vec == 0 && in % vec == 0 && out % (vec * sizeof(T)) == 0;
+    };
+    auto run = [&](auto kern, int vec) {
+        const int rows = kReadThreads / (D / vec) * kReadPasses;
+        const int chunks = (R + rows - 1) / rows;
+        const long long grid = 2LL * n * chunks;
+        if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+        cfg.blockDim = dim3(kReadThreads, 1, 1);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const cudaError_t err = cudaLaunchKernelEx(
+            &cfg, kern, static_cast<T*>(k_out), static_cast<T*>(v_out), static_cast<const uint8_t*>(k_cache),
+            static_cast<const uint8_t*>(v_cache), k_scale, v_scale, blocks, chunks, R, D, NB, status);
+        return err != cudaSuccess ? err : cudaGetLastError();
+    };
+    if constexpr (sizeof(T) == 2) {
+        if (fits(8)) return run(kv_read_kernel<T, Fmt, 8>, 8);
+    }
+    if (fits(4)) return run(kv_read_kernel<T, Fmt, 4>, 4);
+    return run(kv_read_kernel<T, Fmt, 1>, 1);
 }
 
 }  // namespace pkv
@@ -71,7 +157,7 @@ extern "C" pkv_status pkv_kv_read_blocks_q8(void* k_out, void* v_out, const void
     if (n < 0 || Hkv < 1 || D < 1 || D > 256 || block_size < 1 || num_blocks < 1 ||
         (out_dtype != PKV_F32 && out_dtype != PKV_BF16) || (cache_dtype != PKV_E4M3 && cache_dtype != PKV_I8))
         return PKV_ERR_INVALID_ARG;
-    if (static_cast<long long>(Hkv) * block_size > 0x7fffffffLL) return PKV_ERR_INVALID_ARG;
+    if (static_cast<long long>(Hkv) * block_size * D > 0x7fffffffLL) return PKV_ERR_INVALID_ARG;
     if (n == 0) return PKV_OK;
     if (!k_out || !v_out || !k_cache || !v_cache || !k_scale || !v_scale || !blocks) return PKV_ERR_INVALID_ARG;
     auto launch = out_dtype == PKV_F32

@@ -15,13 +15,21 @@
 // the angle keeps its full precision at any position, and sincospif needs no
 // range reduction.
 //
-// One warp per row.
+// Vector kernel (D a multiple of 8, 16-byte aligned rows): a lane holds 8 consecutive
+// elements of a row, D / 8 lanes a row, 32 / (D / 8) rows a warp.  A lane's
+// dimensions are the same in every row, so cosines, sines and norm weights are
+// read once per token into registers, and the rotation's partner elements come by
+// shuffle (half a multiple of 8) or through shared memory.  The first rows are
+// loaded before the token's place and angles are known, which hides that chain of
+// loads.  The other kernel (any D and alignment) gives a warp one row, one element
+// per lane and step.
 #include "quant8.cuh"
 
 namespace pkv {
 
 constexpr int kWriteWarps = 8;
 constexpr int kWriteMaxD = 256;
+constexpr int kPassesPerWarp = 12;  // of one token, where there are enough tokens
 
 int device_sm_count();
 
@@ -81,9 +89,17 @@ __device__ __forceinline__ Place place_of(const WriteArgs& a, int t) {
     return p;
 }
 
+// cos and sin of pos * freq (turns in units of 2^-64, whole turns wrap away).
+__device__ __forceinline__ float2 turn_of(int pos, int64_t freq) {
+    const uint64_t f = static_cast<uint64_t>(pos) * static_cast<uint64_t>(freq);
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int64_t>(f)) * 1.0842021724855044e-19f, &s, &c);  // 2^-63
+    return make_float2(c, s);
+}
+
 // T: element type of the rows; Fmt: the 8-bit format, or FmtNone for a cache of T.
 template <typename T, typename Fmt>
-__global__ void __launch_bounds__(kWriteWarps * 32) kv_write_kernel(const WriteArgs a) {
+__global__ void __launch_bounds__(kWriteWarps * 32) kv_write_any_kernel(const WriteArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kPer = kWriteMaxD / 32;
@@ -93,12 +109,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv_write_kernel(const WriteA
     if (a.q_start != nullptr && t >= a.q_start[a.B]) return;  // rows behind the last sequence stay as they are
     const Place p = place_of(a, t);
     if ((!p.ok || p.blk < 0) && threadIdx.x == 0 && blockIdx.y == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
-    for (int j = threadIdx.x; j < a.half; j += blockDim.x) {
-        const uint64_t f = static_cast<uint64_t>(p.pos) * static_cast<uint64_t>(a.freqs[j]);
-        float s, c;
-        sincospif(static_cast<float>(static_cast<int64_t>(f)) * 1.0842021724855044e-19f, &s, &c);  // 2^-63
-        turn[j] = make_float2(c, s);
-    }
+    for (int j = threadIdx.x; j < a.half; j += blockDim.x) turn[j] = turn_of(p.pos, a.freqs[j]);
     __syncthreads();
     const int rows = a.Hq + 2 * a.Hkv;
     for (int r = blockIdx.y * kWriteWarps + warp; r < rows; r += gridDim.y * kWriteWarps) {
@@ -179,7 +190,256 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv_write_kernel(const WriteA
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 const int i = lane + 32 * k;
-                if (i < a.D) dst[i] = from_f32<T>(x[k]);
+                if (i < a.D) dst[i] = is_v ? src[i] : from_f32<T>(x[k]);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ vector kernel
+// 8 elements of T as loaded.
+template <typename T>
+struct Vec8 {
+    uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Vec8<T> load8(const T* p) {
+    Vec8<T> r;
+#pragma unroll
+    for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) r.v[k] = reinterpret_cast<const uint4*>(p)[k];
+    return r;
+}
+__device__ __forceinline__ void to_floats(const Vec8<__nv_bfloat16>& r, float (&x)[8]) {
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[2 * k] = bf16_lo(w[k]);
+        x[2 * k + 1] = bf16_hi(w[k]);
+    }
+}
+__device__ __forceinline__ void to_floats(const Vec8<float>& r, float (&x)[8]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        x[4 * k] = __uint_as_float(r.v[k].x);
+        x[4 * k + 1] = __uint_as_float(r.v[k].y);
+        x[4 * k + 2] = __uint_as_float(r.v[k].z);
+        x[4 * k + 3] = __uint_as_float(r.v[k].w);
+    }
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// Layout of the vector kernel, from the host.
+struct WritePlan {
+    int lanes, per;  // lanes a row, rows a pass
+    int passes;      // passes over a token's rows
+    int magic;       // lane / lanes = lane * magic >> 16
+    int pow2;        // lanes is a power of two
+    int wpt_log2;    // warps per token
+};
+
+// op over the lanes of a row (l: this lane's index among them, base: their first lane).
+template <typename V, typename Op>
+__device__ __forceinline__ V row_reduce(V x, const WritePlan& w, int l, int base, Op op) {
+    if (w.pow2) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            if (o < w.lanes) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+        return x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const V y = __shfl_down_sync(0xffffffffu, x, o);
+        if (l + o < w.lanes) x = op(x, y);
+    }
+    return __shfl_sync(0xffffffffu, x, base);
+}
+
+// kRot: 0 no rotation, 1 pairs (j, j + half) with half a multiple of 8, 2 such pairs
+// with any half, 3 pairs (2j, 2j + 1).
+template <typename T, typename Fmt, int kRot>
+__global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 ? 2 : 3) kv_write_kernel(const WriteArgs a, const WritePlan w) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;  // passes in flight
+    constexpr int kPad = kWriteMaxD + kWriteMaxD / 8;
+    constexpr int kTable = kWriteMaxD / 2 + 8;      // pairs, and 8 that turn nothing
+    __shared__ float rowbuf[kRot == 2 ? kWriteWarps : 1][kRot == 2 ? 2 * kPad : 1];
+    __shared__ __align__(16) float2 turn[kRot == 0 ? 1 : kWriteWarps * kTable];  // [token of the CTA][pair]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wpt = 1 << w.wpt_log2, tok = warp >> w.wpt_log2;
+    const int t = (blockIdx.x << (3 - w.wpt_log2)) + tok;
+    const int sub = (lane * w.magic) >> 16, base = sub * w.lanes, l = lane - base;
+    const int rows = a.Hq + 2 * a.Hkv, passes = w.passes;
+    const int stride = wpt * gridDim.y;
+    const bool in = t < a.T;
+    const int first = blockIdx.y * wpt + (warp & (wpt - 1));
+    // row r of the token (queries, keys, values): its kind's pointer plus r * D
+    const T* qp = static_cast<const T*>(a.q) + t * a.q_stride + 8 * l;
+    const T* kp = static_cast<const T*>(a.k) + t * a.k_stride + 8 * l - a.Hq * a.D;
+    const T* vp = static_cast<const T*>(a.v) + t * a.v_stride + 8 * l - (a.Hq + a.Hkv) * a.D;
+    Vec8<T> raw[kBatch];
+    auto load = [&](int p0) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int r = (p0 + k * stride) * w.per + sub;
+            const T* src = (r < a.Hq ? qp : r < a.Hq + a.Hkv ? kp : vp) + r * a.D;
+            if (in && sub < w.per && r < rows) raw[k] = load8(src);
+        }
+    };
+    load(first);
+    const bool active = in && (a.q_start == nullptr || t < a.q_start[a.B]);  // rows behind the last sequence stay
+    // norm weights and frequencies do not wait for the token's place either
+    Vec8<T> wq, wk;
+    if (a.q_weight != nullptr) wq = load8(static_cast<const T*>(a.q_weight) + 8 * l);
+    if (a.k_weight != nullptr) wk = load8(static_cast<const T*>(a.k_weight) + 8 * l);
+    Place p{0, 0, -1, 0};
+    if (active) p = place_of(a, t);
+    // this lane's cosines and sines: of elements 8 l + e (the sine with the sign it enters
+    // with), or of pairs 4 l + e when interleaved
+    constexpr int kTurns = kRot == 3 ? 4 : kRot != 0 ? 8 : 1;
+    float cs[kTurns], sn[kTurns];
+    if constexpr (kRot != 0) {
+        float2* tt = turn + tok * kTable;
+        if (active) {
+            const int fill = kRot == 3 ? a.D / 2 : a.half + 8;
+            for (int j = (warp & (wpt - 1)) * 32 + lane; j < fill; j += wpt * 32)
+                tt[j] = j < a.half ? turn_of(p.pos, a.freqs[j]) : make_float2(1.f, 0.f);
+        }
+        __syncthreads();
+        if constexpr (kRot == 2) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = 8 * l + e;
+                const float2 v = tt[i < a.half ? i : i < 2 * a.half ? i - a.half : a.half];
+                cs[e] = v.x;
+                sn[e] = i < a.half ? -v.y : v.y;
+            }
+        } else {
+            const int d = a.half >> 3;
+            const int j = kRot == 3 ? 4 * l : 8 * (l < d ? l : l < 2 * d ? l - d : d);
+            const float4* row = reinterpret_cast<const float4*>(tt + j);
+#pragma unroll
+            for (int e = 0; e < kTurns / 2; ++e) {
+                const float4 v = row[e];
+                cs[2 * e] = v.x;
+                cs[2 * e + 1] = v.z;
+                sn[2 * e] = kRot == 1 && l < d ? -v.y : v.y;
+                sn[2 * e + 1] = kRot == 1 && l < d ? -v.w : v.w;
+            }
+        }
+    }
+    if (!active) return;
+    if ((!p.ok || p.blk < 0) && first == 0 && lane == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
+    const float inv_d = 1.0f / static_cast<float>(a.D);
+    T* qo = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.Hq * a.D + 8 * l;
+    const size_t slot0 = static_cast<size_t>(max(p.blk, 0)) * a.Hkv * a.BS + p.slot;  // row of KV head 0
+    for (int p0 = first; p0 < passes; p0 += kBatch * stride) {
+        if (p0 != first) load(p0);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int pass = p0 + k * stride;
+            if (pass >= passes) break;
+            const int r = pass * w.per + sub;
+            const bool mine = sub < w.per && r < rows;
+            const bool is_q = r < a.Hq, is_v = r >= a.Hq + a.Hkv;
+            float x[8];
+            to_floats(raw[k], x);
+            if (pass * w.per < a.Hq + a.Hkv) {  // some row of the pass is a query or a key
+                if (a.q_weight != nullptr || a.k_weight != nullptr) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+                    ss = row_reduce(ss, w, l, base, [](float u, float v) { return u + v; });
+                    const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
+                    if (!is_v && (is_q ? a.q_weight : a.k_weight) != nullptr) {
+                        float g[8];
+                        to_floats(is_q ? wq : wk, g);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * g[e];
+                    }
+                }
+                if constexpr (kRot == 3) {
+                    if (!is_v) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float u = x[2 * e], v = x[2 * e + 1];
+                            x[2 * e] = fmaf(u, cs[e], -v * sn[e]);
+                            x[2 * e + 1] = fmaf(v, cs[e], u * sn[e]);
+                        }
+                    }
+                } else if constexpr (kRot != 0) {
+                    float o[8];
+                    if constexpr (kRot == 1) {
+                        const int d = a.half >> 3, from = base + (l < d ? l + d : l < 2 * d ? l - d : l);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, x[e], from);
+                    } else {
+                        // rows through shared memory, one word of padding per 8
+                        float* buf = rowbuf[warp];
+                        const int at = sub * (a.D + a.D / 8);
+                        __syncwarp();
+                        if (sub < w.per) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) buf[at + 9 * l + e] = x[e];
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int i = 8 * l + e, q = i < a.half ? i + a.half : i < 2 * a.half ? i - a.half : i;
+                            o[e] = sub < w.per ? buf[at + q + (q >> 3)] : 0.f;
+                        }
+                    }
+                    if (!is_v) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], cs[e], o[e] * sn[e]);
+                    }
+                }
+            }
+            if (is_q && mine) {
+                if (!p.ok) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = 0.f;
+                }
+                store8(qo + r * a.D, x);
+            }
+            const bool put = mine && !is_q && p.blk >= 0;
+            const size_t row = slot0 + (is_v ? r - a.Hq - a.Hkv : r - a.Hq) * a.BS;
+            if constexpr (Fmt::kQuant) {
+                if ((pass + 1) * w.per <= a.Hq) continue;  // queries only
+                // the largest |x| as an integer: infinities and NaN are above every finite number
+                uint32_t top = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+                top = row_reduce(top, w, l, base, [](uint32_t u, uint32_t v) { return max(u, v); });
+                const bool finite = top < 0x7f800000u;
+                const float scale = row_scale(__uint_as_float(top), Fmt::kInvQ);
+                const float inv = __frcp_rn(scale);
+                if (put) {
+                    uint2 v = make_uint2(0u, 0u);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(x[e], inv);
+                    if (finite) v = make_uint2(Fmt::encode4(x), Fmt::encode4(x + 4));
+                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + row * a.D + 8 * l) = v;
+                    if (l == 0) {
+                        (is_v ? a.v_scale : a.k_scale)[row] = finite ? scale : __int_as_float(0x7fffffff);
+                        if (!finite) report(a.status, PKV_ERR_NONFINITE);
+                    }
+                }
+            } else if (put) {
+                T* dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) + row * a.D + 8 * l;
+                if (is_v) {  // the bits as they are
+#pragma unroll
+                    for (int e = 0; e < static_cast<int>(sizeof(T)) / 2; ++e) reinterpret_cast<uint4*>(dst)[e] = raw[k].v[e];
+                } else {
+                    store8(dst, x);
+                }
             }
         }
     }
@@ -187,11 +447,8 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv_write_kernel(const WriteA
 
 template <typename T, typename Fmt>
 static cudaError_t launch_typed(const WriteArgs& a, cudaStream_t stream) {
-    const int rows = a.Hq + 2 * a.Hkv;
-    // few tokens: a token's rows over several CTAs
-    const unsigned split = a.T < 2 * device_sm_count() ? static_cast<unsigned>((rows + kWriteWarps - 1) / kWriteWarps) : 1u;
+    const int rows = a.Hq + 2 * a.Hkv, sms = device_sm_count();
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.T), split, 1);
     cfg.blockDim = dim3(kWriteWarps * 32, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -199,7 +456,44 @@ static cudaError_t launch_typed(const WriteArgs& a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, kv_write_kernel<T, Fmt>, a);
+    uintptr_t at = 0;  // every address a lane's 8 elements start from
+    for (const void* x : {static_cast<const void*>(a.q_out), a.q, a.k, a.v, a.q_weight, a.k_weight,
+                          static_cast<const void*>(a.k_cache), static_cast<const void*>(a.v_cache)})
+        at |= reinterpret_cast<uintptr_t>(x);
+    const long long es = sizeof(T);
+    const bool vec = a.D % 8 == 0 && at % 16 == 0 && ((a.q ? a.q_stride : 0) * es) % 16 == 0 &&
+                     (a.k_stride * es) % 16 == 0 && (a.v_stride * es) % 16 == 0;
+    cudaError_t err;
+    if (vec) {
+        WritePlan w;
+        w.lanes = a.D / 8;
+        w.per = 32 / w.lanes;
+        w.magic = 65536 / w.lanes + 1;  // exact for lane < 32, lanes <= 32
+        w.pow2 = (w.lanes & (w.lanes - 1)) == 0;
+        const int passes = w.passes = (rows + w.per - 1) / w.per;
+        // many tokens: a warp takes many passes of one token, which shares the token's place,
+        // angles and weights; few: a token's passes over as many warps and CTAs as there are
+        w.wpt_log2 = 3;
+        int split = 1;
+        while (w.wpt_log2 > 0 && passes < kPassesPerWarp << w.wpt_log2 &&
+               (static_cast<long long>(a.T) << w.wpt_log2) >= 2LL * 24 * sms)
+            --w.wpt_log2;
+        if (w.wpt_log2 == 3)
+            while (split * kWriteWarps < passes && static_cast<long long>(a.T) * split < 2LL * sms) ++split;
+        const int tpc = kWriteWarps >> w.wpt_log2;
+        cfg.gridDim = dim3(static_cast<unsigned>((a.T + tpc - 1) / tpc), static_cast<unsigned>(split), 1);
+        const int rot = a.half == 0 ? 0 : a.interleaved ? 3 : a.half % 8 == 0 ? 1 : 2;
+        auto kern = rot == 0   ? kv_write_kernel<T, Fmt, 0>
+                    : rot == 1 ? kv_write_kernel<T, Fmt, 1>
+                    : rot == 2 ? kv_write_kernel<T, Fmt, 2>
+                               : kv_write_kernel<T, Fmt, 3>;
+        err = cudaLaunchKernelEx(&cfg, kern, a, w);
+    } else {
+        // few tokens: a token's rows over several CTAs
+        const unsigned split = a.T < 2 * sms ? static_cast<unsigned>((rows + kWriteWarps - 1) / kWriteWarps) : 1u;
+        cfg.gridDim = dim3(static_cast<unsigned>(a.T), split, 1);
+        err = cudaLaunchKernelEx(&cfg, kv_write_any_kernel<T, Fmt>, a);
+    }
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 

@@ -11,7 +11,8 @@
 // appending needs no other token's data, and in attention the K scale multiplies
 // a score and the V scale a softmax weight, never a single element.  The floor
 // 2^-64 keeps 1 / scale finite for rows that are all zero.  x_i * (1 / scale) can
-// exceed Q by a rounding of the product; both conversions saturate.
+// exceed Q by roundings of the scale and the product, which both conversions round
+// back to Q.
 // A row that holds a NaN or an infinity is stored as zeros with scale NaN.
 #pragma once
 
@@ -20,6 +21,20 @@
 namespace pkv {
 
 constexpr float kMinScale = 5.421010862427522e-20f;  // 2^-64
+
+// two floats <-> two halves, lo in bits 0-15
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) {
+    float2 f;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}"
+        : "=f"(f.x), "=f"(f.y)
+        : "r"(v));
+    return f;
+}
 
 struct FmtNone {  // rows kept in their own type
     static constexpr bool kQuant = false;
@@ -33,6 +48,9 @@ struct FmtE4M3 {
         uint16_t v;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(v) : "f"(hi), "f"(lo));
         return v;
+    }
+    static __device__ __forceinline__ uint32_t encode4(const float* x) {
+        return encode2(x[0], x[1]) | encode2(x[2], x[3]) << 16;
     }
     // bytes 0, 1 of v -> two halves (exact: every e4m3 number is a half)
     static __device__ __forceinline__ uint32_t decode2(uint16_t v) {
@@ -60,10 +78,15 @@ struct FmtE4M3 {
 struct FmtI8 {
     static constexpr bool kQuant = true;
     static constexpr float kInvQ = 1.0f / 127.0f;
-    static __device__ __forceinline__ uint32_t encode(float x) {
-        return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(x), -127.f), 127.f))) & 0xffu;
+    // |x| <= 127 (1 + 2^-22): adding 1.5 * 2^23 rounds to nearest even into the low byte
+    static __device__ __forceinline__ uint32_t rounded(float x) { return __float_as_uint(__fadd_rn(x, 12582912.f)); }
+    static __device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+        return __byte_perm(rounded(lo), rounded(hi), 0x0040) & 0xffffu;
     }
-    static __device__ __forceinline__ uint32_t encode2(float lo, float hi) { return encode(lo) | encode(hi) << 8; }
+    static __device__ __forceinline__ uint32_t encode4(const float* x) {
+        return __byte_perm(__byte_perm(rounded(x[0]), rounded(x[1]), 0x0040),
+                           __byte_perm(rounded(x[2]), rounded(x[3]), 0x0040), 0x5410);
+    }
     // x + 128 in the low byte of a half whose ulp is 1: 1024 + (x + 128), minus 1152
     static __device__ __forceinline__ uint32_t unbias(uint32_t h) {
         uint32_t r;
