@@ -10,13 +10,16 @@
 // float32 (4 in, 16 out), so that stores are 16 bytes and neighbouring threads
 // write neighbouring 16 bytes; 1 where D or an address does not allow it.  A CTA takes
 // kReadPasses passes of as many whole rows as its threads cover, all loads of the
-// passes first.
+// passes first, with the streaming hint: a cached byte is read once here.
+// HBM-bound.  9216 blocks of 8 heads x 16 x 128 in e4m3 to bf16 (915 MB moved):
+// 4 passes 140 us, 6.55 TB/s, 98% of the measured copy rate; 2 passes 156, 8
+// passes 167 us, 4 passes without the hint 159 us.
 #include "quant8.cuh"
 
 namespace pkv {
 
 constexpr int kReadThreads = 256;
-constexpr int kReadPasses = 8;
+constexpr int kReadPasses = 4;
 
 // kVec bytes as loaded.
 template <int kVec>
@@ -27,13 +30,13 @@ template <int kVec>
 __device__ __forceinline__ Bytes<kVec> load_bytes(const uint8_t* src) {
     Bytes<kVec> r;
     if constexpr (kVec == 8) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src));
         r.w[0] = v.x;
         r.w[1] = v.y;
     } else if constexpr (kVec == 4) {
-        r.w[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+        r.w[0] = __ldcs(reinterpret_cast<const uint32_t*>(src));
     } else {
-        r.w[0] = __ldg(src);
+        r.w[0] = __ldcs(src);
     }
     return r;
 }

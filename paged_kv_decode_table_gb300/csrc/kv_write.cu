@@ -15,14 +15,16 @@
 // the angle keeps its full precision at any position, and sincospif needs no
 // range reduction.
 //
-// Vector kernel (D a multiple of 8, 16-byte aligned rows): a lane holds 8 consecutive
-// elements of a row, D / 8 lanes a row, 32 / (D / 8) rows a warp.  A lane's
+// Vector kernel (D a multiple of 8, 16-byte aligned rows): a lane holds 8 elements of
+// a row in two runs of 4, D / 8 lanes a row, 32 / (D / 8) rows a warp and pass.  A lane's
 // dimensions are the same in every row, so cosines, sines and norm weights are
-// read once per token into registers, and the rotation's partner elements come by
-// shuffle (half a multiple of 8) or through shared memory.  The first rows are
-// loaded before the token's place and angles are known, which hides that chain of
-// loads.  The other kernel (any D and alignment) gives a warp one row, one element
+// read once per token into registers, and for pairs (j, j + half) the second run
+// holds the partners of the first (half a multiple of 4; else they come through
+// shared memory).  The first rows are loaded before the token's place and angles
+// are known, which hides that chain of loads, and later ones kAhead passes early.  The other kernel (any D and alignment) gives a warp one row, one element
 // per lane and step.
+#include <type_traits>
+
 #include "quant8.cuh"
 
 namespace pkv {
@@ -197,42 +199,64 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv_write_any_kernel(const Wr
 }
 
 // ------------------------------------------------------------------ vector kernel
-// 8 elements of T as loaded.
-template <typename T>
-struct Vec8 {
-    uint4 v[sizeof(T) / 2];
-};
-template <typename T>
-__device__ __forceinline__ Vec8<T> load8(const T* p) {
-    Vec8<T> r;
-#pragma unroll
-    for (int k = 0; k < static_cast<int>(sizeof(T)) / 2; ++k) r.v[k] = reinterpret_cast<const uint4*>(p)[k];
+// A lane's 8 elements are two runs of 4, A and B, each as two packed pairs of floats
+// (fma.rn.f32x2: two roundings per instruction).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
     return r;
 }
-__device__ __forceinline__ void to_floats(const Vec8<__nv_bfloat16>& r, float (&x)[8]) {
-    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        x[2 * k] = bf16_lo(w[k]);
-        x[2 * k + 1] = bf16_hi(w[k]);
-    }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(r))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return r;
 }
-__device__ __forceinline__ void to_floats(const Vec8<float>& r, float (&x)[8]) {
+
+// The two runs as loaded (bf16: 8 bytes each, float: 16).
+template <typename T>
+struct Runs;
+template <>
+struct Runs<__nv_bfloat16> {
+    uint2 v[2];
+};
+template <>
+struct Runs<float> {
+    float4 v[2];
+};
+template <typename T>
+__device__ __forceinline__ Runs<T> load_runs(const T* p, int gap) {  // run B lies gap elements behind run A
+    Runs<T> r;
+    using V = std::remove_reference_t<decltype(r.v[0])>;
+    r.v[0] = *reinterpret_cast<const V*>(p);
+    r.v[1] = *reinterpret_cast<const V*>(p + gap);
+    return r;
+}
+__device__ __forceinline__ void to_floats(const Runs<__nv_bfloat16>& r, float2 (&x)[4]) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        x[4 * k] = __uint_as_float(r.v[k].x);
-        x[4 * k + 1] = __uint_as_float(r.v[k].y);
-        x[4 * k + 2] = __uint_as_float(r.v[k].z);
-        x[4 * k + 3] = __uint_as_float(r.v[k].w);
+        x[2 * k] = make_float2(bf16_lo(r.v[k].x), bf16_hi(r.v[k].x));
+        x[2 * k + 1] = make_float2(bf16_lo(r.v[k].y), bf16_hi(r.v[k].y));
     }
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                              pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ void to_floats(const Runs<float>& r, float2 (&x)[4]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        x[2 * k] = make_float2(r.v[k].x, r.v[k].y);
+        x[2 * k + 1] = make_float2(r.v[k].z, r.v[k].w);
+    }
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store_runs(__nv_bfloat16* p, int gap, const float2 (&x)[4]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y));
+    *reinterpret_cast<uint2*>(p + gap) = make_uint2(pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
+}
+__device__ __forceinline__ void store_runs(float* p, int gap, const float2 (&x)[4]) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    *reinterpret_cast<float4*>(p + gap) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
 }
 
 // Layout of the vector kernel, from the host.
@@ -261,184 +285,185 @@ __device__ __forceinline__ V row_reduce(V x, const WritePlan& w, int l, int base
     return __shfl_sync(0xffffffffu, x, base);
 }
 
-// kRot: 0 no rotation, 1 pairs (j, j + half) with half a multiple of 8, 2 such pairs
+// kRot: 0 no rotation, 1 pairs (j, j + half) with half a multiple of 4, 2 such pairs
 // with any half, 3 pairs (2j, 2j + 1).
 template <typename T, typename Fmt, int kRot>
 __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 ? 2 : 3) kv_write_kernel(const WriteArgs a, const WritePlan w) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kBatch = sizeof(T) == 2 ? 4 : 2;  // passes in flight
+    constexpr int kAhead = 2;  // passes in flight per warp
     constexpr int kPad = kWriteMaxD + kWriteMaxD / 8;
-    constexpr int kTable = kWriteMaxD / 2 + 8;      // pairs, and 8 that turn nothing
+    constexpr int kTable = kWriteMaxD / 2;
     __shared__ float rowbuf[kRot == 2 ? kWriteWarps : 1][kRot == 2 ? 2 * kPad : 1];
     __shared__ __align__(16) float2 turn[kRot == 0 ? 1 : kWriteWarps * kTable];  // [token of the CTA][pair]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wpt = 1 << w.wpt_log2, tok = warp >> w.wpt_log2;
     const int t = (blockIdx.x << (3 - w.wpt_log2)) + tok;
     const int sub = (lane * w.magic) >> 16, base = sub * w.lanes, l = lane - base;
-    const int rows = a.Hq + 2 * a.Hkv, passes = w.passes;
+    // the lane's elements: at0 .. at0 + 3 and at0 + gap .. + 3; with kRot 1 the second run
+    // holds the partners of the first, so that no element has to travel
+    const bool turns = kRot == 1 && 4 * l < a.half;
+    const int at0 = turns ? 4 * l : 8 * l, gap = turns ? a.half : 4;
+    const int rows = a.Hq + 2 * a.Hkv, kvrow = a.Hq + a.Hkv;
     const int stride = wpt * gridDim.y;
-    const bool in = t < a.T;
+    const bool in = t < a.T && sub < w.per;
     const int first = blockIdx.y * wpt + (warp & (wpt - 1));
-    // row r of the token (queries, keys, values): its kind's pointer plus r * D
-    const T* qp = static_cast<const T*>(a.q) + t * a.q_stride + 8 * l;
-    const T* kp = static_cast<const T*>(a.k) + t * a.k_stride + 8 * l - a.Hq * a.D;
-    const T* vp = static_cast<const T*>(a.v) + t * a.v_stride + 8 * l - (a.Hq + a.Hkv) * a.D;
-    Vec8<T> raw[kBatch];
-    auto load = [&](int p0) {
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int r = (p0 + k * stride) * w.per + sub;
-            const T* src = (r < a.Hq ? qp : r < a.Hq + a.Hkv ? kp : vp) + r * a.D;
-            if (in && sub < w.per && r < rows) raw[k] = load8(src);
-        }
+    // row r of the token (queries, keys, values) is at its kind's pointer plus r * D
+    const T* qp = static_cast<const T*>(a.q) + t * a.q_stride + at0;
+    const T* kp = static_cast<const T*>(a.k) + t * a.k_stride + at0 - a.Hq * a.D;
+    const T* vp = static_cast<const T*>(a.v) + t * a.v_stride + at0 - kvrow * a.D;
+    Runs<T> raw[kAhead];
+    auto load = [&](Runs<T>& to, int pass) {
+        const int r = pass * w.per + sub;
+        if (in && r < rows) to = load_runs((r < a.Hq ? qp : r < kvrow ? kp : vp) + r * a.D, gap);
     };
-    load(first);
-    const bool active = in && (a.q_start == nullptr || t < a.q_start[a.B]);  // rows behind the last sequence stay
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) load(raw[k], first + k * stride);
+    const bool active = t < a.T && (a.q_start == nullptr || t < a.q_start[a.B]);  // rows behind the last sequence stay
     // norm weights and frequencies do not wait for the token's place either
-    Vec8<T> wq, wk;
-    if (a.q_weight != nullptr) wq = load8(static_cast<const T*>(a.q_weight) + 8 * l);
-    if (a.k_weight != nullptr) wk = load8(static_cast<const T*>(a.k_weight) + 8 * l);
+    const bool norms = a.q_weight != nullptr || a.k_weight != nullptr;
+    Runs<T> wq, wk;
+    if (a.q_weight != nullptr) wq = load_runs(static_cast<const T*>(a.q_weight) + at0, gap);
+    if (a.k_weight != nullptr) wk = load_runs(static_cast<const T*>(a.k_weight) + at0, gap);
     Place p{0, 0, -1, 0};
     if (active) p = place_of(a, t);
-    // this lane's cosines and sines: of elements 8 l + e (the sine with the sign it enters
-    // with), or of pairs 4 l + e when interleaved
-    constexpr int kTurns = kRot == 3 ? 4 : kRot != 0 ? 8 : 1;
-    float cs[kTurns], sn[kTurns];
+    // cosines and sines: of the run's 4 pairs (kRot 1, 3), or of the 8 elements, the sine with
+    // the sign it enters with (kRot 2)
+    float2 cs[kRot == 2 ? 4 : 2], sn[kRot == 2 ? 4 : 2];
     if constexpr (kRot != 0) {
         float2* tt = turn + tok * kTable;
-        if (active) {
-            const int fill = kRot == 3 ? a.D / 2 : a.half + 8;
-            for (int j = (warp & (wpt - 1)) * 32 + lane; j < fill; j += wpt * 32)
-                tt[j] = j < a.half ? turn_of(p.pos, a.freqs[j]) : make_float2(1.f, 0.f);
-        }
+        if (active)
+            for (int j = (warp & (wpt - 1)) * 32 + lane; j < a.half; j += wpt * 32) tt[j] = turn_of(p.pos, a.freqs[j]);
         __syncthreads();
         if constexpr (kRot == 2) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int i = 8 * l + e;
-                const float2 v = tt[i < a.half ? i : i < 2 * a.half ? i - a.half : a.half];
-                cs[e] = v.x;
-                sn[e] = i < a.half ? -v.y : v.y;
+                const float2 v = i < 2 * a.half ? tt[i < a.half ? i : i - a.half] : make_float2(1.f, 0.f);
+                (e & 1 ? cs[e >> 1].y : cs[e >> 1].x) = v.x;
+                (e & 1 ? sn[e >> 1].y : sn[e >> 1].x) = i < a.half ? -v.y : v.y;
             }
-        } else {
-            const int d = a.half >> 3;
-            const int j = kRot == 3 ? 4 * l : 8 * (l < d ? l : l < 2 * d ? l - d : d);
-            const float4* row = reinterpret_cast<const float4*>(tt + j);
+        } else if (4 * l < a.half) {  // entries behind half are unused
+            const float4* row = reinterpret_cast<const float4*>(tt + 4 * l);
 #pragma unroll
-            for (int e = 0; e < kTurns / 2; ++e) {
+            for (int e = 0; e < 2; ++e) {
                 const float4 v = row[e];
-                cs[2 * e] = v.x;
-                cs[2 * e + 1] = v.z;
-                sn[2 * e] = kRot == 1 && l < d ? -v.y : v.y;
-                sn[2 * e + 1] = kRot == 1 && l < d ? -v.w : v.w;
+                cs[e] = make_float2(v.x, v.z);
+                sn[e] = make_float2(v.y, v.w);
             }
         }
     }
     if (!active) return;
     if ((!p.ok || p.blk < 0) && first == 0 && lane == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
     const float inv_d = 1.0f / static_cast<float>(a.D);
-    T* qo = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.Hq * a.D + 8 * l;
+    T* qo = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.Hq * a.D + at0;
     const size_t slot0 = static_cast<size_t>(max(p.blk, 0)) * a.Hkv * a.BS + p.slot;  // row of KV head 0
-    for (int p0 = first; p0 < passes; p0 += kBatch * stride) {
-        if (p0 != first) load(p0);
+    for (int p0 = first; p0 < w.passes; p0 += kAhead * stride) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
+        for (int k = 0; k < kAhead; ++k) {
             const int pass = p0 + k * stride;
-            if (pass >= passes) break;
+            if (pass >= w.passes) break;
             const int r = pass * w.per + sub;
-            const bool mine = sub < w.per && r < rows;
-            const bool is_q = r < a.Hq, is_v = r >= a.Hq + a.Hkv;
-            float x[8];
-            to_floats(raw[k], x);
-            if (pass * w.per < a.Hq + a.Hkv) {  // some row of the pass is a query or a key
-                if (a.q_weight != nullptr || a.k_weight != nullptr) {
-                    float ss = 0.f;
+            const bool mine = in && r < rows;
+            const bool is_q = r < a.Hq, is_v = r >= kvrow;
+            const Runs<T> now = raw[k];
+            load(raw[k], pass + kAhead * stride);
+            float2 x[4];
+            to_floats(now, x);
+            if (pass * w.per < kvrow) {  // some row of the pass is a query or a key
+                if (norms) {
+                    float2 s2 = mul2(x[0], x[0]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                    ss = row_reduce(ss, w, l, base, [](float u, float v) { return u + v; });
+                    for (int e = 1; e < 4; ++e) s2 = fma2(x[e], x[e], s2);
+                    const float ss = row_reduce(s2.x + s2.y, w, l, base, [](float u, float v) { return u + v; });
                     const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
                     if (!is_v && (is_q ? a.q_weight : a.k_weight) != nullptr) {
-                        float g[8];
+                        float2 g[4];
                         to_floats(is_q ? wq : wk, g);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * g[e];
+                        for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], make_float2(inv, inv)), g[e]);
                     }
                 }
-                if constexpr (kRot == 3) {
-                    if (!is_v) {
+                if constexpr (kRot == 1) {
+                    if (!is_v && turns) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float u = x[2 * e], v = x[2 * e + 1];
-                            x[2 * e] = fmaf(u, cs[e], -v * sn[e]);
-                            x[2 * e + 1] = fmaf(v, cs[e], u * sn[e]);
+                        for (int e = 0; e < 2; ++e) {
+                            const float2 u = x[e], v = x[2 + e];
+                            x[e] = fma2(u, cs[e], mul2(v, make_float2(-sn[e].x, -sn[e].y)));
+                            x[2 + e] = fma2(v, cs[e], mul2(u, sn[e]));
                         }
                     }
-                } else if constexpr (kRot != 0) {
-                    float o[8];
-                    if constexpr (kRot == 1) {
-                        const int d = a.half >> 3, from = base + (l < d ? l + d : l < 2 * d ? l - d : l);
+                } else if constexpr (kRot == 3) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, x[e], from);
-                    } else {
-                        // rows through shared memory, one word of padding per 8
-                        float* buf = rowbuf[warp];
-                        const int at = sub * (a.D + a.D / 8);
-                        __syncwarp();
-                        if (sub < w.per) {
+                    for (int e = 0; e < 4; ++e) {
+                        const float c = e & 1 ? cs[e >> 1].y : cs[e >> 1].x, s = e & 1 ? sn[e >> 1].y : sn[e >> 1].x;
+                        const float2 v = x[e];
+                        if (!is_v && 4 * l + e < a.half) x[e] = make_float2(fmaf(v.x, c, -v.y * s), fmaf(v.y, c, v.x * s));
+                    }
+                } else if constexpr (kRot == 2) {
+                    // rows through shared memory, one word of padding per 8
+                    float* buf = rowbuf[warp];
+                    const int at = sub * (a.D + a.D / 8);
+                    __syncwarp();
+                    if (sub < w.per) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) buf[at + 9 * l + e] = x[e];
-                        }
-                        __syncwarp();
+                        for (int e = 0; e < 8; ++e) buf[at + 9 * l + e] = e & 1 ? x[e >> 1].y : x[e >> 1].x;
+                    }
+                    __syncwarp();
+                    if (!is_v && sub < w.per) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const int i = 8 * l + e, q = i < a.half ? i + a.half : i < 2 * a.half ? i - a.half : i;
-                            o[e] = sub < w.per ? buf[at + q + (q >> 3)] : 0.f;
+                            const int i = 8 * l + e, q = i < a.half ? i + a.half : i - a.half;
+                            if (i < 2 * a.half) {
+                                const float o = buf[at + q + (q >> 3)];
+                                float& y = e & 1 ? x[e >> 1].y : x[e >> 1].x;
+                                y = fmaf(y, e & 1 ? cs[e >> 1].y : cs[e >> 1].x, o * (e & 1 ? sn[e >> 1].y : sn[e >> 1].x));
+                            }
                         }
-                    }
-                    if (!is_v) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], cs[e], o[e] * sn[e]);
                     }
                 }
             }
             if (is_q && mine) {
-                if (!p.ok) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = 0.f;
-                }
-                store8(qo + r * a.D, x);
+                if (!p.ok) x[0] = x[1] = x[2] = x[3] = make_float2(0.f, 0.f);
+                store_runs(qo + r * a.D, gap, x);
             }
             const bool put = mine && !is_q && p.blk >= 0;
-            const size_t row = slot0 + (is_v ? r - a.Hq - a.Hkv : r - a.Hq) * a.BS;
+            const size_t row = slot0 + (r - (is_v ? kvrow : a.Hq)) * a.BS;
             if constexpr (Fmt::kQuant) {
                 if ((pass + 1) * w.per <= a.Hq) continue;  // queries only
                 // the largest |x| as an integer: infinities and NaN are above every finite number
                 uint32_t top = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+                for (int e = 0; e < 4; ++e)
+                    top = max(top, max(__float_as_uint(x[e].x) & 0x7fffffffu, __float_as_uint(x[e].y) & 0x7fffffffu));
                 top = row_reduce(top, w, l, base, [](uint32_t u, uint32_t v) { return max(u, v); });
                 const bool finite = top < 0x7f800000u;
                 const float scale = row_scale(__uint_as_float(top), Fmt::kInvQ);
                 const float inv = __frcp_rn(scale);
                 if (put) {
-                    uint2 v = make_uint2(0u, 0u);
+                    uint32_t v0 = 0, v1 = 0;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(x[e], inv);
-                    if (finite) v = make_uint2(Fmt::encode4(x), Fmt::encode4(x + 4));
-                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + row * a.D + 8 * l) = v;
+                    for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], make_float2(inv, inv));
+                    if (finite) {
+                        v0 = Fmt::encode4(&x[0].x);
+                        v1 = Fmt::encode4(&x[2].x);
+                    }
+                    uint8_t* dst = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + row * a.D + at0;
+                    *reinterpret_cast<uint32_t*>(dst) = v0;
+                    *reinterpret_cast<uint32_t*>(dst + gap) = v1;
                     if (l == 0) {
                         (is_v ? a.v_scale : a.k_scale)[row] = finite ? scale : __int_as_float(0x7fffffff);
                         if (!finite) report(a.status, PKV_ERR_NONFINITE);
                     }
                 }
             } else if (put) {
-                T* dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) + row * a.D + 8 * l;
+                T* dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) + row * a.D + at0;
                 if (is_v) {  // the bits as they are
-#pragma unroll
-                    for (int e = 0; e < static_cast<int>(sizeof(T)) / 2; ++e) reinterpret_cast<uint4*>(dst)[e] = raw[k].v[e];
+                    using V = std::remove_const_t<std::remove_reference_t<decltype(now.v[0])>>;
+                    *reinterpret_cast<V*>(dst) = now.v[0];
+                    *reinterpret_cast<V*>(dst + gap) = now.v[1];
                 } else {
-                    store8(dst, x);
+                    store_runs(dst, gap, x);
                 }
             }
         }
@@ -482,7 +507,7 @@ static cudaError_t launch_typed(const WriteArgs& a, cudaStream_t stream) {
             while (split * kWriteWarps < passes && static_cast<long long>(a.T) * split < 2LL * sms) ++split;
         const int tpc = kWriteWarps >> w.wpt_log2;
         cfg.gridDim = dim3(static_cast<unsigned>((a.T + tpc - 1) / tpc), static_cast<unsigned>(split), 1);
-        const int rot = a.half == 0 ? 0 : a.interleaved ? 3 : a.half % 8 == 0 ? 1 : 2;
+        const int rot = a.half == 0 ? 0 : a.interleaved ? 3 : a.half % 4 == 0 ? 1 : 2;
         auto kern = rot == 0   ? kv_write_kernel<T, Fmt, 0>
                     : rot == 1 ? kv_write_kernel<T, Fmt, 1>
                     : rot == 2 ? kv_write_kernel<T, Fmt, 2>
