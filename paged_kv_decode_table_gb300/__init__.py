@@ -717,20 +717,15 @@ def paged_prefill_attention(q, k_cache, v_cache, block_tables, seq_lens, q_start
 
 
 # ---------------------------------------------------------------- 8-bit cache
-# These calls sit in decode loops whose kernels take a few microseconds, so a
-# good argument is recognised with a few attribute reads, and _check_cuda names
-# what is wrong with a bad one.
-def _expect(name, t, dtype, shape, dev):
-    if (type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or t.device != dev
-            or not t.is_contiguous()):
-        _check_cuda(name, t, dtype, shape, dev)
-
-
-def _expect_tables(block_tables, seq_lens, B, dev):
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
-        raise ValueError("block_tables must be [B, max_blocks_per_seq]")
-    _expect("block_tables", block_tables, torch.int32, block_tables.shape, dev)
-    _expect("seq_lens", seq_lens, torch.int32, (B,), dev)
+# These calls sit in decode loops whose kernels take a few microseconds, and an
+# attribute of a tensor costs a tenth of one: each call tests its arguments in one
+# expression, and only where that fails do the _check functions run, which name
+# what is wrong.
+_f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_sms: dict = {}     # SM count by device index
+_q8_need: dict = {}  # workspace bytes by (device index, Hq, Hkv, D)
 
 
 def _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev):
@@ -738,55 +733,78 @@ def _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev):
         raise TypeError(f"k_cache must be torch.float8_e4m3fn or torch.int8, got {k_cache.dtype}")
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [num_blocks, Hkv, block_size, D]")
-    if dev.type != "cuda":
-        raise ValueError("k_cache must be a CUDA tensor")
-    shape = k_cache.shape
-    _expect("k_cache", k_cache, k_cache.dtype, shape, dev)
-    _expect("v_cache", v_cache, k_cache.dtype, shape, dev)
-    _expect("k_scale", k_scale, torch.float32, shape[:3], dev)
-    _expect("v_scale", v_scale, torch.float32, shape[:3], dev)
+    _check_cuda("k_cache", k_cache, k_cache.dtype, device=dev)
+    _check_cuda("v_cache", v_cache, k_cache.dtype, k_cache.shape, dev)
+    _check_cuda("k_scale", k_scale, _f32, k_cache.shape[:3], dev)
+    _check_cuda("v_scale", v_scale, _f32, k_cache.shape[:3], dev)
 
 
-def _status_ptr(status, dev):
-    if status is None:
-        return None
-    _expect("status", status, torch.int32, (1,), dev)
-    return status.data_ptr()
+def _check_tables(block_tables, seq_lens, B, status, dev):
+    _check_cuda("block_tables", block_tables, _i32, device=dev)
+    _check_cuda("seq_lens", seq_lens, _i32, (B,), dev)
+    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+        raise ValueError("block_tables must be [B, max_blocks_per_seq]")
+    if status is not None:
+        _check_cuda("status", status, _i32, (1,), dev)
 
 
-def _code_of(t):
-    code = _CODES.get(t.dtype)
-    return _dtype_code(t) if code is None else code
+def _unclear():
+    raise ValueError("an argument has an unsupported kind")  # a tensor the checks above let pass
 
 
-def _launch(name, dev, *args):
-    """Call the library's `name` on the current stream of `dev`, with `dev` current."""
-    fn = getattr(_lib or load_library(), name)
-    if torch.cuda.current_device() == dev.index:
-        code = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+def _cache_ok(k_cache, v_cache, k_scale, v_scale, shape, dev):
+    dt, rows = k_cache.dtype, shape[:3]
+    return (len(shape) == 4 and dt in _CODES_Q8 and v_cache.dtype is dt and k_scale.dtype is _f32
+            and v_scale.dtype is _f32 and v_cache.shape == shape and k_scale.shape == rows and v_scale.shape == rows
+            and dev >= 0 and v_cache.get_device() == dev and k_scale.get_device() == dev
+            and v_scale.get_device() == dev and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_scale.is_contiguous() and v_scale.is_contiguous())
+
+
+def _tables_ok(block_tables, seq_lens, B, status, dev):
+    return (block_tables.dtype is _i32 and seq_lens.dtype is _i32 and block_tables.get_device() == dev
+            and seq_lens.get_device() == dev and block_tables.dim() == 2 and block_tables.shape[0] == B
+            and seq_lens.dim() == 1 and block_tables.is_contiguous() and seq_lens.is_contiguous()
+            and (status is None or (status.dtype is _i32 and status.shape == (1,) and status.get_device() == dev)))
+
+
+def _launch(name, dev, fn, *args):
+    """Call the library on the current stream of device index `dev`, with that device current."""
+    if _current_device() == dev:
+        code = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+            code = fn(*args, _raw_stream(dev))
     if code != 0:
         raise PkvError(name, code)
 
 
 def _append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, q_start, status):
-    dev = k_cache.device
-    _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
-    NB, Hkv, BS, D = k_cache.shape
-    B = seq_lens.shape[0]
-    T = B if q_start is None else k_new.shape[0]
-    code = _code_of(k_new)
-    _expect("k_new", k_new, k_new.dtype, (T, Hkv, D), dev)
-    _expect("v_new", v_new, k_new.dtype, (T, Hkv, D), dev)
-    _expect_tables(block_tables, seq_lens, B, dev)
-    if q_start is not None:
-        _expect("q_start", q_start, torch.int32, (B + 1,), dev)
-    _launch("pkv_kv_append_q8", dev, k_new.data_ptr(), v_new.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-            seq_lens.data_ptr(), None if q_start is None else q_start.data_ptr(), B, T, Hkv, D, BS, NB, code,
-            _CODES_Q8[k_cache.dtype], _status_ptr(status, dev))
+    shape, dev, dt = k_cache.shape, k_cache.get_device(), k_new.dtype
+    code = _CODES.get(dt)
+    B, T = seq_lens.shape[0], k_new.shape[0]
+    if not (_cache_ok(k_cache, v_cache, k_scale, v_scale, shape, dev) and code is not None
+            and _tables_ok(block_tables, seq_lens, B, status, dev) and k_new.shape == (T, shape[1], shape[3])
+            and v_new.shape == k_new.shape and v_new.dtype is dt and k_new.get_device() == dev
+            and v_new.get_device() == dev and k_new.is_contiguous() and v_new.is_contiguous()
+            and (T == B if q_start is None else
+                 q_start.dtype is _i32 and q_start.shape == (B + 1,) and q_start.get_device() == dev
+                 and q_start.is_contiguous())):
+        d = k_cache.device
+        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, d)
+        _dtype_code(k_new)
+        rows = (B if q_start is None else T, shape[1], shape[3])
+        _check_cuda("k_new", k_new, k_new.dtype, rows, d)
+        _check_cuda("v_new", v_new, k_new.dtype, rows, d)
+        _check_tables(block_tables, seq_lens, B, status, d)
+        if q_start is not None:
+            _check_cuda("q_start", q_start, _i32, (B + 1,), d)
+        _unclear()
+    _launch("pkv_kv_append_q8", dev, (_lib or load_library()).pkv_kv_append_q8, k_new.data_ptr(), v_new.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], seq_lens.data_ptr(), None if q_start is None else q_start.data_ptr(), B, T,
+            shape[1], shape[3], shape[2], shape[0], code, _CODES_Q8[k_cache.dtype],
+            None if status is None else status.data_ptr())
 
 
 def kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, status=None):
@@ -807,21 +825,35 @@ def kv_read_blocks_q8(k_cache, v_cache, k_scale, v_scale, blocks, k_out=None, v_
                       status=None):
     """Blocks `blocks` (int32 [n]) of an 8-bit cache as an unquantised pool:
     returns (k, v) [n, Hkv, block_size, D] in `dtype` (that of k_out if given)."""
-    dev = k_cache.device
-    _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
-    NB, Hkv, BS, D = k_cache.shape
+    shape, dev = k_cache.shape, k_cache.get_device()
+    if not (_cache_ok(k_cache, v_cache, k_scale, v_scale, shape, dev) and blocks.dtype is _i32 and blocks.dim() == 1
+            and blocks.get_device() == dev and blocks.is_contiguous()
+            and (status is None or (status.dtype is _i32 and status.shape == (1,) and status.get_device() == dev))):
+        d = k_cache.device
+        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, d)
+        _check_cuda("blocks", blocks, _i32, (blocks.shape[0],), d)
+        if status is not None:
+            _check_cuda("status", status, _i32, (1,), d)
+        _unclear()
     n = blocks.shape[0]
-    _expect("blocks", blocks, torch.int32, (n,), dev)
-    if k_out is None:
-        k_out = torch.empty((n, Hkv, BS, D), dtype=dtype if v_out is None else v_out.dtype, device=dev)
-    if v_out is None:
-        v_out = torch.empty_like(k_out)
-    code = _code_of(k_out)
-    _expect("k_out", k_out, k_out.dtype, (n, Hkv, BS, D), dev)
-    _expect("v_out", v_out, k_out.dtype, (n, Hkv, BS, D), dev)
-    _launch("pkv_kv_read_blocks_q8", dev, k_out.data_ptr(), v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            k_scale.data_ptr(), v_scale.data_ptr(), blocks.data_ptr(), n, Hkv, D, BS, NB, code,
-            _CODES_Q8[k_cache.dtype], _status_ptr(status, dev))
+    want = (n, shape[1], shape[2], shape[3])
+    if k_out is None and v_out is None:
+        # one allocation for both pools
+        k_out, v_out = torch.empty((2, *want), dtype=dtype, device=k_cache.device).unbind(0)
+    else:
+        if k_out is None:
+            k_out = torch.empty_like(v_out)
+        elif v_out is None:
+            v_out = torch.empty_like(k_out)
+        _check_cuda("k_out", k_out, k_out.dtype, want, k_cache.device)
+        _check_cuda("v_out", v_out, k_out.dtype, want, k_cache.device)
+    code = _CODES.get(k_out.dtype)
+    if code is None:
+        code = _dtype_code(k_out)
+    _launch("pkv_kv_read_blocks_q8", dev, (_lib or load_library()).pkv_kv_read_blocks_q8, k_out.data_ptr(),
+            v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            blocks.data_ptr(), n, shape[1], shape[3], shape[2], shape[0], code, _CODES_Q8[k_cache.dtype],
+            None if status is None else status.data_ptr())
     return k_out, v_out
 
 
@@ -835,30 +867,38 @@ def paged_decode_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_table
     bfloat16; returns out [B, Hq, D].  Without `workspace` one is allocated for
     the call, so calls on several streams, or captured in several graphs, do not
     share it."""
-    dev = k_cache.device
-    _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
-    NB, Hkv, BS, D = k_cache.shape
-    B, Hq = q.shape[0], q.shape[1]
-    code = _code_of(q)
-    _expect("q", q, q.dtype, (B, Hq, D), dev)
-    _expect_tables(block_tables, seq_lens, B, dev)
+    shape, dev, dt, qs = k_cache.shape, k_cache.get_device(), q.dtype, q.shape
+    code = _CODES.get(dt)
+    if not (_cache_ok(k_cache, v_cache, k_scale, v_scale, shape, dev) and code is not None and len(qs) == 3
+            and qs[2] == shape[3] and q.get_device() == dev and q.is_contiguous()
+            and _tables_ok(block_tables, seq_lens, qs[0], status, dev) and seq_lens.shape[0] == qs[0]):
+        d = k_cache.device
+        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, d)
+        _dtype_code(q)
+        _check_cuda("q", q, dt, (q.shape[0], q.shape[1], shape[3]), d)
+        _check_tables(block_tables, seq_lens, q.shape[0], status, d)
+        _unclear()
+    B, Hq, D = qs
+    lib = _lib or load_library()
     if out is None:
         out = torch.empty_like(q)
     else:
-        _expect("out", out, q.dtype, q.shape, dev)
+        _check_cuda("out", out, dt, qs, q.device)
     if workspace is None:
-        lib = _lib or load_library()
-        sms = torch.cuda.get_device_properties(dev).multi_processor_count
-        need = lib.pkv_decode_q8_workspace_bytes(B, Hq, Hkv, D, sms)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        ws_bytes = need
+        key = (dev, Hq, shape[1], D)
+        ws_bytes = _q8_need.get(key)
+        if ws_bytes is None:
+            if dev not in _sms:
+                _sms[dev] = torch.cuda.get_device_properties(dev).multi_processor_count
+            ws_bytes = _q8_need[key] = lib.pkv_decode_q8_workspace_bytes(B, Hq, shape[1], D, _sms[dev])
+        workspace = torch.empty(ws_bytes or 16, dtype=_u8, device=k_cache.device)
     else:
-        _check_cuda("workspace", workspace, device=dev)
+        _check_cuda("workspace", workspace, device=q.device)
         ws_bytes = workspace.numel() * workspace.element_size()
-    _launch("pkv_paged_decode_attention_q8", dev, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
-            block_tables.shape[1], seq_lens.data_ptr(), B, Hq, Hkv, D, BS, NB, scale, code,
-            _CODES_Q8[k_cache.dtype], workspace.data_ptr(), ws_bytes, _status_ptr(status, dev))
+    _launch("pkv_paged_decode_attention_q8", dev, lib.pkv_paged_decode_attention_q8, out.data_ptr(), q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
+            block_tables.shape[1], seq_lens.data_ptr(), B, Hq, shape[1], D, shape[2], shape[0], scale, code,
+            _CODES_Q8[k_cache.dtype], workspace.data_ptr(), ws_bytes, None if status is None else status.data_ptr())
     return out
 
 
@@ -877,22 +917,24 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, inv_freq=None, device="cuda"
     return torch.tensor([t - (1 << 64) if t >> 63 else t for t in turns], dtype=torch.int64, device=device)
 
 
-def _expect_rows(name, t, dtype, shape, dev):
-    """A [T, H, D] view whose tokens may lie any distance apart; returns that distance."""
-    if (type(t) is not torch.Tensor or t.dtype is not dtype or t.shape != shape or t.device != dev):
-        if not isinstance(t, torch.Tensor) or t.dim() != 3 or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-            raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    T, H, D = shape
+def _check_rows(name, t, dtype, shape, dev):
+    """A [T, H, D] view whose tokens may lie any distance apart."""
+    if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if _token_stride(t, shape[1], shape[2]) < 0:
+        raise ValueError(f"{name}: the heads of a token must be dense ([H, D] rows) and tokens must not overlap")
+
+
+def _token_stride(t, H, D):
+    """Elements between the tokens of a [T, H, D] view with dense heads; -1 if it is none."""
     st = t.stride()
     if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
-        raise ValueError(f"{name}: the heads of a token must be dense ([H, D] rows)")
-    if T <= 1:
+        return -1
+    if t.shape[0] <= 1:
         return H * D
-    if st[0] < H * D:
-        raise ValueError(f"{name}: tokens overlap")
-    return st[0]
+    return st[0] if st[0] >= H * D else -1
 
 
 def qk_norm_rope_append(q, k_new, v_new, q_weight, k_weight, eps, freqs, k_cache, v_cache, block_tables, seq_lens,
@@ -906,44 +948,68 @@ def qk_norm_rope_append(q, k_new, v_new, q_weight, k_weight, eps, freqs, k_cache
     any distance apart, so views of one projection output will do).  T is B (one
     token per sequence) or, with q_start, the packed chunks of kv_append_chunk.
     The cache is of q's type, or an 8-bit one with its k_scale and v_scale."""
-    dev = k_cache.device
-    NB, Hkv, BS, D = k_cache.shape
-    code = _code_of(q)
-    if k_scale is None and v_scale is None:
-        if dev.type != "cuda":
-            raise ValueError("k_cache must be a CUDA tensor")
-        cache_code = code
-        _expect("k_cache", k_cache, q.dtype, k_cache.shape, dev)
-        _expect("v_cache", v_cache, q.dtype, k_cache.shape, dev)
-    else:
-        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
-        cache_code = _CODES_Q8[k_cache.dtype]
-    B, T, Hq = seq_lens.shape[0], q.shape[0], q.shape[1]
-    if q_start is not None:
-        _expect("q_start", q_start, torch.int32, (B + 1,), dev)
-    elif T != B:
-        raise ValueError(f"q has {T} tokens for {B} sequences: pass q_start")
-    qs = _expect_rows("q", q, q.dtype, (T, Hq, D), dev)
-    ks = _expect_rows("k_new", k_new, q.dtype, (T, Hkv, D), dev)
-    vs = _expect_rows("v_new", v_new, q.dtype, (T, Hkv, D), dev)
-    if q_weight is not None:
-        _expect("q_weight", q_weight, q.dtype, (D,), dev)
-    if k_weight is not None:
-        _expect("k_weight", k_weight, q.dtype, (D,), dev)
-    rot = 0
-    if freqs is not None:
-        rot = 2 * freqs.shape[0]
-        _expect("freqs", freqs, torch.int64, (rot // 2,), dev)
-    _expect_tables(block_tables, seq_lens, B, dev)
+    shape, dev, dt, qs = k_cache.shape, k_cache.get_device(), q.dtype, q.shape
+    code = _CODES.get(dt)
+    q8 = k_scale is not None or v_scale is not None
+    ok = len(shape) == 4 and len(qs) == 3 and k_new.dim() == 3 and v_new.dim() == 3
+    if ok:
+        NB, Hkv, BS, D = shape
+        T, Hq = qs[0], qs[1]
+        B, kvs = seq_lens.shape[0], (T, Hkv, D)
+        ok = (code is not None and qs[2] == D and k_new.shape == kvs and v_new.shape == kvs and k_new.dtype is dt
+              and v_new.dtype is dt and q.get_device() == dev and k_new.get_device() == dev
+              and v_new.get_device() == dev and _tables_ok(block_tables, seq_lens, B, status, dev)
+              and (_cache_ok(k_cache, v_cache, k_scale, v_scale, shape, dev)
+                   if k_scale is not None and v_scale is not None else
+                   not q8 and dev >= 0 and k_cache.dtype is dt and v_cache.dtype is dt and v_cache.shape == shape
+                   and v_cache.get_device() == dev and k_cache.is_contiguous() and v_cache.is_contiguous())
+              and (T == B if q_start is None else
+                   q_start.dtype is _i32 and q_start.shape == (B + 1,) and q_start.get_device() == dev
+                   and q_start.is_contiguous())
+              and (q_weight is None or (q_weight.dtype is dt and q_weight.shape == (D,) and q_weight.get_device() == dev
+                                        and q_weight.is_contiguous()))
+              and (k_weight is None or (k_weight.dtype is dt and k_weight.shape == (D,) and k_weight.get_device() == dev
+                                        and k_weight.is_contiguous()))
+              and (freqs is None or (freqs.dtype is torch.int64 and freqs.dim() == 1 and freqs.get_device() == dev
+                                     and freqs.is_contiguous())))
+    if ok:
+        qst, kst, vst = _token_stride(q, Hq, D), _token_stride(k_new, Hkv, D), _token_stride(v_new, Hkv, D)
+        ok = qst >= 0 and kst >= 0 and vst >= 0
+    if not ok:
+        d = k_cache.device
+        _dtype_code(q)
+        if k_cache.dim() != 4 or q.dim() != 3:
+            raise ValueError("k_cache must be [num_blocks, Hkv, block_size, D], q [T, Hq, D]")
+        if q8:
+            _check_cache_q8(k_cache, v_cache, k_scale, v_scale, d)
+        else:
+            _check_cuda("k_cache", k_cache, dt)
+            _check_cuda("v_cache", v_cache, dt, shape, d)
+        B, T = seq_lens.shape[0], qs[0]
+        if q_start is not None:
+            _check_cuda("q_start", q_start, _i32, (B + 1,), d)
+        elif T != B:
+            raise ValueError(f"q has {T} tokens for {B} sequences: pass q_start")
+        _check_rows("q", q, dt, (T, qs[1], shape[3]), d)
+        _check_rows("k_new", k_new, dt, (T, shape[1], shape[3]), d)
+        _check_rows("v_new", v_new, dt, (T, shape[1], shape[3]), d)
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                _check_cuda(name, w, dt, (shape[3],), d)
+        if freqs is not None:
+            _check_cuda("freqs", freqs, torch.int64, (freqs.shape[0],), d)
+        _check_tables(block_tables, seq_lens, B, status, d)
+        _unclear()
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        q_out = torch.empty(qs, dtype=dt, device=k_cache.device)
     else:
-        _expect("q_out", q_out, q.dtype, (T, Hq, D), dev)
-    _launch("pkv_qk_norm_rope_append", dev, q_out.data_ptr(), q.data_ptr(), qs, k_new.data_ptr(), ks,
-            v_new.data_ptr(), vs, None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(), eps, None if freqs is None else freqs.data_ptr(), rot,
-            interleaved, k_cache.data_ptr(), v_cache.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
-            None if v_scale is None else v_scale.data_ptr(), block_tables.data_ptr(), block_tables.shape[1],
-            seq_lens.data_ptr(), None if q_start is None else q_start.data_ptr(), B, T, Hq, Hkv, D, BS, NB, code,
-            cache_code, _status_ptr(status, dev))
+        _check_cuda("q_out", q_out, dt, qs, k_cache.device)
+    _launch("pkv_qk_norm_rope_append", dev, (_lib or load_library()).pkv_qk_norm_rope_append, q_out.data_ptr(),
+            q.data_ptr(), qst, k_new.data_ptr(), kst, v_new.data_ptr(), vst,
+            None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
+            None if freqs is None else freqs.data_ptr(), 0 if freqs is None else 2 * freqs.shape[0], interleaved,
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if q8 else None,
+            v_scale.data_ptr() if q8 else None, block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+            None if q_start is None else q_start.data_ptr(), B, T, Hq, Hkv, D, BS, NB, code,
+            _CODES_Q8[k_cache.dtype] if q8 else code, None if status is None else status.data_ptr())
     return q_out

@@ -43,6 +43,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "quant8.cuh"
@@ -1033,8 +1034,16 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     float* part_ml = reinterpret_cast<float*>(ws);
     float* part_o = reinterpret_cast<float*>(ws + wl.o);
     auto kern = decode_q8_kernel<T, Fmt, DP, kN, kSplit>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // the kernel's limit is raised to the device's once per device
+    static std::atomic<uint64_t> raised{0};
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
+    if (dev >= 64 || !(raised.load() >> dev & 1)) {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(budget));
+        if (err != cudaSuccess) return err;
+        if (dev < 64) raised.fetch_or(1ull << dev);
+    }
     cudaLaunchConfig_t cfg = {};
     // Short sequences (by the table's width) and few of them: one CTA each, so that no
     // join is launched.

@@ -21,7 +21,8 @@
 // read once per token into registers, and for pairs (j, j + half) the second run
 // holds the partners of the first (half a multiple of 4; else they come through
 // shared memory).  The first rows are loaded before the token's place and angles
-// are known, which hides that chain of loads, and later ones kAhead passes early.  The other kernel (any D and alignment) gives a warp one row, one element
+// are known, which hides that chain of loads, and later ones kAhead passes early.
+// Queries, keys and values have a loop each.  The other kernel (any D and alignment) gives a warp one row, one element
 // per lane and step.
 #include <type_traits>
 
@@ -68,14 +69,21 @@ struct Place {
     int ok, pos, blk, slot;
 };
 
+// Called by a whole warp with one t.
 __device__ __forceinline__ Place place_of(const WriteArgs& a, int t) {
     Place p{0, 0, -1, 0};
     int b = t, n = 1, i = 0;
     if (a.q_start != nullptr) {
-        int lo = 0, hi = a.B - 1;  // the last b with q_start[b] <= t
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.q_start[mid] <= t) lo = mid; else hi = mid - 1;
+        // the last b with q_start[b] <= t: 32 probes per round, so 1024 sequences take two
+        // dependent loads
+        int lo = 0, count = a.B;  // in [lo, lo + count)
+        const int lane = threadIdx.x & 31;
+        while (count > 1) {
+            const int step = (count + 31) / 32, at = lane * step;
+            const unsigned below = __ballot_sync(0xffffffffu, at < count && (at == 0 || a.q_start[lo + at] <= t));
+            const int hit = 31 - __clz(below);  // lane 0 always is
+            lo += hit * step;
+            count = min(step, count - hit * step);
         }
         b = lo;
         n = a.q_start[b + 1] - a.q_start[b];
@@ -262,7 +270,8 @@ __device__ __forceinline__ void store_runs(float* p, int gap, const float2 (&x)[
 // Layout of the vector kernel, from the host.
 struct WritePlan {
     int lanes, per;  // lanes a row, rows a pass
-    int passes;      // passes over a token's rows
+    int qpasses, kvpasses;  // passes over a token's query rows, and over its key (or value) rows
+    float inv_d;
     int magic;       // lane / lanes = lane * magic >> 16
     int pow2;        // lanes is a power of two
     int wpt_log2;    // warps per token
@@ -288,12 +297,14 @@ __device__ __forceinline__ V row_reduce(V x, const WritePlan& w, int l, int base
 // kRot: 0 no rotation, 1 pairs (j, j + half) with half a multiple of 4, 2 such pairs
 // with any half, 3 pairs (2j, 2j + 1).
 template <typename T, typename Fmt, int kRot>
-__global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 ? 2 : 3) kv_write_kernel(const WriteArgs a, const WritePlan w) {
+__global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 ? 2 : 3)
+    kv_write_kernel(const __grid_constant__ WriteArgs a, const __grid_constant__ WritePlan w) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kAhead = 2;  // passes in flight per warp
+    constexpr int kAhead = 2;  // passes in flight per warp and kind
     constexpr int kPad = kWriteMaxD + kWriteMaxD / 8;
     constexpr int kTable = kWriteMaxD / 2;
+    enum { kQ, kK, kV };
     __shared__ float rowbuf[kRot == 2 ? kWriteWarps : 1][kRot == 2 ? 2 * kPad : 1];
     __shared__ __align__(16) float2 turn[kRot == 0 ? 1 : kWriteWarps * kTable];  // [token of the CTA][pair]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -304,24 +315,30 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 ? 2 : 3) kv_write_
     // holds the partners of the first, so that no element has to travel
     const bool turns = kRot == 1 && 4 * l < a.half;
     const int at0 = turns ? 4 * l : 8 * l, gap = turns ? a.half : 4;
-    const int rows = a.Hq + 2 * a.Hkv, kvrow = a.Hq + a.Hkv;
-    const int stride = wpt * gridDim.y;
     const bool in = t < a.T && sub < w.per;
-    const int first = blockIdx.y * wpt + (warp & (wpt - 1));
-    // row r of the token (queries, keys, values) is at its kind's pointer plus r * D
-    const T* qp = static_cast<const T*>(a.q) + t * a.q_stride + at0;
-    const T* kp = static_cast<const T*>(a.k) + t * a.k_stride + at0 - a.Hq * a.D;
-    const T* vp = static_cast<const T*>(a.v) + t * a.v_stride + at0 - kvrow * a.D;
-    Runs<T> raw[kAhead];
-    auto load = [&](Runs<T>& to, int pass) {
-        const int r = pass * w.per + sub;
-        if (in && r < rows) to = load_runs((r < a.Hq ? qp : r < kvrow ? kp : vp) + r * a.D, gap);
+    // passes first, first + stride, .. of the queries', then the keys', then the values' passes
+    const int stride = wpt * gridDim.y, first = blockIdx.y * wpt + (warp & (wpt - 1));
+    const int qpass = w.qpasses, kvpass = w.kvpasses;
+    auto head_of = [&](int pass) { return pass * w.per + sub; };
+    auto begin_of = [&](int done) {  // this warp's first pass of a kind that follows `done` passes
+        const int x = (first - done) % stride;
+        return x < 0 ? x + stride : x;
     };
+    const int k0 = begin_of(qpass), v0 = begin_of(qpass + kvpass);
+    const T* qp = static_cast<const T*>(a.q) + t * a.q_stride + at0;
+    const T* kp = static_cast<const T*>(a.k) + t * a.k_stride + at0;
+    const T* vp = static_cast<const T*>(a.v) + t * a.v_stride + at0;
+    auto load = [&](Runs<T>& to, const T* src, int pass, int heads) {
+        const int h = head_of(pass);
+        if (in && h < heads) to = load_runs(src + h * a.D, gap);
+    };
+    Runs<T> raw[kAhead], rawk, rawv;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) load(raw[k], first + k * stride);
+    for (int k = 0; k < kAhead; ++k) load(raw[k], qp, first + k * stride, a.Hq);
+    load(rawk, kp, k0, a.Hkv);
+    load(rawv, vp, v0, a.Hkv);
     const bool active = t < a.T && (a.q_start == nullptr || t < a.q_start[a.B]);  // rows behind the last sequence stay
     // norm weights and frequencies do not wait for the token's place either
-    const bool norms = a.q_weight != nullptr || a.k_weight != nullptr;
     Runs<T> wq, wk;
     if (a.q_weight != nullptr) wq = load_runs(static_cast<const T*>(a.q_weight) + at0, gap);
     if (a.k_weight != nullptr) wk = load_runs(static_cast<const T*>(a.k_weight) + at0, gap);
@@ -355,118 +372,137 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 ? 2 : 3) kv_write_
     }
     if (!active) return;
     if ((!p.ok || p.blk < 0) && first == 0 && lane == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
-    const float inv_d = 1.0f / static_cast<float>(a.D);
-    T* qo = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.Hq * a.D + at0;
-    const size_t slot0 = static_cast<size_t>(max(p.blk, 0)) * a.Hkv * a.BS + p.slot;  // row of KV head 0
-    for (int p0 = first; p0 < w.passes; p0 += kAhead * stride) {
+
+    auto norm = [&](float2 (&x)[4], const float2 (&g)[4]) {
+        float2 s2 = mul2(x[0], x[0]);
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int pass = p0 + k * stride;
-            if (pass >= w.passes) break;
-            const int r = pass * w.per + sub;
-            const bool mine = in && r < rows;
-            const bool is_q = r < a.Hq, is_v = r >= kvrow;
-            const Runs<T> now = raw[k];
-            load(raw[k], pass + kAhead * stride);
-            float2 x[4];
-            to_floats(now, x);
-            if (pass * w.per < kvrow) {  // some row of the pass is a query or a key
-                if (norms) {
-                    float2 s2 = mul2(x[0], x[0]);
+        for (int e = 1; e < 4; ++e) s2 = fma2(x[e], x[e], s2);
+        const float ss = row_reduce(s2.x + s2.y, w, l, base, [](float u, float v) { return u + v; });
+        const float inv = rsqrtf(fmaf(ss, w.inv_d, a.eps));
 #pragma unroll
-                    for (int e = 1; e < 4; ++e) s2 = fma2(x[e], x[e], s2);
-                    const float ss = row_reduce(s2.x + s2.y, w, l, base, [](float u, float v) { return u + v; });
-                    const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
-                    if (!is_v && (is_q ? a.q_weight : a.k_weight) != nullptr) {
-                        float2 g[4];
-                        to_floats(is_q ? wq : wk, g);
+        for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], make_float2(inv, inv)), g[e]);
+    };
+    auto rotate = [&](float2 (&x)[4]) {
+        if constexpr (kRot == 1) {
+            if (turns) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], make_float2(inv, inv)), g[e]);
-                    }
-                }
-                if constexpr (kRot == 1) {
-                    if (!is_v && turns) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float2 u = x[e], v = x[2 + e];
-                            x[e] = fma2(u, cs[e], mul2(v, make_float2(-sn[e].x, -sn[e].y)));
-                            x[2 + e] = fma2(v, cs[e], mul2(u, sn[e]));
-                        }
-                    }
-                } else if constexpr (kRot == 3) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float c = e & 1 ? cs[e >> 1].y : cs[e >> 1].x, s = e & 1 ? sn[e >> 1].y : sn[e >> 1].x;
-                        const float2 v = x[e];
-                        if (!is_v && 4 * l + e < a.half) x[e] = make_float2(fmaf(v.x, c, -v.y * s), fmaf(v.y, c, v.x * s));
-                    }
-                } else if constexpr (kRot == 2) {
-                    // rows through shared memory, one word of padding per 8
-                    float* buf = rowbuf[warp];
-                    const int at = sub * (a.D + a.D / 8);
-                    __syncwarp();
-                    if (sub < w.per) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) buf[at + 9 * l + e] = e & 1 ? x[e >> 1].y : x[e >> 1].x;
-                    }
-                    __syncwarp();
-                    if (!is_v && sub < w.per) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const int i = 8 * l + e, q = i < a.half ? i + a.half : i - a.half;
-                            if (i < 2 * a.half) {
-                                const float o = buf[at + q + (q >> 3)];
-                                float& y = e & 1 ? x[e >> 1].y : x[e >> 1].x;
-                                y = fmaf(y, e & 1 ? cs[e >> 1].y : cs[e >> 1].x, o * (e & 1 ? sn[e >> 1].y : sn[e >> 1].x));
-                            }
-                        }
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    const float2 u = x[e], v = x[2 + e];
+                    x[e] = fma2(u, cs[e], mul2(v, make_float2(-sn[e].x, -sn[e].y)));
+                    x[2 + e] = fma2(v, cs[e], mul2(u, sn[e]));
                 }
             }
-            if (is_q && mine) {
-                if (!p.ok) x[0] = x[1] = x[2] = x[3] = make_float2(0.f, 0.f);
-                store_runs(qo + r * a.D, gap, x);
+        } else if constexpr (kRot == 3) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float c = e & 1 ? cs[e >> 1].y : cs[e >> 1].x, s = e & 1 ? sn[e >> 1].y : sn[e >> 1].x;
+                const float2 v = x[e];
+                if (4 * l + e < a.half) x[e] = make_float2(fmaf(v.x, c, -v.y * s), fmaf(v.y, c, v.x * s));
             }
-            const bool put = mine && !is_q && p.blk >= 0;
-            const size_t row = slot0 + (r - (is_v ? kvrow : a.Hq)) * a.BS;
-            if constexpr (Fmt::kQuant) {
-                if ((pass + 1) * w.per <= a.Hq) continue;  // queries only
-                // the largest |x| as an integer: infinities and NaN are above every finite number
-                uint32_t top = 0;
+        } else if constexpr (kRot == 2) {
+            // rows through shared memory, one word of padding per 8
+            float* buf = rowbuf[warp];
+            const int at = sub * (a.D + a.D / 8);
+            __syncwarp();
+            if (sub < w.per) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    top = max(top, max(__float_as_uint(x[e].x) & 0x7fffffffu, __float_as_uint(x[e].y) & 0x7fffffffu));
-                top = row_reduce(top, w, l, base, [](uint32_t u, uint32_t v) { return max(u, v); });
-                const bool finite = top < 0x7f800000u;
-                const float scale = row_scale(__uint_as_float(top), Fmt::kInvQ);
-                const float inv = __frcp_rn(scale);
-                if (put) {
-                    uint32_t v0 = 0, v1 = 0;
+                for (int e = 0; e < 8; ++e) buf[at + 9 * l + e] = e & 1 ? x[e >> 1].y : x[e >> 1].x;
+            }
+            __syncwarp();
+            if (sub < w.per) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], make_float2(inv, inv));
-                    if (finite) {
-                        v0 = Fmt::encode4(&x[0].x);
-                        v1 = Fmt::encode4(&x[2].x);
+                for (int e = 0; e < 8; ++e) {
+                    const int i = 8 * l + e, q = i < a.half ? i + a.half : i - a.half;
+                    if (i < 2 * a.half) {
+                        const float o = buf[at + q + (q >> 3)];
+                        float& y = e & 1 ? x[e >> 1].y : x[e >> 1].x;
+                        y = fmaf(y, e & 1 ? cs[e >> 1].y : cs[e >> 1].x, o * (e & 1 ? sn[e >> 1].y : sn[e >> 1].x));
                     }
-                    uint8_t* dst = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache) + row * a.D + at0;
-                    *reinterpret_cast<uint32_t*>(dst) = v0;
-                    *reinterpret_cast<uint32_t*>(dst + gap) = v1;
-                    if (l == 0) {
-                        (is_v ? a.v_scale : a.k_scale)[row] = finite ? scale : __int_as_float(0x7fffffff);
-                        if (!finite) report(a.status, PKV_ERR_NONFINITE);
-                    }
-                }
-            } else if (put) {
-                T* dst = static_cast<T*>(is_v ? a.v_cache : a.k_cache) + row * a.D + at0;
-                if (is_v) {  // the bits as they are
-                    using V = std::remove_const_t<std::remove_reference_t<decltype(now.v[0])>>;
-                    *reinterpret_cast<V*>(dst) = now.v[0];
-                    *reinterpret_cast<V*>(dst + gap) = now.v[1];
-                } else {
-                    store_runs(dst, gap, x);
                 }
             }
         }
+    };
+    const size_t slot0 = static_cast<size_t>(max(p.blk, 0)) * a.Hkv * a.BS + p.slot;  // row of KV head 0
+    // a key or value row into the cache
+    auto put = [&](float2 (&x)[4], const Runs<T>& now, int h, void* cache, float* scales, bool is_v) {
+        const bool mine = in && h < a.Hkv && p.blk >= 0;
+        const size_t row = slot0 + static_cast<size_t>(h) * a.BS;
+        if constexpr (Fmt::kQuant) {
+            // the largest |x| as an integer: infinities and NaN are above every finite number
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                top = max(top, max(__float_as_uint(x[e].x) & 0x7fffffffu, __float_as_uint(x[e].y) & 0x7fffffffu));
+            top = row_reduce(top, w, l, base, [](uint32_t u, uint32_t v) { return max(u, v); });
+            const bool finite = top < 0x7f800000u;
+            const float scale = row_scale(__uint_as_float(top), Fmt::kInvQ);
+            const float inv = __frcp_rn(scale);
+            if (mine) {
+                uint32_t v0 = 0, v1 = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], make_float2(inv, inv));
+                if (finite) {
+                    v0 = Fmt::encode4(&x[0].x);
+                    v1 = Fmt::encode4(&x[2].x);
+                }
+                uint8_t* dst = static_cast<uint8_t*>(cache) + row * a.D + at0;
+                *reinterpret_cast<uint32_t*>(dst) = v0;
+                *reinterpret_cast<uint32_t*>(dst + gap) = v1;
+                if (l == 0) {
+                    scales[row] = finite ? scale : __int_as_float(0x7fffffff);
+                    if (!finite) report(a.status, PKV_ERR_NONFINITE);
+                }
+            }
+        } else if (mine) {
+            T* dst = static_cast<T*>(cache) + row * a.D + at0;
+            if (is_v) {  // the bits as they are
+                using V = std::remove_const_t<std::remove_reference_t<decltype(now.v[0])>>;
+                *reinterpret_cast<V*>(dst) = now.v[0];
+                *reinterpret_cast<V*>(dst + gap) = now.v[1];
+            } else {
+                store_runs(dst, gap, x);
+            }
+        }
+    };
+
+    {  // queries
+        float2 g[4];
+        if (a.q_weight != nullptr) to_floats(wq, g);
+        T* qo = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.Hq * a.D + at0;
+        for (int p0 = first; p0 < qpass; p0 += kAhead * stride) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int pass = p0 + k * stride;
+                if (pass >= qpass) break;
+                float2 x[4];
+                to_floats(raw[k], x);
+                load(raw[k], qp, pass + kAhead * stride, a.Hq);
+                if (a.q_weight != nullptr) norm(x, g);
+                rotate(x);
+                if (!p.ok) x[0] = x[1] = x[2] = x[3] = make_float2(0.f, 0.f);
+                const int h = head_of(pass);
+                if (in && h < a.Hq) store_runs(qo + h * a.D, gap, x);
+            }
+        }
+    }
+    {  // keys
+        float2 g[4];
+        if (a.k_weight != nullptr) to_floats(wk, g);
+        for (int pass = k0; pass < kvpass; pass += stride) {
+            float2 x[4];
+            to_floats(rawk, x);
+            load(rawk, kp, pass + stride, a.Hkv);
+            if (a.k_weight != nullptr) norm(x, g);
+            rotate(x);
+            put(x, rawk, head_of(pass), a.k_cache, a.k_scale, false);
+        }
+    }
+    for (int pass = v0; pass < kvpass; pass += stride) {
+        float2 x[4];
+        const Runs<T> now = rawv;
+        to_floats(now, x);
+        load(rawv, vp, pass + stride, a.Hkv);
+        put(x, now, head_of(pass), a.v_cache, a.v_scale, true);
     }
 }
 
@@ -495,7 +531,10 @@ static cudaError_t launch_typed(const WriteArgs& a, cudaStream_t stream) {
         w.per = 32 / w.lanes;
         w.magic = 65536 / w.lanes + 1;  // exact for lane < 32, lanes <= 32
         w.pow2 = (w.lanes & (w.lanes - 1)) == 0;
-        const int passes = w.passes = (rows + w.per - 1) / w.per;
+        w.qpasses = (a.Hq + w.per - 1) / w.per;
+        w.kvpasses = (a.Hkv + w.per - 1) / w.per;
+        w.inv_d = 1.0f / static_cast<float>(a.D);
+        const int passes = w.qpasses + 2 * w.kvpasses;
         // many tokens: a warp takes many passes of one token, which shares the token's place,
         // angles and weights; few: a token's passes over as many warps and CTAs as there are
         w.wpt_log2 = 3;
