@@ -5,7 +5,9 @@ in-tree by ``paged_kv_decode_table_gb300.build``).  Every function here only
 checks and marshals torch tensors (device, dtype, contiguity, shapes) and passes
 raw device pointers plus the current CUDA stream; all arithmetic runs in the
 library's CUDA kernels.  There is no CPU fallback: if the library cannot be
-loaded, every call raises.
+loaded, every call raises.  The calls of the 8-bit cache and qk_norm_rope_append
+go through a small native module (``_torch_calls``) instead of ctypes, because
+their kernels take less time than testing their arguments in Python.
 
 Calls (names follow the C ABI):
   kv_append(k_new, v_new, k_cache, v_cache, block_tables, seq_lens)
@@ -32,6 +34,7 @@ block_size, D] with float32 scales [num_blocks, Hkv, block_size], one per row.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 import threading
@@ -717,94 +720,68 @@ def paged_prefill_attention(q, k_cache, v_cache, block_tables, seq_lens, q_start
 
 
 # ---------------------------------------------------------------- 8-bit cache
-# These calls sit in decode loops whose kernels take a few microseconds, and an
-# attribute of a tensor costs a tenth of one: each call tests its arguments in one
-# expression, and only where that fails do the _check functions run, which name
-# what is wrong.
-_f32, _i32, _u8 = torch.float32, torch.int32, torch.uint8
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
-_sms: dict = {}     # SM count by device index
-_q8_need: dict = {}  # workspace bytes by (device index, Hq, Hkv, D)
+# These calls sit in decode loops whose kernels take a few microseconds, so their
+# arguments are tested and passed on by the native module _torch_calls
+# (csrc/torch_calls.cpp).  It answers -1 where an argument is not what it should
+# be; the _check functions then name it.
+_calls = None
+
+
+def _native():
+    global _calls
+    if _calls is None:
+        load_library()  # before torch_calls, which links to it
+        if not os.path.exists(os.path.join(_HERE, "_torch_calls.so")):
+            raise RuntimeError("_torch_calls.so is missing: run paged_kv_decode_table_gb300.build.build() first")
+        _calls = importlib.import_module("._torch_calls", __package__)
+    return _calls
+
+
+def _failed(name, code):
+    if code > 0:
+        raise PkvError(name, code)
+    raise ValueError(f"{name}: an argument has an unsupported kind or size")
 
 
 def _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev):
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
     if k_cache.dtype not in _CODES_Q8:
         raise TypeError(f"k_cache must be torch.float8_e4m3fn or torch.int8, got {k_cache.dtype}")
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [num_blocks, Hkv, block_size, D]")
     _check_cuda("k_cache", k_cache, k_cache.dtype, device=dev)
     _check_cuda("v_cache", v_cache, k_cache.dtype, k_cache.shape, dev)
-    _check_cuda("k_scale", k_scale, _f32, k_cache.shape[:3], dev)
-    _check_cuda("v_scale", v_scale, _f32, k_cache.shape[:3], dev)
+    _check_cuda("k_scale", k_scale, torch.float32, k_cache.shape[:3], dev)
+    _check_cuda("v_scale", v_scale, torch.float32, k_cache.shape[:3], dev)
 
 
 def _check_tables(block_tables, seq_lens, B, status, dev):
-    _check_cuda("block_tables", block_tables, _i32, device=dev)
-    _check_cuda("seq_lens", seq_lens, _i32, (B,), dev)
+    _check_cuda("block_tables", block_tables, torch.int32, device=dev)
+    _check_cuda("seq_lens", seq_lens, torch.int32, (B,), dev)
     if block_tables.dim() != 2 or block_tables.shape[0] != B:
         raise ValueError("block_tables must be [B, max_blocks_per_seq]")
     if status is not None:
-        _check_cuda("status", status, _i32, (1,), dev)
-
-
-def _unclear():
-    raise ValueError("an argument has an unsupported kind")  # a tensor the checks above let pass
-
-
-def _cache_ok(k_cache, v_cache, k_scale, v_scale, shape, dev):
-    dt, rows = k_cache.dtype, shape[:3]
-    return (len(shape) == 4 and dt in _CODES_Q8 and v_cache.dtype is dt and k_scale.dtype is _f32
-            and v_scale.dtype is _f32 and v_cache.shape == shape and k_scale.shape == rows and v_scale.shape == rows
-            and dev >= 0 and v_cache.get_device() == dev and k_scale.get_device() == dev
-            and v_scale.get_device() == dev and k_cache.is_contiguous() and v_cache.is_contiguous()
-            and k_scale.is_contiguous() and v_scale.is_contiguous())
-
-
-def _tables_ok(block_tables, seq_lens, B, status, dev):
-    return (block_tables.dtype is _i32 and seq_lens.dtype is _i32 and block_tables.get_device() == dev
-            and seq_lens.get_device() == dev and block_tables.dim() == 2 and block_tables.shape[0] == B
-            and seq_lens.dim() == 1 and block_tables.is_contiguous() and seq_lens.is_contiguous()
-            and (status is None or (status.dtype is _i32 and status.shape == (1,) and status.get_device() == dev)))
-
-
-def _launch(name, dev, fn, *args):
-    """Call the library on the current stream of device index `dev`, with that device current."""
-    if _current_device() == dev:
-        code = fn(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            code = fn(*args, _raw_stream(dev))
-    if code != 0:
-        raise PkvError(name, code)
+        _check_cuda("status", status, torch.int32, (1,), dev)
 
 
 def _append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, q_start, status):
-    shape, dev, dt = k_cache.shape, k_cache.get_device(), k_new.dtype
-    code = _CODES.get(dt)
-    B, T = seq_lens.shape[0], k_new.shape[0]
-    if not (_cache_ok(k_cache, v_cache, k_scale, v_scale, shape, dev) and code is not None
-            and _tables_ok(block_tables, seq_lens, B, status, dev) and k_new.shape == (T, shape[1], shape[3])
-            and v_new.shape == k_new.shape and v_new.dtype is dt and k_new.get_device() == dev
-            and v_new.get_device() == dev and k_new.is_contiguous() and v_new.is_contiguous()
-            and (T == B if q_start is None else
-                 q_start.dtype is _i32 and q_start.shape == (B + 1,) and q_start.get_device() == dev
-                 and q_start.is_contiguous())):
-        d = k_cache.device
-        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, d)
+    code = (_calls or _native()).append(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens,
+                                        q_start, status)
+    if code == 0:
+        return
+    if code < 0:
+        dev = k_cache.device
+        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
         _dtype_code(k_new)
-        rows = (B if q_start is None else T, shape[1], shape[3])
-        _check_cuda("k_new", k_new, k_new.dtype, rows, d)
-        _check_cuda("v_new", v_new, k_new.dtype, rows, d)
-        _check_tables(block_tables, seq_lens, B, status, d)
+        B = seq_lens.shape[0]
+        rows = (B if q_start is None else k_new.shape[0], k_cache.shape[1], k_cache.shape[3])
+        _check_cuda("k_new", k_new, k_new.dtype, rows, dev)
+        _check_cuda("v_new", v_new, k_new.dtype, rows, dev)
+        _check_tables(block_tables, seq_lens, B, status, dev)
         if q_start is not None:
-            _check_cuda("q_start", q_start, _i32, (B + 1,), d)
-        _unclear()
-    _launch("pkv_kv_append_q8", dev, (_lib or load_library()).pkv_kv_append_q8, k_new.data_ptr(), v_new.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
-            block_tables.shape[1], seq_lens.data_ptr(), None if q_start is None else q_start.data_ptr(), B, T,
-            shape[1], shape[3], shape[2], shape[0], code, _CODES_Q8[k_cache.dtype],
-            None if status is None else status.data_ptr())
+            _check_cuda("q_start", q_start, torch.int32, (B + 1,), dev)
+    _failed("pkv_kv_append_q8", code)
 
 
 def kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, status=None):
@@ -824,37 +801,26 @@ def kv_append_chunk_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_t
 def kv_read_blocks_q8(k_cache, v_cache, k_scale, v_scale, blocks, k_out=None, v_out=None, dtype=torch.bfloat16,
                       status=None):
     """Blocks `blocks` (int32 [n]) of an 8-bit cache as an unquantised pool:
-    returns (k, v) [n, Hkv, block_size, D] in `dtype` (that of k_out if given)."""
-    shape, dev = k_cache.shape, k_cache.get_device()
-    if not (_cache_ok(k_cache, v_cache, k_scale, v_scale, shape, dev) and blocks.dtype is _i32 and blocks.dim() == 1
-            and blocks.get_device() == dev and blocks.is_contiguous()
-            and (status is None or (status.dtype is _i32 and status.shape == (1,) and status.get_device() == dev))):
-        d = k_cache.device
-        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, d)
-        _check_cuda("blocks", blocks, _i32, (blocks.shape[0],), d)
+    returns (k, v) [n, Hkv, block_size, D] in `dtype` (that of k_out or v_out if given)."""
+    r = (_calls or _native()).read(k_cache, v_cache, k_scale, v_scale, blocks, k_out, v_out, dtype, status)
+    if type(r) is tuple:
+        return r
+    if r < 0:
+        dev = k_cache.device
+        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
+        _check_cuda("blocks", blocks, torch.int32, (blocks.numel(),), dev)
+        given = k_out if k_out is not None else v_out
+        if given is None and dtype not in _CODES:
+            raise TypeError(f"unsupported element type {dtype} (float32 or bfloat16)")
+        if given is not None:
+            _dtype_code(given)
+        want = (blocks.shape[0], *k_cache.shape[1:])
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is not None:
+                _check_cuda(name, t, given.dtype, want, dev)
         if status is not None:
-            _check_cuda("status", status, _i32, (1,), d)
-        _unclear()
-    n = blocks.shape[0]
-    want = (n, shape[1], shape[2], shape[3])
-    if k_out is None and v_out is None:
-        # one allocation for both pools
-        k_out, v_out = torch.empty((2, *want), dtype=dtype, device=k_cache.device).unbind(0)
-    else:
-        if k_out is None:
-            k_out = torch.empty_like(v_out)
-        elif v_out is None:
-            v_out = torch.empty_like(k_out)
-        _check_cuda("k_out", k_out, k_out.dtype, want, k_cache.device)
-        _check_cuda("v_out", v_out, k_out.dtype, want, k_cache.device)
-    code = _CODES.get(k_out.dtype)
-    if code is None:
-        code = _dtype_code(k_out)
-    _launch("pkv_kv_read_blocks_q8", dev, (_lib or load_library()).pkv_kv_read_blocks_q8, k_out.data_ptr(),
-            v_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-            blocks.data_ptr(), n, shape[1], shape[3], shape[2], shape[0], code, _CODES_Q8[k_cache.dtype],
-            None if status is None else status.data_ptr())
-    return k_out, v_out
+            _check_cuda("status", status, torch.int32, (1,), dev)
+    _failed("pkv_kv_read_blocks_q8", r)
 
 
 def decode_q8_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, num_sms: int = 0) -> int:
@@ -867,39 +833,21 @@ def paged_decode_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_table
     bfloat16; returns out [B, Hq, D].  Without `workspace` one is allocated for
     the call, so calls on several streams, or captured in several graphs, do not
     share it."""
-    shape, dev, dt, qs = k_cache.shape, k_cache.get_device(), q.dtype, q.shape
-    code = _CODES.get(dt)
-    if not (_cache_ok(k_cache, v_cache, k_scale, v_scale, shape, dev) and code is not None and len(qs) == 3
-            and qs[2] == shape[3] and q.get_device() == dev and q.is_contiguous()
-            and _tables_ok(block_tables, seq_lens, qs[0], status, dev) and seq_lens.shape[0] == qs[0]):
-        d = k_cache.device
-        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, d)
+    r = (_calls or _native()).attend(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, out, scale,
+                                     workspace, status)
+    if type(r) is not int:
+        return r
+    if r < 0:
+        dev = k_cache.device
+        _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
         _dtype_code(q)
-        _check_cuda("q", q, dt, (q.shape[0], q.shape[1], shape[3]), d)
-        _check_tables(block_tables, seq_lens, q.shape[0], status, d)
-        _unclear()
-    B, Hq, D = qs
-    lib = _lib or load_library()
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _check_cuda("out", out, dt, qs, q.device)
-    if workspace is None:
-        key = (dev, Hq, shape[1], D)
-        ws_bytes = _q8_need.get(key)
-        if ws_bytes is None:
-            if dev not in _sms:
-                _sms[dev] = torch.cuda.get_device_properties(dev).multi_processor_count
-            ws_bytes = _q8_need[key] = lib.pkv_decode_q8_workspace_bytes(B, Hq, shape[1], D, _sms[dev])
-        workspace = torch.empty(ws_bytes or 16, dtype=_u8, device=k_cache.device)
-    else:
-        _check_cuda("workspace", workspace, device=q.device)
-        ws_bytes = workspace.numel() * workspace.element_size()
-    _launch("pkv_paged_decode_attention_q8", dev, lib.pkv_paged_decode_attention_q8, out.data_ptr(), q.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_tables.data_ptr(),
-            block_tables.shape[1], seq_lens.data_ptr(), B, Hq, shape[1], D, shape[2], shape[0], scale, code,
-            _CODES_Q8[k_cache.dtype], workspace.data_ptr(), ws_bytes, None if status is None else status.data_ptr())
-    return out
+        _check_cuda("q", q, q.dtype, (q.shape[0], q.shape[1], k_cache.shape[3]), dev)
+        _check_tables(block_tables, seq_lens, q.shape[0], status, dev)
+        if out is not None:
+            _check_cuda("out", out, q.dtype, q.shape, dev)
+        if workspace is not None:
+            _check_cuda("workspace", workspace, device=dev)
+    _failed("pkv_paged_decode_attention_q8", r)
 
 
 def rope_freqs(rot_dim: int, base: float = 10000.0, inv_freq=None, device="cuda") -> torch.Tensor:
@@ -923,18 +871,9 @@ def _check_rows(name, t, dtype, shape, dev):
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if _token_stride(t, shape[1], shape[2]) < 0:
+    T, H, D = shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D) or (T > 1 and t.stride(0) < H * D):
         raise ValueError(f"{name}: the heads of a token must be dense ([H, D] rows) and tokens must not overlap")
-
-
-def _token_stride(t, H, D):
-    """Elements between the tokens of a [T, H, D] view with dense heads; -1 if it is none."""
-    st = t.stride()
-    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
-        return -1
-    if t.shape[0] <= 1:
-        return H * D
-    return st[0] if st[0] >= H * D else -1
 
 
 def qk_norm_rope_append(q, k_new, v_new, q_weight, k_weight, eps, freqs, k_cache, v_cache, block_tables, seq_lens,
@@ -948,68 +887,34 @@ def qk_norm_rope_append(q, k_new, v_new, q_weight, k_weight, eps, freqs, k_cache
     any distance apart, so views of one projection output will do).  T is B (one
     token per sequence) or, with q_start, the packed chunks of kv_append_chunk.
     The cache is of q's type, or an 8-bit one with its k_scale and v_scale."""
-    shape, dev, dt, qs = k_cache.shape, k_cache.get_device(), q.dtype, q.shape
-    code = _CODES.get(dt)
-    q8 = k_scale is not None or v_scale is not None
-    ok = len(shape) == 4 and len(qs) == 3 and k_new.dim() == 3 and v_new.dim() == 3
-    if ok:
-        NB, Hkv, BS, D = shape
-        T, Hq = qs[0], qs[1]
-        B, kvs = seq_lens.shape[0], (T, Hkv, D)
-        ok = (code is not None and qs[2] == D and k_new.shape == kvs and v_new.shape == kvs and k_new.dtype is dt
-              and v_new.dtype is dt and q.get_device() == dev and k_new.get_device() == dev
-              and v_new.get_device() == dev and _tables_ok(block_tables, seq_lens, B, status, dev)
-              and (_cache_ok(k_cache, v_cache, k_scale, v_scale, shape, dev)
-                   if k_scale is not None and v_scale is not None else
-                   not q8 and dev >= 0 and k_cache.dtype is dt and v_cache.dtype is dt and v_cache.shape == shape
-                   and v_cache.get_device() == dev and k_cache.is_contiguous() and v_cache.is_contiguous())
-              and (T == B if q_start is None else
-                   q_start.dtype is _i32 and q_start.shape == (B + 1,) and q_start.get_device() == dev
-                   and q_start.is_contiguous())
-              and (q_weight is None or (q_weight.dtype is dt and q_weight.shape == (D,) and q_weight.get_device() == dev
-                                        and q_weight.is_contiguous()))
-              and (k_weight is None or (k_weight.dtype is dt and k_weight.shape == (D,) and k_weight.get_device() == dev
-                                        and k_weight.is_contiguous()))
-              and (freqs is None or (freqs.dtype is torch.int64 and freqs.dim() == 1 and freqs.get_device() == dev
-                                     and freqs.is_contiguous())))
-    if ok:
-        qst, kst, vst = _token_stride(q, Hq, D), _token_stride(k_new, Hkv, D), _token_stride(v_new, Hkv, D)
-        ok = qst >= 0 and kst >= 0 and vst >= 0
-    if not ok:
-        d = k_cache.device
+    r = (_calls or _native()).prepare(q, k_new, v_new, q_weight, k_weight, eps, freqs, k_cache, v_cache, block_tables,
+                                      seq_lens, q_start, k_scale, v_scale, interleaved, q_out, status)
+    if type(r) is not int:
+        return r
+    if r < 0:
+        dev = k_cache.device
         _dtype_code(q)
         if k_cache.dim() != 4 or q.dim() != 3:
             raise ValueError("k_cache must be [num_blocks, Hkv, block_size, D], q [T, Hq, D]")
-        if q8:
-            _check_cache_q8(k_cache, v_cache, k_scale, v_scale, d)
+        if k_scale is None and v_scale is None:
+            _check_cuda("k_cache", k_cache, q.dtype)
+            _check_cuda("v_cache", v_cache, q.dtype, k_cache.shape, dev)
         else:
-            _check_cuda("k_cache", k_cache, dt)
-            _check_cuda("v_cache", v_cache, dt, shape, d)
-        B, T = seq_lens.shape[0], qs[0]
+            _check_cache_q8(k_cache, v_cache, k_scale, v_scale, dev)
+        (T, Hq, _), (_, Hkv, _, D), B = q.shape, k_cache.shape, seq_lens.shape[0]
         if q_start is not None:
-            _check_cuda("q_start", q_start, _i32, (B + 1,), d)
+            _check_cuda("q_start", q_start, torch.int32, (B + 1,), dev)
         elif T != B:
             raise ValueError(f"q has {T} tokens for {B} sequences: pass q_start")
-        _check_rows("q", q, dt, (T, qs[1], shape[3]), d)
-        _check_rows("k_new", k_new, dt, (T, shape[1], shape[3]), d)
-        _check_rows("v_new", v_new, dt, (T, shape[1], shape[3]), d)
+        _check_rows("q", q, q.dtype, (T, Hq, D), dev)
+        _check_rows("k_new", k_new, q.dtype, (T, Hkv, D), dev)
+        _check_rows("v_new", v_new, q.dtype, (T, Hkv, D), dev)
         for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
             if w is not None:
-                _check_cuda(name, w, dt, (shape[3],), d)
+                _check_cuda(name, w, q.dtype, (D,), dev)
         if freqs is not None:
-            _check_cuda("freqs", freqs, torch.int64, (freqs.shape[0],), d)
-        _check_tables(block_tables, seq_lens, B, status, d)
-        _unclear()
-    if q_out is None:
-        q_out = torch.empty(qs, dtype=dt, device=k_cache.device)
-    else:
-        _check_cuda("q_out", q_out, dt, qs, k_cache.device)
-    _launch("pkv_qk_norm_rope_append", dev, (_lib or load_library()).pkv_qk_norm_rope_append, q_out.data_ptr(),
-            q.data_ptr(), qst, k_new.data_ptr(), kst, v_new.data_ptr(), vst,
-            None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
-            None if freqs is None else freqs.data_ptr(), 0 if freqs is None else 2 * freqs.shape[0], interleaved,
-            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if q8 else None,
-            v_scale.data_ptr() if q8 else None, block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
-            None if q_start is None else q_start.data_ptr(), B, T, Hq, Hkv, D, BS, NB, code,
-            _CODES_Q8[k_cache.dtype] if q8 else code, None if status is None else status.data_ptr())
-    return q_out
+            _check_cuda("freqs", freqs, torch.int64, (freqs.numel(),), dev)
+        _check_tables(block_tables, seq_lens, B, status, dev)
+        if q_out is not None:
+            _check_cuda("q_out", q_out, q.dtype, q.shape, dev)
+    _failed("pkv_qk_norm_rope_append", r)

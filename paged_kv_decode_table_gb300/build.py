@@ -1,8 +1,10 @@
-"""Build the CUDA library ``libpkv.so`` in-tree for sm_103a.
+"""Build the CUDA library ``libpkv.so`` and the module ``_torch_calls`` in-tree.
 
-Each ``csrc/*.cu`` translation unit is compiled by nvcc in parallel, then linked
-into one shared library next to this file.  The CUDA runtime is linked
-statically, so loading the library needs only the NVIDIA driver.
+Each ``csrc/*.cu`` translation unit is compiled by nvcc for sm_103a in parallel,
+then linked into one shared library next to this file.  The CUDA runtime is
+linked statically, so loading the library needs only the NVIDIA driver.
+``csrc/torch_calls.cpp`` becomes a Python module that links to that library and
+to the installed torch.
 """
 from __future__ import annotations
 
@@ -11,12 +13,15 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build", "pkv")
 LIB = os.path.join(HERE, "libpkv.so")
+CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
+CALLS = os.path.join(HERE, "_torch_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -35,23 +40,37 @@ def _sources():
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(ROOT, "include", "pkv.h")]
+    return _sources() + [CALLS_SRC] + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(ROOT, "include", "pkv.h")]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libpkv.so; returns its path."""
+    """Compile and link libpkv.so and _torch_calls.so; returns the path of the former."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     objs = []
+
+    import torch
+    torch_root = os.path.dirname(torch.__file__)
+    calls_obj = os.path.join(BUILD, "torch_calls.o")
+
+    def compile_calls():
+        inc = [os.path.join(torch_root, "include"), os.path.join(torch_root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")]
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               f"-I{os.path.join(ROOT, 'include')}", *[a for p in inc for a in ("-isystem", p)],
+               "-c", CALLS_SRC, "-o", calls_obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src).replace(".cu", ".o"))
@@ -64,13 +83,23 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        calls = ex.submit(compile_calls)
         objs = list(ex.map(compile_one, _sources()))
+        calls.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    torch_lib = os.path.join(torch_root, "lib")
+    cmd = ["g++", "-shared", "-o", tmp, calls_obj, f"-L{HERE}", "-l:libpkv.so", "-Wl,-rpath,$ORIGIN", f"-L{torch_lib}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{torch_lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
     return LIB
 
 
