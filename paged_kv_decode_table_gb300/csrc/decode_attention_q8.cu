@@ -30,7 +30,9 @@
 //    movmatrix turns the weights from S^T's layout into P^T's.
 //  * bf16 queries are exact in float16 and the weights are rounded to it (2^-11);
 //    float32 queries carry what that rounding leaves of q and of the weights in a
-//    second float16 and a second MMA (kSplit), which gives float32 accuracy.
+//    second float16 and a second MMA (kSplit), and sum each step apart before
+//    adding it: the result is within 7e-7 of the exact one in the 2-norm over
+//    500 to 60000 positions (1.0e-6 without the separate sums).
 //  * Weights are normalised by a running maximum of s_j + log2(vs_j), the largest
 //    contribution rather than the largest score, so that p_j * vs_j fits float16
 //    whatever the V scales are.  Scales below 2^-64 count as 2^-64 there, which
@@ -460,8 +462,15 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                     Fmt::decode4(w[2 * u + 1], a[1], a[3]);
 #pragma unroll
                     for (int n = 0; n < kN; ++n) {
-                        mma_f16_16816(s[n][u], a, qb[n][c + u][0], qb[n][c + u][1]);
-                        if constexpr (kSplit) mma_f16_16816(s[n][u], a, ql[n][c + u][0], ql[n][c + u][1]);
+                        if constexpr (kSplit) {
+                            float z[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma_f16_16816(z, a, ql[n][c + u][0], ql[n][c + u][1]);
+                            mma_f16_16816(z, a, qb[n][c + u][0], qb[n][c + u][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) s[n][u][e] += z[e];
+                        } else {
+                            mma_f16_16816(s[n][u], a, qb[n][c + u][0], qb[n][c + u][1]);
+                        }
                     }
                 }
             }
@@ -512,6 +521,15 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 }
             }
         }
+        // kSplit: the step's products are summed apart and added to the running sums by
+        // rounded additions, because the MMA's own accumulation truncates
+        float F[kSplit ? kChunks : 1][kSplit ? kN : 1][4];
+        if constexpr (kSplit) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                for (int n = 0; n < kN; ++n) F[c][n][0] = F[c][n][1] = F[c][n][2] = F[c][n][3] = 0.f;
+        }
 #pragma unroll
         for (int k = 0; k < kQ8Sub; ++k) {
             if (kPart && k * kQ8Tok >= ntok) break;
@@ -553,11 +571,23 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                     Fmt::decode4_pairs(kPart ? w[2 * u + 1] & keep1 : w[2 * u + 1], a[2], a[3]);
 #pragma unroll
                     for (int n = 0; n < kN; ++n) {
-                        mma_f16_16816(O[c + u][n], a, pb[n][0], pb[n][1]);
-                        if constexpr (kSplit) mma_f16_16816(O[c + u][n], a, pl2[n][0], pl2[n][1]);
+                        if constexpr (kSplit) {
+                            mma_f16_16816(F[c + u][n], a, pl2[n][0], pl2[n][1]);
+                            mma_f16_16816(F[c + u][n], a, pb[n][0], pb[n][1]);
+                        } else {
+                            mma_f16_16816(O[c + u][n], a, pb[n][0], pb[n][1]);
+                        }
                     }
                 }
             }
+        }
+        if constexpr (kSplit) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+                for (int n = 0; n < kN; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) O[c][n][e] += F[c][n][e];
         }
     };
 
