@@ -78,6 +78,7 @@ struct Q8Plan {
     int UB;          // units of 16 positions per block
     int nst;         // ring stages
     int stage_bytes, scale_unit, q_bytes, scratch_bytes;
+    int q_stride;    // bytes between q's rows in shared memory
     int direct;      // one CTA per (sequence, group), no join
     int pack;        // D = 64: two positions per 128-byte row of a tile
     int B, Hq, Hkv, G, D, BS, NB, max_blocks;
@@ -119,6 +120,11 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     return r;
 }
 
+__device__ __forceinline__ float4 load_row4(const __nv_bfloat16* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
+}
+__device__ __forceinline__ float4 load_row4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void store_row2(__nv_bfloat16* p, float x, float y) {
     *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(x, y);
 }
@@ -211,13 +217,20 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     int* sch = reinterpret_cast<int*>(meta + kQ8MaxStages);  // [0, 33) scan scratch, 33: b0, 34: s0
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // lengths, then block ids, then K and V: three dependent loads, from HBM where the
+    // caches of the last step have pushed them out of L2; the first two and q come to L2
+    // while the predecessor ends
+    const unsigned worker = blockIdx.x * blockDim.x + threadIdx.x;
+    prefetch_l2(seq_lens, static_cast<size_t>(pl.B) * 4, worker);
+    prefetch_l2(block_tables, static_cast<size_t>(pl.B) * pl.max_blocks * 4, worker);
+    prefetch_l2(q, static_cast<size_t>(pl.B) * pl.Hq * pl.D * sizeof(T), worker);
     if (threadIdx.x == 0) {
         for (int s = 0; s < nst; ++s) {
             mbar_init(&full[s], 1 + 32);  // the TMA bytes, and each producer lane's scale copies
             mbar_init(&empty[s], CW);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&qfull[s], 1);
+            mbar_init(&qfull[s], 32);  // each producer lane's copies
             mbar_init(&qempty[s], CW);
         }
         for (int s = 0; s < kQ8Warps; ++s) {
@@ -337,9 +350,11 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             if (lane != 0) return;
             for (int k = max(0, it - nst); k < it; ++k)
                 mbar_wait(&full[k % nst], static_cast<uint32_t>(k / nst) & 1u, pl.polls);
-            for (int pk = max(0, piece - 2); pk < piece; ++pk)
-                mbar_wait(&qfull[pk & 1], static_cast<uint32_t>(pk >> 1) & 1u, pl.polls);
         };
+        // 16-byte chunks of a row of q; this lane's first one, and the step to its next one
+        const int q_chunks = pl.D * static_cast<int>(sizeof(T)) / 16;
+        const int q_row = lane / q_chunks, q_col = lane - q_row * q_chunks;
+        const int q_drow = 32 / q_chunks, q_dcol = 32 - q_drow * q_chunks;
         int stage = 0;
         uint32_t parity = 1;  // of the empty barriers: the first round finds them free
         for (int i = start, it = 0; i < end; ++i, ++it) {
@@ -375,15 +390,22 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 tma_load_3d(kd + half_stage, &tmV, 0, s.tok >> pl.pack, row, &full[stage]);
             }
             if (first) {
-                if (lane == 0) {
-                    const int qs = piece & 1;
-                    const int rows = min(pl.R, pl.Hq - s.g * pl.R);  // the last group may have fewer heads
-                    const uint32_t bytes = static_cast<uint32_t>(rows) * pl.D * sizeof(T);
-                    mbar_arrive_expect_tx(&qfull[qs], bytes);
-                    tma_load_1d(qring + static_cast<size_t>(qs) * pl.q_bytes,
-                                q + (static_cast<size_t>(s.b) * pl.Hq + static_cast<size_t>(s.g) * pl.R) * pl.D, bytes,
-                                &qfull[qs]);
+                const int qs = piece & 1;
+                const int rows = min(pl.R, pl.Hq - s.g * pl.R);  // the last group may have fewer heads
+                const uint8_t* src = reinterpret_cast<const uint8_t*>(
+                    q + (static_cast<size_t>(s.b) * pl.Hq + static_cast<size_t>(s.g) * pl.R) * pl.D);
+                uint8_t* dst = qring + static_cast<size_t>(qs) * pl.q_bytes;
+                int row = q_row, col = q_col;
+                for (int x = lane; x < rows * q_chunks; x += 32) {
+                    cp_async16(dst + row * pl.q_stride + col * 16, src + x * 16);
+                    row += q_drow;
+                    col += q_dcol;
+                    if (col >= q_chunks) {
+                        col -= q_chunks;
+                        ++row;
+                    }
                 }
+                cp_async_arrive(&qfull[qs]);
                 ++piece;
             }
             if (bad && lane == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
@@ -523,7 +545,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
         }
         // kSplit: the step's products are summed apart and added to the running sums by
         // rounded additions, because the MMA's own accumulation truncates
-        float F[kSplit ? kChunks : 1][kSplit ? kN : 1][4];
+        [[maybe_unused]] float F[kSplit ? kChunks : 1][kSplit ? kN : 1][4];
         if constexpr (kSplit) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
@@ -604,8 +626,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 return;
             }
             // head g (of each n-tile): dims 16 c + 4 r .. + 3
-            const T* qsm = reinterpret_cast<const T*>(qring + static_cast<size_t>(qs) * pl.q_bytes) +
-                           static_cast<size_t>(hh * pl.G) * pl.D;
+            const uint8_t* qsm = qring + static_cast<size_t>(qs) * pl.q_bytes + hh * pl.G * pl.q_stride;
             // (none for the heads that a last, smaller group lacks)
             const int qrows = (mt.vb % NG) * HG + hh < pl.Hkv ? pl.G : 0;
             float v[kN][kChunks][4], amax = 0.f;
@@ -613,13 +634,16 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             for (int n = 0; n < kN; ++n) {
                 const int row = qc * kHeads + 8 * n + g;
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int d = c * 16 + 4 * r;
-                        v[n][c][e] = row < qrows && d < pl.D ? to_f32(qsm[row * pl.D + d + e]) : 0.f;
-                        amax = fmaxf(amax, fabsf(v[n][c][e]));
-                    }
+                for (int c = 0; c < kChunks; ++c) {
+                    const int d = c * 16 + 4 * r;
+                    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (row < qrows && d < pl.D) z = load_row4(reinterpret_cast<const T*>(qsm + row * pl.q_stride) + d);
+                    v[n][c][0] = z.x;
+                    v[n][c][1] = z.y;
+                    v[n][c][2] = z.z;
+                    v[n][c][3] = z.w;
+                    amax = fmaxf(amax, fmaxf(fmaxf(fabsf(z.x), fabsf(z.y)), fmaxf(fabsf(z.z), fabsf(z.w))));
+                }
             }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -1047,7 +1071,10 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     const int tiles = pl.HG * pl.slots * kQ8Sub;
     pl.stage_bytes = 2 * tiles * kQ8Tok * DP;
     pl.scale_unit = pl.HG * kQ8Tok * 4;
-    pl.q_bytes = pl.R * pl.D * static_cast<int>(sizeof(T));
+    // rows 32 (bf16) or 64 bytes apart modulo 128, so that the 8 heads a warp reads at
+    // once fall on different banks
+    pl.q_stride = (pl.D * static_cast<int>(sizeof(T)) + 127) / 128 * 128 + 16 * static_cast<int>(sizeof(T));
+    pl.q_bytes = pl.R * pl.q_stride;
     pl.scratch_bytes = (pl.slots - 1) * pl.HG * pl.QC * (8 * kN * (DP + 6)) * 4;
     const size_t fixed = 1024 + 2 * static_cast<size_t>(pl.q_bytes) + pl.scratch_bytes +
                          (2 * kQ8MaxStages + 4 + 2 * kQ8Warps) * sizeof(uint64_t) + kQ8MaxStages * sizeof(Q8Meta) +

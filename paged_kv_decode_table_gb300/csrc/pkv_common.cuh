@@ -110,6 +110,15 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// Ask for the lines of [p, p + bytes) in L2, shared out over `workers` threads, one
+// line each (a larger range is taken in part).  Reads nothing, so it may stand before
+// griddepcontrol.wait: what the predecessor still writes goes through the same L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, size_t bytes, unsigned worker) {
+    const uintptr_t first = reinterpret_cast<uintptr_t>(p) & ~static_cast<uintptr_t>(127);
+    const uintptr_t at = first + static_cast<uintptr_t>(worker) * 128;
+    if (at < reinterpret_cast<uintptr_t>(p) + bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(at < reinterpret_cast<uintptr_t>(p) ? reinterpret_cast<uintptr_t>(p) : at) : "memory");
+}
+
 // ---------------------------------------------------------------- tensor core (warp-level)
 __device__ __forceinline__ void ldmatrix_x4(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3,
                                             uint32_t addr) {
