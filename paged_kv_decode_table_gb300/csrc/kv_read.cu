@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kReadThreads)
                    const uint8_t* __restrict__ v_cache, const float* __restrict__ k_scale,
                    const float* __restrict__ v_scale, const int32_t* __restrict__ blocks, int chunks, int R, int D,
                    int NB, int32_t* status) {
+    prefetch_l2(blocks, static_cast<size_t>(gridDim.x / (2 * chunks)) * 4, blockIdx.x * kReadThreads + threadIdx.x);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // CTA: (block, K or V, chunk of rows)

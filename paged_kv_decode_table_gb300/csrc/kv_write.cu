@@ -63,40 +63,60 @@ __device__ __forceinline__ float warp_max(float x) {
     return x;
 }
 
-// Where token t goes.  ok: the sequence's length and chunk are valid (pos is
-// set); blk < 0: no valid block for that position.
+// Where token t goes.  live: a token of some sequence (the rows behind the last one are
+// not); ok: the sequence's length and chunk are valid, and pos and slot are set.
+// blk_raw is the table's entry, still unchecked: its load is not waited for here.
 struct Place {
-    int ok, pos, blk, slot;
+    int live, ok, pos, slot, blk_raw;
+    __device__ __forceinline__ int blk(int NB) const { return ok && blk_raw >= 0 && blk_raw < NB ? blk_raw : -1; }
 };
 
-// Called by a whole warp with one t.
+// Called by a whole warp with one t < T.
 __device__ __forceinline__ Place place_of(const WriteArgs& a, int t) {
-    Place p{0, 0, -1, 0};
-    int b = t, n = 1, i = 0;
+    Place p{1, 0, 0, 0, -1};
+    int b = t, n = 1, i = 0, L;
     if (a.q_start != nullptr) {
-        // the last b with q_start[b] <= t: 32 probes per round, so 1024 sequences take two
-        // dependent loads
-        int lo = 0, count = a.B;  // in [lo, lo + count)
+        // the last b with q_start[b] <= t: 32 probes per round, and with at most 32
+        // sequences left one round trip brings their starts, ends and lengths
         const int lane = threadIdx.x & 31;
-        while (count > 1) {
+        const int tend = a.q_start[a.B];
+        int lo = 0, count = a.B;  // in [lo, lo + count)
+        while (count > 32) {
             const int step = (count + 31) / 32, at = lane * step;
             const unsigned below = __ballot_sync(0xffffffffu, at < count && (at == 0 || a.q_start[lo + at] <= t));
             const int hit = 31 - __clz(below);  // lane 0 always is
             lo += hit * step;
             count = min(step, count - hit * step);
         }
-        b = lo;
-        n = a.q_start[b + 1] - a.q_start[b];
-        i = t - a.q_start[b];
+        const int mine = lo + min(lane, count - 1);
+        const int s0 = a.q_start[mine], s1 = a.q_start[mine + 1], len = a.seq_lens[mine];
+        const unsigned below = __ballot_sync(0xffffffffu, lane < count && (lane == 0 || s0 <= t));
+        const int hit = 31 - __clz(below);
+        b = lo + hit;
+        const int start = __shfl_sync(0xffffffffu, s0, hit);
+        n = __shfl_sync(0xffffffffu, s1, hit) - start;
+        L = __shfl_sync(0xffffffffu, len, hit);
+        i = t - start;
+        p.live = t < tend;
+    } else {
+        L = a.seq_lens[b];
     }
-    const int L = a.seq_lens[b];
     if (i < 0 || i >= n || L < n || static_cast<long long>(L) > static_cast<long long>(a.max_blocks) * a.BS) return p;
     p.ok = 1;
     p.pos = L - n + i;
-    p.slot = p.pos % a.BS;
-    const int blk = a.block_tables[static_cast<size_t>(b) * a.max_blocks + p.pos / a.BS];
-    p.blk = blk >= 0 && blk < a.NB ? blk : -1;
+    const int lb = static_cast<int>(static_cast<unsigned>(p.pos) / static_cast<unsigned>(a.BS));
+    p.slot = p.pos - lb * a.BS;
+    p.blk_raw = a.block_tables[static_cast<size_t>(b) * a.max_blocks + lb];
     return p;
+}
+
+// Asks for the token-independent inputs of the kernels below before the predecessor ends.
+__device__ __forceinline__ void write_prefetch(const WriteArgs& a) {
+    const unsigned worker = (blockIdx.x * gridDim.y + blockIdx.y) * blockDim.x + threadIdx.x;
+    prefetch_l2(a.seq_lens, static_cast<size_t>(a.B) * 4, worker);
+    prefetch_l2(a.block_tables, static_cast<size_t>(a.B) * a.max_blocks * 4, worker);
+    if (a.q_start != nullptr) prefetch_l2(a.q_start, static_cast<size_t>(a.B + 1) * 4, worker);
+    if (a.half > 0) prefetch_l2(a.freqs, static_cast<size_t>(a.half) * 8, worker);
 }
 
 // cos and sin of pos * freq (turns in units of 2^-64, whole turns wrap away).
@@ -110,15 +130,17 @@ __device__ __forceinline__ float2 turn_of(int pos, int64_t freq) {
 // T: element type of the rows; Fmt: the 8-bit format, or FmtNone for a cache of T.
 template <typename T, typename Fmt>
 __global__ void __launch_bounds__(kWriteWarps * 32) kv_write_any_kernel(const WriteArgs a) {
+    write_prefetch(a);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kPer = kWriteMaxD / 32;
     __shared__ float2 turn[kWriteMaxD / 2];
     __shared__ float rowbuf[kWriteWarps][kWriteMaxD];
     const int t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (a.q_start != nullptr && t >= a.q_start[a.B]) return;  // rows behind the last sequence stay as they are
     const Place p = place_of(a, t);
-    if ((!p.ok || p.blk < 0) && threadIdx.x == 0 && blockIdx.y == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
+    if (!p.live) return;  // rows behind the last sequence stay as they are
+    const int blk = p.blk(a.NB);
+    if (blk < 0 && threadIdx.x == 0 && blockIdx.y == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
     for (int j = threadIdx.x; j < a.half; j += blockDim.x) turn[j] = turn_of(p.pos, a.freqs[j]);
     __syncthreads();
     const int rows = a.Hq + 2 * a.Hkv;
@@ -129,7 +151,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv_write_any_kernel(const Wr
                        : is_v ? static_cast<const T*>(a.v) + t * a.v_stride
                               : static_cast<const T*>(a.k) + t * a.k_stride;
         src += static_cast<size_t>(h) * a.D;
-        if (!is_q && p.blk < 0) continue;
+        if (!is_q && blk < 0) continue;
         float x[kPer];
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
@@ -173,7 +195,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv_write_any_kernel(const Wr
             }
             continue;
         }
-        const size_t row = (static_cast<size_t>(p.blk) * a.Hkv + h) * a.BS + p.slot;
+        const size_t row = (static_cast<size_t>(blk) * a.Hkv + h) * a.BS + p.slot;
         if constexpr (Fmt::kQuant) {
             float amax = 0.f;
             bool finite = true;
@@ -299,6 +321,7 @@ __device__ __forceinline__ V row_reduce(V x, const WritePlan& w, int l, int base
 template <typename T, typename Fmt, int kRot>
 __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 ? 2 : 3)
     kv_write_kernel(const __grid_constant__ WriteArgs a, const __grid_constant__ WritePlan w) {
+    write_prefetch(a);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     constexpr int kAhead = 2;  // passes in flight per warp and kind
@@ -337,13 +360,13 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
     for (int k = 0; k < kAhead; ++k) load(raw[k], qp, first + k * stride, a.Hq);
     load(rawk, kp, k0, a.Hkv);
     load(rawv, vp, v0, a.Hkv);
-    const bool active = t < a.T && (a.q_start == nullptr || t < a.q_start[a.B]);  // rows behind the last sequence stay
     // norm weights and frequencies do not wait for the token's place either
     Runs<T> wq, wk;
     if (a.q_weight != nullptr) wq = load_runs(static_cast<const T*>(a.q_weight) + at0, gap);
     if (a.k_weight != nullptr) wk = load_runs(static_cast<const T*>(a.k_weight) + at0, gap);
-    Place p{0, 0, -1, 0};
-    if (active) p = place_of(a, t);
+    Place p{0, 0, 0, 0, -1};
+    if (t < a.T) p = place_of(a, t);
+    const bool active = p.live;  // the rows behind the last sequence stay
     // cosines and sines: of the run's 4 pairs (kRot 1, 3), or of the 8 elements, the sine with
     // the sign it enters with (kRot 2)
     float2 cs[kRot == 2 ? 4 : 2], sn[kRot == 2 ? 4 : 2];
@@ -371,7 +394,6 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
         }
     }
     if (!active) return;
-    if ((!p.ok || p.blk < 0) && first == 0 && lane == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
 
     auto norm = [&](float2 (&x)[4], const float2 (&g)[4]) {
         float2 s2 = mul2(x[0], x[0]);
@@ -422,10 +444,11 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
             }
         }
     };
-    const size_t slot0 = static_cast<size_t>(max(p.blk, 0)) * a.Hkv * a.BS + p.slot;  // row of KV head 0
+    int blk = -1;      // set after the queries
+    size_t slot0 = 0;  // cache row of KV head 0
     // a key or value row into the cache
     auto put = [&](float2 (&x)[4], const Runs<T>& now, int h, void* cache, float* scales, bool is_v) {
-        const bool mine = in && h < a.Hkv && p.blk >= 0;
+        const bool mine = in && h < a.Hkv && blk >= 0;
         const size_t row = slot0 + static_cast<size_t>(h) * a.BS;
         if constexpr (Fmt::kQuant) {
             // the largest |x| as an integer: infinities and NaN are above every finite number
@@ -485,6 +508,9 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
             }
         }
     }
+    blk = p.blk(a.NB);
+    slot0 = static_cast<size_t>(max(blk, 0)) * a.Hkv * a.BS + p.slot;
+    if (blk < 0 && first == 0 && lane == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
     {  // keys
         float2 g[4];
         if (a.k_weight != nullptr) to_floats(wk, g);
