@@ -22,7 +22,8 @@
 // holds the partners of the first (half a multiple of 4; else they come through
 // shared memory).  The first rows are loaded before the token's place and angles
 // are known, which hides that chain of loads, and later ones kAhead passes early.
-// Queries, keys and values have a loop each.  The other kernel (any D and alignment) gives a warp one row, one element
+// Two rows per lane are in work at once, two queries or a key and a value, which overlaps
+// their reductions' shuffles; head sizes 64 and 128 have those lanes as constants.  The other kernel (any D and alignment) gives a warp one row, one element
 // per lane and step.
 #include <type_traits>
 
@@ -32,7 +33,7 @@ namespace pkv {
 
 constexpr int kWriteWarps = 8;
 constexpr int kWriteMaxD = 256;
-constexpr int kPassesPerWarp = 12;  // of one token, where there are enough tokens
+constexpr int kPairsPerWarp = 8;  // pairs of passes of one token, where there are enough tokens
 
 int device_sm_count();
 
@@ -295,71 +296,72 @@ struct WritePlan {
     int qpasses, kvpasses;  // passes over a token's query rows, and over its key (or value) rows
     float inv_d;
     int magic;       // lane / lanes = lane * magic >> 16
-    int pow2;        // lanes is a power of two
     int wpt_log2;    // warps per token
 };
 
-// op over the lanes of a row (l: this lane's index among them, base: their first lane).
-template <typename V, typename Op>
-__device__ __forceinline__ V row_reduce(V x, const WritePlan& w, int l, int base, Op op) {
-    if (w.pow2) {
+// op over the lanes of a row, for two rows at once (their shuffles overlap).  kLanes: lanes a
+// row where that is a power of two, else 0 (l: this lane's index among w.lanes, base: their
+// first lane).
+template <int kLanes, typename V, typename Op>
+__device__ __forceinline__ void row_reduce(V (&x)[2], const WritePlan& w, int l, int base, Op op) {
+    if constexpr (kLanes > 0) {
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) x[k] = op(x[k], __shfl_xor_sync(0xffffffffu, x[k], o));
+    } else {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
-            if (o < w.lanes) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
-        return x;
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const V y = __shfl_down_sync(0xffffffffu, x, o);
-        if (l + o < w.lanes) x = op(x, y);
+            for (int k = 0; k < 2; ++k) {
+                const V y = __shfl_down_sync(0xffffffffu, x[k], o);
+                if (l + o < w.lanes) x[k] = op(x[k], y);
+            }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) x[k] = __shfl_sync(0xffffffffu, x[k], base);
     }
-    return __shfl_sync(0xffffffffu, x, base);
 }
 
 // kRot: 0 no rotation, 1 pairs (j, j + half) with half a multiple of 4, 2 such pairs
 // with any half, 3 pairs (2j, 2j + 1).
-template <typename T, typename Fmt, int kRot>
+template <typename T, typename Fmt, int kRot, int kLanes>
 __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 ? 2 : 3)
     kv_write_kernel(const __grid_constant__ WriteArgs a, const __grid_constant__ WritePlan w) {
     write_prefetch(a);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kAhead = 2;  // passes in flight per warp and kind
     constexpr int kPad = kWriteMaxD + kWriteMaxD / 8;
     constexpr int kTable = kWriteMaxD / 2;
-    enum { kQ, kK, kV };
     __shared__ float rowbuf[kRot == 2 ? kWriteWarps : 1][kRot == 2 ? 2 * kPad : 1];
     __shared__ __align__(16) float2 turn[kRot == 0 ? 1 : kWriteWarps * kTable];  // [token of the CTA][pair]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wpt = 1 << w.wpt_log2, tok = warp >> w.wpt_log2;
     const int t = (blockIdx.x << (3 - w.wpt_log2)) + tok;
-    const int sub = (lane * w.magic) >> 16, base = sub * w.lanes, l = lane - base;
+    const int lanes = kLanes > 0 ? kLanes : w.lanes, per = kLanes > 0 ? 32 / kLanes : w.per;
+    const int sub = kLanes > 0 ? lane / kLanes : (lane * w.magic) >> 16, base = sub * lanes, l = lane - base;
     // the lane's elements: at0 .. at0 + 3 and at0 + gap .. + 3; with kRot 1 the second run
     // holds the partners of the first, so that no element has to travel
     const bool turns = kRot == 1 && 4 * l < a.half;
     const int at0 = turns ? 4 * l : 8 * l, gap = turns ? a.half : 4;
-    const bool in = t < a.T && sub < w.per;
-    // passes first, first + stride, .. of the queries', then the keys', then the values' passes
+    const bool in = t < a.T && sub < per;
+    // this warp's passes: first, first + stride, .. of the queries', two at a time, then of the
+    // keys' with the values' beside them
     const int stride = wpt * gridDim.y, first = blockIdx.y * wpt + (warp & (wpt - 1));
     const int qpass = w.qpasses, kvpass = w.kvpasses;
-    auto head_of = [&](int pass) { return pass * w.per + sub; };
-    auto begin_of = [&](int done) {  // this warp's first pass of a kind that follows `done` passes
-        const int x = (first - done) % stride;
-        return x < 0 ? x + stride : x;
-    };
-    const int k0 = begin_of(qpass), v0 = begin_of(qpass + kvpass);
+    int kv0 = (first - qpass) % stride;
+    if (kv0 < 0) kv0 += stride;
     const T* qp = static_cast<const T*>(a.q) + t * a.q_stride + at0;
     const T* kp = static_cast<const T*>(a.k) + t * a.k_stride + at0;
     const T* vp = static_cast<const T*>(a.v) + t * a.v_stride + at0;
     auto load = [&](Runs<T>& to, const T* src, int pass, int heads) {
-        const int h = head_of(pass);
+        const int h = pass * per + sub;
         if (in && h < heads) to = load_runs(src + h * a.D, gap);
     };
-    Runs<T> raw[kAhead], rawk, rawv;
+    Runs<T> raw[2], rawkv[2];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) load(raw[k], qp, first + k * stride, a.Hq);
-    load(rawk, kp, k0, a.Hkv);
-    load(rawv, vp, v0, a.Hkv);
+    for (int k = 0; k < 2; ++k) load(raw[k], qp, first + k * stride, a.Hq);
+    load(rawkv[0], kp, kv0, a.Hkv);
+    load(rawkv[1], vp, kv0, a.Hkv);
     // norm weights and frequencies do not wait for the token's place either
     Runs<T> wq, wk;
     if (a.q_weight != nullptr) wq = load_runs(static_cast<const T*>(a.q_weight) + at0, gap);
@@ -395,15 +397,18 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
     }
     if (!active) return;
 
-    auto norm = [&](float2 (&x)[4], const float2 (&g)[4]) {
+    auto square = [](const float2 (&x)[4]) {
         float2 s2 = mul2(x[0], x[0]);
 #pragma unroll
         for (int e = 1; e < 4; ++e) s2 = fma2(x[e], x[e], s2);
-        const float ss = row_reduce(s2.x + s2.y, w, l, base, [](float u, float v) { return u + v; });
+        return s2.x + s2.y;
+    };
+    auto scaled = [&](float2 (&x)[4], float ss, const float2 (&g)[4]) {
         const float inv = rsqrtf(fmaf(ss, w.inv_d, a.eps));
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = mul2(mul2(x[e], make_float2(inv, inv)), g[e]);
     };
+    auto sum = [](float u, float v) { return u + v; };
     auto rotate = [&](float2 (&x)[4]) {
         if constexpr (kRot == 1) {
             if (turns) {
@@ -426,12 +431,12 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
             float* buf = rowbuf[warp];
             const int at = sub * (a.D + a.D / 8);
             __syncwarp();
-            if (sub < w.per) {
+            if (sub < per) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) buf[at + 9 * l + e] = e & 1 ? x[e >> 1].y : x[e >> 1].x;
             }
             __syncwarp();
-            if (sub < w.per) {
+            if (sub < per) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int i = 8 * l + e, q = i < a.half ? i + a.half : i - a.half;
@@ -444,91 +449,92 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
             }
         }
     };
-    int blk = -1;      // set after the queries
-    size_t slot0 = 0;  // cache row of KV head 0
-    // a key or value row into the cache
-    auto put = [&](float2 (&x)[4], const Runs<T>& now, int h, void* cache, float* scales, bool is_v) {
-        const bool mine = in && h < a.Hkv && blk >= 0;
-        const size_t row = slot0 + static_cast<size_t>(h) * a.BS;
-        if constexpr (Fmt::kQuant) {
-            // the largest |x| as an integer: infinities and NaN are above every finite number
-            uint32_t top = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                top = max(top, max(__float_as_uint(x[e].x) & 0x7fffffffu, __float_as_uint(x[e].y) & 0x7fffffffu));
-            top = row_reduce(top, w, l, base, [](uint32_t u, uint32_t v) { return max(u, v); });
-            const bool finite = top < 0x7f800000u;
-            const float scale = row_scale(__uint_as_float(top), Fmt::kInvQ);
-            const float inv = __frcp_rn(scale);
-            if (mine) {
-                uint32_t v0 = 0, v1 = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], make_float2(inv, inv));
-                if (finite) {
-                    v0 = Fmt::encode4(&x[0].x);
-                    v1 = Fmt::encode4(&x[2].x);
-                }
-                uint8_t* dst = static_cast<uint8_t*>(cache) + row * a.D + at0;
-                *reinterpret_cast<uint32_t*>(dst) = v0;
-                *reinterpret_cast<uint32_t*>(dst + gap) = v1;
-                if (l == 0) {
-                    scales[row] = finite ? scale : __int_as_float(0x7fffffff);
-                    if (!finite) report(a.status, PKV_ERR_NONFINITE);
-                }
-            }
-        } else if (mine) {
-            T* dst = static_cast<T*>(cache) + row * a.D + at0;
-            if (is_v) {  // the bits as they are
-                using V = std::remove_const_t<std::remove_reference_t<decltype(now.v[0])>>;
-                *reinterpret_cast<V*>(dst) = now.v[0];
-                *reinterpret_cast<V*>(dst + gap) = now.v[1];
-            } else {
-                store_runs(dst, gap, x);
-            }
-        }
-    };
-
     {  // queries
         float2 g[4];
         if (a.q_weight != nullptr) to_floats(wq, g);
         T* qo = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.Hq * a.D + at0;
-        for (int p0 = first; p0 < qpass; p0 += kAhead * stride) {
+        for (int pass = first; pass < qpass; pass += 2 * stride) {
+            float2 x[2][4];
+            float ss[2];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int pass = p0 + k * stride;
-                if (pass >= qpass) break;
-                float2 x[4];
-                to_floats(raw[k], x);
-                load(raw[k], qp, pass + kAhead * stride, a.Hq);
-                if (a.q_weight != nullptr) norm(x, g);
-                rotate(x);
-                if (!p.ok) x[0] = x[1] = x[2] = x[3] = make_float2(0.f, 0.f);
-                const int h = head_of(pass);
-                if (in && h < a.Hq) store_runs(qo + h * a.D, gap, x);
+            for (int k = 0; k < 2; ++k) {
+                to_floats(raw[k], x[k]);
+                load(raw[k], qp, pass + (2 + k) * stride, a.Hq);
+                ss[k] = square(x[k]);
+            }
+            if (a.q_weight != nullptr) {
+                row_reduce<kLanes>(ss, w, l, base, sum);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) scaled(x[k], ss[k], g);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                rotate(x[k]);
+                if (!p.ok) x[k][0] = x[k][1] = x[k][2] = x[k][3] = make_float2(0.f, 0.f);
+                const int h = (pass + k * stride) * per + sub;
+                if (in && h < a.Hq) store_runs(qo + h * a.D, gap, x[k]);
             }
         }
     }
-    blk = p.blk(a.NB);
-    slot0 = static_cast<size_t>(max(blk, 0)) * a.Hkv * a.BS + p.slot;
+    const int blk = p.blk(a.NB);
+    const size_t slot0 = static_cast<size_t>(max(blk, 0)) * a.Hkv * a.BS + p.slot;  // cache row of KV head 0
     if (blk < 0 && first == 0 && lane == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
-    {  // keys
-        float2 g[4];
-        if (a.k_weight != nullptr) to_floats(wk, g);
-        for (int pass = k0; pass < kvpass; pass += stride) {
-            float2 x[4];
-            to_floats(rawk, x);
-            load(rawk, kp, pass + stride, a.Hkv);
-            if (a.k_weight != nullptr) norm(x, g);
-            rotate(x);
-            put(x, rawk, head_of(pass), a.k_cache, a.k_scale, false);
+    float2 g[4];
+    if (a.k_weight != nullptr) to_floats(wk, g);
+    for (int pass = kv0; pass < kvpass; pass += stride) {  // x[0]: a key row, x[1]: the value row
+        float2 x[2][4];
+        const Runs<T> vnow = rawkv[1];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) to_floats(rawkv[k], x[k]);
+        load(rawkv[0], kp, pass + stride, a.Hkv);
+        load(rawkv[1], vp, pass + stride, a.Hkv);
+        if (a.k_weight != nullptr) {
+            float ss[2] = {square(x[0]), 0.f};
+            row_reduce<kLanes>(ss, w, l, base, sum);
+            scaled(x[0], ss[0], g);
         }
-    }
-    for (int pass = v0; pass < kvpass; pass += stride) {
-        float2 x[4];
-        const Runs<T> now = rawv;
-        to_floats(now, x);
-        load(rawv, vp, pass + stride, a.Hkv);
-        put(x, now, head_of(pass), a.v_cache, a.v_scale, true);
+        rotate(x[0]);
+        const int h = pass * per + sub;
+        const bool mine = in && h < a.Hkv && blk >= 0;
+        const size_t row = slot0 + static_cast<size_t>(h) * a.BS, at = row * a.D + at0;
+        if constexpr (Fmt::kQuant) {
+            // the largest |x| as an integer: infinities and NaN are above every finite number
+            uint32_t top[2] = {0u, 0u};
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    top[k] = max(top[k], max(__float_as_uint(x[k][e].x) & 0x7fffffffu, __float_as_uint(x[k][e].y) & 0x7fffffffu));
+            row_reduce<kLanes>(top, w, l, base, [](uint32_t u, uint32_t v) { return max(u, v); });
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const bool finite = top[k] < 0x7f800000u;
+                const float scale = row_scale(__uint_as_float(top[k]), Fmt::kInvQ);
+                const float inv = __frcp_rn(scale);
+                uint32_t v0 = 0, v1 = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[k][e] = mul2(x[k][e], make_float2(inv, inv));
+                if (finite) {
+                    v0 = Fmt::encode4(&x[k][0].x);
+                    v1 = Fmt::encode4(&x[k][2].x);
+                }
+                if (mine) {
+                    uint8_t* dst = static_cast<uint8_t*>(k ? a.v_cache : a.k_cache) + at;
+                    *reinterpret_cast<uint32_t*>(dst) = v0;
+                    *reinterpret_cast<uint32_t*>(dst + gap) = v1;
+                    if (l == 0) {
+                        (k ? a.v_scale : a.k_scale)[row] = finite ? scale : __int_as_float(0x7fffffff);
+                        if (!finite) report(a.status, PKV_ERR_NONFINITE);
+                    }
+                }
+            }
+        } else if (mine) {
+            store_runs(static_cast<T*>(a.k_cache) + at, gap, x[0]);
+            T* dst = static_cast<T*>(a.v_cache) + at;  // the bits as they are
+            using V = std::remove_const_t<std::remove_reference_t<decltype(vnow.v[0])>>;
+            *reinterpret_cast<V*>(dst) = vnow.v[0];
+            *reinterpret_cast<V*>(dst + gap) = vnow.v[1];
+        }
     }
 }
 
@@ -556,27 +562,32 @@ static cudaError_t launch_typed(const WriteArgs& a, cudaStream_t stream) {
         w.lanes = a.D / 8;
         w.per = 32 / w.lanes;
         w.magic = 65536 / w.lanes + 1;  // exact for lane < 32, lanes <= 32
-        w.pow2 = (w.lanes & (w.lanes - 1)) == 0;
         w.qpasses = (a.Hq + w.per - 1) / w.per;
         w.kvpasses = (a.Hkv + w.per - 1) / w.per;
         w.inv_d = 1.0f / static_cast<float>(a.D);
-        const int passes = w.qpasses + 2 * w.kvpasses;
+        const int passes = (w.qpasses + 1) / 2 + w.kvpasses;  // pairs of passes
         // many tokens: a warp takes many passes of one token, which shares the token's place,
         // angles and weights; few: a token's passes over as many warps and CTAs as there are
         w.wpt_log2 = 3;
         int split = 1;
-        while (w.wpt_log2 > 0 && passes < kPassesPerWarp << w.wpt_log2 &&
-               (static_cast<long long>(a.T) << w.wpt_log2) >= 2LL * 24 * sms)
+        while (w.wpt_log2 > 0 && passes < kPairsPerWarp << w.wpt_log2 &&
+               (static_cast<long long>(a.T) << w.wpt_log2) >= 12LL * sms)
             --w.wpt_log2;
         if (w.wpt_log2 == 3)
-            while (split * kWriteWarps < passes && static_cast<long long>(a.T) * split < 2LL * sms) ++split;
+            while (split * kWriteWarps < w.qpasses + w.kvpasses && static_cast<long long>(a.T) * split < 2LL * sms) ++split;
         const int tpc = kWriteWarps >> w.wpt_log2;
         cfg.gridDim = dim3(static_cast<unsigned>((a.T + tpc - 1) / tpc), static_cast<unsigned>(split), 1);
         const int rot = a.half == 0 ? 0 : a.interleaved ? 3 : a.half % 4 == 0 ? 1 : 2;
-        auto kern = rot == 0   ? kv_write_kernel<T, Fmt, 0>
-                    : rot == 1 ? kv_write_kernel<T, Fmt, 1>
-                    : rot == 2 ? kv_write_kernel<T, Fmt, 2>
-                               : kv_write_kernel<T, Fmt, 3>;
+        auto pick = [&](auto lanes) {
+            constexpr int kLanes = decltype(lanes)::value;
+            if (rot == 0) return kv_write_kernel<T, Fmt, 0, kLanes>;
+            if (rot == 1) return kv_write_kernel<T, Fmt, 1, kLanes>;
+            return kv_write_kernel<T, Fmt, 3, kLanes>;
+        };
+        auto kern = rot == 2         ? kv_write_kernel<T, Fmt, 2, 0>
+                    : w.lanes == 16 ? pick(std::integral_constant<int, 16>())
+                    : w.lanes == 8  ? pick(std::integral_constant<int, 8>())
+                                    : pick(std::integral_constant<int, 0>());
         err = cudaLaunchKernelEx(&cfg, kern, a, w);
     } else {
         // few tokens: a token's rows over several CTAs

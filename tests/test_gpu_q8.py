@@ -56,6 +56,9 @@ APPENDS = [  # (Hkv, D, BS, lens, counts or None for one token each)
     (2, 256, 48, [100, 49], [60, 49]),
     (12, 16, 64, [64, 65], None),
     (3, 36, 16, [30, 20], [7, 20]),
+    # many tokens: several of them a CTA
+    (2, 64, 16, [700, 31], [700, 0]),
+    (3, 128, 32, [900, 40, 77], [650, 33, 77]),
 ]
 
 
@@ -333,6 +336,12 @@ PREPARE = [  # (Hq, Hkv, D, BS, rot, interleaved, norms, lens, counts)
     (2, 1, 5, 3, 4, True, True, [7, 8], None),
     (1, 1, 2, 1, 2, False, True, [3], [3]),
     (16, 4, 112, 16, 26, False, True, [300, 1], [150, 1]),
+    # many tokens: several of them a CTA
+    (8, 2, 64, 16, 64, False, True, [800, 300], [640, 77]),
+    (3, 1, 128, 16, 128, True, True, [700], [700]),
+    (6, 3, 128, 32, 40, False, False, [650, 90, 5], [650, 33, 5]),
+    (2, 2, 64, 16, 0, False, True, [100620, 44], [620, 2]),
+    (5, 5, 64, 16, 22, True, True, [700, 9], [610, 9]),
 ]
 
 
@@ -433,6 +442,39 @@ def test_norm_rope_append_in_place_and_rows_behind_the_last_sequence():
     same = pkv.qk_norm_rope_append(gq, gk, gv, *args, k2, v2, bt.cuda(), i32(lens).cuda(), q_start=qs, q_out=gq)
     assert same is gq and torch.equal(gq[:9], want[:9]) and torch.equal(gq[9:].cpu(), q[9:])
     assert torch.equal(k1, k2) and torch.equal(v1, v2)
+
+
+def test_many_tokens_in_place_with_rows_behind_and_bad_sequences():
+    """Several tokens a CTA: 40 sequences, some of them bad, and rows that belong to none."""
+    Hq, Hkv, D, BS = 4, 2, 128, 16
+    g = torch.Generator().manual_seed(33)
+    counts = [(7 * b) % 41 for b in range(40)]
+    lens = [n + 3 * b for b, n in enumerate(counts)]
+    bt, nb = R.tables(lens, BS, g)
+    T = sum(counts) + 5
+    assert T > 700
+    bad_len, bad_blk = 11, 23
+    lens[bad_len] = counts[bad_len] - 1
+    bt[bad_blk, (lens[bad_blk] - 1) // BS] = nb
+    qs = torch.zeros(41, dtype=torch.int32)
+    qs[1:] = torch.cumsum(i32(counts), 0)
+    q, k, v = (torch.randn(T, h, D, generator=g).bfloat16() for h in (Hq, Hkv, Hkv))
+    pool = torch.zeros(nb, Hkv, BS, D).bfloat16()
+    gq, gk, gv, kc, vc = cuda(q, k, v, pool, pool)
+    st = pkv.new_status()
+    out = pkv.qk_norm_rope_append(gq, gk, gv, None, None, 0.0, None, kc, vc, bt.cuda(), i32(lens).cuda(),
+                                  q_start=qs.cuda(), q_out=gq, status=st)
+    assert pkv.check_status(st) == 4 and out is gq
+    want = q.clone()
+    want[qs[bad_len]:qs[bad_len + 1]] = 0
+    assert torch.equal(gq.cpu(), want)
+    wk, wv = pool.clone(), pool.clone()
+    for b, n in enumerate(counts):
+        for i in range(n):
+            pos, t = lens[b] - n + i, int(qs[b]) + i
+            if b != bad_len and int(bt[b, pos // BS]) < nb:
+                wk[int(bt[b, pos // BS]), :, pos % BS], wv[int(bt[b, pos // BS]), :, pos % BS] = k[t], v[t]
+    assert torch.equal(kc.cpu(), wk) and torch.equal(vc.cpu(), wv)
 
 
 def test_norm_rope_append_bad_sequences():
