@@ -95,7 +95,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     tmp = CALLS + f".tmp{os.getpid()}"
     torch_lib = os.path.join(torch_root, "lib")
     cmd = ["g++", "-shared", "-o", tmp, calls_obj, f"-L{HERE}", "-l:libpkv.so", "-Wl,-rpath,$ORIGIN", f"-L{torch_lib}",
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{torch_lib}"]
+           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{torch_lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

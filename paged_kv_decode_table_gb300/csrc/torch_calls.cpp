@@ -11,8 +11,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -107,6 +106,11 @@ void* stream_of(at::DeviceIndex dev) { return c10::cuda::getCurrentCUDAStream(de
 
 PyObject* code(long c) { return PyLong_FromLong(c); }
 
+// A new tensor beside `like` (on its device, which is current).
+Tensor fresh(at::IntArrayRef shape, ScalarType type, const Tensor* like) {
+    return at::detail::empty_cuda(shape, type, like->device(), std::nullopt);
+}
+
 // append(k_new, v_new, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, q_start, status)
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -152,9 +156,8 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!float_code(type, &dtype) || !optional(a[5], type, c.dev, shape) || !optional(a[6], type, c.dev, shape))
         return code(-1);
     const c10::cuda::OptionalCUDAGuard guard(c.k->device());
-    const auto options = c.k->options().dtype(type);
-    const Tensor ko = a[5] != Py_None ? THPVariable_Unpack(a[5]) : at::empty(shape, options);
-    const Tensor vo = a[6] != Py_None ? THPVariable_Unpack(a[6]) : at::empty(shape, options);
+    const Tensor ko = a[5] != Py_None ? THPVariable_Unpack(a[5]) : fresh(shape, type, c.k);
+    const Tensor vo = a[6] != Py_None ? THPVariable_Unpack(a[6]) : fresh(shape, type, c.k);
     const pkv_status r = pkv_kv_read_blocks_q8(
         ko.data_ptr(), vo.data_ptr(), c.k->data_ptr(), c.v->data_ptr(), c.ks, c.vs, ids->data_ptr<int32_t>(),
         static_cast<int>(ids->size(0)), c.Hkv, c.D, c.BS, c.NB, dtype, c.code, pointer<int32_t>(a[8]), stream_of(c.dev));
@@ -185,12 +188,12 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[9] != Py_None && (!(ws = tensor(a[9])) || !is(ws, ws->scalar_type(), c.dev))) return code(-1);
     const c10::cuda::OptionalCUDAGuard guard(c.k->device());
     const int Hq = static_cast<int>(q->size(1));
-    Tensor out = a[7] != Py_None ? THPVariable_Unpack(a[7]) : at::empty(q->sizes(), q->options());
+    Tensor out = a[7] != Py_None ? THPVariable_Unpack(a[7]) : fresh(q->sizes(), q->scalar_type(), q);
     Tensor own;
     size_t bytes;
     if (!ws) {
         bytes = pkv_decode_q8_workspace_bytes(s.B, Hq, c.Hkv, c.D, 0);
-        own = at::empty({static_cast<int64_t>(bytes < 16 ? 16 : bytes)}, q->options().dtype(ScalarType::Byte));
+        own = fresh({static_cast<int64_t>(bytes < 16 ? 16 : bytes)}, ScalarType::Byte, q);
         ws = &own;
     } else {
         bytes = ws->nbytes();
@@ -238,7 +241,7 @@ PyObject* prepare(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int interleaved = PyObject_IsTrue(a[14]);
     if (interleaved < 0) return nullptr;
     const c10::cuda::OptionalCUDAGuard guard(c.k->device());
-    Tensor out = a[15] != Py_None ? THPVariable_Unpack(a[15]) : at::empty(q->sizes(), q->options());
+    Tensor out = a[15] != Py_None ? THPVariable_Unpack(a[15]) : fresh(q->sizes(), type, q);
     const pkv_status r = pkv_qk_norm_rope_append(
         out.data_ptr(), q->data_ptr(), qs, pointer<>(a[1]), ks, pointer<>(a[2]), vs, pointer<>(a[3]), pointer<>(a[4]),
         static_cast<float>(eps), freqs ? freqs->data_ptr<int64_t>() : nullptr,
