@@ -66,7 +66,7 @@ constexpr int kQ8MaxStages = 12;
 constexpr int kQ8Tok = 16;  // positions per tile
 constexpr int kQ8Warps = 8;  // consumer warps at most
 constexpr int kQ8Sub = 2;    // tiles a warp takes of one step
-constexpr long long kDirectBytes = 256 << 10;  // a CTA's share up to which no split is worth a join
+constexpr int kDirectSteps = 3;  // steps of a sequence up to which a join is not worth it
 constexpr float kLag = 8.f;  // contributions stay below 2^8 of the running maximum
 
 // How a call is laid out; computed on the host, passed to both kernels.
@@ -1015,8 +1015,9 @@ struct Q8Layout {  // workspace
     size_t o, total;
 };
 
-// Group size and slots for a shape; false where the fast kernel does not apply.
-static bool q8_shape(int Hq, int Hkv, int D, int BS, pkv_dtype dt, Q8Plan& pl) {
+// Group size and slots for a shape, with at least min_groups head groups where the heads
+// allow it; false where the fast kernel does not apply.
+static bool q8_shape(int Hq, int Hkv, int D, int BS, pkv_dtype dt, int min_groups, Q8Plan& pl) {
     if (D % 16 != 0 || D > 128 || BS % 16 != 0) return false;
     const int G = Hq / Hkv, rows = dt == PKV_F32 || G <= 8 ? 8 : 16;  // query heads per warp
     pl.QC = (G + rows - 1) / rows;
@@ -1024,7 +1025,7 @@ static bool q8_shape(int Hq, int Hkv, int D, int BS, pkv_dtype dt, Q8Plan& pl) {
     // as few groups as the warps allow, of equal size (the last one up to NG - 1 heads
     // smaller: 11 heads are 6 + 5; the tile of the missing head is read and not used)
     const int most = kQ8Warps / pl.QC;
-    pl.NG = (Hkv + most - 1) / most;
+    pl.NG = std::max((Hkv + most - 1) / most, std::min(min_groups, Hkv));
     pl.HG = (Hkv + pl.NG - 1) / pl.NG;
     pl.NG = (Hkv + pl.HG - 1) / pl.HG;
     pl.UB = BS / kQ8Tok;
@@ -1102,11 +1103,9 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
         if (dev < 64) raised.fetch_or(1ull << dev);
     }
     cudaLaunchConfig_t cfg = {};
-    // Short sequences (by the table's width) and few of them: one CTA each, so that no
-    // join is launched.
     const int step_tok = pl.slots * kQ8Sub * kQ8Tok;
     const long long most = (static_cast<long long>(pl.max_blocks) * pl.BS + step_tok - 1) / step_tok;
-    pl.direct = static_cast<long long>(pl.B) * pl.NG <= P && most * static_cast<long long>(per) <= kDirectBytes;
+    if (pl.direct && most > kDirectSteps) return cudaSuccess;
     cfg.gridDim = dim3(static_cast<unsigned>(pl.direct ? pl.B * pl.NG : P), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>((pl.HG * pl.QC * pl.slots + 1) * 32), 1, 1);
     cfg.dynamicSmemBytes = smem;
@@ -1151,10 +1150,23 @@ static cudaError_t launch_q8(Q8Plan pl, bool fast, void* out, const void* q, con
         using I2 = std::integral_constant<int, 2>;
         using I64 = std::integral_constant<int, 64>;
         using I128 = std::integral_constant<int, 128>;
-        if constexpr (sizeof(T) == 2) {
-            if (pl.G > 8) err = pl.D <= 64 ? run(I64(), I2()) : run(I128(), I2());
+        auto go = [&]() {
+            if constexpr (sizeof(T) == 2) {
+                if (pl.G > 8) return pl.D <= 64 ? run(I64(), I2()) : run(I128(), I2());
+            }
+            return pl.D <= 64 ? run(I64(), I1()) : run(I128(), I1());
+        };
+        // Few and short sequences (by the table's width): a CTA for each (sequence, head
+        // group) and no join, with as many groups as there are SMs for.
+        const Q8Plan split = pl;
+        pl.direct = pl.B <= P && q8_shape(pl.Hq, pl.Hkv, pl.D, pl.BS, sizeof(T) == 4 ? PKV_F32 : PKV_BF16, P / pl.B, pl) &&
+                    pl.B * pl.NG <= P;
+        if (pl.direct) {
+            err = go();
+            if (err != cudaSuccess || done) return err;
         }
-        if (sizeof(T) == 4 || pl.G <= 8) err = pl.D <= 64 ? run(I64(), I1()) : run(I128(), I1());
+        pl = split;
+        err = go();
         if (err != cudaSuccess || done) return err;
     }
     cudaLaunchConfig_t cfg = {};
@@ -1185,7 +1197,7 @@ extern "C" size_t pkv_decode_q8_workspace_bytes(int B, int Hq, int Hkv, int D, i
     size_t need = 256;
     for (pkv_dtype dt : {PKV_F32, PKV_BF16}) {
         Q8Plan pl = {};
-        if (q8_shape(Hq, Hkv, D, 16, dt, pl)) need = std::max(need, q8_layout(pl.R, D, P).total);
+        if (q8_shape(Hq, Hkv, D, 16, dt, 1, pl)) need = std::max(need, q8_layout(pl.R, D, P).total);
     }
     return need;
 }
@@ -1210,7 +1222,7 @@ extern "C" pkv_status pkv_paged_decode_attention_q8(
     if (P <= 0) return PKV_ERR_CUDA;
     if (scale <= 0.f) scale = 1.0f / sqrtf(static_cast<float>(D));
     Q8Plan pl = {};
-    bool fast = q8_shape(Hq, Hkv, D, block_size, dtype, pl);
+    bool fast = q8_shape(Hq, Hkv, D, block_size, dtype, 1, pl);
     pl.G = Hq / Hkv;
     pl.B = B;
     pl.Hq = Hq;

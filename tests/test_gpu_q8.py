@@ -204,6 +204,10 @@ ATTENTION = [  # (Hq, Hkv, D, BS, lens)
     (10, 5, 192, 32, [65]),
     (3, 1, 1, 1, [5, 2]),
     (130, 1, 64, 16, [40, 300]),
+    (32, 8, 128, 16, [(13 * b) % 90 for b in range(40)]),  # 3 + 3 + 2 KV heads a CTA
+    (10, 5, 64, 32, [(5 * b) % 64 for b in range(150)]),
+    (9, 9, 128, 16, [1000, 33]),                           # two groups, the second smaller, split
+    (60, 5, 112, 16, [1000, 170, 0, 33]),
 ]
 
 
