@@ -481,7 +481,7 @@ pkv_status pkv_paged_decode_attention_q8(void* out, const void* q, const void* k
  *     t = 2 pi pos freqs[j] 2^-64, j < rot_dim / 2, (a, c) = (j, j + rot_dim / 2)
  *     or, with interleaved != 0, (2j, 2j + 1); elements from rot_dim on stay.
  * The query rows go to q_out [T_new, Hq, D] (which may be q itself when q is
- * dense), the key and value rows into the cache: as they are when cache_dtype
+ * dense, and otherwise overlaps none of the inputs), the key and value rows into the cache: as they are when cache_dtype
  * == dtype (k_scale and v_scale ignored), quantised when it is PKV_E4M3 or
  * PKV_I8.  Everything is float32 between one load and one rounding.
  * freqs: device int64 [rot_dim / 2], turns per position as 64-bit fractions of a

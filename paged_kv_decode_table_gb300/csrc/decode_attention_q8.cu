@@ -38,14 +38,13 @@
 //    whatever the V scales are.  Scales below 2^-64 count as 2^-64 there, which
 //    bounds p_j by 2^72.  The maximum is renewed (shuffles, rescaled sums) only
 //    when a contribution exceeds it by 2^kLag: a vote decides.
-//  * q is multiplied by a power of two that puts the warp's largest element into
+//  * q is multiplied by a power of two per head that puts its largest element into
 //    [2^14, 2^15).
 // Other shapes: one CTA per (sequence, query head), CUDA-core fp32.
 #include <cuda.h>
 #include <math.h>
 
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "quant8.cuh"
@@ -439,7 +438,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     float O[kChunks][kN][4];
     uint32_t qb[kN][kChunks][2];
     [[maybe_unused]] uint32_t ql[kSplit ? kN : 1][kSplit ? kChunks : 1][2];
-    float smul = 0.f;
+    float smul[kN][2];  // what a score of heads 8 n + 2 r + e is multiplied by
     float m[kN][2], mu[kN][2], l[kN][2];  // of heads 8 n + 2 r + e; mu: m, or 0 where m is -inf
     bool poisoned = false;
     int piece = 0, stage = 0;
@@ -502,14 +501,14 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const bool in = !kPart || k * kQ8Tok + 8 * t + g < ntok;
-                const float kk = ks[8 * t + g] * smul, vv = vs[8 * t + g];
+                const float kk = ks[8 * t + g], vv = vs[8 * t + g];
                 const float lg = lg2f(fmaxf(fabsf(vv), kMinScale));
                 vsc[k][t] = in ? vv : 0.f;
 #pragma unroll
                 for (int n = 0; n < kN; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float a = (s[n][0][2 * t + e] + s[n][1][2 * t + e]) * kk;
+                        const float a = (s[n][0][2 * t + e] + s[n][1][2 * t + e]) * (kk * smul[n][e]);
                         x[k][n][2 * t + e] = in ? a : -INFINITY;
                         tmax[n][e] = fmaxf(tmax[n][e], in ? a + lg : -INFINITY);
                     }
@@ -629,41 +628,41 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             const uint8_t* qsm = qring + static_cast<size_t>(qs) * pl.q_bytes + hh * pl.G * pl.q_stride;
             // (none for the heads that a last, smaller group lacks)
             const int qrows = (mt.vb % NG) * HG + hh < pl.Hkv ? pl.G : 0;
-            float v[kN][kChunks][4], amax = 0.f;
 #pragma unroll
             for (int n = 0; n < kN; ++n) {
                 const int row = qc * kHeads + 8 * n + g;
+                float v[kChunks][4], amax = 0.f;
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
                     const int d = c * 16 + 4 * r;
                     float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (row < qrows && d < pl.D) z = load_row4(reinterpret_cast<const T*>(qsm + row * pl.q_stride) + d);
-                    v[n][c][0] = z.x;
-                    v[n][c][1] = z.y;
-                    v[n][c][2] = z.z;
-                    v[n][c][3] = z.w;
+                    v[c][0] = z.x;
+                    v[c][1] = z.y;
+                    v[c][2] = z.z;
+                    v[c][3] = z.w;
                     amax = fmaxf(amax, fmaxf(fmaxf(fabsf(z.x), fabsf(z.y)), fmaxf(fabsf(z.z), fabsf(z.w))));
                 }
-            }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                // amax in [2^(ex-127), 2^(ex-126)) -> [2^14, 2^15); not below 2^-100, infinite: 255
+                const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23), 27);
+                const float fac = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
+                const float mul = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23) * pl.scale_log2;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            // amax in [2^(ex-127), 2^(ex-126)) -> [2^14, 2^15); not below 2^-100, infinite: 255
-            const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23), 27);
-            const float fac = __uint_as_float(static_cast<uint32_t>(268 - ex) << 23);
-            smul = __uint_as_float(static_cast<uint32_t>(ex - 14) << 23) * pl.scale_log2;
-#pragma unroll
-            for (int n = 0; n < kN; ++n)
+                for (int e = 0; e < 2; ++e) smul[n][e] = __shfl_sync(0xffffffffu, mul, 4 * (2 * r + e));
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c)
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        const float a = v[n][c][2 * p] * fac, b = v[n][c][2 * p + 1] * fac;
+                        const float a = v[c][2 * p] * fac, b = v[c][2 * p + 1] * fac;
                         qb[n][c][p] = pack_f16x2(a, b);
                         if constexpr (kSplit) {
                             const float2 f = unpack_f16x2(qb[n][c][p]);
                             ql[n][c][p] = pack_f16x2(a - f.x, b - f.y);
                         }
                     }
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&qempty[qs]);
             poisoned = false;
@@ -1092,16 +1091,8 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     float* part_ml = reinterpret_cast<float*>(ws);
     float* part_o = reinterpret_cast<float*>(ws + wl.o);
     auto kern = decode_q8_kernel<T, Fmt, DP, kN, kSplit>;
-    // the kernel's limit is raised to the device's once per device
-    static std::atomic<uint64_t> raised{0};
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
-    if (dev >= 64 || !(raised.load() >> dev & 1)) {
-        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(budget));
-        if (err != cudaSuccess) return err;
-        if (dev < 64) raised.fetch_or(1ull << dev);
-    }
     cudaLaunchConfig_t cfg = {};
     const int step_tok = pl.slots * kQ8Sub * kQ8Tok;
     const long long most = (static_cast<long long>(pl.max_blocks) * pl.BS + step_tok - 1) / step_tok;

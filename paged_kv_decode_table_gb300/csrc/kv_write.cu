@@ -623,7 +623,8 @@ extern "C" pkv_status pkv_kv_append_q8(const void* k_new, const void* v_new, voi
                                        int T_new, int Hkv, int D, int block_size, int num_blocks, pkv_dtype dtype,
                                        pkv_dtype cache_dtype, int32_t* dev_status, void* stream) {
     if (B < 0 || T_new < 0 || Hkv < 1 || D < 1 || D > pkv::kWriteMaxD || block_size < 1 || num_blocks < 1 ||
-        max_blocks_per_seq < 1 || !plain(dtype) || !is8(cache_dtype) || (!q_start && T_new != B))
+        max_blocks_per_seq < 1 || !plain(dtype) || !is8(cache_dtype) || (!q_start && T_new != B) ||
+        static_cast<long long>(Hkv) * D > 0x7fffffffLL)
         return PKV_ERR_INVALID_ARG;
     if (B == 0 || T_new == 0) return PKV_OK;
     if (!k_new || !v_new || !k_cache || !v_cache || !k_scale || !v_scale || !block_tables || !seq_lens)
@@ -661,7 +662,8 @@ extern "C" pkv_status pkv_qk_norm_rope_append(
         (!q_start && T_new != B) || rot_dim < 0 || rot_dim > D || rot_dim % 2 != 0 || !(eps >= 0.f))
         return PKV_ERR_INVALID_ARG;
     const long long qrow = static_cast<long long>(Hq) * D, kvrow = static_cast<long long>(Hkv) * D;
-    if (q_stride < qrow || k_stride < kvrow || v_stride < kvrow) return PKV_ERR_INVALID_ARG;
+    if (q_stride < qrow || k_stride < kvrow || v_stride < kvrow || qrow > 0x7fffffffLL || kvrow > 0x7fffffffLL)
+        return PKV_ERR_INVALID_ARG;
     if (B == 0 || T_new == 0) return PKV_OK;
     if (!q_out || !q || !k_new || !v_new || !k_cache || !v_cache || !block_tables || !seq_lens ||
         (rot_dim > 0 && !freqs) || (is8(cache_dtype) && (!k_scale || !v_scale)))

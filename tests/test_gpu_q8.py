@@ -298,6 +298,57 @@ def test_attention_over_a_row_with_nan_is_nan():
     assert bool(torch.isnan(out[0]).all()) and bool(torch.isfinite(out[1]).all())
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (24, 2)])
+def test_a_head_of_q_is_alone_with_its_infinities_and_its_size(Hq, Hkv):
+    """Heads of one group share a warp: one with an infinity, one with NaN and one of
+    1e30 leave the others' results as they are."""
+    lens = [300, 40]
+    g = torch.Generator().manual_seed(61)
+    bt, nb = R.tables(lens, 16, g)
+    k, v, ks, vs = R.random_cache(nb, Hkv, 16, 64, "i8", g)
+    q = torch.randn(2, Hq, 64, generator=g).bfloat16()
+    ref, tol = R.attention(q, k, v, ks, vs, bt, lens, dtype="bf16")
+    bad = q.clone()
+    bad[0, 1, 5], bad[0, 3, 7], bad[1, 2] = math.inf, math.nan, 1e30
+    out = pkv.paged_decode_attention_q8(*cuda(bad, k, v, ks, vs, bt, i32(lens))).cpu().double()
+    hit = torch.zeros(2, Hq, dtype=torch.bool)
+    hit[0, 1] = hit[0, 3] = hit[1, 2] = True
+    assert bool(((out - ref).abs() <= tol)[~hit].all())
+    assert bool(torch.isnan(out[0, 1]).all()) and bool(torch.isnan(out[0, 3]).all())
+
+
+def test_addresses_that_are_not_16_byte_aligned():
+    """Every call on tensors that begin one element into their storage."""
+    def shifted(t):
+        flat = torch.zeros(t.numel() + 1, dtype=torch.uint8 if t.element_size() == 1 else t.dtype, device="cuda")
+        out = flat[1:].view(t.dtype).view(t.shape)
+        out.copy_(t.cuda())
+        assert out.is_contiguous() and out.data_ptr() % 16
+        return out
+
+    Hq, Hkv, D, BS, lens = 8, 2, 64, 16, [70, 33, 1]
+    g = torch.Generator().manual_seed(62)
+    bt, nb = R.tables(lens, BS, g)
+    k, v, ks, vs = R.random_cache(nb, Hkv, BS, D, "e4m3", g)
+    q, kn, vn = (torch.randn(3, h, D, generator=g).bfloat16() for h in (Hq, Hkv, Hkv))
+    odd = [shifted(t) for t in (q, k, v, ks, vs)]
+    gbt, sl = bt.cuda(), i32(lens).cuda()
+    out = pkv.paged_decode_attention_q8(*odd, gbt, sl, out=shifted(torch.zeros_like(q)))
+    ref, tol = R.attention(q, k, v, ks, vs, bt, lens, dtype="bf16")
+    assert bool(((out.cpu().double() - ref).abs() <= tol).all())
+    w = (1 + 0.1 * torch.randn(D, generator=g)).bfloat16()
+    even = cuda(k.clone(), v.clone(), ks.clone(), vs.clone())
+    freqs = pkv.rope_freqs(D)
+    q1 = pkv.qk_norm_rope_append(shifted(q), shifted(kn), shifted(vn), shifted(w), shifted(w), 1e-6, freqs, *odd[1:3],
+                                 gbt, sl, k_scale=odd[3], v_scale=odd[4])
+    q2 = pkv.qk_norm_rope_append(*cuda(q, kn, vn, w, w), 1e-6, freqs, *even[:2], gbt, sl, k_scale=even[2],
+                                 v_scale=even[3])
+    # two kernels whose sums are grouped differently: a bf16 step, a float32 half-step of the scale
+    assert bool(((q1.float() - q2.float()).abs() <= 2.0 ** -7 * q2.float().abs() + 1e-6).all())
+    assert torch.equal(odd[2].view(torch.uint8), even[1].view(torch.uint8)) and torch.equal(odd[4], even[3])
+    assert bool(((odd[3] - even[2]).abs() <= 2.0 ** -20 * even[2]).all())
+
+
 def test_attention_beyond_32_bit_offsets():
     """Pools of more than 2^31 bytes, read at their far end, and an append there."""
     Hkv, D, BS, lens = 8, 128, 16, [50, 33]
