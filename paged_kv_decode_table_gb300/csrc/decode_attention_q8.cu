@@ -64,7 +64,6 @@ int attention_silent_cta();
 constexpr int kQ8MaxStages = 12;
 constexpr int kQ8Tok = 16;  // positions per tile
 constexpr int kQ8Warps = 8;  // consumer warps at most
-constexpr int kQ8Sub = 2;    // tiles a warp takes of one step
 constexpr int kDirectSteps = 3;  // steps of a sequence up to which a join is not worth it
 constexpr float kLag = 8.f;  // contributions stay below 2^8 of the running maximum
 
@@ -72,7 +71,7 @@ constexpr float kLag = 8.f;  // contributions stay below 2^8 of the running maxi
 struct Q8Plan {
     int HG, NG;      // KV heads per group, groups (the last one may have fewer heads)
     int QC;          // chunks of query heads per KV head (8 or 16 heads each)
-    int slots;       // tiles along the cache per step
+    int slots, sub;  // a step is slots x sub tiles along the cache, sub of them a warp's
     int R;           // query rows per group: HG * G
     int UB;          // units of 16 positions per block
     int nst;         // ring stages
@@ -145,7 +144,7 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 
 // Steps of sequence b in one head group (0 for a length outside [0, max_blocks * BS]).
 __device__ __forceinline__ int q8_steps(const int32_t* seq_lens, int b, const Q8Plan& pl) {
-    const int L = seq_lens[b], T = pl.slots * kQ8Sub * kQ8Tok;
+    const int L = seq_lens[b], T = pl.slots * pl.sub * kQ8Tok;
     return (L >= 0 && static_cast<long long>(L) <= static_cast<long long>(pl.max_blocks) * pl.BS)
                ? static_cast<int>((static_cast<long long>(L) + T - 1) / T)
                : 0;
@@ -187,7 +186,7 @@ __device__ __forceinline__ uint32_t q8_at(int tok, int c, int pack) {
 }
 
 // kN: n-tiles of 8 query heads per warp; kSplit: float32 accuracy (see above).
-template <typename T, typename Fmt, int DP, int kN, bool kSplit>
+template <typename T, typename Fmt, int DP, int kN, bool kSplit, int kSub>
 __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ Q8Plan pl, const T* __restrict__ q, T* __restrict__ out,
@@ -200,7 +199,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int nst = pl.nst, HG = pl.HG, QC = pl.QC, slots = pl.slots;
     const int HV = HG * QC, CW = HV * slots;
-    const int units = slots * kQ8Sub;  // 16-position units per step
+    const int units = slots * kSub;  // 16-position units per step
     const int tile_bytes = kQ8Tok * DP, unit_bytes = HG * tile_bytes, half_stage = units * unit_bytes;
     const int scale_half = units * pl.scale_unit;
     uint8_t* scales = smem + static_cast<size_t>(nst) * pl.stage_bytes;
@@ -295,7 +294,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
 
     if (warp == CW) {
         // ------------------------------------------------ producer warp
-        // Lane u fetches the K and V tiles of unit u (slot u / kQ8Sub) by TMA; the
+        // Lane u fetches the K and V tiles of unit u (slot u % slots) by TMA; the
         // scales, 64 bytes per unit and head, come by 16-byte cp.async of the whole warp
         // (a TMA copy of 64 bytes costs as much issue time as one of 16 KB).  The
         // block ids are read two steps ahead.
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
         if (start + 1 < end) nxt = fetch(start + 1);
         // this lane's chunks of the scales: (unit, head, quarter) of chunk lane + 32 x
         const int chunks = units * HG * 4;
-        constexpr int kScaleChunks = kQ8Warps * kQ8Sub * 4 / 32;
+        constexpr int kScaleChunks = kQ8Warps * kSub * 4 / 32;
         int su[kScaleChunks], srow[kScaleChunks], sq[kScaleChunks];
 #pragma unroll
         for (int x = 0; x < kScaleChunks; ++x) {
@@ -444,29 +443,37 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     int piece = 0, stage = 0;
     uint32_t parity = 0;
     const uint32_t smem_base = smem_u32(smem);
-    const int tile_off = (slot * kQ8Sub * HG + hh) * tile_bytes;
-    const int scale_off = slot * kQ8Sub * pl.scale_unit + hh * (kQ8Tok * 4);
+    // this warp's tile k of a step is unit k * slots + slot
+    const int tile_off = (slot * HG + hh) * tile_bytes, tile_next = slots * unit_bytes;
+    const int scale_off = slot * pl.scale_unit + hh * (kQ8Tok * 4), scale_next = slots * pl.scale_unit;
+    const int tok_next = slots * kQ8Tok;
     // ldmatrix: lane group mi gives the rows of matrix mi: (positions 8 (mi & 1) ..,
     // chunk + (mi >> 1))
     uint32_t lm[kChunks / 2];
 #pragma unroll
     for (int c = 0; c < kChunks / 2; ++c) lm[c] = q8_at<DP>((mi & 1) * 8 + rr, 2 * c + (mi >> 1), pl.pack);
 
-    // One step's kQ8Sub tiles; kPart: some of their positions lie behind the end.
+    // One step's kSub tiles; kPart: some of their positions lie behind the end.
     auto tiles = [&](auto part, int ntok) {
         constexpr bool kPart = decltype(part)::value;
         const uint32_t kb0 = smem_base + static_cast<uint32_t>(stage) * pl.stage_bytes + tile_off;
         const uint8_t* sc0 = scales + static_cast<size_t>(stage) * 2 * scale_half + scale_off;
-        float x[kQ8Sub][kN][4];  // scores of position g (+ 8 for 2, 3), heads 2r, 2r + 1
-        float vsc[kQ8Sub][2];
+        float x[kSub][kN][4];  // scores of position g (+ 8 for 2, 3), heads 2r, 2r + 1
+        float vsc[kSub][2];
         bool over = false;
         float tmax[kN][2];
 #pragma unroll
         for (int n = 0; n < kN; ++n) tmax[n][0] = tmax[n][1] = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < kQ8Sub; ++k) {
+        for (int k = 0; k < kSub; ++k) {
+            if (kPart && k * tok_next >= ntok) {  // no such tile
+                vsc[k][0] = vsc[k][1] = 0.f;
+#pragma unroll
+                for (int n = 0; n < kN; ++n) x[k][n][0] = x[k][n][1] = x[k][n][2] = x[k][n][3] = -INFINITY;
+                continue;
+            }
             // ---- S^T = K Q^T, in two independent chains
-            const uint32_t kb = kb0 + k * unit_bytes;
+            const uint32_t kb = kb0 + k * tile_next;
             float s[kN][2][4];
 #pragma unroll
             for (int n = 0; n < kN; ++n)
@@ -496,11 +503,11 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 }
             }
             // ---- scaled scores, and the largest contribution s_j + log2(vs_j)
-            const float* ks = reinterpret_cast<const float*>(sc0 + k * pl.scale_unit);
-            const float* vs = reinterpret_cast<const float*>(sc0 + k * pl.scale_unit + scale_half);
+            const float* ks = reinterpret_cast<const float*>(sc0 + k * scale_next);
+            const float* vs = reinterpret_cast<const float*>(sc0 + k * scale_next + scale_half);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const bool in = !kPart || k * kQ8Tok + 8 * t + g < ntok;
+                const bool in = !kPart || k * tok_next + 8 * t + g < ntok;
                 const float kk = ks[8 * t + g], vv = vs[8 * t + g];
                 const float lg = lg2f(fmaxf(fabsf(vv), kMinScale));
                 vsc[k][t] = in ? vv : 0.f;
@@ -552,8 +559,8 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 for (int n = 0; n < kN; ++n) F[c][n][0] = F[c][n][1] = F[c][n][2] = F[c][n][3] = 0.f;
         }
 #pragma unroll
-        for (int k = 0; k < kQ8Sub; ++k) {
-            if (kPart && k * kQ8Tok >= ntok) break;
+        for (int k = 0; k < kSub; ++k) {
+            if (kPart && k * tok_next >= ntok) break;
             // ---- weights, float16, in P^T's layout
             uint32_t pb[kN][2];
             [[maybe_unused]] uint32_t pl2[kSplit ? kN : 1][2];
@@ -574,10 +581,10 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 }
             // ---- O^T += V^T P^T.  Positions behind the end have weight 0; their bytes
             // are cleared because an e4m3 NaN would survive the product.
-            const uint32_t vb = kb0 + half_stage + k * unit_bytes;
+            const uint32_t vb = kb0 + half_stage + k * tile_next;
             uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
             if (kPart) {
-                const int left = ntok - k * kQ8Tok - 2 * r;
+                const int left = ntok - k * tok_next - 2 * r;
                 keep0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
                 keep1 = (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
             }
@@ -677,10 +684,10 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 for (int c = 0; c < kChunks; ++c) O[c][n][0] = O[c][n][1] = O[c][n][2] = O[c][n][3] = 0.f;
             }
         }
-        const int ntok = mt.left - slot * (kQ8Sub * kQ8Tok);  // positions from this warp's first one to the end
+        const int ntok = mt.left - slot * kQ8Tok;  // positions from this warp's first one to the end
         poisoned = poisoned || (mt.flags & kQBad);
         if (!poisoned) {
-            if (ntok >= kQ8Sub * kQ8Tok)
+            if (ntok >= (kSub - 1) * tok_next + kQ8Tok)
                 tiles(std::false_type(), ntok);
             else if (ntok > 0)
                 tiles(std::true_type(), ntok);
@@ -1029,6 +1036,7 @@ static bool q8_shape(int Hq, int Hkv, int D, int BS, pkv_dtype dt, int min_group
     pl.NG = (Hkv + pl.HG - 1) / pl.HG;
     pl.UB = BS / kQ8Tok;
     pl.pack = D == 64;
+    pl.sub = D <= 64 ? 4 : 2;  // steps of about 64 KB
     pl.slots = 1;
     while (pl.slots * 2 * pl.HG * pl.QC <= kQ8Warps) pl.slots *= 2;
     pl.G = G;
@@ -1068,7 +1076,8 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
                                   void* workspace, int P, int32_t* status, cudaStream_t stream, bool* done) {
     *done = false;
     constexpr bool kSplit = sizeof(T) == 4;
-    const int tiles = pl.HG * pl.slots * kQ8Sub;
+    constexpr int kSub = DP == 64 ? 4 : 2;
+    const int tiles = pl.HG * pl.slots * kSub;
     pl.stage_bytes = 2 * tiles * kQ8Tok * DP;
     pl.scale_unit = pl.HG * kQ8Tok * 4;
     // rows 32 (bf16) or 64 bytes apart modulo 128, so that the 8 heads a warp reads at
@@ -1079,7 +1088,7 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     const size_t fixed = 1024 + 2 * static_cast<size_t>(pl.q_bytes) + pl.scratch_bytes +
                          (2 * kQ8MaxStages + 4 + 2 * kQ8Warps) * sizeof(uint64_t) + kQ8MaxStages * sizeof(Q8Meta) +
                          40 * sizeof(int) + 16;
-    const size_t per = pl.stage_bytes + 2 * static_cast<size_t>(pl.slots) * kQ8Sub * pl.scale_unit;
+    const size_t per = pl.stage_bytes + 2 * static_cast<size_t>(pl.slots) * kSub * pl.scale_unit;
     const size_t budget = static_cast<size_t>(max_optin_smem());
     if (fixed + 2 * per > budget) return cudaSuccess;
     pl.nst = static_cast<int>(std::min<size_t>(kQ8MaxStages, (budget - fixed) / per));
@@ -1090,11 +1099,11 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     float* part_ml = reinterpret_cast<float*>(ws);
     float* part_o = reinterpret_cast<float*>(ws + wl.o);
-    auto kern = decode_q8_kernel<T, Fmt, DP, kN, kSplit>;
+    auto kern = decode_q8_kernel<T, Fmt, DP, kN, kSplit, kSub>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    const int step_tok = pl.slots * kQ8Sub * kQ8Tok;
+    const int step_tok = pl.slots * kSub * kQ8Tok;
     const long long most = (static_cast<long long>(pl.max_blocks) * pl.BS + step_tok - 1) / step_tok;
     if (pl.direct && most > kDirectSteps) return cudaSuccess;
     cfg.gridDim = dim3(static_cast<unsigned>(pl.direct ? pl.B * pl.NG : P), 1, 1);
