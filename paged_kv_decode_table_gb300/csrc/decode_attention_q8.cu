@@ -181,11 +181,11 @@ __device__ __forceinline__ uint32_t q8_at(int tok, int c, int pack) {
         c += (tok & 1) * 4;
         tok >>= 1;
     }
-    if (DP == 128 || pack) return static_cast<uint32_t>(tok * 128 + ((c ^ (tok & 7)) << 4));
+    if (DP > 64 || pack) return static_cast<uint32_t>(tok * 128 + ((c ^ (tok & 7)) << 4));
     return static_cast<uint32_t>(tok * 64 + ((c ^ ((tok >> 1) & 3)) << 4));
 }
 
-// kN: n-tiles of 8 query heads per warp; kSplit: float32 accuracy (see above).
+// DP: dimensions computed (64, 96 or 128; D may be smaller); kN: n-tiles of 8 query heads per warp; kSplit: float32 accuracy (see above).
 template <typename T, typename Fmt, int DP, int kN, bool kSplit, int kSub>
 __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -194,13 +194,13 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                      const int32_t* __restrict__ block_tables, const int32_t* __restrict__ seq_lens,
                      float* __restrict__ part_ml, float* __restrict__ part_o,
                      int32_t* status) {
-    constexpr int kChunks = DP / 16;
+    constexpr int kChunks = DP / 16, kPitch = DP == 64 ? 64 : 128;  // bytes of a tile's row
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int nst = pl.nst, HG = pl.HG, QC = pl.QC, slots = pl.slots;
     const int HV = HG * QC, CW = HV * slots;
     const int units = slots * kSub;  // 16-position units per step
-    const int tile_bytes = kQ8Tok * DP, unit_bytes = HG * tile_bytes, half_stage = units * unit_bytes;
+    const int tile_bytes = kQ8Tok * kPitch, unit_bytes = HG * tile_bytes, half_stage = units * unit_bytes;
     const int scale_half = units * pl.scale_unit;
     uint8_t* scales = smem + static_cast<size_t>(nst) * pl.stage_bytes;
     uint8_t* qring = scales + static_cast<size_t>(nst) * 2 * scale_half;
@@ -1053,9 +1053,9 @@ static Q8Layout q8_layout(int R, int D, int P) {
     return w;
 }
 
-// A pool [NB * Hkv][BS][D] of bytes in boxes of 16 positions x HG heads x DP bytes
+// A pool [NB * Hkv][BS][D] of bytes in boxes of 16 positions x HG heads x `pitch` bytes
 // (bytes beyond D arrive as zeros).
-static bool q8_map(CUtensorMap* map, const void* pool, const Q8Plan& pl, int DP) {
+static bool q8_map(CUtensorMap* map, const void* pool, const Q8Plan& pl, int pitch) {
     EncodeTiledFn enc = get_encode_fn();
     if (!enc) return false;
     const cuuint64_t heads = static_cast<cuuint64_t>(pl.NB) * pl.Hkv;
@@ -1063,10 +1063,10 @@ static bool q8_map(CUtensorMap* map, const void* pool, const Q8Plan& pl, int DP)
     const int pack = pl.pack;  // 128-byte rows of two positions
     cuuint64_t dim[3] = {static_cast<cuuint64_t>(pl.D) << pack, static_cast<cuuint64_t>(pl.BS) >> pack, heads};
     cuuint64_t stride[2] = {static_cast<cuuint64_t>(pl.D) << pack, static_cast<cuuint64_t>(pl.D) * pl.BS};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(DP) << pack, static_cast<cuuint32_t>(kQ8Tok) >> pack,
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(pitch) << pack, static_cast<cuuint32_t>(kQ8Tok) >> pack,
                          static_cast<cuuint32_t>(pl.HG)};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dim, stride, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, DP == 128 || pack ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, pitch == 128 || pack ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1076,9 +1076,9 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
                                   void* workspace, int P, int32_t* status, cudaStream_t stream, bool* done) {
     *done = false;
     constexpr bool kSplit = sizeof(T) == 4;
-    constexpr int kSub = DP == 64 ? 4 : 2;
+    constexpr int kSub = DP == 64 ? 4 : 2, kPitch = DP == 64 ? 64 : 128;
     const int tiles = pl.HG * pl.slots * kSub;
-    pl.stage_bytes = 2 * tiles * kQ8Tok * DP;
+    pl.stage_bytes = 2 * tiles * kQ8Tok * kPitch;
     pl.scale_unit = pl.HG * kQ8Tok * 4;
     // rows 32 (bf16) or 64 bytes apart modulo 128, so that the 8 heads a warp reads at
     // once fall on different banks
@@ -1094,7 +1094,7 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     pl.nst = static_cast<int>(std::min<size_t>(kQ8MaxStages, (budget - fixed) / per));
     const size_t smem = fixed + pl.nst * per;
     CUtensorMap tmK, tmV;
-    if (!q8_map(&tmK, k, pl, DP) || !q8_map(&tmV, v, pl, DP)) return cudaSuccess;
+    if (!q8_map(&tmK, k, pl, kPitch) || !q8_map(&tmV, v, pl, kPitch)) return cudaSuccess;
     const Q8Layout wl = q8_layout(pl.R, pl.D, P);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     float* part_ml = reinterpret_cast<float*>(ws);
@@ -1149,12 +1149,14 @@ static cudaError_t launch_q8(Q8Plan pl, bool fast, void* out, const void* q, con
         using I1 = std::integral_constant<int, 1>;
         using I2 = std::integral_constant<int, 2>;
         using I64 = std::integral_constant<int, 64>;
+        using I96 = std::integral_constant<int, 96>;
         using I128 = std::integral_constant<int, 128>;
         auto go = [&]() {
             if constexpr (sizeof(T) == 2) {
-                if (pl.G > 8) return pl.D <= 64 ? run(I64(), I2()) : run(I128(), I2());
+                if (pl.G > 8)
+                    return pl.D <= 64 ? run(I64(), I2()) : pl.D <= 96 ? run(I96(), I2()) : run(I128(), I2());
             }
-            return pl.D <= 64 ? run(I64(), I1()) : run(I128(), I1());
+            return pl.D <= 64 ? run(I64(), I1()) : pl.D <= 96 ? run(I96(), I1()) : run(I128(), I1());
         };
         // Few and short sequences (by the table's width): a CTA for each (sequence, head
         // group) and no join, with as many groups as there are SMs for.
