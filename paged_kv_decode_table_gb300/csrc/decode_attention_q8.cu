@@ -78,12 +78,19 @@ struct Q8Plan {
     int stage_bytes, scale_unit, q_bytes, scratch_bytes;
     int q_stride;    // bytes between q's rows in shared memory
     int direct;      // one CTA per (sequence, group), no join
-    int pack;        // D = 64: two positions per 128-byte row of a tile
+    int layout;      // of a tile in shared memory: kSwizzled, kPacked or kDense
+    int tok_shift;   // log2 of the positions per row of the tensor map
     int B, Hq, Hkv, G, D, BS, NB, max_blocks;
     float scale_log2;
     uint32_t polls;
     int silent_cta;
 };
+
+// D = 128: rows of 128 bytes, one per position, 128-byte swizzle.  D = 64: two positions
+// per such row.  Other D: rows of D bytes one behind the other (copied as one run per
+// head, because the TMA takes as long for a row of 80 bytes as for two of 128); ldmatrix
+// reads them without bank conflicts where D / 16 is odd, with two-way ones at 32 and 96.
+enum : int { kSwizzled, kPacked, kDense };
 
 struct Q8Meta {
     int vb;     // sequence * NG + group
@@ -172,17 +179,14 @@ __device__ __forceinline__ int q8_scan(int v, int* red, int& total) {
     return before + x - v;
 }
 
-// Byte offset of 16-byte chunk c of position `tok` in a TMA-swizzled tile: rows of 128
-// bytes (128-byte swizzle), rows of 64 (64-byte swizzle), or with pack rows of 128
-// bytes that hold two positions.
-template <int DP>
-__device__ __forceinline__ uint32_t q8_at(int tok, int c, int pack) {
-    if (DP == 64 && pack) {
+// Byte offset of 16-byte chunk c of position `tok` in a tile.
+__device__ __forceinline__ uint32_t q8_at(int tok, int c, const Q8Plan& pl) {
+    if (pl.layout == kDense) return static_cast<uint32_t>(tok * pl.D + c * 16);
+    if (pl.layout == kPacked) {
         c += (tok & 1) * 4;
         tok >>= 1;
     }
-    if (DP > 64 || pack) return static_cast<uint32_t>(tok * 128 + ((c ^ (tok & 7)) << 4));
-    return static_cast<uint32_t>(tok * 64 + ((c ^ ((tok >> 1) & 3)) << 4));
+    return static_cast<uint32_t>(tok * 128 + ((c ^ (tok & 7)) << 4));
 }
 
 // DP: dimensions computed (64, 96 or 128; D may be smaller); kN: n-tiles of 8 query heads per warp; kSplit: float32 accuracy (see above).
@@ -194,13 +198,16 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                      const int32_t* __restrict__ block_tables, const int32_t* __restrict__ seq_lens,
                      float* __restrict__ part_ml, float* __restrict__ part_o,
                      int32_t* status) {
-    constexpr int kChunks = DP / 16, kPitch = DP == 64 ? 64 : 128;  // bytes of a tile's row
+    constexpr int kChunks = DP / 16;
+    // chunks from here on may lie behind D: a K byte there is the next row's, and an e4m3 NaN
+    // survives the product with q's zero
+    constexpr int kMaybe = !Fmt::kHasNaN ? kChunks : DP == 64 ? 1 : kChunks - 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int nst = pl.nst, HG = pl.HG, QC = pl.QC, slots = pl.slots;
     const int HV = HG * QC, CW = HV * slots;
     const int units = slots * kSub;  // 16-position units per step
-    const int tile_bytes = kQ8Tok * kPitch, unit_bytes = HG * tile_bytes, half_stage = units * unit_bytes;
+    const int tile_bytes = kQ8Tok * pl.D, unit_bytes = HG * tile_bytes, half_stage = units * unit_bytes;
     const int scale_half = units * pl.scale_unit;
     uint8_t* scales = smem + static_cast<size_t>(nst) * pl.stage_bytes;
     uint8_t* qring = scales + static_cast<size_t>(nst) * 2 * scale_half;
@@ -384,8 +391,8 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             const int row = s.blk * pl.Hkv + s.g * HG;
             if (good) {
                 uint8_t* kd = smem + static_cast<size_t>(stage) * pl.stage_bytes + lane * unit_bytes;
-                tma_load_3d(kd, &tmK, 0, s.tok >> pl.pack, row, &full[stage]);
-                tma_load_3d(kd + half_stage, &tmV, 0, s.tok >> pl.pack, row, &full[stage]);
+                tma_load_3d(kd, &tmK, 0, s.tok >> pl.tok_shift, row, &full[stage]);
+                tma_load_3d(kd + half_stage, &tmV, 0, s.tok >> pl.tok_shift, row, &full[stage]);
             }
             if (first) {
                 const int qs = piece & 1;
@@ -451,7 +458,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     // chunk + (mi >> 1))
     uint32_t lm[kChunks / 2];
 #pragma unroll
-    for (int c = 0; c < kChunks / 2; ++c) lm[c] = q8_at<DP>((mi & 1) * 8 + rr, 2 * c + (mi >> 1), pl.pack);
+    for (int c = 0; c < kChunks / 2; ++c) lm[c] = q8_at((mi & 1) * 8 + rr, 2 * c + (mi >> 1), pl);
 
     // One step's kSub tiles; kPart: some of their positions lie behind the end.
     auto tiles = [&](auto part, int ntok) {
@@ -485,6 +492,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 ldmatrix_x4(w[0], w[1], w[2], w[3], kb + lm[c / 2]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
+                    if (c + u >= kMaybe && 16 * (c + u) >= pl.D) break;
                     uint32_t a[4];
                     Fmt::decode4(w[2 * u], a[0], a[2]);
                     Fmt::decode4(w[2 * u + 1], a[1], a[3]);
@@ -1035,7 +1043,8 @@ static bool q8_shape(int Hq, int Hkv, int D, int BS, pkv_dtype dt, int min_group
     pl.HG = (Hkv + pl.NG - 1) / pl.NG;
     pl.NG = (Hkv + pl.HG - 1) / pl.HG;
     pl.UB = BS / kQ8Tok;
-    pl.pack = D == 64;
+    pl.layout = D == 128 ? kSwizzled : D == 64 ? kPacked : kDense;
+    pl.tok_shift = D == 128 ? 0 : D == 64 ? 1 : 4;
     pl.sub = D <= 64 ? 4 : 2;  // steps of about 64 KB
     pl.slots = 1;
     while (pl.slots * 2 * pl.HG * pl.QC <= kQ8Warps) pl.slots *= 2;
@@ -1053,21 +1062,23 @@ static Q8Layout q8_layout(int R, int D, int P) {
     return w;
 }
 
-// A pool [NB * Hkv][BS][D] of bytes in boxes of 16 positions x HG heads x `pitch` bytes
-// (bytes beyond D arrive as zeros).
-static bool q8_map(CUtensorMap* map, const void* pool, const Q8Plan& pl, int pitch) {
+// A pool [NB * Hkv][BS][D] of bytes in boxes of 16 positions x HG heads, the positions in
+// rows of 2^tok_shift (128-byte rows, or for kDense one row of 16 D bytes a head).
+static bool q8_map(CUtensorMap* map, const void* pool, const Q8Plan& pl) {
     EncodeTiledFn enc = get_encode_fn();
     if (!enc) return false;
-    const cuuint64_t heads = static_cast<cuuint64_t>(pl.NB) * pl.Hkv;
-    cuuint32_t one[3] = {1, 1, 1};
-    const int pack = pl.pack;  // 128-byte rows of two positions
-    cuuint64_t dim[3] = {static_cast<cuuint64_t>(pl.D) << pack, static_cast<cuuint64_t>(pl.BS) >> pack, heads};
-    cuuint64_t stride[2] = {static_cast<cuuint64_t>(pl.D) << pack, static_cast<cuuint64_t>(pl.D) * pl.BS};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(pitch) << pack, static_cast<cuuint32_t>(kQ8Tok) >> pack,
+    const bool dense = pl.layout == kDense;
+    const cuuint64_t row = static_cast<cuuint64_t>(pl.D) << pl.tok_shift, elem = dense ? 8 : 1;
+    cuuint64_t dim[3] = {row / elem, static_cast<cuuint64_t>(pl.BS) >> pl.tok_shift,
+                         static_cast<cuuint64_t>(pl.NB) * pl.Hkv};
+    cuuint64_t stride[2] = {row, static_cast<cuuint64_t>(pl.D) * pl.BS};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(row / elem), static_cast<cuuint32_t>(kQ8Tok) >> pl.tok_shift,
                          static_cast<cuuint32_t>(pl.HG)};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dim, stride, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, pitch == 128 || pack ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    cuuint32_t one[3] = {1, 1, 1};
+    return enc(map, dense ? CU_TENSOR_MAP_DATA_TYPE_UINT64 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool),
+               dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               dense ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename T, typename Fmt, int DP, int kN>
@@ -1076,9 +1087,9 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
                                   void* workspace, int P, int32_t* status, cudaStream_t stream, bool* done) {
     *done = false;
     constexpr bool kSplit = sizeof(T) == 4;
-    constexpr int kSub = DP == 64 ? 4 : 2, kPitch = DP == 64 ? 64 : 128;
+    constexpr int kSub = DP == 64 ? 4 : 2;
     const int tiles = pl.HG * pl.slots * kSub;
-    pl.stage_bytes = 2 * tiles * kQ8Tok * kPitch;
+    pl.stage_bytes = 2 * tiles * kQ8Tok * pl.D;
     pl.scale_unit = pl.HG * kQ8Tok * 4;
     // rows 32 (bf16) or 64 bytes apart modulo 128, so that the 8 heads a warp reads at
     // once fall on different banks
@@ -1094,7 +1105,7 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     pl.nst = static_cast<int>(std::min<size_t>(kQ8MaxStages, (budget - fixed) / per));
     const size_t smem = fixed + pl.nst * per;
     CUtensorMap tmK, tmV;
-    if (!q8_map(&tmK, k, pl, kPitch) || !q8_map(&tmV, v, pl, kPitch)) return cudaSuccess;
+    if (!q8_map(&tmK, k, pl) || !q8_map(&tmV, v, pl)) return cudaSuccess;
     const Q8Layout wl = q8_layout(pl.R, pl.D, P);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     float* part_ml = reinterpret_cast<float*>(ws);

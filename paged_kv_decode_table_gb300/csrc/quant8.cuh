@@ -41,7 +41,7 @@ struct FmtNone {  // rows kept in their own type
 };
 
 struct FmtE4M3 {
-    static constexpr bool kQuant = true;
+    static constexpr bool kQuant = true, kHasNaN = true;
     static constexpr float kInvQ = 1.0f / 448.0f;
     // two floats -> two bytes (lo in bits 0-7)
     static __device__ __forceinline__ uint32_t encode2(float lo, float hi) {
@@ -76,7 +76,7 @@ struct FmtE4M3 {
 };
 
 struct FmtI8 {
-    static constexpr bool kQuant = true;
+    static constexpr bool kQuant = true, kHasNaN = false;
     static constexpr float kInvQ = 1.0f / 127.0f;
     // |x| <= 127 (1 + 2^-22): adding 1.5 * 2^23 rounds to nearest even into the low byte
     static __device__ __forceinline__ uint32_t rounded(float x) { return __float_as_uint(__fadd_rn(x, 12582912.f)); }
