@@ -117,6 +117,62 @@ __global__ void __launch_bounds__(kReadThreads)
     }
 }
 
+// Blocks of few rows: the rows of all blocks in one order, cut into CTAs whatever block they
+// are of.  8479 blocks of 1 head x 64 x 32 in int8 to bf16 (109 MB moved): 18.9 us, 5.8
+// TB/s; a CTA per block 38.7 us.  Large blocks stay with the kernel above, which is 2%
+// faster on them.
+constexpr int kRowsPasses = 6;
+
+template <typename T, typename Fmt, int kVec>
+__global__ void __launch_bounds__(kReadThreads)
+    kv_read_rows_kernel(T* __restrict__ k_out, T* __restrict__ v_out, const uint8_t* __restrict__ k_cache,
+                        const uint8_t* __restrict__ v_cache, const float* __restrict__ k_scale,
+                        const float* __restrict__ v_scale, const int32_t* __restrict__ blocks, int chunks, int n, int R,
+                        int D, int NB, int32_t* status) {
+    prefetch_l2(blocks, static_cast<size_t>(n) * 4, blockIdx.x * kReadThreads + threadIdx.x);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int per_row = D / kVec, rows = kReadThreads / per_row;  // threads per row, rows per pass
+    const int sub = threadIdx.x / per_row, col = (threadIdx.x - sub * per_row) * kVec;
+    // CTA: (K or V, chunk of all rows)
+    const unsigned chunk = blockIdx.x % static_cast<unsigned>(chunks);
+    const bool is_v = blockIdx.x >= static_cast<unsigned>(chunks);
+    const uint8_t* src = (is_v ? v_cache : k_cache) + col;
+    const float* sc = is_v ? v_scale : k_scale;
+    T* dst = (is_v ? v_out : k_out) + col;
+    Bytes<kVec> raw[kRowsPasses];
+    float scale[kRowsPasses];
+    if (sub >= rows) return;
+    const unsigned last = static_cast<unsigned>(n) * R - 1u, r0 = chunk * static_cast<unsigned>(rows * kRowsPasses) + sub;
+    int blk[kRowsPasses];
+    unsigned in_blk[kRowsPasses];
+#pragma unroll
+    for (int p = 0; p < kRowsPasses; ++p) {
+        const unsigned r = min(r0 + p * rows, last), i = r / static_cast<unsigned>(R);
+        blk[p] = blocks[i];
+        in_blk[p] = r - i * R;
+    }
+#pragma unroll
+    for (int p = 0; p < kRowsPasses; ++p) {
+        const bool good = blk[p] >= 0 && blk[p] < NB;
+        if (!good && !is_v && col == 0 && in_blk[p] == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
+        const size_t row = static_cast<size_t>(good ? blk[p] : 0) * R + in_blk[p];
+        raw[p] = load_bytes<kVec>(src + row * D);
+        scale[p] = __ldg(sc + row);
+        if (!good) blk[p] = -1;
+    }
+#pragma unroll
+    for (int p = 0; p < kRowsPasses; ++p) {
+        const unsigned r = r0 + p * rows;
+        if (r > last) break;
+        float x[kVec];
+        decode_row<Fmt, kVec>(raw[p], x);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) x[e] = blk[p] >= 0 ? x[e] * scale[p] : 0.f;
+        store_row<T, kVec>(dst + static_cast<size_t>(r) * D, x);
+    }
+}
+
 template <typename T, typename Fmt>
 static cudaError_t launch_read(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
                                const float* k_scale, const float* v_scale, const int32_t* blocks, int n, int R, int D,
@@ -126,10 +182,13 @@ static cudaError_t launch_read(void* k_out, void* v_out, const void* k_cache, co
         const uintptr_t in = reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache);
         return D % vec == 0 && in % vec == 0 && out % (vec * sizeof(T)) == 0;
     };
-    auto run = [&](auto kern, int vec) {
-        const int rows = kReadThreads / (D / vec) * kReadPasses;
-        const int chunks = (R + rows - 1) / rows;
-        const long long grid = 2LL * n * chunks;
+    auto run = [&](auto block_kern, auto rows_kern, int vec) {
+        // blocks that would leave more than an eighth of a CTA's rows idle share CTAs
+        const int pass = kReadThreads / (D / vec), rows = pass * kReadPasses;
+        const long long all = static_cast<long long>(n) * R, idle = (rows - R % rows) % rows;
+        const bool share = idle * 8 > R + idle && all < (1LL << 31);
+        const long long per = share ? static_cast<long long>(pass) * kRowsPasses : rows;
+        const long long chunks = ((share ? all : R) + per - 1) / per, grid = (share ? 2LL : 2LL * n) * chunks;
         if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -140,16 +199,20 @@ static cudaError_t launch_read(void* k_out, void* v_out, const void* k_cache, co
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        const cudaError_t err = cudaLaunchKernelEx(
-            &cfg, kern, static_cast<T*>(k_out), static_cast<T*>(v_out), static_cast<const uint8_t*>(k_cache),
-            static_cast<const uint8_t*>(v_cache), k_scale, v_scale, blocks, chunks, R, D, NB, status);
+        T *ko = static_cast<T*>(k_out), *vo = static_cast<T*>(v_out);
+        const uint8_t *kc = static_cast<const uint8_t*>(k_cache), *vc = static_cast<const uint8_t*>(v_cache);
+        const int nch = static_cast<int>(chunks);
+        const cudaError_t err = share ? cudaLaunchKernelEx(&cfg, rows_kern, ko, vo, kc, vc, k_scale, v_scale, blocks, nch,
+                                                           n, R, D, NB, status)
+                                      : cudaLaunchKernelEx(&cfg, block_kern, ko, vo, kc, vc, k_scale, v_scale, blocks,
+                                                           nch, R, D, NB, status);
         return err != cudaSuccess ? err : cudaGetLastError();
     };
     if constexpr (sizeof(T) == 2) {
-        if (fits(8)) return run(kv_read_kernel<T, Fmt, 8>, 8);
+        if (fits(8)) return run(kv_read_kernel<T, Fmt, 8>, kv_read_rows_kernel<T, Fmt, 8>, 8);
     }
-    if (fits(4)) return run(kv_read_kernel<T, Fmt, 4>, 4);
-    return run(kv_read_kernel<T, Fmt, 1>, 1);
+    if (fits(4)) return run(kv_read_kernel<T, Fmt, 4>, kv_read_rows_kernel<T, Fmt, 4>, 4);
+    return run(kv_read_kernel<T, Fmt, 1>, kv_read_rows_kernel<T, Fmt, 1>, 1);
 }
 
 }  // namespace pkv

@@ -148,7 +148,7 @@ def test_append_skips_what_it_cannot_place():
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("Hkv,D,BS", [(8, 128, 16), (3, 80, 32), (1, 4, 4), (5, 100, 8), (2, 256, 16), (1, 1, 1),
-                                      (7, 24, 5), (2, 36, 16)])
+                                      (7, 24, 5), (2, 36, 16), (8, 128, 32), (3, 64, 48)])
 def test_read_blocks_bit_for_bit(Hkv, D, BS, dtype, fmt):
     g = torch.Generator().manual_seed(7)
     k, v, ks, vs = R.random_cache(11, Hkv, BS, D, fmt, g)
