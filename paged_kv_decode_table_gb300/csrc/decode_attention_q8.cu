@@ -105,6 +105,13 @@ __device__ __forceinline__ float ex2f(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// With subnormal results: a weight p_j is about 1 / vs_j, and with V scales near 2^119 (rows
+// near the largest float) weights of 2^-7 of the largest would be flushed to zero.
+__device__ __forceinline__ float ex2f_subnormal(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float lg2f(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -576,7 +583,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             for (int n = 0; n < kN; ++n)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const float p0 = ex2f(x[k][n][2 * t] - mu[n][0]), p1 = ex2f(x[k][n][2 * t + 1] - mu[n][1]);
+                    const float p0 = ex2f_subnormal(x[k][n][2 * t] - mu[n][0]), p1 = ex2f_subnormal(x[k][n][2 * t + 1] - mu[n][1]);
                     l[n][0] += p0;
                     l[n][1] += p1;
                     const float w0 = p0 * vsc[k][t], w1 = p1 * vsc[k][t];
@@ -999,7 +1006,7 @@ __global__ void __launch_bounds__(kGen8Threads)
         const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
         const float alpha = expf(m - mu);
         const float p = tid < n ? expf(s - mu) : 0.f;
-        ps[tid] = p * vs;
+        ps[tid] = p * (vs * 0x1p-40f);  // sums of up to 2^31 rows near the largest float stay finite
         float sm = p;
         for (int off = 16; off > 0; off >>= 1) sm += __shfl_xor_sync(0xffffffffu, sm, off);
         if (lane == 0) red[warp] = sm;
@@ -1017,7 +1024,7 @@ __global__ void __launch_bounds__(kGen8Threads)
         }
     }
     if (bad && tid == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
-    const float inv = bad || l == 0.f ? 0.f : 1.f / l;
+    const float inv = bad || l == 0.f ? 0.f : 0x1p40f / l;
     for (int k = 0; k < 2; ++k) {
         const int d = tid + k * kGen8Threads;
         if (d < D) o[d] = from_f32<T>(bad ? 0.f : acc[k] * inv);

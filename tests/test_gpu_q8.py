@@ -180,6 +180,24 @@ def test_read_bad_ids_give_zero_blocks_and_unaligned_outputs_work():
     assert bool((flat[:, 0] == 9).all())
 
 
+@pytest.mark.parametrize("Hkv,D,BS", [(1, 5, 3), (3, 80, 32), (2, 24, 1)])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_copy_blocks_of_an_8_bit_cache(Hkv, D, BS, fmt):
+    g = torch.Generator().manual_seed(31)
+    pools = R.random_cache(9, Hkv, BS, D, fmt, g)
+    k, v, ks, vs = cuda(*(p.clone() for p in pools))
+    st = pkv.new_status()
+    src, dst = [0, 0, 7, 9], [3, 5, 8, 1]  # one source twice; the last id is out of range
+    pkv.copy_blocks(k, v, i32(src).cuda(), i32(dst).cuda(), status=st, k_scale=ks, v_scale=vs)
+    assert pkv.check_status(st) == 4
+    for got, want in zip((k, v, ks, vs), pools):
+        want = want.clone()
+        raw = want.view(torch.uint8) if want.dtype != torch.float32 else want
+        for a, b in zip(src[:3], dst[:3]):
+            raw[b] = raw[a]
+        assert torch.equal(got.cpu().view(raw.dtype), raw)
+
+
 # ------------------------------------------------------------------ attention
 ATTENTION = [  # (Hq, Hkv, D, BS, lens)
     (32, 8, 128, 16, [1, 0, 16, 17, 255, 700, 31, 15]),
@@ -266,6 +284,23 @@ def test_attention_wide_scales(fmt):
             out = pkv.paged_decode_attention_q8(*cuda(qq, k, v, ks, vs, bt, i32(lens)))
             ref, tol = R.attention(qq, k, v, ks, vs, bt, lens, dtype=dtype)
             assert bool(((out.cpu().double() - ref).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,lens", [(8, 2, 64, [300, 17]), (8, 2, 128, [2000]), (4, 2, 100, [300, 40])])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_attention_over_values_near_the_largest_float(Hq, Hkv, D, lens, fmt):
+    """V scales up to 2^119.  Exponents are then shifted by up to 119 instead of 64, which
+    enters the bound's 144 * 2^-24 as 2 * 119 + 16: less than twice the bound."""
+    g = torch.Generator().manual_seed(22)
+    bt, nb = R.tables(lens, 16, g)
+    k, v, ks, vs = R.random_cache(nb, Hkv, 16, D, fmt, g)
+    vs = 2.0 ** 119 * (0.5 + 0.5 * torch.rand(vs.shape, generator=g))
+    q = torch.randn(len(lens), Hq, D, generator=g)
+    for dtype in DTYPES:
+        qq = q.to(DTYPES[dtype])
+        out = pkv.paged_decode_attention_q8(*cuda(qq, k, v, ks, vs, bt, i32(lens)))
+        ref, tol = R.attention(qq, k, v, ks, vs, bt, lens, dtype=dtype)
+        assert bool(((out.cpu().double() - ref).abs() <= 2 * tol).all())
 
 
 @pytest.mark.parametrize("Hq,Hkv,D,BS", [(32, 8, 128, 16), (4, 2, 100, 16), (8, 1, 64, 32)])
