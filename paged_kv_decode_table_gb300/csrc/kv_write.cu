@@ -25,6 +25,7 @@
 // Two rows per lane are in work at once, two queries or a key and a value, which overlaps
 // their reductions' shuffles; head sizes 64 and 128 have those lanes as constants.  The other kernel (any D and alignment) gives a warp one row, one element
 // per lane and step.
+#include <algorithm>
 #include <type_traits>
 
 #include "quant8.cuh"
@@ -566,15 +567,20 @@ static cudaError_t launch_typed(const WriteArgs& a, cudaStream_t stream) {
         w.kvpasses = (a.Hkv + w.per - 1) / w.per;
         w.inv_d = 1.0f / static_cast<float>(a.D);
         const int passes = (w.qpasses + 1) / 2 + w.kvpasses;  // pairs of passes
-        // many tokens: a warp takes many passes of one token, which shares the token's place,
-        // angles and weights; few: a token's passes over as many warps and CTAs as there are
+        // Many tokens: a warp takes many passes of one token, which shares the token's place,
+        // angles and weights, and a CTA several tokens; one warp a token only where two of each
+        // would not be resident at once.  32 + 8 heads x 128 in bf16, 5111 tokens: 30 us with a
+        // warp a token, 46 with eight; 1227 tokens: 10.7 with one, 8.9 with two; 425: 8.1, 5.1,
+        // 4.4 with four, 4.0 with eight; 96: 3.6 with four, 3.0 with eight.
         w.wpt_log2 = 3;
         int split = 1;
         while (w.wpt_log2 > 0 && passes < kPairsPerWarp << w.wpt_log2 &&
-               (static_cast<long long>(a.T) << w.wpt_log2) >= 12LL * sms)
+               (static_cast<long long>(a.T) << w.wpt_log2) >= (w.wpt_log2 > 1 ? 12LL : 24LL) * sms)
             --w.wpt_log2;
+        // few: a pass per warp, over as many CTAs as that takes and the SMs hold 1.5 of each
+        // (39 tokens 2.95 -> 2.69 us; two CTAs for 117 tokens 3.0 -> 3.6)
         if (w.wpt_log2 == 3)
-            while (split * kWriteWarps < w.qpasses + w.kvpasses && static_cast<long long>(a.T) * split < 2LL * sms) ++split;
+            split = std::max(1, std::min((w.qpasses + w.kvpasses + kWriteWarps - 1) / kWriteWarps, 3 * sms / 2 / a.T));
         const int tpc = kWriteWarps >> w.wpt_log2;
         cfg.gridDim = dim3(static_cast<unsigned>((a.T + tpc - 1) / tpc), static_cast<unsigned>(split), 1);
         const int rot = a.half == 0 ? 0 : a.interleaved ? 3 : a.half % 4 == 0 ? 1 : 2;
