@@ -397,6 +397,14 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
         }
     }
     if (!active) return;
+    if (!p.ok) {  // a bad length or chunk: zero queries, no append
+        const float2 zero[4] = {};
+        T* qo = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.Hq * a.D + at0;
+        for (int pass = first; pass < qpass; pass += stride)
+            if (in && pass * per + sub < a.Hq) store_runs(qo + (pass * per + sub) * a.D, gap, zero);
+        if (first == 0 && lane == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
+        return;
+    }
 
     auto square = [](const float2 (&x)[4]) {
         float2 s2 = mul2(x[0], x[0]);
@@ -471,15 +479,17 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 rotate(x[k]);
-                if (!p.ok) x[k][0] = x[k][1] = x[k][2] = x[k][3] = make_float2(0.f, 0.f);
                 const int h = (pass + k * stride) * per + sub;
                 if (in && h < a.Hq) store_runs(qo + h * a.D, gap, x[k]);
             }
         }
     }
     const int blk = p.blk(a.NB);
-    const size_t slot0 = static_cast<size_t>(max(blk, 0)) * a.Hkv * a.BS + p.slot;  // cache row of KV head 0
-    if (blk < 0 && first == 0 && lane == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
+    if (blk < 0) {
+        if (first == 0 && lane == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    const size_t slot0 = static_cast<size_t>(blk) * a.Hkv * a.BS + p.slot;  // cache row of KV head 0
     float2 g[4];
     if (a.k_weight != nullptr) to_floats(wk, g);
     for (int pass = kv0; pass < kvpass; pass += stride) {  // x[0]: a key row, x[1]: the value row
@@ -496,7 +506,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
         }
         rotate(x[0]);
         const int h = pass * per + sub;
-        const bool mine = in && h < a.Hkv && blk >= 0;
+        const bool mine = in && h < a.Hkv;
         const size_t row = slot0 + static_cast<size_t>(h) * a.BS, at = row * a.D + at0;
         if constexpr (Fmt::kQuant) {
             // the largest |x| as an integer: infinities and NaN are above every finite number
