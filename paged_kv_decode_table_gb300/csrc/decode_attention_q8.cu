@@ -11,9 +11,9 @@
 // joins the sequences that several ranges share.
 //  * A tile is 16 positions of one KV head.  A step is slots x kSub tiles of
 //    consecutive positions of `HG` KV heads (at most 8 x kSub tiles), fetched by TMA
-//    boxes of 16 positions x HG heads into one stage of an mbarrier ring.  The steps of all (sequence, head group) pairs, one
-//    after the other, are cut into one range per CTA; every CTA finds its range
-//    itself from seq_lens.
+//    boxes of 16 positions x HG heads into one stage of an mbarrier ring.  The steps of
+//    all (sequence, head group) pairs, one after the other, are cut into one range per
+//    CTA; every CTA finds its range itself from seq_lens.
 //  * One consumer warp per (KV head, chunk of its query heads, slot) takes kSub
 //    tiles of every step: with 8 KV heads the 8 warps are the heads, with one head
 //    they are 8 slots along the cache, so a model split over devices keeps every
@@ -41,6 +41,18 @@
 //  * q is multiplied by a power of two per head that puts its largest element into
 //    [2^14, 2^15).
 // Other shapes: one CTA per (sequence, query head), CUDA-core fp32.
+//
+// What bounds it: HBM where the cache is large.  8 sequences of 32768-131072 positions, 64
+// query and 8 KV heads of 128 in int8: 231 us for 1.53 GB, 6.6 TB/s, 99% of the measured
+// copy rate.  64 sequences of 512-4096, 32 and 8 heads: 58 us for 332 MB, 86%; the rest is
+// the start (2.5 us), the end of the slowest SM (2.3 us) and the join (3.5 us).  With the
+// arithmetic left out the same kernel takes 57 us, so the tensor and issue pipes (17% and
+// 32% busy) hide behind the copies.  They do not with 16 query heads a group (128 and 8
+// heads: 85 us, 58%) and with float32 queries (63 us, 79%; two MMAs for one).  One short
+// sequence is a chain of latencies, lengths -> block ids -> K and V -> result: 6.4 us.
+// mma.sync and not tcgen05: a float16 query needs float16 keys, so the converted numbers, twice
+// the bytes that came, would go back to shared memory before tcgen05.mma could read them,
+// and the tensor pipe is not what the kernel waits for.
 #include <cuda.h>
 #include <math.h>
 
@@ -64,7 +76,10 @@ int attention_silent_cta();
 constexpr int kQ8MaxStages = 12;
 constexpr int kQ8Tok = 16;  // positions per tile
 constexpr int kQ8Warps = 8;  // consumer warps at most
-constexpr int kDirectSteps = 3;  // steps of a sequence up to which a join is not worth it
+// Steps of a sequence up to which a join is not worth it.  Direct against split: 1 sequence of
+// up to 256 positions, 32 and 8 heads 6.4 : 8.5 us, 16 of up to 512 8.5 : 11.2 us; at 1024 (6
+// steps) 9.1 : 8.8 us for one, 10.8 : 9.0 for four, 12.2 : 12.6 for 16.
+constexpr int kDirectSteps = 3;
 constexpr float kLag = 8.f;  // contributions stay below 2^8 of the running maximum
 
 // How a call is laid out; computed on the host, passed to both kernels.
@@ -196,7 +211,9 @@ __device__ __forceinline__ uint32_t q8_at(int tok, int c, const Q8Plan& pl) {
     return static_cast<uint32_t>(tok * 128 + ((c ^ (tok & 7)) << 4));
 }
 
-// DP: dimensions computed (64, 96 or 128; D may be smaller); kN: n-tiles of 8 query heads per warp; kSplit: float32 accuracy (see above).
+// DP: dimensions computed (64, 96 or 128; D may be smaller; 96 of 128 for D = 80 and 96 took
+// 15.6 -> 14.3 us off 37 float32 sequences of up to 1500); kN: n-tiles of 8 query heads per
+// warp; kSplit: float32 accuracy (see above); kSub: tiles a warp takes of a step.
 template <typename T, typename Fmt, int DP, int kN, bool kSplit, int kSub>
 __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -818,7 +835,9 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
 // M = max m_c, out = sum o_c 2^(m_c - M) / sum l_c 2^(m_c - M) over the pieces of
 // a sequence that several ranges share: the piece of its first range f in slot
 // 2f + 1, of a later range c in slot 2c.  kUnitWarps warps per (sequence, query
-// head): one where there are many, four (over the pieces) where there are few.
+// head): one where there are many, four (over the pieces) where there are few.  The whole
+// call with one and with four: 64 x 32 of them 57.7 and 60.8 us, 512 x 32 114 and 138 us;
+// 8 x 32 in sequences of 100-1000 12.3 and 10.1 us, 8 x 64 in long ones 236 and 231 us.
 // Sequences within one range were written by the main kernel; empty and invalid
 // ones get zeros here.
 constexpr int kJoinWarps = 4;
@@ -950,6 +969,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 }
 
 // ------------------------------------------------------------------ generic kernel
+// D not a multiple of 16 or above 128, block sizes that are not multiples of 16, addresses that
+// are not 16-byte aligned, more than 64 (float32) or 128 query heads a KV head.  A thread takes
+// one position's score, then one or two dimensions of the output; bound by the latency of
+// its byte loads.
 constexpr int kGen8Threads = 128;
 
 template <typename T, typename Fmt>
@@ -1052,7 +1075,7 @@ static bool q8_shape(int Hq, int Hkv, int D, int BS, pkv_dtype dt, int min_group
     pl.UB = BS / kQ8Tok;
     pl.layout = D == 128 ? kSwizzled : D == 64 ? kPacked : kDense;
     pl.tok_shift = D == 128 ? 0 : D == 64 ? 1 : 4;
-    pl.sub = D <= 64 ? 4 : 2;  // steps of about 64 KB
+    pl.sub = D <= 64 ? 4 : 2;  // steps of about 64 KB (D 64, 64 x 512-8192: 60.7 us with 2, 56.1 with 4)
     pl.slots = 1;
     while (pl.slots * 2 * pl.HG * pl.QC <= kQ8Warps) pl.slots *= 2;
     pl.G = G;
