@@ -271,6 +271,10 @@ template <>
 struct Runs<float> {
     float4 v[2];
 };
+template <typename Run, typename T>
+__device__ __forceinline__ void copy_run(Run* to, const T* from) {  // asynchronous
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from), "n"(sizeof(Run)) : "memory");
+}
 template <typename T>
 __device__ __forceinline__ Runs<T> load_runs(const T* p, int gap) {  // run B lies gap elements behind run A
     Runs<T> r;
@@ -365,15 +369,66 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
     const T* qp = static_cast<const T*>(a.q) + t * a.q_stride + at0;
     const T* kp = static_cast<const T*>(a.k) + t * a.k_stride + at0;
     const T* vp = static_cast<const T*>(a.v) + t * a.v_stride + at0;
-    auto load = [&](Runs<T>& to, const T* src, int pass, int heads) {
+    // With a rotation, pairs of rows come through a ring of kDepth pairs per warp, of which a
+    // lane reads only what it copied itself: more is in flight than registers would hold (6147
+    // tokens of 32 + 8 heads 32.9 -> 29.1 us; four pairs are no faster than two).  Without one
+    // (the appends: few pairs a token) the next pair waits in registers (512 tokens of 8 heads
+    // 2.5 us, 2.6 with the ring).
+    constexpr bool kRing = kRot != 0;
+    constexpr int kDepth = !kRing || (kRot == 2 && sizeof(T) == 4) ? 1 : 2;
+    using Run = std::remove_reference_t<decltype(Runs<T>().v[0])>;
+    __shared__ __align__(16) Run ring[kRing ? kWriteWarps : 1][kDepth][4][32];
+    Runs<T> held[2];
+    auto load = [&](int k, int slot, const T* src, int pass, int heads) {
         const int h = pass * per + sub;
-        if (in && h < heads) to = load_runs(src + h * a.D, gap);
+        if (!in || h >= heads) return;
+        src += h * a.D;
+        if constexpr (kRing) {
+            copy_run(&ring[warp][slot][2 * k][lane], src);
+            copy_run(&ring[warp][slot][2 * k + 1][lane], src + gap);
+        } else {
+            held[k] = load_runs(src, gap);
+        }
     };
-    Runs<T> raw[2], rawkv[2];
+    // the pairs: first those of queries, then the keys' passes with the values'
+    int lq = first, lkv = kv0, lslot = 0;
+    auto load_next = [&]() {
+        if constexpr (kRing) {
+            if (lq < qpass) {
+                load(0, lslot, qp, lq, a.Hq);
+                load(1, lslot, qp, lq + stride, a.Hq);
+                lq += 2 * stride;
+            } else if (lkv < kvpass) {
+                load(0, lslot, kp, lkv, a.Hkv);
+                load(1, lslot, vp, lkv, a.Hkv);
+                lkv += stride;
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        } else {  // selects: with the branches 581 tokens of 8 heads take 3.1 us for 2.7
+            const bool is_q = lq < qpass;
+            load(0, 0, is_q ? qp : kp, is_q ? lq : lkv, is_q ? a.Hq : a.Hkv);
+            load(1, 0, is_q ? qp : vp, is_q ? lq + stride : lkv, is_q ? a.Hq : a.Hkv);
+            lkv += is_q ? 0 : stride;
+            lq += is_q ? 2 * stride : 0;
+        }
+        if (++lslot == kDepth) lslot = 0;
+    };
 #pragma unroll
-    for (int k = 0; k < 2; ++k) load(raw[k], qp, first + k * stride, a.Hq);
-    load(rawkv[0], kp, kv0, a.Hkv);
-    load(rawkv[1], vp, kv0, a.Hkv);
+    for (int k = 0; k < kDepth; ++k) load_next();
+    int slot = 0;
+    auto take = [&](Runs<T> (&to)[2]) {
+        if constexpr (kRing) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+#pragma unroll
+            for (int k = 0; k < 4; ++k) to[k >> 1].v[k & 1] = ring[warp][slot][k][lane];
+            if (++slot == kDepth) slot = 0;
+            __syncwarp();
+        } else {
+            to[0] = held[0];
+            to[1] = held[1];
+        }
+        load_next();
+    };
     // norm weights and frequencies do not wait for the token's place either
     Runs<T> wq, wk;
     if (a.q_weight != nullptr) wq = load_runs(static_cast<const T*>(a.q_weight) + at0, gap);
@@ -407,14 +462,16 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
             }
         }
     }
-    if (!active) return;
+    // no copy outlives its CTA
+    auto settle = [] { if constexpr (kRing) asm volatile("cp.async.wait_all;" ::: "memory"); };
+    if (!active) return settle();
     if (!p.ok) {  // a bad length or chunk: zero queries, no append
         const float2 zero[4] = {};
         T* qo = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.Hq * a.D + at0;
         for (int pass = first; pass < qpass; pass += stride)
             if (in && pass * per + sub < a.Hq) store_runs(qo + (pass * per + sub) * a.D, gap, zero);
         if (first == 0 && lane == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
-        return;
+        return settle();
     }
 
     auto square = [](const float2 (&x)[4]) {
@@ -474,12 +531,13 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
         if (a.q_weight != nullptr) to_floats(wq, g);
         T* qo = static_cast<T*>(a.q_out) + static_cast<size_t>(t) * a.Hq * a.D + at0;
         for (int pass = first; pass < qpass; pass += 2 * stride) {
+            Runs<T> raw[2];
+            take(raw);
             float2 x[2][4];
             float ss[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 to_floats(raw[k], x[k]);
-                load(raw[k], qp, pass + (2 + k) * stride, a.Hq);
                 ss[k] = square(x[k]);
             }
             if (a.q_weight != nullptr) {
@@ -498,18 +556,17 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
     const int blk = p.blk(a.NB);
     if (blk < 0) {
         if (first == 0 && lane == 0) report(a.status, PKV_ERR_DEVICE_BOUNDS);
-        return;
+        return settle();
     }
     const size_t slot0 = static_cast<size_t>(blk) * a.Hkv * a.BS + p.slot;  // cache row of KV head 0
     float2 g[4];
     if (a.k_weight != nullptr) to_floats(wk, g);
     for (int pass = kv0; pass < kvpass; pass += stride) {  // x[0]: a key row, x[1]: the value row
         float2 x[2][4];
-        const Runs<T> vnow = rawkv[1];
+        Runs<T> raw[2];
+        take(raw);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) to_floats(rawkv[k], x[k]);
-        load(rawkv[0], kp, pass + stride, a.Hkv);
-        load(rawkv[1], vp, pass + stride, a.Hkv);
+        for (int k = 0; k < 2; ++k) to_floats(raw[k], x[k]);
         if (a.k_weight != nullptr) {
             float ss[2] = {square(x[0]), 0.f};
             row_reduce<kLanes>(ss, w, l, base, sum);
@@ -553,9 +610,8 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
         } else if (mine) {
             store_runs(static_cast<T*>(a.k_cache) + at, gap, x[0]);
             T* dst = static_cast<T*>(a.v_cache) + at;  // the bits as they are
-            using V = std::remove_const_t<std::remove_reference_t<decltype(vnow.v[0])>>;
-            *reinterpret_cast<V*>(dst) = vnow.v[0];
-            *reinterpret_cast<V*>(dst + gap) = vnow.v[1];
+            *reinterpret_cast<Run*>(dst) = raw[1].v[0];
+            *reinterpret_cast<Run*>(dst + gap) = raw[1].v[1];
         }
     }
 }
