@@ -48,6 +48,7 @@ constexpr int kWriteMaxD = 256;
 constexpr int kPairsPerWarp = 8;
 
 int device_sm_count();
+constexpr int kMinWarpsLog2 = 2;
 
 struct WriteArgs {
     void* q_out;
@@ -313,6 +314,7 @@ struct WritePlan {
     float inv_d;
     int magic;       // lane / lanes = lane * magic >> 16
     int wpt_log2;    // warps per token
+    int warps_log2;  // warps per CTA
 };
 
 // op over the lanes of a row, for two rows at once (their shuffles overlap).  kLanes: lanes a
@@ -338,6 +340,18 @@ __device__ __forceinline__ void row_reduce(V (&x)[2], const WritePlan& w, int l,
     }
 }
 
+// Dynamic shared memory of a warp: its ring, its token's cosines and sines, its rows.
+template <typename T, int kRot>
+struct WriteShared {
+    static constexpr bool kRing = kRot != 0;
+    static constexpr int kDepth = !kRing || (kRot == 2 && sizeof(T) == 4) ? 1 : 2;
+    static constexpr int kRingBytes = kRing ? kDepth * 4 * 32 * 4 * static_cast<int>(sizeof(T)) : 0;
+    static constexpr int kTable = kRot == 0 ? 0 : kWriteMaxD / 2;             // float2
+    static constexpr int kRows = kRot == 2 ? 2 * (kWriteMaxD + kWriteMaxD / 8) : 0;  // float
+    static constexpr int kBytes = kRingBytes + kTable * 8 + kRows * 4;
+    static_assert(kBytes % 16 == 0 && kWriteWarps * kBytes <= 48 * 1024, "default limit");
+};
+
 // kRot: 0 no rotation, 1 pairs (j, j + half) with half a multiple of 4, 2 such pairs
 // with any half, 3 pairs (2j, 2j + 1).
 template <typename T, typename Fmt, int kRot, int kLanes>
@@ -346,13 +360,11 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
     write_prefetch(a);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kPad = kWriteMaxD + kWriteMaxD / 8;
-    constexpr int kTable = kWriteMaxD / 2;
-    __shared__ float rowbuf[kRot == 2 ? kWriteWarps : 1][kRot == 2 ? 2 * kPad : 1];
-    __shared__ __align__(16) float2 turn[kRot == 0 ? 1 : kWriteWarps * kTable];  // [token of the CTA][pair]
+    using Shared = WriteShared<T, kRot>;
+    extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wpt = 1 << w.wpt_log2, tok = warp >> w.wpt_log2;
-    const int t = (blockIdx.x << (3 - w.wpt_log2)) + tok;
+    const int t = (blockIdx.x << (w.warps_log2 - w.wpt_log2)) + tok;
     const int lanes = kLanes > 0 ? kLanes : w.lanes, per = kLanes > 0 ? 32 / kLanes : w.per;
     const int sub = kLanes > 0 ? lane / kLanes : (lane * w.magic) >> 16, base = sub * lanes, l = lane - base;
     // the lane's elements: at0 .. at0 + 3 and at0 + gap .. + 3; with kRot 1 the second run
@@ -374,18 +386,19 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
     // tokens of 32 + 8 heads 32.9 -> 29.1 us; four pairs are no faster than two).  Without one
     // (the appends: few pairs a token) the next pair waits in registers (512 tokens of 8 heads
     // 2.5 us, 2.6 with the ring).
-    constexpr bool kRing = kRot != 0;
-    constexpr int kDepth = !kRing || (kRot == 2 && sizeof(T) == 4) ? 1 : 2;
+    constexpr bool kRing = Shared::kRing;
+    constexpr int kDepth = Shared::kDepth;
     using Run = std::remove_reference_t<decltype(Runs<T>().v[0])>;
-    __shared__ __align__(16) Run ring[kRing ? kWriteWarps : 1][kDepth][4][32];
+    uint8_t* mine = smem + warp * Shared::kBytes;
+    Run* ring = reinterpret_cast<Run*>(mine) + lane;  // [kDepth][row of the pair][run][lane]
     Runs<T> held[2];
     auto load = [&](int k, int slot, const T* src, int pass, int heads) {
         const int h = pass * per + sub;
         if (!in || h >= heads) return;
         src += h * a.D;
         if constexpr (kRing) {
-            copy_run(&ring[warp][slot][2 * k][lane], src);
-            copy_run(&ring[warp][slot][2 * k + 1][lane], src + gap);
+            copy_run(ring + (slot * 4 + 2 * k) * 32, src);
+            copy_run(ring + (slot * 4 + 2 * k + 1) * 32, src + gap);
         } else {
             held[k] = load_runs(src, gap);
         }
@@ -420,7 +433,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
         if constexpr (kRing) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
 #pragma unroll
-            for (int k = 0; k < 4; ++k) to[k >> 1].v[k & 1] = ring[warp][slot][k][lane];
+            for (int k = 0; k < 4; ++k) to[k >> 1].v[k & 1] = ring[(slot * 4 + k) * 32];
             if (++slot == kDepth) slot = 0;
             __syncwarp();
         } else {
@@ -440,7 +453,8 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
     // the sign it enters with (kRot 2)
     float2 cs[kRot == 2 ? 4 : 2], sn[kRot == 2 ? 4 : 2];
     if constexpr (kRot != 0) {
-        float2* tt = turn + tok * kTable;
+        // of the token's first warp
+        float2* tt = reinterpret_cast<float2*>(smem + (tok << w.wpt_log2) * Shared::kBytes + Shared::kRingBytes);
         if (active)
             for (int j = (warp & (wpt - 1)) * 32 + lane; j < a.half; j += wpt * 32) tt[j] = turn_of(p.pos, a.freqs[j]);
         __syncthreads();
@@ -505,7 +519,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
             }
         } else if constexpr (kRot == 2) {
             // rows through shared memory, one word of padding per 8
-            float* buf = rowbuf[warp];
+            float* buf = reinterpret_cast<float*>(mine + Shared::kRingBytes + Shared::kTable * 8);
             const int at = sub * (a.D + a.D / 8);
             __syncwarp();
             if (sub < per) {
@@ -574,7 +588,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
         }
         rotate(x[0]);
         const int h = pass * per + sub;
-        const bool mine = in && h < a.Hkv;
+        const bool store = in && h < a.Hkv;
         const size_t row = slot0 + static_cast<size_t>(h) * a.BS, at = row * a.D + at0;
         if constexpr (Fmt::kQuant) {
             // the largest |x| as an integer: infinities and NaN are above every finite number
@@ -597,7 +611,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
                     v0 = Fmt::encode4(&x[k][0].x);
                     v1 = Fmt::encode4(&x[k][2].x);
                 }
-                if (mine) {
+                if (store) {
                     uint8_t* dst = static_cast<uint8_t*>(k ? a.v_cache : a.k_cache) + at;
                     *reinterpret_cast<uint32_t*>(dst) = v0;
                     *reinterpret_cast<uint32_t*>(dst + gap) = v1;
@@ -607,7 +621,7 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
                     }
                 }
             }
-        } else if (mine) {
+        } else if (store) {
             store_runs(static_cast<T*>(a.k_cache) + at, gap, x[0]);
             T* dst = static_cast<T*>(a.v_cache) + at;  // the bits as they are
             *reinterpret_cast<Run*>(dst) = raw[1].v[0];
@@ -658,7 +672,9 @@ static cudaError_t launch_typed(const WriteArgs& a, cudaStream_t stream) {
         // (39 tokens 2.95 -> 2.69 us; two CTAs for 117 tokens 3.0 -> 3.6)
         if (w.wpt_log2 == 3)
             split = std::max(1, std::min((w.qpasses + w.kvpasses + kWriteWarps - 1) / kWriteWarps, 3 * sms / 2 / a.T));
-        const int tpc = kWriteWarps >> w.wpt_log2;
+        w.warps_log2 = std::max(w.wpt_log2, kMinWarpsLog2);
+        cfg.blockDim = dim3(32u << w.warps_log2, 1, 1);
+        const int tpc = 1 << (w.warps_log2 - w.wpt_log2);
         cfg.gridDim = dim3(static_cast<unsigned>((a.T + tpc - 1) / tpc), static_cast<unsigned>(split), 1);
         const int rot = a.half == 0 ? 0 : a.interleaved ? 3 : a.half % 4 == 0 ? 1 : 2;
         auto pick = [&](auto lanes) {
@@ -671,6 +687,10 @@ static cudaError_t launch_typed(const WriteArgs& a, cudaStream_t stream) {
                     : w.lanes == 16 ? pick(std::integral_constant<int, 16>())
                     : w.lanes == 8  ? pick(std::integral_constant<int, 8>())
                                     : pick(std::integral_constant<int, 0>());
+        const int warp_bytes = rot == 0   ? WriteShared<T, 0>::kBytes
+                               : rot == 2 ? WriteShared<T, 2>::kBytes
+                                          : WriteShared<T, 1>::kBytes;  // and 3
+        cfg.dynamicSmemBytes = static_cast<size_t>(warp_bytes) << w.warps_log2;
         err = cudaLaunchKernelEx(&cfg, kern, a, w);
     } else {
         // few tokens: a token's rows over several CTAs
