@@ -27,13 +27,12 @@
 // (64 tokens of 32 + 8 heads 3.2 -> 3.0 us).  The other kernel (any D and alignment) gives a
 // warp one row, one element per lane and step.
 //
-// Bound by instruction issue and load latency, not yet by HBM: 6144 tokens of 32 + 8 heads
-// of 128 in bf16, normalised and rotated into a bf16 cache, 32.9 us for 151 MB, 4.6 TB/s, 69%
-// of the measured copy rate, 57% of the issue slots; without the norm 31.6, as a plain copy
-// through the same registers 31.3 us.  The quantising append of as many tokens of 8 heads: 14
-// us under the profiler, of which 62% of the issue slots.  64 tokens 2.9 us, 1 token 2.2 us:
-// launch and three dependent loads.  Two designs that fed consumer warps by bulk copies
-// through shared memory took 34.8 and 37.5 us on the first case against 35.8 then.
+// Bound by instruction issue, then HBM: 6147 tokens of 32 + 8 heads of 128 in bf16, normalised
+// and rotated into a bf16 cache, 27.2 us for 151 MB, 5.5 TB/s, 83% of the measured copy rate,
+// two thirds of the issue slots.  The quantising append of 5226 tokens of 8 heads 9.7 us for
+// 32 MB, 50%, at as many issue slots.  64 tokens 2.8 us, 1 token 2.3 us: launch and three
+// dependent loads.  Two designs that fed consumer warps by bulk copies, one CTA or two an SM, took 34.8 and 37.5 us on the
+// first case when this one took 35.8.
 #include <algorithm>
 #include <type_traits>
 
@@ -43,12 +42,12 @@ namespace pkv {
 
 constexpr int kWriteWarps = 8;
 constexpr int kWriteMaxD = 256;
-// Pairs of passes of one token, where there are enough tokens.  64 + 8 heads, 5226 and 10697
-// tokens: 4 pairs 48.7 and 95.1, 8 44.1 and 85.9, 16 47.0 and 82.7 us.
+constexpr int kSmShared = 228 * 1024;  // an SM's, of which a CTA takes 1 KB besides its own
+// Pairs of passes of one token, where there are enough tokens.  128 + 8 heads, 2420 and 10697
+// tokens: 4 pairs 36.5 and 147, 8 31.6 and 124, 16 33.5 and 120 us.
 constexpr int kPairsPerWarp = 8;
 
 int device_sm_count();
-constexpr int kMinWarpsLog2 = 2;
 
 struct WriteArgs {
     void* q_out;
@@ -659,20 +658,20 @@ static cudaError_t launch_typed(const WriteArgs& a, cudaStream_t stream) {
         w.inv_d = 1.0f / static_cast<float>(a.D);
         const int passes = (w.qpasses + 1) / 2 + w.kvpasses;  // pairs of passes
         // Many tokens: a warp takes many passes of one token, which shares the token's place,
-        // angles and weights, and a CTA several tokens; one warp a token only where two of each
-        // would not be resident at once.  32 + 8 heads x 128 in bf16, 5111 tokens: 30 us with a
-        // warp a token, 46 with eight; 1227 tokens: 10.7 with one, 8.9 with two; 425: 8.1, 5.1,
-        // 4.4 with four, 4.0 with eight; 96: 3.6 with four, 3.0 with eight.
+        // angles and weights, and a CTA several tokens; fewer warps a token only where more of
+        // them would not all be resident, eight only up to half of that.  32 + 8 heads x 128 in
+        // bf16: 5226 tokens 24.3 us with a warp a token, 26.1 with two; 1227: 8.9 with one, 7.5
+        // with two; 581: 4.9 with two, 4.3 with four; 254: 3.4 with four, 3.8 with eight.
         w.wpt_log2 = 3;
         int split = 1;
         while (w.wpt_log2 > 0 && passes < kPairsPerWarp << w.wpt_log2 &&
-               (static_cast<long long>(a.T) << w.wpt_log2) >= (w.wpt_log2 > 1 ? 12LL : 24LL) * sms)
+               (static_cast<long long>(a.T) << w.wpt_log2) >= (w.wpt_log2 == 3 ? 12LL : 24LL) * sms)
             --w.wpt_log2;
         // few: a pass per warp, over as many CTAs as that takes and the SMs hold 1.5 of each
         // (39 tokens 2.95 -> 2.69 us; two CTAs for 117 tokens 3.0 -> 3.6)
         if (w.wpt_log2 == 3)
             split = std::max(1, std::min((w.qpasses + w.kvpasses + kWriteWarps - 1) / kWriteWarps, 3 * sms / 2 / a.T));
-        w.warps_log2 = std::max(w.wpt_log2, kMinWarpsLog2);
+        w.warps_log2 = std::max(w.wpt_log2, 2);  // small CTAs: less to wait for at the end (6147 tokens 29.3 -> 27.2 us)
         cfg.blockDim = dim3(32u << w.warps_log2, 1, 1);
         const int tpc = 1 << (w.warps_log2 - w.wpt_log2);
         cfg.gridDim = dim3(static_cast<unsigned>((a.T + tpc - 1) / tpc), static_cast<unsigned>(split), 1);
@@ -690,7 +689,13 @@ static cudaError_t launch_typed(const WriteArgs& a, cudaStream_t stream) {
         const int warp_bytes = rot == 0   ? WriteShared<T, 0>::kBytes
                                : rot == 2 ? WriteShared<T, 2>::kBytes
                                           : WriteShared<T, 1>::kBytes;  // and 3
-        cfg.dynamicSmemBytes = static_cast<size_t>(warp_bytes) << w.warps_log2;
+        // CTAs that are all resident at once are not dealt evenly over the SMs (660 CTAs, 4.3 an SM:
+        // some get 6).  Shared memory that leaves room for just ceil of the mean evens them out:
+        // 2641 tokens of 32 + 8 heads 15.2 -> 13.6 us, 953 8.1 -> 6.4.  Below 4 an SM that would
+        // take more than the 48 KB a kernel has by default.
+        const int per_sm = static_cast<int>((static_cast<long long>(cfg.gridDim.x) * split + sms - 1) / sms);
+        const int even = per_sm >= 4 ? std::min((kSmShared / per_sm - 1024) / 128 * 128, 48 * 1024) : 0;
+        cfg.dynamicSmemBytes = std::max((warp_bytes << w.warps_log2), even);
         err = cudaLaunchKernelEx(&cfg, kern, a, w);
     } else {
         // few tokens: a token's rows over several CTAs
