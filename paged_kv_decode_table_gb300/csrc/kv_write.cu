@@ -260,6 +260,13 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     return r;
 }
 
+// max(|a|, |b|, |c|), NaN if one of them is.
+__device__ __forceinline__ float abs_max(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // The two runs as loaded (bf16: 8 bytes each, float: 16).
 template <typename T>
 struct Runs;
@@ -590,18 +597,18 @@ __global__ void __launch_bounds__(kWriteWarps * 32, kRot == 2 || sizeof(T) == 4 
         const bool store = in && h < a.Hkv;
         const size_t row = slot0 + static_cast<size_t>(h) * a.BS, at = row * a.D + at0;
         if constexpr (Fmt::kQuant) {
-            // the largest |x| as an integer: infinities and NaN are above every finite number
-            uint32_t top[2] = {0u, 0u};
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    top[k] = max(top[k], max(__float_as_uint(x[k][e].x) & 0x7fffffffu, __float_as_uint(x[k][e].y) & 0x7fffffffu));
-            row_reduce<kLanes>(top, w, l, base, [](uint32_t u, uint32_t v) { return max(u, v); });
+            float top[2];  // the largest |x|, NaN if there is one
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const bool finite = top[k] < 0x7f800000u;
-                const float scale = row_scale(__uint_as_float(top[k]), Fmt::kInvQ);
+                top[k] = abs_max(0.f, x[k][0].x, x[k][0].y);
+#pragma unroll
+                for (int e = 1; e < 4; ++e) top[k] = abs_max(top[k], x[k][e].x, x[k][e].y);
+            }
+            row_reduce<kLanes>(top, w, l, base, [](float u, float v) { return abs_max(u, u, v); });
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const bool finite = top[k] < INFINITY;
+                const float scale = row_scale(top[k], Fmt::kInvQ);
                 const float inv = __frcp_rn(scale);
                 uint32_t v0 = 0, v1 = 0;
 #pragma unroll
