@@ -838,63 +838,114 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
 // head): one where there are many, four (over the pieces) where there are few.  The whole
 // call with one and with four: 64 x 32 of them 57.7 and 60.8 us, 512 x 32 114 and 138 us;
 // 8 x 32 in sequences of 100-1000 12.3 and 10.1 us, 8 x 64 in long ones 236 and 231 us.
-// Sequences within one range were written by the main kernel; empty and invalid
-// ones get zeros here.
+// kCuts: the units are the rows at the starts of ranges instead of those of all sequences,
+// where there are fewer of them; a start that cuts a (sequence, group) first joins it (1000
+// sequences of 100-500, 32 and 8 heads 131 -> 118 us, 512 of 128-1024 114 -> 109).
+// Sequences within one range were written by the main kernel; empty and invalid ones get
+// zeros here, with kCuts from CTAs of their own.
+constexpr int kZeroSeqs = 16;
 constexpr int kJoinWarps = 4;
 constexpr int kJoinGroup = 8;
 
-template <typename T, int kUnitWarps>
+template <typename T, int kUnitWarps, bool kCuts>
 __global__ void __launch_bounds__(kJoinWarps * 32)
     decode_q8_join_kernel(const __grid_constant__ Q8Plan pl, const int32_t* __restrict__ seq_lens,
                           const float* __restrict__ part_ml, const float* __restrict__ part_o, T* __restrict__ out,
                           int P, int32_t* status) {
     __shared__ float4 accsh[kJoinWarps][32];
     __shared__ float mlsh[kJoinWarps][2];
-    __shared__ int sums[kJoinWarps][2];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const unsigned units = static_cast<unsigned>(pl.B) * pl.Hq;
-    const unsigned u0 = blockIdx.x * (kJoinWarps / kUnitWarps), u = u0 + warp / kUnitWarps;
-    const int w0 = warp % kUnitWarps;
-    const bool in = u < units;
-    const int b = static_cast<int>((in ? u : u0) / pl.Hq), bfirst = static_cast<int>(u0 / pl.Hq);
-    const int qh = in ? static_cast<int>(u - static_cast<unsigned>(b) * pl.Hq) : 0, grp = qh / pl.R;
+    __shared__ int sums[kCuts ? 36 : 2 * kJoinWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % kUnitWarps;
     // Where the sequence's steps lie in the order, from the lengths: they are older than the
     // main kernel, which launched this one after its own wait, so everything up to the
     // partials' addresses is done before the wait.
-    const int L = seq_lens[b];
-    int all = 0, before = 0;
-    for (int x = threadIdx.x; x < pl.B; x += kJoinWarps * 32) {
-        const int n = q8_steps(seq_lens, x, pl);
-        all += n;
-        before += x < bfirst ? n : 0;
-    }
-    all = __reduce_add_sync(0xffffffffu, all);
-    before = __reduce_add_sync(0xffffffffu, before);
-    if (lane == 0) {
-        sums[warp][0] = all;
-        sums[warp][1] = before;
-    }
-    __syncthreads();
-    all = before = 0;
+    int pieces = 0, f = 0, row = 0;
+    bool invalid = false, empty = false;
+    unsigned u = 0;  // row of out
+    if constexpr (kCuts) {
+        static_assert(kUnitWarps == 1, "rows of a cut");
+        const int per = (pl.R + kJoinWarps - 1) / kJoinWarps, c = 1 + static_cast<int>(blockIdx.x) / per;
+        if (c >= P) {  // a CTA for kZeroSeqs sequences: zeros for those without steps
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+            const int b0 = (static_cast<int>(blockIdx.x) - (P - 1) * per) * kZeroSeqs;
+            for (int b = b0 + warp; b < min(pl.B, b0 + kZeroSeqs); b += kJoinWarps) {
+                if (q8_steps(seq_lens, b, pl) != 0) continue;
+                T* o = out + static_cast<size_t>(b) * pl.Hq * pl.D;
+                for (int e = lane; e < pl.Hq * pl.D; e += 32) o[e] = from_f32<T>(0.f);
+                if (lane == 0 && seq_lens[b] != 0) report(status, PKV_ERR_DEVICE_BOUNDS);
+            }
+            return;
+        }
+        row = (static_cast<int>(blockIdx.x) - (c - 1) * per) * kJoinWarps + warp;
+        int sum = 0, total, carry = 0;
+        for (int x = threadIdx.x; x < pl.B; x += kJoinWarps * 32) sum += pl.NG * q8_steps(seq_lens, x, pl);
+        q8_scan(sum, sums, total);
+        const int W = (total + P - 1) / P;
+        const long long at = static_cast<long long>(c) * W;
+        if (at < total) {  // uniform over the CTA; then one sequence holds step `at`
+            const int start = static_cast<int>(at);
+            for (int base = 0; base < pl.B; base += kJoinWarps * 32) {
+                const int x = base + threadIdx.x, n = x < pl.B ? pl.NG * q8_steps(seq_lens, x, pl) : 0;
+                int tot;
+                const int sb = carry + q8_scan(n, sums, tot);
+                if (n > 0 && sb <= start && start < sb + n) {
+                    sums[33] = x;
+                    sums[34] = sb;
+                    sums[35] = n;
+                }
+                carry += tot;
+                if (carry > start) break;  // same decision in every thread
+            }
+            __syncthreads();
+            const int b = sums[33], n = sums[35] / pl.NG, grp = (start - sums[34]) / n, first = sums[34] + grp * n;
+            f = first / W;
+            if (first < start && f == c - 1 && row < min(pl.R, pl.Hq - grp * pl.R)) {
+                pieces = (first + n - 1) / W - f + 1;
+                u = static_cast<unsigned>(b) * pl.Hq + grp * pl.R + row;
+            }
+        }
+    } else {
+        const unsigned units = static_cast<unsigned>(pl.B) * pl.Hq;
+        const unsigned u0 = blockIdx.x * (kJoinWarps / kUnitWarps);
+        u = u0 + warp / kUnitWarps;
+        const bool in = u < units;
+        const int b = static_cast<int>((in ? u : u0) / pl.Hq), bfirst = static_cast<int>(u0 / pl.Hq);
+        const int qh = in ? static_cast<int>(u - static_cast<unsigned>(b) * pl.Hq) : 0, grp = qh / pl.R;
+        const int n = q8_steps(seq_lens, b, pl);
+        int all = 0, before = 0;
+        for (int x = threadIdx.x; x < pl.B; x += kJoinWarps * 32) {
+            const int k = q8_steps(seq_lens, x, pl);
+            all += k;
+            before += x < bfirst ? k : 0;
+        }
+        all = __reduce_add_sync(0xffffffffu, all);
+        before = __reduce_add_sync(0xffffffffu, before);
+        if (lane == 0) {
+            sums[2 * warp] = all;
+            sums[2 * warp + 1] = before;
+        }
+        __syncthreads();
+        all = before = 0;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        all += sums[w][0];
-        before += sums[w][1];
+        for (int w = 0; w < kJoinWarps; ++w) {
+            all += sums[2 * w];
+            before += sums[2 * w + 1];
+        }
+        for (int x = bfirst; x < b; ++x) before += q8_steps(seq_lens, x, pl);
+        if (in && n > 0) {
+            const int W = (all * pl.NG + P - 1) / P, first = before * pl.NG + grp * n;
+            f = first / W;
+            pieces = (first + n - 1) / W - f + 1;
+        }
+        empty = in && n == 0;
+        invalid = empty && seq_lens[b] != 0 && qh == 0 && w0 == 0;
+        row = qh - grp * pl.R;
     }
-    for (int x = bfirst; x < b; ++x) before += q8_steps(seq_lens, x, pl);
-    const bool valid = L >= 0 && static_cast<long long>(L) <= static_cast<long long>(pl.max_blocks) * pl.BS;
-    const int n = valid ? q8_steps(seq_lens, b, pl) : 0;
-    int pieces = 0, f = 0;
-    if (in && n > 0) {
-        const int W = (all * pl.NG + P - 1) / P, first = before * pl.NG + grp * n;
-        f = first / W;
-        pieces = (first + n - 1) / W - f + 1;
-    }
-    const int row = qh - grp * pl.R;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (in && !valid && qh == 0 && w0 == 0 && lane == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
-    const bool write = in && pieces != 1;
+    if (invalid && lane == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
+    const bool write = empty || pieces > 1;
     if (kUnitWarps == 1 && !write) return;
     if (pieces == 1) pieces = 0;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1164,13 +1215,19 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
         return cudaGetLastError();
     }
     const long long units = static_cast<long long>(pl.B) * pl.Hq;
-    const bool many = units >= 8LL * P;
-    cfg.gridDim = dim3(static_cast<unsigned>(many ? (units + kJoinWarps - 1) / kJoinWarps : units), 1, 1);
+    const bool many = units >= 8LL * P, cuts = many && pl.B * static_cast<long long>(pl.NG) > P && P > 1;
+    const long long per_cut = (pl.R + kJoinWarps - 1) / kJoinWarps;
+    cfg.gridDim = dim3(static_cast<unsigned>(cuts   ? (P - 1) * per_cut + (pl.B + kZeroSeqs - 1) / kZeroSeqs
+                                             : many ? (units + kJoinWarps - 1) / kJoinWarps
+                                                    : units),
+                       1, 1);
     cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    err = cudaLaunchKernelEx(&cfg, many ? decode_q8_join_kernel<T, 1> : decode_q8_join_kernel<T, kJoinWarps>, pl,
-                             seq_lens, static_cast<const float*>(part_ml), static_cast<const float*>(part_o),
-                             static_cast<T*>(out), P, status);
+    auto join = cuts   ? decode_q8_join_kernel<T, 1, true>
+                : many ? decode_q8_join_kernel<T, 1, false>
+                       : decode_q8_join_kernel<T, kJoinWarps, false>;
+    err = cudaLaunchKernelEx(&cfg, join, pl, seq_lens, static_cast<const float*>(part_ml),
+                             static_cast<const float*>(part_o), static_cast<T*>(out), P, status);
     if (err != cudaSuccess) return err;
     *done = true;
     return cudaGetLastError();

@@ -267,6 +267,31 @@ def test_attention_split_over_many_ranges(Hq, Hkv, D, lens, fmt):
     run_attention(Hq, Hkv, D, 16, lens, fmt, "f32", seed=13, scale=0.37)
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 64), (36, 9, 80), (20, 2, 128)])
+def test_attention_of_more_sequences_than_sms(Hq, Hkv, D):
+    """More (sequence, head group) pairs than ranges: joined where a range cuts one; empty
+    sequences, bad lengths and bad blocks between them."""
+    lens = [(0, 5, 90, 0, 333, 17)[b % 6] for b in range(400)]
+    lens[57] = 3000
+    for dtype in DTYPES:
+        out = run_attention(Hq, Hkv, D, 16, lens, "e4m3", dtype, seed=15)
+        assert bool((out[::6] == 0).all())
+    g = torch.Generator().manual_seed(16)
+    bt, nb = R.tables(lens, 16, g)
+    k, v, ks, vs = R.random_cache(nb, Hkv, 16, D, "i8", g)
+    q = torch.randn(400, Hq, D, generator=g).bfloat16()
+    bad_bt, bad_lens = bt.clone(), list(lens)
+    bad_lens[1], bad_lens[399], bad_bt[57, 100], bad_bt[4, 3] = -1, bt.shape[1] * 16 + 1, nb, -7
+    bad = [1, 399, 57, 4]
+    good = [b for b in range(400) if b not in bad]
+    st = pkv.new_status()
+    out = pkv.paged_decode_attention_q8(*cuda(q, k, v, ks, vs, bad_bt, i32(bad_lens)), status=st)
+    assert pkv.check_status(st) == 4
+    assert bool((out[bad] == 0).all())
+    ref, tol = R.attention(q, k, v, ks, vs, bt, lens, dtype="bf16")
+    assert bool(((out.cpu().double() - ref).abs() <= tol)[good].all())
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_attention_wide_scales(fmt):
     """V scales and scores spread over many orders of magnitude: the weights are
