@@ -211,8 +211,9 @@ __device__ __forceinline__ uint32_t q8_at(int tok, int c, const Q8Plan& pl) {
     return static_cast<uint32_t>(tok * 128 + ((c ^ (tok & 7)) << 4));
 }
 
-// DP: dimensions computed (64, 96 or 128; D may be smaller; 96 of 128 for D = 80 and 96 took
-// 15.6 -> 14.3 us off 37 float32 sequences of up to 1500); kN: n-tiles of 8 query heads per
+// DP: dimensions computed (32, 64, 96 or 128; D may be smaller).  96 of 128 for D = 80 took 37
+// float32 sequences of up to 1500 from 15.6 to 14.3 us, 32 of 64 for D = 32 169 sequences of
+// 1733-3682 with 10 query heads a group from 107 to 86 us.  kN: n-tiles of 8 query heads per
 // warp; kSplit: float32 accuracy (see above); kSub: tiles a warp takes of a step.
 template <typename T, typename Fmt, int DP, int kN, bool kSplit, int kSub>
 __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
@@ -223,9 +224,9 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                      float* __restrict__ part_ml, float* __restrict__ part_o,
                      int32_t* status) {
     constexpr int kChunks = DP / 16;
-    // chunks from here on may lie behind D: a K byte there is the next row's, and an e4m3 NaN
+    // the last chunk may lie behind D: a K byte there is the next row's, and an e4m3 NaN
     // survives the product with q's zero
-    constexpr int kMaybe = !Fmt::kHasNaN ? kChunks : DP == 64 ? 1 : kChunks - 1;
+    constexpr int kMaybe = !Fmt::kHasNaN ? kChunks : kChunks - 1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int nst = pl.nst, HG = pl.HG, QC = pl.QC, slots = pl.slots;
@@ -1168,7 +1169,7 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
                                   void* workspace, int P, int32_t* status, cudaStream_t stream, bool* done) {
     *done = false;
     constexpr bool kSplit = sizeof(T) == 4;
-    constexpr int kSub = DP == 64 ? 4 : 2;
+    constexpr int kSub = DP <= 64 ? 4 : 2;
     const int tiles = pl.HG * pl.slots * kSub;
     pl.stage_bytes = 2 * tiles * kQ8Tok * pl.D;
     pl.scale_unit = pl.HG * kQ8Tok * 4;
@@ -1246,15 +1247,22 @@ static cudaError_t launch_q8(Q8Plan pl, bool fast, void* out, const void* q, con
         };
         using I1 = std::integral_constant<int, 1>;
         using I2 = std::integral_constant<int, 2>;
+        using I32 = std::integral_constant<int, 32>;
         using I64 = std::integral_constant<int, 64>;
         using I96 = std::integral_constant<int, 96>;
         using I128 = std::integral_constant<int, 128>;
         auto go = [&]() {
             if constexpr (sizeof(T) == 2) {
                 if (pl.G > 8)
-                    return pl.D <= 64 ? run(I64(), I2()) : pl.D <= 96 ? run(I96(), I2()) : run(I128(), I2());
+                    return pl.D <= 32   ? run(I32(), I2())
+                           : pl.D <= 64 ? run(I64(), I2())
+                           : pl.D <= 96 ? run(I96(), I2())
+                                        : run(I128(), I2());
             }
-            return pl.D <= 64 ? run(I64(), I1()) : pl.D <= 96 ? run(I96(), I1()) : run(I128(), I1());
+            return pl.D <= 32   ? run(I32(), I1())
+                   : pl.D <= 64 ? run(I64(), I1())
+                   : pl.D <= 96 ? run(I96(), I1())
+                                : run(I128(), I1());
         };
         // Few and short sequences (by the table's width): a CTA for each (sequence, head
         // group) and no join, with as many groups as there are SMs for.
