@@ -43,12 +43,12 @@
 // Other shapes: one CTA per (sequence, query head), CUDA-core fp32.
 //
 // What bounds it: HBM where the cache is large.  8 sequences of 32768-131072 positions, 64
-// query and 8 KV heads of 128 in int8: 231 us for 1.53 GB, 6.6 TB/s, 99% of the measured
+// query and 8 KV heads of 128 in int8: 233 us for 1.53 GB, 6.6 TB/s, 98% of the measured
 // copy rate.  64 sequences of 512-4096, 32 and 8 heads: 58 us for 332 MB, 86%; the rest is
 // the start (2.5 us), the end of the slowest SM (2.3 us) and the join (3.5 us).  With the
 // arithmetic left out the same kernel takes 57 us, so the tensor and issue pipes (17% and
 // 32% busy) hide behind the copies.  They do not with 16 query heads a group (128 and 8
-// heads: 85 us, 58%) and with float32 queries (63 us, 79%; two MMAs for one).  One short
+// heads: 84 us, 59%) and with float32 queries (63 us, 78%; two MMAs for one).  One short
 // sequence is a chain of latencies, lengths -> block ids -> K and V -> result: 6.4 us.
 // mma.sync and not tcgen05: a float16 query needs float16 keys, so the converted numbers, twice
 // the bytes that came, would go back to shared memory before tcgen05.mma could read them,
@@ -213,7 +213,7 @@ __device__ __forceinline__ uint32_t q8_at(int tok, int c, const Q8Plan& pl) {
 
 // DP: dimensions computed (32, 64, 96 or 128; D may be smaller).  96 of 128 for D = 80 took 37
 // float32 sequences of up to 1500 from 15.6 to 14.3 us, 32 of 64 for D = 32 169 sequences of
-// 1733-3682 with 10 query heads a group from 107 to 86 us.  kN: n-tiles of 8 query heads per
+// 1733-3682 with 10 query heads a group from 107 to 86 us (81 with two floats an instruction).  kN: n-tiles of 8 query heads per
 // warp; kSplit: float32 accuracy (see above); kSub: tiles a warp takes of a step.
 template <typename T, typename Fmt, int DP, int kN, bool kSplit, int kSub>
 __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
@@ -545,13 +545,16 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 const float lg = lg2f(fmaxf(fabsf(vv), kMinScale));
                 vsc[k][t] = in ? vv : 0.f;
 #pragma unroll
-                for (int n = 0; n < kN; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float a = (s[n][0][2 * t + e] + s[n][1][2 * t + e]) * (kk * smul[n][e]);
-                        x[k][n][2 * t + e] = in ? a : -INFINITY;
-                        tmax[n][e] = fmaxf(tmax[n][e], in ? a + lg : -INFINITY);
-                    }
+                for (int n = 0; n < kN; ++n) {
+                    const float2 sum = add2(make_float2(s[n][0][2 * t], s[n][0][2 * t + 1]),
+                                            make_float2(s[n][1][2 * t], s[n][1][2 * t + 1]));
+                    const float2 a = mul2(sum, mul2(make_float2(kk, kk), make_float2(smul[n][0], smul[n][1])));
+                    const float2 c = add2(a, make_float2(lg, lg));
+                    x[k][n][2 * t] = in ? a.x : -INFINITY;
+                    x[k][n][2 * t + 1] = in ? a.y : -INFINITY;
+                    tmax[n][0] = fmaxf(tmax[n][0], in ? c.x : -INFINITY);
+                    tmax[n][1] = fmaxf(tmax[n][1], in ? c.y : -INFINITY);
+                }
             }
         }
 #pragma unroll
@@ -601,10 +604,13 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             for (int n = 0; n < kN; ++n)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const float p0 = ex2f_subnormal(x[k][n][2 * t] - mu[n][0]), p1 = ex2f_subnormal(x[k][n][2 * t + 1] - mu[n][1]);
-                    l[n][0] += p0;
-                    l[n][1] += p1;
-                    const float w0 = p0 * vsc[k][t], w1 = p1 * vsc[k][t];
+                    const float2 d = add2(make_float2(x[k][n][2 * t], x[k][n][2 * t + 1]), make_float2(-mu[n][0], -mu[n][1]));
+                    const float2 p = make_float2(ex2f_subnormal(d.x), ex2f_subnormal(d.y));
+                    const float2 sum = add2(make_float2(l[n][0], l[n][1]), p);
+                    l[n][0] = sum.x;
+                    l[n][1] = sum.y;
+                    const float2 wt = mul2(p, make_float2(vsc[k][t], vsc[k][t]));
+                    const float w0 = wt.x, w1 = wt.y;
                     const uint32_t hi = pack_f16x2(w0, w1);
                     pb[n][t] = transpose_8x8(hi);
                     if constexpr (kSplit) {

@@ -242,24 +242,6 @@ __global__ void __launch_bounds__(kWriteWarps * 32) kv_write_any_kernel(const Wr
 }
 
 // ------------------------------------------------------------------ vector kernel
-// A lane's 8 elements are two runs of 4, A and B, each as two packed pairs of floats
-// (fma.rn.f32x2: two roundings per instruction).
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;"
-        : "=l"(reinterpret_cast<unsigned long long&>(r))
-        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
-          "l"(reinterpret_cast<unsigned long long&>(c)));
-    return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;"
-        : "=l"(reinterpret_cast<unsigned long long&>(r))
-        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
-    return r;
-}
-
 // max(|a|, |b|, |c|), NaN if one of them is.
 __device__ __forceinline__ float abs_max(float a, float b, float c) {
     float r;
@@ -267,6 +249,7 @@ __device__ __forceinline__ float abs_max(float a, float b, float c) {
     return r;
 }
 
+// A lane's 8 elements are two runs of 4, A and B, each as two packed pairs of floats.
 // The two runs as loaded (bf16: 8 bytes each, float: 16).
 template <typename T>
 struct Runs;
