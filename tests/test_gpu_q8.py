@@ -457,6 +457,12 @@ PREPARE = [  # (Hq, Hkv, D, BS, rot, interleaved, norms, lens, counts)
     (6, 3, 128, 32, 40, False, False, [650, 90, 5], [650, 33, 5]),
     (2, 2, 64, 16, 0, False, True, [100620, 44], [620, 2]),
     (5, 5, 64, 16, 22, True, True, [700, 9], [610, 9]),
+    # more: two warps a token, then one
+    (4, 1, 128, 16, 128, False, True, [1500, 90], [1400, 7]),
+    (3, 1, 64, 16, 26, False, True, [2700, 40], [2600, 30]),
+    (4, 2, 64, 16, 48, True, True, [2700], [2600]),
+    (2, 1, 128, 16, 0, False, True, [2100, 3], [2000, 0]),
+    (6, 2, 80, 32, 80, False, False, [7000], [6900]),
 ]
 
 
@@ -590,6 +596,32 @@ def test_many_tokens_in_place_with_rows_behind_and_bad_sequences():
             if b != bad_len and int(bt[b, pos // BS]) < nb:
                 wk[int(bt[b, pos // BS]), :, pos % BS], wv[int(bt[b, pos // BS]), :, pos % BS] = k[t], v[t]
     assert torch.equal(kc.cpu(), wk) and torch.equal(vc.cpu(), wv)
+
+
+@pytest.mark.parametrize("D,rot,inter", [(128, 128, False), (64, 26, False), (80, 48, True), (128, 0, False)])
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("n", [1, 30, 300, 700])
+def test_in_place_is_the_same_bits(D, rot, inter, dtype, n):
+    """q_out is q, with rows copied ahead of their use; one sequence of five cannot be placed."""
+    Hq, Hkv, BS, B = 8, 2, 16, 5
+    g = torch.Generator().manual_seed(34)
+    lens = [n + 11 * b for b in range(B)]
+    bt, nb = R.tables(lens, BS, g)
+    lens[3] = n - 1  # shorter than its chunk
+    qs = i32([n * b for b in range(B + 1)]).cuda()
+    q, k, v = (torch.randn(n * B, h, D, generator=g).to(DTYPES[dtype]).cuda() for h in (Hq, Hkv, Hkv))
+    w = torch.rand(D, generator=g).to(DTYPES[dtype]).cuda()
+    args = (1e-6, pkv.rope_freqs(rot) if rot else None)
+    runs = []
+    for own in (True, False):
+        qq = q.clone()
+        pools = [torch.zeros(nb, Hkv, BS, D, dtype=DTYPES[dtype], device="cuda") for _ in range(2)]
+        st = pkv.new_status()
+        out = pkv.qk_norm_rope_append(qq, k, v, w, w, *args, *pools, bt.cuda(), i32(lens).cuda(), q_start=qs,
+                                      interleaved=inter, q_out=qq if own else None, status=st)
+        assert pkv.check_status(st) == 4 and bool((out[3 * n:4 * n] == 0).all())
+        runs.append((out, *pools))
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
 
 
 def test_norm_rope_append_bad_sequences():
