@@ -335,7 +335,8 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
         int cn = q8_steps(seq_lens, b, pl), cL = seq_lens[b], g = 0;
         struct Step {
             int b, g, j, n, cs, L;
-            int blk;  // lane u: the block of unit u, -1: invalid, -2: behind the end
+            bool in;  // lane u: unit u lies before the end
+            int blk;  // lane u: the block of unit u as the table has it, any integer
             int tok;  // lane u: the unit's first slot in its block
         };
         auto fetch = [&](int i) {  // walk on to step i
@@ -348,9 +349,10 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                     cL = seq_lens[b];
                 }
             }
-            Step s{b, g, i - cs, cn, cs, cL, -2, 0};
+            Step s{b, g, i - cs, cn, cs, cL, false, -1, 0};
             const unsigned u = static_cast<unsigned>(s.j) * units + lane;
             if (lane < units && u * kQ8Tok < static_cast<unsigned>(cL)) {
+                s.in = true;
                 const unsigned lb = pl.UB == 1 ? u : u / static_cast<unsigned>(pl.UB);
                 s.tok = static_cast<int>(u - lb * pl.UB) * kQ8Tok;
                 s.blk = block_tables[static_cast<size_t>(b) * pl.max_blocks + lb];
@@ -392,9 +394,9 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             cur = nxt;
             if (i + 2 < end) nxt = fetch(i + 2);
             const bool first = s.j == 0 || i == start, last = s.j == s.n - 1 || i == end - 1;
-            const bool good = s.blk >= 0 && s.blk < pl.NB;
+            const bool good = s.in && s.blk >= 0 && s.blk < pl.NB;
             const unsigned live = __ballot_sync(0xffffffffu, good);
-            const bool bad = __any_sync(0xffffffffu, s.blk != -2 && !good);
+            const bool bad = __any_sync(0xffffffffu, s.in && !good);
             bool ok = mbar_wait(&empty[stage], parity, pl.polls);
             if (first && ok) ok = mbar_wait(&qempty[piece & 1], (static_cast<uint32_t>(piece >> 1) & 1u) ^ 1u, pl.polls);
             if (!__all_sync(0xffffffffu, ok)) {
