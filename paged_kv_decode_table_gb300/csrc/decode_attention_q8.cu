@@ -28,15 +28,18 @@
 //    transposed in 16-bit units, which yields even and odd dimensions of two
 //    positions, and rows g and g + 8 of the MMA are dimensions 2g and 2g + 1.
 //    movmatrix turns the weights from S^T's layout into P^T's.
-//  * bf16 queries are exact in float16 and the weights are rounded to it (2^-11);
+//  * bf16 queries are exact in float16 and the weights are rounded to it (2^-11 of a
+//    weight, at least 2^-34 of the largest);
 //    float32 queries carry what that rounding leaves of q and of the weights in a
-//    second float16 and a second MMA (kSplit), and sum each step apart before
-//    adding it: the result is within 7e-7 of the exact one in the 2-norm over
-//    500 to 60000 positions (1.0e-6 without the separate sums).
+//    second float16, the weights' 2^11 times as large, and a second MMA (kSplit: 2^-22
+//    and 2^-45), and sum each step apart before adding it.  The 2-norm of the error is
+//    below 6e-7 of the result for random float32 queries over 500 to 60000 positions;
+//    with one weight 2^25 times as large as each of 32767 behind it, all in one warp,
+//    1.1e-5, which are the roundings of the float32 running sums.
 //  * Weights are normalised by a running maximum of s_j + log2(vs_j), the largest
 //    contribution rather than the largest score, so that p_j * vs_j fits float16
 //    whatever the V scales are.  Scales below 2^-64 count as 2^-64 there, which
-//    bounds p_j by 2^72.  The maximum is renewed (shuffles, rescaled sums) only
+//    bounds p_j by 2^77.  The maximum is renewed (shuffles, rescaled sums) only
 //    when a contribution exceeds it by 2^kLag: a vote decides.
 //  * q is multiplied by a power of two per head that puts its largest element into
 //    [2^14, 2^15).
@@ -80,7 +83,12 @@ constexpr int kQ8Warps = 8;  // consumer warps at most
 // up to 256 positions, 32 and 8 heads 6.4 : 8.5 us, 16 of up to 512 8.5 : 11.2 us; at 1024 (6
 // steps) 9.1 : 8.8 us for one, 10.8 : 9.0 for four, 12.2 : 12.6 for 16.
 constexpr int kDirectSteps = 3;
-constexpr float kLag = 8.f;  // contributions stay below 2^8 of the running maximum
+// Contributions stay below 2^kLag of the running maximum, and weights are 2^kShift times as
+// large as relative to it, so that the float16 ones, at most 2^13, reach down to 2^-34 of the
+// largest.  (The 2^3 up to float16's limit are for scores so large that their own rounding is
+// a factor.)
+constexpr float kLag = 4.f, kShift = 9.f;
+constexpr float kLowUp = 2048.f;  // what the second float16 of a weight is scaled by
 
 // How a call is laid out; computed on the host, passed to both kernels.
 struct Q8Plan {
@@ -211,6 +219,9 @@ __device__ __forceinline__ uint32_t q8_at(int tok, int c, const Q8Plan& pl) {
     return static_cast<uint32_t>(tok * 128 + ((c ^ (tok & 7)) << 4));
 }
 
+// Floats of a warp's place for accumulators set aside: its heads' sums and maxima.
+__host__ __device__ constexpr int q8_aside_floats(int DP, int kN) { return 8 * kN * DP + 64 * kN; }
+
 // DP: dimensions computed (32, 64, 96 or 128; D may be smaller).  96 of 128 for D = 80 took 37
 // float32 sequences of up to 1500 from 15.6 to 14.3 us, 32 of 64 for D = 32 169 sequences of
 // 1733-3682 with 10 query heads a group from 107 to 86 us (81 with two floats an instruction).  kN: n-tiles of 8 query heads per
@@ -221,7 +232,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                      const __grid_constant__ Q8Plan pl, const T* __restrict__ q, T* __restrict__ out,
                      const float* __restrict__ k_scale, const float* __restrict__ v_scale,
                      const int32_t* __restrict__ block_tables, const int32_t* __restrict__ seq_lens,
-                     float* __restrict__ part_ml, float* __restrict__ part_o,
+                     float* __restrict__ part_ml, float* __restrict__ part_o, float* __restrict__ aside,
                      int32_t* status) {
     constexpr int kChunks = DP / 16;
     // the last chunk may lie behind D: a K byte there is the next row's, and an e4m3 NaN
@@ -472,7 +483,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     uint32_t qb[kN][kChunks][2];
     [[maybe_unused]] uint32_t ql[kSplit ? kN : 1][kSplit ? kChunks : 1][2];
     float smul[kN][2];  // what a score of heads 8 n + 2 r + e is multiplied by
-    float m[kN][2], mu[kN][2], l[kN][2];  // of heads 8 n + 2 r + e; mu: m, or 0 where m is -inf
+    float m[kN][2], mu[kN][2], l[kN][2];  // of heads 8 n + 2 r + e; mu: m - kShift where m is finite
     bool poisoned = false;
     int piece = 0, stage = 0;
     uint32_t parity = 0;
@@ -573,8 +584,9 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
                     const float mn = fmaxf(m[n][e], mx);
-                    mu[n][e] = mn == -INFINITY ? 0.f : mn;
-                    al[e] = ex2f(m[n][e] - mu[n][e]);
+                    const float base = mn == -INFINITY ? 0.f : mn;
+                    mu[n][e] = base - kShift;
+                    al[e] = ex2f(m[n][e] - base);
                     m[n][e] = mn;
                     l[n][e] *= al[e];
                 }
@@ -587,76 +599,154 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 }
             }
         }
-        // kSplit: the step's products are summed apart and added to the running sums by
-        // rounded additions, because the MMA's own accumulation truncates
-        [[maybe_unused]] float F[kSplit ? kChunks : 1][kSplit ? kN : 1][4];
-        if constexpr (kSplit) {
+        // ---- weights, float16, in P^T's layout.  Their sum is taken over the step first: one
+        // by one, those below 2^-24 of the running sum would leave it as it is.
+        float2 lsum[kN];
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-                for (int n = 0; n < kN; ++n) F[c][n][0] = F[c][n][1] = F[c][n][2] = F[c][n][3] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < kSub; ++k) {
-            if (kPart && k * tok_next >= ntok) break;
-            // ---- weights, float16, in P^T's layout
-            uint32_t pb[kN][2];
-            [[maybe_unused]] uint32_t pl2[kSplit ? kN : 1][2];
+        for (int n = 0; n < kN; ++n) lsum[n] = make_float2(0.f, 0.f);
+        auto weights = [&](int k, uint32_t (&hi)[kN][2], uint32_t (&lo)[kSplit ? kN : 1][2]) {
 #pragma unroll
             for (int n = 0; n < kN; ++n)
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const float2 d = add2(make_float2(x[k][n][2 * t], x[k][n][2 * t + 1]), make_float2(-mu[n][0], -mu[n][1]));
                     const float2 p = make_float2(ex2f_subnormal(d.x), ex2f_subnormal(d.y));
-                    const float2 sum = add2(make_float2(l[n][0], l[n][1]), p);
-                    l[n][0] = sum.x;
-                    l[n][1] = sum.y;
+                    lsum[n] = add2(lsum[n], p);
                     const float2 wt = mul2(p, make_float2(vsc[k][t], vsc[k][t]));
-                    const float w0 = wt.x, w1 = wt.y;
-                    const uint32_t hi = pack_f16x2(w0, w1);
-                    pb[n][t] = transpose_8x8(hi);
+                    const uint32_t h = pack_f16x2(wt.x, wt.y);
+                    hi[n][t] = transpose_8x8(h);
                     if constexpr (kSplit) {
-                        const float2 f = unpack_f16x2(hi);
-                        pl2[n][t] = transpose_8x8(pack_f16x2(w0 - f.x, w1 - f.y));
+                        const float2 f = unpack_f16x2(h);
+                        lo[n][t] = transpose_8x8(pack_f16x2((wt.x - f.x) * kLowUp, (wt.y - f.y) * kLowUp));
                     }
                 }
-            // ---- O^T += V^T P^T.  Positions behind the end have weight 0; their bytes
-            // are cleared because an e4m3 NaN would survive the product.
-            const uint32_t vb = kb0 + half_stage + k * tile_next;
-            uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
-            if (kPart) {
-                const int left = ntok - k * tok_next - 2 * r;
-                keep0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
-                keep1 = (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
+        };
+        // V of tile k, chunks c and c + 1.  Positions behind the end have weight 0; their bytes are
+        // cleared because an e4m3 NaN would survive the product.
+        auto load_v = [&](int k, int c, uint32_t (&w)[4]) {
+            ldmatrix_x4_trans(w[0], w[1], w[2], w[3], kb0 + half_stage + k * tile_next + lm[c / 2]);
+            if (!kPart) return;
+            const int left = ntok - k * tok_next - 2 * r;
+            const uint32_t keep0 = (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+            const uint32_t keep1 = (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
+            w[0] &= keep0;
+            w[1] &= keep1;
+            w[2] &= keep0;
+            w[3] &= keep1;
+        };
+        // ---- O^T += V^T P^T
+        if constexpr (kSplit) {
+            // A step's products are summed apart (F; with the weights' second float16, 2^11 times as
+            // large, E) and added by rounded additions: the MMA truncates what it adds to about 2^-24
+            // of its accumulator.
+            uint32_t pb[kSub][kN][2], pl2[kSub][kN][2];
+#pragma unroll
+            for (int k = 0; k < kSub; ++k) {
+                if (kPart && k * tok_next >= ntok) break;
+                weights(k, pb[k], pl2[k]);
             }
 #pragma unroll
             for (int c = 0; c < kChunks; c += 2) {
-                uint32_t w[4];
-                ldmatrix_x4_trans(w[0], w[1], w[2], w[3], vb + lm[c / 2]);
+                float F[2][kN][4], E[2][kN][4];
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    uint32_t a[4];
-                    Fmt::decode4_pairs(kPart ? w[2 * u] & keep0 : w[2 * u], a[0], a[1]);
-                    Fmt::decode4_pairs(kPart ? w[2 * u + 1] & keep1 : w[2 * u + 1], a[2], a[3]);
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int n = 0; n < kN; ++n) {
-                        if constexpr (kSplit) {
-                            mma_f16_16816(F[c + u][n], a, pl2[n][0], pl2[n][1]);
-                            mma_f16_16816(F[c + u][n], a, pb[n][0], pb[n][1]);
-                        } else {
-                            mma_f16_16816(O[c + u][n], a, pb[n][0], pb[n][1]);
+                    for (int n = 0; n < kN; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) F[u][n][e] = E[u][n][e] = 0.f;
+#pragma unroll
+                for (int k = 0; k < kSub; ++k) {
+                    if (kPart && k * tok_next >= ntok) break;
+                    uint32_t w[4];
+                    load_v(k, c, w);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t a[4];
+                        Fmt::decode4_pairs(w[2 * u], a[0], a[1]);
+                        Fmt::decode4_pairs(w[2 * u + 1], a[2], a[3]);
+#pragma unroll
+                        for (int n = 0; n < kN; ++n) {
+                            mma_f16_16816(E[u][n], a, pl2[k][n][0], pl2[k][n][1]);
+                            mma_f16_16816(F[u][n], a, pb[k][n][0], pb[k][n][1]);
                         }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int n = 0; n < kN; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) O[c + u][n][e] += fmaf(E[u][n][e], 1.f / kLowUp, F[u][n][e]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kSub; ++k) {
+                if (kPart && k * tok_next >= ntok) break;
+                uint32_t pb[kN][2], none[1][2];
+                weights(k, pb, none);
+#pragma unroll
+                for (int c = 0; c < kChunks; c += 2) {
+                    uint32_t w[4];
+                    load_v(k, c, w);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t a[4];
+                        Fmt::decode4_pairs(w[2 * u], a[0], a[1]);
+                        Fmt::decode4_pairs(w[2 * u + 1], a[2], a[3]);
+#pragma unroll
+                        for (int n = 0; n < kN; ++n) mma_f16_16816(O[c + u][n], a, pb[n][0], pb[n][1]);
                     }
                 }
             }
         }
-        if constexpr (kSplit) {
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
+        for (int n = 0; n < kN; ++n) {
+            const float2 sum = add2(make_float2(l[n][0], l[n][1]), lsum[n]);
+            l[n][0] = sum.x;
+            l[n][1] = sum.y;
+        }
+    };
+
+    // bf16: the MMA truncates what it adds to about 2^-24 of its accumulator, so that of a long
+    // tail behind one large weight little would be left.  Every kAside steps (4096 positions of a
+    // warp, at most 2^-12 of the result lost in them) the accumulators are added, rescaled, to this
+    // warp's place in the workspace and begin again at zero; a range's last ones fetch what is there.
+    // The code for it costs about 1% (64 x 512-4096 58.2 -> 58.4 us, 8 x 32K-128K 233.7 -> 235.6), summing
+    // every step apart as above up to 5%, and 16 heads a group have no registers for that (128
+    // and 8 heads 84 -> 103 us).
+    constexpr int kAside = 4096 / (kQ8Tok * kSub);
+    [[maybe_unused]] int steps = 0;  // of this piece so far
+    [[maybe_unused]] auto set_aside = [&](bool leave) {
+        float* tile = aside + (static_cast<size_t>(blockIdx.x) * kQ8Warps + warp) * q8_aside_floats(DP, kN);
+        float4* to = reinterpret_cast<float4*>(tile) + lane;
+        float2* to_m = reinterpret_cast<float2*>(tile + DP * kHeads) + lane;
+        const bool old = steps > kAside;
 #pragma unroll
-                for (int n = 0; n < kN; ++n)
+        for (int n = 0; n < kN; ++n) {
+            float f[2] = {0.f, 0.f};
+            if (old) {
+                const float2 mo = to_m[n * 32];
+                f[0] = ex2f(mo.x - (m[n][0] == -INFINITY ? 0.f : m[n][0]));
+                f[1] = ex2f(mo.y - (m[n][1] == -INFINITY ? 0.f : m[n][1]));
+            }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) O[c][n][e] += F[c][n][e];
+            for (int c = 0; c < kChunks; ++c) {
+                float4* at = to + (c * kN + n) * 32;
+                float4 v = make_float4(O[c][n][0], O[c][n][1], O[c][n][2], O[c][n][3]);
+                if (old) {
+                    const float4 o = *at;
+                    v = make_float4(fmaf(o.x, f[0], v.x), fmaf(o.y, f[1], v.y), fmaf(o.z, f[0], v.z), fmaf(o.w, f[1], v.w));
+                }
+                if (!leave) {
+                    *at = v;
+                    v = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                O[c][n][0] = v.x;
+                O[c][n][1] = v.y;
+                O[c][n][2] = v.z;
+                O[c][n][3] = v.w;
+            }
+            if (!leave) to_m[n * 32] = make_float2(m[n][0], m[n][1]);
         }
     };
 
@@ -714,6 +804,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&qempty[qs]);
             poisoned = false;
+            if constexpr (!kSplit) steps = 0;
 #pragma unroll
             for (int n = 0; n < kN; ++n) {
 #pragma unroll
@@ -738,6 +829,11 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
         if (++stage == nst) {
             stage = 0;
             parity ^= 1u;
+        }
+        if constexpr (!kSplit) {
+            ++steps;
+            const bool leave = mt.flags & kQLast;
+            if (leave ? steps > kAside : steps % kAside == 0) set_aside(leave);
         }
         if (!(mt.flags & kQLast)) continue;
 
@@ -1116,7 +1212,7 @@ __global__ void __launch_bounds__(kGen8Threads)
 
 // ------------------------------------------------------------------ host side
 struct Q8Layout {  // workspace
-    size_t o, total;
+    size_t o, aside, total;
 };
 
 // Group size and slots for a shape, with at least min_groups head groups where the heads
@@ -1144,11 +1240,14 @@ static bool q8_shape(int Hq, int Hkv, int D, int BS, pkv_dtype dt, int min_group
 }
 
 // Two partial results per CTA of (max, sum) and D floats for every row of a group.
-static Q8Layout q8_layout(int R, int D, int P) {
+// With aside: the accumulators that a CTA's warps set aside (bf16; of up to 16 heads).
+static Q8Layout q8_layout(int R, int D, int P, bool aside) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     Q8Layout w;
     w.o = up(static_cast<size_t>(2) * P * R * 2 * sizeof(float));
-    w.total = up(w.o + static_cast<size_t>(2) * P * R * D * sizeof(float));
+    w.aside = up(w.o + static_cast<size_t>(2) * P * R * D * sizeof(float));
+    const int DP = (D + 31) / 32 * 32;
+    w.total = up(w.aside + (aside ? static_cast<size_t>(P) * kQ8Warps * q8_aside_floats(DP, 2) * sizeof(float) : 0));
     return w;
 }
 
@@ -1196,10 +1295,11 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     const size_t smem = fixed + pl.nst * per;
     CUtensorMap tmK, tmV;
     if (!q8_map(&tmK, k, pl) || !q8_map(&tmV, v, pl)) return cudaSuccess;
-    const Q8Layout wl = q8_layout(pl.R, pl.D, P);
+    const Q8Layout wl = q8_layout(pl.R, pl.D, P, !kSplit);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     float* part_ml = reinterpret_cast<float*>(ws);
     float* part_o = reinterpret_cast<float*>(ws + wl.o);
+    float* aside = reinterpret_cast<float*>(ws + wl.aside);
     auto kern = decode_q8_kernel<T, Fmt, DP, kN, kSplit, kSub>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
@@ -1217,7 +1317,7 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, pl, static_cast<const T*>(q), static_cast<T*>(out),
-                             ks, vs, block_tables, seq_lens, part_ml, part_o, status);
+                             ks, vs, block_tables, seq_lens, part_ml, part_o, aside, status);
     if (err != cudaSuccess) return err;
     if (pl.direct) {
         *done = true;
@@ -1313,7 +1413,7 @@ extern "C" size_t pkv_decode_q8_workspace_bytes(int B, int Hq, int Hkv, int D, i
     size_t need = 256;
     for (pkv_dtype dt : {PKV_F32, PKV_BF16}) {
         Q8Plan pl = {};
-        if (q8_shape(Hq, Hkv, D, 16, dt, 1, pl)) need = std::max(need, q8_layout(pl.R, D, P).total);
+        if (q8_shape(Hq, Hkv, D, 16, dt, 1, pl)) need = std::max(need, q8_layout(pl.R, D, P, dt == PKV_BF16).total);
     }
     return need;
 }

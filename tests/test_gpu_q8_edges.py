@@ -8,6 +8,7 @@ from tests import q8_ref as R
 pytestmark = pytest.mark.gpu
 FMTS = ["e4m3", "i8"]
 DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+U24 = 2.0 ** -24  # half a float32 step, relative
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -78,3 +79,94 @@ def test_one_bad_id_alone_is_reported(path):
     out = pkv.paged_decode_attention_q8(*cuda(q, k, v, ks, vs, bt, i32(lens)), status=st).cpu()
     assert pkv.check_status(st) == 4
     assert torch.equal(out[3], torch.zeros_like(out[3])) and (out[2] != 0).any()
+
+
+# ------------------------------------------------------------------ peaked rows
+def peaked_cache(L, D, BS, Hkv, fmt, gap, gen):
+    """One sequence, the same in every KV head: the key at position 5 scores `gap` nats above a
+    flat tail for q [D]; V has mean 1.  Returns q, the pools and the table, and the rows in float64."""
+    q = torch.randn(D, generator=gen)
+    u = q / q.norm()
+    kk = 0.1 * torch.randn(L, D, generator=gen)
+    kk -= (kk @ u)[:, None] * u  # the tail scores about 0
+    kk[5] = u * (gap * D ** 0.5 / q.norm())
+    vv = 1 + 0.2 * torch.randn(L, D, generator=gen)
+    vv[5, 0] = 4  # a larger scale, hence a larger contribution, than the tail's rows
+    bt, nb = R.tables([L], BS, gen, spare=0)
+    at = bt[0, torch.arange(L) // BS].long() * BS + torch.arange(L) % BS
+    pools, rows = [], []
+    for x in (kk, vv):
+        vals, sc = R.store(x, fmt)
+        pool, scale = torch.zeros(nb * BS, D, dtype=torch.uint8), torch.zeros(nb * BS)
+        pool[at], scale[at] = vals.view(torch.uint8), sc
+        pools += [pool.view(nb, 1, BS, D).expand(nb, Hkv, BS, D).contiguous().view(R.DT[fmt]),
+                  scale.view(nb, 1, BS).expand(nb, Hkv, BS).contiguous()]
+        rows.append((vals.float().double(), sc.double()))
+    return q, pools[0], pools[2], pools[1], pools[3], bt, rows
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype,many,L,D,gap", [("f32", True, 32768, 16, 17.0), ("f32", True, 8192, 128, 17.0),
+                                                ("f32", False, 32768, 16, 17.0), ("bf16", True, 1 << 20, 16, 17.0)])
+def test_a_long_flat_tail_behind_one_large_weight(dtype, many, L, D, gap, fmt):
+    """A first token that takes nearly all of the weight, and a tail whose single contributions
+    are below 2^-25 of it but whose sum matters.  As many sequences as SMs, over the same
+    blocks, so that a warp meets a whole sequence; and five, which the SMs share.
+
+    Tolerance, per element, with p the weights, out the result, W = sum p |v|,
+    C = sum p |v - out| and S = max scale sum |q k|:
+      scores   2 D truncated additions, 24 more roundings of S, 160 of the exponents' size:
+               d = ((2 D + 24) S + 160) 2^-24 in every weight, numerator and sum alike: 2 d C;
+      sums     of n = L / 32 or L / 64 steps in the numerator and in the sum, and 700 additions within a
+               step, between warps and between ranges, a rounding each: (2 n + 700) 2^-24 W; bf16
+               adds tiles of 16 positions instead, each truncated: 2^-23 W L / 16 more;
+      weights  a float16 rounding, 2^-11 W (bf16), or two, 2^-22 W (float32), and for weights near
+               float16's smallest number half of it: 2^-34 of the largest weight (bf16), 2^-45
+               with the second float16 (float32), times sum |v numbers|;
+      output   2^-8 or 2^-24 of itself.
+    """
+    g = torch.Generator().manual_seed(21)
+    Hkv, G = 8, 2
+    B = torch.cuda.get_device_properties(0).multi_processor_count if many else 5
+    q, k, v, ks, vs, bt, ((kn, ksc), (vn, vsc)) = peaked_cache(L, D, 16, Hkv, fmt, gap, g)
+    qq = torch.stack([q, 1.02 * q]).to(DTYPES[dtype])
+    kk, vv = kn * ksc[:, None], vn * vsc[:, None]
+    p = torch.softmax(D ** -0.5 * qq.double() @ kk.T, -1)
+    want = p @ vv
+    S = D ** -0.5 * (qq.double().abs() @ kk.abs().T).amax(-1, keepdim=True)
+    W = p @ vv.abs()
+    C = torch.stack([p[h] @ (vv - want[h]).abs() for h in range(G)])
+    n = L / (64 if D <= 64 else 32)
+    if dtype == "bf16":
+        rel, floor, last = 2.0 ** -11 + 2.0 ** -23 * L / 16, 2.0 ** -34, 2.0 ** -8
+    else:
+        rel, floor, last = 2.0 ** -22, 2.0 ** -45, U24
+    tol = (2 * ((2 * D + 24) * S + 160) * U24 * C + ((2 * n + 700) * U24 + rel) * W
+           + floor * (p * vsc).amax(-1, keepdim=True) * vn.abs().sum(0) + last * want.abs())
+    # the tail adds more than that, in contributions that are each below 2^-25 of the largest
+    assert p[:, 6:].sum(-1).min() > 2 * (tol / want.abs()).max()
+    w = p * vsc
+    assert (w[:, 6:] < 2.0 ** -25 * w[:, 5:6]).all()
+    gq = qq.repeat(Hkv, 1).expand(B, Hkv * G, D).contiguous().cuda()
+    out = pkv.paged_decode_attention_q8(gq, *cuda(k, v, ks, vs, bt.expand(B, -1).contiguous(), i32([L] * B)))
+    err = (out.cpu().double().view(B, Hkv, G, D) - want).abs()
+    assert (err <= tol).all(), (err / want.abs()).max().item()
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,L", [("bf16", 16, 8, 64, 13000), ("bf16", 128, 8, 128, 9000),
+                                              ("bf16", 8, 1, 64, 70000), ("bf16", 10, 5, 80, 9000), ("f32", 16, 8, 64, 9000)])
+def test_long_ranges_with_late_maxima(dtype, Hq, Hkv, D, L):
+    """Ranges of whole long sequences (as many as SMs, over the same blocks) whose scores grow along
+    the cache, so that the maximum is renewed after parts of the sums were set aside."""
+    g = torch.Generator().manual_seed(61)
+    B = torch.cuda.get_device_properties(0).multi_processor_count
+    bt, nb = R.tables([L], 16, g, spare=0)
+    k, v, ks, vs = R.random_cache(nb, Hkv, 16, D, "e4m3", g)
+    grow = torch.zeros(nb, 16)
+    grow[bt[0].long()] = (torch.arange(nb * 16) / L).view(nb, 16)
+    ks *= 0.2 + 1.8 * grow[:, None, :]
+    q = torch.randn(1, Hq, D, generator=g).to(DTYPES[dtype])
+    want, tol = R.attention(q, k, v, ks, vs, bt, [L], dtype=dtype)
+    out = pkv.paged_decode_attention_q8(q.expand(B, -1, -1).contiguous().cuda(), *cuda(k, v, ks, vs),
+                                        bt.expand(B, -1).contiguous().cuda(), i32([L] * B).cuda()).cpu().double()
+    assert ((out - want).abs() <= tol).all(), ((out - want).norm() / (B ** 0.5 * want.norm())).item()
