@@ -35,7 +35,7 @@
 //    and 2^-45), and sum each step apart before adding it.  The 2-norm of the error is
 //    below 6e-7 of the result for random float32 queries over 500 to 60000 positions;
 //    with one weight 2^25 times as large as each of 32767 behind it, all in one warp,
-//    1.1e-5, which are the roundings of the float32 running sums.
+//    1.1e-5, the roundings of the float32 running sums.
 //  * Weights are normalised by a running maximum of s_j + log2(vs_j), the largest
 //    contribution rather than the largest score, so that p_j * vs_j fits float16
 //    whatever the V scales are.  Scales below 2^-64 count as 2^-64 there, which
@@ -135,6 +135,17 @@ __device__ __forceinline__ float ex2f_subnormal(float x) {
     asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// 2^d, d <= 0, as the square of 2^(d / 2): what sums are multiplied by when the maximum they are relative to
+// changes.  A sum of weights is up to 2^77 a position where V scales are 2^-64 (rows of zeros),
+// and the maximum may rise by 2^185 where rows near the largest float follow, so that
+// 2^d alone would be flushed to zero while the product with the sum is not negligible.  (The
+// maximum and the sums as floats with one ex2 lose such rows; this costs 0-1%.)
+struct Shrink {
+    float half;  // 2^(d / 2)
+    __device__ __forceinline__ explicit Shrink(float d) : half(ex2f(0.5f * d)) {}
+    __device__ __forceinline__ float of(float sum) const { return sum * half * half; }
+    __device__ __forceinline__ float both() const { return half * half; }
+};
 __device__ __forceinline__ float lg2f(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -586,9 +597,10 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                     const float mn = fmaxf(m[n][e], mx);
                     const float base = mn == -INFINITY ? 0.f : mn;
                     mu[n][e] = base - kShift;
-                    al[e] = ex2f(m[n][e] - base);
+                    const Shrink by(m[n][e] - base);
+                    al[e] = by.both();
                     m[n][e] = mn;
-                    l[n][e] *= al[e];
+                    l[n][e] = by.of(l[n][e]);
                 }
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
@@ -889,9 +901,10 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                         const int head = 8 * n + 2 * r + e;
                         const float2 ml = *reinterpret_cast<const float2*>(t + kHeads * kRow + 2 * head);
                         const float mn = fmaxf(m[n][e], ml.x), base = mn == -INFINITY ? 0.f : mn;
-                        const float fa = ex2f(m[n][e] - base), fb = ex2f(ml.x - base);
+                        const Shrink sa(m[n][e] - base), sb(ml.x - base);
+                        const float fa = sa.both(), fb = sb.both();
                         m[n][e] = mn;
-                        l[n][e] = fmaf(l[n][e], fa, ml.y * fb);
+                        l[n][e] = sa.of(l[n][e]) + sb.of(ml.y);
 #pragma unroll
                         for (int c = 0; c < kChunks; ++c) {
                             const float2 o = *reinterpret_cast<const float2*>(t + head * kRow + 16 * c + 2 * g);
@@ -1071,16 +1084,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         float mn = M;
 #pragma unroll
         for (int k = 0; k < kJoinGroup; ++k) mn = fmaxf(mn, ml[k].x);
-        const float mu = mn == -INFINITY ? 0.f : mn, fa = ex2f(M - mu);
+        const float mu = mn == -INFINITY ? 0.f : mn;
+        const Shrink by(M - mu);
+        const float fa = by.both();
         bool bad = l < 0.f;
-        l *= fa;
+        l = by.of(l);
         acc = make_float4(acc.x * fa, acc.y * fa, acc.z * fa, acc.w * fa);
         M = mn;
 #pragma unroll
         for (int k = 0; k < kJoinGroup; ++k) {
-            const float w = ex2f(ml[k].x - mu);
+            const Shrink byk(ml[k].x - mu);
+            const float w = byk.both();
             bad = bad || ml[k].y < 0.f;
-            l = fmaf(ml[k].y, w, l);
+            l += byk.of(ml[k].y);
             acc.x = fmaf(o[k].x, w, acc.x);
             acc.y = fmaf(o[k].y, w, acc.y);
             acc.z = fmaf(o[k].z, w, acc.z);
@@ -1100,14 +1116,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         for (int w = 1; w < kUnitWarps; ++w) mn = fmaxf(mn, mlsh[warp + w][0]);
         const float mu = mn == -INFINITY ? 0.f : mn;
         bool bad = l < 0.f;
-        const float fa = ex2f(M - mu);
-        l *= fa;
+        const Shrink by(M - mu);
+        const float fa = by.both();
+        l = by.of(l);
         acc = make_float4(acc.x * fa, acc.y * fa, acc.z * fa, acc.w * fa);
         for (int w = 1; w < kUnitWarps; ++w) {
-            const float f2 = ex2f(mlsh[warp + w][0] - mu);
+            const Shrink byw(mlsh[warp + w][0] - mu);
+            const float f2 = byw.both();
             const float4 o = accsh[warp + w][lane];
             bad = bad || mlsh[warp + w][1] < 0.f;
-            l = fmaf(mlsh[warp + w][1], f2, l);
+            l += byw.of(mlsh[warp + w][1]);
             acc.x = fmaf(o.x, f2, acc.x);
             acc.y = fmaf(o.y, f2, acc.y);
             acc.z = fmaf(o.z, f2, acc.z);

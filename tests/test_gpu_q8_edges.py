@@ -170,3 +170,28 @@ def test_long_ranges_with_late_maxima(dtype, Hq, Hkv, D, L):
     out = pkv.paged_decode_attention_q8(q.expand(B, -1, -1).contiguous().cuda(), *cuda(k, v, ks, vs),
                                         bt.expand(B, -1).contiguous().cuda(), i32([L] * B).cuda()).cpu().double()
     assert ((out - want).abs() <= tol).all(), ((out - want).norm() / (B ** 0.5 * want.norm())).item()
+
+
+# ------------------------------------------------------------------ V scales far apart
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [([700], 4, 1, 128), ([600, 90], 8, 2, 64), ([9000, 4000], 8, 8, 128),
+                                           ([5000], 16, 1, 80)])
+def test_zero_rows_keep_their_weight_beside_huge_ones(lens, Hq, Hkv, D, fmt, dtype):
+    """Rows of V that are zero (scale 2^-64) in one part of a sequence and about 1e36 in another:
+    the zero rows take their share of the weight."""
+    BS = 16
+    g = torch.Generator().manual_seed(31)
+    for zeros_first in (True, False):
+        bt, nb = R.tables(lens, BS, g)
+        k, v, ks, vs = R.random_cache(nb, Hkv, BS, D, fmt, g)
+        x = torch.randn(nb, Hkv, BS, D, generator=g) * 1e36
+        for b, L in enumerate(lens):
+            blocks = bt[b, :-(-L // BS)].long()
+            half = len(blocks) // 2
+            x[blocks[:half] if zeros_first else blocks[half:]] = 0
+        v, vs = R.store(x, fmt)
+        q = torch.randn(len(lens), Hq, D, generator=g).to(DTYPES[dtype])
+        want, tol = R.attention(q, k, v, ks, vs, bt, lens, dtype=dtype)
+        out = pkv.paged_decode_attention_q8(*cuda(q, k, v, ks, vs, bt, i32(lens))).cpu().double()
+        assert ((out - want).abs() <= tol).all(), ((out - want).norm() / want.norm()).item()
