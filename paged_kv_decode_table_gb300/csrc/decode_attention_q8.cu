@@ -1319,7 +1319,9 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     float* part_o = reinterpret_cast<float*>(ws + wl.o);
     float* aside = reinterpret_cast<float*>(ws + wl.aside);
     auto kern = decode_q8_kernel<T, Fmt, DP, kN, kSplit, kSub>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // The limit belongs to the kernel, not to the call: always the device's largest, so that
+    // another thread's call with other sizes cannot lower it between here and the launch.
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(budget));
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     const int step_tok = pl.slots * kSub * kQ8Tok;

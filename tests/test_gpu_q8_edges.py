@@ -1,4 +1,7 @@
 """The 8-bit cache's calls at the edges of what they are documented for."""
+import ctypes
+import threading
+
 import pytest
 import torch
 
@@ -195,3 +198,53 @@ def test_zero_rows_keep_their_weight_beside_huge_ones(lens, Hq, Hkv, D, fmt, dty
         want, tol = R.attention(q, k, v, ks, vs, bt, lens, dtype=dtype)
         out = pkv.paged_decode_attention_q8(*cuda(q, k, v, ks, vs, bt, i32(lens))).cpu().double()
         assert ((out - want).abs() <= tol).all(), ((out - want).norm() / want.norm()).item()
+
+
+# ------------------------------------------------------------------ threads
+def raw_q8(lib, q, k, v, ks, vs, bt, lens, out, ws, stream):
+    B, Hq, D = q.shape
+    NB, Hkv, BS, _ = k.shape
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    args = (p(out), p(q), p(k), p(v), p(ks), p(vs), p(bt), bt.shape[1], p(lens), B, Hq, Hkv, D, BS, NB,
+            ctypes.c_float(0.0), 1, 2, p(ws), ws.numel(), None, ctypes.c_void_p(stream.cuda_stream))
+    return lambda: lib.pkv_paged_decode_attention_q8(*args)
+
+
+def in_threads(calls, rounds):
+    """Every call `rounds` times, each in a thread of its own; the status codes that came back."""
+    codes = [set() for _ in calls]
+    start = threading.Barrier(len(calls))
+
+    def work(i):
+        start.wait()
+        for _ in range(rounds):
+            codes[i].add(int(calls[i]()))
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    [t.start() for t in ts]
+    [t.join() for t in ts]
+    return codes
+
+
+def test_threads_with_shapes_of_one_kernel():
+    """Head sizes 80 and 96 and 1, 3 and 8 KV heads share a kernel and need different amounts of shared
+    memory; ctypes lets the threads run at the same time."""
+    lib = pkv.load_library()
+    calls, keep = [], []
+    for n, (Hq, Hkv, D) in enumerate([(8, 8, 80), (8, 8, 96), (8, 1, 80), (6, 3, 96)]):
+        g = torch.Generator().manual_seed(n)
+        lens = [900, 1500]
+        bt, nb = R.tables(lens, 16, g)
+        k, v, ks, vs = R.random_cache(nb, Hkv, 16, D, "e4m3", g)
+        q = torch.randn(2, Hq, D, generator=g).to(torch.bfloat16)
+        t = cuda(q, k, v, ks, vs, bt, i32(lens))
+        want = pkv.paged_decode_attention_q8(*t)
+        out = torch.zeros_like(want)
+        ws = torch.empty(max(16, pkv.decode_q8_workspace_bytes(2, Hq, Hkv, D)), dtype=torch.uint8, device="cuda")
+        s = torch.cuda.Stream()
+        keep.append((t, want, out, ws, s))
+        calls.append(raw_q8(lib, *t, out, ws, s))
+    torch.cuda.synchronize()
+    assert in_threads(calls, 4000) == [{0}] * len(calls)
+    torch.cuda.synchronize()
+    for _, want, out, _, _ in keep:
+        assert torch.equal(want, out)
