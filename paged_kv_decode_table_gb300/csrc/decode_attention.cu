@@ -1030,7 +1030,9 @@ cudaError_t launch_decode_attention(void* out, const void* q, const void* k_cach
     const int G = Hq / Hkv;
     const unsigned threads = static_cast<unsigned>((Hkv + 1) * 32);
     auto kern = G > 8 ? decode_attn_fast_kernel<true> : decode_attn_fast_kernel<false>;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(fp.smem));
+    // The limit belongs to the kernel, not to the call: always the device's largest, so that
+    // another thread's call with other sizes cannot lower it between here and the launch.
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, max_optin_smem());
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(P), 1, 1);

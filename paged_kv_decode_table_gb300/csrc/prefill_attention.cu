@@ -434,7 +434,10 @@ cudaError_t launch_prefill_attention(void* out, const void* q, const void* k_cac
     cfg.stream = stream;
     // up to 4 query heads per KV head: 128-thread CTAs, four per SM; else 256 threads, two per SM
     auto kern = G <= 4 ? prefill_attn_kernel<128, 4> : prefill_attn_kernel<256, 2>;
-    cudaError_t aerr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // what the kernel's largest CTA needs, whatever this call does: another thread's call with other
+    // sizes must not lower the limit between here and the launch
+    cudaError_t aerr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kPRingBytes + 4096 * (G <= 4 ? 4 : 8));
     if (aerr != cudaSuccess) return aerr;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

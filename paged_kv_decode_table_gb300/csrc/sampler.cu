@@ -1460,6 +1460,13 @@ static SamplerPlan make_plan(int V, int nc, bool smem_slice) {
     return p;
 }
 
+// The kernel's shared-memory limit: what its largest plan needs, whatever this call does, so
+// that another thread's call with other sizes cannot lower it before the launch.
+static cudaError_t raise_sampler_smem() {
+    return cudaFuncSetAttribute(sampler_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(sizeof(SampSmem) + kSliceSmemMax * sizeof(float)));
+}
+
 // Clusters of plan p that can be resident at once on the current device (0 on error).
 static int resident_clusters(const SamplerPlan& p) {
     static std::mutex mu;
@@ -1472,9 +1479,7 @@ static int resident_clusters(const SamplerPlan& p) {
         auto it = cache.find(key);
         if (it != cache.end()) return it->second;
     }
-    if (cudaFuncSetAttribute(sampler_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(p.smem)) != cudaSuccess)
-        return 0;
+    if (raise_sampler_smem() != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.nc) * 64u, 1, 1);
     cfg.blockDim = dim3(kST, 1, 1);
@@ -1541,8 +1546,7 @@ cudaError_t launch_sampler(int32_t* tokens, const float* logits, int B, int V, c
     const SamplerPlan sp = plan_sampler(B, V, sms);
     // more rows than SMs: heaviest rows first
     const int lpt_B = (B > sms && B < (1 << 21)) ? B : 0;
-    cudaError_t err = cudaFuncSetAttribute(sampler_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           static_cast<int>(sp.smem));
+    cudaError_t err = raise_sampler_smem();
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(B) * sp.nc, 1, 1);
