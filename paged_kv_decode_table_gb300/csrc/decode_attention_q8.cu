@@ -44,6 +44,9 @@
 //  * q is multiplied by a power of two per head that puts its largest element into
 //    [2^14, 2^15).
 // Other shapes: one CTA per (sequence, query head), CUDA-core fp32.
+// No input is read through the read-only path (__ldg, const __restrict__): these kernels start
+// while their predecessor still writes what they read after griddepcontrol.wait, and the
+// join while the main kernel writes its partial results.
 //
 // What bounds it: HBM where the cache is large.  8 sequences of 32768-131072 positions, 64
 // query and 8 KV heads of 128 in int8: 233 us for 1.53 GB, 6.6 TB/s, 98% of the measured
@@ -240,11 +243,9 @@ __host__ __device__ constexpr int q8_aside_floats(int DP, int kN) { return 8 * k
 template <typename T, typename Fmt, int DP, int kN, bool kSplit, int kSub>
 __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                     const __grid_constant__ Q8Plan pl, const T* __restrict__ q, T* __restrict__ out,
-                     const float* __restrict__ k_scale, const float* __restrict__ v_scale,
-                     const int32_t* __restrict__ block_tables, const int32_t* __restrict__ seq_lens,
-                     float* __restrict__ part_ml, float* __restrict__ part_o, float* __restrict__ aside,
-                     int32_t* status) {
+                     const __grid_constant__ Q8Plan pl, const T* q, T* out, const float* k_scale,
+                     const float* v_scale, const int32_t* block_tables, const int32_t* seq_lens, float* part_ml,
+                     float* part_o, float* aside, int32_t* status) {
     constexpr int kChunks = DP / 16;
     // the last chunk may lie behind D: a K byte there is the next row's, and an e4m3 NaN
     // survives the product with q's zero
@@ -967,9 +968,8 @@ constexpr int kJoinGroup = 8;
 
 template <typename T, int kUnitWarps, bool kCuts>
 __global__ void __launch_bounds__(kJoinWarps * 32)
-    decode_q8_join_kernel(const __grid_constant__ Q8Plan pl, const int32_t* __restrict__ seq_lens,
-                          const float* __restrict__ part_ml, const float* __restrict__ part_o, T* __restrict__ out,
-                          int P, int32_t* status) {
+    decode_q8_join_kernel(const __grid_constant__ Q8Plan pl, const int32_t* seq_lens, const float* part_ml,
+                          const float* part_o, T* out, int P, int32_t* status) {
     __shared__ float4 accsh[kJoinWarps][32];
     __shared__ float mlsh[kJoinWarps][2];
     __shared__ int sums[kCuts ? 36 : 2 * kJoinWarps];
@@ -1077,8 +1077,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         for (int k = 0; k < kJoinGroup; ++k) {
             const int p = p0 + k * kUnitWarps;
             const size_t at = (static_cast<size_t>(2 * (f + p) + (p == 0 ? 1 : 0))) * pl.R + row;
-            ml[k] = p < pieces ? __ldg(reinterpret_cast<const float2*>(part_ml + 2 * at)) : make_float2(-INFINITY, 0.f);
-            o[k] = p < pieces && col ? __ldg(reinterpret_cast<const float4*>(part_o + at * pl.D + 4 * lane))
+            ml[k] = p < pieces ? __ldcg(reinterpret_cast<const float2*>(part_ml + 2 * at)) : make_float2(-INFINITY, 0.f);
+            o[k] = p < pieces && col ? __ldcg(reinterpret_cast<const float4*>(part_o + at * pl.D + 4 * lane))
                                      : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         float mn = M;
@@ -1151,11 +1151,10 @@ constexpr int kGen8Threads = 128;
 
 template <typename T, typename Fmt>
 __global__ void __launch_bounds__(kGen8Threads)
-    decode_q8_generic_kernel(T* __restrict__ out, const T* __restrict__ q, const uint8_t* __restrict__ k_cache,
-                             const uint8_t* __restrict__ v_cache, const float* __restrict__ k_scale,
-                             const float* __restrict__ v_scale, const int32_t* __restrict__ block_tables,
-                             int max_blocks, const int32_t* __restrict__ seq_lens, int Hq, int Hkv, int D, int BS,
-                             int NB, float scale, int32_t* status) {
+    decode_q8_generic_kernel(T* out, const T* q, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
+                             const float* v_scale, const int32_t* block_tables, int max_blocks,
+                             const int32_t* seq_lens, int Hq, int Hkv, int D, int BS, int NB, float scale,
+                             int32_t* status) {
     __shared__ float qs[256];
     __shared__ float ps[kGen8Threads];
     __shared__ long long rows[kGen8Threads];

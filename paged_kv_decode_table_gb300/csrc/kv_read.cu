@@ -10,10 +10,12 @@
 // float32 (4 in, 16 out), so that stores are 16 bytes and neighbouring threads
 // write neighbouring 16 bytes; 1 where D or an address does not allow it.  A CTA takes
 // kReadPasses passes of as many whole rows as its threads cover, all loads of the
-// passes first, with the streaming hint: a cached byte is read once here.
+// passes first, with the streaming hint: a cached byte is read once here.  No input is read
+// through the read-only path (__ldg, const __restrict__): the kernel may start while the append
+// before it still writes them.
 // HBM-bound.  9216 blocks of 8 heads x 16 x 128 in e4m3 to bf16 (915 MB moved):
-// 4 passes 140 us, 6.55 TB/s, 98% of the measured copy rate; 2 passes 156, 8
-// passes 167 us, 4 passes without the hint 159 us.
+// 4 passes 138 us, 6.63 TB/s, 99% of the measured copy rate.  With the scales through the
+// read-only path 4 passes took 140 us, 2 passes 156, 8 passes 167, 4 without the hint 159.
 #include "quant8.cuh"
 
 namespace pkv {
@@ -75,10 +77,8 @@ __device__ __forceinline__ void store_row(T* dst, const float (&x)[kVec]) {
 
 template <typename T, typename Fmt, int kVec>
 __global__ void __launch_bounds__(kReadThreads)
-    kv_read_kernel(T* __restrict__ k_out, T* __restrict__ v_out, const uint8_t* __restrict__ k_cache,
-                   const uint8_t* __restrict__ v_cache, const float* __restrict__ k_scale,
-                   const float* __restrict__ v_scale, const int32_t* __restrict__ blocks, int chunks, int R, int D,
-                   int NB, int32_t* status) {
+    kv_read_kernel(T* k_out, T* v_out, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
+                   const float* v_scale, const int32_t* blocks, int chunks, int R, int D, int NB, int32_t* status) {
     prefetch_l2(blocks, static_cast<size_t>(gridDim.x / (2 * chunks)) * 4, blockIdx.x * kReadThreads + threadIdx.x);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kReadThreads)
     for (int p = 0; p < kReadPasses; ++p) {
         const int r = min(r0 + p * rows, last);
         raw[p] = load_bytes<kVec>(src + r * D);
-        scale[p] = __ldg(sc + r);
+        scale[p] = sc[r];
     }
 #pragma unroll
     for (int p = 0; p < kReadPasses; ++p) {
@@ -118,17 +118,16 @@ __global__ void __launch_bounds__(kReadThreads)
 }
 
 // Blocks of few rows: the rows of all blocks in one order, cut into CTAs whatever block they
-// are of.  8479 blocks of 1 head x 64 x 32 in int8 to bf16 (109 MB moved): 18.9 us, 5.8
-// TB/s; a CTA per block and pool 38.7 us.  4000 blocks of 12 x 16 x 32: 28.6 against 32.4 us.
+// are of.  8479 blocks of 1 head x 64 x 32 in int8 to bf16 (109 MB moved): 18.2 us, 6.0
+// TB/s; a CTA per block and pool 38.7 us.  4000 blocks of 12 x 16 x 32: 27.3 against 32.4 us.
 // Large blocks stay with the kernel above, which is 2% faster on them.
 constexpr int kRowsPasses = 6;
 
 template <typename T, typename Fmt, int kVec>
 __global__ void __launch_bounds__(kReadThreads)
-    kv_read_rows_kernel(T* __restrict__ k_out, T* __restrict__ v_out, const uint8_t* __restrict__ k_cache,
-                        const uint8_t* __restrict__ v_cache, const float* __restrict__ k_scale,
-                        const float* __restrict__ v_scale, const int32_t* __restrict__ blocks, int chunks, int n, int R,
-                        int D, int NB, int32_t* status) {
+    kv_read_rows_kernel(T* k_out, T* v_out, const uint8_t* k_cache, const uint8_t* v_cache, const float* k_scale,
+                        const float* v_scale, const int32_t* blocks, int chunks, int n, int R, int D, int NB,
+                        int32_t* status) {
     prefetch_l2(blocks, static_cast<size_t>(n) * 4, blockIdx.x * kReadThreads + threadIdx.x);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(kReadThreads)
         if (!good && !is_v && col == 0 && in_blk[p] == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
         const size_t row = static_cast<size_t>(good ? blk[p] : 0) * R + in_blk[p];
         raw[p] = load_bytes<kVec>(src + row * D);
-        scale[p] = __ldg(sc + row);
+        scale[p] = sc[row];
         if (!good) blk[p] = -1;
     }
 #pragma unroll

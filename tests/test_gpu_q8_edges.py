@@ -248,3 +248,35 @@ def test_threads_with_shapes_of_one_kernel():
     torch.cuda.synchronize()
     for _, want, out, _, _ in keep:
         assert torch.equal(want, out)
+
+
+# ------------------------------------------------------------------ calls one behind the other
+@pytest.mark.parametrize("fmt", FMTS)
+def test_calls_that_start_before_their_predecessor_ends(fmt):
+    """Appends, read-backs and attention over the same few blocks, back to back: every call sees all
+    that the one before it wrote."""
+    Hq, Hkv, D, BS, B, rounds = 8, 8, 128, 16, 24, 30
+    g = torch.Generator().manual_seed(71)
+    bt, nb = R.tables([64] * B, BS, g)
+    k, v, ks, vs = cuda(*R.random_cache(nb, Hkv, BS, D, fmt, g))
+    bt, ids = bt.cuda(), torch.arange(nb, dtype=torch.int32).cuda()
+    kn, vn = (torch.randn(rounds, B, Hkv, D, generator=g).cuda() for _ in range(2))
+    q = torch.randn(rounds, B, Hq, D, generator=g).cuda()
+    lens = [i32([1 + (7 * r) % 64] * B).cuda() for r in range(rounds)]
+
+    def chain(sync):
+        pools = [t.clone() for t in (k, v, ks, vs)]
+        res = []
+        for r in range(rounds):
+            for call in (lambda: pkv.kv_append_q8(kn[r], vn[r], *pools, bt, lens[r]),
+                         lambda: pkv.kv_read_blocks_q8(*pools, ids),
+                         lambda: pkv.paged_decode_attention_q8(q[r], *pools, bt, lens[r])):
+                x = call()
+                res += [] if x is None else list(x) if type(x) is tuple else [x]
+                if sync:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return res + pools
+
+    for a, b in zip(chain(True), chain(False)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
