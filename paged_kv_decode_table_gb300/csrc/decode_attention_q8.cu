@@ -83,7 +83,7 @@ constexpr int kQ8MaxStages = 12;
 constexpr int kQ8Tok = 16;  // positions per tile
 constexpr int kQ8Warps = 8;  // consumer warps at most
 // Steps of a sequence up to which a join is not worth it.  Direct against split: 1 sequence of
-// up to 256 positions, 32 and 8 heads 6.4 : 8.5 us, 16 of up to 512 8.5 : 11.2 us; at 1024 (6
+// up to 256 positions, 32 and 8 heads 6.4 : 8.5 us, 16 of up to 512 8.5 : 11.2 us; at 1024 (4
 // steps) 9.1 : 8.8 us for one, 10.8 : 9.0 for four, 12.2 : 12.6 for 16.
 constexpr int kDirectSteps = 3;
 // Contributions stay below 2^kLag of the running maximum, and weights are 2^kShift times as
@@ -1323,9 +1323,6 @@ static cudaError_t launch_q8_fast(Q8Plan pl, void* out, const void* q, const voi
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(budget));
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    const int step_tok = pl.slots * kSub * kQ8Tok;
-    const long long most = (static_cast<long long>(pl.max_blocks) * pl.BS + step_tok - 1) / step_tok;
-    if (pl.direct && most > kDirectSteps) return cudaSuccess;
     cfg.gridDim = dim3(static_cast<unsigned>(pl.direct ? pl.B * pl.NG : P), 1, 1);
     cfg.blockDim = dim3(static_cast<unsigned>((pl.HG * pl.QC * pl.slots + 1) * 32), 1, 1);
     cfg.dynamicSmemBytes = smem;
@@ -1394,8 +1391,11 @@ static cudaError_t launch_q8(Q8Plan pl, bool fast, void* out, const void* q, con
         // Few and short sequences (by the table's width): a CTA for each (sequence, head
         // group) and no join, with as many groups as there are SMs for.
         const Q8Plan split = pl;
+        auto short_table = [](const Q8Plan& p) {
+            return static_cast<long long>(p.max_blocks) * p.BS <= kDirectSteps * p.slots * p.sub * kQ8Tok;
+        };
         pl.direct = pl.B <= P && q8_shape(pl.Hq, pl.Hkv, pl.D, pl.BS, sizeof(T) == 4 ? PKV_F32 : PKV_BF16, P / pl.B, pl) &&
-                    pl.B * pl.NG <= P;
+                    pl.B * pl.NG <= P && short_table(pl);
         if (pl.direct) {
             err = go();
             if (err != cudaSuccess || done) return err;
