@@ -486,7 +486,8 @@ pkv_status pkv_paged_decode_attention_q8(void* out, const void* q, const void* k
  * PKV_I8.  Everything is float32 between one load and one rounding.
  * freqs: device int64 [rot_dim / 2], turns per position as 64-bit fractions of a
  * turn: round(f_j / (2 pi) * 2^64) for angle f_j per position; the integer
- * product with pos wraps by whole turns, so far positions lose nothing.
+ * product with pos wraps by whole turns, and t is off by at most 2^-28 of a turn
+ * at every position alike.
  * rot_dim 0: no rotation.  q, k_new, v_new: rows of a token dense ([H, D]),
  * tokens q_stride / k_stride / v_stride elements apart (three views of one
  * projection output, for instance).  1 <= D <= 256, rot_dim even and <= D.

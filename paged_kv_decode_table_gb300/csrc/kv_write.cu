@@ -11,9 +11,9 @@
 //             8 bits with a scale (quant8.cuh).
 // Everything between the load and the store is float32 and each result is
 // rounded once.  The frequency comes as turns per position in units of 2^-64
-// (a 64-bit integer): pos * f wraps modulo one turn in integer arithmetic, so
-// the angle keeps its full precision at any position, and sincospif needs no
-// range reduction.
+// (a 64-bit integer): pos * f wraps modulo one turn in integer arithmetic, and the
+// nearest quarter turn is taken off there too, before the one rounding to float32:
+// the angle is off by at most 2^-28 of a turn, at every position alike.
 //
 // Vector kernel (D a multiple of 8, 16-byte aligned rows): a lane holds 8 elements of
 // a row in two runs of 4, D / 8 lanes a row, 32 / (D / 8) rows a warp and pass.  A lane's
@@ -132,12 +132,16 @@ __device__ __forceinline__ void write_prefetch(const WriteArgs& a) {
     if (a.half > 0) prefetch_l2(a.freqs, static_cast<size_t>(a.half) * 8, worker);
 }
 
-// cos and sin of pos * freq (turns in units of 2^-64, whole turns wrap away).
+// cos and sin of pos * freq (turns in units of 2^-64, whole turns wrap away).  What is left of
+// the nearest quarter turn is within 1/4 of a half-turn, where float32 rounds by 2^-27.
 __device__ __forceinline__ float2 turn_of(int pos, int64_t freq) {
     const uint64_t f = static_cast<uint64_t>(pos) * static_cast<uint64_t>(freq);
+    const unsigned quarter = static_cast<unsigned>((f + (1ull << 61)) >> 62);
+    const int64_t rest = static_cast<int64_t>(f - (static_cast<uint64_t>(quarter) << 62));
     float s, c;
-    sincospif(static_cast<float>(static_cast<int64_t>(f)) * 1.0842021724855044e-19f, &s, &c);  // 2^-63
-    return make_float2(c, s);
+    sincospif(static_cast<float>(rest) * 1.0842021724855044e-19f, &s, &c);  // 2^-63
+    const float x = quarter & 1 ? s : c, y = quarter & 1 ? c : s;
+    return make_float2(quarter == 1 || quarter == 2 ? -x : x, quarter >= 2 ? -y : y);
 }
 
 // T: element type of the rows; Fmt: the 8-bit format, or FmtNone for a cache of T.

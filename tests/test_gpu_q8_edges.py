@@ -1,5 +1,6 @@
 """The 8-bit cache's calls at the edges of what they are documented for."""
 import ctypes
+import math
 import threading
 
 import pytest
@@ -280,3 +281,34 @@ def test_calls_that_start_before_their_predecessor_ends(fmt):
 
     for a, b in zip(chain(True), chain(False)):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# ------------------------------------------------------------------ rotation
+@pytest.mark.parametrize("D,interleaved,at", [(128, False, 0), (128, True, 0), (20, False, 0), (64, False, 1)])
+def test_cosines_and_sines_at_any_angle(D, interleaved, at):
+    """Rows (1, 0) per pair give the cosine and the sine themselves.  The angle, a 64-bit
+    fraction of a turn, is rounded once to float32 within an eighth of a turn of a whole
+    quarter: at most 2^-27 half-turns, pi * 2^-27 < 0.4 * 2^-24 in the result; sincospif adds at
+    most 1 ulp of the result, which is at most 2^-23 of it."""
+    g = torch.Generator().manual_seed(41)
+    T, half = 64, D // 2
+    hi, lo = (torch.randint(0, 2 ** 32, (half,), generator=g) for _ in range(2))
+    freqs = ((hi - 2 ** 31) << 32) | lo  # any 64-bit integer
+    lens = [1 + int(x) for x in torch.randint(0, 64, (T,), generator=g)]
+    bt, nb = R.tables(lens, 16, g)
+    row = torch.zeros(D)
+    row[0::2 if interleaved else 1][:half] = 1
+    buf = torch.zeros(T * D + at)
+    x = row.repeat(T, 1, 1)
+    gq = buf.cuda()[at:].view(T, 1, D)  # at: an address that is not 16-byte aligned
+    gq.copy_(x)
+    kc, vc = (torch.zeros(nb, 1, 16, D, device="cuda") for _ in range(2))
+    out = pkv.qk_norm_rope_append(gq, gq.clone(), gq.clone(), None, None, 0.0, freqs.cuda(), kc, vc, *cuda(bt, i32(lens)),
+                                  interleaved=interleaved).cpu().double()[:, 0]
+    ang = torch.tensor([[2 * math.pi * (((L - 1) * int(f)) % 2 ** 64 / 2 ** 64) for f in freqs] for L in lens],
+                       dtype=torch.float64)
+    cos, sin = (out[:, 0::2], out[:, 1::2]) if interleaved else (out[:, :half], out[:, half:])
+    for got, want in ((cos, torch.cos(ang)), (sin, torch.sin(ang))):
+        # 2^-50: the float64 angle's own rounding, at most 2 pi 2^-53
+        tol = 0.4 * U24 + 2.0 ** -23 * want.abs() + 2.0 ** -50
+        assert ((got - want).abs() <= tol).all(), (((got - want).abs() - tol).max() / U24).item()
