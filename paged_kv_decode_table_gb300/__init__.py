@@ -372,7 +372,13 @@ class DecodeStep:
     the same shapes while the object is used (refill them in place between
     steps).  Returns the tokens tensor from run().  With k_scale and v_scale
     the cache is an 8-bit one, and the append and the attention are
-    pkv_kv_append_q8 and pkv_paged_decode_attention_q8."""
+    pkv_kv_append_q8 and pkv_paged_decode_attention_q8.
+
+    The step appends k_new and v_new as they are, in every run(): keys and
+    queries have to be normalised and rotated before.  Behind
+    qk_norm_rope_append, which appends by itself, it would overwrite the
+    prepared key with the raw one; call paged_decode_attention or
+    paged_decode_attention_q8 and sample_tokens there instead."""
 
     def __init__(self, q, k_new, v_new, k_cache, v_cache, block_tables, seq_lens, logits, temperature, top_k,
                  top_p, seeds, offsets, out=None, tokens=None, workspace=None, status=None, min_p=None,
@@ -886,7 +892,9 @@ def qk_norm_rope_append(q, k_new, v_new, q_weight, k_weight, eps, freqs, k_cache
     q [T, Hq, D], k_new / v_new [T, Hkv, D] (float32 or bfloat16; tokens may be
     any distance apart, so views of one projection output will do).  T is B (one
     token per sequence) or, with q_start, the packed chunks of kv_append_chunk.
-    The cache is of q's type, or an 8-bit one with its k_scale and v_scale."""
+    The cache is of q's type, or an 8-bit one with its k_scale and v_scale.  The
+    append is done here: attention follows by paged_decode_attention or
+    paged_decode_attention_q8, not by a DecodeStep, which appends again."""
     r = (_calls or _native()).prepare(q, k_new, v_new, q_weight, k_weight, eps, freqs, k_cache, v_cache, block_tables,
                                       seq_lens, q_start, k_scale, v_scale, interleaved, q_out, status)
     if type(r) is not int:
