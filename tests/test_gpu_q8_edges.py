@@ -312,3 +312,61 @@ def test_cosines_and_sines_at_any_angle(D, interleaved, at):
         # 2^-50: the float64 angle's own rounding, at most 2 pi 2^-53
         tol = 0.4 * U24 + 2.0 ** -23 * want.abs() + 2.0 ** -50
         assert ((got - want).abs() <= tol).all(), (((got - want).abs() - tol).max() / U24).item()
+
+
+# ------------------------------------------------------------------ graphs
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_prompt_and_a_decode_step_captured_and_replayed(fmt):
+    """Preparation, append, read-back and attention in one graph, replayed on new inputs and
+    lengths: the bytes and numbers of the same calls made one by one."""
+    Hq, Hkv, D, BS, B = 8, 2, 64, 16, 4
+    g = torch.Generator().manual_seed(51)
+    bt, nb = R.tables([200] * B, BS, g)
+    table, freqs = bt.cuda(), pkv.rope_freqs(D)
+    w = torch.rand(D, generator=g).to(torch.bfloat16).cuda() + 0.5
+    qs = i32([0, 20, 20, 53, 60]).cuda()
+
+    def buffers():
+        pools = cuda(*R.random_cache(nb, Hkv, BS, D, fmt, torch.Generator().manual_seed(52)))
+        q, kv, q1, kv1 = (torch.zeros(n, h, D, dtype=torch.bfloat16, device="cuda")
+                          for n, h in ((60, Hq), (60, 2 * Hkv), (B, Hq), (B, 2 * Hkv)))
+        return (*pools, q, kv, q1, kv1, torch.zeros(2, B, dtype=torch.int32, device="cuda"), pkv.new_status())
+
+    def calls(k, v, ks, vs, q, kv, q1, kv1, lens, st):
+        kn, vn = kv[:, :Hkv], kv[:, Hkv:]
+        qo = pkv.qk_norm_rope_append(q, kn, vn, w, w, 1e-6, freqs, k, v, table, lens[0], qs, ks, vs, status=st)
+        pkv.kv_append_q8(kv1[:, :Hkv].contiguous(), kv1[:, Hkv:].contiguous(), k, v, ks, vs, table, lens[1],
+                         status=st)
+        rk, rv = pkv.kv_read_blocks_q8(k, v, ks, vs, table[2], status=st)
+        a = pkv.paged_decode_attention_q8(q1, k, v, ks, vs, table, lens[1], status=st)
+        return qo, rk, rv, a
+
+    cap, plain = buffers(), buffers()
+
+    def fill(bufs, seed):
+        gen = torch.Generator().manual_seed(seed)
+        for t in bufs[4:8]:
+            t.copy_(torch.randn(t.shape, generator=gen))
+        lens = [40 + int(x) for x in torch.randint(0, 100, (B,), generator=gen)]
+        bufs[8].copy_(i32([lens, [n + 1 for n in lens]]))
+
+    fill(cap, 1)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls(*cap)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(*cap)
+    for t, fresh in zip(cap[:4], buffers()[:4]):
+        t.copy_(fresh)
+    for seed in (2, 3, 4):
+        fill(cap, seed)
+        fill(plain, seed)
+        graph.replay()
+        want = calls(*plain)
+        torch.cuda.synchronize()
+        for a, b in zip((*got, *cap[:4]), (*want, *plain[:4])):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert pkv.check_status(cap[9]) == 0 and pkv.check_status(plain[9]) == 0
