@@ -49,12 +49,12 @@
 // join while the main kernel writes its partial results.
 //
 // What bounds it: HBM where the cache is large.  8 sequences of 32768-131072 positions, 64
-// query and 8 KV heads of 128 in int8: 233 us for 1.53 GB, 6.6 TB/s, 98% of the measured
+// query and 8 KV heads of 128 in int8: 234 us for 1.53 GB, 6.5 TB/s, 98% of the measured
 // copy rate.  64 sequences of 512-4096, 32 and 8 heads: 58 us for 332 MB, 86%; the rest is
 // the start (2.5 us), the end of the slowest SM (2.3 us) and the join (3.5 us).  With the
 // arithmetic left out the same kernel takes 57 us, so the tensor and issue pipes (17% and
 // 32% busy) hide behind the copies.  They do not with 16 query heads a group (128 and 8
-// heads: 84 us, 59%) and with float32 queries (63 us, 78%; two MMAs for one).  One short
+// heads: 85 us, 59%) and with float32 queries (64 us, 78%; two MMAs for one).  One short
 // sequence is a chain of latencies, lengths -> block ids -> K and V -> result: 6.4 us.
 // mma.sync and not tcgen05: a float16 query needs float16 keys, so the converted numbers, twice
 // the bytes that came, would go back to shared memory before tcgen05.mma could read them,
@@ -141,8 +141,7 @@ __device__ __forceinline__ float ex2f_subnormal(float x) {
 // 2^d, d <= 0, as the square of 2^(d / 2): what sums are multiplied by when the maximum they are relative to
 // changes.  A sum of weights is up to 2^77 a position where V scales are 2^-64 (rows of zeros),
 // and the maximum may rise by 2^185 where rows near the largest float follow, so that
-// 2^d alone would be flushed to zero while the product with the sum is not negligible.  (The
-// maximum and the sums as floats with one ex2 lose such rows; this costs 0-1%.)
+// 2^d alone would be flushed to zero while the product with the sum is not negligible.
 struct Shrink {
     float half;  // 2^(d / 2)
     __device__ __forceinline__ explicit Shrink(float d) : half(ex2f(0.5f * d)) {}
@@ -238,7 +237,7 @@ __host__ __device__ constexpr int q8_aside_floats(int DP, int kN) { return 8 * k
 
 // DP: dimensions computed (32, 64, 96 or 128; D may be smaller).  96 of 128 for D = 80 took 37
 // float32 sequences of up to 1500 from 15.6 to 14.3 us, 32 of 64 for D = 32 169 sequences of
-// 1733-3682 with 10 query heads a group from 107 to 86 us (81 with two floats an instruction).  kN: n-tiles of 8 query heads per
+// 1733-3682 with 10 query heads a group from 107 to 86 us.  kN: n-tiles of 8 query heads per
 // warp; kSplit: float32 accuracy (see above); kSub: tiles a warp takes of a step.
 template <typename T, typename Fmt, int DP, int kN, bool kSplit, int kSub>
 __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
@@ -721,19 +720,19 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
     };
 
     // bf16: the MMA truncates what it adds to about 2^-24 of its accumulator, so that of a long
-    // tail behind one large weight little would be left.  Every kAside steps (4096 positions of a
-    // warp, at most 2^-12 of the result lost in them) the accumulators are added, rescaled, to this
+    // tail behind one large weight little would be left.  Every kAside steps (8192 positions of a
+    // warp, at most 2^-11 of the result lost in them) the accumulators are added, rescaled, to this
     // warp's place in the workspace and begin again at zero; a range's last ones fetch what is there.
-    // The code for it costs about 1% (64 x 512-4096 58.2 -> 58.4 us, 8 x 32K-128K 233.7 -> 235.6), summing
-    // every step apart as above up to 5%, and 16 heads a group have no registers for that (128
-    // and 8 heads 84 -> 103 us).
-    constexpr int kAside = 4096 / (kQ8Tok * kSub);
-    [[maybe_unused]] int steps = 0;  // of this piece so far
+    // The code for it costs 0-1% (64 x 512-4096 58.0 -> 58.2 us; with heads of 32 dimensions
+    // 81 -> 84), 4096 positions 1% more on ranges just longer than that, summing every step apart as
+    // above up to 5%, and 16 heads a group have no registers for that (128 and 8 heads 84 -> 103).
+    constexpr int kAside = 8192 / (kQ8Tok * kSub);
+    [[maybe_unused]] int steps = 0;  // of this piece so far, but for its last
     [[maybe_unused]] auto set_aside = [&](bool leave) {
         float* tile = aside + (static_cast<size_t>(blockIdx.x) * kQ8Warps + warp) * q8_aside_floats(DP, kN);
         float4* to = reinterpret_cast<float4*>(tile) + lane;
         float2* to_m = reinterpret_cast<float2*>(tile + DP * kHeads) + lane;
-        const bool old = steps > kAside;
+        const bool old = leave || steps > kAside;
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
             float f[2] = {0.f, 0.f};
@@ -843,12 +842,21 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
             stage = 0;
             parity ^= 1u;
         }
-        if constexpr (!kSplit) {
-            ++steps;
-            const bool leave = mt.flags & kQLast;
-            if (leave ? steps > kAside : steps % kAside == 0) set_aside(leave);
+        const bool leave = mt.flags & kQLast;
+        if constexpr (kSplit) {
+            if (!leave) continue;
+        } else {
+            // the one way back for nearly all steps comes first (12 heads 85.2 -> 83.8 us), but for
+            // 16 heads of 128, whose registers spill (91 us for 85)
+            if constexpr (kN * DP < 256) {
+                if (!leave && ++steps % kAside != 0) continue;
+                if (!leave || steps >= kAside) set_aside(leave);
+            } else {
+                if (!leave) ++steps;
+                if (leave ? steps >= kAside : steps % kAside == 0) set_aside(leave);
+            }
+            if (!leave) continue;
         }
-        if (!(mt.flags & kQLast)) continue;
 
         // ---------------------------------------------- the range leaves (sequence, group) mt.vb
 #pragma unroll
@@ -1077,7 +1085,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         for (int k = 0; k < kJoinGroup; ++k) {
             const int p = p0 + k * kUnitWarps;
             const size_t at = (static_cast<size_t>(2 * (f + p) + (p == 0 ? 1 : 0))) * pl.R + row;
-            ml[k] = p < pieces ? __ldcg(reinterpret_cast<const float2*>(part_ml + 2 * at)) : make_float2(-INFINITY, 0.f);
+            ml[k] = p < pieces ? __ldcg(reinterpret_cast<const float2*>(part_ml + 2 * at)) : make_float2(kCuts ? -INFINITY : ml[0].x, 0.f);
             o[k] = p < pieces && col ? __ldcg(reinterpret_cast<const float4*>(part_o + at * pl.D + 4 * lane))
                                      : make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -1087,20 +1095,35 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
         const float mu = mn == -INFINITY ? 0.f : mn;
         const Shrink by(M - mu);
         const float fa = by.both();
-        bool bad = l < 0.f;
+        bool bad = l < 0.f, flushed = false;
         l = by.of(l);
         acc = make_float4(acc.x * fa, acc.y * fa, acc.z * fa, acc.w * fa);
         M = mn;
 #pragma unroll
         for (int k = 0; k < kJoinGroup; ++k) {
-            const Shrink byk(ml[k].x - mu);
-            const float w = byk.both();
+            float w;
+            // 2^d first and the flushed ones again where there are any, against Shrink for all: 64 x
+            // 512-4096 58.0 : 58.6 us, 37 x 0-1500 13.6 : 14.3; with cuts, whose many short CTAs want
+            // few registers (56 : 72), 512 x 128-1024 112.6 : 110.5.
+            if constexpr (kCuts) {
+                const Shrink byk(ml[k].x - mu);
+                w = byk.both();
+                l += byk.of(ml[k].y);
+            } else {
+                w = ex2f(ml[k].x - mu);
+                flushed = flushed || w == 0.f;
+                l = fmaf(ml[k].y, w, l);
+            }
             bad = bad || ml[k].y < 0.f;
-            l += byk.of(ml[k].y);
             acc.x = fmaf(o[k].x, w, acc.x);
             acc.y = fmaf(o[k].y, w, acc.y);
             acc.z = fmaf(o[k].z, w, acc.z);
             acc.w = fmaf(o[k].w, w, acc.w);
+        }
+        if (flushed) {  // a sum may make up for the zero
+#pragma unroll
+            for (int k = 0; k < kJoinGroup; ++k)
+                if (ex2f(ml[k].x - mu) == 0.f) l += Shrink(ml[k].x - mu).of(ml[k].y);
         }
         if (bad) l = -INFINITY;  // stays: a poisoned piece makes the row zero
     }
