@@ -13,7 +13,8 @@
 // Hkv * BS * D elements per pool, so a pair is two contiguous memcpys.  The
 // grid has one CTA per (pair, pool, chunk of kChunk bytes); each thread moves
 // 16-byte vectors, four in flight.  HBM-bound: bytes = 2 x (read + write) per
-// pool and pair.
+// pool and pair.  No input is read through the read-only path: the kernel may
+// start while the append before it still writes the blocks.
 #include "pkv_common.cuh"
 
 namespace pkv {
@@ -23,8 +24,7 @@ constexpr int kCopyUnroll = 4;
 constexpr long long kChunk = static_cast<long long>(kCopyThreads) * kCopyUnroll * 16;  // 16 KB per CTA
 
 __global__ void __launch_bounds__(kCopyThreads)
-    copy_blocks_kernel(uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
-                       const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n_pairs,
+    copy_blocks_kernel(uint8_t* k_cache, uint8_t* v_cache, const int32_t* src, const int32_t* dst, int n_pairs,
                        long long block_bytes, int chunks, int NB, int vec_ok, int32_t* status) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kCopyThreads)
 #pragma unroll
         for (int u = 0; u < kCopyUnroll; ++u) {
             const long long v = v0 + threadIdx.x + static_cast<long long>(u) * kCopyThreads;
-            if (v < v1) r[u] = __ldg(f4 + v);
+            if (v < v1) r[u] = f4[v];
         }
 #pragma unroll
         for (int u = 0; u < kCopyUnroll; ++u) {

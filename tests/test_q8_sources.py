@@ -7,7 +7,7 @@ import pytest
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "paged_kv_decode_table_gb300", "csrc")
 
 
-@pytest.mark.parametrize("name", ["decode_attention_q8.cu", "kv_read.cu", "kv_write.cu"])
+@pytest.mark.parametrize("name", ["decode_attention_q8.cu", "kv_read.cu", "kv_write.cu", "copy_blocks.cu"])
 def test_kernels_that_start_early_use_no_read_only_loads(name):
     """These kernels may start while their predecessor writes their inputs.  Loads through
     the read-only path (__ldg, ld.global.nc, const __restrict__ parameters) are for
