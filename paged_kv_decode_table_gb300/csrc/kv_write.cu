@@ -28,7 +28,7 @@
 // warp one row, one element per lane and step.
 //
 // Bound by instruction issue, then HBM: 6147 tokens of 32 + 8 heads of 128 in bf16, normalised
-// and rotated into a bf16 cache, 27.2 us for 151 MB, 5.5 TB/s, 83% of the measured copy rate,
+// and rotated into a bf16 cache, 27.4 us for 151 MB, 5.5 TB/s, 82% of the measured copy rate,
 // two thirds of the issue slots.  The quantising append of 5226 tokens of 8 heads 9.5 us for
 // 32 MB, 50%, at as many issue slots.  64 tokens 2.8 us, 1 token 2.3 us: launch and three
 // dependent loads.  Two designs that fed consumer warps by bulk copies, one CTA or two an SM,
