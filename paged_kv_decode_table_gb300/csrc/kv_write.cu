@@ -668,7 +668,7 @@ static cudaError_t launch_typed(const WriteArgs& a, cudaStream_t stream) {
         w.warps_log2 = std::max(w.wpt_log2, 2);  // small CTAs: less to wait for at the end (6147 tokens 29.3 -> 27.2 us)
         cfg.blockDim = dim3(32u << w.warps_log2, 1, 1);
         const int tpc = 1 << (w.warps_log2 - w.wpt_log2);
-        cfg.gridDim = dim3(static_cast<unsigned>((a.T + tpc - 1) / tpc), static_cast<unsigned>(split), 1);
+        cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(a.T) + tpc - 1) / tpc), static_cast<unsigned>(split), 1);
         const int rot = a.half == 0 ? 0 : a.interleaved ? 3 : a.half % 4 == 0 ? 1 : 2;
         auto pick = [&](auto lanes) {
             constexpr int kLanes = decltype(lanes)::value;
