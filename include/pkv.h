@@ -14,6 +14,9 @@
  * pkv_seq_*) hands out block ids and reports the copy-on-write pairs that
  * pkv_copy_blocks copies on the GPU before the step's append.
  * Chunked prefill: pkv_kv_append_chunk and pkv_paged_prefill_attention.
+ * Changed scores (tanh cap, distance bias, window): pkv_paged_decode_attention_scored,
+ * pkv_paged_prefill_attention_scored; shared prefixes read once:
+ * pkv_paged_decode_attention_shared.
  * 8-bit cache: pkv_kv_append_q8, pkv_kv_read_blocks_q8,
  * pkv_paged_decode_attention_q8; pkv_qk_norm_rope_append prepares queries and
  * keys and appends in one pass, to either kind of cache.
@@ -471,6 +474,94 @@ pkv_status pkv_paged_decode_attention_q8(void* out, const void* q, const void* k
                                          int32_t* dev_status, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Attention with changed scores.  For a query of head qh at position pos and key
+ * j < L, h = qh / (Hq / Hkv):
+ *   t = scale * <q, K_j>,  u = softcap * tanh(t / softcap)  (softcap 0: u = t),
+ *   s_j = u + slopes[qh] * (j - pos)                        (slopes NULL: s_j = u);
+ * key j takes part where j < prefix_lens[b] (NULL: 0; what lies past L does not
+ * exist), or where j <= pos and, with window > 0, j > pos - window.
+ *   out = sum_j softmax(s)_j V_j over the keys that take part.
+ * The cap comes before the slope.  slopes: device float32 [Hq], finite, of any
+ * sign.  A window of w is the last w positions, the query's own among them.
+ * prefix_lens: device int32 [B]: the first positions of a sequence that stay in
+ * sight of every query whatever the window is, and of a prefill chunk's queries
+ * before them too (a prefix that attends in both directions; its keys have to be
+ * in the cache).  softcap negative, NaN or subnormal, or scale / softcap or softcap *
+ * log2(e) out of float32's range: PKV_ERR_INVALID_ARG.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Workspace bytes pkv_paged_decode_attention_scored needs (num_sms <= 0: the
+ * current device).  Returns 0 on error.  Pure host arithmetic when num_sms > 0. */
+size_t pkv_decode_scored_workspace_bytes(int B, int Hq, int Hkv, int D, int num_sms);
+
+/*
+ * pkv_paged_decode_attention with changed scores; pos = seq_lens[b] - 1, L == 0
+ * gives zeros.  dtype: PKV_F32 or PKV_BF16, of q, out and the cache.  Any Hq %
+ * Hkv == 0, any block_size, 1 <= D <= 256.  Only positions that take part are
+ * read; the others, and the slots past L, may hold anything, NaN included.
+ * workspace: device, 16-byte aligned, at least pkv_decode_scored_workspace_bytes(B,
+ * Hq, Hkv, D, 0) bytes, contents ignored on entry; calls that can overlap on the
+ * GPU need a workspace each.  Bad lengths and block ids (of blocks that are read)
+ * give zero output and PKV_ERR_DEVICE_BOUNDS.
+ */
+pkv_status pkv_paged_decode_attention_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, int max_blocks_per_seq,
+                                             const int32_t* seq_lens, const int32_t* prefix_lens, int B, int Hq,
+                                             int Hkv, int D, int block_size, int num_blocks, float scale,
+                                             float softcap, const float* slopes, int window, pkv_dtype dtype,
+                                             void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                             void* stream);
+
+/*
+ * pkv_paged_prefill_attention with changed scores: query row t of sequence b is
+ * at position pos as there.  bf16 only, D = 128, block_size a multiple of 16, Hq
+ * / Hkv <= 8, 16-byte aligned q, out and pools (else PKV_ERR_UNSUPPORTED).  Key
+ * tiles that no row of a query tile sees are not read.  A row that is given no
+ * weight is still multiplied: an infinity or NaN in V at a position that some
+ * queries see reaches queries within 256 / (Hq / Hkv) tokens of them that do not.
+ */
+pkv_status pkv_paged_prefill_attention_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                              const int32_t* block_tables, int max_blocks_per_seq,
+                                              const int32_t* seq_lens, const int32_t* q_start,
+                                              const int32_t* prefix_lens, int B, int T_new, int Hq, int Hkv, int D,
+                                              int block_size, int num_blocks, float scale, float softcap,
+                                              const float* slopes, int window, pkv_dtype dtype, int32_t* dev_status,
+                                              void* stream);
+
+/* Workspace bytes pkv_paged_decode_attention_shared needs (num_sms <= 0: the
+ * current device).  Returns 0 on error.  Pure host arithmetic when num_sms > 0. */
+size_t pkv_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D, int num_sms);
+
+/*
+ * Decode attention of a batch whose sequences share prefixes (pkv_seq_fork makes
+ * such; pkv_shared_groups finds them): the result of
+ * pkv_paged_decode_attention_scored without window and prefix_lens, with each
+ * shared prefix read once for all sequences of its group.  Sequences
+ * group_start[g] .. group_start[g + 1] - 1, g < N, are group g; group_start:
+ * device int32 [N + 1], non-decreasing, group_start[0] = 0, group_start[N] <= B;
+ * sequences behind the last group, and groups of one, share nothing.  The first
+ * floor(shared_lens[g] / block_size) table entries of all sequences of a group
+ * must be the same (its first sequence's are used); shared_lens: device int32
+ * [N].  A sequence shorter than that prefix (but for length 0, which gives
+ * zeros), a shared length outside the table, and everything that
+ * pkv_paged_decode_attention_scored finds: zero output and
+ * PKV_ERR_DEVICE_BOUNDS, for every sequence where group_start is none.  N may be 0.
+ * Prefixes are read once for bf16, D = 64 or 128, block_size a multiple of 16, Hq
+ * / Hkv <= 128 and 16-byte aligned q, out and pools; elsewhere the result is the
+ * same without the saving.  workspace as there, of at least
+ * pkv_decode_shared_workspace_bytes(B, Hq, Hkv, D, 0) bytes.
+ */
+pkv_status pkv_paged_decode_attention_shared(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                             const int32_t* block_tables, int max_blocks_per_seq,
+                                             const int32_t* seq_lens, const int32_t* group_start,
+                                             const int32_t* shared_lens, int N, int B, int Hq, int Hkv, int D,
+                                             int block_size, int num_blocks, float scale, float softcap,
+                                             const float* slopes, pkv_dtype dtype, void* workspace,
+                                             size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/*
  * Norm, rotation and append in one pass: what lies between the query / key /
  * value projections and the attention of a step or a prefill chunk.  For every
  * new token at position pos (as in pkv_kv_append, or with q_start as in
@@ -530,6 +621,14 @@ pkv_status pkv_qk_norm_rope_append(void* q_out, const void* q, int64_t q_stride,
  *   block_tables rows of max_blocks_per_seq block ids for seqs[0..n) (host
  *                int32 [n, max_blocks_per_seq], unused entries -1) and their
  *                lengths (host int32 [n]), ready to upload.
+ *   shared_groups cuts seqs[0..n) into runs of neighbours that share leading
+ *                blocks, as pkv_paged_decode_attention_shared takes them: a run
+ *                goes on while its sequences have at least min_blocks (>= 1)
+ *                whole leading blocks in common.  Host int32 group_start [n + 1]
+ *                and shared_lens [n] (tokens, whole blocks; 0 for a run of one)
+ *                are filled up to *n_groups, of which the caller passes on
+ *                group_start[0 .. *n_groups].  A block is whole where every
+ *                sequence of the run has filled it.
  *   num_free / refcount / seq_length report state (-1 on a bad argument).
  */
 typedef struct pkv_block_pool pkv_block_pool;
@@ -544,6 +643,8 @@ pkv_status pkv_seq_free(pkv_block_pool* pool, int64_t seq);
 int pkv_seq_length(const pkv_block_pool* pool, int64_t seq);
 pkv_status pkv_block_tables(const pkv_block_pool* pool, const int64_t* seqs, int n, int32_t* block_tables,
                             int32_t* seq_lens);
+pkv_status pkv_shared_groups(const pkv_block_pool* pool, const int64_t* seqs, int n, int min_blocks,
+                             int32_t* group_start, int32_t* shared_lens, int* n_groups);
 
 #ifdef __cplusplus
 }

@@ -5,9 +5,9 @@ in-tree by ``paged_kv_decode_table_gb300.build``).  Every function here only
 checks and marshals torch tensors (device, dtype, contiguity, shapes) and passes
 raw device pointers plus the current CUDA stream; all arithmetic runs in the
 library's CUDA kernels.  There is no CPU fallback: if the library cannot be
-loaded, every call raises.  The calls of the 8-bit cache and qk_norm_rope_append
-go through a small native module (``_torch_calls``) instead of ctypes, because
-their kernels take less time than testing their arguments in Python.
+loaded, every call raises.  The calls of the 8-bit cache, qk_norm_rope_append and
+attention with changed scores or shared prefixes go through a small native module
+(``_torch_calls``) instead of ctypes, because their kernels take less time than testing their arguments in Python.
 
 Calls (names follow the C ABI):
   kv_append(k_new, v_new, k_cache, v_cache, block_tables, seq_lens)
@@ -23,6 +23,9 @@ Calls (names follow the C ABI):
   kv_read_blocks_q8(k_cache, v_cache, k_scale, v_scale, blocks, dtype=torch.bfloat16)
   paged_decode_attention_q8(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, out=None, scale=0.0)
   qk_norm_rope_append(q, k_new, v_new, q_weight, k_weight, eps, freqs, k_cache, v_cache, block_tables, seq_lens, ...)
+  paged_decode_attention_scored(q, k_cache, v_cache, block_tables, seq_lens, softcap, slopes, window, prefix_lens)
+  paged_prefill_attention_scored(q, k_cache, v_cache, block_tables, seq_lens, q_start, softcap, slopes, window, ...)
+  paged_decode_attention_shared(q, k_cache, v_cache, block_tables, seq_lens, group_start, shared_lens, softcap, slopes)
   rope_freqs(rot_dim, base=10000.0)                       the rotation's frequencies as 64-bit turns
   BlockPool(num_blocks, block_size, max_blocks_per_seq)   host-side refcounted block ids
   DecodeStep(q, k_new, v_new, k_cache, v_cache, block_tables, seq_lens, logits, ...).run()
@@ -48,7 +51,8 @@ __all__ = ["PkvError", "load_library", "library_path", "kv_append", "paged_decod
            "spec_verify_workspace_bytes", "apply_logits_processors", "kv_append_chunk",
            "paged_prefill_attention", "DecodeStep", "test_set_wait_limit", "kv_append_q8", "kv_append_chunk_q8",
            "kv_read_blocks_q8", "paged_decode_attention_q8", "decode_q8_workspace_bytes", "qk_norm_rope_append",
-           "rope_freqs"]
+           "rope_freqs", "paged_decode_attention_scored", "paged_prefill_attention_scored",
+           "paged_decode_attention_shared", "decode_scored_workspace_bytes", "decode_shared_workspace_bytes"]
 
 STATUS = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED", 3: "PKV_ERR_CUDA",
           4: "PKV_ERR_DEVICE_BOUNDS", 5: "PKV_ERR_TIMEOUT", 6: "PKV_ERR_NONFINITE", 7: "PKV_ERR_CAPACITY"}
@@ -151,6 +155,20 @@ def load_library():
         lib.pkv_qk_norm_rope_append.argtypes = [P, P, i64, P, i64, P, i64, P, P, f32, P, i32, i32, P, P, P, P, P, i32,
                                                 P, P, i32, i32, i32, i32, i32, i32, i32, i32, i32, P, P]
         lib.pkv_qk_norm_rope_append.restype = i32
+        for name in ("pkv_decode_scored_workspace_bytes", "pkv_decode_shared_workspace_bytes"):
+            getattr(lib, name).argtypes = [i32, i32, i32, i32, i32]
+            getattr(lib, name).restype = sz
+        lib.pkv_paged_decode_attention_scored.argtypes = [P, P, P, P, P, i32, P, P, i32, i32, i32, i32, i32, i32, f32,
+                                                          f32, P, i32, i32, P, sz, P, P]
+        lib.pkv_paged_decode_attention_scored.restype = i32
+        lib.pkv_paged_prefill_attention_scored.argtypes = [P, P, P, P, P, i32, P, P, P, i32, i32, i32, i32, i32, i32,
+                                                           i32, f32, f32, P, i32, i32, P, P]
+        lib.pkv_paged_prefill_attention_scored.restype = i32
+        lib.pkv_paged_decode_attention_shared.argtypes = [P, P, P, P, P, i32, P, P, P, i32, i32, i32, i32, i32, i32,
+                                                          i32, f32, f32, P, i32, P, sz, P, P]
+        lib.pkv_paged_decode_attention_shared.restype = i32
+        lib.pkv_shared_groups.argtypes = [P, P, i32, i32, P, P, P]
+        lib.pkv_shared_groups.restype = i32
         lib.pkv_test_set_wait_limit.argtypes = [ctypes.c_uint32, i32]
         lib.pkv_test_set_wait_limit.restype = i32
         _lib = lib
@@ -604,6 +622,18 @@ class BlockPool:
                                                                ctypes.c_void_p(sl.data_ptr())))
         return bt, sl
 
+    def shared_groups(self, seqs, min_blocks: int = 1):
+        """Neighbours in `seqs` that share leading blocks, as paged_decode_attention_shared takes them:
+        (group_start int32 [N + 1], shared_lens int32 [N]) as CPU tensors."""
+        n = len(seqs)
+        ids = (ctypes.c_int64 * max(1, n))(*seqs)
+        start, shared = torch.zeros(n + 1, dtype=torch.int32), torch.zeros(n, dtype=torch.int32)
+        groups = ctypes.c_int()
+        _raise("pkv_shared_groups", self._lib.pkv_shared_groups(self._p, ids, n, int(min_blocks),
+                                                                ctypes.c_void_p(start.data_ptr()),
+                                                                ctypes.c_void_p(shared.data_ptr()), ctypes.byref(groups)))
+        return start[:groups.value + 1].clone(), shared[:groups.value].clone()
+
 
 def spec_verify_workspace_bytes(B: int, gamma: int) -> int:
     return int(load_library().pkv_spec_verify_workspace_bytes(B, gamma))
@@ -725,7 +755,7 @@ def paged_prefill_attention(q, k_cache, v_cache, block_tables, seq_lens, q_start
     return out
 
 
-# ---------------------------------------------------------------- 8-bit cache
+# ---------------------------------------------------------------- native calls
 # These calls sit in decode loops whose kernels take a few microseconds, so their
 # arguments are tested and passed on by the native module _torch_calls
 # (csrc/torch_calls.cpp).  It answers -1 where an argument is not what it should
@@ -926,3 +956,91 @@ def qk_norm_rope_append(q, k_new, v_new, q_weight, k_weight, eps, freqs, k_cache
         if q_out is not None:
             _check_cuda("q_out", q_out, q.dtype, q.shape, dev)
     _failed("pkv_qk_norm_rope_append", r)
+
+
+# ---------------------------------------------------------------- changed scores, shared prefixes
+def decode_scored_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, num_sms: int = 0) -> int:
+    return int(load_library().pkv_decode_scored_workspace_bytes(B, Hq, Hkv, D, num_sms))
+
+
+def decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, num_sms: int = 0) -> int:
+    return int(load_library().pkv_decode_shared_workspace_bytes(B, Hq, Hkv, D, num_sms))
+
+
+def _scored_failed(name, code, q, k_cache, v_cache, block_tables, seq_lens, slopes, out, workspace, status, more):
+    if code < 0:
+        _dtype_code(q)
+        dev = k_cache.device
+        if k_cache.dim() != 4 or q.dim() != 3:
+            raise ValueError("k_cache must be [num_blocks, Hkv, block_size, D], q [rows, Hq, D]")
+        _check_cuda("k_cache", k_cache, q.dtype)
+        _check_cuda("v_cache", v_cache, q.dtype, k_cache.shape, dev)
+        B = seq_lens.shape[0]
+        _check_cuda("q", q, q.dtype, (q.shape[0] if "q_start" in more else B, q.shape[1], k_cache.shape[3]), dev)
+        _check_tables(block_tables, seq_lens, B, status, dev)
+        if slopes is not None:
+            _check_cuda("slopes", slopes, torch.float32, (q.shape[1],), dev)
+        for key, (t, shape) in more.items():
+            if t is not None:
+                _check_cuda(key, t, torch.int32, shape, dev)
+            elif key != "prefix_lens":
+                raise TypeError(f"{key} must be a torch.Tensor")
+        if out is not None:
+            _check_cuda("out", out, q.dtype, q.shape, dev)
+        if workspace is not None:
+            _check_cuda("workspace", workspace, device=dev)
+    _failed(name, code)
+
+
+def paged_decode_attention_scored(q, k_cache, v_cache, block_tables, seq_lens, softcap: float = 0.0, slopes=None,
+                                  window: int = 0, prefix_lens=None, out=None, scale: float = 0.0, workspace=None,
+                                  status=None):
+    """paged_decode_attention with changed scores; returns out [B, Hq, D].
+
+    With softcap > 0 a score t becomes softcap * tanh(t / softcap); slopes
+    (float32 [Hq]) add slopes[head] * (key - position).  window > 0 leaves the last
+    `window` positions in sight, and with prefix_lens (int32 [B]) the first
+    prefix_lens[b] as well.  q and the cache are float32 or bfloat16.  Without
+    `workspace` one is allocated for the call, so calls on several streams, or
+    captured in several graphs, do not share it."""
+    r = (_calls or _native()).attend_scored(q, k_cache, v_cache, block_tables, seq_lens, softcap, slopes, window,
+                                            prefix_lens, out, scale, workspace, status)
+    if type(r) is not int:
+        return r
+    _scored_failed("pkv_paged_decode_attention_scored", r, q, k_cache, v_cache, block_tables, seq_lens, slopes, out,
+                   workspace, status, {"prefix_lens": (prefix_lens, (seq_lens.shape[0],))})
+
+
+def paged_prefill_attention_scored(q, k_cache, v_cache, block_tables, seq_lens, q_start, softcap: float = 0.0,
+                                   slopes=None, window: int = 0, prefix_lens=None, out=None, scale: float = 0.0,
+                                   status=None):
+    """paged_prefill_attention with the scores of paged_decode_attention_scored;
+    returns out [T_new, Hq, D].  The first prefix_lens[b] positions of a sequence
+    are seen by all its queries, those before them included."""
+    r = (_calls or _native()).prefill_scored(q, k_cache, v_cache, block_tables, seq_lens, q_start, softcap, slopes,
+                                             window, prefix_lens, out, scale, status)
+    if type(r) is not int:
+        return r
+    B = seq_lens.shape[0]
+    _scored_failed("pkv_paged_prefill_attention_scored", r, q, k_cache, v_cache, block_tables, seq_lens, slopes, out,
+                   None, status, {"q_start": (q_start, (B + 1,)), "prefix_lens": (prefix_lens, (B,))})
+
+
+def paged_decode_attention_shared(q, k_cache, v_cache, block_tables, seq_lens, group_start, shared_lens,
+                                  softcap: float = 0.0, slopes=None, out=None, scale: float = 0.0, workspace=None,
+                                  status=None):
+    """paged_decode_attention (with softcap and slopes as in
+    paged_decode_attention_scored) of sequences that share prefixes, each of which
+    is read once; returns out [B, Hq, D].
+
+    Sequences group_start[g] .. group_start[g + 1] - 1 (int32 [N + 1]) have the same
+    first shared_lens[g] // block_size entries (int32 [N]) in their tables, as
+    BlockPool.shared_groups finds them.  Without `workspace` one is allocated for
+    the call."""
+    r = (_calls or _native()).attend_shared(q, k_cache, v_cache, block_tables, seq_lens, group_start, shared_lens,
+                                            softcap, slopes, out, scale, workspace, status)
+    if type(r) is not int:
+        return r
+    N = shared_lens.shape[0] if isinstance(shared_lens, torch.Tensor) and shared_lens.dim() == 1 else 0
+    _scored_failed("pkv_paged_decode_attention_shared", r, q, k_cache, v_cache, block_tables, seq_lens, slopes, out,
+                   workspace, status, {"group_start": (group_start, (N + 1,)), "shared_lens": (shared_lens, (N,))})

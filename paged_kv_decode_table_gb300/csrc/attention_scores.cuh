@@ -1,0 +1,76 @@
+// attention_scores.cuh -- the scores of the *_scored and *_shared attention calls.
+//
+// For query head qh at position pos and key j, with t = <q, K_j>:
+//   u = cap tanh(scale t / cap)  (cap > 0),  else scale t
+//   s = u + slopes[qh] (j - pos)  (slopes given),  else u
+// and key j < L takes part where j < prefix, or j <= pos and (window <= 0 or j > pos - window).
+// The kernels work with s log2(e), so that a weight is one exp2.
+#pragma once
+
+#include <math.h>
+
+#include "pkv_common.cuh"
+
+namespace pkv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Passed to the kernels by value.
+struct ScoreArgs {
+    float mul;                   // scale log2(e)
+    float in, cap_log2;          // scale / cap and cap log2(e); 0: no cap
+    const float* slopes;         // [Hq] or NULL
+    int window;                  // <= 0: none
+    const int32_t* prefix_lens;  // [B] or NULL
+};
+// False where a number is out of range: the cap negative, NaN or subnormal, or a product of the two not finite.
+inline bool make_scores(ScoreArgs* sa, float scale, int D, float cap, const float* slopes, int window,
+                        const int32_t* prefix_lens) {
+    if (!(scale > 0.f)) scale = 1.0f / sqrtf(static_cast<float>(D));
+    *sa = ScoreArgs{scale * kLog2e, cap > 0.f ? scale / cap : 0.f, cap * kLog2e, slopes, window, prefix_lens};
+    return (cap == 0.f || cap >= 1.17549435e-38f) && sa->mul <= 3.0e38f && sa->in <= 3.0e38f && sa->cap_log2 <= 3.0e38f;
+}
+
+// The positions that the one query of a decode step sees: [0, pfx) and [lo, L), pfx <= lo.
+struct Seen {
+    int L, lo, pfx;
+    __device__ __forceinline__ bool at(int j) const { return j < L && (j >= lo || j < pfx); }
+};
+__device__ __forceinline__ Seen decode_seen(const ScoreArgs& sa, int b, int L) {
+    Seen s{L, 0, 0};
+    if (sa.window > 0 && sa.window < L) {
+        s.lo = L - sa.window;
+        if (sa.prefix_lens != nullptr) s.pfx = min(max(sa.prefix_lens[b], 0), L);
+        if (s.pfx >= s.lo) s.pfx = s.lo = 0;
+    }
+    return s;
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// cap log2(e) tanh(x), x = scale t / cap.  Up to |x| = 1/4 the Taylor polynomial x (1 - x^2/3 + 2x^4/15 - 17x^6/315
+// + 62x^8/2835): what it leaves out is below 2^-26.7 of x, so a small score keeps its relative accuracy whatever the
+// cap is.  Beyond, 1 - 2 / (e^(2x) + 1), whose error is about 2^-23 of the cap; e^(2x) = infinity gives 1.
+constexpr float kTanhSmall = 0.25f;
+__device__ __forceinline__ float tanh_small(float x) {
+    const float y = x * x;
+    float p = fmaf(y, 62.f / 2835.f, -17.f / 315.f);
+    p = fmaf(p, y, 2.f / 15.f);
+    p = fmaf(p, y, -1.f / 3.f);
+    return fmaf(x * y, p, x);
+}
+__device__ __forceinline__ float tanh_large(float x) {
+    return fmaf(-2.f, rcp_approx(ex2_approx(x * (2.f * kLog2e)) + 1.f), 1.f);
+}
+__device__ __forceinline__ float capped_tanh(float x) { return fabsf(x) <= kTanhSmall ? tanh_small(x) : tanh_large(x); }
+
+}  // namespace pkv

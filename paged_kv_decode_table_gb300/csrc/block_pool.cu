@@ -156,4 +156,33 @@ pkv_status pkv_block_tables(const pkv_block_pool* p, const int64_t* seqs, int n,
     return PKV_OK;
 }
 
+// The blocks that are read once instead of once per sequence: (members - 1) * common.  A neighbour joins a run
+// where that does not fall, so one that has little in common does not cost a run its long prefix.
+pkv_status pkv_shared_groups(const pkv_block_pool* p, const int64_t* seqs, int n, int min_blocks, int32_t* group_start,
+                             int32_t* shared_lens, int* n_groups) {
+    if (!p || n < 0 || min_blocks < 1 || !group_start || !n_groups || (n > 0 && (!seqs || !shared_lens)))
+        return PKV_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i)
+        if (!p->seqs.count(seqs[i])) return PKV_ERR_INVALID_ARG;
+    int groups = 0;
+    group_start[0] = 0;
+    for (int i = 0; i < n;) {
+        const pkv_block_pool::Seq& first = p->seqs.find(seqs[i])->second;
+        long long common = first.len / p->block_size, members = 1;
+        for (; i + members < n; ++members) {
+            const pkv_block_pool::Seq& s = p->seqs.find(seqs[i + members])->second;
+            const long long most = common < s.len / p->block_size ? common : s.len / p->block_size;
+            long long same = 0;
+            while (same < most && s.blocks[static_cast<size_t>(same)] == first.blocks[static_cast<size_t>(same)]) ++same;
+            if (same < min_blocks || members * same < (members - 1) * common) break;
+            common = same;
+        }
+        shared_lens[groups++] = members > 1 ? static_cast<int32_t>(common * p->block_size) : 0;
+        i += static_cast<int>(members);
+        group_start[groups] = i;
+    }
+    *n_groups = groups;
+    return PKV_OK;
+}
+
 }  // extern "C"

@@ -5,7 +5,7 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
-#include "pkv_common.cuh"
+#include "attention_scores.cuh"
 
 namespace pkv {
 cudaError_t launch_kv_append(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
@@ -26,7 +26,7 @@ bool prefill_tc_supported(int Hq, int Hkv, int D, int BS, const void* q, const v
 cudaError_t launch_prefill_tc(void* out, const void* q, const void* k_cache, const void* v_cache,
                               const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,
                               const int32_t* q_start, int B, int T_new, int Hq, int Hkv, int BS, int NB, float scale,
-                              int32_t* status, cudaStream_t stream);
+                              const ScoreArgs* scored, int32_t* status, cudaStream_t stream);
 cudaError_t launch_typical_sampler(int32_t* tokens, const float* logits, int B, int V, const float* temperature,
                                    const float* typical_p, const uint64_t* seeds, const uint64_t* offsets,
                                    int32_t* status, cudaStream_t stream);
@@ -154,10 +154,31 @@ pkv_status pkv_paged_prefill_attention(void* out, const void* q, const void* k_c
     if (pkv::prefill_tc_supported(Hq, Hkv, D, block_size, q, out, k_cache, v_cache))
         return cuda_status(pkv::launch_prefill_tc(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                                                   seq_lens, q_start, B, T_new, Hq, Hkv, block_size, num_blocks,
-                                                  scale, dev_status, static_cast<cudaStream_t>(stream)));
+                                                  scale, nullptr, dev_status, static_cast<cudaStream_t>(stream)));
     return cuda_status(pkv::launch_prefill_attention(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                                                      seq_lens, q_start, B, T_new, Hq, Hkv, block_size, num_blocks,
                                                      scale, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+pkv_status pkv_paged_prefill_attention_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                              const int32_t* block_tables, int max_blocks_per_seq,
+                                              const int32_t* seq_lens, const int32_t* q_start,
+                                              const int32_t* prefix_lens, int B, int T_new, int Hq, int Hkv, int D,
+                                              int block_size, int num_blocks, float scale, float softcap,
+                                              const float* slopes, int window, pkv_dtype dtype, int32_t* dev_status,
+                                              void* stream) {
+    pkv::ScoreArgs sc;
+    if (B < 0 || T_new < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || block_size < 1 || num_blocks < 1 ||
+        max_blocks_per_seq < 1 || !dtype_ok(dtype) ||
+        !pkv::make_scores(&sc, scale, D, softcap, slopes, window, prefix_lens))
+        return PKV_ERR_INVALID_ARG;
+    if (B == 0 || T_new == 0) return PKV_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !q_start) return PKV_ERR_INVALID_ARG;
+    if (dtype != PKV_BF16 || !pkv::prefill_tc_supported(Hq, Hkv, D, block_size, q, out, k_cache, v_cache))
+        return PKV_ERR_UNSUPPORTED;
+    return cuda_status(pkv::launch_prefill_tc(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
+                                              q_start, B, T_new, Hq, Hkv, block_size, num_blocks, 1.f, &sc, dev_status,
+                                              static_cast<cudaStream_t>(stream)));
 }
 
 size_t pkv_decode_workspace_bytes(int B, int Hq, int D, int num_sms) {

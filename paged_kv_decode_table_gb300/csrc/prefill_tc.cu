@@ -51,7 +51,7 @@
 #include <cuda.h>
 #include <math.h>
 
-#include "pkv_common.cuh"
+#include "attention_scores.cuh"
 
 namespace pkv {
 
@@ -212,12 +212,44 @@ __device__ __forceinline__ int tc_tiles_longer(int n, int L, int TC, int v) {
     return cnt;
 }
 
+// The 64 products of a row with the keys from kbase on become scores in the log2 domain, -infinity where the row at
+// position `pos` does not see the key.  first, last: the positions of the query tile's rows; slope: of the row's
+// head, times log2(e).
+__device__ __forceinline__ void score_tile(uint32_t (&sr)[2][32], int kbase, int pos, int first, int last, int pfx,
+                                           float slope, const ScoreArgs& sc) {
+    if (sc.cap_log2 > 0.f) {
+#pragma unroll
+        for (int c = 0; c < kTcKeys; ++c)
+            sr[c >> 5][c & 31] = __float_as_uint(sc.cap_log2 * capped_tanh(__uint_as_float(sr[c >> 5][c & 31]) * sc.in));
+    } else {
+#pragma unroll
+        for (int c = 0; c < kTcKeys; ++c)
+            sr[c >> 5][c & 31] = __float_as_uint(__uint_as_float(sr[c >> 5][c & 31]) * sc.mul);
+    }
+    if (sc.slopes != nullptr) {
+        const float at = slope * static_cast<float>(kbase - pos);
+#pragma unroll
+        for (int c = 0; c < kTcKeys; ++c)
+            sr[c >> 5][c & 31] =
+                __float_as_uint(__uint_as_float(sr[c >> 5][c & 31]) + fmaf(slope, static_cast<float>(c), at));
+    }
+    // some key is hidden from some row of the query tile
+    if (kbase + kTcKeys > pfx && (kbase + kTcKeys - 1 > first || (sc.window > 0 && kbase <= last - sc.window))) {
+        const int lo = sc.window > 0 ? pos - sc.window + 1 - kbase : -kbase, hi = pos - kbase, near = pfx - kbase;
+#pragma unroll
+        for (int c = 0; c < kTcKeys; ++c)
+            if (!(c < near || (c <= hi && c >= lo))) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+    }
+}
+
+// kScored: the scores of attention_scores.cuh (sc), else plain ones (sc unused).
+template <bool kScored>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ out,
                       const int32_t* __restrict__ block_tables, int max_blocks, const int32_t* __restrict__ seq_lens,
                       const int32_t* __restrict__ q_start, int B, int Hq, int Hkv, int BS, int NB, float scale_log2,
-                      int32_t* status) {
+                      const __grid_constant__ ScoreArgs sc, int32_t* status) {
     extern __shared__ uint8_t tc_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tc_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sP = base;                          // P of query tile t at t kTcPBytes
@@ -344,8 +376,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         active = false;
     }
-    const int plast = p0 + nt - 1;                    // the CTA's last position (keys 0 .. plast are read)
-    const int ntiles = active ? plast / kTcKeys + 1 : 0;
+    // scored: keys below pfx are seen by every row, keys below wlo (and not below pfx) by no row of the CTA
+    [[maybe_unused]] int pfx = 0, wlo = 0;
+    if constexpr (kScored) {
+        if (active && sc.prefix_lens != nullptr) pfx = min(max(sc.prefix_lens[b], 0), L);
+        if (active && sc.window > 0) wlo = max(0, p0 - sc.window + 1);
+    }
+    const int plast = max(p0 + nt, pfx) - 1;          // the CTA's last key (keys 0 .. plast are read)
+    // key tile i of the walk is tile i, behind the prefix's tiles (near) tile i + skip
+    [[maybe_unused]] const int near = (pfx + kTcKeys - 1) / kTcKeys, skip = max(0, wlo / kTcKeys - near);
+    const int ntiles = active ? plast / kTcKeys + 1 - (kScored ? skip : 0) : 0;
+    auto key_tile = [&](int i) { return kScored && i >= near ? i + skip : i; };
     // iteration j handles key tile (j + rot) mod ntiles (any order gives the same softmax)
     const int rot = ntiles > 0 ? static_cast<int>((blockIdx.x * 13u) % static_cast<unsigned>(ntiles)) : 0;
     const int nblk_used = active ? plast / BS + 1 : 0;
@@ -390,7 +431,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int win0 = -kTcWin;
         for (int j = 0; j < ntiles && !fail; ++j) {
             const int s = j % kTcStages;
-            const int kt = j + rot < ntiles ? j + rot : j + rot - ntiles;
+            const int kt = key_tile(j + rot < ntiles ? j + rot : j + rot - ntiles);
             const int kb0 = (kt * kTcKeys) / BS, kb1 = min(nblk_used - 1, (kt * kTcKeys + kTcKeys - 1) / BS);
             if (kb0 < win0 || kb1 >= win0 + kTcWin) {  // move this warp's window of the block table
                 __syncwarp();
@@ -410,7 +451,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int key0 = kt * kTcKeys + 16 * (bi & 3);
                 const int kb = key0 / BS;
                 int blk = 0, slot = 0;
-                if (kb < nblk_used) {  // later keys: any valid rows (masked; their V rows are cleared)
+                // later keys and those that no row sees: any valid rows (masked; their V rows are cleared)
+                if (kb < nblk_used && !(kScored && key0 + 16 <= wlo && key0 >= pfx)) {
                     blk = tbl[kb - win0];
                     slot = key0 - kb * BS;
                     if (blk < 0 || blk >= NB) {
@@ -504,6 +546,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t tq = tmem + 256 * qt;
         const int p0t = p0 + qt * TQ;  // the query tile's first position
         float m_ref = -INFINITY, lsum = 0.f;
+        [[maybe_unused]] float slope = 0.f;
+        if constexpr (kScored) slope = sc.slopes != nullptr ? sc.slopes[qh] * kLog2e : 0.f;
         for (int j = 0; j < ntiles; ++j) {
             if (!__all_sync(0xffffffffu, mbar_wait(&sm->s_full[qt], j & 1))) {  // tcgen05.ld needs the whole warp
                 fail = true;
@@ -515,15 +559,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_ld32(tq + lrow + 96, sr[1]);
             tc_fence_before();
             mbar_arrive(&sm->s_free[qt]);  // S may take the next tile
-            const int kt = j + rot < ntiles ? j + rot : j + rot - ntiles;
+            const int kt = key_tile(j + rot < ntiles ? j + rot : j + rot - ntiles);
             const int kbase = kt * kTcKeys;
+            if constexpr (kScored) score_tile(sr, kbase, pos, p0t, min(p0t + TQ, p0 + nt) - 1, pfx, slope, sc);
             // maximum of the raw scores (the scale is positive), eight chains;
             // the causal mask only on tiles that reach past the query tile's first position
             // (three-input maxima: two scores per instruction, four chains)
             float mxs[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) mxs[k] = -INFINITY;
-            if (kbase + kTcKeys - 1 > p0t) {
+            if (!kScored && kbase + kTcKeys - 1 > p0t) {
 #pragma unroll
                 for (int c = 0; c < kTcKeys; ++c) {
                     const float v = kbase + c <= pos ? __uint_as_float(sr[c >> 5][c & 31]) : -INFINITY;
@@ -534,7 +579,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int c = 0; c < kTcKeys; c += 2)
                 mxs[(c >> 1) & 3] = tc_max3(mxs[(c >> 1) & 3], __uint_as_float(sr[c >> 5][c & 31]),
                                             __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
-            const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * scale_log2;
+            const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * (kScored ? 1.f : scale_log2);
             // the reference maximum moves only when the row maximum passes it by more than 8
             const float m_new = mx > m_ref + 8.f ? mx : m_ref;
             const bool resc = m_new != m_ref;
@@ -551,7 +596,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int c = 0; c < kTcKeys / 2; ++c) {
                 float t0, t1;
                 tc_fma2(t0, t1, __uint_as_float(sr[(2 * c) >> 5][(2 * c) & 31]),
-                        __uint_as_float(sr[(2 * c + 1) >> 5][(2 * c + 1) & 31]), scale_log2, nmu);
+                        __uint_as_float(sr[(2 * c + 1) >> 5][(2 * c + 1) & 31]), kScored ? 1.f : scale_log2, nmu);
                 const float e0 = tc_ex2(t0), e1 = tc_ex2(t1);
                 pk[c] = pack_bf16x2(e0, e1);
                 tc_add2(ls[c & 3][0], ls[c & 3][1], e0, e1);
@@ -576,11 +621,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tc_st32(tq + lrow + 128 + 32 * cc, o);
                 }
             }
-            if (qt == 0 && kt == ntiles - 1) {  // the V rows of keys at or past L may hold anything: clear them
-                const int rlo = max(0, min(kTcKeys, L - kbase));
+            // the V rows of keys at or past L may hold anything: clear them (scored: those of every key no row sees)
+            if (qt == 0 && (kScored ? kbase + kTcKeys - 1 > plast || (kbase < wlo && kbase + kTcKeys > pfx) : kt == ntiles - 1)) {
+                const int rlo = kScored ? 0 : max(0, min(kTcKeys, L - kbase));
                 uint8_t* vb = sKV + static_cast<size_t>(j % kTcStages) * kTcStageBytes + kTcKBytes;
                 for (int idx = r; idx < (kTcKeys - rlo) * 16; idx += kTcRows) {
                     const int rr = rlo + (idx >> 4), half = (idx >> 3) & 1, ch = idx & 7;
+                    if (kScored && kbase + rr <= plast && (kbase + rr >= wlo || kbase + rr < pfx)) continue;
                     *reinterpret_cast<uint4*>(vb + kTcGroupBytes * (rr >> 4) + half * (kTcGroupBytes / 2) +
                                               (rr & 15) * 128 + ch * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
@@ -676,14 +723,15 @@ bool prefill_tc_supported(int Hq, int Hkv, int D, int BS, const void* q, const v
 cudaError_t launch_prefill_tc(void* out, const void* q, const void* k_cache, const void* v_cache,
                               const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,
                               const int32_t* q_start, int B, int T_new, int Hq, int Hkv, int BS, int NB, float scale,
-                              int32_t* status, cudaStream_t stream) {
+                              const ScoreArgs* scored, int32_t* status, cudaStream_t stream) {
     const int G = Hq / Hkv, TC = kTcQT * (kTcRows / G);
     const long long tiles = static_cast<long long>(T_new) / TC + B;
     if (tiles * Hkv > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     CUtensorMap tmK, tmV;
     if (!encode_pool_k16(&tmK, k_cache, NB, Hkv, BS) || !encode_pool_box_halves(&tmV, v_cache, NB, Hkv, BS, 16))
         return cudaErrorInvalidValue;
-    cudaError_t err = cudaFuncSetAttribute(prefill_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    auto kern = scored != nullptr ? prefill_tc_kernel<true> : prefill_tc_kernel<false>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(kTcSmemBytes));
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -697,9 +745,9 @@ cudaError_t launch_prefill_tc(void* out, const void* q, const void* k_cache, con
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const float scale_log2 = scale * 1.4426950408889634f;
-    err = cudaLaunchKernelEx(&cfg, prefill_tc_kernel, tmK, tmV, static_cast<const __nv_bfloat16*>(q),
+    err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, static_cast<const __nv_bfloat16*>(q),
                              static_cast<__nv_bfloat16*>(out), block_tables, max_blocks, seq_lens, q_start, B, Hq, Hkv,
-                             BS, NB, scale_log2, status);
+                             BS, NB, scale_log2, scored != nullptr ? *scored : ScoreArgs{}, status);
     if (err != cudaSuccess) return err;
     return cudaGetLastError();
 }

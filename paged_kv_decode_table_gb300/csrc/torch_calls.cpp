@@ -1,5 +1,5 @@
-// torch_calls.cpp -- the calls of the 8-bit cache and of the query / key preparation for torch
-// tensors.
+// torch_calls.cpp -- the calls of the 8-bit cache, of the query / key preparation and of attention with
+// changed scores or shared prefixes for torch tensors.
 //
 // These calls sit in decode loops whose kernels take two to five microseconds, where
 // testing ten tensors' attributes and converting twenty arguments in Python costs
@@ -252,11 +252,136 @@ PyObject* prepare(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// A float argument; false with a Python error set where it is none.
+bool number(PyObject* o, float* v) {
+    const double x = PyFloat_AsDouble(o);
+    *v = static_cast<float>(x);
+    return x != -1.0 || !PyErr_Occurred();
+}
+// An int argument, limited to 32 bits; false with a Python error set where it is none.
+bool integer(PyObject* o, int* v) {
+    int overflow = 0;
+    const long long x = PyLong_AsLongLongAndOverflow(o, &overflow);
+    *v = overflow > 0 || x > INT_MAX ? INT_MAX : overflow < 0 || x < INT_MIN ? INT_MIN : static_cast<int>(x);
+    return x != -1 || overflow != 0 || !PyErr_Occurred();
+}
+
+// What the calls with changed scores share: q [rows, Hq, D], an unquantised cache, sequences, slopes, out.
+struct Scored {
+    Cache c;
+    Sequences s;
+    const Tensor* q;
+    pkv_dtype dtype;
+    int Hq;
+    float softcap, scale;
+
+    // -1: a Python error is set; 0: an argument is not what it should be; 1: good
+    int take(PyObject* qo, PyObject* ko, PyObject* vo, PyObject* bto, PyObject* slo, PyObject* capo, PyObject* slopes,
+             PyObject* outo, PyObject* scaleo, PyObject* sto) {
+        q = tensor(qo);
+        if (!q || q->dim() != 3 || q->size(0) > INT_MAX || q->size(1) > INT_MAX || !float_code(q->scalar_type(), &dtype))
+            return 0;
+        const ScalarType type = q->scalar_type();
+        if (!c.take(ko, vo, Py_None, Py_None, &type) || !s.take(bto, slo, sto, c.dev) || !is(q, type, c.dev) ||
+            q->size(2) != c.D || !optional(slopes, ScalarType::Float, c.dev, {q->size(1)}) ||
+            !optional(outo, type, c.dev, q->sizes()))
+            return 0;
+        Hq = static_cast<int>(q->size(1));
+        return number(capo, &softcap) && number(scaleo, &scale) ? 1 : -1;
+    }
+    Tensor result(PyObject* outo) const {
+        return outo != Py_None ? THPVariable_Unpack(outo) : fresh(q->sizes(), q->scalar_type(), q);
+    }
+};
+
+// The workspace argument, or a new one of `need` bytes; none where the argument is no tensor of the device.
+const Tensor* workspace(PyObject* o, size_t need, const Tensor* like, Tensor* own) {
+    if (o == Py_None) {
+        *own = fresh({static_cast<int64_t>(need < 16 ? 16 : need)}, ScalarType::Byte, like);
+        return own;
+    }
+    const Tensor* t = tensor(o);
+    return t && is(t, t->scalar_type(), like->get_device()) ? t : nullptr;
+}
+
+// attend_scored(q, k_cache, v_cache, block_tables, seq_lens, softcap, slopes, window, prefix_lens, out, scale,
+//               workspace, status) -> out
+PyObject* attend_scored(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Scored x;
+    int window = 0;
+    const int ok = n == 13 ? x.take(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[9], a[10], a[12]) : 0;
+    if (ok < 0 || (ok && !integer(a[7], &window))) return nullptr;
+    if (!ok || x.q->size(0) != x.s.B || !optional(a[8], ScalarType::Int, x.c.dev, {x.s.B})) return code(-1);
+    const c10::cuda::OptionalCUDAGuard guard(x.c.k->device());
+    Tensor own;
+    const Tensor* ws = workspace(a[11], a[11] == Py_None ? pkv_decode_scored_workspace_bytes(x.s.B, x.Hq, x.c.Hkv, x.c.D, 0) : 0,
+                                 x.q, &own);
+    if (!ws) return code(-1);
+    Tensor out = x.result(a[9]);
+    const pkv_status r = pkv_paged_decode_attention_scored(
+        out.data_ptr(), x.q->data_ptr(), x.c.k->data_ptr(), x.c.v->data_ptr(), x.s.tables, x.s.max_blocks, x.s.lens,
+        pointer<int32_t>(a[8]), x.s.B, x.Hq, x.c.Hkv, x.c.D, x.c.BS, x.c.NB, x.scale, x.softcap, pointer<float>(a[6]),
+        window, x.dtype, ws->data_ptr(), ws->nbytes(), x.s.status, stream_of(x.c.dev));
+    return r != PKV_OK ? code(r) : THPVariable_Wrap(std::move(out));
+    END_HANDLE_TH_ERRORS
+}
+
+// prefill_scored(q, k_cache, v_cache, block_tables, seq_lens, q_start, softcap, slopes, window, prefix_lens, out,
+//                scale, status) -> out
+PyObject* prefill_scored(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Scored x;
+    int window = 0;
+    const int ok = n == 13 ? x.take(a[0], a[1], a[2], a[3], a[4], a[6], a[7], a[10], a[11], a[12]) : 0;
+    if (ok < 0 || (ok && !integer(a[8], &window))) return nullptr;
+    if (!ok || !is(tensor(a[5]), ScalarType::Int, x.c.dev, {x.s.B + 1}) ||
+        !optional(a[9], ScalarType::Int, x.c.dev, {x.s.B}))
+        return code(-1);
+    const c10::cuda::OptionalCUDAGuard guard(x.c.k->device());
+    Tensor out = x.result(a[10]);
+    const pkv_status r = pkv_paged_prefill_attention_scored(
+        out.data_ptr(), x.q->data_ptr(), x.c.k->data_ptr(), x.c.v->data_ptr(), x.s.tables, x.s.max_blocks, x.s.lens,
+        pointer<int32_t>(a[5]), pointer<int32_t>(a[9]), x.s.B, static_cast<int>(x.q->size(0)), x.Hq, x.c.Hkv, x.c.D,
+        x.c.BS, x.c.NB, x.scale, x.softcap, pointer<float>(a[7]), window, x.dtype, x.s.status, stream_of(x.c.dev));
+    return r != PKV_OK ? code(r) : THPVariable_Wrap(std::move(out));
+    END_HANDLE_TH_ERRORS
+}
+
+// attend_shared(q, k_cache, v_cache, block_tables, seq_lens, group_start, shared_lens, softcap, slopes, out, scale,
+//               workspace, status) -> out
+PyObject* attend_shared(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Scored x;
+    const int ok = n == 13 ? x.take(a[0], a[1], a[2], a[3], a[4], a[7], a[8], a[9], a[10], a[12]) : 0;
+    if (ok < 0) return nullptr;
+    const Tensor* shared = ok ? tensor(a[6]) : nullptr;
+    if (!ok || x.q->size(0) != x.s.B || !is(shared, ScalarType::Int, x.c.dev) || shared->dim() != 1 ||
+        shared->size(0) > INT_MAX - 1 || !is(tensor(a[5]), ScalarType::Int, x.c.dev, {shared->size(0) + 1}))
+        return code(-1);
+    const c10::cuda::OptionalCUDAGuard guard(x.c.k->device());
+    Tensor own;
+    const Tensor* ws = workspace(a[11], a[11] == Py_None ? pkv_decode_shared_workspace_bytes(x.s.B, x.Hq, x.c.Hkv, x.c.D, 0) : 0,
+                                 x.q, &own);
+    if (!ws) return code(-1);
+    Tensor out = x.result(a[9]);
+    const pkv_status r = pkv_paged_decode_attention_shared(
+        out.data_ptr(), x.q->data_ptr(), x.c.k->data_ptr(), x.c.v->data_ptr(), x.s.tables, x.s.max_blocks, x.s.lens,
+        pointer<int32_t>(a[5]), pointer<int32_t>(a[6]), static_cast<int>(shared->size(0)), x.s.B, x.Hq, x.c.Hkv, x.c.D,
+        x.c.BS, x.c.NB, x.scale, x.softcap, pointer<float>(a[8]), x.dtype, ws->data_ptr(), ws->nbytes(), x.s.status,
+        stream_of(x.c.dev));
+    return r != PKV_OK ? code(r) : THPVariable_Wrap(std::move(out));
+    END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef methods[] = {
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(append)), METH_FASTCALL, nullptr},
     {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(read)), METH_FASTCALL, nullptr},
     {"attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(attend)), METH_FASTCALL, nullptr},
     {"prepare", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(prepare)), METH_FASTCALL, nullptr},
+    {"attend_scored", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(attend_scored)), METH_FASTCALL, nullptr},
+    {"prefill_scored", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(prefill_scored)), METH_FASTCALL, nullptr},
+    {"attend_shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(attend_shared)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
