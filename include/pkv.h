@@ -548,10 +548,10 @@ size_t pkv_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D, int num_
  * zeros), a shared length outside the table, and everything that
  * pkv_paged_decode_attention_scored finds: zero output and
  * PKV_ERR_DEVICE_BOUNDS, for every sequence where group_start is none.  N may be 0.
- * Prefixes are read once for bf16, D = 64 or 128, block_size a multiple of 16, Hq
- * / Hkv <= 128 and 16-byte aligned q, out and pools; elsewhere the result is the
- * same without the saving.  workspace as there, of at least
- * pkv_decode_shared_workspace_bytes(B, Hq, Hkv, D, 0) bytes.
+ * bf16, D = 64 or 128, block_size a multiple of 16, Hq / Hkv <= 128, 16-byte
+ * aligned q, out and pools, fewer than 2^31 pool rows (else PKV_ERR_UNSUPPORTED:
+ * pkv_paged_decode_attention_scored takes any shape).  workspace as there, of at
+ * least pkv_decode_shared_workspace_bytes(B, Hq, Hkv, D, 0) bytes.
  */
 pkv_status pkv_paged_decode_attention_shared(void* out, const void* q, const void* k_cache, const void* v_cache,
                                              const int32_t* block_tables, int max_blocks_per_seq,

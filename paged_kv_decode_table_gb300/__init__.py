@@ -1043,4 +1043,4 @@ def paged_decode_attention_shared(q, k_cache, v_cache, block_tables, seq_lens, g
         return r
     N = shared_lens.shape[0] if isinstance(shared_lens, torch.Tensor) and shared_lens.dim() == 1 else 0
     _scored_failed("pkv_paged_decode_attention_shared", r, q, k_cache, v_cache, block_tables, seq_lens, slopes, out,
-                   workspace, status, {"group_start": (group_start, (N + 1,)), "shared_lens": (shared_lens, (N,))})
+                   workspace, status, {"shared_lens": (shared_lens, (N,)), "group_start": (group_start, (N + 1,))})

@@ -1,0 +1,790 @@
+// decode_attention_shared.cu -- decode attention of sequences that share prefixes ("LLM inference serving tutorial"
+// 4.2: sequences hold the same physical blocks by reference count; 4.1 of "Suy luan & Toi uu hoa (Inference)":
+// online softmax, whose partial results can be joined in any order).
+//
+// softmax over a sequence's keys is taken in two parts, the group's prefix and what the sequence has of its own; each
+// leaves (max, sum, sum of products) per row, and out = sum o_c 2^(m_c - M) / sum l_c 2^(m_c - M).
+//  1. prefix_tc_kernel: the queries of a group's members and of the query heads of one KV head are the rows of one
+//     matrix (members x Hq / Hkv), which meets every prefix key once.  A tile of K and V serves up to 256 rows.
+//  2. decode_split_kernel<.., kShared> (decode_attention_scored.cu): the positions behind the prefix, per sequence.
+//  3. shared_join_kernel: a warp per row.
+// 2 does not wait for 1: an SM that has no prefix work left takes up the rest.
+//
+// prefix_tc_kernel: a persistent kernel, one CTA per SM.  Work = (group, KV head, tile of up to 256 rows) x key tiles of
+// 64; all of it in one order, cut into one range of key tiles per CTA, so that a few rows over a long prefix and many
+// groups over short ones fill the device alike.  What a range covers of one (group, head, row tile) is a piece.
+//  * Operands as in prefill_tc.cu: Q (bf16) in tensor memory, K and V by TMA in boxes of 16 keys through a ring,
+//    S = Q K^T (M 128, N 64, K = D) and O += P V (M 128, N = D, K 64) by one issuing thread each, P through a
+//    128-byte-swizzled shared tile, S and O in tensor memory (256 columns per query tile of 128 rows).
+//  * Thread r of a query tile's four softmax warps owns row r.  A maximum is renewed (and O in tensor memory
+//    rescaled) only when a score exceeds it by 2^8.
+//  * A piece leaves its row maxima, sums and float32 O: 512 bytes per row of 128 dimensions, written through the P tile
+//    so that a warp stores whole 128-byte lines.
+// Every mbarrier wait is bounded; a CTA that gives up records PKV_ERR_TIMEOUT, waits (bounded) for its own TMA copies,
+// and frees its tensor memory.
+#include <cuda.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "attention_split.cuh"
+#include "tensor_core.cuh"
+
+namespace pkv {
+
+int device_sm_count();
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn get_encode_fn();
+bool split_applies(SplitPlan& pl, const void* out, const void* q, const void* k, const void* v, pkv_dtype dtype);
+bool split_shape(int Hq, int Hkv, int D, int BS, int min_groups, SplitPlan& pl);
+size_t split_space(const SplitPlan& pl, int P, int B, bool shared, void* base, SplitSpace* ws);
+cudaError_t launch_split_shared(const SplitPlan& pl, const SplitSpace& ws, const void* q, const void* k, const void* v,
+                                const int32_t* block_tables, const int32_t* seq_lens, int P, int32_t* status,
+                                cudaStream_t stream, bool* done);
+bool scored_shape_valid(int B, int Hq, int Hkv, int D, int BS, int NB, int max_blocks, pkv_dtype dtype);
+
+constexpr int kPxRows = 128, kPxTiles = 2, kPxKeys = 64;
+constexpr int kPxProd = 3;     // producer warps
+constexpr int kPxWin = 640;    // block-table entries kept in shared memory, per producer warp
+constexpr int kPxMarks = 16;   // pieces of which a bad block is remembered; more than the ring has stages
+constexpr int kPxPBytes = kPxRows * kPxKeys * 2;
+// warps 0-7: softmax (warp w: query tile w / 4); 8, 11, 12: producers; 9: S MMAs (and the TMEM allocation); 10: PV MMAs
+constexpr int kPxWarpProd = 8, kPxWarpS = 9, kPxWarpPV = 10;
+constexpr int kPxThreads = 13 * 32;
+constexpr int kPxTmemCols = 512;  // query tile t: Q at 256 t, S at 256 t + 64, O at 256 t + 128
+constexpr int kPxMinTiles = 2;    // key tiles of a range at least
+
+template <int kD>
+struct Px {
+    static constexpr int kStages = kD == 128 ? 5 : 10;
+    static constexpr int kKBytes = kPxKeys * kD * 2;
+    static constexpr int kGroup = 16 * kD * 2;  // 16 keys
+    static constexpr int kStageBytes = 2 * kKBytes;
+    static constexpr size_t kOperands = kPxTiles * static_cast<size_t>(kPxPBytes) + kStages * static_cast<size_t>(kStageBytes);
+};
+struct PxShared {  // follows the 1024-aligned operand area
+    uint64_t kv_full[10], kv_empty[10];
+    uint64_t q_full[kPxTiles], s_full[kPxTiles], s_free[kPxTiles], p_full[kPxTiles], o_done[kPxTiles];
+    uint32_t tmem_base;
+    int g0, base0, red[33];
+    int bad[kPxMarks];
+    int tbl[kPxProd][kPxWin];
+};
+template <int kD>
+constexpr size_t kPxSmem = 1024 + Px<kD>::kOperands + sizeof(PxShared);
+static_assert(kPxSmem<128> <= 227 * 1024 && kPxSmem<64> <= 227 * 1024, "shared memory of one CTA");
+
+// Written by the prefix kernel's first CTA for the join.
+struct PxHead {
+    int W;      // key tiles per range
+    int valid;  // group_start is one
+};
+struct PxSpace {
+    PxHead* head;
+    int2* plan;   // of every group: (first key tile in the order, key tiles of a row tile)
+    float2* ml;   // (max, sum): 2 slots per CTA of 256 rows, then a place per row of out
+    float* o;
+    int rows;     // of a slot
+};
+
+struct PxPlan {
+    int B, Hq, Hkv, G, BS, NB, max_blocks;
+    int TQ, TC;  // members per query tile and per row tile
+    ScoreArgs sc;
+    GroupArgs groups;
+};
+
+// Key tiles of one row tile of group g, and its row tiles (0 where there is no prefix to share).
+__device__ __forceinline__ void px_group(const PxPlan& pl, int g, int& nt, int& rt) {
+    const int n = pl.groups.start[g + 1] - pl.groups.start[g];
+    const int P = n > 1 ? group_prefix(pl.groups, pl.max_blocks, pl.BS, g) : 0;
+    nt = P > 0 ? (P + kPxKeys - 1) / kPxKeys : 0;
+    rt = n > 1 ? (n + pl.TC - 1) / pl.TC : 0;
+}
+
+// A role's walk over the CTA's pieces.
+struct PxWalk {
+    int g, base, nt, rt;             // group, its first key tile in the order, its key tiles and row tiles
+    int first, n;                    // its first sequence, its members
+    int h, tile, k0, k1;             // the piece: KV head, row tile, key tiles [k0, k1)
+    __device__ __forceinline__ void load(const PxPlan& pl) {
+        px_group(pl, g, nt, rt);
+        first = pl.groups.start[g];
+        n = pl.groups.start[g + 1] - first;
+    }
+    __device__ __forceinline__ PxWalk(const PxPlan& pl, int g0, int base0) : g(g0), base(base0) { load(pl); }
+    // The piece at key tile `at` of a range that ends at `end`.
+    __device__ __forceinline__ void to(const PxPlan& pl, int at, int end) {
+        while (at >= base + pl.Hkv * rt * nt) {
+            base += pl.Hkv * rt * nt;
+            ++g;
+            load(pl);
+        }
+        const int rel = at - base, work = rel / nt;
+        k0 = rel - work * nt;
+        k1 = min(nt, k0 + end - at);
+        h = work / rt;
+        tile = work - h * rt;
+    }
+    // Query tiles of the piece that hold members.
+    __device__ __forceinline__ int tiles(const PxPlan& pl) const { return n - tile * pl.TC > pl.TQ ? 2 : 1; }
+};
+
+template <int kD, bool kScored>
+__global__ void __launch_bounds__(kPxThreads, 1)
+    prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ PxPlan pl, const __nv_bfloat16* q, const int32_t* block_tables,
+                     const int32_t* seq_lens, const PxSpace ws, int32_t* status) {
+    using C = Px<kD>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t px_raw[];
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(px_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sP = base;  // P of query tile t at t kPxPBytes
+    uint8_t* sKV = base + kPxTiles * kPxPBytes;
+    PxShared* sm = reinterpret_cast<PxShared*>(base + C::kOperands);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int BS = pl.BS, G = pl.G;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm->kv_full[s], kPxProd);  // one arrival (with its bytes) per producer warp
+            mbar_init(&sm->kv_empty[s], 1);
+        }
+        for (int t = 0; t < kPxTiles; ++t) {
+            mbar_init(&sm->q_full[t], kPxRows);
+            mbar_init(&sm->s_full[t], 1);
+            mbar_init(&sm->s_free[t], kPxRows);
+            mbar_init(&sm->p_full[t], kPxRows);
+            mbar_init(&sm->o_done[t], 1);
+        }
+        fence_mbar_init();
+        prefetch_tmap(&tmK);
+        prefetch_tmap(&tmV);
+        sm->g0 = sm->base0 = 0;
+        for (int i = 0; i < kPxMarks; ++i) sm->bad[i] = 0;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- the whole work, and this CTA's range of it: key tiles [start, end)
+    const int N = pl.groups.N;
+    auto scan = [&](int v, int& total) {  // over the CTA; exclusive
+        int x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) sm->red[warp] = x;
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int w = 0; w < kPxThreads / 32; ++w) {
+            const int r = sm->red[w];
+            if (w < warp) before += r;
+            all += r;
+        }
+        __syncthreads();
+        total = all;
+        return before + x - v;
+    };
+    bool wrong = false;
+    int sum = 0, total;
+    for (int g = tid; g < N; g += kPxThreads) {
+        const int s = pl.groups.start[g], e = pl.groups.start[g + 1];
+        if (s > e || s < 0 || e > pl.B || (g == 0 && s != 0)) {
+            wrong = true;
+            continue;
+        }
+        int nt, rt;
+        px_group(pl, g, nt, rt);
+        sum += pl.Hkv * nt * rt;
+    }
+    wrong = __syncthreads_or(wrong) != 0;
+    scan(sum, total);
+    const int P = static_cast<int>(gridDim.x);
+    const int W = max(kPxMinTiles, (total + P - 1) / P);
+    if (blockIdx.x == 0 && tid == 0) {
+        *ws.head = PxHead{W, wrong ? 0 : 1};
+        if (wrong) report(status, PKV_ERR_DEVICE_BOUNDS);
+    }
+    const int start = min(total, static_cast<int>(blockIdx.x) * W), end = min(total, start + W);
+    if (wrong || (start >= end && blockIdx.x != 0)) return;  // uniform over the CTA
+    int carry = 0;
+    for (int g0 = 0; g0 < N; g0 += kPxThreads) {
+        const int g = g0 + tid;
+        int nt = 0, rt = 0, tot;
+        if (g < N) px_group(pl, g, nt, rt);
+        const int n = pl.Hkv * nt * rt, at = carry + scan(n, tot);
+        if (n > 0 && at <= start && start < at + n) {  // exactly one thread of the CTA
+            sm->g0 = g;
+            sm->base0 = at;
+        }
+        if (blockIdx.x == 0 && g < N) ws.plan[g] = make_int2(at, nt);
+        carry += tot;
+        if (carry > start && blockIdx.x != 0) break;  // same decision in every thread
+    }
+    if (start >= end) return;
+    if (warp == kPxWarpS) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
+                     "r"(kPxTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem_base;
+    const int g0 = sm->g0, base0 = sm->base0;
+
+    bool fail = false;
+    if (warp == kPxWarpProd || warp > kPxWarpPV) {
+        // ------------------------------------------------ producer warps 8, 11, 12
+        // Warp pw issues boxes i = pw, pw + 3, pw + 6 of every tile (box i: K of 16-key group i for i < 4, V of group
+        // i - 4 otherwise), with block ids from its own window of the block table, and arms the stage's transaction
+        // count with its own bytes.
+        const int pw = warp == kPxWarpProd ? 0 : warp - kPxWarpPV;
+        const int nbox = pw < 2 ? 3 : 2;
+        int* tbl = sm->tbl[pw];
+        PxWalk w(pl, g0, base0);
+        int j = 0;
+        for (int at = start, piece = 0; at < end && !fail; at += w.k1 - w.k0, ++piece) {
+            w.to(pl, at, end);
+            const int32_t* trow = block_tables + static_cast<size_t>(w.first) * pl.max_blocks;
+            const int nblk = group_prefix(pl.groups, pl.max_blocks, BS, w.g) / BS;
+            int win0 = -kPxWin;
+            for (int kt = w.k0; kt < w.k1 && !fail; ++kt, ++j) {
+                const int s = j % kStages;
+                const int kb0 = (kt * kPxKeys) / BS, kb1 = min(nblk - 1, (kt * kPxKeys + kPxKeys - 1) / BS);
+                if (kb0 < win0 || kb1 >= win0 + kPxWin) {  // move this warp's window of the block table
+                    __syncwarp();
+                    win0 = kb0;
+                    for (int i = lane; i < kPxWin; i += 32) tbl[i] = win0 + i < nblk ? trow[win0 + i] : 0;
+                    __syncwarp();
+                }
+                if (lane == 0 && !mbar_wait(&sm->kv_empty[s], ((j / kStages) & 1) ^ 1)) {
+                    report(status, PKV_ERR_TIMEOUT);
+                    fail = true;
+                }
+                fail = __shfl_sync(0xffffffffu, fail, 0);
+                if (fail) break;
+                const int bi = pw + 3 * lane;
+                int row = 0;
+                if (lane < nbox) {  // the pool row of box bi's first key
+                    const int key0 = kt * kPxKeys + 16 * (bi & 3), kb = key0 / BS;
+                    int blk = 0, slot = 0;
+                    if (kb < nblk) {  // keys behind the prefix: any valid rows (masked; their V rows are cleared)
+                        blk = tbl[kb - win0];
+                        slot = key0 - kb * BS;
+                        if (blk < 0 || blk >= pl.NB) {
+                            *const_cast<volatile int*>(&sm->bad[piece % kPxMarks]) = piece + 1;
+                            report(status, PKV_ERR_DEVICE_BOUNDS);
+                            blk = 0;
+                        }
+                    }
+                    row = (blk * pl.Hkv + w.h) * BS + slot;
+                }
+                __syncwarp();  // the marks precede the arrival
+                if (lane == 0) mbar_arrive_expect_tx(&sm->kv_full[s], nbox * C::kGroup);
+                __syncwarp();  // the arrival precedes this warp's copies
+                if (lane < nbox) {
+                    uint8_t* st = sKV + static_cast<size_t>(s) * C::kStageBytes + (bi < 4 ? 0 : C::kKBytes) + C::kGroup * (bi & 3);
+                    if constexpr (kD == 64) {
+                        tma_load_2d(st, bi < 4 ? &tmK : &tmV, 0, row, &sm->kv_full[s]);
+                    } else {
+                        if (bi < 4)  // [8-row half][64-dimension half][8 rows][128 B]
+                            tma_load_4d(st, &tmK, 0, 0, 0, row >> 3, &sm->kv_full[s]);
+                        else  // [64-dimension half][16 rows][128 B]
+                            tma_load_3d(st, &tmV, 0, row, 0, &sm->kv_full[s]);
+                    }
+                }
+                __syncwarp();
+            }
+        }
+        // no copy of this CTA may still be in flight when it exits
+        if (lane == 0)
+            for (int i = max(0, j - kStages); i < j; ++i) mbar_wait(&sm->kv_full[i % kStages], (i / kStages) & 1);
+    } else if (warp == kPxWarpS) {
+        // ------------------------------------------------ S = Q K^T (lane 0 issues)
+        if (lane == 0) {
+            constexpr uint32_t idS = tc_idesc(kPxRows, kPxKeys, false);
+            const uint32_t kva = smem_u32(sKV);
+            PxWalk w(pl, g0, base0);
+            int j = 0, done[kPxTiles] = {0, 0}, pieces[kPxTiles] = {0, 0};
+            for (int at = start; at < end && !fail; at += w.k1 - w.k0) {
+                w.to(pl, at, end);
+                const int nq = w.tiles(pl);
+                for (int kt = w.k0; kt < w.k1 && !fail; ++kt, ++j) {
+                    const int s = j % kStages;
+                    if (!mbar_wait(&sm->kv_full[s], (j / kStages) & 1)) {
+                        fail = true;
+                        break;
+                    }
+                    const uint32_t kb = kva + s * C::kStageBytes;
+                    for (int t = 0; t < nq; ++t) {
+                        if ((kt == w.k0 && !mbar_wait(&sm->q_full[t], pieces[t] & 1)) ||
+                            (done[t] >= 1 && !mbar_wait(&sm->s_free[t], (done[t] - 1) & 1))) {
+                            fail = true;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < kD / 16; ++kk)
+                            tc_mma_ta(tmem + 256 * t + 64, tmem + 256 * t + 8 * kk,
+                                      kD == 64 ? tc_desc(kb + 32 * kk, 16, 1024)
+                                               : tc_desc(kb + (kk >> 2) * 1024 + 32 * (kk & 3), 16, 2048),
+                                      idS, kk > 0 ? 1u : 0u);
+                        tc_commit(&sm->s_full[t]);
+                        ++done[t];
+                    }
+                }
+                for (int t = 0; t < nq; ++t) ++pieces[t];
+            }
+            if (fail) report(status, PKV_ERR_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (warp == kPxWarpPV) {
+        // ------------------------------------------------ O += P V (lane 0 issues)
+        if (lane == 0) {
+            constexpr uint32_t idO = tc_idesc(kPxRows, kD, true);
+            const uint32_t pa = smem_u32(sP), kva = smem_u32(sKV);
+            PxWalk w(pl, g0, base0);
+            int j = 0, done[kPxTiles] = {0, 0};
+            for (int at = start; at < end && !fail; at += w.k1 - w.k0) {
+                w.to(pl, at, end);
+                const int nq = w.tiles(pl);
+                for (int kt = w.k0; kt < w.k1 && !fail; ++kt, ++j) {
+                    const int s = j % kStages;
+                    const uint32_t vb = kva + s * C::kStageBytes + C::kKBytes;
+                    for (int t = 0; t < nq; ++t) {  // query tile 0 first: its softmax warps clear V rows
+                        if (!mbar_wait(&sm->p_full[t], done[t] & 1)) {
+                            fail = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t pb = pa + t * kPxPBytes;
+#pragma unroll
+                        for (int kk = 0; kk < kPxKeys / 16; ++kk)
+                            tc_mma(tmem + 256 * t + 128, tc_desc(pb + 32 * kk, 16, 1024),
+                                   tc_desc(vb + C::kGroup * kk, C::kGroup / 2, 1024), idO, (kt > w.k0 || kk > 0) ? 1u : 0u);
+                        tc_commit(&sm->o_done[t]);
+                        ++done[t];
+                    }
+                    if (!fail) tc_commit(&sm->kv_empty[s]);
+                }
+            }
+            if (fail) report(status, PKV_ERR_TIMEOUT);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ softmax warps: thread r of query tile qt owns row r
+        const int qt = warp >> 2, r = tid & (kPxRows - 1);
+        const uint32_t lrow = static_cast<uint32_t>((warp & 3) * 32) << 16;  // this warp's TMEM lanes
+        const uint32_t tq = tmem + 256 * qt + lrow;
+        uint8_t* pbuf = sP + qt * kPxPBytes;
+        PxWalk w(pl, g0, base0);
+        int j = 0, done = 0;  // key tiles of the CTA, and of this query tile
+        for (int at = start, piece = 0; at < end && !fail; at += w.k1 - w.k0, ++piece) {
+            w.to(pl, at, end);
+            if (qt >= w.tiles(pl)) {
+                j += w.k1 - w.k0;
+                continue;
+            }
+            const int member = w.tile * pl.TC + qt * pl.TQ + r / G, qh = w.h * G + r % G;
+            const bool valid = r < pl.TQ * G && member < w.n;  // the other rows are zero queries
+            const int b = w.first + (valid ? member : 0);
+            {
+                const uint4* src = reinterpret_cast<const uint4*>(q + (static_cast<size_t>(b) * pl.Hq + qh) * kD);
+#pragma unroll
+                for (int hv = 0; hv < kD / 64; ++hv) {
+                    uint32_t x[32];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint4 v = valid ? src[8 * hv + c] : make_uint4(0u, 0u, 0u, 0u);
+                        x[4 * c] = v.x;
+                        x[4 * c + 1] = v.y;
+                        x[4 * c + 2] = v.z;
+                        x[4 * c + 3] = v.w;
+                    }
+                    tc_st32(tq + 32 * hv, x);
+                }
+                tc_fence_before();
+                mbar_arrive(&sm->q_full[qt]);
+            }
+            const int prefix = group_prefix(pl.groups, pl.max_blocks, BS, w.g);
+            [[maybe_unused]] const int pos = kScored && valid ? seq_lens[b] - 1 : 0;
+            [[maybe_unused]] const float slope = kScored && pl.sc.slopes != nullptr ? pl.sc.slopes[qh] * kLog2e : 0.f;
+            float m_ref = -INFINITY, lsum = 0.f;
+            for (int kt = w.k0; kt < w.k1; ++kt, ++j, ++done) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&sm->s_full[qt], done & 1))) {  // tcgen05.ld needs the whole warp
+                    fail = true;
+                    break;
+                }
+                tc_fence_after();
+                uint32_t sr[2][32];
+                tc_ld32(tq + 64, sr[0]);
+                tc_ld32(tq + 96, sr[1]);
+                tc_fence_before();
+                mbar_arrive(&sm->s_free[qt]);  // S may take the next tile
+                const int kbase = kt * kPxKeys;
+                if constexpr (kScored) tc_scores(sr, kbase - pos, slope, pl.sc);
+                const bool tail = kbase + kPxKeys > prefix;
+                if (tail) {
+#pragma unroll
+                    for (int c = 0; c < kPxKeys; ++c)
+                        if (kbase + c >= prefix) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+                }
+                float mxs[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mxs[k] = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < kPxKeys; c += 2)
+                    mxs[(c >> 1) & 3] = tc_max3(mxs[(c >> 1) & 3], __uint_as_float(sr[c >> 5][c & 31]),
+                                                __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
+                const float mul = kScored ? 1.f : pl.sc.mul;
+                const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * mul;
+                const float m_new = mx > m_ref + 8.f ? mx : m_ref;
+                const bool resc = m_new != m_ref;
+                const float a = resc ? tc_ex2(m_ref - m_new) : 1.f;
+                m_ref = m_new;
+                const float nmu = m_ref == -INFINITY ? 0.f : -m_ref;
+                uint32_t pk[kPxKeys / 2];
+                float ls[4][2];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) ls[k][0] = ls[k][1] = 0.f;
+#pragma unroll
+                for (int c = 0; c < kPxKeys / 2; ++c) {
+                    float t0, t1;
+                    tc_fma2(t0, t1, __uint_as_float(sr[(2 * c) >> 5][(2 * c) & 31]),
+                            __uint_as_float(sr[(2 * c + 1) >> 5][(2 * c + 1) & 31]), mul, nmu);
+                    const float e0 = tc_ex2(t0), e1 = tc_ex2(t1);
+                    pk[c] = pack_bf16x2(e0, e1);
+                    tc_add2(ls[c & 3][0], ls[c & 3][1], e0, e1);
+                }
+                lsum = lsum * a + (((ls[0][0] + ls[0][1]) + (ls[1][0] + ls[1][1])) +
+                                   ((ls[2][0] + ls[2][1]) + (ls[3][0] + ls[3][1])));
+                // the PV of the tile before is complete: O may be rescaled and the P tile rewritten
+                if (kt > w.k0) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (done - 1) & 1))) {
+                        fail = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+                        for (int cc = 0; cc < kD / 32; ++cc) {
+                            uint32_t o[32];
+                            tc_ld32(tq + 128 + 32 * cc, o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                            tc_st32(tq + 128 + 32 * cc, o);
+                        }
+                    }
+                }
+                if (tail && qt == 0) {  // the V rows of keys behind the prefix may hold anything: clear them
+                    const int rlo = prefix - kbase;
+                    uint8_t* vb = sKV + static_cast<size_t>(j % kStages) * C::kStageBytes + C::kKBytes;
+                    constexpr int kRowChunks = kD / 8;
+                    for (int idx = r; idx < (kPxKeys - rlo) * kRowChunks; idx += kPxRows) {
+                        const int rr = rlo + idx / kRowChunks, half = (idx / 8) % (kRowChunks / 8), ch = idx & 7;
+                        *reinterpret_cast<uint4*>(vb + C::kGroup * (rr >> 4) + half * 2048 + (rr & 15) * 128 + ch * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch)
+                    *reinterpret_cast<uint4*>(pbuf + sw128(r, ch)) =
+                        make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
+                fence_proxy_async_smem();  // P and the cleared V rows, for the PV MMA
+                tc_fence_before();
+                mbar_arrive(&sm->p_full[qt]);
+            }
+            if (!fail && !__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (done - 1) & 1))) fail = true;
+            if (fail) {
+                if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+                break;
+            }
+            // ---- the piece's rows: a place per row of out where it is the whole prefix, else this range's slot
+            tc_fence_after();
+            const bool whole = w.k0 == 0 && w.k1 == w.nt;
+            const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (w.k0 > 0 ? 0 : 1);
+            const size_t own = whole ? 2 * static_cast<size_t>(gridDim.x) * ws.rows + static_cast<size_t>(b) * pl.Hq + qh
+                                     : slot * ws.rows + qt * kPxRows + r;
+            const bool broken = *const_cast<volatile int*>(&sm->bad[piece % kPxMarks]) == piece + 1;
+            if (valid) ws.ml[own] = make_float2(m_ref, broken ? -1.f : lsum);
+            // the P tile is free: 32 columns of the warp's 32 rows go through its quarter of it
+            float4* stage = reinterpret_cast<float4*>(pbuf + (warp & 3) * 4096);
+            const int own_lo = valid ? static_cast<int>(own) : -1, own_hi = valid ? static_cast<int>(own >> 32) : -1;
+#pragma unroll 1
+            for (int cc = 0; cc < kD / 32; ++cc) {
+                uint32_t o[32];
+                tc_ld32(tq + 128 + 32 * cc, o);
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    stage[lane * 8 + (c ^ (lane & 7))] =
+                        make_float4(__uint_as_float(o[4 * c]), __uint_as_float(o[4 * c + 1]),
+                                    __uint_as_float(o[4 * c + 2]), __uint_as_float(o[4 * c + 3]));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int rr = 4 * i + (lane >> 3), c = lane & 7;
+                    const int lo = __shfl_sync(0xffffffffu, own_lo, rr), hi = __shfl_sync(0xffffffffu, own_hi, rr);
+                    const float4 v = stage[rr * 8 + (c ^ (rr & 7))];
+                    if (hi >= 0) {
+                        const size_t to = (static_cast<size_t>(hi) << 32) | static_cast<uint32_t>(lo);
+                        *reinterpret_cast<float4*>(ws.o + to * kD + 32 * cc + 4 * c) = v;
+                    }
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+        }
+    }
+    // ---- every role is done with TMEM
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kPxWarpS) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kPxTmemCols) : "memory");
+    }
+}
+
+// ------------------------------------------------------------------ join
+// A warp a row: the pieces of its group's prefix, then those of what its sequence has of its own.
+constexpr int kSjWarps = 4;
+constexpr int kSjGroup = 8;  // pieces in flight
+
+template <int kD>
+__global__ void __launch_bounds__(kSjWarps * 32)
+    shared_join_kernel(const __grid_constant__ PxPlan pl, const PxSpace px, const SplitSpace ws, const int R,
+                       const int32_t* seq_lens, __nv_bfloat16* out, const int P, int32_t* status) {
+    const long long row = static_cast<long long>(blockIdx.x) * kSjWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (row >= static_cast<long long>(pl.B) * pl.Hq) return;
+    const int b = static_cast<int>(row / pl.Hq), qh = static_cast<int>(row - static_cast<long long>(b) * pl.Hq);
+    constexpr int kCols = kD / 32;  // of a lane
+    float acc[kCols] = {};
+    float M = -INFINITY, l = 0.f;
+    const int L = seq_lens[b];
+    bool bad = px.head->valid == 0 || L < 0 || static_cast<long long>(L) > static_cast<long long>(pl.max_blocks) * pl.BS;
+    const int g = bad ? -1 : group_of(pl.groups, b);
+    const int prefix = g < 0 ? 0 : group_prefix(pl.groups, pl.max_blocks, pl.BS, g);
+    bad = bad || (L > 0 && (prefix < 0 || L < prefix));
+    if (bad && lane == 0 && qh == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
+    if (!bad && L > 0) {
+        auto take = [&](const float2* mls, const float* os, int pieces, auto place) {
+            for (int p0 = 0; p0 < pieces; p0 += kSjGroup) {
+                float2 ml[kSjGroup];
+                float o[kSjGroup][kCols];
+#pragma unroll
+                for (int k = 0; k < kSjGroup; ++k) {
+                    ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i) o[k][i] = 0.f;
+                    if (p0 + k < pieces) {
+                        const size_t at = place(p0 + k);
+                        ml[k] = __ldcg(mls + at);
+                        if constexpr (kCols == 4) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(os + at * kD) + lane);
+                            o[k][0] = v.x;
+                            o[k][1] = v.y;
+                            o[k][2] = v.z;
+                            o[k][3] = v.w;
+                        } else {
+                            const float2 v = __ldcg(reinterpret_cast<const float2*>(os + at * kD) + lane);
+                            o[k][0] = v.x;
+                            o[k][1] = v.y;
+                        }
+                    }
+                }
+                float mn = M;
+#pragma unroll
+                for (int k = 0; k < kSjGroup; ++k) mn = fmaxf(mn, ml[k].x);
+                const float mu = mn == -INFINITY ? 0.f : mn, fa = ex2_approx(M - mu);
+                l *= fa;
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) acc[i] *= fa;
+                M = mn;
+#pragma unroll
+                for (int k = 0; k < kSjGroup; ++k) {
+                    const float f = ex2_approx(ml[k].x - mu);
+                    bad = bad || ml[k].y < 0.f;  // a piece that could not be read makes the row zero
+                    l = fmaf(ml[k].y, f, l);
+#pragma unroll
+                    for (int i = 0; i < kCols; ++i) acc[i] = fmaf(o[k][i], f, acc[i]);
+                }
+            }
+        };
+        if (prefix > 0) {
+            const int2 plan = px.plan[g];
+            const int member = b - pl.groups.start[g], rt = (pl.groups.start[g + 1] - pl.groups.start[g] + pl.TC - 1) / pl.TC;
+            const int tile = member / pl.TC, in = member - tile * pl.TC, qt = in / pl.TQ, W = px.head->W;
+            const int h = qh / pl.G, r = (in - qt * pl.TQ) * pl.G + qh - h * pl.G;
+            const int first = plan.x + (h * rt + tile) * plan.y, f = first / W, pieces = (first + plan.y - 1) / W - f + 1;
+            take(px.ml, px.o, pieces, [&](int p) {
+                return pieces == 1 ? 2 * static_cast<size_t>(P) * px.rows + row
+                                   : (2 * static_cast<size_t>(f + p) + (p == 0 ? 1 : 0)) * px.rows + qt * kPxRows + r;
+            });
+        }
+        const int2 info = ws.info[b];
+        if (info.y > 0) {
+            const int grp = qh / R, W = ws.head->W;
+            const int first = info.x + grp * info.y, f = first / W, pieces = (first + info.y - 1) / W - f + 1;
+            take(ws.ml, ws.o, pieces, [&](int p) {
+                return pieces == 1 ? 2 * static_cast<size_t>(P) * R + row
+                                   : (2 * static_cast<size_t>(f + p) + (p == 0 ? 1 : 0)) * R + (qh - grp * R);
+            });
+        }
+    }
+    const bool zero = bad || l == 0.f;
+    const float inv = 1.f / l;
+    __nv_bfloat16* to = out + row * kD + kCols * lane;
+    if constexpr (kCols == 4)
+        *reinterpret_cast<uint2*>(to) = zero ? make_uint2(0u, 0u)
+                                             : make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                          pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    else
+        *reinterpret_cast<uint32_t*>(to) = zero ? 0u : pack_bf16x2(acc[0] * inv, acc[1] * inv);
+}
+
+// ------------------------------------------------------------------ host side
+bool encode_pool_k16(CUtensorMap* map, const void* pool, int NB, int Hkv, int BS);
+bool encode_pool_box_halves(CUtensorMap* map, const void* pool, int NB, int Hkv, int BS, int box_rows);
+
+// A pool of 64-element rows in boxes of 16 rows, 128-byte swizzle.
+static bool encode_pool_rows64(CUtensorMap* map, const void* pool, long long rows) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    cuuint64_t dim[2] = {64, static_cast<cuuint64_t>(rows)}, stride[1] = {128};
+    cuuint32_t box[2] = {64, 16}, one[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), dim, stride, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [head][plan of up to B groups][(max, sum)][O]
+static size_t px_space(int B, int Hq, int Hkv, int D, int P, void* base, PxSpace* ws) {
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const int G = Hq / Hkv, rows = B > kPxRows / G ? kPxTiles * kPxRows : kPxRows;
+    const size_t places = 2 * static_cast<size_t>(P) * rows + static_cast<size_t>(B) * Hq;
+    const size_t ml = up(256 + sizeof(int2) * static_cast<size_t>(B)), o = up(ml + places * sizeof(float2));
+    if (ws != nullptr) {
+        uint8_t* p = static_cast<uint8_t*>(base);
+        ws->head = reinterpret_cast<PxHead*>(p);
+        ws->plan = reinterpret_cast<int2*>(p + 256);
+        ws->ml = reinterpret_cast<float2*>(p + ml);
+        ws->o = reinterpret_cast<float*>(p + o);
+        ws->rows = rows;
+    }
+    return up(o + places * D * sizeof(float));
+}
+
+template <int kD>
+static cudaError_t launch_shared(const PxPlan& px, SplitPlan pl, void* out, const void* q, const void* k, const void* v,
+                                 const int32_t* block_tables, const int32_t* seq_lens, void* workspace, int P,
+                                 int32_t* status, cudaStream_t stream) {
+    CUtensorMap tmK, tmV;
+    const long long rows = static_cast<long long>(pl.NB) * pl.Hkv * pl.BS;
+    if (kD == 64 ? !encode_pool_rows64(&tmK, k, rows) || !encode_pool_rows64(&tmV, v, rows)
+                 : !encode_pool_k16(&tmK, k, pl.NB, pl.Hkv, pl.BS) || !encode_pool_box_halves(&tmV, v, pl.NB, pl.Hkv, pl.BS, 16))
+        return cudaErrorInvalidValue;
+    PxSpace pws = {};
+    SplitSpace ws = {};
+    const size_t used = px_space(pl.B, pl.Hq, pl.Hkv, pl.D, P, workspace, &pws);
+    split_space(pl, P, pl.B, true, static_cast<uint8_t*>(workspace) + used, &ws);
+    const bool scored = pl.sc.cap_log2 > 0.f || pl.sc.slopes != nullptr;
+    auto kern = scored ? prefix_tc_kernel<kD, true> : prefix_tc_kernel<kD, false>;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPxSmem<kD>));
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(P), 1, 1);
+    cfg.blockDim = dim3(kPxThreads, 1, 1);
+    cfg.dynamicSmemBytes = kPxSmem<kD>;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, px, static_cast<const __nv_bfloat16*>(q), block_tables, seq_lens, pws, status);
+    if (err != cudaSuccess) return err;
+    bool done = false;
+    err = launch_split_shared(pl, ws, q, k, v, block_tables, seq_lens, P, status, stream, &done);
+    if (err != cudaSuccess || !done) return err != cudaSuccess ? err : cudaErrorInvalidValue;
+    const long long n = static_cast<long long>(pl.B) * pl.Hq;
+    cfg.gridDim = dim3(static_cast<unsigned>((n + kSjWarps - 1) / kSjWarps), 1, 1);
+    cfg.blockDim = dim3(kSjWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    err = cudaLaunchKernelEx(&cfg, shared_join_kernel<kD>, px, pws, ws, pl.R, seq_lens, static_cast<__nv_bfloat16*>(out), P, status);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+}  // namespace pkv
+
+extern "C" size_t pkv_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D, int num_sms) {
+    using namespace pkv;
+    const size_t plain = pkv_decode_scored_workspace_bytes(B, Hq, Hkv, D, num_sms);
+    if (plain == 0) return 0;
+    const int P = num_sms > 0 ? num_sms : device_sm_count();
+    SplitPlan pl = {};
+    pl.Hq = Hq;
+    pl.D = D;
+    if ((D != 64 && D != 128) || Hq / Hkv > kPxRows || !split_shape(Hq, Hkv, D, 16, 1, pl)) return plain;
+    return std::max(plain, px_space(B, Hq, Hkv, D, P, nullptr, nullptr) + split_space(pl, P, B, true, nullptr, nullptr));
+}
+
+extern "C" pkv_status pkv_paged_decode_attention_shared(
+    void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    int max_blocks_per_seq, const int32_t* seq_lens, const int32_t* group_start, const int32_t* shared_lens, int N,
+    int B, int Hq, int Hkv, int D, int block_size, int num_blocks, float scale, float softcap, const float* slopes,
+    pkv_dtype dtype, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+    using namespace pkv;
+    ScoreArgs sc;
+    if (!scored_shape_valid(B, Hq, Hkv, D, block_size, num_blocks, max_blocks_per_seq, dtype) ||
+        !make_scores(&sc, scale, D, softcap, slopes, 0, nullptr) || N < 0 || N > B)
+        return PKV_ERR_INVALID_ARG;
+    if (N == 0)
+        return pkv_paged_decode_attention_scored(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
+                                                 nullptr, B, Hq, Hkv, D, block_size, num_blocks, scale, softcap, slopes, 0,
+                                                 dtype, workspace, workspace_bytes, dev_status, stream);
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !group_start || !shared_lens || !workspace ||
+        (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
+        return PKV_ERR_INVALID_ARG;
+    SplitPlan pl = {};
+    pl.B = B;
+    pl.Hq = Hq;
+    pl.Hkv = Hkv;
+    pl.G = Hq / Hkv;
+    pl.D = D;
+    pl.BS = block_size;
+    pl.NB = num_blocks;
+    pl.max_blocks = max_blocks_per_seq;
+    pl.sc = sc;
+    pl.groups = GroupArgs{group_start, shared_lens, N};
+    PxPlan px = {};
+    px.B = B;
+    px.Hq = Hq;
+    px.Hkv = Hkv;
+    px.G = pl.G;
+    px.BS = block_size;
+    px.NB = num_blocks;
+    px.max_blocks = max_blocks_per_seq;
+    px.TQ = pl.G <= kPxRows ? kPxRows / pl.G : 0;
+    px.TC = kPxTiles * px.TQ;
+    px.sc = sc;
+    px.groups = pl.groups;
+    if ((D != 64 && D != 128) || px.TQ == 0 || !split_applies(pl, out, q, k_cache, v_cache, dtype)) return PKV_ERR_UNSUPPORTED;
+    // pool rows and key tiles stay in 32 bits
+    const long long tiles = (static_cast<long long>(max_blocks_per_seq) * block_size / kPxKeys + 1) * Hkv *
+                            (static_cast<long long>(B) / px.TC + N);
+    if (static_cast<long long>(num_blocks) * Hkv * block_size >= (1LL << 31) || tiles >= (1LL << 30)) return PKV_ERR_UNSUPPORTED;
+    const int P = device_sm_count();
+    if (workspace_bytes < pkv_decode_shared_workspace_bytes(B, Hq, Hkv, D, P > 0 ? P : 1)) return PKV_ERR_INVALID_ARG;
+    if (P <= 0) return PKV_ERR_CUDA;
+    const cudaError_t err = (D == 64 ? launch_shared<64> : launch_shared<128>)(
+        px, pl, out, q, k_cache, v_cache, block_tables, seq_lens, workspace, P, dev_status, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}

@@ -51,7 +51,7 @@
 #include <cuda.h>
 #include <math.h>
 
-#include "attention_scores.cuh"
+#include "tensor_core.cuh"
 
 namespace pkv {
 
@@ -85,107 +85,6 @@ constexpr size_t kTcOperandBytes = kTcQT * static_cast<size_t>(kTcPBytes) + kTcS
 constexpr size_t kTcSmemBytes = 1024 + kTcOperandBytes + sizeof(TcSmem);
 static_assert(kTcSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
-// ------------------------------------------------------------------ tcgen05 helpers
-// Shared-memory matrix descriptor, 128-byte swizzle: start address, leading
-// byte offset (K-major: unused; MN-major: the stride between 64-element atoms
-// along M / N), stride byte offset (the stride between groups of 8 rows), the
-// descriptor version of this architecture.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-// Instruction descriptor of kind::f16: bf16 A and B, fp32 accumulator, M x N,
-// B K-major or MN-major (A always K-major here).
-__host__ __device__ constexpr uint32_t tc_idesc(int M, int N, bool b_mn_major) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
-           (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-// The same with A (M x 16 bf16, row m in TMEM lane m, two elements per column) in tensor memory.
-__device__ __forceinline__ void tc_mma_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-// Arrive on bar once every tcgen05 operation this thread issued so far is complete.
-__device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// 32 consecutive columns of this thread's TMEM lane (warp w reads lanes 32 (w % 4) ..).
-__device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tc_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-// Byte offset of (row, 16-byte chunk) in a tile of 128-byte rows with the
-// 128-byte swizzle (the chunk index XOR the row's low three bits).
-__device__ __forceinline__ uint32_t sw128(int row, int chunk) {
-    return static_cast<uint32_t>(row) * 128u + (static_cast<uint32_t>(chunk ^ (row & 7)) << 4);
-}
-// 4-D tiled copy (the K boxes); x, y, z, w are the box's start coordinates.
-__device__ __forceinline__ void tma_load_4d(void* smem_dst, const void* tmap, int x, int y, int z, int w,
-                                            uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(smem_u32(smem_dst)),
-        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-        : "memory");
-}
-// max(a, b, c) in one instruction
-__device__ __forceinline__ float tc_max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-// (x0, x1) = (a0 b + c, a1 b + c) and (s0, s1) += (a0, a1) as paired fp32 operations
-__device__ __forceinline__ void tc_fma2(float& x0, float& x1, float a0, float a1, float b, float c) {
-    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
-        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
-        : "=f"(x0), "=f"(x1)
-        : "f"(a0), "f"(a1), "f"(b), "f"(c));
-}
-__device__ __forceinline__ void tc_add2(float& s0, float& s1, float a0, float a1) {
-    asm("{\n\t.reg .b64 ra, rs;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rs, {%0, %1};\n\t"
-        "add.rn.f32x2 rs, rs, ra;\n\tmov.b64 {%0, %1}, rs;\n\t}"
-        : "+f"(s0), "+f"(s1)
-        : "f"(a0), "f"(a1));
-}
-__device__ __forceinline__ float tc_ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ int warp_sum_i(int x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -217,22 +116,7 @@ __device__ __forceinline__ int tc_tiles_longer(int n, int L, int TC, int v) {
 // head, times log2(e).
 __device__ __forceinline__ void score_tile(uint32_t (&sr)[2][32], int kbase, int pos, int first, int last, int pfx,
                                            float slope, const ScoreArgs& sc) {
-    if (sc.cap_log2 > 0.f) {
-#pragma unroll
-        for (int c = 0; c < kTcKeys; ++c)
-            sr[c >> 5][c & 31] = __float_as_uint(sc.cap_log2 * capped_tanh(__uint_as_float(sr[c >> 5][c & 31]) * sc.in));
-    } else {
-#pragma unroll
-        for (int c = 0; c < kTcKeys; ++c)
-            sr[c >> 5][c & 31] = __float_as_uint(__uint_as_float(sr[c >> 5][c & 31]) * sc.mul);
-    }
-    if (sc.slopes != nullptr) {
-        const float at = slope * static_cast<float>(kbase - pos);
-#pragma unroll
-        for (int c = 0; c < kTcKeys; ++c)
-            sr[c >> 5][c & 31] =
-                __float_as_uint(__uint_as_float(sr[c >> 5][c & 31]) + fmaf(slope, static_cast<float>(c), at));
-    }
+    tc_scores(sr, kbase - pos, slope, sc);
     // some key is hidden from some row of the query tile
     if (kbase + kTcKeys > pfx && (kbase + kTcKeys - 1 > first || (sc.window > 0 && kbase <= last - sc.window))) {
         const int lo = sc.window > 0 ? pos - sc.window + 1 - kbase : -kbase, hi = pos - kbase, near = pfx - kbase;
@@ -686,7 +570,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // [8-row group][half][8 rows][128 B]: for either half, successive 8-row groups
 // sit 2048 bytes apart, so a 64-key tile of four boxes is one K-major,
 // 128-byte-swizzled operand per half with a 2048-byte group stride.
-static bool encode_pool_k16(CUtensorMap* map, const void* pool, int NB, int Hkv, int BS) {
+bool encode_pool_k16(CUtensorMap* map, const void* pool, int NB, int Hkv, int BS) {
     typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);

@@ -1,0 +1,210 @@
+"""Decode attention over shared prefixes against float64 formulas, and in a step with the other calls."""
+import pytest
+import torch
+
+import paged_kv_decode_table_gb300 as pkv
+import scored_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from paged_kv_decode_table_gb300 import build
+    build.build()
+    pkv.load_library()
+
+
+def _cu(a):
+    return torch.tensor(a, dtype=torch.int32, device="cuda")
+
+
+def make(seed, groups, Hq, Hkv, D, BS, dtype, q_size=1.5, loose=()):
+    """groups: (shared tokens, lengths) of each; loose: lengths of sequences behind the last group."""
+    lens = [L for _, ls in groups for L in ls] + list(loose)
+    x = R.make(seed, lens, Hq, Hkv, D, BS, dtype, q_size=q_size)
+    start, at = [0], 0
+    for shared, ls in groups:
+        whole = shared // BS
+        for b in range(at + 1, at + len(ls)):
+            if ls[b - at] >= whole * BS:
+                x["block_tables"][b, :whole] = x["block_tables"][at, :whole]
+        at += len(ls)
+        start.append(at)
+    x["group_start"], x["shared_lens"] = _cu(start), _cu([s for s, _ in groups])
+    return x
+
+
+def call(x, **kw):
+    return pkv.paged_decode_attention_shared(x["q"], x["k_cache"], x["v_cache"], x["block_tables"], x["seq_lens"],
+                                             x["group_start"], x["shared_lens"], **kw)
+
+
+GROUPS = [
+    [(64, [64, 65, 100, 80])],
+    [(160, [170, 300, 160]), (0, [40]), (33, [50, 33, 900]), (48, [48])],
+    [(1000, [1000 + i for i in range(40)])],
+    [(2048, [2050, 2049]), (2048, [2048, 2100]), (16, [16, 17])],
+    [(0, [5, 0, 70])],
+    [(15, [15, 16])],
+]
+
+
+@pytest.mark.parametrize("groups", range(len(GROUPS)))
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,BS", [
+    (BF, 32, 8, 128, 16), (BF, 8, 2, 64, 16), (BF, 21, 3, 128, 32), (BF, 12, 12, 64, 48), (BF, 32, 2, 128, 64),
+    (BF, 40, 1, 64, 16), (BF, 1, 1, 128, 16), (BF, 120, 1, 128, 16), (BF, 200, 2, 64, 16)])
+def test_groups(dtype, Hq, Hkv, D, BS, groups):
+    x = make(groups, GROUPS[groups], Hq, Hkv, D, BS, dtype, loose=(20, 0))
+    st = pkv.new_status()
+    got = call(x, status=st)
+    ref, tol = R.reference(x)
+    assert pkv.check_status(st) == 0
+    R.check(got, ref, tol)
+
+
+@pytest.mark.parametrize("D,softcap,slopes", [(128, 9.0, False), (128, 0.0, True), (64, 20.0, True)])
+def test_scores(D, softcap, slopes):
+    x = make(3, [(700, [700 + 3 * i for i in range(20)]), (96, [100, 200])], 24, 4, D, 16, BF, q_size=4.0)
+    sl = R.slopes(24) if slopes else None
+    got = call(x, softcap=softcap, slopes=sl)
+    R.check(got, *R.reference(x, softcap=softcap, slopes=sl))
+
+
+def test_long_prefix_many_rows():
+    x = make(5, [(12000, [12000 + 7 * i for i in range(48)])], 32, 4, 128, 16, BF)
+    R.check(call(x), *R.reference(x))
+
+
+def test_many_groups():
+    x = make(6, [(48, [48 + i % 9, 60, 49 + i]) for i in range(90)], 8, 4, 128, 16, BF)
+    R.check(call(x), *R.reference(x))
+
+
+def test_no_groups():
+    x = make(7, [], 8, 2, 128, 16, BF, loose=(100, 3000, 1))
+    R.check(call(x), *R.reference(x))
+
+
+def test_bad_members_tables_and_groups():
+    groups = [(64, [64, 30, 100, 0]), (32, [60, 60])]
+    x = make(8, groups, 8, 2, 128, 16, BF)
+    ref, tol = R.reference(x)
+    st = pkv.new_status()
+    got = call(x, status=st)  # sequence 1 is shorter than its group's prefix; the empty one is no error
+    assert pkv.check_status(st) == 4
+    assert (got[1] == 0).all() and (got[3] == 0).all()
+    R.check(got, ref, tol, [0, 2, 3, 4, 5])
+    x["seq_lens"][1] = 0
+    for where, rows in (((0, 1), [3, 4, 5]), ((2, 5), [0, 3, 4, 5]), ((4, 0), [0, 2, 3])):
+        y = dict(x, block_tables=x["block_tables"].clone())
+        y["block_tables"][where] = 10 ** 6
+        st = pkv.new_status()
+        got = call(y, status=st)
+        assert pkv.check_status(st) == 4
+        bad = {(0, 1): [0, 2], (2, 5): [2], (4, 0): [4, 5]}[where]
+        assert (got[bad] == 0).all()
+        R.check(got, ref, tol, rows)
+    for start in ([0, 5, 4], [1, 4, 6], [0, 4, 7], [0, -1, 6]):
+        st = pkv.new_status()
+        got = call(dict(x, group_start=_cu(start)), status=st)
+        assert pkv.check_status(st) == 4, start
+        assert (got == 0).all(), start
+    for shared in ([-16, 32], [64, 10 ** 6]):
+        st = pkv.new_status()
+        got = call(dict(x, shared_lens=_cu(shared)), status=st)
+        assert pkv.check_status(st) == 4
+        good, bad = ([4, 5], [0, 2]) if shared[0] < 0 else ([0, 2], [4, 5])
+        assert (got[bad] == 0).all()
+        R.check(got, ref, tol, good)
+
+
+def test_streams_and_graphs():
+    xs = [make(30 + i, [(1600, [1600 + 50 * j for j in range(9)]), (320, [400, 500 + i])], 32, 8, 128, 16, BF)
+          for i in range(2)]
+    want = [call(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s, x in zip(streams, xs):
+            with torch.cuda.stream(s):
+                got.append(call(x))
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert torch.equal(o, want[i % 2])
+    graphs, outs = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(call(x))
+        graphs.append(g)
+    for x in xs:
+        x["q"].copy_(-x["q"])
+    want = [call(x) for x in xs]
+    for x, w in zip(xs, want):
+        R.check(w, *R.reference(x))
+    for g in (graphs[0], graphs[1], graphs[0], graphs[0]):
+        g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+def test_prompt_forks_and_decodes():
+    """A prompt prefilled in two chunks with changed scores, forked, and decoded step by step behind its shared blocks."""
+    Hq, Hkv, D, BS, cap = 16, 4, 128, 16, 12.0
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").to(BF)
+    pool = pkv.BlockPool(64, BS, 16)
+    k, v = (torch.full((64, Hkv, BS, D), float("nan"), dtype=BF, device="cuda") for _ in range(2))
+    pool.add(0, 150)
+    keys, values = rand(150, Hkv, D), rand(150, Hkv, D)
+    for lo, hi in ((0, 100), (100, 150)):
+        bt, _ = pool.tables([0])
+        bt, sl, qs = bt.cuda(), _cu([hi]), _cu([0, hi - lo])
+        pkv.kv_append_chunk(keys[lo:hi].contiguous(), values[lo:hi].contiguous(), k, v, bt, sl, qs)
+        x = dict(q=rand(hi - lo, Hq, D), k_cache=k, v_cache=v, block_tables=bt, seq_lens=sl, q_start=qs, lens=[hi],
+                 start=[0, hi - lo], BS=BS)
+        got = pkv.paged_prefill_attention_scored(x["q"], k, v, bt, sl, qs, softcap=cap, window=60)
+        R.check(got, *R.reference(x, softcap=cap, window=60))
+    for child in (1, 2):
+        pool.fork(0, child)
+    seqs = [0, 1, 2]
+    for step in range(12):
+        pairs = [p for p in (pool.append(s) for s in seqs) if p]
+        if pairs:
+            pkv.copy_blocks(k, v, _cu([a for a, _ in pairs]), _cu([b for _, b in pairs]))
+        bt, sl = pool.tables(seqs)
+        start, shared = pool.shared_groups(seqs)
+        assert start.tolist() == [0, 3] and shared.tolist() == [144]
+        bt, sl = bt.cuda(), sl.cuda()
+        pkv.kv_append(rand(3, Hkv, D), rand(3, Hkv, D), k, v, bt, sl)
+        x = dict(q=rand(3, Hq, D), k_cache=k, v_cache=v, block_tables=bt, seq_lens=sl, lens=sl.tolist(),
+                 start=[0, 1, 2, 3], BS=BS)
+        got = pkv.paged_decode_attention_shared(x["q"], k, v, bt, sl, start.cuda(), shared.cuda(), softcap=cap)
+        R.check(got, *R.reference(x, softcap=cap))
+        got = pkv.paged_decode_attention_scored(x["q"], k, v, bt, sl, softcap=cap, window=60)
+        R.check(got, *R.reference(x, softcap=cap, window=60))
+
+
+def test_refusals():
+    x = make(1, [(32, [40, 50])], 8, 2, 128, 16, BF)
+    for kw, err in ((dict(group_start=_cu([0])), ValueError), (dict(shared_lens=_cu([[32]])), ValueError),
+                    (dict(group_start=torch.tensor([0, 2], device="cuda")), TypeError),
+                    (dict(group_start=None), TypeError), (dict(shared_lens=None), TypeError),
+                    # more groups than sequences
+                    (dict(group_start=_cu([0, 1, 2, 2]), shared_lens=_cu([0, 0, 0])), pkv.PkvError)):
+        with pytest.raises(err):
+            call(dict(x, **kw))
+    with pytest.raises(pkv.PkvError):
+        call(x, softcap=-2.0)
+    for y in (make(1, [(32, [40, 50])], 8, 2, 80, 16, BF), make(1, [(32, [40, 50])], 8, 2, 128, 16, F32)):
+        with pytest.raises(pkv.PkvError):
+            call(y)
+    with pytest.raises(pkv.PkvError):
+        call(x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
