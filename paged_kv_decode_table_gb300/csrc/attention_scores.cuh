@@ -57,20 +57,23 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
-// cap log2(e) tanh(x), x = scale t / cap.  Up to |x| = 1/4 the Taylor polynomial x (1 - x^2/3 + 2x^4/15 - 17x^6/315
-// + 62x^8/2835): what it leaves out is below 2^-26.7 of x, so a small score keeps its relative accuracy whatever the
-// cap is.  Beyond, 1 - 2 / (e^(2x) + 1), whose error is about 2^-23 of the cap; e^(2x) = infinity gives 1.
-constexpr float kTanhSmall = 0.25f;
-__device__ __forceinline__ float tanh_small(float x) {
-    const float y = x * x;
-    float p = fmaf(y, 62.f / 2835.f, -17.f / 315.f);
-    p = fmaf(p, y, 2.f / 15.f);
-    p = fmaf(p, y, -1.f / 3.f);
-    return fmaf(x * y, p, x);
+// tanh(x), x = scale t / cap.  For |x| <= 1, x times a polynomial in x^2: the minimax one of five for the relative
+// error, 2^-20.7 of tanh(x) (found by linear programming on a grid), so that a small score keeps its relative accuracy
+// whatever the cap is.  Beyond, 1 - 2 / (e^(2x) + 1), off by about 2^-23; e^(2x) = infinity gives 1.  The kernels vote:
+// the polynomial (eight operations on the FMA pipe) where all scores of a warp's tile are within the cap, else the
+// second form (two on the slower special-function pipe) for all of them.
+constexpr float kTanh0 = 0.99999941f, kTanh1 = -0.33329042f, kTanh2 = 0.13281434f, kTanh3 = -0.05160567f,
+                kTanh4 = 0.01674311f, kTanh5 = -0.00306706f;
+__device__ __forceinline__ float tanh_within(float x) {
+    const float w = x * x;
+    float p = fmaf(kTanh5, w, kTanh4);
+    p = fmaf(p, w, kTanh3);
+    p = fmaf(p, w, kTanh2);
+    p = fmaf(p, w, kTanh1);
+    return x * fmaf(p, w, kTanh0);
 }
-__device__ __forceinline__ float tanh_large(float x) {
+__device__ __forceinline__ float tanh_beyond(float x) {
     return fmaf(-2.f, rcp_approx(ex2_approx(x * (2.f * kLog2e)) + 1.f), 1.f);
 }
-__device__ __forceinline__ float capped_tanh(float x) { return fabsf(x) <= kTanhSmall ? tanh_small(x) : tanh_large(x); }
 
 }  // namespace pkv

@@ -450,18 +450,18 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         z[n][e] = (s[n][0][e] + s[n][1][e]) * pl.sc.in;
-                        large = large || !(fabsf(z[n][e]) <= kTanhSmall);
+                        large = large || fabsf(z[n][e]) > 1.f;
                     }
                 if (__any_sync(0xffffffffu, large)) {
 #pragma unroll
                     for (int n = 0; n < kN; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[k][n][e] = pl.sc.cap_log2 * capped_tanh(z[n][e]);
+                        for (int e = 0; e < 4; ++e) x[k][n][e] = pl.sc.cap_log2 * tanh_beyond(z[n][e]);
                 } else {
 #pragma unroll
                     for (int n = 0; n < kN; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[k][n][e] = pl.sc.cap_log2 * tanh_small(z[n][e]);
+                        for (int e = 0; e < 4; ++e) x[k][n][e] = pl.sc.cap_log2 * tanh_within(z[n][e]);
                 }
             } else {
 #pragma unroll

@@ -13,6 +13,9 @@
 // prefix_tc_kernel: a persistent kernel, one CTA per SM.  Work = (group, KV head, tile of up to 256 rows) x key tiles of
 // 64; all of it in one order, cut into one range of key tiles per CTA, so that a few rows over a long prefix and many
 // groups over short ones fill the device alike.  What a range covers of one (group, head, row tile) is a piece.
+//  * Where all members fit into 128 rows, both query tiles hold them and take every other key tile, each with results
+//    of its own: two chains of products and softmax stay in flight (16 groups of 16 rows over 1024-4096 keys took 51 us
+//    with one).
 //  * Operands as in prefill_tc.cu: Q (bf16) in tensor memory, K and V by TMA in boxes of 16 keys through a ring,
 //    S = Q K^T (M 128, N 64, K = D) and O += P V (M 128, N = D, K 64) by one issuing thread each, P through a
 //    128-byte-swizzled shared tile, S and O in tensor memory (256 columns per query tile of 128 rows).
@@ -52,7 +55,7 @@ constexpr int kPxMarks = 16;   // pieces of which a bad block is remembered; mor
 constexpr int kPxPBytes = kPxRows * kPxKeys * 2;
 // warps 0-7: softmax (warp w: query tile w / 4); 8, 11, 12: producers; 9: S MMAs (and the TMEM allocation); 10: PV MMAs
 constexpr int kPxWarpProd = 8, kPxWarpS = 9, kPxWarpPV = 10;
-constexpr int kPxThreads = 13 * 32;
+constexpr int kPxThreads = 16 * 32;  // (13-15 have registers to pass on)
 constexpr int kPxTmemCols = 512;  // query tile t: Q at 256 t, S at 256 t + 64, O at 256 t + 128
 constexpr int kPxMinTiles = 2;    // key tiles of a range at least
 
@@ -84,10 +87,10 @@ struct PxHead {
 struct PxSpace {
     PxHead* head;
     int2* plan;   // of every group: (first key tile in the order, key tiles of a row tile)
-    float2* ml;   // (max, sum): 2 slots per CTA of 256 rows, then a place per row of out
+    float2* ml;   // (max, sum): 2 slots per CTA of 256 rows, then two places per row of out
     float* o;
-    int rows;     // of a slot
 };
+constexpr int kPxSlot = kPxTiles * kPxRows;  // rows of a slot
 
 struct PxPlan {
     int B, Hq, Hkv, G, BS, NB, max_blocks;
@@ -128,16 +131,17 @@ struct PxWalk {
         h = work / rt;
         tile = work - h * rt;
     }
-    // Query tiles of the piece that hold members.
-    __device__ __forceinline__ int tiles(const PxPlan& pl) const { return n - tile * pl.TC > pl.TQ ? 2 : 1; }
+    // All rows fit into one query tile: both hold them, tile t takes key tiles k0 + t, k0 + t + 2, ..
+    __device__ __forceinline__ bool dual(const PxPlan& pl) const { return n - tile * pl.TC <= pl.TQ; }
 };
 
-template <int kD, bool kScored>
+template <int kD, bool kCap, bool kSlope>
 __global__ void __launch_bounds__(kPxThreads, 1)
     prefix_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ PxPlan pl, const __nv_bfloat16* q, const int32_t* block_tables,
                      const int32_t* seq_lens, const PxSpace ws, int32_t* status) {
     using C = Px<kD>;
+    constexpr bool kScored = kCap || kSlope;
     constexpr int kStages = C::kStages;
     extern __shared__ uint8_t px_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(px_raw) + 1023) & ~uintptr_t(1023));
@@ -239,7 +243,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     const int g0 = sm->g0, base0 = sm->base0;
 
     bool fail = false;
-    if (warp == kPxWarpProd || warp > kPxWarpPV) {
+    if (warp == kPxWarpProd || warp == kPxWarpPV + 1 || warp == kPxWarpPV + 2) {
+        tc_fewer_registers();
         // ------------------------------------------------ producer warps 8, 11, 12
         // Warp pw issues boxes i = pw, pw + 3, pw + 6 of every tile (box i: K of 16-key group i for i < 4, V of group
         // i - 4 otherwise), with block ids from its own window of the block table, and arms the stage's transaction
@@ -306,6 +311,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         if (lane == 0)
             for (int i = max(0, j - kStages); i < j; ++i) mbar_wait(&sm->kv_full[i % kStages], (i / kStages) & 1);
     } else if (warp == kPxWarpS) {
+        tc_fewer_registers();
         // ------------------------------------------------ S = Q K^T (lane 0 issues)
         if (lane == 0) {
             constexpr uint32_t idS = tc_idesc(kPxRows, kPxKeys, false);
@@ -314,7 +320,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             int j = 0, done[kPxTiles] = {0, 0}, pieces[kPxTiles] = {0, 0};
             for (int at = start; at < end && !fail; at += w.k1 - w.k0) {
                 w.to(pl, at, end);
-                const int nq = w.tiles(pl);
+                const bool dual = w.dual(pl);
                 for (int kt = w.k0; kt < w.k1 && !fail; ++kt, ++j) {
                     const int s = j % kStages;
                     if (!mbar_wait(&sm->kv_full[s], (j / kStages) & 1)) {
@@ -322,8 +328,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                         break;
                     }
                     const uint32_t kb = kva + s * C::kStageBytes;
-                    for (int t = 0; t < nq; ++t) {
-                        if ((kt == w.k0 && !mbar_wait(&sm->q_full[t], pieces[t] & 1)) ||
+                    const int ta = dual ? (kt - w.k0) & 1 : 0, tb = dual ? ta : 1;
+                    for (int t = ta; t <= tb; ++t) {
+                        if ((kt - w.k0 < (dual ? 2 : 1) && !mbar_wait(&sm->q_full[t], pieces[t] & 1)) ||
                             (done[t] >= 1 && !mbar_wait(&sm->s_free[t], (done[t] - 1) & 1))) {
                             fail = true;
                             break;
@@ -339,12 +346,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                         ++done[t];
                     }
                 }
-                for (int t = 0; t < nq; ++t) ++pieces[t];
+                ++pieces[0];
+                if (!dual || w.k1 - w.k0 > 1) ++pieces[1];
             }
             if (fail) report(status, PKV_ERR_TIMEOUT);
         }
         __syncwarp();
     } else if (warp == kPxWarpPV) {
+        tc_fewer_registers();
         // ------------------------------------------------ O += P V (lane 0 issues)
         if (lane == 0) {
             constexpr uint32_t idO = tc_idesc(kPxRows, kD, true);
@@ -353,11 +362,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             int j = 0, done[kPxTiles] = {0, 0};
             for (int at = start; at < end && !fail; at += w.k1 - w.k0) {
                 w.to(pl, at, end);
-                const int nq = w.tiles(pl);
+                const bool dual = w.dual(pl);
                 for (int kt = w.k0; kt < w.k1 && !fail; ++kt, ++j) {
                     const int s = j % kStages;
                     const uint32_t vb = kva + s * C::kStageBytes + C::kKBytes;
-                    for (int t = 0; t < nq; ++t) {  // query tile 0 first: its softmax warps clear V rows
+                    const int ta = dual ? (kt - w.k0) & 1 : 0, tb = dual ? ta : 1;
+                    for (int t = ta; t <= tb; ++t) {  // query tile 0 first: its softmax warps clear V rows
                         if (!mbar_wait(&sm->p_full[t], done[t] & 1)) {
                             fail = true;
                             break;
@@ -367,7 +377,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < kPxKeys / 16; ++kk)
                             tc_mma(tmem + 256 * t + 128, tc_desc(pb + 32 * kk, 16, 1024),
-                                   tc_desc(vb + C::kGroup * kk, C::kGroup / 2, 1024), idO, (kt > w.k0 || kk > 0) ? 1u : 0u);
+                                   tc_desc(vb + C::kGroup * kk, C::kGroup / 2, 1024), idO,
+                                   (kt - w.k0 >= (dual ? 2 : 1) || kk > 0) ? 1u : 0u);
                         tc_commit(&sm->o_done[t]);
                         ++done[t];
                     }
@@ -377,24 +388,23 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             if (fail) report(status, PKV_ERR_TIMEOUT);
         }
         __syncwarp();
-    } else {
+    } else if (warp < 8) {
+        tc_more_registers();
         // ------------------------------------------------ softmax warps: thread r of query tile qt owns row r
         const int qt = warp >> 2, r = tid & (kPxRows - 1);
         const uint32_t lrow = static_cast<uint32_t>((warp & 3) * 32) << 16;  // this warp's TMEM lanes
         const uint32_t tq = tmem + 256 * qt + lrow;
         uint8_t* pbuf = sP + qt * kPxPBytes;
         PxWalk w(pl, g0, base0);
-        int j = 0, done = 0;  // key tiles of the CTA, and of this query tile
+        int done = 0;  // key tiles of this query tile
         for (int at = start, piece = 0; at < end && !fail; at += w.k1 - w.k0, ++piece) {
             w.to(pl, at, end);
-            if (qt >= w.tiles(pl)) {
-                j += w.k1 - w.k0;
-                continue;
-            }
-            const int member = w.tile * pl.TC + qt * pl.TQ + r / G, qh = w.h * G + r % G;
+            const bool dual = w.dual(pl);
+            const int step = dual ? 2 : 1, k0 = w.k0 + (dual ? qt : 0);  // this query tile's first key tile
+            const int member = w.tile * pl.TC + (dual ? 0 : qt * pl.TQ) + r / G, qh = w.h * G + r % G;
             const bool valid = r < pl.TQ * G && member < w.n;  // the other rows are zero queries
             const int b = w.first + (valid ? member : 0);
-            {
+            if (k0 < w.k1) {
                 const uint4* src = reinterpret_cast<const uint4*>(q + (static_cast<size_t>(b) * pl.Hq + qh) * kD);
 #pragma unroll
                 for (int hv = 0; hv < kD / 64; ++hv) {
@@ -413,10 +423,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 mbar_arrive(&sm->q_full[qt]);
             }
             const int prefix = group_prefix(pl.groups, pl.max_blocks, BS, w.g);
-            [[maybe_unused]] const int pos = kScored && valid ? seq_lens[b] - 1 : 0;
-            [[maybe_unused]] const float slope = kScored && pl.sc.slopes != nullptr ? pl.sc.slopes[qh] * kLog2e : 0.f;
+            [[maybe_unused]] const int pos = kSlope && valid ? seq_lens[b] - 1 : 0;
+            [[maybe_unused]] const float slope = kSlope ? pl.sc.slopes[qh] * kLog2e : 0.f;
             float m_ref = -INFINITY, lsum = 0.f;
-            for (int kt = w.k0; kt < w.k1; ++kt, ++j, ++done) {
+            for (int kt = k0; kt < w.k1; kt += step, ++done) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&sm->s_full[qt], done & 1))) {  // tcgen05.ld needs the whole warp
                     fail = true;
                     break;
@@ -428,7 +438,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 tc_fence_before();
                 mbar_arrive(&sm->s_free[qt]);  // S may take the next tile
                 const int kbase = kt * kPxKeys;
-                if constexpr (kScored) tc_scores(sr, kbase - pos, slope, pl.sc);
+                if constexpr (kScored) tc_scores<kCap, kSlope>(sr, kbase - pos, slope, pl.sc);
                 const bool tail = kbase + kPxKeys > prefix;
                 if (tail) {
 #pragma unroll
@@ -465,7 +475,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 lsum = lsum * a + (((ls[0][0] + ls[0][1]) + (ls[1][0] + ls[1][1])) +
                                    ((ls[2][0] + ls[2][1]) + (ls[3][0] + ls[3][1])));
                 // the PV of the tile before is complete: O may be rescaled and the P tile rewritten
-                if (kt > w.k0) {
+                if (kt > k0) {
                     if (!__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (done - 1) & 1))) {
                         fail = true;
                         break;
@@ -482,9 +492,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                         }
                     }
                 }
-                if (tail && qt == 0) {  // the V rows of keys behind the prefix may hold anything: clear them
+                if (tail && (dual || qt == 0)) {  // the V rows of keys behind the prefix may hold anything: clear them
                     const int rlo = prefix - kbase;
-                    uint8_t* vb = sKV + static_cast<size_t>(j % kStages) * C::kStageBytes + C::kKBytes;
+                    uint8_t* vb = sKV + static_cast<size_t>((at - start + kt - w.k0) % kStages) * C::kStageBytes + C::kKBytes;
                     constexpr int kRowChunks = kD / 8;
                     for (int idx = r; idx < (kPxKeys - rlo) * kRowChunks; idx += kPxRows) {
                         const int rr = rlo + idx / kRowChunks, half = (idx / 8) % (kRowChunks / 8), ch = idx & 7;
@@ -500,7 +510,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 tc_fence_before();
                 mbar_arrive(&sm->p_full[qt]);
             }
-            if (!fail && !__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (done - 1) & 1))) fail = true;
+            if (!fail && k0 < w.k1 && !__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (done - 1) & 1))) fail = true;
             if (fail) {
                 if (lane == 0) report(status, PKV_ERR_TIMEOUT);
                 break;
@@ -509,8 +519,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             tc_fence_after();
             const bool whole = w.k0 == 0 && w.k1 == w.nt;
             const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (w.k0 > 0 ? 0 : 1);
-            const size_t own = whole ? 2 * static_cast<size_t>(gridDim.x) * ws.rows + static_cast<size_t>(b) * pl.Hq + qh
-                                     : slot * ws.rows + qt * kPxRows + r;
+            const size_t own = whole ? 2 * static_cast<size_t>(gridDim.x) * kPxSlot +
+                                           (static_cast<size_t>(dual ? qt : 0) * pl.B + b) * pl.Hq + qh
+                                     : slot * kPxSlot + qt * kPxRows + r;
             const bool broken = *const_cast<volatile int*>(&sm->bad[piece % kPxMarks]) == piece + 1;
             if (valid) ws.ml[own] = make_float2(m_ref, broken ? -1.f : lsum);
             // the P tile is free: 32 columns of the warp's 32 rows go through its quarter of it
@@ -519,7 +530,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll 1
             for (int cc = 0; cc < kD / 32; ++cc) {
                 uint32_t o[32];
-                tc_ld32(tq + 128 + 32 * cc, o);
+                if (k0 < w.k1) {
+                    tc_ld32(tq + 128 + 32 * cc, o);
+                } else {  // no key tile: nothing was summed
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) o[c] = 0u;
+                }
 #pragma unroll
                 for (int c = 0; c < 8; ++c)
                     stage[lane * 8 + (c ^ (lane & 7))] =
@@ -540,6 +556,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             }
             tc_fence_before();
         }
+    } else {
+        tc_fewer_registers();
     }
     // ---- every role is done with TMEM
     tc_fence_before();
@@ -559,20 +577,26 @@ template <int kD>
 __global__ void __launch_bounds__(kSjWarps * 32)
     shared_join_kernel(const __grid_constant__ PxPlan pl, const PxSpace px, const SplitSpace ws, const int R,
                        const int32_t* seq_lens, __nv_bfloat16* out, const int P, int32_t* status) {
-    const long long row = static_cast<long long>(blockIdx.x) * kSjWarps + (threadIdx.x >> 5);
+    const long long rows = static_cast<long long>(pl.B) * pl.Hq;
+    const long long row = min(static_cast<long long>(blockIdx.x) * kSjWarps + (threadIdx.x >> 5), rows - 1);
     const int lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (row >= static_cast<long long>(pl.B) * pl.Hq) return;
     const int b = static_cast<int>(row / pl.Hq), qh = static_cast<int>(row - static_cast<long long>(b) * pl.Hq);
     constexpr int kCols = kD / 32;  // of a lane
     float acc[kCols] = {};
     float M = -INFINITY, l = 0.f;
+    // What only the inputs say comes before the wait: they are older than the prefix kernel, which started this
+    // chain after its own wait.
     const int L = seq_lens[b];
-    bool bad = px.head->valid == 0 || L < 0 || static_cast<long long>(L) > static_cast<long long>(pl.max_blocks) * pl.BS;
-    const int g = bad ? -1 : group_of(pl.groups, b);
+    bool bad = L < 0 || static_cast<long long>(L) > static_cast<long long>(pl.max_blocks) * pl.BS;
+    const int g = group_of(pl.groups, b);
     const int prefix = g < 0 ? 0 : group_prefix(pl.groups, pl.max_blocks, pl.BS, g);
     bad = bad || (L > 0 && (prefix < 0 || L < prefix));
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const PxHead head = *px.head;
+    const int2 plan = prefix > 0 ? px.plan[g] : make_int2(0, 0), info = ws.info[b];
+    const int Wo = ws.head->W;
+    bad = bad || head.valid == 0;
     if (bad && lane == 0 && qh == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
     if (!bad && L > 0) {
         auto take = [&](const float2* mls, const float* os, int pieces, auto place) {
@@ -619,20 +643,21 @@ __global__ void __launch_bounds__(kSjWarps * 32)
             }
         };
         if (prefix > 0) {
-            const int2 plan = px.plan[g];
             const int member = b - pl.groups.start[g], rt = (pl.groups.start[g + 1] - pl.groups.start[g] + pl.TC - 1) / pl.TC;
-            const int tile = member / pl.TC, in = member - tile * pl.TC, qt = in / pl.TQ, W = px.head->W;
+            const int tile = member / pl.TC, in = member - tile * pl.TC, qt = in / pl.TQ, W = head.W;
             const int h = qh / pl.G, r = (in - qt * pl.TQ) * pl.G + qh - h * pl.G;
+            const bool dual = pl.groups.start[g + 1] - pl.groups.start[g] - tile * pl.TC <= pl.TQ;
             const int first = plan.x + (h * rt + tile) * plan.y, f = first / W, pieces = (first + plan.y - 1) / W - f + 1;
-            take(px.ml, px.o, pieces, [&](int p) {
-                return pieces == 1 ? 2 * static_cast<size_t>(P) * px.rows + row
-                                   : (2 * static_cast<size_t>(f + p) + (p == 0 ? 1 : 0)) * px.rows + qt * kPxRows + r;
+            take(px.ml, px.o, dual ? 2 * pieces : pieces, [&](int x) {
+                const int p = dual ? x >> 1 : x, t = dual ? x & 1 : qt;
+                return pieces == 1 ? 2 * static_cast<size_t>(P) * kPxSlot +
+                                         (static_cast<size_t>(dual ? t : 0) * pl.B + b) * pl.Hq + qh
+                                   : (2 * static_cast<size_t>(f + p) + (p == 0 ? 1 : 0)) * kPxSlot + t * kPxRows + r;
             });
         }
-        const int2 info = ws.info[b];
         if (info.y > 0) {
-            const int grp = qh / R, W = ws.head->W;
-            const int first = info.x + grp * info.y, f = first / W, pieces = (first + info.y - 1) / W - f + 1;
+            const int grp = qh / R;
+            const int first = info.x + grp * info.y, f = first / Wo, pieces = (first + info.y - 1) / Wo - f + 1;
             take(ws.ml, ws.o, pieces, [&](int p) {
                 return pieces == 1 ? 2 * static_cast<size_t>(P) * R + row
                                    : (2 * static_cast<size_t>(f + p) + (p == 0 ? 1 : 0)) * R + (qh - grp * R);
@@ -666,10 +691,9 @@ static bool encode_pool_rows64(CUtensorMap* map, const void* pool, long long row
 }
 
 // [head][plan of up to B groups][(max, sum)][O]
-static size_t px_space(int B, int Hq, int Hkv, int D, int P, void* base, PxSpace* ws) {
+static size_t px_space(int B, int Hq, int D, int P, void* base, PxSpace* ws) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    const int G = Hq / Hkv, rows = B > kPxRows / G ? kPxTiles * kPxRows : kPxRows;
-    const size_t places = 2 * static_cast<size_t>(P) * rows + static_cast<size_t>(B) * Hq;
+    const size_t places = 2 * static_cast<size_t>(P) * kPxSlot + 2 * static_cast<size_t>(B) * Hq;
     const size_t ml = up(256 + sizeof(int2) * static_cast<size_t>(B)), o = up(ml + places * sizeof(float2));
     if (ws != nullptr) {
         uint8_t* p = static_cast<uint8_t*>(base);
@@ -677,7 +701,6 @@ static size_t px_space(int B, int Hq, int Hkv, int D, int P, void* base, PxSpace
         ws->plan = reinterpret_cast<int2*>(p + 256);
         ws->ml = reinterpret_cast<float2*>(p + ml);
         ws->o = reinterpret_cast<float*>(p + o);
-        ws->rows = rows;
     }
     return up(o + places * D * sizeof(float));
 }
@@ -693,10 +716,11 @@ static cudaError_t launch_shared(const PxPlan& px, SplitPlan pl, void* out, cons
         return cudaErrorInvalidValue;
     PxSpace pws = {};
     SplitSpace ws = {};
-    const size_t used = px_space(pl.B, pl.Hq, pl.Hkv, pl.D, P, workspace, &pws);
+    const size_t used = px_space(pl.B, pl.Hq, pl.D, P, workspace, &pws);
     split_space(pl, P, pl.B, true, static_cast<uint8_t*>(workspace) + used, &ws);
-    const bool scored = pl.sc.cap_log2 > 0.f || pl.sc.slopes != nullptr;
-    auto kern = scored ? prefix_tc_kernel<kD, true> : prefix_tc_kernel<kD, false>;
+    const bool sloped = pl.sc.slopes != nullptr;
+    auto kern = pl.sc.cap_log2 > 0.f ? (sloped ? prefix_tc_kernel<kD, true, true> : prefix_tc_kernel<kD, true, false>)
+                                     : (sloped ? prefix_tc_kernel<kD, false, true> : prefix_tc_kernel<kD, false, false>);
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kPxSmem<kD>));
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -733,7 +757,7 @@ extern "C" size_t pkv_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int 
     pl.Hq = Hq;
     pl.D = D;
     if ((D != 64 && D != 128) || Hq / Hkv > kPxRows || !split_shape(Hq, Hkv, D, 16, 1, pl)) return plain;
-    return std::max(plain, px_space(B, Hq, Hkv, D, P, nullptr, nullptr) + split_space(pl, P, B, true, nullptr, nullptr));
+    return std::max(plain, px_space(B, Hq, D, P, nullptr, nullptr) + split_space(pl, P, B, true, nullptr, nullptr));
 }
 
 extern "C" pkv_status pkv_paged_decode_attention_shared(

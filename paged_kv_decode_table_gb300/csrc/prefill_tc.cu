@@ -72,6 +72,10 @@ constexpr int kTcWin = 640;                  // block-table entries kept in shar
 // 11 and 12: producers; warp 9: S MMAs (and the TMEM allocation); warp 10: PV MMAs
 constexpr int kTcWarpProd = 8, kTcWarpS = 9, kTcWarpPV = 10;
 constexpr int kTcThreads = 13 * 32;
+// With changed scores a softmax thread needs more than the 128 registers that 13 warps leave it: 16 warps (13-15 idle),
+// which can pass theirs on by warpgroup.
+constexpr int kTcScoredThreads = 16 * 32;
+enum : int { kPlain = 0, kMasked = 1, kCapped = 2, kSloped = 4 };
 constexpr int kTcTmemCols = 512;             // query tile t: Q at 256 t, S at 256 t + 64, O at 256 t + 128
 
 struct TcSmem {  // follows the 1024-aligned operand area
@@ -114,9 +118,10 @@ __device__ __forceinline__ int tc_tiles_longer(int n, int L, int TC, int v) {
 // The 64 products of a row with the keys from kbase on become scores in the log2 domain, -infinity where the row at
 // position `pos` does not see the key.  first, last: the positions of the query tile's rows; slope: of the row's
 // head, times log2(e).
+template <int kKind>
 __device__ __forceinline__ void score_tile(uint32_t (&sr)[2][32], int kbase, int pos, int first, int last, int pfx,
                                            float slope, const ScoreArgs& sc) {
-    tc_scores(sr, kbase - pos, slope, sc);
+    tc_scores<(kKind & kCapped) != 0, (kKind & kSloped) != 0>(sr, kbase - pos, slope, sc);
     // some key is hidden from some row of the query tile
     if (kbase + kTcKeys > pfx && (kbase + kTcKeys - 1 > first || (sc.window > 0 && kbase <= last - sc.window))) {
         const int lo = sc.window > 0 ? pos - sc.window + 1 - kbase : -kbase, hi = pos - kbase, near = pfx - kbase;
@@ -126,14 +131,15 @@ __device__ __forceinline__ void score_tile(uint32_t (&sr)[2][32], int kbase, int
     }
 }
 
-// kScored: the scores of attention_scores.cuh (sc), else plain ones (sc unused).
-template <bool kScored>
-__global__ void __launch_bounds__(kTcThreads, 1)
+// kKind: kPlain, or kMasked (the masks of attention_scores.cuh) with kCapped and kSloped where its scores are.
+template <int kKind>
+__global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ out,
                       const int32_t* __restrict__ block_tables, int max_blocks, const int32_t* __restrict__ seq_lens,
                       const int32_t* __restrict__ q_start, int B, int Hq, int Hkv, int BS, int NB, float scale_log2,
                       const __grid_constant__ ScoreArgs sc, int32_t* status) {
+    constexpr bool kScored = kKind != kPlain;
     extern __shared__ uint8_t tc_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tc_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sP = base;                          // P of query tile t at t kTcPBytes
@@ -300,7 +306,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
 
     bool fail = false;
-    if ((warp == kTcWarpProd || warp > kTcWarpPV) && active) {
+    if ((warp == kTcWarpProd || (warp > kTcWarpPV && warp < kTcThreads / 32)) && active) {
+        if constexpr (kScored) tc_fewer_registers();
         // ------------------------------------------------ producer warps 8, 11, 12
         // The three warps work independently: warp pw issues boxes i = pw, pw + 3,
         // pw + 6 of every tile (box i: K of 16-key group i for i < 4, V of group
@@ -363,6 +370,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int j = max(0, ntiles - kTcStages); j < ntiles; ++j)
                 mbar_wait(&sm->kv_full[j % kTcStages], (j / kTcStages) & 1);
     } else if (warp == kTcWarpS && active) {
+        if constexpr (kScored) tc_fewer_registers();
         // ------------------------------------------------ S = Q K^T for both query tiles (lane 0 issues)
         // Q (A) from tensor memory, K (B) from the stage.  S_j of query tile t
         // overwrites S_{j-1} once the softmax has read it, so it runs while the
@@ -394,6 +402,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         __syncwarp();
     } else if (warp == kTcWarpPV && active) {
+        if constexpr (kScored) tc_fewer_registers();
         // ------------------------------------------------ O += P V for both query tiles (lane 0 issues)
         // P of query tile t (bf16, a K-major 128-byte-swizzled shared tile) is
         // the A operand.  Both P tiles of key tile j were written after the
@@ -425,13 +434,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         __syncwarp();
     } else if (softmax_warp && active) {
+        if constexpr (kScored) tc_more_registers();
         // ------------------------------------------------ softmax warps: thread r of query tile qt owns row r
         const uint32_t lrow = static_cast<uint32_t>((warp & 3) * 32) << 16;  // this warp's TMEM lanes
         const uint32_t tq = tmem + 256 * qt;
         const int p0t = p0 + qt * TQ;  // the query tile's first position
         float m_ref = -INFINITY, lsum = 0.f;
         [[maybe_unused]] float slope = 0.f;
-        if constexpr (kScored) slope = sc.slopes != nullptr ? sc.slopes[qh] * kLog2e : 0.f;
+        if constexpr (kScored) slope = kKind & kSloped ? sc.slopes[qh] * kLog2e : 0.f;
         for (int j = 0; j < ntiles; ++j) {
             if (!__all_sync(0xffffffffu, mbar_wait(&sm->s_full[qt], j & 1))) {  // tcgen05.ld needs the whole warp
                 fail = true;
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_arrive(&sm->s_free[qt]);  // S may take the next tile
             const int kt = key_tile(j + rot < ntiles ? j + rot : j + rot - ntiles);
             const int kbase = kt * kTcKeys;
-            if constexpr (kScored) score_tile(sr, kbase, pos, p0t, min(p0t + TQ, p0 + nt) - 1, pfx, slope, sc);
+            if constexpr (kScored) score_tile<kKind>(sr, kbase, pos, p0t, min(p0t + TQ, p0 + nt) - 1, pfx, slope, sc);
             // maximum of the raw scores (the scale is positive), eight chains;
             // the causal mask only on tiles that reach past the query tile's first position
             // (three-input maxima: two scores per instruction, four chains)
@@ -553,6 +563,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
         }
+    } else if (kScored && active) {
+        tc_fewer_registers();
     }
     // ---- every role is done with TMEM
     tc_fence_before();
@@ -614,13 +626,16 @@ cudaError_t launch_prefill_tc(void* out, const void* q, const void* k_cache, con
     CUtensorMap tmK, tmV;
     if (!encode_pool_k16(&tmK, k_cache, NB, Hkv, BS) || !encode_pool_box_halves(&tmV, v_cache, NB, Hkv, BS, 16))
         return cudaErrorInvalidValue;
-    auto kern = scored != nullptr ? prefill_tc_kernel<true> : prefill_tc_kernel<false>;
+    const bool cap = scored != nullptr && scored->cap_log2 > 0.f, sloped = scored != nullptr && scored->slopes != nullptr;
+    auto kern = scored == nullptr ? prefill_tc_kernel<kPlain>
+                : cap             ? (sloped ? prefill_tc_kernel<kMasked | kCapped | kSloped> : prefill_tc_kernel<kMasked | kCapped>)
+                                  : (sloped ? prefill_tc_kernel<kMasked | kSloped> : prefill_tc_kernel<kMasked>);
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(kTcSmemBytes));
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * Hkv), 1, 1);  // KV head innermost
-    cfg.blockDim = dim3(kTcThreads, 1, 1);
+    cfg.blockDim = dim3(scored != nullptr ? kTcScoredThreads : kTcThreads, 1, 1);
     cfg.dynamicSmemBytes = kTcSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

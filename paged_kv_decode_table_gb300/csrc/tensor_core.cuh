@@ -107,25 +107,82 @@ __device__ __forceinline__ float tc_ex2(float x) {
     return y;
 }
 
+// Pairs of floats in a 64-bit register.
+__device__ __forceinline__ uint64_t tc_pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t tc_pair(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void tc_unpair(uint32_t& a, uint32_t& b, uint64_t v) {
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t tc_mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t tc_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // The 64 products of a row with a tile's keys become scores in the log2 domain.  dist: the first key's position less
-// the row's; slope: of the row's head, times log2(e).
+// the row's; slope: of the row's head, times log2(e).  All lanes of the warp take part.
+template <bool kCap, bool kSlope>
 __device__ __forceinline__ void tc_scores(uint32_t (&sr)[2][32], int dist, float slope, const ScoreArgs& sc) {
-    if (sc.cap_log2 > 0.f) {
+    auto at = [&](int c) -> uint32_t& { return sr[c >> 5][c & 31]; };
+    [[maybe_unused]] const float bias = slope * static_cast<float>(dist);
+    // (the bias of keys c, c + 1) added to a * b
+    auto add = [&](uint64_t a, uint64_t b, int c) {
+        if constexpr (!kSlope) return tc_mul2(a, b);
+        const uint64_t s2 = tc_pair(slope, slope), b2 = tc_pair(bias, bias);
+        return tc_fma2(a, b, tc_fma2(s2, tc_pair(static_cast<float>(c), static_cast<float>(c + 1)), b2));
+    };
+    if constexpr (kCap) {
+        float big[2] = {0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-            sr[c >> 5][c & 31] = __float_as_uint(sc.cap_log2 * capped_tanh(__uint_as_float(sr[c >> 5][c & 31]) * sc.in));
+        for (int c = 0; c < 64; c += 2)
+            big[(c >> 1) & 1] = tc_max3(big[(c >> 1) & 1], fabsf(__uint_as_float(at(c))), fabsf(__uint_as_float(at(c + 1))));
+        const uint64_t in2 = tc_pair(sc.in, sc.in), cap2 = tc_pair(sc.cap_log2, sc.cap_log2);
+        if (__all_sync(0xffffffffu, !(fmaxf(big[0], big[1]) * sc.in > 1.f))) {
+            const uint64_t c0 = tc_pair(kTanh0 * sc.cap_log2, kTanh0 * sc.cap_log2),
+                           c1 = tc_pair(kTanh1 * sc.cap_log2, kTanh1 * sc.cap_log2),
+                           c2 = tc_pair(kTanh2 * sc.cap_log2, kTanh2 * sc.cap_log2),
+                           c3 = tc_pair(kTanh3 * sc.cap_log2, kTanh3 * sc.cap_log2),
+                           c4 = tc_pair(kTanh4 * sc.cap_log2, kTanh4 * sc.cap_log2),
+                           c5 = tc_pair(kTanh5 * sc.cap_log2, kTanh5 * sc.cap_log2);
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+                const uint64_t x = tc_mul2(tc_pair(at(c), at(c + 1)), in2), w = tc_mul2(x, x);
+                const uint64_t p = tc_fma2(tc_fma2(tc_fma2(tc_fma2(tc_fma2(c5, w, c4), w, c3), w, c2), w, c1), w, c0);
+                tc_unpair(at(c), at(c + 1), add(x, p, c));
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+                const uint64_t x = tc_mul2(tc_pair(at(c), at(c + 1)), in2);
+                uint32_t x0, x1;
+                tc_unpair(x0, x1, x);
+                const uint64_t t = tc_pair(tanh_beyond(__uint_as_float(x0)), tanh_beyond(__uint_as_float(x1)));
+                tc_unpair(at(c), at(c + 1), add(t, cap2, c));
+            }
+        }
     } else {
+        const uint64_t m2 = tc_pair(sc.mul, sc.mul);
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-            sr[c >> 5][c & 31] = __float_as_uint(__uint_as_float(sr[c >> 5][c & 31]) * sc.mul);
-    }
-    if (sc.slopes != nullptr) {
-        const float at = slope * static_cast<float>(dist);
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-            sr[c >> 5][c & 31] =
-                __float_as_uint(__uint_as_float(sr[c >> 5][c & 31]) + fmaf(slope, static_cast<float>(c), at));
+        for (int c = 0; c < 64; c += 2) tc_unpair(at(c), at(c + 1), add(tc_pair(at(c), at(c + 1)), m2, c));
     }
 }
+
+// Registers move from the warps that issue copies and MMAs to those of the softmax: 512 threads are launched with 128
+// each, two warpgroups of softmax take 176, the two others keep 80.
+__device__ __forceinline__ void tc_more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 176;"); }
+__device__ __forceinline__ void tc_fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;"); }
 
 }  // namespace pkv
