@@ -50,7 +50,6 @@ bool scored_shape_valid(int B, int Hq, int Hkv, int D, int BS, int NB, int max_b
 
 constexpr int kPxRows = 128, kPxTiles = 2, kPxKeys = 64;
 constexpr int kPxProd = 3;     // producer warps
-constexpr int kPxWin = 640;    // block-table entries kept in shared memory, per producer warp
 constexpr int kPxMarks = 16;   // pieces of which a bad block is remembered; more than the ring has stages
 constexpr int kPxPBytes = kPxRows * kPxKeys * 2;
 // warps 0-7: softmax (warp w: query tile w / 4); 8, 11, 12: producers; 9: S MMAs (and the TMEM allocation); 10: PV MMAs
@@ -71,9 +70,9 @@ struct PxShared {  // follows the 1024-aligned operand area
     uint64_t kv_full[10], kv_empty[10];
     uint64_t q_full[kPxTiles], s_full[kPxTiles], s_free[kPxTiles], p_full[kPxTiles], o_done[kPxTiles];
     uint32_t tmem_base;
-    int g0, base0, red[33];
+    int at[7];  // where the CTA's range begins: a group as PxWalk has it
+    int red[32];
     int bad[kPxMarks];
-    int tbl[kPxProd][kPxWin];
 };
 template <int kD>
 constexpr size_t kPxSmem = 1024 + Px<kD>::kOperands + sizeof(PxShared);
@@ -99,25 +98,36 @@ struct PxPlan {
     GroupArgs groups;
 };
 
-// Key tiles of one row tile of group g, and its row tiles (0 where there is no prefix to share).
-__device__ __forceinline__ void px_group(const PxPlan& pl, int g, int& nt, int& rt) {
-    const int n = pl.groups.start[g + 1] - pl.groups.start[g];
-    const int P = n > 1 ? group_prefix(pl.groups, pl.max_blocks, pl.BS, g) : 0;
-    nt = P > 0 ? (P + kPxKeys - 1) / kPxKeys : 0;
-    rt = n > 1 ? (n + pl.TC - 1) / pl.TC : 0;
-}
-
 // A role's walk over the CTA's pieces.
 struct PxWalk {
-    int g, base, nt, rt;             // group, its first key tile in the order, its key tiles and row tiles
-    int first, n;                    // its first sequence, its members
-    int h, tile, k0, k1;             // the piece: KV head, row tile, key tiles [k0, k1)
-    __device__ __forceinline__ void load(const PxPlan& pl) {
-        px_group(pl, g, nt, rt);
-        first = pl.groups.start[g];
-        n = pl.groups.start[g + 1] - first;
+    int g, base;          // group, its first key tile in the order
+    int first, n;         // its first sequence, its members
+    int prefix, nt, rt;   // positions read once; key tiles of one row tile; row tiles (0 where there is nothing to share)
+    int h, tile, k0, k1;  // the piece: KV head, row tile, key tiles [k0, k1)
+    // Group g from its entries, which were loaded together.
+    __device__ __forceinline__ void set(const PxPlan& pl, int from, int to, int shared) {
+        first = from;
+        n = to - from;
+        prefix = n > 1 && shared > 0 && static_cast<long long>(shared) <= static_cast<long long>(pl.max_blocks) * pl.BS
+                     ? shared / pl.BS * pl.BS : 0;
+        nt = (prefix + kPxKeys - 1) / kPxKeys;
+        rt = prefix > 0 ? (n + pl.TC - 1) / pl.TC : 0;
     }
-    __device__ __forceinline__ PxWalk(const PxPlan& pl, int g0, int base0) : g(g0), base(base0) { load(pl); }
+    __device__ __forceinline__ void load(const PxPlan& pl) {
+        set(pl, pl.groups.start[g], pl.groups.start[g + 1], pl.groups.shared[g]);
+    }
+    __device__ __forceinline__ void put(int* at) const {
+        at[0] = g;
+        at[1] = base;
+        at[2] = first;
+        at[3] = n;
+        at[4] = prefix;
+        at[5] = nt;
+        at[6] = rt;
+    }
+    PxWalk() = default;
+    __device__ __forceinline__ explicit PxWalk(const int* at)
+        : g(at[0]), base(at[1]), first(at[2]), n(at[3]), prefix(at[4]), nt(at[5]), rt(at[6]) {}
     // The piece at key tile `at` of a range that ends at `end`.
     __device__ __forceinline__ void to(const PxPlan& pl, int at, int end) {
         while (at >= base + pl.Hkv * rt * nt) {
@@ -149,8 +159,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     uint8_t* sKV = base + kPxTiles * kPxPBytes;
     PxShared* sm = reinterpret_cast<PxShared*>(base + C::kOperands);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int BS = pl.BS, G = pl.G;
-
+    const int BS = pl.BS, G = pl.G, N = pl.groups.N;
+    // groups, then block ids, then K and V: three dependent loads; the first two and q come to L2 while the
+    // predecessor ends
+    const unsigned worker = blockIdx.x * blockDim.x + tid;
+    prefetch_l2(pl.groups.start, (static_cast<size_t>(N) + 1) * 4, worker);
+    prefetch_l2(pl.groups.shared, static_cast<size_t>(N) * 4, worker);
+    prefetch_l2(block_tables, static_cast<size_t>(pl.B) * pl.max_blocks * 4, worker);
+    prefetch_l2(q, static_cast<size_t>(pl.B) * pl.Hq * kD * 2, worker);
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&sm->kv_full[s], kPxProd);  // one arrival (with its bytes) per producer warp
@@ -166,14 +182,18 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         fence_mbar_init();
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
-        sm->g0 = sm->base0 = 0;
         for (int i = 0; i < kPxMarks; ++i) sm->bad[i] = 0;
+    }
+    if (warp == kPxWarpS) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
+                     "r"(kPxTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the whole work, and this CTA's range of it: key tiles [start, end)
-    const int N = pl.groups.N;
     auto scan = [&](int v, int& total) {  // over the CTA; exclusive
         int x = v;
 #pragma unroll
@@ -194,19 +214,17 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         return before + x - v;
     };
     bool wrong = false;
-    int sum = 0, total;
-    for (int g = tid; g < N; g += kPxThreads) {
+    int sum = 0, total, mine = 0;  // mine: key tiles of group tid
+    PxWalk own;
+    for (int g = N - 1 - (N - 1 - tid) % kPxThreads; g >= tid && g < N; g -= kPxThreads) {  // group tid comes last
         const int s = pl.groups.start[g], e = pl.groups.start[g + 1];
-        if (s > e || s < 0 || e > pl.B || (g == 0 && s != 0)) {
-            wrong = true;
-            continue;
-        }
-        int nt, rt;
-        px_group(pl, g, nt, rt);
-        sum += pl.Hkv * nt * rt;
+        own.set(pl, s, e, pl.groups.shared[g]);
+        wrong = wrong || s > e || s < 0 || e > pl.B || (g == 0 && s != 0);
+        mine = pl.Hkv * own.nt * own.rt;
+        sum += mine;
     }
     wrong = __syncthreads_or(wrong) != 0;
-    scan(sum, total);
+    int before = scan(sum, total);
     const int P = static_cast<int>(gridDim.x);
     const int W = max(kPxMinTiles, (total + P - 1) / P);
     if (blockIdx.x == 0 && tid == 0) {
@@ -214,59 +232,60 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         if (wrong) report(status, PKV_ERR_DEVICE_BOUNDS);
     }
     const int start = min(total, static_cast<int>(blockIdx.x) * W), end = min(total, start + W);
-    if (wrong || (start >= end && blockIdx.x != 0)) return;  // uniform over the CTA
+    const bool idle = wrong || start >= end;  // uniform over the CTA
     int carry = 0;
-    for (int g0 = 0; g0 < N; g0 += kPxThreads) {
+    for (int g0 = 0; g0 < N && !wrong && (!idle || blockIdx.x == 0); g0 += kPxThreads) {
         const int g = g0 + tid;
-        int nt = 0, rt = 0, tot;
-        if (g < N) px_group(pl, g, nt, rt);
-        const int n = pl.Hkv * nt * rt, at = carry + scan(n, tot);
-        if (n > 0 && at <= start && start < at + n) {  // exactly one thread of the CTA
-            sm->g0 = g;
-            sm->base0 = at;
+        int tot = total;
+        if (N > kPxThreads) {  // else the scan above was this one
+            mine = 0;
+            if (g < N) {
+                own.g = g;
+                own.load(pl);
+                mine = pl.Hkv * own.nt * own.rt;
+            }
+            before = scan(mine, tot);
         }
-        if (blockIdx.x == 0 && g < N) ws.plan[g] = make_int2(at, nt);
+        const int at = carry + before;
+        if (mine > 0 && at <= start && start < at + mine) {  // exactly one thread of the CTA
+            own.g = g;
+            own.base = at;
+            own.put(sm->at);
+        }
+        if (blockIdx.x == 0 && g < N) ws.plan[g] = make_int2(at, own.nt);
         carry += tot;
         if (carry > start && blockIdx.x != 0) break;  // same decision in every thread
-    }
-    if (start >= end) return;
-    if (warp == kPxWarpS) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
-                     "r"(kPxTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm->tmem_base;
-    const int g0 = sm->g0, base0 = sm->base0;
 
     bool fail = false;
-    if (warp == kPxWarpProd || warp == kPxWarpPV + 1 || warp == kPxWarpPV + 2) {
+    if (idle) {
+        // nothing but the tensor memory to give back
+    } else if (warp == kPxWarpProd || warp == kPxWarpPV + 1 || warp == kPxWarpPV + 2) {
         tc_fewer_registers();
         // ------------------------------------------------ producer warps 8, 11, 12
         // Warp pw issues boxes i = pw, pw + 3, pw + 6 of every tile (box i: K of 16-key group i for i < 4, V of group
-        // i - 4 otherwise), with block ids from its own window of the block table, and arms the stage's transaction
-        // count with its own bytes.
+        // i - 4 otherwise), and arms the stage's transaction count with its own bytes.  Block
+        // ids come 32 a load, a lane each, and the next 32 ahead of their use.
         const int pw = warp == kPxWarpProd ? 0 : warp - kPxWarpPV;
         const int nbox = pw < 2 ? 3 : 2;
-        int* tbl = sm->tbl[pw];
-        PxWalk w(pl, g0, base0);
+        PxWalk w(sm->at);
         int j = 0;
         for (int at = start, piece = 0; at < end && !fail; at += w.k1 - w.k0, ++piece) {
             w.to(pl, at, end);
             const int32_t* trow = block_tables + static_cast<size_t>(w.first) * pl.max_blocks;
-            const int nblk = group_prefix(pl.groups, pl.max_blocks, BS, w.g) / BS;
-            int win0 = -kPxWin;
+            const int nblk = w.prefix / BS;
+            auto ids = [&](int i) { return i < nblk ? trow[i] : 0; };
+            int have = (w.k0 * kPxKeys) / BS, cur = ids(have + lane), nxt = ids(have + 32 + lane);
             for (int kt = w.k0; kt < w.k1 && !fail; ++kt, ++j) {
                 const int s = j % kStages;
-                const int kb0 = (kt * kPxKeys) / BS, kb1 = min(nblk - 1, (kt * kPxKeys + kPxKeys - 1) / BS);
-                if (kb0 < win0 || kb1 >= win0 + kPxWin) {  // move this warp's window of the block table
-                    __syncwarp();
-                    win0 = kb0;
-                    for (int i = lane; i < kPxWin; i += 32) tbl[i] = win0 + i < nblk ? trow[win0 + i] : 0;
-                    __syncwarp();
+                if ((kt * kPxKeys) / BS - have >= 32) {  // a tile is in at most five blocks
+                    have += 32;
+                    cur = nxt;
+                    nxt = ids(have + 32 + lane);
                 }
                 if (lane == 0 && !mbar_wait(&sm->kv_empty[s], ((j / kStages) & 1) ^ 1)) {
                     report(status, PKV_ERR_TIMEOUT);
@@ -275,12 +294,13 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 fail = __shfl_sync(0xffffffffu, fail, 0);
                 if (fail) break;
                 const int bi = pw + 3 * lane;
+                const int key0 = kt * kPxKeys + 16 * (bi & 3), kb = key0 / BS;
+                const int id0 = __shfl_sync(0xffffffffu, cur, (kb - have) & 31), id1 = __shfl_sync(0xffffffffu, nxt, (kb - have) & 31);
                 int row = 0;
                 if (lane < nbox) {  // the pool row of box bi's first key
-                    const int key0 = kt * kPxKeys + 16 * (bi & 3), kb = key0 / BS;
                     int blk = 0, slot = 0;
                     if (kb < nblk) {  // keys behind the prefix: any valid rows (masked; their V rows are cleared)
-                        blk = tbl[kb - win0];
+                        blk = kb - have < 32 ? id0 : id1;
                         slot = key0 - kb * BS;
                         if (blk < 0 || blk >= pl.NB) {
                             *const_cast<volatile int*>(&sm->bad[piece % kPxMarks]) = piece + 1;
@@ -316,7 +336,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         if (lane == 0) {
             constexpr uint32_t idS = tc_idesc(kPxRows, kPxKeys, false);
             const uint32_t kva = smem_u32(sKV);
-            PxWalk w(pl, g0, base0);
+            PxWalk w(sm->at);
             int j = 0, done[kPxTiles] = {0, 0}, pieces[kPxTiles] = {0, 0};
             for (int at = start; at < end && !fail; at += w.k1 - w.k0) {
                 w.to(pl, at, end);
@@ -358,7 +378,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         if (lane == 0) {
             constexpr uint32_t idO = tc_idesc(kPxRows, kD, true);
             const uint32_t pa = smem_u32(sP), kva = smem_u32(sKV);
-            PxWalk w(pl, g0, base0);
+            PxWalk w(sm->at);
             int j = 0, done[kPxTiles] = {0, 0};
             for (int at = start; at < end && !fail; at += w.k1 - w.k0) {
                 w.to(pl, at, end);
@@ -395,34 +415,44 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const uint32_t lrow = static_cast<uint32_t>((warp & 3) * 32) << 16;  // this warp's TMEM lanes
         const uint32_t tq = tmem + 256 * qt + lrow;
         uint8_t* pbuf = sP + qt * kPxPBytes;
-        PxWalk w(pl, g0, base0);
+        PxWalk w(sm->at);
+        const int rm = r / G, rh = r - rm * G;  // the row's member in the query tile, and query head
+        // The piece's queries as A of S = Q K^T; rows without a member are zero queries.
+        auto put_q = [&](const PxWalk& x) {
+            const bool dual = x.dual(pl);
+            if (x.k0 + (dual ? qt : 0) >= x.k1) return;
+            const int member = x.tile * pl.TC + (dual ? 0 : qt * pl.TQ) + rm;
+            const bool valid = rm < pl.TQ && member < x.n;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                q + (static_cast<size_t>(x.first + (valid ? member : 0)) * pl.Hq + x.h * G + rh) * kD);
+#pragma unroll
+            for (int hv = 0; hv < kD / 64; ++hv) {
+                uint32_t y[32];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 v = valid ? src[8 * hv + c] : make_uint4(0u, 0u, 0u, 0u);
+                    y[4 * c] = v.x;
+                    y[4 * c + 1] = v.y;
+                    y[4 * c + 2] = v.z;
+                    y[4 * c + 3] = v.w;
+                }
+                tc_st32(tq + 32 * hv, y);
+            }
+            tc_fence_before();
+            mbar_arrive(&sm->q_full[qt]);
+        };
         int done = 0;  // key tiles of this query tile
+        PxWalk next = w;
+        next.to(pl, start, end);
+        put_q(next);
         for (int at = start, piece = 0; at < end && !fail; at += w.k1 - w.k0, ++piece) {
-            w.to(pl, at, end);
+            w = next;
             const bool dual = w.dual(pl);
             const int step = dual ? 2 : 1, k0 = w.k0 + (dual ? qt : 0);  // this query tile's first key tile
-            const int member = w.tile * pl.TC + (dual ? 0 : qt * pl.TQ) + r / G, qh = w.h * G + r % G;
-            const bool valid = r < pl.TQ * G && member < w.n;  // the other rows are zero queries
+            const int member = w.tile * pl.TC + (dual ? 0 : qt * pl.TQ) + rm, qh = w.h * G + rh;
+            const bool valid = rm < pl.TQ && member < w.n;
             const int b = w.first + (valid ? member : 0);
-            if (k0 < w.k1) {
-                const uint4* src = reinterpret_cast<const uint4*>(q + (static_cast<size_t>(b) * pl.Hq + qh) * kD);
-#pragma unroll
-                for (int hv = 0; hv < kD / 64; ++hv) {
-                    uint32_t x[32];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const uint4 v = valid ? src[8 * hv + c] : make_uint4(0u, 0u, 0u, 0u);
-                        x[4 * c] = v.x;
-                        x[4 * c + 1] = v.y;
-                        x[4 * c + 2] = v.z;
-                        x[4 * c + 3] = v.w;
-                    }
-                    tc_st32(tq + 32 * hv, x);
-                }
-                tc_fence_before();
-                mbar_arrive(&sm->q_full[qt]);
-            }
-            const int prefix = group_prefix(pl.groups, pl.max_blocks, BS, w.g);
+            const int prefix = w.prefix;
             [[maybe_unused]] const int pos = kSlope && valid ? seq_lens[b] - 1 : 0;
             [[maybe_unused]] const float slope = kSlope ? pl.sc.slopes[qh] * kLog2e : 0.f;
             float m_ref = -INFINITY, lsum = 0.f;
@@ -510,6 +540,11 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 tc_fence_before();
                 mbar_arrive(&sm->p_full[qt]);
             }
+            // all S of the piece are read: the next one's queries, whose S runs while this one's results are stored
+            if (!fail && at + w.k1 - w.k0 < end) {
+                next.to(pl, at + w.k1 - w.k0, end);
+                put_q(next);
+            }
             if (!fail && k0 < w.k1 && !__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (done - 1) & 1))) fail = true;
             if (fail) {
                 if (lane == 0) report(status, PKV_ERR_TIMEOUT);
@@ -527,8 +562,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             // the P tile is free: 32 columns of the warp's 32 rows go through its quarter of it
             float4* stage = reinterpret_cast<float4*>(pbuf + (warp & 3) * 4096);
             const int own_lo = valid ? static_cast<int>(own) : -1, own_hi = valid ? static_cast<int>(own >> 32) : -1;
+            const bool any = __any_sync(0xffffffffu, valid);
 #pragma unroll 1
-            for (int cc = 0; cc < kD / 32; ++cc) {
+            for (int cc = 0; any && cc < kD / 32; ++cc) {
                 uint32_t o[32];
                 if (k0 < w.k1) {
                     tc_ld32(tq + 128 + 32 * cc, o);
