@@ -337,7 +337,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             constexpr uint32_t idS = tc_idesc(kPxRows, kPxKeys, false);
             const uint32_t kva = smem_u32(sKV);
             PxWalk w(sm->at);
-            int j = 0, done[kPxTiles] = {0, 0}, pieces[kPxTiles] = {0, 0};
+            // bit t: the phase of query tile t's barriers, and whether it had a tile (indexed arrays would lie in local
+            // memory)
+            uint32_t free_ = 1u | 2u, had = 0, queries = 0;
+            int j = 0;
             for (int at = start; at < end && !fail; at += w.k1 - w.k0) {
                 w.to(pl, at, end);
                 const bool dual = w.dual(pl);
@@ -350,8 +353,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     const uint32_t kb = kva + s * C::kStageBytes;
                     const int ta = dual ? (kt - w.k0) & 1 : 0, tb = dual ? ta : 1;
                     for (int t = ta; t <= tb; ++t) {
-                        if ((kt - w.k0 < (dual ? 2 : 1) && !mbar_wait(&sm->q_full[t], pieces[t] & 1)) ||
-                            (done[t] >= 1 && !mbar_wait(&sm->s_free[t], (done[t] - 1) & 1))) {
+                        if ((kt - w.k0 < (dual ? 2 : 1) && !mbar_wait(&sm->q_full[t], (queries >> t) & 1u)) ||
+                            ((had >> t) & 1u && !mbar_wait(&sm->s_free[t], (free_ >> t) & 1u))) {
                             fail = true;
                             break;
                         }
@@ -363,11 +366,11 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                                                : tc_desc(kb + (kk >> 2) * 1024 + 32 * (kk & 3), 16, 2048),
                                       idS, kk > 0 ? 1u : 0u);
                         tc_commit(&sm->s_full[t]);
-                        ++done[t];
+                        had |= 1u << t;
+                        free_ ^= 1u << t;
                     }
                 }
-                ++pieces[0];
-                if (!dual || w.k1 - w.k0 > 1) ++pieces[1];
+                queries ^= 1u | (!dual || w.k1 - w.k0 > 1 ? 2u : 0u);
             }
             if (fail) report(status, PKV_ERR_TIMEOUT);
         }
@@ -379,7 +382,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             constexpr uint32_t idO = tc_idesc(kPxRows, kD, true);
             const uint32_t pa = smem_u32(sP), kva = smem_u32(sKV);
             PxWalk w(sm->at);
-            int j = 0, done[kPxTiles] = {0, 0};
+            uint32_t phase = 0;  // bit t: of query tile t
+            int j = 0;
             for (int at = start; at < end && !fail; at += w.k1 - w.k0) {
                 w.to(pl, at, end);
                 const bool dual = w.dual(pl);
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     const uint32_t vb = kva + s * C::kStageBytes + C::kKBytes;
                     const int ta = dual ? (kt - w.k0) & 1 : 0, tb = dual ? ta : 1;
                     for (int t = ta; t <= tb; ++t) {  // query tile 0 first: its softmax warps clear V rows
-                        if (!mbar_wait(&sm->p_full[t], done[t] & 1)) {
+                        if (!mbar_wait(&sm->p_full[t], (phase >> t) & 1u)) {
                             fail = true;
                             break;
                         }
@@ -400,7 +404,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                                    tc_desc(vb + C::kGroup * kk, C::kGroup / 2, 1024), idO,
                                    (kt - w.k0 >= (dual ? 2 : 1) || kk > 0) ? 1u : 0u);
                         tc_commit(&sm->o_done[t]);
-                        ++done[t];
+                        phase ^= 1u << t;
                     }
                     if (!fail) tc_commit(&sm->kv_empty[s]);
                 }

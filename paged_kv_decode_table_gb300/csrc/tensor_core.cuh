@@ -132,51 +132,94 @@ __device__ __forceinline__ uint64_t tc_fma2(uint64_t a, uint64_t b, uint64_t c) 
     return r;
 }
 
-// The 64 products of a row with a tile's keys become scores in the log2 domain.  dist: the first key's position less
-// the row's; slope: of the row's head, times log2(e).  All lanes of the warp take part.
-template <bool kCap, bool kSlope>
-__device__ __forceinline__ void tc_scores(uint32_t (&sr)[2][32], int dist, float slope, const ScoreArgs& sc) {
+__device__ __forceinline__ uint64_t tc_add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The products of a row with a tile's keys become scores in the log2 domain.  dist: the first key's position less
+// the row's; slope: of the row's head, times log2(e).  All lanes of the warp take part.  Four pairs go through each
+// operation together: their chains hide one another's latency.
+template <bool kCap, bool kSlope, int kChunks>
+__device__ __forceinline__ void tc_scores(uint32_t (&sr)[kChunks][32], int dist, float slope, const ScoreArgs& sc) {
+    constexpr int kBlock = 4;
     auto at = [&](int c) -> uint32_t& { return sr[c >> 5][c & 31]; };
-    [[maybe_unused]] const float bias = slope * static_cast<float>(dist);
-    // (the bias of keys c, c + 1) added to a * b
-    auto add = [&](uint64_t a, uint64_t b, int c) {
-        if constexpr (!kSlope) return tc_mul2(a, b);
-        const uint64_t s2 = tc_pair(slope, slope), b2 = tc_pair(bias, bias);
-        return tc_fma2(a, b, tc_fma2(s2, tc_pair(static_cast<float>(c), static_cast<float>(c + 1)), b2));
+    auto both = [](float v) { return tc_pair(v, v); };
+    [[maybe_unused]] const uint64_t slope2 = both(slope), step2 = both(2.f * kBlock);
+    [[maybe_unused]] uint64_t away[kBlock];  // positions of the block's keys less the row's, exact
+    auto far = [&]() {
+#pragma unroll
+        for (int k = 0; k < kBlock; ++k) away[k] = tc_pair(static_cast<float>(dist + 2 * k), static_cast<float>(dist + 2 * k + 1));
     };
+    // a * b, with slopes plus the bias, for the pairs from c on
+    auto finish = [&](const uint64_t (&a)[kBlock], const uint64_t (&b)[kBlock], int c) {
+        uint64_t v[kBlock];
+        if constexpr (kSlope) {
+#pragma unroll
+            for (int k = 0; k < kBlock; ++k) v[k] = tc_mul2(slope2, away[k]);
+#pragma unroll
+            for (int k = 0; k < kBlock; ++k) v[k] = tc_fma2(a[k], b[k], v[k]);
+#pragma unroll
+            for (int k = 0; k < kBlock; ++k) away[k] = tc_add2(away[k], step2);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kBlock; ++k) v[k] = tc_mul2(a[k], b[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kBlock; ++k) tc_unpair(at(c + 2 * k), at(c + 2 * k + 1), v[k]);
+    };
+    if constexpr (kSlope) far();
     if constexpr (kCap) {
-        float big[2] = {0.f, 0.f};
+        float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 64; c += 2)
-            big[(c >> 1) & 1] = tc_max3(big[(c >> 1) & 1], fabsf(__uint_as_float(at(c))), fabsf(__uint_as_float(at(c + 1))));
-        const uint64_t in2 = tc_pair(sc.in, sc.in), cap2 = tc_pair(sc.cap_log2, sc.cap_log2);
-        if (__all_sync(0xffffffffu, !(fmaxf(big[0], big[1]) * sc.in > 1.f))) {
-            const uint64_t c0 = tc_pair(kTanh0 * sc.cap_log2, kTanh0 * sc.cap_log2),
-                           c1 = tc_pair(kTanh1 * sc.cap_log2, kTanh1 * sc.cap_log2),
-                           c2 = tc_pair(kTanh2 * sc.cap_log2, kTanh2 * sc.cap_log2),
-                           c3 = tc_pair(kTanh3 * sc.cap_log2, kTanh3 * sc.cap_log2),
-                           c4 = tc_pair(kTanh4 * sc.cap_log2, kTanh4 * sc.cap_log2),
-                           c5 = tc_pair(kTanh5 * sc.cap_log2, kTanh5 * sc.cap_log2);
+        for (int c = 0; c < 32 * kChunks; c += 2)
+            big[(c >> 1) & 3] = tc_max3(big[(c >> 1) & 3], fabsf(__uint_as_float(at(c))), fabsf(__uint_as_float(at(c + 1))));
+        const uint64_t in2 = both(sc.in), cap2 = both(sc.cap_log2);
+        if (__all_sync(0xffffffffu, !(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * sc.in > 1.f))) {
+            const uint64_t coef[6] = {both(kTanh0 * sc.cap_log2), both(kTanh1 * sc.cap_log2), both(kTanh2 * sc.cap_log2),
+                                      both(kTanh3 * sc.cap_log2), both(kTanh4 * sc.cap_log2), both(kTanh5 * sc.cap_log2)};
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-                const uint64_t x = tc_mul2(tc_pair(at(c), at(c + 1)), in2), w = tc_mul2(x, x);
-                const uint64_t p = tc_fma2(tc_fma2(tc_fma2(tc_fma2(tc_fma2(c5, w, c4), w, c3), w, c2), w, c1), w, c0);
-                tc_unpair(at(c), at(c + 1), add(x, p, c));
+            for (int c = 0; c < 32 * kChunks; c += 2 * kBlock) {
+                uint64_t x[kBlock], w[kBlock], p[kBlock];
+#pragma unroll
+                for (int k = 0; k < kBlock; ++k) x[k] = tc_mul2(tc_pair(at(c + 2 * k), at(c + 2 * k + 1)), in2);
+#pragma unroll
+                for (int k = 0; k < kBlock; ++k) w[k] = tc_mul2(x[k], x[k]);
+#pragma unroll
+                for (int k = 0; k < kBlock; ++k) p[k] = tc_fma2(coef[5], w[k], coef[4]);
+#pragma unroll
+                for (int e = 3; e >= 0; --e)
+#pragma unroll
+                    for (int k = 0; k < kBlock; ++k) p[k] = tc_fma2(p[k], w[k], coef[e]);
+                finish(x, p, c);
             }
         } else {
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-                const uint64_t x = tc_mul2(tc_pair(at(c), at(c + 1)), in2);
-                uint32_t x0, x1;
-                tc_unpair(x0, x1, x);
-                const uint64_t t = tc_pair(tanh_beyond(__uint_as_float(x0)), tanh_beyond(__uint_as_float(x1)));
-                tc_unpair(at(c), at(c + 1), add(t, cap2, c));
+            for (int c = 0; c < 32 * kChunks; c += 2 * kBlock) {
+                uint64_t t[kBlock], b[kBlock];
+#pragma unroll
+                for (int k = 0; k < kBlock; ++k) {
+                    uint32_t x0, x1;
+                    tc_unpair(x0, x1, tc_mul2(tc_pair(at(c + 2 * k), at(c + 2 * k + 1)), in2));
+                    t[k] = tc_pair(tanh_beyond(__uint_as_float(x0)), tanh_beyond(__uint_as_float(x1)));
+                    b[k] = cap2;
+                }
+                finish(t, b, c);
             }
         }
     } else {
-        const uint64_t m2 = tc_pair(sc.mul, sc.mul);
+        const uint64_t m2 = both(sc.mul);
 #pragma unroll
-        for (int c = 0; c < 64; c += 2) tc_unpair(at(c), at(c + 1), add(tc_pair(at(c), at(c + 1)), m2, c));
+        for (int c = 0; c < 32 * kChunks; c += 2 * kBlock) {
+            uint64_t x[kBlock], b[kBlock];
+#pragma unroll
+            for (int k = 0; k < kBlock; ++k) {
+                x[k] = tc_pair(at(c + 2 * k), at(c + 2 * k + 1));
+                b[k] = m2;
+            }
+            finish(x, b, c);
+        }
     }
 }
 
