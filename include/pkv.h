@@ -514,11 +514,19 @@ pkv_status pkv_paged_decode_attention_scored(void* out, const void* q, const voi
                                              void* workspace, size_t workspace_bytes, int32_t* dev_status,
                                              void* stream);
 
+/* Workspace bytes pkv_paged_prefill_attention_scored needs (num_sms <= 0: the
+ * current device): partial results where the query tiles are fewer than the SMs
+ * (at most about 40 MB on 152), else 0, as on errors.  Pure host arithmetic when
+ * num_sms > 0. */
+size_t pkv_prefill_scored_workspace_bytes(int B, int T_new, int Hq, int Hkv, int D, int num_sms);
+
 /*
  * pkv_paged_prefill_attention with changed scores: query row t of sequence b is
  * at position pos as there.  bf16 only, D = 128, block_size a multiple of 16, Hq
- * / Hkv <= 8, 16-byte aligned q, out and pools (else PKV_ERR_UNSUPPORTED).  Key
- * tiles that no row of a query tile sees are not read.  A row that is given no
+ * / Hkv <= 8, 16-byte aligned q, out and pools (else PKV_ERR_UNSUPPORTED).
+ * workspace: device, 16-byte aligned, at least pkv_prefill_scored_workspace_bytes(B,
+ * T_new, Hq, Hkv, D, 0) bytes (may be NULL where that is 0), contents ignored on
+ * entry; calls that can overlap on the GPU need a workspace each.  Key tiles that no row of a query tile sees are not read.  A row that is given no
  * weight is still multiplied: an infinity or NaN in V at a position that some
  * queries see reaches queries within 256 / (Hq / Hkv) tokens of them that do not.
  */
@@ -527,8 +535,8 @@ pkv_status pkv_paged_prefill_attention_scored(void* out, const void* q, const vo
                                               const int32_t* seq_lens, const int32_t* q_start,
                                               const int32_t* prefix_lens, int B, int T_new, int Hq, int Hkv, int D,
                                               int block_size, int num_blocks, float scale, float softcap,
-                                              const float* slopes, int window, pkv_dtype dtype, int32_t* dev_status,
-                                              void* stream);
+                                              const float* slopes, int window, pkv_dtype dtype, void* workspace,
+                                              size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /* Workspace bytes pkv_paged_decode_attention_shared needs (num_sms <= 0: the
  * current device).  Returns 0 on error.  Pure host arithmetic when num_sms > 0. */

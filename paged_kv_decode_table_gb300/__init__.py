@@ -52,7 +52,8 @@ __all__ = ["PkvError", "load_library", "library_path", "kv_append", "paged_decod
            "paged_prefill_attention", "DecodeStep", "test_set_wait_limit", "kv_append_q8", "kv_append_chunk_q8",
            "kv_read_blocks_q8", "paged_decode_attention_q8", "decode_q8_workspace_bytes", "qk_norm_rope_append",
            "rope_freqs", "paged_decode_attention_scored", "paged_prefill_attention_scored",
-           "paged_decode_attention_shared", "decode_scored_workspace_bytes", "decode_shared_workspace_bytes"]
+           "paged_decode_attention_shared", "decode_scored_workspace_bytes", "decode_shared_workspace_bytes",
+           "prefill_scored_workspace_bytes"]
 
 STATUS = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED", 3: "PKV_ERR_CUDA",
           4: "PKV_ERR_DEVICE_BOUNDS", 5: "PKV_ERR_TIMEOUT", 6: "PKV_ERR_NONFINITE", 7: "PKV_ERR_CAPACITY"}
@@ -162,8 +163,10 @@ def load_library():
                                                           f32, P, i32, i32, P, sz, P, P]
         lib.pkv_paged_decode_attention_scored.restype = i32
         lib.pkv_paged_prefill_attention_scored.argtypes = [P, P, P, P, P, i32, P, P, P, i32, i32, i32, i32, i32, i32,
-                                                           i32, f32, f32, P, i32, i32, P, P]
+                                                           i32, f32, f32, P, i32, i32, P, sz, P, P]
         lib.pkv_paged_prefill_attention_scored.restype = i32
+        lib.pkv_prefill_scored_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+        lib.pkv_prefill_scored_workspace_bytes.restype = sz
         lib.pkv_paged_decode_attention_shared.argtypes = [P, P, P, P, P, i32, P, P, P, i32, i32, i32, i32, i32, i32,
                                                           i32, f32, f32, P, i32, P, sz, P, P]
         lib.pkv_paged_decode_attention_shared.restype = i32
@@ -967,6 +970,10 @@ def decode_shared_workspace_bytes(B: int, Hq: int, Hkv: int, D: int, num_sms: in
     return int(load_library().pkv_decode_shared_workspace_bytes(B, Hq, Hkv, D, num_sms))
 
 
+def prefill_scored_workspace_bytes(B: int, T_new: int, Hq: int, Hkv: int, D: int, num_sms: int = 0) -> int:
+    return int(load_library().pkv_prefill_scored_workspace_bytes(B, T_new, Hq, Hkv, D, num_sms))
+
+
 def _scored_failed(name, code, q, k_cache, v_cache, block_tables, seq_lens, slopes, out, workspace, status, more):
     if code < 0:
         _dtype_code(q)
@@ -1013,17 +1020,18 @@ def paged_decode_attention_scored(q, k_cache, v_cache, block_tables, seq_lens, s
 
 def paged_prefill_attention_scored(q, k_cache, v_cache, block_tables, seq_lens, q_start, softcap: float = 0.0,
                                    slopes=None, window: int = 0, prefix_lens=None, out=None, scale: float = 0.0,
-                                   status=None):
+                                   workspace=None, status=None):
     """paged_prefill_attention with the scores of paged_decode_attention_scored;
     returns out [T_new, Hq, D].  The first prefix_lens[b] positions of a sequence
-    are seen by all its queries, those before them included."""
+    are seen by all its queries, those before them included.  Without `workspace`
+    one is allocated for the call."""
     r = (_calls or _native()).prefill_scored(q, k_cache, v_cache, block_tables, seq_lens, q_start, softcap, slopes,
-                                             window, prefix_lens, out, scale, status)
+                                             window, prefix_lens, out, scale, workspace, status)
     if type(r) is not int:
         return r
     B = seq_lens.shape[0]
     _scored_failed("pkv_paged_prefill_attention_scored", r, q, k_cache, v_cache, block_tables, seq_lens, slopes, out,
-                   None, status, {"q_start": (q_start, (B + 1,)), "prefix_lens": (prefix_lens, (B,))})
+                   workspace, status, {"q_start": (q_start, (B + 1,)), "prefix_lens": (prefix_lens, (B,))})
 
 
 def paged_decode_attention_shared(q, k_cache, v_cache, block_tables, seq_lens, group_start, shared_lens,

@@ -26,7 +26,8 @@ bool prefill_tc_supported(int Hq, int Hkv, int D, int BS, const void* q, const v
 cudaError_t launch_prefill_tc(void* out, const void* q, const void* k_cache, const void* v_cache,
                               const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,
                               const int32_t* q_start, int B, int T_new, int Hq, int Hkv, int BS, int NB, float scale,
-                              const ScoreArgs* scored, int32_t* status, cudaStream_t stream);
+                              const ScoreArgs* scored, void* workspace, int P, int32_t* status, cudaStream_t stream);
+size_t prefill_scored_workspace_bytes(int B, int T_new, int Hq, int Hkv, int P);
 cudaError_t launch_typical_sampler(int32_t* tokens, const float* logits, int B, int V, const float* temperature,
                                    const float* typical_p, const uint64_t* seeds, const uint64_t* offsets,
                                    int32_t* status, cudaStream_t stream);
@@ -154,10 +155,16 @@ pkv_status pkv_paged_prefill_attention(void* out, const void* q, const void* k_c
     if (pkv::prefill_tc_supported(Hq, Hkv, D, block_size, q, out, k_cache, v_cache))
         return cuda_status(pkv::launch_prefill_tc(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                                                   seq_lens, q_start, B, T_new, Hq, Hkv, block_size, num_blocks,
-                                                  scale, nullptr, dev_status, static_cast<cudaStream_t>(stream)));
+                                                  scale, nullptr, nullptr, 0, dev_status, static_cast<cudaStream_t>(stream)));
     return cuda_status(pkv::launch_prefill_attention(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                                                      seq_lens, q_start, B, T_new, Hq, Hkv, block_size, num_blocks,
                                                      scale, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+size_t pkv_prefill_scored_workspace_bytes(int B, int T_new, int Hq, int Hkv, int D, int num_sms) {
+    if (B < 0 || T_new < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1) return 0;
+    const int P = num_sms > 0 ? num_sms : pkv::device_sm_count();
+    return P > 0 && D == 128 ? pkv::prefill_scored_workspace_bytes(B, T_new, Hq, Hkv, P) : 0;
 }
 
 pkv_status pkv_paged_prefill_attention_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -165,8 +172,8 @@ pkv_status pkv_paged_prefill_attention_scored(void* out, const void* q, const vo
                                               const int32_t* seq_lens, const int32_t* q_start,
                                               const int32_t* prefix_lens, int B, int T_new, int Hq, int Hkv, int D,
                                               int block_size, int num_blocks, float scale, float softcap,
-                                              const float* slopes, int window, pkv_dtype dtype, int32_t* dev_status,
-                                              void* stream) {
+                                              const float* slopes, int window, pkv_dtype dtype, void* workspace,
+                                              size_t workspace_bytes, int32_t* dev_status, void* stream) {
     pkv::ScoreArgs sc;
     if (B < 0 || T_new < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || block_size < 1 || num_blocks < 1 ||
         max_blocks_per_seq < 1 || !dtype_ok(dtype) ||
@@ -176,9 +183,14 @@ pkv_status pkv_paged_prefill_attention_scored(void* out, const void* q, const vo
     if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !q_start) return PKV_ERR_INVALID_ARG;
     if (dtype != PKV_BF16 || !pkv::prefill_tc_supported(Hq, Hkv, D, block_size, q, out, k_cache, v_cache))
         return PKV_ERR_UNSUPPORTED;
+    const int P = pkv::device_sm_count();
+    const size_t need = pkv::prefill_scored_workspace_bytes(B, T_new, Hq, Hkv, P > 0 ? P : 1);
+    if (workspace_bytes < need || (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u))))
+        return PKV_ERR_INVALID_ARG;
+    if (P <= 0) return PKV_ERR_CUDA;
     return cuda_status(pkv::launch_prefill_tc(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
-                                              q_start, B, T_new, Hq, Hkv, block_size, num_blocks, 1.f, &sc, dev_status,
-                                              static_cast<cudaStream_t>(stream)));
+                                              q_start, B, T_new, Hq, Hkv, block_size, num_blocks, 1.f, &sc, workspace, P,
+                                              dev_status, static_cast<cudaStream_t>(stream)));
 }
 
 size_t pkv_decode_workspace_bytes(int B, int Hq, int D, int num_sms) {

@@ -51,6 +51,8 @@
 #include <cuda.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "tensor_core.cuh"
 
 namespace pkv {
@@ -131,6 +133,14 @@ __device__ __forceinline__ void score_tile(uint32_t (&sr)[2][32], int kbase, int
     }
 }
 
+// Few query tiles over long key ranges (scored): S CTAs take a share of a pair of query tiles' keys each and leave
+// maxima, sums and float32 O of their rows, [T_new * Hq][S], to prefill_join_kernel.
+struct TcSplit {
+    int S;
+    float2* ml;
+    float* o;
+};
+
 // kKind: kPlain, or kMasked (the masks of attention_scores.cuh) with kCapped and kSloped where its scores are.
 template <int kKind>
 __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThreads, 1)
@@ -138,8 +148,9 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                       const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ out,
                       const int32_t* __restrict__ block_tables, int max_blocks, const int32_t* __restrict__ seq_lens,
                       const int32_t* __restrict__ q_start, int B, int Hq, int Hkv, int BS, int NB, float scale_log2,
-                      const __grid_constant__ ScoreArgs sc, int32_t* status) {
+                      const __grid_constant__ ScoreArgs sc, const __grid_constant__ TcSplit split, int32_t* status) {
     constexpr bool kScored = kKind != kPlain;
+    const int S = kScored ? split.S : 1;  // CTAs along the keys of a pair of query tiles
     extern __shared__ uint8_t tc_raw[];
     uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tc_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sP = base;                          // P of query tile t at t kTcPBytes
@@ -149,6 +160,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
     const int G = Hq / Hkv, h = static_cast<int>(blockIdx.x) % Hkv;
     const int TQ = kTcRows / G;    // chunk tokens per query tile (rows TQ G .. 127 are padding)
     const int TC = kTcQT * TQ;     // chunk tokens per CTA
+    [[maybe_unused]] const int share = kScored ? static_cast<int>(blockIdx.x) / Hkv % S : 0;
 
     // ---- prologue, independent of the inputs
     if (tid == 0) {
@@ -184,7 +196,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
         // sequences are ordered by their number of key tiles, longest first (ties:
         // sequence order, then tile order), so that the longest start in the first
         // wave.  v = the rank's key-tile count, found by bisection on the counts.
-        const int k = static_cast<int>(blockIdx.x) / Hkv;
+        const int k = static_cast<int>(blockIdx.x) / Hkv / S;
         int total = 0, vmax = 0;
         for (int b0 = 0; b0 < B; b0 += 32) {
             const int bb = b0 + lane;
@@ -260,7 +272,9 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
     const bool row_valid = active && softmax_warp && r < TQ * G && tl < nt;  // rows TQ G .. 127: padding
     if (bad_len) {
         if (tid == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
-        if (row_valid) {
+        if (row_valid && S > 1) {  // a share that cannot be read makes the row zero
+            split.ml[(static_cast<size_t>(t0 + tl) * Hq + qh) * S + share] = make_float2(-INFINITY, -1.f);
+        } else if (row_valid) {
             uint4* o = reinterpret_cast<uint4*>(out + (static_cast<size_t>(t0 + tl) * Hq + qh) * kTcDim);
             for (int c = 0; c < 16; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -275,8 +289,11 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
     const int plast = max(p0 + nt, pfx) - 1;          // the CTA's last key (keys 0 .. plast are read)
     // key tile i of the walk is tile i, behind the prefix's tiles (near) tile i + skip
     [[maybe_unused]] const int near = (pfx + kTcKeys - 1) / kTcKeys, skip = max(0, wlo / kTcKeys - near);
-    const int ntiles = active ? plast / kTcKeys + 1 - (kScored ? skip : 0) : 0;
-    auto key_tile = [&](int i) { return kScored && i >= near ? i + skip : i; };
+    const int nall = active ? plast / kTcKeys + 1 - (kScored ? skip : 0) : 0;
+    // this CTA's share of them: [first, first + ntiles)
+    const int first = kScored ? static_cast<int>(static_cast<long long>(nall) * share / S) : 0;
+    const int ntiles = kScored ? static_cast<int>(static_cast<long long>(nall) * (share + 1) / S) - first : nall;
+    auto key_tile = [&](int i) { return kScored ? (i + first >= near ? i + first + skip : i + first) : i; };
     // iteration j handles key tile (j + rot) mod ntiles (any order gives the same softmax)
     const int rot = ntiles > 0 ? static_cast<int>((blockIdx.x * 13u) % static_cast<unsigned>(ntiles)) : 0;
     const int nblk_used = active ? plast / BS + 1 : 0;
@@ -544,11 +561,27 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             if (lane == 0) report(status, PKV_ERR_TIMEOUT);
         } else {
             tc_fence_after();
+            if (S > 1) {
+                const size_t at = row_valid ? (static_cast<size_t>(t0 + tl) * Hq + qh) * S + share : 0;
+                if (row_valid) split.ml[at] = make_float2(m_ref, sm->bad ? -1.f : lsum);
+                float4* to = reinterpret_cast<float4*>(split.o + at * kTcDim);
+#pragma unroll 1
+                for (int cc = 0; ntiles > 0 && cc < kTcDim / 32; ++cc) {
+                    uint32_t o[32];
+                    tc_ld32(tq + lrow + 128 + 32 * cc, o);
+                    if (row_valid) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            to[8 * cc + i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                         __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    }
+                }
+            }
             const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
             const bool store = row_valid && !sm->bad;
             uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<size_t>(t0 + (row_valid ? tl : 0)) * Hq + qh) * kTcDim);
 #pragma unroll 1
-            for (int cc = 0; cc < kTcDim / 32; ++cc) {
+            for (int cc = 0; S == 1 && cc < kTcDim / 32; ++cc) {
                 uint32_t o[32];
                 tc_ld32(tq + lrow + 128 + 32 * cc, o);
                 uint32_t w[16];
@@ -574,6 +607,43 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcTmemCols)
                      : "memory");
     }
+}
+
+// out = sum o_s 2^(m_s - M) / sum l_s 2^(m_s - M) over a row's shares, a warp a row; a share without keys has l = 0 and
+// no O.  Rows behind the last sequence stay as they are.
+__global__ void __launch_bounds__(128)
+    prefill_join_kernel(__nv_bfloat16* out, const TcSplit split, const int32_t* q_start, int B, int T_new, int Hq) {
+    const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const long long rows = static_cast<long long>(min(q_start[B], T_new)) * Hq;  // older than the kernel before
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (row >= rows) return;
+    const float2* ml = split.ml + row * split.S;
+    const float2 mine = lane < split.S ? __ldcg(ml + lane) : make_float2(-INFINITY, 0.f);
+    const float2 more = lane + 32 < split.S ? __ldcg(ml + lane + 32) : make_float2(-INFINITY, 0.f);
+    float M = fmaxf(mine.x, more.x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float mu = M == -INFINITY ? 0.f : M, f0 = tc_ex2(mine.x - mu), f1 = tc_ex2(more.x - mu);
+    const bool bad = __any_sync(0xffffffffu, mine.y < 0.f || more.y < 0.f);
+    float l = mine.y * f0 + more.y * f1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* os = reinterpret_cast<const float4*>(split.o + row * split.S * kTcDim) + lane;
+#pragma unroll 4
+    for (int s = 0; s < split.S; ++s) {
+        const float w = __shfl_sync(0xffffffffu, s < 32 ? f0 : f1, s & 31), sum = __shfl_sync(0xffffffffu, s < 32 ? mine.y : more.y, s & 31);
+        if (sum == 0.f) continue;
+        const float4 v = __ldcg(os + static_cast<size_t>(s) * (kTcDim / 4));
+        acc = make_float4(fmaf(v.x, w, acc.x), fmaf(v.y, w, acc.y), fmaf(v.z, w, acc.z), fmaf(v.w, w, acc.w));
+    }
+    const bool zero = bad || l == 0.f;
+    const float inv = 1.f / l;
+    const uint2 v = zero ? make_uint2(0u, 0u)
+                         : make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    reinterpret_cast<uint2*>(out + row * kTcDim)[lane] = v;
 }
 
 // The K pool [NB, Hkv, BS, 128] bf16 in four dimensions: (64 elements, 8 rows,
@@ -616,13 +686,40 @@ bool prefill_tc_supported(int Hq, int Hkv, int D, int BS, const void* q, const v
            a16(v);
 }
 
+// CTAs along the keys: as many as fill the SMs once, where the pairs of query tiles are fewer.
+constexpr int kTcShares = 64;     // at most
+constexpr int kTcShareTiles = 4;  // key tiles a share has at least, by the table's width or the window
+static long long tc_units(int B, int T_new, int Hq, int Hkv) {
+    return (static_cast<long long>(T_new) / (kTcQT * (kTcRows / (Hq / Hkv))) + B) * Hkv;
+}
+static int tc_shares(int B, int T_new, int Hq, int Hkv, long long longest, int P) {
+    const long long units = std::max(1LL, tc_units(B, T_new, Hq, Hkv));
+    const long long tiles = std::max(1LL, longest / (kTcKeys * kTcShareTiles));
+    return static_cast<int>(std::max(1LL, std::min({P / units, tiles, static_cast<long long>(kTcShares)})));
+}
+static size_t tc_part_o(long long places) { return static_cast<size_t>((places * 8 + 255) / 256 * 256); }
+size_t prefill_scored_workspace_bytes(int B, int T_new, int Hq, int Hkv, int P) {
+    if (Hq / Hkv > 8) return 0;
+    const int S = tc_shares(B, T_new, Hq, Hkv, 0x7fffffffLL, P);
+    const long long places = static_cast<long long>(T_new) * Hq * S;
+    return S == 1 ? 0 : tc_part_o(places) + static_cast<size_t>(places) * kTcDim * 4;
+}
+
 cudaError_t launch_prefill_tc(void* out, const void* q, const void* k_cache, const void* v_cache,
                               const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,
                               const int32_t* q_start, int B, int T_new, int Hq, int Hkv, int BS, int NB, float scale,
-                              const ScoreArgs* scored, int32_t* status, cudaStream_t stream) {
+                              const ScoreArgs* scored, void* workspace, int P, int32_t* status, cudaStream_t stream) {
     const int G = Hq / Hkv, TC = kTcQT * (kTcRows / G);
     const long long tiles = static_cast<long long>(T_new) / TC + B;
     if (tiles * Hkv > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    TcSplit split{1, nullptr, nullptr};
+    if (scored != nullptr) {
+        long long longest = std::min(static_cast<long long>(max_blocks) * BS, 0x7fffffffLL);
+        if (scored->window > 0 && scored->prefix_lens == nullptr) longest = std::min(longest, static_cast<long long>(scored->window) + TC);
+        split.S = tc_shares(B, T_new, Hq, Hkv, longest, P);
+        split.ml = static_cast<float2*>(workspace);
+        split.o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tc_part_o(static_cast<long long>(T_new) * Hq * split.S));
+    }
     CUtensorMap tmK, tmV;
     if (!encode_pool_k16(&tmK, k_cache, NB, Hkv, BS) || !encode_pool_box_halves(&tmV, v_cache, NB, Hkv, BS, 16))
         return cudaErrorInvalidValue;
@@ -634,7 +731,7 @@ cudaError_t launch_prefill_tc(void* out, const void* q, const void* k_cache, con
                                            static_cast<int>(kTcSmemBytes));
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * Hkv), 1, 1);  // KV head innermost
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * Hkv * split.S), 1, 1);  // KV head innermost
     cfg.blockDim = dim3(scored != nullptr ? kTcScoredThreads : kTcThreads, 1, 1);
     cfg.dynamicSmemBytes = kTcSmemBytes;
     cfg.stream = stream;
@@ -646,9 +743,13 @@ cudaError_t launch_prefill_tc(void* out, const void* q, const void* k_cache, con
     const float scale_log2 = scale * 1.4426950408889634f;
     err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, static_cast<const __nv_bfloat16*>(q),
                              static_cast<__nv_bfloat16*>(out), block_tables, max_blocks, seq_lens, q_start, B, Hq, Hkv,
-                             BS, NB, scale_log2, scored != nullptr ? *scored : ScoreArgs{}, status);
-    if (err != cudaSuccess) return err;
-    return cudaGetLastError();
+                             BS, NB, scale_log2, scored != nullptr ? *scored : ScoreArgs{}, split, status);
+    if (err != cudaSuccess || split.S == 1) return err != cudaSuccess ? err : cudaGetLastError();
+    cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(T_new) * Hq + 3) / 4), 1, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.dynamicSmemBytes = 0;
+    err = cudaLaunchKernelEx(&cfg, prefill_join_kernel, static_cast<__nv_bfloat16*>(out), split, q_start, B, T_new, Hq);
+    return err != cudaSuccess ? err : cudaGetLastError();
 }
 
 }  // namespace pkv

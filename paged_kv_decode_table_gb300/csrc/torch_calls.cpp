@@ -328,22 +328,28 @@ PyObject* attend_scored(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // prefill_scored(q, k_cache, v_cache, block_tables, seq_lens, q_start, softcap, slopes, window, prefix_lens, out,
-//                scale, status) -> out
+//                scale, workspace, status) -> out
 PyObject* prefill_scored(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     Scored x;
     int window = 0;
-    const int ok = n == 13 ? x.take(a[0], a[1], a[2], a[3], a[4], a[6], a[7], a[10], a[11], a[12]) : 0;
+    const int ok = n == 14 ? x.take(a[0], a[1], a[2], a[3], a[4], a[6], a[7], a[10], a[11], a[13]) : 0;
     if (ok < 0 || (ok && !integer(a[8], &window))) return nullptr;
     if (!ok || !is(tensor(a[5]), ScalarType::Int, x.c.dev, {x.s.B + 1}) ||
         !optional(a[9], ScalarType::Int, x.c.dev, {x.s.B}))
         return code(-1);
     const c10::cuda::OptionalCUDAGuard guard(x.c.k->device());
+    const int T = static_cast<int>(x.q->size(0));
+    const size_t need = a[12] == Py_None ? pkv_prefill_scored_workspace_bytes(x.s.B, T, x.Hq, x.c.Hkv, x.c.D, 0) : 0;
+    Tensor own;
+    const Tensor* ws = nullptr;
+    if ((need > 0 || a[12] != Py_None) && !(ws = workspace(a[12], need, x.q, &own))) return code(-1);
     Tensor out = x.result(a[10]);
     const pkv_status r = pkv_paged_prefill_attention_scored(
         out.data_ptr(), x.q->data_ptr(), x.c.k->data_ptr(), x.c.v->data_ptr(), x.s.tables, x.s.max_blocks, x.s.lens,
-        pointer<int32_t>(a[5]), pointer<int32_t>(a[9]), x.s.B, static_cast<int>(x.q->size(0)), x.Hq, x.c.Hkv, x.c.D,
-        x.c.BS, x.c.NB, x.scale, x.softcap, pointer<float>(a[7]), window, x.dtype, x.s.status, stream_of(x.c.dev));
+        pointer<int32_t>(a[5]), pointer<int32_t>(a[9]), x.s.B, T, x.Hq, x.c.Hkv, x.c.D, x.c.BS, x.c.NB, x.scale, x.softcap,
+        pointer<float>(a[7]), window, x.dtype, ws ? ws->data_ptr() : nullptr, ws ? ws->nbytes() : 0, x.s.status,
+        stream_of(x.c.dev));
     return r != PKV_OK ? code(r) : THPVariable_Wrap(std::move(out));
     END_HANDLE_TH_ERRORS
 }

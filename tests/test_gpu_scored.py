@@ -159,6 +159,23 @@ def test_prefill_ragged(Hq, Hkv, BS, chunks, before, mask):
     R.check(got, ref, tol)
 
 
+@pytest.mark.parametrize("Hq,Hkv,BS,chunks,before", [
+    (8, 1, 16, [3], [5000]), (16, 2, 16, [40, 1, 0], [3000, 900, 100]), (4, 4, 48, [200], [100]), (5, 5, 32, [70], [9000])])
+@pytest.mark.parametrize("mask", range(len(MASKS)))
+def test_prefill_few_rows_over_long_ranges(Hq, Hkv, BS, chunks, before, mask):
+    m = dict(MASKS[mask])
+    lens = [a + b for a, b in zip(chunks, before)]
+    x = R.make(mask + Hq, lens, Hq, Hkv, 128, BS, BF, chunks=chunks, q_size=5.0 if "softcap" in m else 1.5)
+    sl = R.slopes(Hq) if m.pop("slopes", False) else None
+    pre = _prefix(m.pop("prefix", None), lens)
+    R.hide(x, m.get("window", 0), pre)
+    assert pkv.prefill_scored_workspace_bytes(len(lens), sum(chunks), Hq, Hkv, 128) > 0  # the keys are split
+    st = pkv.new_status()
+    got = _prefill(x, st, slopes=sl, prefix_lens=pre, **m)
+    assert pkv.check_status(st) == 0
+    R.check(got, *R.reference(x, slopes=sl, prefix=pre, **m))
+
+
 def test_prefill_prefix_seen_by_all_rows():
     # the whole chunk attends in both directions, in tiles behind the first one too
     x = R.make(3, [600], 8, 1, 128, 16, BF, chunks=[600])
@@ -187,6 +204,16 @@ def test_prefill_bad_tables_and_rows_behind_the_last():
 
 
 # ------------------------------------------------------------------ as a program uses them
+def test_prefill_workspace():
+    x = R.make(6, [900], 8, 2, 128, 16, BF, chunks=[20])
+    need = pkv.prefill_scored_workspace_bytes(1, 20, 8, 2, 128)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    ref, tol = R.reference(x, softcap=9.0)
+    R.check(_prefill(x, softcap=9.0, workspace=ws), ref, tol)
+    with pytest.raises(pkv.PkvError):
+        _prefill(x, workspace=ws[:need - 256])
+
+
 def test_streams_and_graphs():
     xs = [R.make(20 + i, [500 + 900 * i, 40, 3000], 32, 8, 128, 16, BF) for i in range(2)]
     refs = [R.reference(x, softcap=15.0, window=600) for x in xs]

@@ -29,9 +29,9 @@ def shared(lib, o=X, q=X, k=X, v=X, bt=X, mb=4, sl=X, gs=X, sh=X, N=1, B=2, Hq=4
 
 
 def prefill(lib, o=X, q=X, k=X, v=X, bt=X, mb=4, sl=X, qs=X, pre=None, B=2, T=4, Hq=4, Hkv=2, D=128, BS=16, NB=4,
-            scale=0.0, cap=0.0, slopes=None, window=0, dt=1):
+            scale=0.0, cap=0.0, slopes=None, window=0, dt=1, ws=X, wb=1 << 40):
     return lib.pkv_paged_prefill_attention_scored(o, q, k, v, bt, mb, sl, qs, pre, B, T, Hq, Hkv, D, BS, NB, scale, cap,
-                                                  slopes, window, dt, None, None)
+                                                  slopes, window, dt, ws, wb, None, None)
 
 
 SHAPES = [dict(B=-1), dict(Hq=0), dict(Hkv=0), dict(Hq=5), dict(D=0), dict(BS=0), dict(NB=0), dict(mb=0), dict(dt=2),
@@ -74,6 +74,10 @@ def test_workspaces_are_host_arithmetic(lib):
         assert a >= 2 * 152 * 32 * 130 * 4
         assert f(64, 32, 5, 128, num_sms=152) == 0 and f(-1, 32, 8, 128, num_sms=152) == 0
         assert f(0, 32, 8, 128, num_sms=152) > 0 and f(3, 6, 2, 33, num_sms=152) > 0
+    f = pkv.prefill_scored_workspace_bytes
+    assert f(16, 8192, 32, 8, 128, num_sms=152) == 0  # 1152 pairs of query tiles
+    assert f(1, 64, 32, 8, 128, num_sms=152) >= 64 * 32 * 9 * 130 * 4  # 16 of them: 9 shares
+    assert f(1, 64, 33, 8, 128, num_sms=152) == 0 and f(1, 64, 32, 8, 64, num_sms=152) == 0
     # and 256 rows of one KV head per SM, twice, behind them
     assert pkv.decode_shared_workspace_bytes(64, 32, 8, 128, num_sms=152) >= 2 * 152 * (32 + 256) * 130 * 4
 
