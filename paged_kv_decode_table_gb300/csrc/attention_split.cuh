@@ -50,6 +50,11 @@ struct SplitSpace {
     float* o;        // its sums of products
 };
 
+// Whether group g's bounds can be those of a group (all groups': start is an array of such).
+__device__ __forceinline__ bool group_valid(const GroupArgs& ga, int B, int g) {
+    const int s = ga.start[g], e = ga.start[g + 1];
+    return s <= e && s >= 0 && e <= B && (g > 0 || s == 0);
+}
 // The group of sequence b, -1 where it has none (start non-decreasing).
 __device__ __forceinline__ int group_of(const GroupArgs& ga, int b) {
     int lo = 0, hi = ga.N;

@@ -80,6 +80,10 @@ __device__ __forceinline__ Span span_of(const SplitPlan& pl, const int32_t* seq_
         if (s.seen.lo < 0 || s.seen.lo >= L) return s;
     } else {
         s.seen = decode_seen(pl.sc, b, L);
+        if (pl.groups.N > 0) {  // a call with shared prefixes that reads them per sequence: the same refusals
+            const int shared = shared_prefix(pl.groups, pl.max_blocks, pl.BS, b);
+            if (shared < 0 || L < shared) return s;
+        }
     }
     s.near = (s.seen.pfx + kUnit - 1) / kUnit;
     const int first = max(s.near, s.seen.lo / kUnit);
@@ -186,8 +190,21 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
     // Only after the wait: the joining kernel's predecessors are complete then.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- this CTA's range of steps: [start, end), which begins in sequence b0, whose first step is s0
     const int nthr = blockDim.x, B = pl.B, NG = pl.NG;
+    if (!kShared && pl.groups.N > 0) {  // group_start is none: zeros for every sequence
+        bool wrong = false;
+        for (int g = threadIdx.x; g < pl.groups.N; g += nthr) wrong = wrong || !group_valid(pl.groups, B, g);
+        if (__syncthreads_or(wrong)) {
+            const size_t all = static_cast<size_t>(B) * pl.Hq * pl.D, step = static_cast<size_t>(gridDim.x) * nthr;
+            for (size_t e = worker; e < all; e += step) out[e] = from_f32<__nv_bfloat16>(0.f);
+            if (threadIdx.x == 0) {
+                report(status, PKV_ERR_DEVICE_BOUNDS);
+                if (!pl.direct) ws.cuts[blockIdx.x] = SplitCut{0, 0, 0, 0};
+            }
+            return;
+        }
+    }
+    // ---- this CTA's range of steps: [start, end), which begins in sequence b0, whose first step is s0
     int W = 1, start, end, b0, s0;
     if (!kShared && pl.direct) {
         b0 = static_cast<int>(blockIdx.x) / NG;
@@ -1205,9 +1222,10 @@ size_t decode_scored_workspace_bytes(int B, int Hq, int Hkv, int D, int P) {
 // Arguments checked; B > 0.
 cudaError_t launch_decode_scored(void* out, const void* q, const void* k, const void* v, const int32_t* block_tables,
                                  int max_blocks, const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int BS, int NB,
-                                 const ScoreArgs& sc, pkv_dtype dtype, void* workspace, int P, int32_t* status,
-                                 cudaStream_t stream) {
+                                 const ScoreArgs& sc, const GroupArgs& groups, pkv_dtype dtype, void* workspace, int P,
+                                 int32_t* status, cudaStream_t stream) {
     SplitPlan pl = {};
+    pl.groups = groups;
     pl.B = B;
     pl.Hq = Hq;
     pl.Hkv = Hkv;
@@ -1284,6 +1302,7 @@ extern "C" pkv_status pkv_paged_decode_attention_scored(
     if (P <= 0) return PKV_ERR_CUDA;
     const cudaError_t err =
         launch_decode_scored(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, B, Hq, Hkv, D,
-                             block_size, num_blocks, sc, dtype, workspace, P, dev_status, static_cast<cudaStream_t>(stream));
+                             block_size, num_blocks, sc, GroupArgs{}, dtype, workspace, P, dev_status,
+                             static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

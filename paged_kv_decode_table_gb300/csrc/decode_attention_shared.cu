@@ -46,6 +46,10 @@ size_t split_space(const SplitPlan& pl, int P, int B, bool shared, void* base, S
 cudaError_t launch_split_shared(const SplitPlan& pl, const SplitSpace& ws, const void* q, const void* k, const void* v,
                                 const int32_t* block_tables, const int32_t* seq_lens, int P, int32_t* status,
                                 cudaStream_t stream, bool* done);
+cudaError_t launch_decode_scored(void* out, const void* q, const void* k, const void* v, const int32_t* block_tables,
+                                 int max_blocks, const int32_t* seq_lens, int B, int Hq, int Hkv, int D, int BS, int NB,
+                                 const ScoreArgs& sc, const GroupArgs& groups, pkv_dtype dtype, void* workspace, int P,
+                                 int32_t* status, cudaStream_t stream);
 bool scored_shape_valid(int B, int Hq, int Hkv, int D, int BS, int NB, int max_blocks, pkv_dtype dtype);
 
 constexpr int kPxRows = 128, kPxTiles = 2, kPxKeys = 64;
@@ -217,9 +221,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     int sum = 0, total, mine = 0;  // mine: key tiles of group tid
     PxWalk own;
     for (int g = N - 1 - (N - 1 - tid) % kPxThreads; g >= tid && g < N; g -= kPxThreads) {  // group tid comes last
-        const int s = pl.groups.start[g], e = pl.groups.start[g + 1];
-        own.set(pl, s, e, pl.groups.shared[g]);
-        wrong = wrong || s > e || s < 0 || e > pl.B || (g == 0 && s != 0);
+        own.set(pl, pl.groups.start[g], pl.groups.start[g + 1], pl.groups.shared[g]);
+        wrong = wrong || !group_valid(pl.groups, pl.B, g);
         mine = pl.Hkv * own.nt * own.rt;
         sum += mine;
     }
@@ -609,21 +612,22 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 }
 
 // ------------------------------------------------------------------ join
-// A warp a row: the pieces of its group's prefix, then those of what its sequence has of its own.
+// A row's pieces are those of its group's prefix, then those of what its sequence has of its own.  kUnit warps a row: one
+// where the rows fill the SMs, four where they are few.
 constexpr int kSjWarps = 4;
-constexpr int kSjGroup = 8;  // pieces in flight
+constexpr int kSjGroup = 4;  // pieces in flight, of a warp
+constexpr int kSjManyRows = 32;  // rows per SM from which one warp a row fills it
 
-template <int kD>
+template <int kD, int kUnit>
 __global__ void __launch_bounds__(kSjWarps * 32)
     shared_join_kernel(const __grid_constant__ PxPlan pl, const PxSpace px, const SplitSpace ws, const int R,
                        const int32_t* seq_lens, __nv_bfloat16* out, const int P, int32_t* status) {
-    const long long rows = static_cast<long long>(pl.B) * pl.Hq;
-    const long long row = min(static_cast<long long>(blockIdx.x) * kSjWarps + (threadIdx.x >> 5), rows - 1);
-    const int lane = threadIdx.x & 31;
+    constexpr int kRows = kSjWarps / kUnit, kCols = kD / 32;  // rows of a CTA, columns of a lane
+    __shared__ float part[kUnit > 1 ? kSjWarps : 1][32][kCols + 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % kUnit;
+    const long long rows = static_cast<long long>(pl.B) * pl.Hq, row0 = static_cast<long long>(blockIdx.x) * kRows + warp / kUnit;
+    const long long row = min(row0, rows - 1);
     const int b = static_cast<int>(row / pl.Hq), qh = static_cast<int>(row - static_cast<long long>(b) * pl.Hq);
-    constexpr int kCols = kD / 32;  // of a lane
-    float acc[kCols] = {};
-    float M = -INFINITY, l = 0.f;
     // What only the inputs say comes before the wait: they are older than the prefix kernel, which started this
     // chain after its own wait.
     const int L = seq_lens[b];
@@ -631,79 +635,126 @@ __global__ void __launch_bounds__(kSjWarps * 32)
     const int g = group_of(pl.groups, b);
     const int prefix = g < 0 ? 0 : group_prefix(pl.groups, pl.max_blocks, pl.BS, g);
     bad = bad || (L > 0 && (prefix < 0 || L < prefix));
+    // the row in its row tile
+    int first_seq = 0, rt = 0, tile = 0, qt = 0, r = 0;
+    const int h = qh / pl.G, grp = qh / R;
+    bool dual = false;
+    if (prefix > 0) {
+        first_seq = pl.groups.start[g];
+        const int n = pl.groups.start[g + 1] - first_seq, member = b - first_seq;
+        rt = (n + pl.TC - 1) / pl.TC;
+        tile = member / pl.TC;
+        const int in = member - tile * pl.TC;
+        qt = in / pl.TQ;
+        r = (in - qt * pl.TQ) * pl.G + qh - h * pl.G;
+        dual = n - tile * pl.TC <= pl.TQ;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const PxHead head = *px.head;
     const int2 plan = prefix > 0 ? px.plan[g] : make_int2(0, 0), info = ws.info[b];
     const int Wo = ws.head->W;
     bad = bad || head.valid == 0;
-    if (bad && lane == 0 && qh == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
+    if (bad && lane == 0 && qh == 0 && w0 == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
+    // pieces [0, np) lie in ranges pf .. of the prefix's key tiles (twice that many where dual), the others in ranges of
+    int np = 0, pf = 0, no = 0, of = 0;
     if (!bad && L > 0) {
-        auto take = [&](const float2* mls, const float* os, int pieces, auto place) {
-            for (int p0 = 0; p0 < pieces; p0 += kSjGroup) {
-                float2 ml[kSjGroup];
-                float o[kSjGroup][kCols];
-#pragma unroll
-                for (int k = 0; k < kSjGroup; ++k) {
-                    ml[k] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i) o[k][i] = 0.f;
-                    if (p0 + k < pieces) {
-                        const size_t at = place(p0 + k);
-                        ml[k] = __ldcg(mls + at);
-                        if constexpr (kCols == 4) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(os + at * kD) + lane);
-                            o[k][0] = v.x;
-                            o[k][1] = v.y;
-                            o[k][2] = v.z;
-                            o[k][3] = v.w;
-                        } else {
-                            const float2 v = __ldcg(reinterpret_cast<const float2*>(os + at * kD) + lane);
-                            o[k][0] = v.x;
-                            o[k][1] = v.y;
-                        }
-                    }
-                }
-                float mn = M;
-#pragma unroll
-                for (int k = 0; k < kSjGroup; ++k) mn = fmaxf(mn, ml[k].x);
-                const float mu = mn == -INFINITY ? 0.f : mn, fa = ex2_approx(M - mu);
-                l *= fa;
-#pragma unroll
-                for (int i = 0; i < kCols; ++i) acc[i] *= fa;
-                M = mn;
-#pragma unroll
-                for (int k = 0; k < kSjGroup; ++k) {
-                    const float f = ex2_approx(ml[k].x - mu);
-                    bad = bad || ml[k].y < 0.f;  // a piece that could not be read makes the row zero
-                    l = fmaf(ml[k].y, f, l);
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i) acc[i] = fmaf(o[k][i], f, acc[i]);
-                }
-            }
-        };
         if (prefix > 0) {
-            const int member = b - pl.groups.start[g], rt = (pl.groups.start[g + 1] - pl.groups.start[g] + pl.TC - 1) / pl.TC;
-            const int tile = member / pl.TC, in = member - tile * pl.TC, qt = in / pl.TQ, W = head.W;
-            const int h = qh / pl.G, r = (in - qt * pl.TQ) * pl.G + qh - h * pl.G;
-            const bool dual = pl.groups.start[g + 1] - pl.groups.start[g] - tile * pl.TC <= pl.TQ;
-            const int first = plan.x + (h * rt + tile) * plan.y, f = first / W, pieces = (first + plan.y - 1) / W - f + 1;
-            take(px.ml, px.o, dual ? 2 * pieces : pieces, [&](int x) {
-                const int p = dual ? x >> 1 : x, t = dual ? x & 1 : qt;
-                return pieces == 1 ? 2 * static_cast<size_t>(P) * kPxSlot +
-                                         (static_cast<size_t>(dual ? t : 0) * pl.B + b) * pl.Hq + qh
-                                   : (2 * static_cast<size_t>(f + p) + (p == 0 ? 1 : 0)) * kPxSlot + t * kPxRows + r;
-            });
+            const int first = plan.x + (h * rt + tile) * plan.y;
+            pf = first / head.W;
+            np = (first + plan.y - 1) / head.W - pf + 1;
         }
         if (info.y > 0) {
-            const int grp = qh / R;
-            const int first = info.x + grp * info.y, f = first / Wo, pieces = (first + info.y - 1) / Wo - f + 1;
-            take(ws.ml, ws.o, pieces, [&](int p) {
-                return pieces == 1 ? 2 * static_cast<size_t>(P) * R + row
-                                   : (2 * static_cast<size_t>(f + p) + (p == 0 ? 1 : 0)) * R + (qh - grp * R);
-            });
+            const int first = info.x + grp * info.y;
+            of = first / Wo;
+            no = (first + info.y - 1) / Wo - of + 1;
         }
     }
+    const int npx = dual ? 2 * np : np, n = npx + no;
+    float acc[kCols] = {};
+    float M = -INFINITY, l = 0.f;
+    for (int x0 = w0; x0 < n; x0 += kUnit * kSjGroup) {
+        float2 ml[kSjGroup];
+        float o[kSjGroup][kCols];
+#pragma unroll
+        for (int k = 0; k < kSjGroup; ++k) {
+            const int x = x0 + k * kUnit;
+            ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) o[k][i] = 0.f;
+            if (x < n) {
+                const float2* mls;
+                const float* os;
+                if (x < npx) {
+                    const int p = dual ? x >> 1 : x, t = dual ? x & 1 : qt;
+                    const size_t at = np == 1 ? 2 * static_cast<size_t>(P) * kPxSlot + (static_cast<size_t>(dual ? t : 0) * pl.B + b) * pl.Hq + qh
+                                              : (2 * static_cast<size_t>(pf + p) + (p == 0 ? 1 : 0)) * kPxSlot + t * kPxRows + r;
+                    mls = px.ml + at;
+                    os = px.o + at * kD;
+                } else {
+                    const int p = x - npx;
+                    const size_t at = no == 1 ? 2 * static_cast<size_t>(P) * R + row
+                                              : (2 * static_cast<size_t>(of + p) + (p == 0 ? 1 : 0)) * R + (qh - grp * R);
+                    mls = ws.ml + at;
+                    os = ws.o + at * kD;
+                }
+                ml[k] = __ldcg(mls);
+                if constexpr (kCols == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(os) + lane);
+                    o[k][0] = v.x;
+                    o[k][1] = v.y;
+                    o[k][2] = v.z;
+                    o[k][3] = v.w;
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2*>(os) + lane);
+                    o[k][0] = v.x;
+                    o[k][1] = v.y;
+                }
+            }
+        }
+        float mn = M;
+#pragma unroll
+        for (int k = 0; k < kSjGroup; ++k) mn = fmaxf(mn, ml[k].x);
+        const float mu = mn == -INFINITY ? 0.f : mn, fa = ex2_approx(M - mu);
+        l *= fa;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) acc[i] *= fa;
+        M = mn;
+#pragma unroll
+        for (int k = 0; k < kSjGroup; ++k) {
+            const float f = ex2_approx(ml[k].x - mu);
+            bad = bad || ml[k].y < 0.f;  // a piece that could not be read makes the row zero
+            l = fmaf(ml[k].y, f, l);
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) acc[i] = fmaf(o[k][i], f, acc[i]);
+        }
+    }
+    if constexpr (kUnit > 1) {
+        float* mine = part[warp][lane];
+        mine[0] = M;
+        mine[1] = bad ? -1.f : l;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) mine[2 + i] = acc[i];
+        __syncthreads();
+        if (w0 != 0) return;
+        float mn = M;
+#pragma unroll
+        for (int u = 1; u < kUnit; ++u) mn = fmaxf(mn, part[warp + u][lane][0]);
+        const float mu = mn == -INFINITY ? 0.f : mn, fa = ex2_approx(M - mu);
+        l *= fa;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) acc[i] *= fa;
+#pragma unroll
+        for (int u = 1; u < kUnit; ++u) {
+            const float* other = part[warp + u][lane];
+            const float f = ex2_approx(other[0] - mu);
+            bad = bad || other[1] < 0.f;
+            l = fmaf(other[1], f, l);
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) acc[i] = fmaf(other[2 + i], f, acc[i]);
+        }
+    }
+    if (row0 >= rows) return;
     const bool zero = bad || l == 0.f;
     const float inv = 1.f / l;
     __nv_bfloat16* to = out + row * kD + kCols * lane;
@@ -716,6 +767,12 @@ __global__ void __launch_bounds__(kSjWarps * 32)
 }
 
 // ------------------------------------------------------------------ host side
+// Bytes of cache (by the table's width, each sequence's own) up to which two kernels that read a prefix per sequence take
+// less time than three that read it once.  Per sequence against once: 8 groups of 8, prefix 86, 5 KV heads x 64
+// (10 MB) 7.1 : 16.0 us; 5 of 32, 60, 7 x 128 (37 MB) 14.5 : 28.7; 1 of 16, 1575, 6 x 64 (39 MB) 17.9 : 15.6; 2 of 7, 1782,
+// 5 x 128 (65 MB) 31.0 : 26.3; 5 of 17, 271, 8 x 128 (100 MB) 36.4 : 36.2; groups of one, 6533, 11 x 128 52 : 57.
+constexpr long long kPxReadPerSequence = 48LL << 20;
+
 bool encode_pool_k16(CUtensorMap* map, const void* pool, int NB, int Hkv, int BS);
 bool encode_pool_box_halves(CUtensorMap* map, const void* pool, int NB, int Hkv, int BS, int box_rows);
 
@@ -779,10 +836,12 @@ static cudaError_t launch_shared(const PxPlan& px, SplitPlan pl, void* out, cons
     err = launch_split_shared(pl, ws, q, k, v, block_tables, seq_lens, P, status, stream, &done);
     if (err != cudaSuccess || !done) return err != cudaSuccess ? err : cudaErrorInvalidValue;
     const long long n = static_cast<long long>(pl.B) * pl.Hq;
-    cfg.gridDim = dim3(static_cast<unsigned>((n + kSjWarps - 1) / kSjWarps), 1, 1);
+    const bool many = n >= kSjManyRows * P;
+    const int per = many ? kSjWarps : 1;  // rows of a CTA
+    cfg.gridDim = dim3(static_cast<unsigned>((n + per - 1) / per), 1, 1);
     cfg.blockDim = dim3(kSjWarps * 32, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    err = cudaLaunchKernelEx(&cfg, shared_join_kernel<kD>, px, pws, ws, pl.R, seq_lens, static_cast<__nv_bfloat16*>(out), P, status);
+    err = cudaLaunchKernelEx(&cfg, many ? shared_join_kernel<kD, 1> : shared_join_kernel<kD, kSjWarps>, px, pws, ws, pl.R, seq_lens, static_cast<__nv_bfloat16*>(out), P, status);
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
@@ -848,6 +907,14 @@ extern "C" pkv_status pkv_paged_decode_attention_shared(
     const int P = device_sm_count();
     if (workspace_bytes < pkv_decode_shared_workspace_bytes(B, Hq, Hkv, D, P > 0 ? P : 1)) return PKV_ERR_INVALID_ARG;
     if (P <= 0) return PKV_ERR_CUDA;
+    // Small batches, and such whose groups cannot have two members on average, are read per sequence
+    const long long width = static_cast<long long>(max_blocks_per_seq) * block_size;
+    if (B < 2 * N || 4LL * B * width * Hkv * D <= kPxReadPerSequence) {
+        const cudaError_t err = launch_decode_scored(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens, B, Hq,
+                                                     Hkv, D, block_size, num_blocks, sc, pl.groups, dtype, workspace, P,
+                                                     dev_status, static_cast<cudaStream_t>(stream));
+        return err == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    }
     const cudaError_t err = (D == 64 ? launch_shared<64> : launch_shared<128>)(
         px, pl, out, q, k_cache, v_cache, block_tables, seq_lens, workspace, P, dev_status, static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;

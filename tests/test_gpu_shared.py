@@ -23,8 +23,9 @@ def _cu(a):
     return torch.tensor(a, dtype=torch.int32, device="cuda")
 
 
-def make(seed, groups, Hq, Hkv, D, BS, dtype, q_size=1.5, loose=()):
-    """groups: (shared tokens, lengths) of each; loose: lengths of sequences behind the last group."""
+def make(seed, groups, Hq, Hkv, D, BS, dtype, q_size=1.5, loose=(), wide=True):
+    """groups: (shared tokens, lengths) of each; loose: lengths of sequences behind the last group; wide: a table so
+    wide that the call does not take the batch for a small one, whose prefixes it reads per sequence."""
     lens = [L for _, ls in groups for L in ls] + list(loose)
     x = R.make(seed, lens, Hq, Hkv, D, BS, dtype, q_size=q_size)
     start, at = [0], 0
@@ -36,6 +37,10 @@ def make(seed, groups, Hq, Hkv, D, BS, dtype, q_size=1.5, loose=()):
         at += len(ls)
         start.append(at)
     x["group_start"], x["shared_lens"] = _cu(start), _cu([s for s, _ in groups])
+    if wide:
+        B, width = x["block_tables"].shape
+        more = max(0, (48 << 20) // (4 * B * BS * Hkv * D) + 1 - width)
+        x["block_tables"] = torch.cat([x["block_tables"], torch.full((B, more), -1, dtype=torch.int32, device="cuda")], 1)
     return x
 
 
@@ -54,12 +59,13 @@ GROUPS = [
 ]
 
 
+@pytest.mark.parametrize("wide", [True, False])
 @pytest.mark.parametrize("groups", range(len(GROUPS)))
 @pytest.mark.parametrize("dtype,Hq,Hkv,D,BS", [
     (BF, 32, 8, 128, 16), (BF, 8, 2, 64, 16), (BF, 21, 3, 128, 32), (BF, 12, 12, 64, 48), (BF, 32, 2, 128, 64),
     (BF, 40, 1, 64, 16), (BF, 1, 1, 128, 16), (BF, 120, 1, 128, 16), (BF, 200, 2, 64, 16)])
-def test_groups(dtype, Hq, Hkv, D, BS, groups):
-    x = make(groups, GROUPS[groups], Hq, Hkv, D, BS, dtype, loose=(20, 0))
+def test_groups(dtype, Hq, Hkv, D, BS, groups, wide):
+    x = make(groups, GROUPS[groups], Hq, Hkv, D, BS, dtype, loose=(20, 0), wide=wide)
     st = pkv.new_status()
     got = call(x, status=st)
     ref, tol = R.reference(x)
@@ -90,9 +96,10 @@ def test_no_groups():
     R.check(call(x), *R.reference(x))
 
 
-def test_bad_members_tables_and_groups():
+@pytest.mark.parametrize("wide", [True, False])
+def test_bad_members_tables_and_groups(wide):
     groups = [(64, [64, 30, 100, 0]), (32, [60, 60])]
-    x = make(8, groups, 8, 2, 128, 16, BF)
+    x = make(8, groups, 8, 2, 128, 16, BF, wide=wide)
     ref, tol = R.reference(x)
     st = pkv.new_status()
     got = call(x, status=st)  # sequence 1 is shorter than its group's prefix; the empty one is no error
@@ -100,21 +107,21 @@ def test_bad_members_tables_and_groups():
     assert (got[1] == 0).all() and (got[3] == 0).all()
     R.check(got, ref, tol, [0, 2, 3, 4, 5])
     x["seq_lens"][1] = 0
-    for where, rows in (((0, 1), [3, 4, 5]), ((2, 5), [0, 3, 4, 5]), ((4, 0), [0, 2, 3])):
+    # a block of a prefix (in the tables of all its members), of one sequence
+    for members, entry, bad in (([0, 1, 2, 3], 1, [0, 2]), ([2], 5, [2]), ([4, 5], 0, [4, 5])):
         y = dict(x, block_tables=x["block_tables"].clone())
-        y["block_tables"][where] = 10 ** 6
+        y["block_tables"][members, entry] = 10 ** 6
         st = pkv.new_status()
         got = call(y, status=st)
         assert pkv.check_status(st) == 4
-        bad = {(0, 1): [0, 2], (2, 5): [2], (4, 0): [4, 5]}[where]
         assert (got[bad] == 0).all()
-        R.check(got, ref, tol, rows)
+        R.check(got, ref, tol, [i for i in range(6) if i not in bad and i != 1])
     for start in ([0, 5, 4], [1, 4, 6], [0, 4, 7], [0, -1, 6]):
         st = pkv.new_status()
         got = call(dict(x, group_start=_cu(start)), status=st)
         assert pkv.check_status(st) == 4, start
         assert (got == 0).all(), start
-    for shared in ([-16, 32], [64, 10 ** 6]):
+    for shared in ([-16, 32], [64, 2 ** 31 - 1]):
         st = pkv.new_status()
         got = call(dict(x, shared_lens=_cu(shared)), status=st)
         assert pkv.check_status(st) == 4
