@@ -42,9 +42,9 @@
 //    which case the row of O in TMEM and the running sum are rescaled first;
 //    P (bf16, values at most 2^8) goes to shared memory for the PV MMA, and
 //    the sum accumulates the fp32 values.  Rows past the chunk are
-//    computed on zero queries and not stored.  The V rows of keys at or past
-//    the sequence length (which may hold anything, NaN included) are cleared
-//    before the last PV MMAs.
+//    computed on zero queries and not stored.  The V rows of the last tile's
+//    keys past the CTA's last position (which may hold anything, NaN included)
+//    are cleared before the last PV MMAs.
 //  * Epilogue: O / sum from TMEM to the bf16 output rows.
 // Every mbarrier wait is bounded; a CTA that gives up records PKV_ERR_TIMEOUT,
 // waits (bounded) for its own TMA copies, and still frees its TMEM.
@@ -532,9 +532,10 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                     tc_st32(tq + lrow + 128 + 32 * cc, o);
                 }
             }
-            // the V rows of keys at or past L may hold anything: clear them (scored: those of every key no row sees)
+            // the V rows of keys past the CTA's last one (not in the cache yet, past L, or another block's) may hold
+            // anything: clear them (scored: those of every key that no row sees)
             if (qt == 0 && (kScored ? kbase + kTcKeys - 1 > plast || (kbase < wlo && kbase + kTcKeys > pfx) : kt == ntiles - 1)) {
-                const int rlo = kScored ? 0 : max(0, min(kTcKeys, L - kbase));
+                const int rlo = kScored ? 0 : plast + 1 - kbase;
                 uint8_t* vb = sKV + static_cast<size_t>(j % kTcStages) * kTcStageBytes + kTcKBytes;
                 for (int idx = r; idx < (kTcKeys - rlo) * 16; idx += kTcRows) {
                     const int rr = rlo + (idx >> 4), half = (idx >> 3) & 1, ch = idx & 7;

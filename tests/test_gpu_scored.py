@@ -203,6 +203,17 @@ def test_prefill_bad_tables_and_rows_behind_the_last():
     assert (got[80:120] == 0).all() and (got[120:] == 7).all()
 
 
+@pytest.mark.parametrize("before", [0, 10, 40])
+def test_plain_prefill_reads_no_other_block(before):
+    """Tiles end behind the last position that their CTA needs; block 0, which no sequence holds, is NaN."""
+    x = R.make(8, [before + 300], 32, 8, 128, 16, BF, chunks=[300])
+    for name in ("k_cache", "v_cache"):
+        x[name] = torch.cat([torch.full_like(x[name][:1], float("nan")), x[name]])
+    x["block_tables"] += 1
+    got = pkv.paged_prefill_attention(x["q"], x["k_cache"], x["v_cache"], x["block_tables"], x["seq_lens"], x["q_start"])
+    R.check(got, *R.reference(x))
+
+
 # ------------------------------------------------------------------ as a program uses them
 def test_prefill_workspace():
     x = R.make(6, [900], 8, 2, 128, 16, BF, chunks=[20])
