@@ -19,11 +19,10 @@
 // mma.sync and not tcgen05: one query per sequence gives a group 1 to 16 rows of work per cached byte pair, far
 // below what the tensor pipe needs to matter, and a 128-row tile would be empty rows.
 //
-// Generic kernel (other shapes): one CTA per (sequence, KV head, up to 8 of its query heads, share of the visible
-// positions).  Tiles of 32 visible positions come to shared memory as float32; warp w takes the 32
-// scores of query head w (a lane a position) and their running maximum and sum, then a thread takes
-// four dimensions of one head's output.  Positions that the mask hides are never loaded.  The shares'
-// results are joined by a second kernel.
+// Generic kernel (float32, other shapes): one CTA per (sequence, KV head, up to 8 of its query heads, share of the visible
+// positions).  Tiles of 32 visible positions come to shared memory as float32; warp w takes the scores of two query
+// heads (a lane a position) and their running maxima and sums, then a thread takes four dimensions of two heads'
+// outputs.  Positions that the mask hides are never loaded.  The shares' results are joined by a second kernel.
 //
 // No input is read through the read-only path (__ldg, const __restrict__): these kernels start while their
 // predecessor still writes what they read after griddepcontrol.wait.
@@ -810,9 +809,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
 }
 
 // ------------------------------------------------------------------ generic kernel
-constexpr int kGenThreads = 256;
+constexpr int kGenThreads = 128;
 constexpr int kGenPos = 32;    // positions a tile
-constexpr int kGenHeads = 8;   // query heads a CTA
+constexpr int kGenHeads = 8;   // query heads a CTA, two a warp
 constexpr int kGenShares = 64;  // at most
 
 struct GenericPlan {
@@ -827,19 +826,27 @@ static int generic_stride(int D) {
     const int quads = (D + 3) / 4;
     return 4 * (quads | 1);
 }
+// float32 rows of whole 16 bytes are copied as they are, a tile ahead; other rows are converted on their way.
+template <typename T, bool kVec>
+constexpr bool kGenAhead = kVec && sizeof(T) == 4;
 
+// Bound by shared-memory reads: a position's K and V row are read once for two heads, 12 bytes of shared memory a byte of
+// cache with 8 heads, so about 40% of the copy rate where there is much to read; short batches by their chain of
+// lengths, block ids, rows and the join.  37 sequences of up to 1500 (window 300), 21 and 3 heads of 80 in float32:
+// GENERIC_US us for 20 MB.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kGenThreads)
     decode_scored_generic_kernel(const __grid_constant__ GenericPlan pl, T* out, const T* q, const T* k_cache,
                                  const T* v_cache, const int32_t* block_tables, const int32_t* seq_lens, float* part,
                                  int32_t* status) {
+    constexpr bool kAhead = kGenAhead<T, kVec>;
     extern __shared__ __align__(16) float gen_smem[];
-    __shared__ float ps[kGenHeads][kGenPos], factor[kGenHeads];
+    __shared__ __align__(16) float ps[kGenHeads][kGenPos];
+    __shared__ float factor[kGenHeads], ends[kGenHeads][2];
     __shared__ long long rows[2][kGenPos];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, D = pl.D, DS = pl.stride;
-    float* ks = gen_smem;
-    float* vs = ks + kGenPos * DS;
-    float* qs = vs + kGenPos * DS;
+    const int tile_floats = 2 * kGenPos * DS;  // K rows, V rows
+    float* qs = gen_smem + (kAhead ? 2 : 1) * tile_floats;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     unsigned u = blockIdx.x;
@@ -854,137 +861,223 @@ __global__ void __launch_bounds__(kGenThreads)
     bool bad = L < 0 || static_cast<long long>(L) > static_cast<long long>(pl.max_blocks) * pl.BS;
     const Seen seen = decode_seen(pl.sc, b, bad ? 0 : L);
     const int visible = seen.pfx + seen.L - seen.lo, tiles = (visible + kGenPos - 1) / kGenPos;
-    const int per = (tiles + pl.shares - 1) / pl.shares, t0 = share * per, t1 = min(tiles, t0 + per);
+    const int per = (tiles + pl.shares - 1) / pl.shares, t0 = min(tiles, share * per), t1 = min(tiles, t0 + per);
+    bool miss = false;
+    auto position = [&](int i) { return i < seen.pfx ? i : seen.lo + (i - seen.pfx); };
+    // warp 0: the block of its lane's position in tile t, asked for early; and the rows of the tile's positions
+    auto ask = [&](int t) {
+        const int i = t * kGenPos + lane;
+        return t < t1 && i < visible ? block_tables[static_cast<size_t>(b) * pl.max_blocks + position(i) / pl.BS] : -1;
+    };
+    auto locate = [&](int t, int blk) {
+        const int i = t * kGenPos + lane;
+        long long row = -1;
+        if (i < visible) {
+            if (blk < 0 || blk >= pl.NB) miss = true;
+            else row = (static_cast<long long>(blk) * pl.Hkv + h) * pl.BS + position(i) % pl.BS;
+        }
+        rows[t & 1][lane] = row;
+    };
+    int blk = -1;
+    // Tile t to its place; rows that are not there, or behind the last, are left out.
+    auto fetch = [&](int t) {
+        float* to = gen_smem + (kAhead ? (t & 1) * tile_floats : 0);
+        const int n = min(kGenPos, visible - t * kGenPos);
+        if constexpr (kVec) {
+            constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+            const int vecs = D / kPer;
+            int p = tid / vecs, c = tid - p * vecs;
+            const int dp = kGenThreads / vecs, dc = kGenThreads - dp * vecs;
+            while (p < 2 * n) {
+                const int which = p >= n, x = p - which * n;
+                const long long row = rows[t & 1][x];
+                if (row >= 0) {
+                    const T* from = (which ? v_cache : k_cache) + row * D + c * kPer;
+                    float* at = to + (which * kGenPos + x) * DS + c * kPer;
+                    if constexpr (kAhead) {
+                        split_cp16(at, from);
+                    } else {
+                        const uint4 z = *reinterpret_cast<const uint4*>(from);
+                        reinterpret_cast<float4*>(at)[0] = make_float4(bf16_lo(z.x), bf16_hi(z.x), bf16_lo(z.y), bf16_hi(z.y));
+                        reinterpret_cast<float4*>(at)[1] = make_float4(bf16_lo(z.z), bf16_hi(z.z), bf16_lo(z.w), bf16_hi(z.w));
+                    }
+                }
+                p += dp;
+                c += dc;
+                if (c >= vecs) {
+                    c -= vecs;
+                    ++p;
+                }
+            }
+        } else {
+            for (int p = warp; p < n; p += kGenThreads / 32) {
+                const long long row = rows[t & 1][p];
+                if (row < 0) continue;
+                const T *kr = k_cache + row * D, *vr = v_cache + row * D;
+                for (int d = lane; d < D; d += 32) {
+                    to[p * DS + d] = to_f32(kr[d]);
+                    to[(kGenPos + p) * DS + d] = to_f32(vr[d]);
+                }
+            }
+        }
+        if constexpr (kAhead) asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (warp == 0) {
+        const int blk0 = ask(t0), blk1 = ask(t0 + 1);
+        blk = ask(t0 + 2);
+        if (t0 < t1) locate(t0, blk0);
+        if (t0 + 1 < t1) locate(t0 + 1, blk1);
+    }
     // the dimensions between D and the next multiple of 4 are zeros
     for (int e = tid; e < kGenHeads * DS; e += kGenThreads) {
         const int hd = e / DS, d = e - hd * DS;
         qs[e] = hd < nh && d < D ? to_f32(q[(row0 + hd) * D + d]) : 0.f;
     }
     if ((D & 3) != 0)
-        for (int e = tid; e < 2 * kGenPos * DS; e += kGenThreads) ks[e] = 0.f;
-    bool miss = false;
-    auto locate = [&](int t) {  // warp 0: the rows of tile t's positions
-        const int i = t * kGenPos + lane;
-        long long row = -1;
-        if (i < visible) {
-            const int pos = i < seen.pfx ? i : seen.lo + (i - seen.pfx);
-            const int blk = block_tables[static_cast<size_t>(b) * pl.max_blocks + pos / pl.BS];
-            if (blk < 0 || blk >= pl.NB) miss = true;
-            else row = (static_cast<long long>(blk) * pl.Hkv + h) * pl.BS + pos % pl.BS;
-        }
-        rows[t & 1][lane] = row;
-    };
+        for (int e = tid; e < tile_floats; e += kGenThreads) gen_smem[e] = 0.f;
+    bad = __syncthreads_or(miss) != 0 || bad;
+    if constexpr (kAhead)
+        if (!bad && t0 < t1) fetch(t0);
     const int quads = (D + 3) / 4;
-    float m = -INFINITY, l = 0.f;  // of head `warp`
-    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-    const float slope = pl.sc.slopes != nullptr && warp < nh
-                            ? pl.sc.slopes[h * pl.G + chunk * kGenHeads + warp] * kLog2e : 0.f;
-    if (warp == 0 && t0 < t1) locate(t0);
-    for (int t = t0; t < t1; ++t) {
-        bad = __syncthreads_or(miss) != 0;  // the rows are there, the last tile is used
-        if (bad) break;
-        if (warp == 0 && t + 1 < t1) locate(t + 1);
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of heads 2 warp, 2 warp + 1
+    float4 acc[2][2];  // [quad tid % .. of this thread][head of the pair]
+#pragma unroll
+    for (int a = 0; a < 2; ++a) acc[a][0] = acc[a][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    float slope[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+        slope[e] = pl.sc.slopes != nullptr && 2 * warp + e < nh
+                       ? pl.sc.slopes[h * pl.G + chunk * kGenHeads + 2 * warp + e] * kLog2e : 0.f;
+    for (int t = t0; t < t1 && !bad; ++t) {
         const int n = min(kGenPos, visible - t * kGenPos);
-        if constexpr (kVec) {
-            constexpr int kPer = 16 / static_cast<int>(sizeof(T));
-            const int vecs = D / kPer;
-            for (int e = tid; e < 2 * n * vecs; e += kGenThreads) {
-                const int which = e >= n * vecs, x = e - which * n * vecs, p = x / vecs, c = x - p * vecs;
-                const uint4 z = *reinterpret_cast<const uint4*>((which ? v_cache : k_cache) + rows[t & 1][p] * D + c * kPer);
-                float4* to = reinterpret_cast<float4*>((which ? vs : ks) + p * DS + c * kPer);
-                if constexpr (sizeof(T) == 4) {
-                    to[0] = make_float4(__uint_as_float(z.x), __uint_as_float(z.y), __uint_as_float(z.z), __uint_as_float(z.w));
-                } else {
-                    to[0] = make_float4(bf16_lo(z.x), bf16_hi(z.x), bf16_lo(z.y), bf16_hi(z.y));
-                    to[1] = make_float4(bf16_lo(z.z), bf16_hi(z.z), bf16_lo(z.w), bf16_hi(z.w));
-                }
+        const float* ks = gen_smem + (kAhead ? (t & 1) * tile_floats : 0);
+        const float* vs = ks + kGenPos * DS;
+        if constexpr (kAhead) {
+            if (t + 1 < t1) {
+                fetch(t + 1);
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
             }
         } else {
-            for (int p = warp; p < n; p += kGenThreads / 32) {
-                const T *kr = k_cache + rows[t & 1][p] * D, *vr = v_cache + rows[t & 1][p] * D;
-                for (int d = lane; d < D; d += 32) {
-                    ks[p * DS + d] = to_f32(kr[d]);
-                    vs[p * DS + d] = to_f32(vr[d]);
-                }
-            }
+            fetch(t);
         }
-        __syncthreads();
-        if (warp < nh) {
-            float x = -INFINITY;
+        __syncthreads();  // the tile is there; the rows of tile t are used
+        if (warp == 0 && t + 2 < t1) {
+            locate(t + 2, blk);
+            blk = ask(t + 3);
+        }
+        if (2 * warp < nh) {
+            float x[2] = {-INFINITY, -INFINITY};
             if (lane < n) {
-                const int i = t * kGenPos + lane, pos = i < seen.pfx ? i : seen.lo + (i - seen.pfx);
                 const float4 *kr = reinterpret_cast<const float4*>(ks + lane * DS),
-                             *qr = reinterpret_cast<const float4*>(qs + warp * DS);
-                float s0 = 0.f, s1 = 0.f;
+                             *q0 = reinterpret_cast<const float4*>(qs + 2 * warp * DS),
+                             *q1 = reinterpret_cast<const float4*>(qs + (2 * warp + 1) * DS);
+                float s[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll 4
                 for (int c = 0; c < quads; ++c) {
-                    const float4 a = kr[c], w = qr[c];
-                    s0 = fmaf(a.x, w.x, fmaf(a.y, w.y, s0));
-                    s1 = fmaf(a.z, w.z, fmaf(a.w, w.w, s1));
+                    const float4 a = kr[c], w0 = q0[c], w1 = q1[c];
+                    s[0][0] = fmaf(a.x, w0.x, fmaf(a.y, w0.y, s[0][0]));
+                    s[0][1] = fmaf(a.z, w0.z, fmaf(a.w, w0.w, s[0][1]));
+                    s[1][0] = fmaf(a.x, w1.x, fmaf(a.y, w1.y, s[1][0]));
+                    s[1][1] = fmaf(a.z, w1.z, fmaf(a.w, w1.w, s[1][1]));
                 }
-                x = s0 + s1;
-                x = pl.sc.cap_log2 > 0.f ? pl.sc.cap_log2 * tanhf(x * pl.sc.in) : x * pl.sc.mul;
-                x = fmaf(slope, static_cast<float>(pos - (L - 1)), x);
+                const float away = static_cast<float>(position(t * kGenPos + lane) - (L - 1));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    x[e] = s[e][0] + s[e][1];
+                    x[e] = pl.sc.cap_log2 > 0.f ? pl.sc.cap_log2 * tanhf(x[e] * pl.sc.in) : x[e] * pl.sc.mul;
+                    x[e] = fmaf(slope[e], away, x[e]);
+                }
             }
-            float mx = x;
+            float mx[2] = {x[0], x[1]};
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
-            const float p = lane < n ? exp2f(x - mu) : 0.f, f = exp2f(m - mu);
-            float sum = p;
+            for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            l = fmaf(l, f, sum);
-            m = mn;
-            ps[warp][lane] = p;
-            if (lane == 0) factor[warp] = f;
+                for (int e = 0; e < 2; ++e) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], o));
+            float w[2], sum[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float mn = fmaxf(m[e], mx[e]), mu = mn == -INFINITY ? 0.f : mn, f = exp2f(m[e] - mu);
+                w[e] = lane < n ? exp2f(x[e] - mu) : 0.f;
+                sum[e] = w[e];
+                l[e] *= f;
+                m[e] = mn;
+                ps[2 * warp + e][lane] = w[e];
+                if (lane == 0) factor[2 * warp + e] = f;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], o);
+            l[0] += sum[0];
+            l[1] += sum[1];
         }
         __syncthreads();
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-            const int x = tid + a * kGenThreads, hd = x / quads, c = x - hd * quads;
-            if (hd >= nh) continue;
-            const float f = factor[hd];
-            float4 o = make_float4(acc[a].x * f, acc[a].y * f, acc[a].z * f, acc[a].w * f);
+            const int x = tid + a * kGenThreads, hp = x / quads, c = x - hp * quads;  // a pair of heads, four dimensions
+            if (2 * hp >= nh) continue;
+            const float f0 = factor[2 * hp], f1 = factor[2 * hp + 1];
+            float4 o0 = acc[a][0], o1 = acc[a][1];
+            o0 = make_float4(o0.x * f0, o0.y * f0, o0.z * f0, o0.w * f0);
+            o1 = make_float4(o1.x * f1, o1.y * f1, o1.z * f1, o1.w * f1);
             const float* v = vs + 4 * c;
-            for (int p = 0; p < n; ++p) {
-                const float w = ps[hd][p];
+            auto take = [&](int p, float w0, float w1) {
                 const float4 z = *reinterpret_cast<const float4*>(v + p * DS);
-                o.x = fmaf(w, z.x, o.x);
-                o.y = fmaf(w, z.y, o.y);
-                o.z = fmaf(w, z.z, o.z);
-                o.w = fmaf(w, z.w, o.w);
+                o0 = make_float4(fmaf(w0, z.x, o0.x), fmaf(w0, z.y, o0.y), fmaf(w0, z.z, o0.z), fmaf(w0, z.w, o0.w));
+                o1 = make_float4(fmaf(w1, z.x, o1.x), fmaf(w1, z.y, o1.y), fmaf(w1, z.z, o1.z), fmaf(w1, z.w, o1.w));
+            };
+            int p = 0;
+            for (; p + 4 <= n; p += 4) {
+                const float4 w0 = *reinterpret_cast<const float4*>(&ps[2 * hp][p]), w1 = *reinterpret_cast<const float4*>(&ps[2 * hp + 1][p]);
+                take(p, w0.x, w1.x);
+                take(p + 1, w0.y, w1.y);
+                take(p + 2, w0.z, w1.z);
+                take(p + 3, w0.w, w1.w);
             }
-            acc[a] = o;
+            for (; p < n; ++p) take(p, ps[2 * hp][p], ps[2 * hp + 1][p]);
+            acc[a][0] = o0;
+            acc[a][1] = o1;
         }
+        bad = __syncthreads_or(miss) != 0;  // of tile t + 2; this one's rows, weights and factors are used
     }
+    if constexpr (kAhead) asm volatile("cp.async.wait_all;" ::: "memory");
     if (bad && tid == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
-    __syncthreads();
-    if (warp < nh && lane == 0) {
-        ps[warp][0] = m;
-        ps[warp][1] = bad ? -1.f : l;  // a share that cannot be read makes the row zero
+    if (lane == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            ends[2 * warp + e][0] = m[e];
+            ends[2 * warp + e][1] = bad ? -1.f : l[e];  // a share that cannot be read makes the row zero
+        }
     }
     __syncthreads();
     // a share's row: maximum, sum, D sums of products
     const int DR = 2 + 4 * quads;
 #pragma unroll
     for (int a = 0; a < 2; ++a) {
-        const int x = tid + a * kGenThreads, hd = x / quads, c = x - hd * quads;
-        if (hd >= nh) continue;
-        const float o[4] = {acc[a].x, acc[a].y, acc[a].z, acc[a].w};
-        const float sum = ps[hd][1];
-        if (pl.shares == 1) {
-            const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-            for (int i = 0; i < 4; ++i)
-                if (4 * c + i < D) out[(row0 + hd) * D + 4 * c + i] = from_f32<T>(sum > 0.f || sum != sum ? o[i] * inv : 0.f);
-        } else {
-            float* to = part + ((row0 + hd) * pl.shares + share) * DR;
-            if (c == 0) *reinterpret_cast<float2*>(to) = make_float2(ps[hd][0], sum);
-            for (int i = 0; i < 2; ++i) *reinterpret_cast<float2*>(to + 2 + 4 * c + 2 * i) = make_float2(o[2 * i], o[2 * i + 1]);
+        const int x = tid + a * kGenThreads, hp = x / quads, c = x - hp * quads;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int hd = 2 * hp + e;
+            if (hd >= nh) continue;
+            const float o[4] = {acc[a][e].x, acc[a][e].y, acc[a][e].z, acc[a][e].w};
+            const float sum = ends[hd][1];
+            if (pl.shares == 1) {
+                const bool some = sum > 0.f || sum != sum;
+                const float inv = 1.f / sum;
+                for (int i = 0; i < 4; ++i)
+                    if (4 * c + i < D) out[(row0 + hd) * D + 4 * c + i] = from_f32<T>(some ? o[i] * inv : 0.f);
+            } else {
+                float* to = part + ((row0 + hd) * pl.shares + share) * DR;
+                if (c == 0) *reinterpret_cast<float2*>(to) = make_float2(ends[hd][0], sum);
+                for (int i = 0; i < 2; ++i) *reinterpret_cast<float2*>(to + 2 + 4 * c + 2 * i) = make_float2(o[2 * i], o[2 * i + 1]);
+            }
         }
     }
 }
 
-// out = sum o_s 2^(m_s - M) / sum l_s 2^(m_s - M) over a row's shares; a warp a row.
+// out = sum o_s 2^(m_s - M) / sum l_s 2^(m_s - M) over a row's shares (at most 64); a warp a row.
 template <typename T>
 __global__ void __launch_bounds__(128)
     decode_scored_shares_kernel(T* out, const float* part, long long nrows, int shares, int D) {
@@ -995,35 +1088,48 @@ __global__ void __launch_bounds__(128)
     if (row >= nrows) return;
     const int DR = 2 + (D + 3) / 4 * 4;
     const float* p = part + row * shares * DR;
-    float M = -INFINITY, l = 0.f, acc[8] = {};
-    bool bad = false;
-    for (int s = 0; s < shares; ++s) M = fmaxf(M, __ldcg(p + s * DR));
-    const float mu = M == -INFINITY ? 0.f : M;
+    float2 ml[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        ml[k] = lane + 32 * k < shares ? __ldcg(reinterpret_cast<const float2*>(p + (lane + 32 * k) * DR)) : make_float2(-INFINITY, 0.f);
+    float M = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float mu = M == -INFINITY ? 0.f : M, f0 = exp2f(ml[0].x - mu), f1 = exp2f(ml[1].x - mu);
+    const bool bad = __any_sync(0xffffffffu, ml[0].y < 0.f || ml[1].y < 0.f);
+    float l = ml[0].y * f0 + ml[1].y * f1, acc[8] = {};
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll 4
     for (int s = 0; s < shares; ++s) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + s * DR));
-        const float w = exp2f(ml.x - mu);
-        bad = bad || ml.y < 0.f;
-        l = fmaf(ml.y, w, l);
+        const float w = __shfl_sync(0xffffffffu, s < 32 ? f0 : f1, s & 31);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (lane + 32 * i < D) acc[i] = fmaf(__ldcg(p + s * DR + 2 + lane + 32 * i), w, acc[i]);
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const float inv = 1.f / l;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (lane + 32 * i < D) out[row * D + lane + 32 * i] = from_f32<T>(bad || l == 0.f ? 0.f : acc[i] * inv);
 }
 
-// CTAs along the positions: four per SM in all where the batch has fewer, and not more than the longest
-// sequence (by the table's width, or the window) has tiles.
-static int generic_shares(long long units, int longest, int P) {
-    const long long want = (4LL * P + units - 1) / units, tiles = (static_cast<long long>(longest) + kGenPos - 1) / kGenPos;
-    return static_cast<int>(std::max(1LL, std::min({want, tiles, static_cast<long long>(kGenShares)})));
+static size_t generic_smem(int D, bool ahead) {
+    return ((ahead ? 4 : 2) * kGenPos + kGenHeads) * static_cast<size_t>(generic_stride(D)) * sizeof(float);
+}
+// CTAs along the positions: as many as an SM holds at once (37 sequences of up to 1500 in float32: 17.5 us, twice as many
+// 22.0); where that leaves shares of more than 12 tiles, up to four times as many, which evens out lengths (16 sequences
+// of 512-4096, 8 x 128 in float32: 140 for 170 us); and not more than the longest sequence (by the table's width, or the
+// window) has tiles.
+static int generic_shares(long long units, int D, bool ahead, int longest, int P) {
+    const long long held = std::min<long long>(12, 225 * 1024 / (generic_smem(D, ahead) + 3 * 1024));
+    const long long tiles = (static_cast<long long>(longest) + kGenPos - 1) / kGenPos;
+    const long long once = held * P / units, more = std::min(4 * held * P / units, tiles / 12);
+    return static_cast<int>(std::max(1LL, std::min({std::max(once, more), tiles, static_cast<long long>(kGenShares)})));
 }
 
 static size_t generic_workspace(int B, int Hq, int Hkv, int D, int P) {
     const long long units = static_cast<long long>(B) * Hkv * ((Hq / Hkv + kGenHeads - 1) / kGenHeads);
-    const int shares = generic_shares(std::max(1LL, units), 0x7fffffff, P);
+    const int shares = generic_shares(std::max(1LL, units), D, false, 0x7fffffff, P);  // (ahead holds fewer)
     return shares == 1 ? 0 : static_cast<size_t>(B) * Hq * shares * (2 + (D + 3) / 4 * 4) * sizeof(float);
 }
 
@@ -1038,11 +1144,12 @@ static cudaError_t launch_generic(GenericPlan pl, void* out, const void* q, cons
     const long long units = static_cast<long long>(pl.B) * pl.Hkv * pl.chunks;
     const long long width = std::min(static_cast<long long>(pl.max_blocks) * pl.BS, 0x7fffffffLL);
     const bool windowed = pl.sc.window > 0 && pl.sc.prefix_lens == nullptr;
-    pl.shares = generic_shares(units, static_cast<int>(windowed ? std::min<long long>(width, pl.sc.window) : width), P);
-    const size_t smem = (2 * kGenPos + kGenHeads) * static_cast<size_t>(pl.stride) * sizeof(float);
+    const bool ahead = sizeof(T) == 4 && vec;
+    pl.shares = generic_shares(units, pl.D, ahead, static_cast<int>(windowed ? std::min<long long>(width, pl.sc.window) : width), P);
+    const size_t smem = generic_smem(pl.D, ahead);
     auto kern = vec ? decode_scored_generic_kernel<T, true> : decode_scored_generic_kernel<T, false>;
     // the limit belongs to the kernel, not to the call: always the same value
-    constexpr int kMost = (2 * kGenPos + kGenHeads) * (256 + 4) * 4;
+    constexpr int kMost = (4 * kGenPos + kGenHeads) * (256 + 4) * 4;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
