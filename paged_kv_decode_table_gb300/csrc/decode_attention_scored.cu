@@ -764,7 +764,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (pl.R + kJoinWarps - 1) / kJoinWarps, c = 1 + static_cast<int>(blockIdx.x) / per;
-    const SplitCut cut = ws.cuts[c];
+    const int4 c4 = __ldcg(reinterpret_cast<const int4*>(ws.cuts + c));
+    const SplitCut cut{c4.x, c4.y, c4.z, c4.w};
     const int row = (static_cast<int>(blockIdx.x) - (c - 1) * per) * kJoinWarps + warp;
     if (cut.pieces == 0 || row >= min(pl.R, pl.Hq - cut.g * pl.R)) return;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -412,6 +412,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     if (!fail) tc_commit(&sm->kv_empty[s]);
                 }
             }
+            // no arrival of this CTA may be outstanding when it exits: the last one follows all others
+            if (!fail && !mbar_wait(&sm->kv_empty[(j - 1) % kStages], ((j - 1) / kStages) & 1)) fail = true;
             if (fail) report(status, PKV_ERR_TIMEOUT);
         }
         __syncwarp();
@@ -651,9 +653,10 @@ __global__ void __launch_bounds__(kSjWarps * 32)
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const PxHead head = *px.head;
-    const int2 plan = prefix > 0 ? px.plan[g] : make_int2(0, 0), info = ws.info[b];
-    const int Wo = ws.head->W;
+    const int2 h2 = __ldcg(reinterpret_cast<const int2*>(px.head));
+    const PxHead head{h2.x, h2.y};
+    const int2 plan = prefix > 0 ? __ldcg(px.plan + g) : make_int2(0, 0), info = __ldcg(ws.info + b);
+    const int Wo = __ldcg(&ws.head->W);
     bad = bad || head.valid == 0;
     if (bad && lane == 0 && qh == 0 && w0 == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
     // pieces [0, np) lie in ranges pf .. of the prefix's key tiles (twice that many where dual), the others in ranges of
