@@ -141,6 +141,9 @@ struct TcSplit {
     float* o;
 };
 
+// With changed scores the softmax warps bound it: 16 chunks of up to 512 behind 512-4096 (32 and 8 heads) take 272 us plain, 298
+// with masks to look at, 405 with every score capped (eight FMAs a score and no pipe to hide them behind); 4 of up to 2048
+// behind 16384-32768 that see 1024 + 100 positions, with slopes, 441 (109 at the measured bf16 rate).
 // kKind: kPlain, or kMasked (the masks of attention_scores.cuh) with kCapped and kSloped where its scores are.
 template <int kKind>
 __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThreads, 1)
@@ -689,7 +692,9 @@ bool prefill_tc_supported(int Hq, int Hkv, int D, int BS, const void* q, const v
 
 // CTAs along the keys: as many as fill the SMs once, where the pairs of query tiles are fewer.
 constexpr int kTcShares = 64;     // at most
-constexpr int kTcShareTiles = 4;  // key tiles a share has at least, by the table's width or the window
+// Key tiles a share has at least, by the table's width or the window.  16 and 2 heads: 40 tokens behind 3000 27.3 us (shares of
+// 1 and more 32.6, of 8 29.7, none 59.6); 1 behind 500 12.5 (11.9, 16.5, 16.6); 1 behind 30000 27.7 (none 451).
+constexpr int kTcShareTiles = 2;
 static long long tc_units(int B, int T_new, int Hq, int Hkv) {
     return (static_cast<long long>(T_new) / (kTcQT * (kTcRows / (Hq / Hkv))) + B) * Hkv;
 }
