@@ -80,6 +80,43 @@ def test_decode_many_short():
     R.check(got, *R.reference(x, window=30, softcap=10.0))
 
 
+@pytest.mark.parametrize("D", [8, 16, 24, 56, 72, 88, 120])
+def test_decode_head_sizes(D):
+    lens = [300, 7, 0, 64]
+    x = R.make(D, lens, 12, 3, D, 16, BF)
+    sl = R.slopes(12)
+    R.check(_decode(x, slopes=sl, window=100), *R.reference(x, slopes=sl, window=100))
+
+
+@pytest.mark.parametrize("dtype,D", [(BF, 128), (F32, 64), (BF, 64)])
+def test_decode_bad_block_in_a_split_sequence(dtype, D):
+    lens = [9000, 5000, 20, 7000]
+    x = R.make(13, lens, 8, 2, D, 16, dtype)
+    ref, tol = R.reference(x)
+    x["block_tables"][1, 150] = -1
+    x["block_tables"][3, 0] = 1 << 30
+    st = pkv.new_status()
+    got = _decode(x, st)
+    assert pkv.check_status(st) == 4
+    assert (got[1] == 0).all() and (got[3] == 0).all()
+    R.check(got, ref, tol, [0, 2])
+
+
+@pytest.mark.parametrize("name", ["q", "k_cache", "v_cache", "out"])
+def test_decode_addresses_off_16_bytes(name):
+    x = R.make(14, [200, 33], 8, 2, 128, 16, BF)
+    ref, tol = R.reference(x, softcap=9.0)
+    def off(t):
+        y = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+        return y.copy_(t)
+    kw = {}
+    if name == "out":
+        kw["out"] = off(torch.empty_like(x["q"]))
+    else:
+        x[name] = off(x[name])
+    R.check(_decode(x, softcap=9.0, **kw), ref, tol)
+
+
 def test_without_changes_is_plain_attention():
     x = R.make(2, [300, 17, 900], 32, 8, 128, 16, BF)
     plain = pkv.paged_decode_attention(x["q"], x["k_cache"], x["v_cache"], x["block_tables"], x["seq_lens"])
@@ -215,6 +252,23 @@ def test_plain_prefill_reads_no_other_block(before):
 
 
 # ------------------------------------------------------------------ as a program uses them
+def test_prefill_split_bad_lengths_and_rows_behind_the_last():
+    chunks, lens = [10, 30, 20], [2000, 2500, 1800]
+    x = R.make(15, lens, 8, 2, 128, 16, BF, chunks=chunks)
+    ref, tol = R.reference(x)
+    bt, sl = x["block_tables"].clone(), x["seq_lens"].clone()
+    bt[1, 100] = -3
+    sl[2] = 16 * bt.shape[1] + 1
+    st = pkv.new_status()
+    q = torch.cat([x["q"], x["q"][:7]])
+    out = torch.full_like(q, 7.0)
+    pkv.paged_prefill_attention_scored(q, x["k_cache"], x["v_cache"], bt, sl, x["q_start"], out=out, status=st)
+    assert pkv.check_status(st) == 4
+    assert pkv.prefill_scored_workspace_bytes(3, 67, 8, 2, 128) > 0
+    R.check(out[:60], ref, tol, list(range(10)))
+    assert (out[10:60] == 0).all() and (out[60:] == 7).all()
+
+
 def test_prefill_workspace():
     x = R.make(6, [900], 8, 2, 128, 16, BF, chunks=[20])
     need = pkv.prefill_scored_workspace_bytes(1, 20, 8, 2, 128)

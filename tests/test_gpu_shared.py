@@ -91,6 +91,14 @@ def test_many_groups():
     R.check(call(x), *R.reference(x))
 
 
+def test_more_groups_and_sequences_than_threads():
+    x = make(16, [(32, [33 + i % 5, 40, 32][:2 + i % 2]) for i in range(600)], 8, 4, 64, 16, BF, loose=(9,))
+    st = pkv.new_status()
+    got = call(x, status=st)
+    assert pkv.check_status(st) == 0
+    R.check(got, *R.reference(x))
+
+
 def test_no_groups():
     x = make(7, [], 8, 2, 128, 16, BF, loose=(100, 3000, 1))
     R.check(call(x), *R.reference(x))
