@@ -488,7 +488,8 @@ pkv_status pkv_paged_decode_attention_q8(void* out, const void* q, const void* k
  * sight of every query whatever the window is, and of a prefill chunk's queries
  * before them too (a prefix that attends in both directions; its keys have to be
  * in the cache).  softcap negative, NaN or subnormal, or scale / softcap or softcap *
- * log2(e) out of float32's range: PKV_ERR_INVALID_ARG.
+ * log2(e) out of float32's range, or an out that overlaps q: PKV_ERR_INVALID_ARG.  A
+ * table wider than 0x7fff0000 positions: PKV_ERR_UNSUPPORTED.
  * ---------------------------------------------------------------------------
  */
 
@@ -526,9 +527,10 @@ size_t pkv_prefill_scored_workspace_bytes(int B, int T_new, int Hq, int Hkv, int
  * / Hkv <= 8, 16-byte aligned q, out and pools (else PKV_ERR_UNSUPPORTED).
  * workspace: device, 16-byte aligned, at least pkv_prefill_scored_workspace_bytes(B,
  * T_new, Hq, Hkv, D, 0) bytes (may be NULL where that is 0), contents ignored on
- * entry; calls that can overlap on the GPU need a workspace each.  Key tiles that no row of a query tile sees are not read.  A row that is given no
- * weight is still multiplied: an infinity or NaN in V at a position that some
- * queries see reaches queries within 256 / (Hq / Hkv) tokens of them that do not.
+ * entry; calls that can overlap on the GPU need a workspace each.  Key tiles that
+ * no row of a query tile sees are not read.  A row that is given no weight is
+ * still multiplied: an infinity or NaN in V at a position that some queries see
+ * reaches queries within 256 / (Hq / Hkv) tokens of them that do not.
  */
 pkv_status pkv_paged_prefill_attention_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
                                               const int32_t* block_tables, int max_blocks_per_seq,
@@ -551,9 +553,10 @@ size_t pkv_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D, int num_
  * device int32 [N + 1], non-decreasing, group_start[0] = 0, group_start[N] <= B;
  * sequences behind the last group, and groups of one, share nothing.  The first
  * floor(shared_lens[g] / block_size) table entries of all sequences of a group
- * must be the same (its first sequence's are used); shared_lens: device int32
- * [N].  A sequence shorter than that prefix (but for length 0, which gives
- * zeros), a shared length outside the table, and everything that
+ * must be the same (small batches are read per sequence, by each one's own
+ * entries, others by one member's for all); shared_lens: device int32 [N].  A
+ * sequence shorter than that prefix (but for length 0, which gives zeros), a
+ * shared length outside the table, and everything that
  * pkv_paged_decode_attention_scored finds: zero output and
  * PKV_ERR_DEVICE_BOUNDS, for every sequence where group_start is none.  N may be 0.
  * bf16, D = 64 or 128, block_size a multiple of 16, Hq / Hkv <= 128, 16-byte

@@ -31,6 +31,14 @@ inline bool make_scores(ScoreArgs* sa, float scale, int D, float cap, const floa
     return (cap == 0.f || cap >= 1.17549435e-38f) && sa->mul <= 3.0e38f && sa->in <= 3.0e38f && sa->cap_log2 <= 3.0e38f;
 }
 
+// Positions stay in 32 bits, with a few tiles to spare.
+inline bool positions_fit(int max_blocks, int BS) { return static_cast<long long>(max_blocks) * BS <= 0x7fff0000LL; }
+// Rows of out are written while others of q are still read.
+inline bool overlap(const void* out, const void* q, size_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out), b = reinterpret_cast<uintptr_t>(q);
+    return a < b ? b - a < bytes : a - b < bytes;
+}
+
 // The positions that the one query of a decode step sees: [0, pfx) and [lo, L), pfx <= lo.
 struct Seen {
     int L, lo, pfx;

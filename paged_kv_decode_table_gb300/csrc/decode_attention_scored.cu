@@ -672,6 +672,7 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
                     float* t = scratch + ((slot - 1) * HV + vh) * kTile;
                     if (!mbar_wait(&mempty[warp], ph ^ 1u, pl.polls)) {
                         if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+                        finish();
                         return;
                     }
 #pragma unroll
@@ -1407,9 +1408,11 @@ extern "C" pkv_status pkv_paged_decode_attention_scored(
         !make_scores(&sc, scale, D, softcap, slopes, window, prefix_lens))
         return PKV_ERR_INVALID_ARG;
     if (B == 0) return PKV_OK;
+    if (!positions_fit(max_blocks_per_seq, block_size)) return PKV_ERR_UNSUPPORTED;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !workspace ||
         (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
         return PKV_ERR_INVALID_ARG;
+    if (overlap(out, q, static_cast<size_t>(B) * Hq * D * (dtype == PKV_F32 ? 4 : 2))) return PKV_ERR_INVALID_ARG;
     const int P = device_sm_count();
     if (workspace_bytes < pkv_decode_scored_workspace_bytes(B, Hq, Hkv, D, P > 0 ? P : 1)) return PKV_ERR_INVALID_ARG;
     if (P <= 0) return PKV_ERR_CUDA;

@@ -474,6 +474,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             [[maybe_unused]] const int pos = kSlope && valid ? seq_lens[b] - 1 : 0;
             [[maybe_unused]] const float slope = kSlope ? pl.sc.slopes[qh] * kLog2e : 0.f;
             float m_ref = -INFINITY, lsum = 0.f;
+            bool broken = false;
             for (int kt = k0; kt < w.k1; kt += step, ++done) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&sm->s_full[qt], done & 1))) {  // tcgen05.ld needs the whole warp
                     fail = true;
@@ -554,6 +555,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 for (int ch = 0; ch < 8; ++ch)
                     *reinterpret_cast<uint4*>(pbuf + sw128(r, ch)) =
                         make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
+                // before this tile is given back: the producers are at most kStages pieces ahead of it
+                if (kt + step >= w.k1) broken = *const_cast<volatile int*>(&sm->bad[piece % kPxMarks]) == piece + 1;
                 fence_proxy_async_smem();  // P and the cleared V rows, for the PV MMA
                 tc_fence_before();
                 mbar_arrive(&sm->p_full[qt]);
@@ -575,7 +578,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             const size_t own = whole ? 2 * static_cast<size_t>(gridDim.x) * kPxSlot +
                                            (static_cast<size_t>(dual ? qt : 0) * pl.B + b) * pl.Hq + qh
                                      : slot * kPxSlot + qt * kPxRows + r;
-            const bool broken = *const_cast<volatile int*>(&sm->bad[piece % kPxMarks]) == piece + 1;
             if (valid) ws.ml[own] = make_float2(m_ref, broken ? -1.f : lsum);
             // the P tile is free: 32 columns of the warp's 32 rows go through its quarter of it
             float4* stage = reinterpret_cast<float4*>(pbuf + (warp & 3) * 4096);
@@ -885,6 +887,7 @@ extern "C" pkv_status pkv_paged_decode_attention_shared(
         return pkv_paged_decode_attention_scored(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
                                                  nullptr, B, Hq, Hkv, D, block_size, num_blocks, scale, softcap, slopes, 0,
                                                  dtype, workspace, workspace_bytes, dev_status, stream);
+    if (!positions_fit(max_blocks_per_seq, block_size)) return PKV_ERR_UNSUPPORTED;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !group_start || !shared_lens || !workspace ||
         (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
         return PKV_ERR_INVALID_ARG;
@@ -916,6 +919,7 @@ extern "C" pkv_status pkv_paged_decode_attention_shared(
     const long long tiles = (static_cast<long long>(max_blocks_per_seq) * block_size / kPxKeys + 1) * Hkv *
                             (static_cast<long long>(B) / px.TC + N);
     if (static_cast<long long>(num_blocks) * Hkv * block_size >= (1LL << 31) || tiles >= (1LL << 30)) return PKV_ERR_UNSUPPORTED;
+    if (overlap(out, q, static_cast<size_t>(B) * Hq * D * 2)) return PKV_ERR_INVALID_ARG;
     const int P = device_sm_count();
     if (workspace_bytes < pkv_decode_shared_workspace_bytes(B, Hq, Hkv, D, P > 0 ? P : 1)) return PKV_ERR_INVALID_ARG;
     if (P <= 0) return PKV_ERR_CUDA;

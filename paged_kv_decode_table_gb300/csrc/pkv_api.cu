@@ -183,6 +183,8 @@ pkv_status pkv_paged_prefill_attention_scored(void* out, const void* q, const vo
     if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !q_start) return PKV_ERR_INVALID_ARG;
     if (dtype != PKV_BF16 || !pkv::prefill_tc_supported(Hq, Hkv, D, block_size, q, out, k_cache, v_cache))
         return PKV_ERR_UNSUPPORTED;
+    if (!pkv::positions_fit(max_blocks_per_seq, block_size)) return PKV_ERR_UNSUPPORTED;
+    if (pkv::overlap(out, q, static_cast<size_t>(T_new) * Hq * D * 2)) return PKV_ERR_INVALID_ARG;
     const int P = pkv::device_sm_count();
     const size_t need = pkv::prefill_scored_workspace_bytes(B, T_new, Hq, Hkv, P > 0 ? P : 1);
     if (workspace_bytes < need || (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u))))

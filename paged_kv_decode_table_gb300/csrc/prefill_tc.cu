@@ -57,6 +57,10 @@
 
 namespace pkv {
 
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn get_encode_fn();
 bool encode_pool_box_halves(CUtensorMap* map, const void* pool, int NB, int Hkv, int BS, int box_rows);
 
 constexpr int kTcDim = 128;
@@ -450,6 +454,8 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                 }
                 if (!fail) tc_commit(&sm->kv_empty[s]);
             }
+            // no arrival of this CTA may be outstanding when it exits: the last one follows all others
+            if (!fail && ntiles > 0 && !mbar_wait(&sm->kv_empty[(ntiles - 1) % kTcStages], ((ntiles - 1) / kTcStages) & 1)) fail = true;
             if (fail) report(status, PKV_ERR_TIMEOUT);
         }
         __syncwarp();
@@ -657,20 +663,7 @@ __global__ void __launch_bounds__(128)
 // sit 2048 bytes apart, so a 64-key tile of four boxes is one K-major,
 // 128-byte-swizzled operand per half with a 2048-byte group stride.
 bool encode_pool_k16(CUtensorMap* map, const void* pool, int NB, int Hkv, int BS) {
-    typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static EncodeFn enc = nullptr;
-    static bool tried = false;
-    if (!tried) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult qres;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qres) ==
-                cudaSuccess &&
-            qres == cudaDriverEntryPointSuccess)
-            enc = reinterpret_cast<EncodeFn>(p);
-        tried = true;
-    }
+    EncodeTiledFn enc = get_encode_fn();
     const cuuint64_t rows = static_cast<cuuint64_t>(NB) * Hkv * BS;
     if (!enc || rows % 8 != 0) return false;
     cuuint64_t gdim[4] = {64, 8, 2, rows / 8};

@@ -312,6 +312,103 @@ def test_streams_and_graphs():
         assert torch.equal(o, w)
 
 
+def test_split_prefill_on_streams_and_in_graphs():
+    xs = [R.make(40 + i, [2000 + 700 * i, 90], 16, 2, 128, 16, BF, chunks=[20, 9]) for i in range(2)]
+    assert pkv.prefill_scored_workspace_bytes(2, 29, 16, 2, 128) > 0
+    want = [_prefill(x, softcap=15.0) for x in xs]
+    for o, x in zip(want, xs):
+        R.check(o, *R.reference(x, softcap=15.0))
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s, x in zip(streams, xs):
+            with torch.cuda.stream(s):
+                got.append(_prefill(x, softcap=15.0))
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert torch.equal(o, want[i % 2])
+    graphs, outs = [], []
+    for x in xs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(_prefill(x, softcap=15.0))
+        graphs.append(g)
+    for x in xs:
+        x["q"].copy_(-x["q"])
+    want = [_prefill(x, softcap=15.0) for x in xs]
+    for g in (graphs[0], graphs[1], graphs[0]):
+        g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+def test_threads():
+    """Calls of different sizes from several threads at once, each on a stream of its own."""
+    import threading
+    calls = []
+    for i in range(3):
+        x = R.make(50 + i, [1200 * (i + 1), 33], 8, 2, (128, 64, 72)[i], 16, BF)
+        calls.append(lambda x=x: _decode(x, softcap=9.0))
+        y = R.make(60 + i, [900 * (i + 1), 40], 8, 2, 128, 16, BF, chunks=[5 + i, 40])
+        calls.append(lambda y=y: _prefill(y, window=200))
+    z = R.make(70, [70, 900], 6, 2, 40, 16, F32)
+    calls.append(lambda: _decode(z, slopes=R.slopes(6)))
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got = [calls[i]() for _ in range(30)]
+        s.synchronize()
+        wrong.extend(i for o in got if not torch.equal(o, want[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_empty_batches_and_padding():
+    x = R.make(1, [70, 0], 8, 2, 128, 16, BF)
+    e = torch.empty(0, 8, 128, dtype=BF, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    assert pkv.paged_decode_attention_scored(e, x["k_cache"], x["v_cache"], x["block_tables"][:0], none).shape == e.shape
+    assert pkv.paged_decode_attention_shared(e, x["k_cache"], x["v_cache"], x["block_tables"][:0], none, none.new_zeros(1),
+                                             none).shape == e.shape
+    qs = torch.zeros(3, dtype=torch.int32, device="cuda")
+    args = (x["k_cache"], x["v_cache"], x["block_tables"], x["seq_lens"])
+    assert pkv.paged_prefill_attention_scored(e, *args, qs).shape == e.shape
+    st = pkv.new_status()
+    for rows in (5, 700):  # rows behind the last sequence, of which none has any
+        q = torch.ones(rows, 8, 128, dtype=BF, device="cuda")
+        out = torch.full_like(q, 3.0)
+        pkv.paged_prefill_attention_scored(q, *args, qs, out=out, status=st)
+        assert (out == 3).all()
+    # a padded batch: sequences of length zero, whose table rows are anything
+    x = R.make(2, [300, 0, 0, 17, 0], 8, 2, 64, 16, BF)
+    for b in (1, 2, 4):
+        x["block_tables"][b] = -7
+    got = _decode(x, st, slopes=R.slopes(8))
+    R.check(got, *R.reference(x, slopes=R.slopes(8)))
+    assert pkv.check_status(st) == 0 and (got[[1, 2, 4]] == 0).all()
+
+
+def test_out_over_q_is_refused():
+    x = R.make(1, [70, 80], 8, 2, 128, 16, BF, chunks=[1, 1])
+    none = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for call in (lambda: _decode(x, out=x["q"]), lambda: _prefill(x, out=x["q"]),
+                 lambda: pkv.paged_decode_attention_shared(*[x[n] for n in ("q", "k_cache", "v_cache", "block_tables", "seq_lens")],
+                                                           none, none[:0], out=x["q"])):
+        with pytest.raises(pkv.PkvError):
+            call()
+
+
 def test_given_out_and_workspace():
     x = R.make(1, [700, 80], 32, 8, 128, 16, BF)
     ws = torch.full((pkv.decode_scored_workspace_bytes(2, 32, 8, 128),), 255, dtype=torch.uint8, device="cuda")

@@ -99,6 +99,63 @@ def test_more_groups_and_sequences_than_threads():
     R.check(got, *R.reference(x))
 
 
+def test_bad_blocks_in_many_short_prefixes():
+    """Several prefixes per CTA, every third of which holds a block that is none: its members are zeros, and no others."""
+    n = 900
+    x = make(17, [(64, [64 + i % 40, 80]) for i in range(n)], 8, 8, 128, 16, BF)
+    ref, tol = R.reference(x)
+    bad = [g for g in range(n) if g % 3 == 1]
+    for g in bad:
+        x["block_tables"][2 * g:2 * g + 2, g % 4] = -1
+    st = pkv.new_status()
+    got = call(x, status=st)
+    assert pkv.check_status(st) == 4
+    rows = [2 * g + i for g in bad for i in range(2)]
+    assert (got[rows] == 0).all()
+    R.check(got, ref, tol, [b for b in range(2 * n) if b // 2 % 3 != 1])
+
+
+@pytest.mark.parametrize("wide", [True, False])
+def test_the_same_sequence_twice(wide):
+    """A sequence that is in the batch twice shares all its whole blocks with itself."""
+    x = make(18, [(96, [96, 96, 96]), (80, [90, 90])], 8, 2, 128, 16, BF, wide=wide)
+    for b, a in ((1, 0), (2, 0), (4, 3)):
+        x["block_tables"][b] = x["block_tables"][a]
+    x["q"][1] = x["q"][0]
+    got = call(x, softcap=8.0)
+    R.check(got, *R.reference(x, softcap=8.0))
+
+
+def test_threads():
+    """Calls of different sizes from several threads at once, each on a stream of its own."""
+    import threading
+    xs = [make(40 + i, [(320 * (i + 1), [700 + i] * (4 + 30 * i)), (48, [50, 60])], 16, 4, (128, 64)[i % 2], 16, BF, wide=i != 2)
+          for i in range(4)]
+    xs += [make(44 + i, [(320 * i, [1000 - i] * (3 + 40 * i))], 16, 4, 128, 16, BF) for i in (1, 2)]
+    want = [call(x) for x in xs]
+    for x, w in zip(xs, want):
+        # the large prefixes of 960 and 1280 are longer than their sequences of 702 and 703, which are zeros
+        short = x["seq_lens"] < x["shared_lens"][torch.bucketize(torch.arange(len(w), device="cuda"), x["group_start"][1:], right=True)]
+        assert (w[short] == 0).all()
+        R.check(w, *R.reference(x), ~short)
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got = [call(xs[i]) for _ in range(30)]
+        s.synchronize()
+        wrong.extend(i for o in got if not torch.equal(o, want[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(xs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 def test_no_groups():
     x = make(7, [], 8, 2, 128, 16, BF, loose=(100, 3000, 1))
     R.check(call(x), *R.reference(x))

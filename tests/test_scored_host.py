@@ -65,6 +65,17 @@ def test_shared_refusals(lib):
         assert shared(lib, **bad) == 2, bad
 
 
+def test_out_over_q_and_too_wide_tables(lib):
+    """Rows of out are written while other rows of q are read; positions are 32-bit numbers."""
+    for call, rows in ((decode, 2), (shared, 2), (prefill, 4)):
+        D = 128
+        for away in (0, 16, -16, rows * 4 * D * 2 - 16):
+            assert call(lib, D=D, q=P(1 << 20), o=P((1 << 20) + away)) == 1, (call, away)
+        assert call(lib, D=D, q=P(1 << 20), mb=0x7fff, BS=1 << 16, wb=0) != 2  # (refused for its workspace)
+        assert call(lib, D=D, q=P(1 << 20), mb=(0x7fff << 12) + 1, BS=16) == 2
+    assert decode(lib, dt=0, q=P(1 << 20), o=P((1 << 20) + 2 * 4 * 64 * 4 - 16)) == 1
+
+
 def test_workspaces_are_host_arithmetic(lib):
     import paged_kv_decode_table_gb300 as pkv
     for f in (pkv.decode_scored_workspace_bytes, pkv.decode_shared_workspace_bytes):
