@@ -144,6 +144,7 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
     decode_split_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                         const __grid_constant__ SplitPlan pl, const __nv_bfloat16* q, __nv_bfloat16* out,
                         const int32_t* block_tables, const int32_t* seq_lens, const SplitSpace ws, int32_t* status) {
+    constexpr bool kEstimate = kShared && shares_sms(8 * kN);
     constexpr int kHalves = DP / 64, kChunks = DP / 16, kSub = split_sub(DP), kHeads = 8 * kN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -225,11 +226,32 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
         }
         __syncthreads();  // the barriers are initialised
     } else {
+        [[maybe_unused]] int from = 0, to = 0, shared = 0;  // of group threadIdx.x: asked for before the lengths' chain
+        if (kEstimate && static_cast<int>(threadIdx.x) < pl.groups.N) {
+            from = pl.groups.start[threadIdx.x];
+            to = pl.groups.start[threadIdx.x + 1];
+            shared = pl.groups.shared[threadIdx.x];
+        }
         const int n_first = static_cast<int>(threadIdx.x) < B ? NG * steps_of<kShared>(pl, seq_lens, threadIdx.x) : 0;
         int tsum = n_first;
         for (int b = threadIdx.x + nthr; b < B; b += nthr) tsum += NG * steps_of<kShared>(pl, seq_lens, b);
+        int ranges = static_cast<int>(gridDim.x);
+        [[maybe_unused]] SharedWork work;
+        [[maybe_unused]] int* sums = reinterpret_cast<int*>(qring);  // (no query is there yet)
+        if constexpr (kEstimate) {
+            work.group(from, to, shared, pl.max_blocks, pl.BS, pl.TQ);
+            for (int g = threadIdx.x + nthr; g < pl.groups.N; g += nthr)
+                work.group(pl.groups.start[g], pl.groups.start[g + 1], pl.groups.shared[g], pl.max_blocks, pl.BS, pl.TQ);
+            for (int b = threadIdx.x; b < B; b += nthr) work.sequence(seq_lens[b], pl.max_blocks, pl.BS);
+            work.put(sums, warp, lane);
+        }
         int total, before = split_scan(tsum, sch, total);
-        if (total > 0) W = (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+        if constexpr (kEstimate) {
+            work.get(sums, nthr >> 5, lane);
+            const int own = work.own_ctas(ranges, B, pl.groups.N, pl.Hkv, NG, pl.units, pl.sc.cap_log2 > 0.f, lane);
+            if (own > 0) ranges = own;
+        }
+        if (total > 0) W = (total + ranges - 1) / ranges;
         start = min(total, static_cast<int>(blockIdx.x) * W);
         end = min(total, start + W);
         if constexpr (!kShared) {

@@ -8,7 +8,8 @@
 //     matrix (members x Hq / Hkv), which meets every prefix key once.  A tile of K and V serves up to 256 rows.
 //  2. decode_split_kernel<.., kShared> (decode_attention_scored.cu): the positions behind the prefix, per sequence.
 //  3. shared_join_kernel: a warp per row.
-// 2 does not wait for 1: an SM that has no prefix work left takes up the rest.
+// 2 does not wait for 1: an SM that has no prefix work left takes up the rest, and where both have much to do they share
+// the SMs out between them (SharedWork).
 //
 // prefix_tc_kernel: a persistent kernel, one CTA per SM.  Work = (group, KV head, tile of up to 256 rows) x key tiles of
 // 64; all of it in one order, cut into one range of key tiles per CTA, so that a few rows over a long prefix and many
@@ -85,6 +86,7 @@ struct PxShared {  // follows the 1024-aligned operand area
     uint32_t tmem_base;
     int at[7];  // where the CTA's range begins: a group as PxWalk has it
     int red[32];
+    int work[3 * kPxThreads / 32];
     int bad[kPxMarks];
 };
 template <int kD>
@@ -109,6 +111,7 @@ struct PxPlan {
     int TQ, TC;  // members per query tile and per row tile
     ScoreArgs sc;
     GroupArgs groups;
+    int NG, units;  // of the split kernel
 };
 
 // A role's walk over the CTA's pieces.
@@ -121,8 +124,7 @@ struct PxWalk {
     __device__ __forceinline__ void set(const PxPlan& pl, int from, int to, int shared) {
         first = from;
         n = to - from;
-        prefix = n > 1 && shared > 0 && static_cast<long long>(shared) <= static_cast<long long>(pl.max_blocks) * pl.BS
-                     ? shared / pl.BS * pl.BS : 0;
+        prefix = group_prefix_of(n, shared, pl.max_blocks, pl.BS);
         nt = (prefix + kPxKeys - 1) / kPxKeys;
         rt = prefix > 0 ? (n + pl.TC - 1) / pl.TC : 0;
     }
@@ -176,6 +178,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     // groups, then block ids, then K and V: three dependent loads; the first two and q come to L2 while the
     // predecessor ends
     const unsigned worker = blockIdx.x * blockDim.x + tid;
+    prefetch_l2(seq_lens, static_cast<size_t>(pl.B) * 4, worker);
     prefetch_l2(pl.groups.start, (static_cast<size_t>(N) + 1) * 4, worker);
     prefetch_l2(pl.groups.shared, static_cast<size_t>(N) * 4, worker);
     prefetch_l2(block_tables, static_cast<size_t>(pl.B) * pl.max_blocks * 4, worker);
@@ -228,16 +231,29 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     };
     bool wrong = false;
     int sum = 0, total, mine = 0;  // mine: key tiles of group tid
+    SharedWork work;
+    const bool estimate = shares_sms(G);
+    const int L0 = estimate && tid < pl.B ? seq_lens[tid] : 0;  // on its way together with the group's entries
     PxWalk own;
     for (int g = N - 1 - (N - 1 - tid) % kPxThreads; g >= tid && g < N; g -= kPxThreads) {  // group tid comes last
         own.set(pl, pl.groups.start[g], pl.groups.start[g + 1], pl.groups.shared[g]);
         wrong = wrong || !group_valid(pl.groups, pl.B, g);
         mine = pl.Hkv * own.nt * own.rt;
         sum += mine;
+        if (estimate) work.group(own.first, own.first + own.n, pl.groups.shared[g], pl.max_blocks, BS, pl.TQ);
+    }
+    if (estimate) {
+        work.sequence(L0, pl.max_blocks, BS);
+        for (int b = tid + kPxThreads; b < pl.B; b += kPxThreads) work.sequence(seq_lens[b], pl.max_blocks, BS);
+        work.put(sm->work, warp, lane);
     }
     wrong = __syncthreads_or(wrong) != 0;
     int before = scan(sum, total);
-    const int P = static_cast<int>(gridDim.x);
+    int P = static_cast<int>(gridDim.x);
+    if (estimate) {
+        work.get(sm->work, kPxThreads / 32, lane);
+        P -= work.own_ctas(P, pl.B, N, pl.Hkv, pl.NG, pl.units, kCap, lane);
+    }
     const int W = max(kPxMinTiles, (total + P - 1) / P);
     if (blockIdx.x == 0 && tid == 0) {
         *ws.head = PxHead{W, wrong ? 0 : 1};
@@ -915,6 +931,9 @@ extern "C" pkv_status pkv_paged_decode_attention_shared(
     px.sc = sc;
     px.groups = pl.groups;
     if ((D != 64 && D != 128) || px.TQ == 0 || !split_applies(pl, out, q, k_cache, v_cache, dtype)) return PKV_ERR_UNSUPPORTED;
+    px.NG = pl.NG;
+    pl.TQ = px.TQ;
+    px.units = pl.units;
     // pool rows and key tiles stay in 32 bits
     const long long tiles = (static_cast<long long>(max_blocks_per_seq) * block_size / kPxKeys + 1) * Hkv *
                             (static_cast<long long>(B) / px.TC + N);

@@ -81,6 +81,17 @@ def test_scores(D, softcap, slopes):
     R.check(got, *R.reference(x, softcap=softcap, slopes=sl))
 
 
+@pytest.mark.parametrize("D,softcap,slopes", [(128, 0.0, False), (128, 12.0, True), (64, 0.0, True)])
+def test_much_behind_the_prefix(D, softcap, slopes):
+    """Prefixes and the sequences' own positions both large: the two kernels share the SMs out."""
+    x = make(19, [(2048, [2348 + 43 * i for i in range(24)]), (700, [1500, 700, 0, 2900])], 16, 4, D, 16, BF, loose=(1200, 5))
+    sl = R.slopes(16) if slopes else None
+    want = call(x, softcap=softcap, slopes=sl)
+    R.check(want, *R.reference(x, softcap=softcap, slopes=sl))
+    for _ in range(20):
+        assert torch.equal(call(x, softcap=softcap, slopes=sl), want)
+
+
 def test_long_prefix_many_rows():
     x = make(5, [(12000, [12000 + 7 * i for i in range(48)])], 32, 4, 128, 16, BF)
     R.check(call(x), *R.reference(x))
