@@ -121,13 +121,14 @@ __device__ __forceinline__ int tc_tiles_longer(int n, int L, int TC, int v) {
     return cnt;
 }
 
-// The 64 products of a row with the keys from kbase on become scores in the log2 domain, -infinity where the row at
-// position `pos` does not see the key.  first, last: the positions of the query tile's rows; slope: of the row's
+// The 64 products of a row with the keys from kbase on become scores in the log2 domain (without cap and slopes they stay
+// products, which the softmax scales), -infinity where the row at position `pos` does not see the key.  first, last: the positions of the query tile's rows; slope: of the row's
 // head, times log2(e).
 template <int kKind>
 __device__ __forceinline__ void score_tile(uint32_t (&sr)[2][32], int kbase, int pos, int first, int last, int pfx,
                                            float slope, const ScoreArgs& sc) {
-    tc_scores<(kKind & kCapped) != 0, (kKind & kSloped) != 0>(sr, kbase - pos, slope, sc);
+    if constexpr ((kKind & (kCapped | kSloped)) != 0)
+        tc_scores<(kKind & kCapped) != 0, (kKind & kSloped) != 0>(sr, kbase - pos, slope, sc);
     // some key is hidden from some row of the query tile
     if (kbase + kTcKeys > pfx && (kbase + kTcKeys - 1 > first || (sc.window > 0 && kbase <= last - sc.window))) {
         const int lo = sc.window > 0 ? pos - sc.window + 1 - kbase : -kbase, hi = pos - kbase, near = pfx - kbase;
@@ -499,7 +500,8 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             for (int c = 0; c < kTcKeys; c += 2)
                 mxs[(c >> 1) & 3] = tc_max3(mxs[(c >> 1) & 3], __uint_as_float(sr[c >> 5][c & 31]),
                                             __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
-            const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * (kScored ? 1.f : scale_log2);
+            const float mul = kKind == kPlain ? scale_log2 : kKind == kMasked ? sc.mul : 1.f;
+            const float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])) * mul;
             // the reference maximum moves only when the row maximum passes it by more than 8
             const float m_new = mx > m_ref + 8.f ? mx : m_ref;
             const bool resc = m_new != m_ref;
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             for (int c = 0; c < kTcKeys / 2; ++c) {
                 float t0, t1;
                 tc_fma2(t0, t1, __uint_as_float(sr[(2 * c) >> 5][(2 * c) & 31]),
-                        __uint_as_float(sr[(2 * c + 1) >> 5][(2 * c + 1) & 31]), kScored ? 1.f : scale_log2, nmu);
+                        __uint_as_float(sr[(2 * c + 1) >> 5][(2 * c + 1) & 31]), mul, nmu);
                 const float e0 = tc_ex2(t0), e1 = tc_ex2(t1);
                 pk[c] = pack_bf16x2(e0, e1);
                 tc_add2(ls[c & 3][0], ls[c & 3][1], e0, e1);
