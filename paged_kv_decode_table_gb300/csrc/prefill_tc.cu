@@ -138,6 +138,9 @@ __device__ __forceinline__ void score_tile(uint32_t (&sr)[2][32], int kbase, int
     }
 }
 
+// The eight softmax warps.
+__device__ __forceinline__ void softmax_barrier() { asm volatile("barrier.sync 1, 256;" ::: "memory"); }
+
 // Few query tiles over long key ranges (scored): S CTAs take a share of a pair of query tiles' keys each and leave
 // maxima, sums and float32 O of their rows, [T_new * Hq][S], to prefill_join_kernel.
 struct TcSplit {
@@ -146,9 +149,9 @@ struct TcSplit {
     float* o;
 };
 
-// With changed scores the softmax warps bound it: 16 chunks of up to 512 behind 512-4096 (32 and 8 heads) take 272 us plain, 298
-// with masks to look at, 405 with every score capped (eight FMAs a score and no pipe to hide them behind); 4 of up to 2048
-// behind 16384-32768 that see 1024 + 100 positions, with slopes, 441 (109 at the measured bf16 rate).
+// With changed scores the softmax warps bound it: 16 chunks of up to 512 behind 512-4096 (32 and 8 heads) take 272 us plain, 299
+// with masks to look at, 386 with every score capped (eight FMAs a score and no pipe to hide them behind); 4 of up to 2048
+// behind 16384-32768 that see 1024 + 100 positions, with slopes, 437 (109 at the measured bf16 rate).
 // kKind: kPlain, or kMasked (the masks of attention_scores.cuh) with kCapped and kSloped where its scores are.
 template <int kKind>
 __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThreads, 1)
@@ -276,7 +279,12 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
     // this thread's row (softmax warps): query tile qt, row r = token tl of the CTA, query head qh
     const bool softmax_warp = warp < 4 * kTcQT;
     const int qt = warp >> 2, r = tid & (kTcRows - 1);
-    const int tl = qt * TQ + r / G, qh = h * G + r % G;
+    // scored: where all rows fit into one query tile, both hold them: tile t takes every other key tile from t on, and the
+    // epilogue joins the two.  Two chains of products and softmax over half the keys each, instead of one over padding: 9
+    // sequences of 2 tokens behind 141-8220, 15 and 5 heads, capped 49 us for 77; 29 of 6 behind 1216-1541, 63 and 9 77 for
+    // 131.  (Barriers then count the key tiles of a query tile, u.)
+    const bool dual = kScored && active && nt <= TQ;
+    const int tl = (dual ? 0 : qt * TQ) + r / G, qh = h * G + r % G;
     const bool row_valid = active && softmax_warp && r < TQ * G && tl < nt;  // rows TQ G .. 127: padding
     if (bad_len) {
         if (tid == 0) report(status, PKV_ERR_DEVICE_BOUNDS);
@@ -410,8 +418,9 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                     break;
                 }
                 const uint32_t kb = kva + s * kTcStageBytes;
-                for (int t = 0; t < kTcQT; ++t) {
-                    if (j >= 1 && !mbar_wait(&sm->s_free[t], (j - 1) & 1)) {
+                const int ta = dual ? j & 1 : 0, tb = dual ? ta : kTcQT - 1, u = dual ? j >> 1 : j;
+                for (int t = ta; t <= tb; ++t) {
+                    if (u >= 1 && !mbar_wait(&sm->s_free[t], (u - 1) & 1)) {
                         fail = true;
                         break;
                     }
@@ -439,8 +448,9 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             for (int j = 0; j < ntiles && !fail; ++j) {
                 const int s = j % kTcStages;
                 const uint32_t vb = kva + s * kTcStageBytes + kTcKBytes;
-                for (int t = 0; t < kTcQT; ++t) {  // query tile 0 first: its softmax warps clear V rows past L
-                    if (!mbar_wait(&sm->p_full[t], j & 1)) {
+                const int ta = dual ? j & 1 : 0, tb = dual ? ta : kTcQT - 1, u = dual ? j >> 1 : j;
+                for (int t = ta; t <= tb; ++t) {  // query tile 0 first: its softmax warps clear V rows past L
+                    if (!mbar_wait(&sm->p_full[t], u & 1)) {
                         fail = true;
                         break;
                     }
@@ -450,7 +460,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                     for (int kk = 0; kk < kTcKeys / 16; ++kk)
                         tc_mma(tmem + 256 * t + 128, tc_desc(pb + 32 * kk, 16, 1024),
                                tc_desc(vb + kTcGroupBytes * kk, kTcGroupBytes / 2, 1024), idO,
-                               (j > 0 || kk > 0) ? 1u : 0u);
+                               (u > 0 || kk > 0) ? 1u : 0u);
                     tc_commit(&sm->o_done[t]);
                 }
                 if (!fail) tc_commit(&sm->kv_empty[s]);
@@ -465,12 +475,14 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
         // ------------------------------------------------ softmax warps: thread r of query tile qt owns row r
         const uint32_t lrow = static_cast<uint32_t>((warp & 3) * 32) << 16;  // this warp's TMEM lanes
         const uint32_t tq = tmem + 256 * qt;
-        const int p0t = p0 + qt * TQ;  // the query tile's first position
+        const int p0t = p0 + (dual ? 0 : qt * TQ);  // the query tile's first position
+        const int step = dual ? 1 : 0, mine = dual ? (ntiles + 1 - qt) >> 1 : ntiles;  // its key tiles
         float m_ref = -INFINITY, lsum = 0.f;
         [[maybe_unused]] float slope = 0.f;
         if constexpr (kScored) slope = kKind & kSloped ? sc.slopes[qh] * kLog2e : 0.f;
-        for (int j = 0; j < ntiles; ++j) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&sm->s_full[qt], j & 1))) {  // tcgen05.ld needs the whole warp
+        for (int u = 0; u < mine; ++u) {
+            const int j = (u << step) + (step & qt);
+            if (!__all_sync(0xffffffffu, mbar_wait(&sm->s_full[qt], u & 1))) {  // tcgen05.ld needs the whole warp
                 fail = true;
                 break;
             }
@@ -525,15 +537,15 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             }
             lsum = lsum * a + (((ls[0][0] + ls[0][1]) + (ls[1][0] + ls[1][1])) +
                                ((ls[2][0] + ls[2][1]) + (ls[3][0] + ls[3][1])));
-            // the PV of tile j - 1 is complete: O may be rescaled and the P tile rewritten
-            if (j > 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (j - 1) & 1))) {
+            // the PV of the tile before is complete: O may be rescaled and the P tile rewritten
+            if (u > 0) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (u - 1) & 1))) {
                     fail = true;
                     break;
                 }
                 tc_fence_after();
             }
-            if (j > 0 && __any_sync(0xffffffffu, resc)) {
+            if (u > 0 && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
                 for (int cc = 0; cc < kTcDim / 32; ++cc) {
                     uint32_t o[32];
@@ -545,7 +557,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             }
             // the V rows of keys past the CTA's last one (not in the cache yet, past L, or another block's) may hold
             // anything: clear them (scored: those of every key that no row sees)
-            if (qt == 0 && (kScored ? kbase + kTcKeys - 1 > plast || (kbase < wlo && kbase + kTcKeys > pfx) : kt == ntiles - 1)) {
+            if ((dual || qt == 0) && (kScored ? kbase + kTcKeys - 1 > plast || (kbase < wlo && kbase + kTcKeys > pfx) : kt == ntiles - 1)) {
                 const int rlo = kScored ? 0 : plast + 1 - kbase;
                 uint8_t* vb = sKV + static_cast<size_t>(j % kTcStages) * kTcStageBytes + kTcKBytes;
                 for (int idx = r; idx < (kTcKeys - rlo) * 16; idx += kTcRows) {
@@ -566,12 +578,55 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             mbar_arrive(&sm->p_full[qt]);
         }
         // ---- epilogue: O / sum of the last PV
-        if (!fail && ntiles > 0 &&
-            !__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (ntiles - 1) & 1)))
-            fail = true;
+        if (!fail && mine > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (mine - 1) & 1))) fail = true;
+        // dual: query tile 1's result goes through the ring (both are done with it) to query tile 0, whose rows take
+        // own O + other O' with the factors below
+        [[maybe_unused]] float own = 1.f, other = 0.f;
+        float4* const there = reinterpret_cast<float4*>(sKV) + r * (kTcDim / 4);  // 16-byte piece c at c ^ (r & 7)
+        if constexpr (kScored) {
+            if (dual) {
+                float2* const ends = reinterpret_cast<float2*>(sKV + kTcRows * kTcDim * 4);
+                tc_fence_after();
+                softmax_barrier();
+                if (qt == 1) {
+                    ends[r] = make_float2(m_ref, lsum);
+#pragma unroll 1
+                    for (int cc = 0; mine > 0 && cc < kTcDim / 32; ++cc) {
+                        uint32_t o[32];
+                        tc_ld32(tq + lrow + 128 + 32 * cc, o);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            there[(8 * cc + i) ^ (r & 7)] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                                                        __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    }
+                }
+                softmax_barrier();
+                if (qt == 0) {
+                    const float2 e = ends[r];
+                    const float m_new = fmaxf(m_ref, e.x), mu = m_new == -INFINITY ? 0.f : m_new;
+                    own = tc_ex2(m_ref - mu);
+                    other = tc_ex2(e.x - mu);
+                    lsum = lsum * own + e.y * other;
+                    m_ref = m_new;
+                }
+            }
+        }
+        auto joined = [&](uint32_t (&o)[32], int cc) {
+            if constexpr (kScored) {
+                if (!dual) return;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 v = ntiles > 1 ? there[(8 * cc + i) ^ (r & 7)] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    o[4 * i] = __float_as_uint(fmaf(v.x, other, __uint_as_float(o[4 * i]) * own));
+                    o[4 * i + 1] = __float_as_uint(fmaf(v.y, other, __uint_as_float(o[4 * i + 1]) * own));
+                    o[4 * i + 2] = __float_as_uint(fmaf(v.z, other, __uint_as_float(o[4 * i + 2]) * own));
+                    o[4 * i + 3] = __float_as_uint(fmaf(v.w, other, __uint_as_float(o[4 * i + 3]) * own));
+                }
+            }
+        };
         if (fail) {
             if (lane == 0) report(status, PKV_ERR_TIMEOUT);
-        } else {
+        } else if (!dual || qt == 0) {
             tc_fence_after();
             if (S > 1) {
                 const size_t at = row_valid ? (static_cast<size_t>(t0 + tl) * Hq + qh) * S + share : 0;
@@ -581,6 +636,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                 for (int cc = 0; ntiles > 0 && cc < kTcDim / 32; ++cc) {
                     uint32_t o[32];
                     tc_ld32(tq + lrow + 128 + 32 * cc, o);
+                    joined(o, cc);
                     if (row_valid) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
@@ -596,6 +652,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             for (int cc = 0; S == 1 && cc < kTcDim / 32; ++cc) {
                 uint32_t o[32];
                 tc_ld32(tq + lrow + 128 + 32 * cc, o);
+                joined(o, cc);
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i)

@@ -213,6 +213,27 @@ def test_prefill_few_rows_over_long_ranges(Hq, Hkv, BS, chunks, before, mask):
     R.check(got, *R.reference(x, slopes=sl, prefix=pre, **m))
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(32, 4), (6, 6), (28, 4)])
+@pytest.mark.parametrize("kw", [{}, dict(softcap=20.0, window=100), dict(window=70, prefix=True), dict(softcap=5.0, slopes=True)])
+@pytest.mark.parametrize("many", [1, 12])
+def test_prefill_chunks_about_one_query_tile(Hq, Hkv, kw, many):
+    """Chunks whose rows fit into one query tile, or just do not, over one key tile and more; `many`: with key ranges
+    that are not split."""
+    TQ = 128 // (Hq // Hkv)
+    chunks = [1, TQ, TQ + 1, 3, TQ - 1, 2 * TQ, 2, 1, 5] * many
+    lens = [n + k for n, k in zip(chunks, [0, 0, 64, 61, 62, 640, 126, 1000, 130] * many)]
+    x = R.make(many, lens, Hq, Hkv, 128, 16, BF, chunks=chunks)
+    kw = dict(kw)
+    if kw.pop("slopes", False):
+        kw["slopes"] = R.slopes(Hq)
+    if kw.pop("prefix", False):
+        pre = [0, 9, 3, 64, 200, 100, 1, 5, 0] * many
+        got = _prefill(x, prefix_lens=torch.tensor(pre, dtype=torch.int32, device="cuda"), **kw)
+        R.check(got, *R.reference(x, prefix=pre, **kw))
+    else:
+        R.check(_prefill(x, **kw), *R.reference(x, **kw))
+
+
 def test_prefill_prefix_seen_by_all_rows():
     # the whole chunk attends in both directions, in tiles behind the first one too
     x = R.make(3, [600], 8, 1, 128, 16, BF, chunks=[600])
