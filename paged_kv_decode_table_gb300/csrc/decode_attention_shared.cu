@@ -25,12 +25,12 @@
 //  * A piece leaves its row maxima, sums and float32 O: 512 bytes per row of 128 dimensions, written through the P tile
 //    so that a warp stores whole 128-byte lines.
 //
-// What bounds it.  Three kernels one after the other, each with its start (lengths or groups, block ids, first tiles: 3-5
-// us) and its end.  64 sequences of 64-1024 behind 8192 tokens, 32 and 8 heads of 128: 63 us, 26 at the copy rate; the
-// prefix kernel 22, of which 7 tiles a CTA take 9; what the sequences have of their own 25; the join 7.  16 groups of 4
-// behind 1024-4096: 66 us (34 at the copy rate): the prefix kernel streams at 6.6 TB/s once its ring is full.  Many rows:
-// the chain of products and softmax, 2600 clocks a tile of 64 keys and 256 rows, 3900 with a cap, whose polynomial fills
-// the FMA pipe: 32 sequences behind 65536 tokens, 64 and 8 heads, cap and slopes 149 us (50).
+// What bounds it.  Starts (lengths or groups, block ids, first tiles: 3-5 us) and ends of three kernels.  64 sequences of
+// 64-1024 behind 8192 tokens, 32 and 8 heads of 128: 49 us, 26 at the copy rate; prefix and own positions side by side 40 (one
+// after the other 22 and 25, 63 in all), the join 7.  16 groups of 4 behind 1024-4096: 63 us (34 at the copy rate): the
+// prefix kernel streams at 6.6 TB/s once its ring is full.  Many rows: the chain of products and softmax, 2600 clocks a tile
+// of 64 keys and 256 rows, 3900 with a cap, whose polynomial fills the FMA pipe: 32 sequences behind 65536 tokens, 64 and 8
+// heads, cap and slopes 152 us (50).
 // Tried and not kept: key tiles of 128 (P over S in tensor memory, half the barriers; 4000 clocks for 128 keys, but with a
 // longer start as fast in all); 16 softmax warps, two threads a row.
 // Every mbarrier wait is bounded; a CTA that gives up records PKV_ERR_TIMEOUT, waits (bounded) for its own TMA copies,

@@ -744,8 +744,8 @@ bool prefill_tc_supported(int Hq, int Hkv, int D, int BS, const void* q, const v
 
 // CTAs along the keys: as many as fill the SMs once, where the pairs of query tiles are fewer.
 constexpr int kTcShares = 64;     // at most
-// Key tiles a share has at least, by the table's width or the window.  16 and 2 heads: 40 tokens behind 3000 27.3 us (shares of
-// 1 and more 32.6, of 8 29.7, none 59.6); 1 behind 500 12.5 (11.9, 16.5, 16.6); 1 behind 30000 27.7 (none 451).
+// Key tiles a share has at least, by the table's width or the window.  16 and 2 heads: 40 tokens behind 3000 27.4 us (shares of
+// 1 and more 32.9, of 8 30.1, none 62.4); 1 behind 500 12.4 (12.2, 15.9, 15.7); 1 behind 30000 27.0 (none 366).
 constexpr int kTcShareTiles = 2;
 static long long tc_units(int B, int T_new, int Hq, int Hkv) {
     return (static_cast<long long>(T_new) / (kTcQT * (kTcRows / (Hq / Hkv))) + B) * Hkv;
