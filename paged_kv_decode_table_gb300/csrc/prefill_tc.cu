@@ -95,16 +95,8 @@ constexpr size_t kTcOperandBytes = kTcQT * static_cast<size_t>(kTcPBytes) + kTcS
 constexpr size_t kTcSmemBytes = 1024 + kTcOperandBytes + sizeof(TcSmem);
 static_assert(kTcSmemBytes <= 227 * 1024, "shared memory of one CTA");
 
-__device__ __forceinline__ int warp_sum_i(int x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-__device__ __forceinline__ int warp_max_i(int x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
-}
+__device__ __forceinline__ int warp_sum_i(int x) { return __reduce_add_sync(0xffffffffu, x); }
+__device__ __forceinline__ int warp_max_i(int x) { return __reduce_max_sync(0xffffffffu, x); }
 // Chunk tiles of one sequence (n chunk tokens, length L after the chunk, TC
 // tokens per tile) that read more than v key tiles.  Full tile c reads up to
 // position L - n + TC (c + 1) - 1, the last tile up to L - 1; the count grows
@@ -116,8 +108,8 @@ __device__ __forceinline__ int tc_tiles_longer(int n, int L, int TC, int v) {
     const long long Lc = max(L, n), P = Lc - n;
     int cnt = (Lc - 1) / kTcKeys + 1 > v ? 1 : 0;
     const long long x = static_cast<long long>(kTcKeys) * v - P + 1;  // full tile c qualifies iff TC (c + 1) >= x
-    const long long cmin = x <= 0 ? 0 : (x + TC - 1) / TC - 1;
-    cnt += static_cast<int>(max(0LL, static_cast<long long>(tiles - 1) - cmin));
+    const int cmin = x <= 0 ? 0 : static_cast<int>((static_cast<unsigned>(x) + TC - 1) / static_cast<unsigned>(TC)) - 1;
+    cnt += max(0, tiles - 1 - cmin);
     return cnt;
 }
 
@@ -335,7 +327,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (softmax_warp || warp == kTcWarpS) asm volatile("barrier.sync 2, 288;" ::: "memory");  // Q is there; the producers go on
     tc_fence_after();
 
     bool fail = false;
