@@ -141,9 +141,11 @@ struct TcSplit {
     float* o;
 };
 
-// With changed scores the softmax warps bound it: 16 chunks of up to 512 behind 512-4096 (32 and 8 heads) take 272 us plain, 299
-// with masks to look at, 386 with every score capped (eight FMAs a score and no pipe to hide them behind); 4 of up to 2048
-// behind 16384-32768 that see 1024 + 100 positions, with slopes, 437 (109 at the measured bf16 rate).
+// What bounds it: S of 64 keys runs at half rate (8 MMAs of N = 64 take 536 clocks, as 16 of N = 128 would), so a tile of 64 keys
+// and 256 rows keeps the tensor pipe busy for 1540 clocks, and takes 2000-2300; with changed scores the softmax warps: 2800
+// with slopes, 3500 with a cap (eight FMAs a score and no pipe to hide them behind).  16 chunks of up to 512 behind 512-4096
+// (32 and 8 heads): 265 us plain, 374 with every score capped; 4 of up to 2048 behind 16384-32768 that see 1024 + 100
+// positions, with slopes, 417 (109 at the measured bf16 rate).
 // kKind: kPlain, or kMasked (the masks of attention_scores.cuh) with kCapped and kSloped where its scores are.
 template <int kKind>
 __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThreads, 1)
