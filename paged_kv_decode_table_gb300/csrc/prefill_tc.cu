@@ -141,9 +141,11 @@ struct TcSplit {
     float* o;
 };
 
-// What bounds it: S of 64 keys runs at half rate (8 MMAs of N = 64 take 536 clocks, as 16 of N = 128 would), so a tile of 64 keys
-// and 256 rows keeps the tensor pipe busy for 1540 clocks, and takes 2000-2300; with changed scores the softmax warps: 2800
-// with slopes, 3500 with a cap (eight FMAs a score and no pipe to hide them behind).  16 chunks of up to 512 behind 512-4096
+// What bounds it: the tensor pipe.  An MMA of M 128, K 16 with A in tensor memory takes 84 clocks (N 64; 88 for N 128), with A in
+// shared memory 70 (N 128): the 16 of S and 8 of PV for 64 keys and 256 rows are 1900 clocks, a tile takes 2000-2300.  (Q in shared
+// memory: 52 clocks an MMA of S, but then shared memory carries 224 KB a tile at 118 bytes a clock, 1900 again, and the ring is
+// two stages shorter: 354 us for 311 plain.)  With changed scores the softmax warps: 2800 with slopes, 3500 with a cap (eight
+// FMAs a score and no pipe to hide them behind).  16 chunks of up to 512 behind 512-4096
 // (32 and 8 heads): 265 us plain, 374 with every score capped; 4 of up to 2048 behind 16384-32768 that see 1024 + 100
 // positions, with slopes, 417 (109 at the measured bf16 rate).
 // kKind: kPlain, or kMasked (the masks of attention_scores.cuh) with kCapped and kSloped where its scores are.
