@@ -250,15 +250,16 @@ __global__ void __launch_bounds__((kFastMaxKvHeads + 1) * 32, 1)
         // with no copy in flight.
         if (static_cast<int>(blockIdx.x) == silent_cta) return;
         int piece = 0;
-        // On a timeout, wait (bounded) for the copies this lane issued that
-        // no consumer has seen land, so that the CTA never exits with a bulk
+        // Before every exit, wait for the copies this lane issued that no
+        // consumer may have seen land, so that the CTA never exits with a bulk
         // copy still writing into its shared memory: the latest round of each
-        // stage (iterations it - nst .. it - 1) and of each query slot.
+        // stage (iterations it - nst .. it - 1) and of each query slot.  Bounded,
+        // but not by the limit that a test lowers: copies that were issued land.
         auto drain = [&](int it) {
             for (int k = max(0, it - nst); k < it; ++k)
-                mbar_wait(&full[k % nst], static_cast<uint32_t>(k / nst) & 1u, max_polls);
+                mbar_wait(&full[k % nst], static_cast<uint32_t>(k / nst) & 1u);
             for (int pk = max(0, piece - 2); pk < piece; ++pk)
-                mbar_wait(&qfull[pk & 1], static_cast<uint32_t>(pk >> 1) & 1u, max_polls);
+                mbar_wait(&qfull[pk & 1], static_cast<uint32_t>(pk >> 1) & 1u);
         };
         for (int i = start, it = 0; i < end; ++i, ++it) {
             while (cs + cn <= i) {
@@ -337,6 +338,7 @@ __global__ void __launch_bounds__((kFastMaxKvHeads + 1) * 32, 1)
             }
             if (!__shfl_sync(0xffffffffu, ok, 0)) return;  // a wait ran out: the whole warp leaves
         }
+        if (lane == 0) drain(end - start);
         return;
     }
 

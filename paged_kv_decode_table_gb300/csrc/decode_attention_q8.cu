@@ -397,13 +397,15 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
         }
         const uint32_t unit_tx = 2u * unit_bytes;
         int piece = 0;
-        // on a timeout: wait (bounded) for the copies in flight, so that none writes
-        // into shared memory after the CTA is gone
+        // before every exit: wait for this warp's copies in flight, so that none writes
+        // into shared memory after the CTA is gone, whether its consumers still wait for
+        // them or have given up (bounded, but not by the limit that a test lowers: copies
+        // that were issued land)
         auto drain = [&](int it) {
             asm volatile("cp.async.wait_all;" ::: "memory");
             if (lane != 0) return;
             for (int k = max(0, it - nst); k < it; ++k)
-                mbar_wait(&full[k % nst], static_cast<uint32_t>(k / nst) & 1u, pl.polls);
+                mbar_wait(&full[k % nst], static_cast<uint32_t>(k / nst) & 1u);
         };
         // 16-byte chunks of a row of q; this lane's first one, and the step to its next one
         const int q_chunks = pl.D * static_cast<int>(sizeof(T)) / 16;
@@ -482,6 +484,7 @@ __global__ void __launch_bounds__((kQ8Warps + 1) * 32, 1)
                 parity ^= 1u;
             }
         }
+        drain(end - start);
         return;
     }
 
