@@ -553,8 +553,9 @@ size_t pkv_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D, int num_
  * device int32 [N + 1], non-decreasing, group_start[0] = 0, group_start[N] <= B;
  * sequences behind the last group, and groups of one, share nothing.  The first
  * floor(shared_lens[g] / block_size) table entries of all sequences of a group
- * must be the same (small batches are read per sequence, by each one's own
- * entries, others by one member's for all); shared_lens: device int32 [N].  A
+ * must be the same, but for members of length 0, whose entries are not read (small
+ * batches are read per sequence, by each one's own entries, others by one member's
+ * for all); shared_lens: device int32 [N].  A
  * sequence shorter than that prefix (but for length 0, which gives zeros), a
  * shared length outside the table, and everything that
  * pkv_paged_decode_attention_scored finds: zero output and

@@ -304,10 +304,27 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         int j = 0;
         for (int at = start, piece = 0; at < end && !fail; at += w.k1 - w.k0, ++piece) {
             w.to(pl, at, end);
+            // The prefix is read by the table row of the first member that has all of it: a member of length 0 or of a
+            // refused length may have anything there.  (Where no member has, any valid rows: all of them get zeros.)  The
+            // first one's length and block ids are on their way together.
             const int32_t* trow = block_tables + static_cast<size_t>(w.first) * pl.max_blocks;
-            const int nblk = w.prefix / BS;
+            int nblk = w.prefix / BS;
             auto ids = [&](int i) { return i < nblk ? trow[i] : 0; };
+            auto has_all = [&](int L) { return L >= w.prefix && static_cast<long long>(L) <= static_cast<long long>(pl.max_blocks) * BS; };
+            const int L0 = seq_lens[w.first];
             int have = (w.k0 * kPxKeys) / BS, cur = ids(have + lane), nxt = ids(have + 32 + lane);
+            if (!has_all(L0)) {
+                unsigned found = 0;
+                int m = 1;
+                for (; m < w.n; m += 32) {
+                    found = __ballot_sync(0xffffffffu, m + lane < w.n && has_all(seq_lens[w.first + min(m + lane, w.n - 1)]));
+                    if (found != 0) break;
+                }
+                if (found != 0) trow += static_cast<size_t>(m + __ffs(found) - 1) * pl.max_blocks;
+                else nblk = 0;
+                cur = ids(have + lane);
+                nxt = ids(have + 32 + lane);
+            }
             for (int kt = w.k0; kt < w.k1 && !fail; ++kt, ++j) {
                 const int s = j % kStages;
                 if ((kt * kPxKeys) / BS - have >= 32) {  // a tile is in at most five blocks

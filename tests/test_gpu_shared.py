@@ -291,3 +291,32 @@ def test_refusals():
             call(y)
     with pytest.raises(pkv.PkvError):
         call(x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("wide", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_groups_that_begin_with_members_without_the_prefix(D, wide):
+    """The prefix is read by a member that has it: rows in front of it may be padding, with anything in their tables."""
+    x = make(12, [(64, [70, 64, 100]), (160, [200] * 40 + [300, 170]), (48, [50, 49])], 8, 2, D, 16, BF, wide=wide)
+    empty = [0] + list(range(3, 3 + 36)) + [45, 46]
+    for b in empty:
+        x["lens"][b] = 0
+    x["seq_lens"] = _cu(x["lens"])
+    ref, tol = R.reference(x)
+    for junk in (-1, 10 ** 6, int(x["block_tables"][1, 0])):
+        y = dict(x, block_tables=x["block_tables"].clone())
+        y["block_tables"][empty] = junk
+        st = pkv.new_status()
+        got = call(y, status=st)
+        assert pkv.check_status(st) == 0
+        assert (got[empty] == 0).all()
+        R.check(got, ref, tol)
+    # members that are refused: one shorter than the prefix, one with a length outside the table
+    y = dict(x, block_tables=x["block_tables"].clone(), seq_lens=x["seq_lens"].clone())
+    y["block_tables"][empty] = 10 ** 6
+    y["seq_lens"][0], y["seq_lens"][3] = 30, 2 ** 31 - 1
+    st = pkv.new_status()
+    got = call(y, status=st)
+    assert pkv.check_status(st) == 4
+    assert (got[empty] == 0).all()
+    R.check(got, ref, tol)
