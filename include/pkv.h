@@ -201,14 +201,17 @@ pkv_status pkv_paged_decode_attention_noalloc(void* out, const void* q, const vo
  * in dev_status and returns instead of hanging.  This call sets, for every
  * later attention call of the process (all threads, all devices):
  *   polls       the poll budget of those waits; 0 restores the default;
- *   silent_cta  one CTA of the split-KV kernel whose loader issues no copy at
- *               all (-1: none), so that its consumers wait on stages nothing
+ *   silent_cta  one CTA of the split-KV kernel, and of the tensor-core kernels
+ *               of prefill and of shared prefixes, whose loader issues no copy
+ *               at all (-1: none), so that its consumers wait on stages nothing
  *               will fill and give up after `polls` polls, with no copy in
  *               flight.
  * With silent_cta >= 0 the output of the sequences that CTA covers is
- * undefined and dev_status reads PKV_ERR_TIMEOUT; the next call after the
- * hook is reset computes normally.  Returns PKV_ERR_INVALID_ARG for
- * silent_cta < -1.  Not synchronised with attention calls on other threads.
+ * undefined (prefill, shared prefixes, and rows that are joined from several
+ * CTAs' parts with changed scores: what they would be, or zeros) and dev_status
+ * reads PKV_ERR_TIMEOUT; the next call after the hook is reset computes
+ * normally.  Returns PKV_ERR_INVALID_ARG for silent_cta < -1.  Not synchronised
+ * with attention calls on other threads.
  */
 pkv_status pkv_test_set_wait_limit(uint32_t polls, int silent_cta);
 

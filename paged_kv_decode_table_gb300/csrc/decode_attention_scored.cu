@@ -166,6 +166,12 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
     auto finish = [] {  // before every exit
         if constexpr (kShared) asm volatile("griddepcontrol.wait;" ::: "memory");
     };
+    auto give_up = [&] {  // a wait ran out: what this CTA's range was to leave may be missing
+        if ((threadIdx.x & 31) == 0) {
+            report(status, PKV_ERR_TIMEOUT);
+            if (kShared || !pl.direct) ws.gave_up[blockIdx.x] = 1;
+        }
+    };
     // lengths, then block ids, then K and V: three dependent loads; the first two and q come to L2 while the
     // predecessor ends
     const unsigned worker = blockIdx.x * blockDim.x + threadIdx.x;
@@ -226,6 +232,7 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
         }
         __syncthreads();  // the barriers are initialised
     } else {
+        if (threadIdx.x == 0) ws.gave_up[blockIdx.x] = 0;  // (barriers follow)
         [[maybe_unused]] int from = 0, to = 0, shared = 0;  // of group threadIdx.x: asked for before the lengths' chain
         if (kEstimate && static_cast<int>(threadIdx.x) < pl.groups.N) {
             from = pl.groups.start[threadIdx.x];
@@ -373,7 +380,7 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
                 ok = mbar_wait(&qempty[pl.qslots == 2 ? piece & 1 : 0],
                                (static_cast<uint32_t>(piece >> (pl.qslots - 1)) & 1u) ^ 1u, pl.polls);
             if (!__all_sync(0xffffffffu, ok)) {
-                if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+                give_up();
                 drain(it);
                 finish();
                 return;
@@ -625,7 +632,7 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
 
     for (int i = start; i < end; ++i) {
         if (!mbar_wait(&full[stage], parity, pl.polls)) {
-            if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+            give_up();
             finish();
             return;
         }
@@ -633,7 +640,7 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
         if (mt.flags & kSFirst) {
             const int qs = pl.qslots == 2 ? piece & 1 : 0;
             if (!mbar_wait(&qfull[qs], static_cast<uint32_t>(piece >> (pl.qslots - 1)) & 1u, pl.polls)) {
-                if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+                give_up();
                 finish();
                 return;
             }
@@ -695,7 +702,7 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
                 if (slot >= d) {
                     float* t = scratch + ((slot - 1) * HV + vh) * kTile;
                     if (!mbar_wait(&mempty[warp], ph ^ 1u, pl.polls)) {
-                        if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+                        give_up();
                         finish();
                         return;
                     }
@@ -720,7 +727,7 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
                 const int from = warp + d * HV;
                 const float* t = scratch + ((slot + d - 1) * HV + vh) * kTile;
                 if (!mbar_wait(&mfull[from], ph, pl.polls)) {
-                    if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+                    give_up();
                     finish();
                     return;
                 }
@@ -801,6 +808,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = -INFINITY, l = 0.f;
     bool bad = false;
+    const int lost = ranges_gave_up(ws.gave_up, cut.f, cut.pieces, lane);
     const bool col = 4 * lane < pl.D;
     for (int p0 = 0; p0 < cut.pieces; p0 += kJoinGroup) {
         float2 ml[kJoinGroup];
@@ -831,6 +839,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             acc.w = fmaf(o[k].w, w, acc.w);
         }
     }
+    bad = bad || __any_sync(0xffffffffu, lost != 0);
     if (!col) return;
     const float inv = 1.f / l;
     const bool zero = bad || l == 0.f;
@@ -1234,17 +1243,18 @@ bool split_shape(int Hq, int Hkv, int D, int BS, int min_groups, SplitPlan& pl) 
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// [head][cuts][info of B sequences][(max, sum)][sums of products]; two partial results per CTA of R rows and, for
+// [head][cuts][ranges that gave up][info of B sequences][(max, sum)][sums of products]; two partial results per CTA of R rows and, for
 // shared prefixes, one per row of out.
 size_t split_space(const SplitPlan& pl, int P, int B, bool shared, void* base, SplitSpace* ws) {
     const size_t slots = static_cast<size_t>(2) * P * pl.R + (shared ? static_cast<size_t>(B) * pl.Hq : 0);
-    const size_t cuts = 256, info = up256(cuts + sizeof(SplitCut) * P);
+    const size_t cuts = 256, gave_up = up256(cuts + sizeof(SplitCut) * P), info = up256(gave_up + sizeof(int) * P);
     const size_t ml = up256(info + (shared ? sizeof(int2) * static_cast<size_t>(B) : 0));
     const size_t o = up256(ml + slots * sizeof(float2));
     if (ws != nullptr) {
         uint8_t* p = static_cast<uint8_t*>(base);
         ws->head = reinterpret_cast<SplitHead*>(p);
         ws->cuts = reinterpret_cast<SplitCut*>(p + cuts);
+        ws->gave_up = reinterpret_cast<int*>(p + gave_up);
         ws->info = reinterpret_cast<int2*>(p + info);
         ws->ml = reinterpret_cast<float2*>(p + ml);
         ws->o = reinterpret_cast<float*>(p + o);

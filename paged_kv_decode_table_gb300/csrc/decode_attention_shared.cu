@@ -33,8 +33,8 @@
 // heads, cap and slopes 152 us (50).
 // Tried and not kept: key tiles of 128 (P over S in tensor memory, half the barriers; 4000 clocks for 128 keys, but with a
 // longer start as fast in all); 16 softmax warps, two threads a row.
-// Every mbarrier wait is bounded; a CTA that gives up records PKV_ERR_TIMEOUT, waits (bounded) for its own TMA copies,
-// and frees its tensor memory.
+// Every mbarrier wait is bounded; a CTA that gives up records PKV_ERR_TIMEOUT, waits (bounded) for its own TMA copies and
+// MMAs, frees its tensor memory, and marks its pieces, whose rows the join then sets to zero.
 #include <cuda.h>
 #include <math.h>
 
@@ -83,6 +83,7 @@ struct Px {
 struct PxShared {  // follows the 1024-aligned operand area
     uint64_t kv_full[10], kv_empty[10];
     uint64_t q_full[kPxTiles], s_full[kPxTiles], s_free[kPxTiles], p_full[kPxTiles], o_done[kPxTiles];
+    uint64_t last[2];  // of a thread that gives up: its MMAs are complete
     uint32_t tmem_base;
     int at[7];  // where the CTA's range begins: a group as PxWalk has it
     int red[32];
@@ -100,6 +101,7 @@ struct PxHead {
 };
 struct PxSpace {
     PxHead* head;
+    int* gave_up;  // one per CTA: 1 where a wait ran out, so that its pieces may be missing
     int2* plan;   // of every group: (first key tile in the order, key tiles of a row tile)
     float2* ml;   // (max, sum): 2 slots per CTA of 256 rows, then two places per row of out
     float* o;
@@ -112,6 +114,8 @@ struct PxPlan {
     ScoreArgs sc;
     GroupArgs groups;
     int NG, units;  // of the split kernel
+    uint32_t polls;  // of a wait
+    int silent_cta;  // test hook: whose loaders issue no copy
 };
 
 // A role's walk over the CTA's pieces.
@@ -194,6 +198,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             mbar_init(&sm->s_free[t], kPxRows);
             mbar_init(&sm->p_full[t], kPxRows);
             mbar_init(&sm->o_done[t], 1);
+            mbar_init(&sm->last[t], 1);
         }
         fence_mbar_init();
         prefetch_tmap(&tmK);
@@ -209,6 +214,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
+    if (tid == 0) ws.gave_up[blockIdx.x] = 0;
     // ---- the whole work, and this CTA's range of it: key tiles [start, end)
     auto scan = [&](int v, int& total) {  // over the CTA; exclusive
         int x = v;
@@ -290,6 +296,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     const uint32_t tmem = sm->tmem_base;
 
     bool fail = false;
+    // A thread that issues MMAs and gives up waits until they are complete: tensor memory is given back behind it, and
+    // no arrival may be outstanding when the CTA exits.
+    auto land = [&](int i) {
+        tc_commit(&sm->last[i]);
+        mbar_wait(&sm->last[i], 0);
+    };
     if (idle) {
         // nothing but the tensor memory to give back
     } else if (warp == kPxWarpProd || warp == kPxWarpPV + 1 || warp == kPxWarpPV + 2) {
@@ -302,7 +314,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const int nbox = pw < 2 ? 3 : 2;
         PxWalk w(sm->at);
         int j = 0;
-        for (int at = start, piece = 0; at < end && !fail; at += w.k1 - w.k0, ++piece) {
+        const int stop = static_cast<int>(blockIdx.x) == pl.silent_cta ? start : end;
+        for (int at = start, piece = 0; at < stop && !fail; at += w.k1 - w.k0, ++piece) {
             w.to(pl, at, end);
             // The prefix is read by the table row of the first member that has all of it: a member of length 0 or of a
             // refused length may have anything there.  (Where no member has, any valid rows: all of them get zeros.)  The
@@ -332,10 +345,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     cur = nxt;
                     nxt = ids(have + 32 + lane);
                 }
-                if (lane == 0 && !mbar_wait(&sm->kv_empty[s], ((j / kStages) & 1) ^ 1)) {
-                    report(status, PKV_ERR_TIMEOUT);
-                    fail = true;
-                }
+                if (lane == 0) fail = !mbar_wait(&sm->kv_empty[s], ((j / kStages) & 1) ^ 1, pl.polls);
                 fail = __shfl_sync(0xffffffffu, fail, 0);
                 if (fail) break;
                 const int bi = pw + 3 * lane;
@@ -374,7 +384,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         }
         // no copy of this CTA may still be in flight when it exits
         if (lane == 0)
-            for (int i = max(0, j - kStages); i < j; ++i) mbar_wait(&sm->kv_full[i % kStages], (i / kStages) & 1);
+            for (int i = max(0, j - kStages); i < j; ++i) mbar_wait(&sm->kv_full[i % kStages], (i / kStages) & 1, kTcLandPolls);
     } else if (warp == kPxWarpS) {
         tc_fewer_registers();
         // ------------------------------------------------ S = Q K^T (lane 0 issues)
@@ -391,15 +401,15 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 const bool dual = w.dual(pl);
                 for (int kt = w.k0; kt < w.k1 && !fail; ++kt, ++j) {
                     const int s = j % kStages;
-                    if (!mbar_wait(&sm->kv_full[s], (j / kStages) & 1)) {
+                    if (!mbar_wait(&sm->kv_full[s], (j / kStages) & 1, pl.polls)) {
                         fail = true;
                         break;
                     }
                     const uint32_t kb = kva + s * C::kStageBytes;
                     const int ta = dual ? (kt - w.k0) & 1 : 0, tb = dual ? ta : 1;
                     for (int t = ta; t <= tb; ++t) {
-                        if ((kt - w.k0 < (dual ? 2 : 1) && !mbar_wait(&sm->q_full[t], (queries >> t) & 1u)) ||
-                            ((had >> t) & 1u && !mbar_wait(&sm->s_free[t], (free_ >> t) & 1u))) {
+                        if ((kt - w.k0 < (dual ? 2 : 1) && !mbar_wait(&sm->q_full[t], (queries >> t) & 1u, pl.polls)) ||
+                            ((had >> t) & 1u && !mbar_wait(&sm->s_free[t], (free_ >> t) & 1u, pl.polls))) {
                             fail = true;
                             break;
                         }
@@ -417,7 +427,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 }
                 queries ^= 1u | (!dual || w.k1 - w.k0 > 1 ? 2u : 0u);
             }
-            if (fail) report(status, PKV_ERR_TIMEOUT);
+            if (fail) land(0);
         }
         __syncwarp();
     } else if (warp == kPxWarpPV) {
@@ -437,7 +447,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                     const uint32_t vb = kva + s * C::kStageBytes + C::kKBytes;
                     const int ta = dual ? (kt - w.k0) & 1 : 0, tb = dual ? ta : 1;
                     for (int t = ta; t <= tb; ++t) {  // query tile 0 first: its softmax warps clear V rows
-                        if (!mbar_wait(&sm->p_full[t], (phase >> t) & 1u)) {
+                        if (!mbar_wait(&sm->p_full[t], (phase >> t) & 1u, pl.polls)) {
                             fail = true;
                             break;
                         }
@@ -456,7 +466,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             }
             // no arrival of this CTA may be outstanding when it exits: the last one follows all others
             if (!fail && !mbar_wait(&sm->kv_empty[(j - 1) % kStages], ((j - 1) / kStages) & 1)) fail = true;
-            if (fail) report(status, PKV_ERR_TIMEOUT);
+            if (fail) land(1);
         }
         __syncwarp();
     } else if (warp < 8) {
@@ -509,7 +519,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             float m_ref = -INFINITY, lsum = 0.f;
             bool broken = false;
             for (int kt = k0; kt < w.k1; kt += step, ++done) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&sm->s_full[qt], done & 1))) {  // tcgen05.ld needs the whole warp
+                if (!__all_sync(0xffffffffu, tc_wait(&sm->s_full[qt], done & 1, pl.polls))) {  // tcgen05.ld needs the whole warp
                     fail = true;
                     break;
                 }
@@ -558,7 +568,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                                    ((ls[2][0] + ls[2][1]) + (ls[3][0] + ls[3][1])));
                 // the PV of the tile before is complete: O may be rescaled and the P tile rewritten
                 if (kt > k0) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (done - 1) & 1))) {
+                    if (!__all_sync(0xffffffffu, tc_wait(&sm->o_done[qt], (done - 1) & 1, pl.polls))) {
                         fail = true;
                         break;
                     }
@@ -599,11 +609,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 next.to(pl, at + w.k1 - w.k0, end);
                 put_q(next);
             }
-            if (!fail && k0 < w.k1 && !__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (done - 1) & 1))) fail = true;
-            if (fail) {
-                if (lane == 0) report(status, PKV_ERR_TIMEOUT);
-                break;
-            }
+            if (!fail && k0 < w.k1 && !__all_sync(0xffffffffu, tc_wait(&sm->o_done[qt], (done - 1) & 1, pl.polls))) fail = true;
+            if (fail) break;
             // ---- the piece's rows: a place per row of out where it is the whole prefix, else this range's slot
             tc_fence_after();
             const bool whole = w.k0 == 0 && w.k1 == w.nt;
@@ -647,6 +654,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         }
     } else {
         tc_fewer_registers();
+    }
+    if (fail && lane == 0) {
+        report(status, PKV_ERR_TIMEOUT);
+        ws.gave_up[blockIdx.x] = 1;
     }
     // ---- every role is done with TMEM
     tc_fence_before();
@@ -717,6 +728,7 @@ __global__ void __launch_bounds__(kSjWarps * 32)
             no = (first + info.y - 1) / Wo - of + 1;
         }
     }
+    const int lost = ranges_gave_up(px.gave_up, pf, np, lane) | ranges_gave_up(ws.gave_up, of, no, lane);
     const int npx = dual ? 2 * np : np, n = npx + no;
     float acc[kCols] = {};
     float M = -INFINITY, l = 0.f;
@@ -801,6 +813,7 @@ __global__ void __launch_bounds__(kSjWarps * 32)
             for (int i = 0; i < kCols; ++i) acc[i] = fmaf(other[2 + i], f, acc[i]);
         }
     }
+    bad = bad || __any_sync(0xffffffffu, lost != 0);
     if (row0 >= rows) return;
     const bool zero = bad || l == 0.f;
     const float inv = 1.f / l;
@@ -834,15 +847,17 @@ static bool encode_pool_rows64(CUtensorMap* map, const void* pool, long long row
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [head][plan of up to B groups][(max, sum)][O]
+// [head][CTAs that gave up][plan of up to B groups][(max, sum)][O]
 static size_t px_space(int B, int Hq, int D, int P, void* base, PxSpace* ws) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t places = 2 * static_cast<size_t>(P) * kPxSlot + 2 * static_cast<size_t>(B) * Hq;
-    const size_t ml = up(256 + sizeof(int2) * static_cast<size_t>(B)), o = up(ml + places * sizeof(float2));
+    const size_t gave_up = 256, plan = up(gave_up + sizeof(int) * P);
+    const size_t ml = up(plan + sizeof(int2) * static_cast<size_t>(B)), o = up(ml + places * sizeof(float2));
     if (ws != nullptr) {
         uint8_t* p = static_cast<uint8_t*>(base);
         ws->head = reinterpret_cast<PxHead*>(p);
-        ws->plan = reinterpret_cast<int2*>(p + 256);
+        ws->gave_up = reinterpret_cast<int*>(p + gave_up);
+        ws->plan = reinterpret_cast<int2*>(p + plan);
         ws->ml = reinterpret_cast<float2*>(p + ml);
         ws->o = reinterpret_cast<float*>(p + o);
     }
@@ -951,6 +966,8 @@ extern "C" pkv_status pkv_paged_decode_attention_shared(
     px.NG = pl.NG;
     pl.TQ = px.TQ;
     px.units = pl.units;
+    px.polls = pl.polls;
+    px.silent_cta = pl.silent_cta;
     // pool rows and key tiles stay in 32 bits
     const long long tiles = (static_cast<long long>(max_blocks_per_seq) * block_size / kPxKeys + 1) * Hkv *
                             (static_cast<long long>(B) / px.TC + N);

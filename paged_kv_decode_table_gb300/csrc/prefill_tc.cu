@@ -47,7 +47,8 @@
 //    are cleared before the last PV MMAs.
 //  * Epilogue: O / sum from TMEM to the bf16 output rows.
 // Every mbarrier wait is bounded; a CTA that gives up records PKV_ERR_TIMEOUT,
-// waits (bounded) for its own TMA copies, and still frees its TMEM.
+// waits (bounded) for its own TMA copies and MMAs, frees its TMEM, and sets the
+// rows that it did not finish to zero.
 #include <cuda.h>
 #include <math.h>
 
@@ -61,6 +62,8 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn get_encode_fn();
+uint32_t attention_wait_polls();
+int attention_silent_cta();
 bool encode_pool_box_halves(CUtensorMap* map, const void* pool, int NB, int Hkv, int BS, int box_rows);
 
 constexpr int kTcDim = 128;
@@ -87,6 +90,7 @@ constexpr int kTcTmemCols = 512;             // query tile t: Q at 256 t, S at 2
 struct TcSmem {  // follows the 1024-aligned operand area
     uint64_t kv_full[kTcStages], kv_empty[kTcStages];
     uint64_t s_full[kTcQT], s_free[kTcQT], p_full[kTcQT], o_done[kTcQT];
+    uint64_t last[2];  // of a thread that gives up: its MMAs are complete
     uint32_t tmem_base;
     int b, tile, bad;
     int tbl[kTcProd][kTcWin];
@@ -140,6 +144,11 @@ struct TcSplit {
     float2* ml;
     float* o;
 };
+// Polls of a wait, and the CTA whose loaders issue no copy (test hook).
+struct TcWaits {
+    uint32_t polls;
+    int silent_cta;
+};
 
 // What bounds it: the tensor pipe.  An MMA of M 128, K 16 with A in tensor memory takes 84 clocks (N 64; 88 for N 128), with A in
 // shared memory 70 (N 128): the 16 of S and 8 of PV for 64 keys and 256 rows are 1900 clocks, a tile takes 2000-2300.  (Q in shared
@@ -155,7 +164,8 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                       const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ out,
                       const int32_t* __restrict__ block_tables, int max_blocks, const int32_t* __restrict__ seq_lens,
                       const int32_t* __restrict__ q_start, int B, int Hq, int Hkv, int BS, int NB, float scale_log2,
-                      const __grid_constant__ ScoreArgs sc, const __grid_constant__ TcSplit split, int32_t* status) {
+                      const __grid_constant__ ScoreArgs sc, const __grid_constant__ TcSplit split,
+                      const __grid_constant__ TcWaits waits, int32_t* status) {
     constexpr bool kScored = kKind != kPlain;
     const int S = kScored ? split.S : 1;  // CTAs along the keys of a pair of query tiles
     extern __shared__ uint8_t tc_raw[];
@@ -180,6 +190,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             mbar_init(&sm->s_free[t], kTcRows);
             mbar_init(&sm->p_full[t], kTcRows);
             mbar_init(&sm->o_done[t], 1);
+            mbar_init(&sm->last[t], 1);
         }
         fence_mbar_init();
         prefetch_tmap(&tmK);
@@ -335,6 +346,12 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
     tc_fence_after();
 
     bool fail = false;
+    // A thread that issues MMAs and gives up waits until they are complete: tensor memory is given back behind it, and
+    // no arrival may be outstanding when the CTA exits.
+    auto land = [&](int i) {
+        tc_commit(&sm->last[i]);
+        mbar_wait(&sm->last[i], 0);
+    };
     if ((warp == kTcWarpProd || (warp > kTcWarpPV && warp < kTcThreads / 32)) && active) {
         if constexpr (kScored) tc_fewer_registers();
         // ------------------------------------------------ producer warps 8, 11, 12
@@ -348,8 +365,9 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
         const int nbox = pw < 2 ? 3 : 2;  // boxes of this warp per tile
         int* tbl = sm->tbl[pw];
         const int32_t* trow = block_tables + static_cast<size_t>(b) * max_blocks;
-        int win0 = -kTcWin;
-        for (int j = 0; j < ntiles && !fail; ++j) {
+        int win0 = -kTcWin, j = 0;
+        const int stop = static_cast<int>(blockIdx.x) == waits.silent_cta ? 0 : ntiles;
+        for (; j < stop; ++j) {
             const int s = j % kTcStages;
             const int kt = key_tile(j + rot < ntiles ? j + rot : j + rot - ntiles);
             const int kb0 = (kt * kTcKeys) / BS, kb1 = min(nblk_used - 1, (kt * kTcKeys + kTcKeys - 1) / BS);
@@ -359,10 +377,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                 for (int i = lane; i < kTcWin; i += 32) tbl[i] = win0 + i < nblk_used ? trow[win0 + i] : 0;
                 __syncwarp();
             }
-            if (lane == 0 && !mbar_wait(&sm->kv_empty[s], ((j / kTcStages) & 1) ^ 1)) {
-                report(status, PKV_ERR_TIMEOUT);
-                fail = true;
-            }
+            if (lane == 0) fail = !mbar_wait(&sm->kv_empty[s], ((j / kTcStages) & 1) ^ 1, waits.polls);
             fail = __shfl_sync(0xffffffffu, fail, 0);
             if (fail) break;
             const int bi = pw + 3 * lane;
@@ -396,8 +411,8 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
         }
         // no copy of this CTA may still be in flight when it exits
         if (lane == 0)
-            for (int j = max(0, ntiles - kTcStages); j < ntiles; ++j)
-                mbar_wait(&sm->kv_full[j % kTcStages], (j / kTcStages) & 1);
+            for (int i = max(0, j - kTcStages); i < j; ++i)
+                mbar_wait(&sm->kv_full[i % kTcStages], (i / kTcStages) & 1, kTcLandPolls);
     } else if (warp == kTcWarpS && active) {
         if constexpr (kScored) tc_fewer_registers();
         // ------------------------------------------------ S = Q K^T for both query tiles (lane 0 issues)
@@ -409,14 +424,14 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             const uint32_t kva = smem_u32(sKV);
             for (int j = 0; j < ntiles && !fail; ++j) {
                 const int s = j % kTcStages;
-                if (!mbar_wait(&sm->kv_full[s], (j / kTcStages) & 1)) {
+                if (!mbar_wait(&sm->kv_full[s], (j / kTcStages) & 1, waits.polls)) {
                     fail = true;
                     break;
                 }
                 const uint32_t kb = kva + s * kTcStageBytes;
                 const int ta = dual ? j & 1 : 0, tb = dual ? ta : kTcQT - 1, u = dual ? j >> 1 : j;
                 for (int t = ta; t <= tb; ++t) {
-                    if (u >= 1 && !mbar_wait(&sm->s_free[t], (u - 1) & 1)) {
+                    if (u >= 1 && !mbar_wait(&sm->s_free[t], (u - 1) & 1, waits.polls)) {
                         fail = true;
                         break;
                     }
@@ -428,7 +443,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                     tc_commit(&sm->s_full[t]);
                 }
             }
-            if (fail) report(status, PKV_ERR_TIMEOUT);
+            if (fail) land(0);
         }
         __syncwarp();
     } else if (warp == kTcWarpPV && active) {
@@ -446,7 +461,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                 const uint32_t vb = kva + s * kTcStageBytes + kTcKBytes;
                 const int ta = dual ? j & 1 : 0, tb = dual ? ta : kTcQT - 1, u = dual ? j >> 1 : j;
                 for (int t = ta; t <= tb; ++t) {  // query tile 0 first: its softmax warps clear V rows past L
-                    if (!mbar_wait(&sm->p_full[t], u & 1)) {
+                    if (!mbar_wait(&sm->p_full[t], u & 1, waits.polls)) {
                         fail = true;
                         break;
                     }
@@ -463,7 +478,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             }
             // no arrival of this CTA may be outstanding when it exits: the last one follows all others
             if (!fail && ntiles > 0 && !mbar_wait(&sm->kv_empty[(ntiles - 1) % kTcStages], ((ntiles - 1) / kTcStages) & 1)) fail = true;
-            if (fail) report(status, PKV_ERR_TIMEOUT);
+            if (fail) land(1);
         }
         __syncwarp();
     } else if (softmax_warp && active) {
@@ -478,7 +493,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
         if constexpr (kScored) slope = kKind & kSloped ? sc.slopes[qh] * kLog2e : 0.f;
         for (int u = 0; u < mine; ++u) {
             const int j = (u << step) + (step & qt);
-            if (!__all_sync(0xffffffffu, mbar_wait(&sm->s_full[qt], u & 1))) {  // tcgen05.ld needs the whole warp
+            if (!__all_sync(0xffffffffu, tc_wait(&sm->s_full[qt], u & 1, waits.polls))) {  // tcgen05.ld needs the whole warp
                 fail = true;
                 break;
             }
@@ -535,7 +550,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                                ((ls[2][0] + ls[2][1]) + (ls[3][0] + ls[3][1])));
             // the PV of the tile before is complete: O may be rescaled and the P tile rewritten
             if (u > 0) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (u - 1) & 1))) {
+                if (!__all_sync(0xffffffffu, tc_wait(&sm->o_done[qt], (u - 1) & 1, waits.polls))) {
                     fail = true;
                     break;
                 }
@@ -574,7 +589,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             mbar_arrive(&sm->p_full[qt]);
         }
         // ---- epilogue: O / sum of the last PV
-        if (!fail && mine > 0 && !__all_sync(0xffffffffu, mbar_wait(&sm->o_done[qt], (mine - 1) & 1))) fail = true;
+        if (!fail && mine > 0 && !__all_sync(0xffffffffu, tc_wait(&sm->o_done[qt], (mine - 1) & 1, waits.polls))) fail = true;
         // dual: query tile 1's result goes through the ring (both are done with it) to query tile 0, whose rows take
         // own O + other O' with the factors below
         [[maybe_unused]] float own = 1.f, other = 0.f;
@@ -585,9 +600,9 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                 tc_fence_after();
                 softmax_barrier();
                 if (qt == 1) {
-                    ends[r] = make_float2(m_ref, lsum);
+                    ends[r] = make_float2(m_ref, fail ? -1.f : lsum);
 #pragma unroll 1
-                    for (int cc = 0; mine > 0 && cc < kTcDim / 32; ++cc) {
+                    for (int cc = 0; mine > 0 && !fail && cc < kTcDim / 32; ++cc) {
                         uint32_t o[32];
                         tc_ld32(tq + lrow + 128 + 32 * cc, o);
 #pragma unroll
@@ -599,6 +614,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                 softmax_barrier();
                 if (qt == 0) {
                     const float2 e = ends[r];
+                    fail = fail || e.y < 0.f;  // (of a whole warp)
                     const float m_new = fmaxf(m_ref, e.x), mu = m_new == -INFINITY ? 0.f : m_new;
                     own = tc_ex2(m_ref - mu);
                     other = tc_ex2(e.x - mu);
@@ -620,9 +636,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                 }
             }
         };
-        if (fail) {
-            if (lane == 0) report(status, PKV_ERR_TIMEOUT);
-        } else if (!dual || qt == 0) {
+        if (!fail && (!dual || qt == 0)) {
             tc_fence_after();
             if (S > 1) {
                 const size_t at = row_valid ? (static_cast<size_t>(t0 + tl) * Hq + qh) * S + share : 0;
@@ -663,6 +677,16 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
         }
     } else if (kScored && active) {
         tc_fewer_registers();
+    }
+    if (fail) {
+        if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+        // what the row's results are to be made of may be missing: zeros
+        if (row_valid && S > 1) {
+            split.ml[(static_cast<size_t>(t0 + tl) * Hq + qh) * S + share] = make_float2(-INFINITY, -1.f);
+        } else if (row_valid) {
+            uint4* o = reinterpret_cast<uint4*>(out + (static_cast<size_t>(t0 + tl) * Hq + qh) * kTcDim);
+            for (int c = 0; c < 16; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
+        }
     }
     // ---- every role is done with TMEM
     tc_fence_before();
@@ -797,7 +821,8 @@ cudaError_t launch_prefill_tc(void* out, const void* q, const void* k_cache, con
     const float scale_log2 = scale * 1.4426950408889634f;
     err = cudaLaunchKernelEx(&cfg, kern, tmK, tmV, static_cast<const __nv_bfloat16*>(q),
                              static_cast<__nv_bfloat16*>(out), block_tables, max_blocks, seq_lens, q_start, B, Hq, Hkv,
-                             BS, NB, scale_log2, scored != nullptr ? *scored : ScoreArgs{}, split, status);
+                             BS, NB, scale_log2, scored != nullptr ? *scored : ScoreArgs{}, split,
+                             TcWaits{attention_wait_polls(), attention_silent_cta()}, status);
     if (err != cudaSuccess || split.S == 1) return err != cudaSuccess ? err : cudaGetLastError();
     cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(T_new) * Hq + 3) / 4), 1, 1);
     cfg.blockDim = dim3(128, 1, 1);

@@ -223,6 +223,16 @@ __device__ __forceinline__ void tc_scores(uint32_t (&sr)[kChunks][32], int dist,
     }
 }
 
+// mbar_wait of a softmax warp, with the first poll apart from the loop: with the limit as an argument the loop alone costs the
+// key tiles 3% (16 chunks of up to 512, capped: 478 us for 465, 463 with a constant limit).
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, uint32_t polls) {
+    return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, polls);
+}
+
+// Polls for copies that were issued to land, which takes microseconds: some ten milliseconds.  Where another of a stage's
+// loading warps gave up, its arrival never comes, and the wait runs out although the copies have landed.
+constexpr uint32_t kTcLandPolls = 1u << 17;
+
 // Registers move from the warps that issue copies and MMAs to those of the softmax: 512 threads are launched with 128
 // each, two warpgroups of softmax take 176, the two others keep 80.
 __device__ __forceinline__ void tc_more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 176;"); }

@@ -67,3 +67,24 @@ def test_decode_of_the_8_bit_cache(lens):
     q = torch.randn(len(lens), 32, 128, generator=g).bfloat16()
     args = [t.cuda() for t in (q, k, v, ks, vs, bt, torch.tensor(lens, dtype=torch.int32))]
     short(lambda st: pkv.paged_decode_attention_q8(*args, status=st))
+
+
+@pytest.mark.parametrize("D,members", [(128, 5), (128, 70), (64, 5)])
+def test_shared_prefixes(D, members):
+    x = R.make(5, [1000 + 10 * i for i in range(members)], 16, 4, D, 16, BF)
+    bt = x["block_tables"]
+    bt[:, :60] = bt[0, :60]
+    more = max(0, (48 << 20) // (4 * members * 16 * 4 * D) + 1 - bt.shape[1])  # so that the prefix is read once
+    bt = torch.cat([bt, torch.full((members, more), -1, dtype=torch.int32, device="cuda")], 1)
+    groups = [torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, members], [960])]
+    short(lambda st: pkv.paged_decode_attention_shared(x["q"], x["k_cache"], x["v_cache"], bt, x["seq_lens"], *groups,
+                                                       softcap=9.0, status=st), 4)
+
+
+@pytest.mark.parametrize("chunks,before", [([40], 3000), ([3], 3000), ([500, 70, 130] * 16, 600)])
+@pytest.mark.parametrize("kw", [None, dict(softcap=9.0)])
+def test_prefill(chunks, before, kw):
+    x = R.make(6, [n + before for n in chunks], 16, 4, 128, 16, BF, chunks=chunks)
+    a = [x[k] for k in ("q", "k_cache", "v_cache", "block_tables", "seq_lens", "q_start")]
+    call = pkv.paged_prefill_attention if kw is None else pkv.paged_prefill_attention_scored
+    short(lambda st: call(*a, status=st, **(kw or {})), 4)
