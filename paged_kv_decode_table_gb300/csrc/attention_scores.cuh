@@ -5,6 +5,12 @@
 //   s = u + slopes[qh] (j - pos)  (slopes given),  else u
 // and key j < L takes part where j < prefix, or j <= pos and (window <= 0 or j > pos - window).
 // The kernels work with s log2(e), so that a weight is one exp2.
+//
+// A softmax stays what it is when a constant is added to a row's scores, so the bias is measured from the key that it
+// favours most, the row's first one that takes part where the slope is negative and its last one otherwise, and not from
+// pos.  It is 0 there and falls from there on: keys that it makes matter have a small one.  Measured from pos, a
+// slope of -0.5 would give the heaviest keys of 131072 a score of -95000, whose float32 neighbours lie 2^-7 apart.  All
+// parts of a row that are joined later measure from the same key.
 #pragma once
 
 #include <math.h>
@@ -43,6 +49,7 @@ inline bool overlap(const void* out, const void* q, size_t bytes) {
 struct Seen {
     int L, lo, pfx;
     __device__ __forceinline__ bool at(int j) const { return j < L && (j >= lo || j < pfx); }
+    __device__ __forceinline__ int first() const { return pfx > 0 ? 0 : lo; }
 };
 __device__ __forceinline__ Seen decode_seen(const ScoreArgs& sa, int b, int L) {
     Seen s{L, 0, 0};

@@ -493,7 +493,9 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
                 for (int n = 0; n < kN; ++n) mma_bf16_16816(s[n][c & 1], a, qb[n][c][0], qb[n][c][1]);
             }
             // ---- scores
-            const float dist = static_cast<float>(p0[k] + g - (mt.L - 1));
+            // the bias's distances: from the last key, and from the sequence's first one that takes part
+            const float dist = static_cast<float>(p0[k] + g - (mt.L - 1)),
+                        dist_first = static_cast<float>(p0[k] + g - (kShared ? 0 : seen.first()));
             if (capped) {
                 float z[kN][4];
                 bool large = false;
@@ -525,7 +527,8 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
             for (int n = 0; n < kN; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    x[k][n][e] = fmaf(slope[n][e & 1], dist + static_cast<float>(8 * (e >> 1)), x[k][n][e]);
+                    x[k][n][e] = fmaf(slope[n][e & 1], (slope[n][e & 1] < 0.f ? dist_first : dist) + static_cast<float>(8 * (e >> 1)),
+                                      x[k][n][e]);
             if (part[k]) {
                 const bool in0 = seen.at(p0[k] + g), in1 = seen.at(p0[k] + g + 8);
 #pragma unroll
@@ -1022,12 +1025,12 @@ __global__ void __launch_bounds__(kGenThreads)
                     s[1][0] = fmaf(a.x, w1.x, fmaf(a.y, w1.y, s[1][0]));
                     s[1][1] = fmaf(a.z, w1.z, fmaf(a.w, w1.w, s[1][1]));
                 }
-                const float away = static_cast<float>(position(t * kGenPos + lane) - (L - 1));
+                const int j = position(t * kGenPos + lane);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     x[e] = s[e][0] + s[e][1];
                     x[e] = pl.sc.cap_log2 > 0.f ? pl.sc.cap_log2 * tanhf(x[e] * pl.sc.in) : x[e] * pl.sc.mul;
-                    x[e] = fmaf(slope[e], away, x[e]);
+                    x[e] = fmaf(slope[e], static_cast<float>(j - (slope[e] < 0.f ? seen.first() : L - 1)), x[e]);
                 }
             }
             float mx[2] = {x[0], x[1]};

@@ -514,8 +514,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             const bool valid = rm < pl.TQ && member < w.n;
             const int b = w.first + (valid ? member : 0);
             const int prefix = w.prefix;
-            [[maybe_unused]] const int pos = kSlope && valid ? seq_lens[b] - 1 : 0;
             [[maybe_unused]] const float slope = kSlope ? pl.sc.slopes[qh] * kLog2e : 0.f;
+            [[maybe_unused]] const int from = kSlope && valid && !(slope < 0.f) ? seq_lens[b] - 1 : 0;  // the bias is 0 there
             float m_ref = -INFINITY, lsum = 0.f;
             bool broken = false;
             for (int kt = k0; kt < w.k1; kt += step, ++done) {
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 tc_fence_before();
                 mbar_arrive(&sm->s_free[qt]);  // S may take the next tile
                 const int kbase = kt * kPxKeys;
-                if constexpr (kScored) tc_scores<kCap, kSlope>(sr, kbase - pos, slope, pl.sc);
+                if constexpr (kScored) tc_scores<kCap, kSlope>(sr, kbase - from, slope, pl.sc);
                 const bool tail = kbase + kPxKeys > prefix;
                 if (tail) {
 #pragma unroll

@@ -118,13 +118,13 @@ __device__ __forceinline__ int tc_tiles_longer(int n, int L, int TC, int v) {
 }
 
 // The 64 products of a row with the keys from kbase on become scores in the log2 domain (without cap and slopes they stay
-// products, which the softmax scales), -infinity where the row at position `pos` does not see the key.  first, last: the positions of the query tile's rows; slope: of the row's
-// head, times log2(e).
+// products, which the softmax scales), -infinity where the row at position `pos` does not see the key.  from: the key that the
+// row's bias is measured from; first, last: the positions of the query tile's rows; slope: of the row's head, times log2(e).
 template <int kKind>
-__device__ __forceinline__ void score_tile(uint32_t (&sr)[2][32], int kbase, int pos, int first, int last, int pfx,
+__device__ __forceinline__ void score_tile(uint32_t (&sr)[2][32], int kbase, int pos, int from, int first, int last, int pfx,
                                            float slope, const ScoreArgs& sc) {
     if constexpr ((kKind & (kCapped | kSloped)) != 0)
-        tc_scores<(kKind & kCapped) != 0, (kKind & kSloped) != 0>(sr, kbase - pos, slope, sc);
+        tc_scores<(kKind & kCapped) != 0, (kKind & kSloped) != 0>(sr, kbase - from, slope, sc);
     // some key is hidden from some row of the query tile
     if (kbase + kTcKeys > pfx && (kbase + kTcKeys - 1 > first || (sc.window > 0 && kbase <= last - sc.window))) {
         const int lo = sc.window > 0 ? pos - sc.window + 1 - kbase : -kbase, hi = pos - kbase, near = pfx - kbase;
@@ -491,6 +491,9 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
         float m_ref = -INFINITY, lsum = 0.f;
         [[maybe_unused]] float slope = 0.f;
         if constexpr (kScored) slope = kKind & kSloped ? sc.slopes[qh] * kLog2e : 0.f;
+        // the key that the bias is measured from: the last one that the row sees, or the first
+        [[maybe_unused]] int from = max(pos, pfx - 1);
+        if ((kKind & kSloped) != 0 && slope < 0.f) from = pfx > 0 || sc.window <= 0 ? 0 : max(0, pos - sc.window + 1);
         for (int u = 0; u < mine; ++u) {
             const int j = (u << step) + (step & qt);
             if (!__all_sync(0xffffffffu, tc_wait(&sm->s_full[qt], u & 1, waits.polls))) {  // tcgen05.ld needs the whole warp
@@ -505,7 +508,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             mbar_arrive(&sm->s_free[qt]);  // S may take the next tile
             const int kt = key_tile(j + rot < ntiles ? j + rot : j + rot - ntiles);
             const int kbase = kt * kTcKeys;
-            if constexpr (kScored) score_tile<kKind>(sr, kbase, pos, p0t, min(p0t + TQ, p0 + nt) - 1, pfx, slope, sc);
+            if constexpr (kScored) score_tile<kKind>(sr, kbase, pos, from, p0t, min(p0t + TQ, p0 + nt) - 1, pfx, slope, sc);
             // maximum of the raw scores (the scale is positive), eight chains;
             // the causal mask only on tiles that reach past the query tile's first position
             // (three-input maxima: two scores per instruction, four chains)

@@ -139,7 +139,7 @@ __device__ __forceinline__ uint64_t tc_add2(uint64_t a, uint64_t b) {
 }
 
 // The products of a row with a tile's keys become scores in the log2 domain.  dist: the first key's position less
-// the row's; slope: of the row's head, times log2(e).  All lanes of the warp take part.  Four pairs go through each
+// that of the key that the row's bias is measured from; slope: of the row's head, times log2(e).  All lanes of the warp take part.  Four pairs go through each
 // operation together: their chains hide one another's latency.
 template <bool kCap, bool kSlope, int kChunks>
 __device__ __forceinline__ void tc_scores(uint32_t (&sr)[kChunks][32], int dist, float slope, const ScoreArgs& sc) {
@@ -147,7 +147,7 @@ __device__ __forceinline__ void tc_scores(uint32_t (&sr)[kChunks][32], int dist,
     auto at = [&](int c) -> uint32_t& { return sr[c >> 5][c & 31]; };
     auto both = [](float v) { return tc_pair(v, v); };
     [[maybe_unused]] const uint64_t slope2 = both(slope), step2 = both(2.f * kBlock);
-    [[maybe_unused]] uint64_t away[kBlock];  // positions of the block's keys less the row's, exact
+    [[maybe_unused]] uint64_t away[kBlock];  // positions of the block's keys less that key's, exact up to 2^24
     auto far = [&]() {
 #pragma unroll
         for (int k = 0; k < kBlock; ++k) away[k] = tc_pair(static_cast<float>(dist + 2 * k), static_cast<float>(dist + 2 * k + 1));
