@@ -161,9 +161,9 @@ struct TcWaits {
 template <int kKind>
 __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                      const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ out,
-                      const int32_t* __restrict__ block_tables, int max_blocks, const int32_t* __restrict__ seq_lens,
-                      const int32_t* __restrict__ q_start, int B, int Hq, int Hkv, int BS, int NB, float scale_log2,
+                      const __nv_bfloat16* q, __nv_bfloat16* out,
+                      const int32_t* block_tables, int max_blocks, const int32_t* seq_lens,
+                      const int32_t* q_start, int B, int Hq, int Hkv, int BS, int NB, float scale_log2,
                       const __grid_constant__ ScoreArgs sc, const __grid_constant__ TcSplit split,
                       const __grid_constant__ TcWaits waits, int32_t* status) {
     constexpr bool kScored = kKind != kPlain;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
             uint32_t w[32];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                const uint4 v = row_valid ? __ldg(src + 8 * hv + c) : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 v = row_valid ? src[8 * hv + c] : make_uint4(0u, 0u, 0u, 0u);
                 w[4 * c] = v.x;
                 w[4 * c + 1] = v.y;
                 w[4 * c + 2] = v.z;

@@ -14,3 +14,7 @@ def test_kernels_that_start_early_use_no_read_only_loads(name):
         code = re.sub(r"//[^\n]*", "", f.read())
     assert "griddepcontrol.wait" in code
     assert not re.findall(r"__ldg\b|ld\.global\.nc|__restrict__", code)
+
+
+def test_prefill_uses_no_read_only_loads():
+    test_kernels_that_start_early_use_no_read_only_loads("prefill_tc.cu")
