@@ -74,9 +74,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 // tanh(x), x = scale t / cap.  For |x| <= 1, x times a polynomial in x^2: the minimax one of five for the relative
 // error, 2^-20.7 of tanh(x) (found by linear programming on a grid), so that a small score keeps its relative accuracy
-// whatever the cap is.  Beyond, 1 - 2 / (e^(2x) + 1), off by about 2^-23; e^(2x) = infinity gives 1.  The kernels vote:
-// the polynomial (eight operations on the FMA pipe) where all scores of a warp's tile are within the cap, else the
-// second form (two on the slower special-function pipe) for all of them.
+// whatever the cap is.  Beyond, 1 - 2 / (e^(2x) + 1), off by about 2^-23 and relatively accurate for these x only; e^(2x) =
+// infinity gives 1.  The kernels vote: where all scores of a warp's tile are within the cap only the polynomial is
+// computed (eight operations on the FMA pipe), else both (the second form is two on the slower special-function pipe), and
+// every score takes its own: what it becomes does not depend on the tile's others, hidden ones among them.
 constexpr float kTanh0 = 0.99999941f, kTanh1 = -0.33329042f, kTanh2 = 0.13281434f, kTanh3 = -0.05160567f,
                 kTanh4 = 0.01674311f, kTanh5 = -0.00306706f;
 __device__ __forceinline__ float tanh_within(float x) {

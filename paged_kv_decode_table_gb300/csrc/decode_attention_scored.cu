@@ -510,7 +510,8 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
 #pragma unroll
                     for (int n = 0; n < kN; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[k][n][e] = pl.sc.cap_log2 * tanh_beyond(z[n][e]);
+                        for (int e = 0; e < 4; ++e)
+                            x[k][n][e] = pl.sc.cap_log2 * (fabsf(z[n][e]) > 1.f ? tanh_beyond(z[n][e]) : tanh_within(z[n][e]));
                 } else {
 #pragma unroll
                     for (int n = 0; n < kN; ++n)

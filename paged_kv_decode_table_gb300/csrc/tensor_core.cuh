@@ -175,37 +175,65 @@ __device__ __forceinline__ void tc_scores(uint32_t (&sr)[kChunks][32], int dist,
 #pragma unroll
         for (int c = 0; c < 32 * kChunks; c += 2)
             big[(c >> 1) & 3] = tc_max3(big[(c >> 1) & 3], fabsf(__uint_as_float(at(c))), fabsf(__uint_as_float(at(c + 1))));
-        const uint64_t in2 = both(sc.in), cap2 = both(sc.cap_log2);
+        const uint64_t in2 = both(sc.in);
+        // x and cap log2(e) tanh(x) / x of the pairs from c on, for scores within the cap
+        auto within = [&](uint64_t (&x)[kBlock], uint64_t (&p)[kBlock], const uint64_t (&coef)[6], int c) {
+            uint64_t w[kBlock];
+#pragma unroll
+            for (int k = 0; k < kBlock; ++k) x[k] = tc_mul2(tc_pair(at(c + 2 * k), at(c + 2 * k + 1)), in2);
+#pragma unroll
+            for (int k = 0; k < kBlock; ++k) w[k] = tc_mul2(x[k], x[k]);
+#pragma unroll
+            for (int k = 0; k < kBlock; ++k) p[k] = tc_fma2(coef[5], w[k], coef[4]);
+#pragma unroll
+            for (int e = 3; e >= 0; --e)
+#pragma unroll
+                for (int k = 0; k < kBlock; ++k) p[k] = tc_fma2(p[k], w[k], coef[e]);
+        };
+        // (The coefficients belong to the branches: ahead of both they cost 9% of a long capped prefix.)
         if (__all_sync(0xffffffffu, !(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])) * sc.in > 1.f))) {
             const uint64_t coef[6] = {both(kTanh0 * sc.cap_log2), both(kTanh1 * sc.cap_log2), both(kTanh2 * sc.cap_log2),
                                       both(kTanh3 * sc.cap_log2), both(kTanh4 * sc.cap_log2), both(kTanh5 * sc.cap_log2)};
 #pragma unroll
             for (int c = 0; c < 32 * kChunks; c += 2 * kBlock) {
-                uint64_t x[kBlock], w[kBlock], p[kBlock];
-#pragma unroll
-                for (int k = 0; k < kBlock; ++k) x[k] = tc_mul2(tc_pair(at(c + 2 * k), at(c + 2 * k + 1)), in2);
-#pragma unroll
-                for (int k = 0; k < kBlock; ++k) w[k] = tc_mul2(x[k], x[k]);
-#pragma unroll
-                for (int k = 0; k < kBlock; ++k) p[k] = tc_fma2(coef[5], w[k], coef[4]);
-#pragma unroll
-                for (int e = 3; e >= 0; --e)
-#pragma unroll
-                    for (int k = 0; k < kBlock; ++k) p[k] = tc_fma2(p[k], w[k], coef[e]);
+                uint64_t x[kBlock], p[kBlock];
+                within(x, p, coef, c);
                 finish(x, p, c);
             }
         } else {
+            const uint64_t coef[6] = {both(kTanh0 * sc.cap_log2), both(kTanh1 * sc.cap_log2), both(kTanh2 * sc.cap_log2),
+                                      both(kTanh3 * sc.cap_log2), both(kTanh4 * sc.cap_log2), both(kTanh5 * sc.cap_log2)};
 #pragma unroll
             for (int c = 0; c < 32 * kChunks; c += 2 * kBlock) {
-                uint64_t t[kBlock], b[kBlock];
+                uint64_t x[kBlock], p[kBlock];
+                within(x, p, coef, c);
+                float most = 0.f;
 #pragma unroll
                 for (int k = 0; k < kBlock; ++k) {
                     uint32_t x0, x1;
-                    tc_unpair(x0, x1, tc_mul2(tc_pair(at(c + 2 * k), at(c + 2 * k + 1)), in2));
-                    t[k] = tc_pair(tanh_beyond(__uint_as_float(x0)), tanh_beyond(__uint_as_float(x1)));
-                    b[k] = cap2;
+                    tc_unpair(x0, x1, x[k]);
+                    most = tc_max3(most, fabsf(__uint_as_float(x0)), fabsf(__uint_as_float(x1)));
                 }
-                finish(t, b, c);
+                if (!__any_sync(0xffffffffu, most > 1.f)) {  // the block is within the cap
+                    finish(x, p, c);
+                    continue;
+                }
+#pragma unroll
+                for (int k = 0; k < kBlock; ++k) {  // tanh(x) and cap log2(e) instead, for scores that are beyond it
+                    uint32_t xe[2], pe[2];
+                    tc_unpair(xe[0], xe[1], x[k]);
+                    tc_unpair(pe[0], pe[1], p[k]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float f = __uint_as_float(xe[e]), t = tanh_beyond(f);
+                        const bool large = fabsf(f) > 1.f;
+                        xe[e] = large ? __float_as_uint(t) : xe[e];
+                        pe[e] = large ? __float_as_uint(sc.cap_log2) : pe[e];
+                    }
+                    x[k] = tc_pair(xe[0], xe[1]);
+                    p[k] = tc_pair(pe[0], pe[1]);
+                }
+                finish(x, p, c);
             }
         }
     } else {
