@@ -491,8 +491,8 @@ pkv_status pkv_paged_decode_attention_q8(void* out, const void* q, const void* k
  * sight of every query whatever the window is, and of a prefill chunk's queries
  * before them too (a prefix that attends in both directions; its keys have to be
  * in the cache).  softcap negative, NaN or subnormal, or scale / softcap or softcap *
- * log2(e) out of float32's range, or an out that overlaps q: PKV_ERR_INVALID_ARG.  A
- * table wider than 0x7fff0000 positions: PKV_ERR_UNSUPPORTED.
+ * log2(e) out of the range of float32's normal numbers, or an out that overlaps q:
+ * PKV_ERR_INVALID_ARG.  A table wider than 0x7fff0000 positions: PKV_ERR_UNSUPPORTED.
  * ---------------------------------------------------------------------------
  */
 

@@ -29,12 +29,14 @@ struct ScoreArgs {
     int window;                  // <= 0: none
     const int32_t* prefix_lens;  // [B] or NULL
 };
-// False where a number is out of range: the cap negative, NaN or subnormal, or a product of the two not finite.
+// False where a number is out of range: the cap negative, NaN or subnormal, scale / cap subnormal (in the products with it
+// scores would lose their digits, and below 2^-149 be all 0), or a product of the two not finite.
 inline bool make_scores(ScoreArgs* sa, float scale, int D, float cap, const float* slopes, int window,
                         const int32_t* prefix_lens) {
     if (!(scale > 0.f)) scale = 1.0f / sqrtf(static_cast<float>(D));
     *sa = ScoreArgs{scale * kLog2e, cap > 0.f ? scale / cap : 0.f, cap * kLog2e, slopes, window, prefix_lens};
-    return (cap == 0.f || cap >= 1.17549435e-38f) && sa->mul <= 3.0e38f && sa->in <= 3.0e38f && sa->cap_log2 <= 3.0e38f;
+    constexpr float kNormal = 1.17549435e-38f;
+    return (cap == 0.f || (cap >= kNormal && sa->in >= kNormal)) && sa->mul <= 3.0e38f && sa->in <= 3.0e38f && sa->cap_log2 <= 3.0e38f;
 }
 
 // Positions stay in 32 bits, with a few tiles to spare.

@@ -140,3 +140,13 @@ def test_shared_groups_keeps_long_prefixes(lib):
     pool.append(6)
     start, shared_lens = (t.tolist() for t in pool.shared_groups([0, 6, 7]))
     assert start == [0, 3] and shared_lens == [4]
+
+
+def test_cap_and_scale_in_the_range_of_normal_numbers(lib):
+    """scale / cap in float32 is what products are multiplied by: subnormal it loses digits, and 0 makes all scores equal."""
+    for call in (decode, shared, prefill):
+        more = dict(N=0) if call is shared else {}
+        for bad in (dict(cap=1e38, scale=1e-8), dict(cap=1e35, scale=1e-6), dict(cap=2e38)):  # (the default scale is below 1)
+            assert call(lib, B=0, **more, **bad) == 1, bad
+        for good in (dict(cap=1e30), dict(cap=1e30, scale=1e-7), dict(cap=2e38, scale=3.0), dict(scale=1e-40)):
+            assert call(lib, B=0, **more, **good) == 0, good
