@@ -556,12 +556,13 @@ size_t pkv_decode_shared_workspace_bytes(int B, int Hq, int Hkv, int D, int num_
  * device int32 [N + 1], non-decreasing, group_start[0] = 0, group_start[N] <= B;
  * sequences behind the last group, and groups of one, share nothing.  The first
  * floor(shared_lens[g] / block_size) table entries of all sequences of a group
- * must be the same, but for members of length 0, whose entries are not read (small
- * batches are read per sequence, by each one's own entries, others by one member's
- * for all); shared_lens: device int32 [N].  A
- * sequence shorter than that prefix (but for length 0, which gives zeros), a
- * shared length outside the table, and everything that
- * pkv_paged_decode_attention_scored finds: zero output and
+ * must be the same, but for members of length 0, whose entries are not read;
+ * shared_lens: device int32 [N].  A prefix is read by one member's entries for all,
+ * or, where that takes less time, by each one's own: batches of at most 48 MB of
+ * cache, counted by the table's width, and those with N > B / 2 groups (empty ones
+ * counted) are read per sequence.  A sequence shorter than its group's prefix (but
+ * for length 0, which gives zeros), a shared length outside the table, and
+ * everything that pkv_paged_decode_attention_scored finds: zero output and
  * PKV_ERR_DEVICE_BOUNDS, for every sequence where group_start is none.  N may be 0.
  * bf16, D = 64 or 128, block_size a multiple of 16, Hq / Hkv <= 128, 16-byte
  * aligned q, out and pools, fewer than 2^31 pool rows (else PKV_ERR_UNSUPPORTED:
@@ -639,11 +640,14 @@ pkv_status pkv_qk_norm_rope_append(void* q_out, const void* q, int64_t q_stride,
  *   shared_groups cuts seqs[0..n) into runs of neighbours that share leading
  *                blocks, as pkv_paged_decode_attention_shared takes them: a run
  *                goes on while its sequences have at least min_blocks (>= 1)
- *                whole leading blocks in common.  Host int32 group_start [n + 1]
- *                and shared_lens [n] (tokens, whole blocks; 0 for a run of one)
- *                are filled up to *n_groups, of which the caller passes on
- *                group_start[0 .. *n_groups].  A block is whole where every
- *                sequence of the run has filled it.
+ *                whole leading blocks in common and the blocks that reading them
+ *                once saves, (members - 1) * common, do not become fewer (a
+ *                neighbour that has little in common does not cost a run its long
+ *                prefix).  Host int32 group_start [n + 1] and shared_lens [n]
+ *                (tokens, whole blocks; 0 for a run of one) are filled up to
+ *                *n_groups, of which the caller passes on group_start[0 ..
+ *                *n_groups].  A block is whole where every sequence of the run
+ *                has filled it.
  *   num_free / refcount / seq_length report state (-1 on a bad argument).
  */
 typedef struct pkv_block_pool pkv_block_pool;

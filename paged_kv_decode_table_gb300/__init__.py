@@ -1043,8 +1043,9 @@ def paged_decode_attention_shared(q, k_cache, v_cache, block_tables, seq_lens, g
 
     Sequences group_start[g] .. group_start[g + 1] - 1 (int32 [N + 1]) have the same
     first shared_lens[g] // block_size entries (int32 [N]) in their tables, as
-    BlockPool.shared_groups finds them.  Without `workspace` one is allocated for
-    the call."""
+    BlockPool.shared_groups finds them; members of length 0 (padding) may have any.
+    Small batches, by the table's width, and such with more than B / 2 groups are
+    read per sequence.  Without `workspace` one is allocated for the call."""
     r = (_calls or _native()).attend_shared(q, k_cache, v_cache, block_tables, seq_lens, group_start, shared_lens,
                                             softcap, slopes, out, scale, workspace, status)
     if type(r) is not int:

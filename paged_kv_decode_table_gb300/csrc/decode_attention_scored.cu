@@ -17,10 +17,10 @@
 //    V is bfloat16 and the MMA takes one type), its sum is of the unrounded ones.
 //  * The maximum is renewed (shuffles, rescaled sums) only when a score exceeds it by 2^kSplitLag: a vote decides.
 // mma.sync and not tcgen05: one query per sequence gives a KV head 1 to 16 rows, a 128-row tile would be empty rows, and
-// the tensor pipe is 9% busy.
-// What bounds it: HBM where the cache is large.  8 sequences of 32768-131072, 64 and 8 heads of 128: 411 us for 2.85 GB, 102%
-// of the measured copy rate; 64 of 512-4096, 32 and 8 heads, capped: 94.6 us for 584 MB, 91%; 512 of 128-4096 that see 4 + 512
-// positions: 174.5 us for 1.05 GB, 89% (units that a window cuts are read whole).  More than 8 query heads a KV head: 71%
+// the tensor pipe is 8% busy.
+// What bounds it: HBM where the cache is large.  8 sequences of 32768-131072, 64 and 8 heads of 128: 413 us for 2.85 GB, 102%
+// of the measured copy rate; 64 of 512-4096, 32 and 8 heads, capped: 95.0 us for 584 MB, 91%; 512 of 128-4096 that see 4 + 512
+// positions: 174.0 us for 1.05 GB, 89% (units that a window cuts are read whole).  More than 8 query heads a KV head: 71%
 // (two n-tiles a warp, whose chain of products is longer than its share of the copies).  One short sequence: 7 us, four
 // dependent trips to memory.
 //
@@ -874,10 +874,10 @@ static int generic_stride(int D) {
 template <typename T, bool kVec>
 constexpr bool kGenAhead = kVec && sizeof(T) == 4;
 
-// Bound by shared-memory reads: a position's K and V row are read once for two heads, 12 bytes of shared memory a byte of
-// cache with 8 heads, so about 40% of the copy rate where there is much to read; short batches by their chain of
-// lengths, block ids, rows and the join.  37 sequences of up to 1500 (window 300), 21 and 3 heads of 80 in float32:
-// 17.5 us for 20 MB; 16 of 512-4096, 32 and 8 heads of 128 in float32 141 us for 302 MB.
+// Bound by the chain of a tile (copy, scores, products, with a barrier between them) and by shared-memory reads: a position's
+// K and V row are read once for two heads, 12 bytes of shared memory a byte of cache with 8 heads.  16 sequences of 512-4096, 32
+// and 8 heads of 128 in float32: 141 us for 302 MB, 32% of the copy rate.  Short batches: lengths, block ids, rows and the join one
+// after the other; 37 sequences of up to 1500 (window 300), 21 and 3 heads of 80 in float32 17.4 us for 20 MB.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kGenThreads)
     decode_scored_generic_kernel(const __grid_constant__ GenericPlan pl, T* out, const T* q, const T* k_cache,

@@ -29,8 +29,9 @@
 // 64-1024 behind 8192 tokens, 32 and 8 heads of 128: 49 us, 26 at the copy rate; prefix and own positions side by side 40 (one
 // after the other 22 and 25, 63 in all), the join 7.  16 groups of 4 behind 1024-4096: 63 us (34 at the copy rate): the
 // prefix kernel streams at 6.6 TB/s once its ring is full.  Many rows: the chain of products and softmax, 2600 clocks a tile
-// of 64 keys and 256 rows, 3900 with a cap, whose polynomial fills the FMA pipe: 32 sequences behind 65536 tokens, 64 and 8
-// heads, cap and slopes 152 us (50).
+// of 64 keys and 256 rows, 3900 with a cap, with two softmax warps a scheduler and no pipe near full (capped, with slopes: FMA
+// pipe 37% busy, tensor pipe 18%, special functions 10%, issue slots 44%): 32 sequences behind 65536 tokens, 64 and 8 heads, cap
+// and slopes 153 us (50).
 // Tried and not kept: key tiles of 128 (P over S in tensor memory, half the barriers; 4000 clocks for 128 keys, but with a
 // longer start as fast in all); 16 softmax warps, two threads a row.
 // Every mbarrier wait is bounded; a CTA that gives up records PKV_ERR_TIMEOUT, waits (bounded) for its own TMA copies and
