@@ -84,7 +84,7 @@ struct Px {
 struct PxShared {  // follows the 1024-aligned operand area
     uint64_t kv_full[10], kv_empty[10];
     uint64_t q_full[kPxTiles], s_full[kPxTiles], s_free[kPxTiles], p_full[kPxTiles], o_done[kPxTiles];
-    uint64_t last[2];  // of a thread that gives up: its MMAs are complete
+    uint64_t last[2];  // of a thread that leaves: its MMAs are complete
     uint32_t tmem_base;
     int at[7];  // where the CTA's range begins: a group as PxWalk has it
     int red[32];
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     const uint32_t tmem = sm->tmem_base;
 
     bool fail = false;
-    // A thread that issues MMAs and gives up waits until they are complete: tensor memory is given back behind it, and
+    // A thread that issues MMAs waits until they are complete before it leaves: tensor memory is given back behind it, and
     // no arrival may be outstanding when the CTA exits.
     auto land = [&](int i) {
         tc_commit(&sm->last[i]);
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 }
                 queries ^= 1u | (!dual || w.k1 - w.k0 > 1 ? 2u : 0u);
             }
-            if (fail) land(0);
+            land(0);  // (the softmax may have given up and not wait for the last ones)
         }
         __syncwarp();
     } else if (warp == kPxWarpPV) {

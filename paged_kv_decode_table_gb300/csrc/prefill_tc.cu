@@ -90,7 +90,7 @@ constexpr int kTcTmemCols = 512;             // query tile t: Q at 256 t, S at 2
 struct TcSmem {  // follows the 1024-aligned operand area
     uint64_t kv_full[kTcStages], kv_empty[kTcStages];
     uint64_t s_full[kTcQT], s_free[kTcQT], p_full[kTcQT], o_done[kTcQT];
-    uint64_t last[2];  // of a thread that gives up: its MMAs are complete
+    uint64_t last[2];  // of a thread that leaves: its MMAs are complete
     uint32_t tmem_base;
     int b, tile, bad;
     int tbl[kTcProd][kTcWin];
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
     tc_fence_after();
 
     bool fail = false;
-    // A thread that issues MMAs and gives up waits until they are complete: tensor memory is given back behind it, and
+    // A thread that issues MMAs waits until they are complete before it leaves: tensor memory is given back behind it, and
     // no arrival may be outstanding when the CTA exits.
     auto land = [&](int i) {
         tc_commit(&sm->last[i]);
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kKind == kPlain ? kTcThreads : kTcScoredThread
                     tc_commit(&sm->s_full[t]);
                 }
             }
-            if (fail) land(0);
+            land(0);  // (the softmax may have given up and not wait for the last ones)
         }
         __syncwarp();
     } else if (warp == kTcWarpPV && active) {

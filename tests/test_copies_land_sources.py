@@ -24,3 +24,16 @@ def test_a_loader_waits_for_its_copies_before_every_exit(name, consumers):
     # what comes last in the loader: its normal exit
     assert re.search(r"drain\(end - start\);\s*(finish\(\);\s*)?return;\s*\}\s*$", loader)
     assert len(re.findall(r"\bdrain\(", loader)) == 2
+
+
+@pytest.mark.parametrize("name", ["prefill_tc.cu", "decode_attention_shared.cu"])
+def test_threads_that_issue_mmas_wait_for_them_before_every_exit(name):
+    """Softmax warps that use up their polls do not wait for the last S, so its issuing thread always does; the PV thread
+    waits for its last commit, or where it gives up for all it issued."""
+    with open(os.path.join(CSRC, name)) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert len(re.findall(r"\}\s*land\(0\);\s*\}\s*__syncwarp\(\);", code)) == 1
+    assert len(re.findall(r"mbar_wait\(&sm->kv_empty\[[^;]*\) fail = true;\s*if \(fail\) land\(1\);\s*\}\s*__syncwarp\(\);", code)) == 1
+    land = code[code.index("auto land"):]
+    land = land[:land.index("};")]
+    assert "tc_commit(&sm->last[i])" in land and "polls" not in land
