@@ -451,7 +451,7 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
     int piece = 0, stage = 0;
     uint32_t parity = 0;
     const uint32_t smem_base = smem_u32(smem);
-    const bool capped = pl.sc.cap_log2 > 0.f;
+    const bool capped = pl.sc.cap_log2 > 0.f, sloped = pl.sc.slopes != nullptr;
     // ldmatrix: lane group mi gives the rows of matrix mi: (positions 8 (mi & 1) .., 16-byte chunk + (mi >> 1))
     uint32_t lm[4];
 #pragma unroll
@@ -493,9 +493,6 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
                 for (int n = 0; n < kN; ++n) mma_bf16_16816(s[n][c & 1], a, qb[n][c][0], qb[n][c][1]);
             }
             // ---- scores
-            // the bias's distances: from the last key, and from the sequence's first one that takes part
-            const float dist = static_cast<float>(p0[k] + g - (mt.L - 1)),
-                        dist_first = static_cast<float>(p0[k] + g - (kShared ? 0 : seen.first()));
             if (capped) {
                 float z[kN][4];
                 bool large = false;
@@ -524,12 +521,17 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[k][n][e] = (s[n][0][e] + s[n][1][e]) * pl.sc.mul;
             }
+            if (sloped) {
+                // the bias's distances: from the last key, and from the sequence's first one that takes part
+                const float dist = static_cast<float>(p0[k] + g - (mt.L - 1)),
+                            dist_first = static_cast<float>(p0[k] + g - (kShared ? 0 : seen.first()));
 #pragma unroll
-            for (int n = 0; n < kN; ++n)
+                for (int n = 0; n < kN; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[k][n][e] = fmaf(slope[n][e & 1], (slope[n][e & 1] < 0.f ? dist_first : dist) + static_cast<float>(8 * (e >> 1)),
-                                      x[k][n][e]);
+                    for (int e = 0; e < 4; ++e)
+                        x[k][n][e] = fmaf(slope[n][e & 1], (slope[n][e & 1] < 0.f ? dist_first : dist) + static_cast<float>(8 * (e >> 1)),
+                                          x[k][n][e]);
+            }
             if (part[k]) {
                 const bool in0 = seen.at(p0[k] + g), in1 = seen.at(p0[k] + g + 8);
 #pragma unroll
