@@ -878,7 +878,7 @@ constexpr bool kGenAhead = kVec && sizeof(T) == 4;
 
 // Bound by the chain of a tile (copy, scores, products, with a barrier between them) and by shared-memory reads: a position's
 // K and V row are read once for two heads, 12 bytes of shared memory a byte of cache with 8 heads.  16 sequences of 512-4096, 32
-// and 8 heads of 128 in float32: 141 us for 302 MB, 32% of the copy rate.  Short batches: lengths, block ids, rows and the join one
+// and 8 heads of 128 in float32: 145 us for 302 MB, 31% of the copy rate.  Short batches: lengths, block ids, rows and the join one
 // after the other; 37 sequences of up to 1500 (window 300), 21 and 3 heads of 80 in float32 17.4 us for 20 MB.
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kGenThreads)
