@@ -207,11 +207,10 @@ pkv_status pkv_paged_decode_attention_noalloc(void* out, const void* q, const vo
  *               will fill and give up after `polls` polls, with no copy in
  *               flight.
  * With silent_cta >= 0 the output of the sequences that CTA covers is
- * undefined (prefill, shared prefixes, and rows that are joined from several
- * CTAs' parts with changed scores: what they would be, or zeros) and dev_status
- * reads PKV_ERR_TIMEOUT; the next call after the hook is reset computes
- * normally.  Returns PKV_ERR_INVALID_ARG for silent_cta < -1.  Not synchronised
- * with attention calls on other threads.
+ * undefined (prefill, changed scores and shared prefixes: what it would be, or
+ * zeros) and dev_status reads PKV_ERR_TIMEOUT; the next call after the hook is
+ * reset computes normally.  Returns PKV_ERR_INVALID_ARG for silent_cta < -1.
+ * Not synchronised with attention calls on other threads.
  */
 pkv_status pkv_test_set_wait_limit(uint32_t polls, int silent_cta);
 

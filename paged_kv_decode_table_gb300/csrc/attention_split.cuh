@@ -46,18 +46,10 @@ struct SplitHead {
 struct SplitSpace {
     SplitHead* head;
     SplitCut* cuts;  // one per range
-    int* gave_up;    // one per range: 1 where a wait of its CTA ran out, so that its partial results may be none
     int2* info;      // shared prefixes: (first step, steps per head group) of every sequence
     float2* ml;      // (max, sum) of every partial result
     float* o;        // its sums of products
 };
-
-// Not 0 in some lane where one of n ranges from `first` on gave up.
-__device__ __forceinline__ int ranges_gave_up(const int* gave_up, int first, int n, int lane) {
-    int v = lane < n ? __ldcg(gave_up + first + lane) : 0;
-    for (int i = lane + 32; i < n; i += 32) v |= __ldcg(gave_up + first + i);
-    return v;
-}
 
 // Whether group g's bounds can be those of a group (all groups': start is an array of such).
 __device__ __forceinline__ bool group_valid(const GroupArgs& ga, int B, int g) {

@@ -137,6 +137,39 @@ __device__ __forceinline__ uint32_t split_transpose(uint32_t v) {
     return r;
 }
 
+// What a consumer warp does whose wait ran out in step `left` of the CTA's range, which ends at `end` and begins at `from` (-1: a
+// direct plan's only piece) in sequence b, whose first step is `at`.  Slot 0's warps, which leave the results, write zeros,
+// or marks that become zeros in the join, for their heads' rows in the pieces that are not done.  (Another slot's warp
+// that gives up lets slot 0's wait for it run out.)
+template <int kHeads, bool kShared>
+__device__ __noinline__ void split_give_up(const SplitPlan& pl, const int32_t* seq_lens, float2* ml, __nv_bfloat16* out,
+                                           int32_t* status, int b, int at, int from, int left, int end, int slot, int hh,
+                                           int qc) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) report(status, PKV_ERR_TIMEOUT);
+    if (slot != 0) return;
+    if (from < 0) from = end - steps_of<kShared>(pl, seq_lens, b);
+    for (; at < end; ++b) {
+        const int n = steps_of<kShared>(pl, seq_lens, b);
+        for (int g = 0; g < pl.NG; ++g, at += n) {
+            if (min(at + n, end) <= max(left, at) || at + n <= from) continue;
+            const bool whole = at >= from && at + n <= end;
+            for (int head = qc * kHeads; head < min(pl.G, (qc + 1) * kHeads); ++head) {
+                const int qr = hh * pl.G + head;
+                if (g * pl.R + qr >= pl.Hq) continue;
+                const size_t row = static_cast<size_t>(b) * pl.Hq + g * pl.R + qr;
+                if (!kShared && whole) {
+                    for (int e = lane; e < pl.D; e += 32) out[row * pl.D + e] = from_f32<__nv_bfloat16>(0.f);
+                } else if (lane == 0) {
+                    ml[whole ? 2 * static_cast<size_t>(gridDim.x) * pl.R + row
+                             : (2 * static_cast<size_t>(blockIdx.x) + (at < from ? 0 : 1)) * pl.R + qr] =
+                        make_float2(-INFINITY, -1.f);
+                }
+            }
+        }
+    }
+}
+
 // DP: dimensions computed, 64 or 128 (D may be smaller: the copies fill in zeros).  kN: n-tiles of 8 query heads
 // per warp.  kShared: positions behind the shared prefix only, every piece left as a partial result.
 template <int DP, int kN, bool kShared>
@@ -160,17 +193,11 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
     uint64_t* mfull = qempty + 2;  // merge slots: one per consumer warp
     uint64_t* mempty = mfull + kSplitWarps;
     SplitMeta* meta = reinterpret_cast<SplitMeta*>(mempty + kSplitWarps);
-    int* sch = reinterpret_cast<int*>(meta + kSplitStages);  // [0, 33) scan scratch, 33: b0, 34: s0, 35: n
+    int* sch = reinterpret_cast<int*>(meta + kSplitStages);  // [0, 33) scan scratch, 33: b0, 34: s0, 35: n, 36: start
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto finish = [] {  // before every exit
         if constexpr (kShared) asm volatile("griddepcontrol.wait;" ::: "memory");
-    };
-    auto give_up = [&] {  // a wait ran out: what this CTA's range was to leave may be missing
-        if ((threadIdx.x & 31) == 0) {
-            report(status, PKV_ERR_TIMEOUT);
-            if (kShared || !pl.direct) ws.gave_up[blockIdx.x] = 1;
-        }
     };
     // lengths, then block ids, then K and V: three dependent loads; the first two and q come to L2 while the
     // predecessor ends
@@ -232,7 +259,6 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
         }
         __syncthreads();  // the barriers are initialised
     } else {
-        if (threadIdx.x == 0) ws.gave_up[blockIdx.x] = 0;  // (barriers follow)
         [[maybe_unused]] int from = 0, to = 0, shared = 0;  // of group threadIdx.x: asked for before the lengths' chain
         if (kEstimate && static_cast<int>(threadIdx.x) < pl.groups.N) {
             from = pl.groups.start[threadIdx.x];
@@ -299,6 +325,7 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
             finish();
             return;
         }
+        if (threadIdx.x == 0) sch[36] = start;
         __syncthreads();
         b0 = sch[33];
         s0 = sch[34];
@@ -380,7 +407,7 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
                 ok = mbar_wait(&qempty[pl.qslots == 2 ? piece & 1 : 0],
                                (static_cast<uint32_t>(piece >> (pl.qslots - 1)) & 1u) ^ 1u, pl.polls);
             if (!__all_sync(0xffffffffu, ok)) {
-                give_up();
+                if (lane == 0) report(status, PKV_ERR_TIMEOUT);
                 drain(it);
                 finish();
                 return;
@@ -636,160 +663,154 @@ __global__ void __launch_bounds__((kSplitWarps + 1) * 32, 1)
         }
     };
 
-    for (int i = start; i < end; ++i) {
-        if (!mbar_wait(&full[stage], parity, pl.polls)) {
-            give_up();
-            finish();
-            return;
-        }
-        const SplitMeta mt = meta[stage];
-        if (mt.flags & kSFirst) {
-            const int qs = pl.qslots == 2 ? piece & 1 : 0;
-            if (!mbar_wait(&qfull[qs], static_cast<uint32_t>(piece >> (pl.qslots - 1)) & 1u, pl.polls)) {
-                give_up();
-                finish();
-                return;
-            }
-            const uint8_t* qsm = qring + static_cast<size_t>(qs) * pl.q_bytes;
-            const int head0 = ((mt.vb % NG) * HG + hh) * pl.G;
-            // (none for the heads that a last, smaller group lacks)
-            const int qrows = (mt.vb % NG) * HG + hh < pl.Hkv ? pl.G : 0;
+    // The step in which a wait ran out, or `end`.
+    auto consume = [&]() -> int {
+        for (int i = start; i < end; ++i) {
+            if (!mbar_wait(&full[stage], parity, pl.polls)) return i;
+            const SplitMeta mt = meta[stage];
+            if (mt.flags & kSFirst) {
+                const int qs = pl.qslots == 2 ? piece & 1 : 0;
+                if (!mbar_wait(&qfull[qs], static_cast<uint32_t>(piece >> (pl.qslots - 1)) & 1u, pl.polls)) return i;
+                const uint8_t* qsm = qring + static_cast<size_t>(qs) * pl.q_bytes;
+                const int head0 = ((mt.vb % NG) * HG + hh) * pl.G;
+                // (none for the heads that a last, smaller group lacks)
+                const int qrows = (mt.vb % NG) * HG + hh < pl.Hkv ? pl.G : 0;
 #pragma unroll
-            for (int n = 0; n < kN; ++n) {
-                const int row = qc * kHeads + 8 * n + g;
+                for (int n = 0; n < kN; ++n) {
+                    const int row = qc * kHeads + 8 * n + g;
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c)
+                    for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        const int at = hh * pl.G + row;
-                        qb[n][c][p] = row < qrows && 16 * c + 8 * p < pl.D
-                                          ? *reinterpret_cast<const uint32_t*>(
-                                                qsm + at * (2 * DP) + (((2 * c + p) ^ (at & 7)) << 4) + 4 * r) : 0u;
+                        for (int p = 0; p < 2; ++p) {
+                            const int at = hh * pl.G + row;
+                            qb[n][c][p] = row < qrows && 16 * c + 8 * p < pl.D
+                                              ? *reinterpret_cast<const uint32_t*>(
+                                                    qsm + at * (2 * DP) + (((2 * c + p) ^ (at & 7)) << 4) + 4 * r) : 0u;
+                        }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int hd = qc * kHeads + 8 * n + 2 * r + e;
+                        slope[n][e] = pl.sc.slopes != nullptr && hd < qrows ? pl.sc.slopes[head0 + hd] * kLog2e : 0.f;
+                        m[n][e] = -INFINITY;
+                        mu[n][e] = l[n][e] = 0.f;
                     }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int hd = qc * kHeads + 8 * n + 2 * r + e;
-                    slope[n][e] = pl.sc.slopes != nullptr && hd < qrows ? pl.sc.slopes[head0 + hd] * kLog2e : 0.f;
-                    m[n][e] = -INFINITY;
-                    mu[n][e] = l[n][e] = 0.f;
+                    for (int c = 0; c < kChunks; ++c) O[c][n][0] = O[c][n][1] = O[c][n][2] = O[c][n][3] = 0.f;
                 }
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) O[c][n][0] = O[c][n][1] = O[c][n][2] = O[c][n][3] = 0.f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&qempty[qs]);
+                poisoned = false;
             }
+            poisoned = poisoned || (mt.flags & kSBad);
+            if (!poisoned) tiles(mt);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&qempty[qs]);
-            poisoned = false;
-        }
-        poisoned = poisoned || (mt.flags & kSBad);
-        if (!poisoned) tiles(mt);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
-        if (++stage == nst) {
-            stage = 0;
-            parity ^= 1u;
-        }
-        if (!(mt.flags & kSLast)) continue;
+            if (lane == 0) mbar_arrive(&empty[stage]);
+            if (++stage == nst) {
+                stage = 0;
+                parity ^= 1u;
+            }
+            if (!(mt.flags & kSLast)) continue;
 
-        // ---------------------------------------------- the range leaves (sequence, group) mt.vb
+            // ---------------------------------------------- the range leaves (sequence, group) mt.vb
 #pragma unroll
-        for (int n = 0; n < kN; ++n)
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
-        if (slots > 1) {
-            // merge the slots: at distance d = slots / 2, .., 1 warp slot in [d, 2d) hands its result to slot - d
-            // through its own scratch tile (rows padded by 4 floats so that the 4 pairs of heads a store touches
-            // fall on different banks).  Each wait is bounded.
-            constexpr int kRow = DP + 4, kTile = kHeads * (kRow + 2);
-            const uint32_t ph = static_cast<uint32_t>(piece) & 1u;
-            bool sent = false;
-            for (int d = slots >> 1; d > 0; d >>= 1) {
-                if (slot >= d) {
-                    float* t = scratch + ((slot - 1) * HV + vh) * kTile;
-                    if (!mbar_wait(&mempty[warp], ph ^ 1u, pl.polls)) {
-                        give_up();
-                        finish();
-                        return;
+                    for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], o);
+            if (slots > 1) {
+                // merge the slots: at distance d = slots / 2, .., 1 warp slot in [d, 2d) hands its result to slot - d
+                // through its own scratch tile (rows padded by 4 floats so that the 4 pairs of heads a store touches
+                // fall on different banks).  Each wait is bounded.
+                constexpr int kRow = DP + 4, kTile = kHeads * (kRow + 2);
+                const uint32_t ph = static_cast<uint32_t>(piece) & 1u;
+                bool sent = false;
+                for (int d = slots >> 1; d > 0; d >>= 1) {
+                    if (slot >= d) {
+                        float* t = scratch + ((slot - 1) * HV + vh) * kTile;
+                        if (!mbar_wait(&mempty[warp], ph ^ 1u, pl.polls)) return i;
+#pragma unroll
+                        for (int n = 0; n < kN; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int head = 8 * n + 2 * r + e;
+#pragma unroll
+                                for (int c = 0; c < kChunks; ++c) {
+                                    t[head * kRow + 16 * c + g] = O[c][n][e];
+                                    t[head * kRow + 16 * c + 8 + g] = O[c][n][2 + e];
+                                }
+                                if (g == 0)
+                                    *reinterpret_cast<float2*>(t + kHeads * kRow + 2 * head) = make_float2(m[n][e], l[n][e]);
+                            }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&mfull[warp]);
+                        sent = true;
+                        break;
                     }
+                    const int from = warp + d * HV;
+                    const float* t = scratch + ((slot + d - 1) * HV + vh) * kTile;
+                    if (!mbar_wait(&mfull[from], ph, pl.polls)) return i;
 #pragma unroll
                     for (int n = 0; n < kN; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int head = 8 * n + 2 * r + e;
+                            const float2 ml = *reinterpret_cast<const float2*>(t + kHeads * kRow + 2 * head);
+                            const float mn = fmaxf(m[n][e], ml.x), base = mn == -INFINITY ? 0.f : mn;
+                            const float fa = ex2_approx(m[n][e] - base), fb = ex2_approx(ml.x - base);
+                            m[n][e] = mn;
+                            l[n][e] = fmaf(l[n][e], fa, ml.y * fb);
 #pragma unroll
                             for (int c = 0; c < kChunks; ++c) {
-                                t[head * kRow + 16 * c + g] = O[c][n][e];
-                                t[head * kRow + 16 * c + 8 + g] = O[c][n][2 + e];
+                                O[c][n][e] = fmaf(O[c][n][e], fa, t[head * kRow + 16 * c + g] * fb);
+                                O[c][n][2 + e] = fmaf(O[c][n][2 + e], fa, t[head * kRow + 16 * c + 8 + g] * fb);
                             }
-                            if (g == 0)
-                                *reinterpret_cast<float2*>(t + kHeads * kRow + 2 * head) = make_float2(m[n][e], l[n][e]);
                         }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&mfull[warp]);
-                    sent = true;
-                    break;
+                    if (lane == 0) mbar_arrive(&mempty[from]);
                 }
-                const int from = warp + d * HV;
-                const float* t = scratch + ((slot + d - 1) * HV + vh) * kTile;
-                if (!mbar_wait(&mfull[from], ph, pl.polls)) {
-                    give_up();
-                    finish();
-                    return;
-                }
+                ++piece;
+                if (sent) continue;
+            } else {
+                ++piece;
+            }
+            const int vb_g = mt.vb % NG, vb_b = mt.vb / NG;
 #pragma unroll
-                for (int n = 0; n < kN; ++n)
+            for (int n = 0; n < kN; ++n)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int head = 8 * n + 2 * r + e;
-                        const float2 ml = *reinterpret_cast<const float2*>(t + kHeads * kRow + 2 * head);
-                        const float mn = fmaxf(m[n][e], ml.x), base = mn == -INFINITY ? 0.f : mn;
-                        const float fa = ex2_approx(m[n][e] - base), fb = ex2_approx(ml.x - base);
-                        m[n][e] = mn;
-                        l[n][e] = fmaf(l[n][e], fa, ml.y * fb);
+                for (int e = 0; e < 2; ++e) {
+                    const int head = qc * kHeads + 8 * n + 2 * r + e;
+                    const int qr = hh * pl.G + head;  // row in the group
+                    if (head >= pl.G || vb_g * pl.R + qr >= pl.Hq) continue;
+                    const size_t row = static_cast<size_t>(vb_b) * pl.Hq + vb_g * pl.R + qr;  // row of out
+                    if (!kShared && (mt.flags & kSWhole)) {
+                        const float inv = poisoned || l[n][e] == 0.f ? 0.f : 1.f / l[n][e];
+                        __nv_bfloat16* o = out + row * pl.D + g;
 #pragma unroll
                         for (int c = 0; c < kChunks; ++c) {
-                            O[c][n][e] = fmaf(O[c][n][e], fa, t[head * kRow + 16 * c + g] * fb);
-                            O[c][n][2 + e] = fmaf(O[c][n][2 + e], fa, t[head * kRow + 16 * c + 8 + g] * fb);
+                            if (16 * c < pl.D) o[16 * c] = from_f32<__nv_bfloat16>(poisoned ? 0.f : O[c][n][e] * inv);
+                            if (16 * c + 8 < pl.D) o[16 * c + 8] = from_f32<__nv_bfloat16>(poisoned ? 0.f : O[c][n][2 + e] * inv);
+                        }
+                    } else {
+                        size_t at = (2 * static_cast<size_t>(blockIdx.x) + ((mt.flags & kSHead) ? 0 : 1)) * pl.R + qr;
+                        if (kShared && (mt.flags & kSWhole)) at = 2 * static_cast<size_t>(gridDim.x) * pl.R + row;
+                        if (g == 0) ws.ml[at] = make_float2(m[n][e], poisoned ? -1.f : l[n][e]);
+                        float* o = ws.o + at * pl.D + g;
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c) {
+                            if (16 * c < pl.D) o[16 * c] = O[c][n][e];
+                            if (16 * c + 8 < pl.D) o[16 * c + 8] = O[c][n][2 + e];
                         }
                     }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&mempty[from]);
-            }
-            ++piece;
-            if (sent) continue;
-        } else {
-            ++piece;
-        }
-        const int vb_g = mt.vb % NG, vb_b = mt.vb / NG;
-#pragma unroll
-        for (int n = 0; n < kN; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int head = qc * kHeads + 8 * n + 2 * r + e;
-                const int qr = hh * pl.G + head;  // row in the group
-                if (head >= pl.G || vb_g * pl.R + qr >= pl.Hq) continue;
-                const size_t row = static_cast<size_t>(vb_b) * pl.Hq + vb_g * pl.R + qr;  // row of out
-                if (!kShared && (mt.flags & kSWhole)) {
-                    const float inv = poisoned || l[n][e] == 0.f ? 0.f : 1.f / l[n][e];
-                    __nv_bfloat16* o = out + row * pl.D + g;
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        if (16 * c < pl.D) o[16 * c] = from_f32<__nv_bfloat16>(poisoned ? 0.f : O[c][n][e] * inv);
-                        if (16 * c + 8 < pl.D) o[16 * c + 8] = from_f32<__nv_bfloat16>(poisoned ? 0.f : O[c][n][2 + e] * inv);
-                    }
-                } else {
-                    size_t at = (2 * static_cast<size_t>(blockIdx.x) + ((mt.flags & kSHead) ? 0 : 1)) * pl.R + qr;
-                    if (kShared && (mt.flags & kSWhole)) at = 2 * static_cast<size_t>(gridDim.x) * pl.R + row;
-                    if (g == 0) ws.ml[at] = make_float2(m[n][e], poisoned ? -1.f : l[n][e]);
-                    float* o = ws.o + at * pl.D + g;
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        if (16 * c < pl.D) o[16 * c] = O[c][n][e];
-                        if (16 * c + 8 < pl.D) o[16 * c + 8] = O[c][n][2 + e];
-                    }
                 }
-            }
+        }
+        return end;
+    };
+    const int left = consume();
+    if (left < end) {
+        const int bb = !kShared && pl.direct ? static_cast<int>(blockIdx.x) / NG : sch[33];
+        split_give_up<kHeads, kShared>(pl, seq_lens, ws.ml, out, status, bb, !kShared && pl.direct ? 0 : sch[34],
+                                       !kShared && pl.direct ? -1 : sch[36], left, end, slot, hh, qc);
     }
     finish();
 }
@@ -814,7 +835,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float M = -INFINITY, l = 0.f;
     bool bad = false;
-    const int lost = ranges_gave_up(ws.gave_up, cut.f, cut.pieces, lane);
     const bool col = 4 * lane < pl.D;
     for (int p0 = 0; p0 < cut.pieces; p0 += kJoinGroup) {
         float2 ml[kJoinGroup];
@@ -845,7 +865,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
             acc.w = fmaf(o[k].w, w, acc.w);
         }
     }
-    bad = bad || __any_sync(0xffffffffu, lost != 0);
     if (!col) return;
     const float inv = 1.f / l;
     const bool zero = bad || l == 0.f;
@@ -1249,18 +1268,17 @@ bool split_shape(int Hq, int Hkv, int D, int BS, int min_groups, SplitPlan& pl) 
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// [head][cuts][ranges that gave up][info of B sequences][(max, sum)][sums of products]; two partial results per CTA of R rows and, for
+// [head][cuts][info of B sequences][(max, sum)][sums of products]; two partial results per CTA of R rows and, for
 // shared prefixes, one per row of out.
 size_t split_space(const SplitPlan& pl, int P, int B, bool shared, void* base, SplitSpace* ws) {
     const size_t slots = static_cast<size_t>(2) * P * pl.R + (shared ? static_cast<size_t>(B) * pl.Hq : 0);
-    const size_t cuts = 256, gave_up = up256(cuts + sizeof(SplitCut) * P), info = up256(gave_up + sizeof(int) * P);
+    const size_t cuts = 256, info = up256(cuts + sizeof(SplitCut) * P);
     const size_t ml = up256(info + (shared ? sizeof(int2) * static_cast<size_t>(B) : 0));
     const size_t o = up256(ml + slots * sizeof(float2));
     if (ws != nullptr) {
         uint8_t* p = static_cast<uint8_t*>(base);
         ws->head = reinterpret_cast<SplitHead*>(p);
         ws->cuts = reinterpret_cast<SplitCut*>(p + cuts);
-        ws->gave_up = reinterpret_cast<int*>(p + gave_up);
         ws->info = reinterpret_cast<int2*>(p + info);
         ws->ml = reinterpret_cast<float2*>(p + ml);
         ws->o = reinterpret_cast<float*>(p + o);

@@ -103,7 +103,6 @@ struct PxHead {
 };
 struct PxSpace {
     PxHead* head;
-    int* gave_up;  // one per CTA: 1 where a wait ran out, so that its pieces may be missing
     int2* plan;   // of every group: (first key tile in the order, key tiles of a row tile)
     float2* ml;   // (max, sum): 2 slots per CTA of 256 rows, then two places per row of out
     float* o;
@@ -216,7 +215,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    if (tid == 0) ws.gave_up[blockIdx.x] = 0;
     // ---- the whole work, and this CTA's range of it: key tiles [start, end)
     auto scan = [&](int v, int& total) {  // over the CTA; exclusive
         int x = v;
@@ -505,6 +503,12 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             tc_fence_before();
             mbar_arrive(&sm->q_full[qt]);
         };
+        // Where the row's part of a piece goes: a place per row of out where it is the whole prefix, else this range's slot.
+        auto place = [&](const PxWalk& x, bool dual, int b) {
+            return x.k0 == 0 && x.k1 == x.nt ? 2 * static_cast<size_t>(gridDim.x) * kPxSlot +
+                                                   (static_cast<size_t>(dual ? qt : 0) * pl.B + b) * pl.Hq + x.h * G + rh
+                                             : (2 * static_cast<size_t>(blockIdx.x) + (x.k0 > 0 ? 0 : 1)) * kPxSlot + qt * kPxRows + r;
+        };
         int done = 0;  // key tiles of this query tile
         PxWalk next = w;
         next.to(pl, start, end);
@@ -613,14 +617,18 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                 put_q(next);
             }
             if (!fail && k0 < w.k1 && !__all_sync(0xffffffffu, tc_wait(&sm->o_done[qt], (done - 1) & 1, pl.polls))) fail = true;
-            if (fail) break;
-            // ---- the piece's rows: a place per row of out where it is the whole prefix, else this range's slot
+            if (fail) {  // this piece's rows and those of the pieces to come are marked: the join sets them to zero
+                for (int x = at; x < end; x += w.k1 - w.k0) {
+                    w.to(pl, x, end);
+                    const bool both = w.dual(pl);
+                    const int m = w.tile * pl.TC + (both ? 0 : qt * pl.TQ) + rm;
+                    if (rm < pl.TQ && m < w.n) ws.ml[place(w, both, w.first + m)] = make_float2(-INFINITY, -1.f);
+                }
+                break;
+            }
+            // ---- the piece's rows
             tc_fence_after();
-            const bool whole = w.k0 == 0 && w.k1 == w.nt;
-            const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (w.k0 > 0 ? 0 : 1);
-            const size_t own = whole ? 2 * static_cast<size_t>(gridDim.x) * kPxSlot +
-                                           (static_cast<size_t>(dual ? qt : 0) * pl.B + b) * pl.Hq + qh
-                                     : slot * kPxSlot + qt * kPxRows + r;
+            const size_t own = place(w, dual, b);
             if (valid) ws.ml[own] = make_float2(m_ref, broken ? -1.f : lsum);
             // the P tile is free: 32 columns of the warp's 32 rows go through its quarter of it
             float4* stage = reinterpret_cast<float4*>(pbuf + (warp & 3) * 4096);
@@ -658,10 +666,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     } else {
         tc_fewer_registers();
     }
-    if (fail && lane == 0) {
-        report(status, PKV_ERR_TIMEOUT);
-        ws.gave_up[blockIdx.x] = 1;
-    }
+    if (fail && lane == 0) report(status, PKV_ERR_TIMEOUT);
     // ---- every role is done with TMEM
     tc_fence_before();
     __syncthreads();
@@ -731,7 +736,6 @@ __global__ void __launch_bounds__(kSjWarps * 32)
             no = (first + info.y - 1) / Wo - of + 1;
         }
     }
-    const int lost = ranges_gave_up(px.gave_up, pf, np, lane) | ranges_gave_up(ws.gave_up, of, no, lane);
     const int npx = dual ? 2 * np : np, n = npx + no;
     float acc[kCols] = {};
     float M = -INFINITY, l = 0.f;
@@ -816,7 +820,6 @@ __global__ void __launch_bounds__(kSjWarps * 32)
             for (int i = 0; i < kCols; ++i) acc[i] = fmaf(other[2 + i], f, acc[i]);
         }
     }
-    bad = bad || __any_sync(0xffffffffu, lost != 0);
     if (row0 >= rows) return;
     const bool zero = bad || l == 0.f;
     const float inv = 1.f / l;
@@ -850,16 +853,15 @@ static bool encode_pool_rows64(CUtensorMap* map, const void* pool, long long row
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [head][CTAs that gave up][plan of up to B groups][(max, sum)][O]
+// [head][plan of up to B groups][(max, sum)][O]
 static size_t px_space(int B, int Hq, int D, int P, void* base, PxSpace* ws) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t places = 2 * static_cast<size_t>(P) * kPxSlot + 2 * static_cast<size_t>(B) * Hq;
-    const size_t gave_up = 256, plan = up(gave_up + sizeof(int) * P);
+    const size_t plan = 256;
     const size_t ml = up(plan + sizeof(int2) * static_cast<size_t>(B)), o = up(ml + places * sizeof(float2));
     if (ws != nullptr) {
         uint8_t* p = static_cast<uint8_t*>(base);
         ws->head = reinterpret_cast<PxHead*>(p);
-        ws->gave_up = reinterpret_cast<int*>(p + gave_up);
         ws->plan = reinterpret_cast<int2*>(p + plan);
         ws->ml = reinterpret_cast<float2*>(p + ml);
         ws->o = reinterpret_cast<float*>(p + o);

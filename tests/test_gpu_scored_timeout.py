@@ -73,11 +73,15 @@ def _lib():
 
 
 @pytest.mark.parametrize("cta", [0, 1])
-def test_silent_loader_of_a_joined_sequence(cta):
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [([40000], 16, 4, 128), ([700] * 300 + [0, 5, 30000], 16, 4, 128),  # pieces, whole ones
+                                           ([300 + i for i in range(200)], 48, 2, 64), ([50] * 400, 22, 11, 128),
+                                           ([60, 30], 16, 4, 128)])  # a CTA for each
+def test_silent_loader_of_decode(lens, Hq, Hkv, D, cta):
     _lib()
-    x = R.make(3, [40000], 16, 4, 128, 16, torch.bfloat16)
+    x = R.make(3, lens, Hq, Hkv, D, 16, torch.bfloat16)
     _gives_up(lambda st, out: pkv.paged_decode_attention_scored(x["q"], x["k_cache"], x["v_cache"], x["block_tables"],
-                                                                x["seq_lens"], softcap=9.0, out=out, status=st), cta)
+                                                                x["seq_lens"], softcap=9.0, out=out, status=st), cta,
+              torch.full_like(x["q"], float("nan")))
 
 
 @pytest.mark.parametrize("D", [64, 128])
