@@ -18,9 +18,9 @@
 //  * The maximum is renewed (shuffles, rescaled sums) only when a score exceeds it by 2^kSplitLag: a vote decides.
 // mma.sync and not tcgen05: one query per sequence gives a KV head 1 to 16 rows, a 128-row tile would be empty rows, and
 // the tensor pipe is 8% busy.
-// What bounds it: HBM where the cache is large.  8 sequences of 32768-131072, 64 and 8 heads of 128: 413 us for 2.85 GB, 102%
-// of the measured copy rate; 64 of 512-4096, 32 and 8 heads, capped: 95.0 us for 584 MB, 91%; 512 of 128-4096 that see 4 + 512
-// positions: 174.0 us for 1.05 GB, 89% (units that a window cuts are read whole).  More than 8 query heads a KV head: 71%
+// What bounds it: HBM where the cache is large.  8 sequences of 32768-131072, 64 and 8 heads of 128: 412 us for 2.85 GB, 102%
+// of the measured copy rate; 64 of 512-4096, 32 and 8 heads, capped: 94.8 us for 584 MB, 91%; 512 of 128-4096 that see 4 + 512
+// positions: 175.0 us for 1.05 GB, 88% (units that a window cuts are read whole).  More than 8 query heads a KV head: 71%
 // (two n-tiles a warp, whose chain of products is longer than its share of the copies).  One short sequence: 7 us, four
 // dependent trips to memory.
 //

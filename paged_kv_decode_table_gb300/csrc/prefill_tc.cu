@@ -154,8 +154,8 @@ struct TcWaits {
 // which only the other query tile hides: two softmax warps a scheduler, and no pipe near full by the counters.  A tile of 64 keys
 // and 256 rows takes 2000-2300 clocks plain, 2800 with slopes, 3500 capped (eight FMAs a score).  8 chunks of 256-512
 // behind 512-4096 (32 and 8 heads): plain 109 us (tensor pipe 33% busy, issue slots 31%), slopes 132 (25%, 38%), capped 166 (20%,
-// 39%; FMA pipe 31%).  16 such chunks: 257 us plain, 369 with every score capped; 4 of up to 2048 behind 16384-32768 that see
-// 1024 + 100 positions, with slopes, 414 (109 at the measured bf16 rate).
+// 39%; FMA pipe 31%).  16 such chunks: 258 us plain, 368 with every score capped; 4 of up to 2048 behind 16384-32768 that see
+// 1024 + 100 positions, with slopes, 412 (109 at the measured bf16 rate).
 // Of a plain tile the MMAs, one after the other, are 1900 clocks: with M 128, K 16 one takes 84 with A in tensor memory (N 64; 88
 // for N 128), 70 with A in shared memory (N 128), and there are 16 of S and 8 of PV.  Q in shared memory (52 clocks an MMA of S)
 // was no way out: shared memory then carries 224 KB a tile at 118 bytes a clock, 1900 again, and the ring is two stages
